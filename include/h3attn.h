@@ -33,8 +33,8 @@
  *   - All compute calls are asynchronous on the given CUDA stream
  *     (a cudaStream_t passed as void*; NULL = the legacy default stream) and
  *     may be issued on any stream.  The library allocates no device memory on
- *     the compute path; only h3attn_plan_create allocates, and
- *     h3attn_plan_destroy frees.
+ *     the compute path; only h3attn_plan_create, h3attn_plan_set_sparse and
+ *     h3attn_plan_set_prefix allocate, and h3attn_plan_destroy frees.
  *   - Functions never throw across the boundary.  Arguments are validated
  *     before anything is launched; on failure nothing is launched, the
  *     status says why, and h3attn_last_error() holds a message.
@@ -56,7 +56,8 @@ extern "C" {
 
 typedef enum {
   H3ATTN_OK = 0,
-  H3ATTN_EINVAL = 1,        /* bad argument: null, misaligned, empty, out of range */
+  H3ATTN_EINVAL = 1,        /* bad argument: null, misaligned, empty, out of range (a listed key tile
+                               outside its document: see h3attn_get_device_error) */
   H3ATTN_EUNSUPPORTED = 2,  /* valid but not built: head_dim != 128, rope_dims != 96, not sm_103 */
   H3ATTN_ENOMEM = 3,        /* device or host allocation failed (plan creation only) */
   H3ATTN_ECUDA = 4,         /* a CUDA runtime/driver call failed; message has the CUDA error */
@@ -280,6 +281,132 @@ h3attn_status h3attn_forward_fp8(h3attn_plan_t plan, const void* q8, const void*
                                  const float* sq, const float* sk, const float* sv, void* o, int64_t o_row_stride,
                                  float softmax_scale, float* lse_out, void* cuda_stream);
 
+/* ---- Block-sparse attention ------------------------------------------------
+ * Long documents at a fraction of their pairs: every query block attends to a
+ * list of its document's 128-key tiles.  The pages name a thresholded sparse
+ * attention (H3 Blackwell Runtime README, "Hot Runtime Service") without
+ * defining it; the rule here is this library's own and is stated in full.
+ *
+ * Blocks: document [a, b) is cut into query blocks of q_block rows, [a + i
+ * q_block, min(a + (i + 1) q_block, b)), numbered over all documents in order
+ * (n_q_blocks of them), and into key tiles [a + 128 j, min(a + 128 (j + 1),
+ * b)), numbered from 0 within the document.
+ *
+ * Lists (device, caller-owned): block_cnt int32 [H, n_q_blocks], the entries
+ * used of each row of block_idx, int32 [H, n_q_blocks, max_blocks].  They may
+ * come from h3attn_block_select or from anywhere else, in any order; a tile
+ * listed twice counts twice, an empty list is allowed, and counts outside
+ * [0, max_blocks] are clamped to it.
+ *
+ * h3attn_plan_set_sparse adds the work list to a plan: q_block is 512 (the
+ * forward's unit of work: the rate of the dense forward on the listed tiles)
+ * or 256 (a finer selection, at about half that rate); max_blocks >= 1 is the
+ * width of the lists and what the work is balanced for.  It allocates and
+ * synchronises cuda_stream, must not be called while a stream is captured, and
+ * may be called once per plan, so that no later call invalidates a captured
+ * graph.
+ * Errors: EINVAL for a NULL plan, another q_block, max_blocks outside
+ * [1, 2^20], lists already set, lists or partial results of 2^31 rows or more;
+ * ENOMEM / ECUDA from allocation or upload. */
+h3attn_status h3attn_plan_set_sparse(h3attn_plan_t plan, int32_t q_block, int32_t max_blocks, void* cuda_stream);
+
+/* Sizes of the sparse lists; any output pointer may be NULL.  EINVAL if
+ * h3attn_plan_set_sparse has not been called. */
+h3attn_status h3attn_plan_sparse_info(h3attn_plan_t plan, int32_t* q_block, int32_t* max_blocks, int32_t* n_q_blocks);
+
+/* Block scores and selection.  With qm_i the mean of the q-hat rows of query
+ * block i and km_j the mean of the k-hat rows of key tile j of its document
+ * (each mean rounded once to fp32), score_ij = <qm_i, km_j>; per head, block i
+ * keeps the min(keep, tiles of the document) tiles with the largest scores,
+ * ties to the lower tile.  Sums and scores are carried to about 2^-44, so that
+ * the answer does not depend on the order of summation; a NaN score ranks
+ * below every number, and one beyond fp32's range as infinite.  keep_own != 0
+ * puts the tiles that overlap the query block before all others.  Writes the
+ * kept tiles in ascending order, -1 behind them up to max_blocks, and their
+ * number.  q_hat, k_hat: bf16 [S,H,128] with qkv_row_stride; block_idx,
+ * block_cnt: as above.  Uses the plan's workspace (see the rule on plans).
+ * Errors: EINVAL for NULL or misaligned (tensors 16, lists 4 bytes) pointers, a
+ * bad stride, keep outside [1, max_blocks], lists that overlap the tensors or
+ * each other, or without h3attn_plan_set_sparse; EUNSUPPORTED for a document of
+ * more than 2,097,152 tokens. */
+h3attn_status h3attn_block_select(h3attn_plan_t plan, const void* q_hat, const void* k_hat, int64_t qkv_row_stride,
+                                  int32_t keep, int32_t keep_own, int32_t* block_idx, int32_t* block_cnt,
+                                  void* cuda_stream);
+
+/* h3attn_forward over the listed tiles: for each head and each query row i of
+ * query block B, with J the keys of the tiles listed for (head, B),
+ *     o_i = sum_{j in J} softmax_j(softmax_scale <q_i, k_j>) v_j
+ *     lse[h*S + i] = ln sum_{j in J} exp(softmax_scale <q_i, k_j>)
+ * and o_i = 0, lse = -inf where J is empty.  A listed tile outside the
+ * document is skipped and reported by h3attn_get_device_error (EINVAL).  Keys
+ * that are not visited, among them the rows behind a document's end, do not
+ * reach o or lse, whatever they hold (NaN included).  Tensors, strides and
+ * errors as h3attn_forward; block_idx, block_cnt: as above, 4-byte aligned, not
+ * overlapping o or lse_out; EINVAL without h3attn_plan_set_sparse. */
+h3attn_status h3attn_forward_sparse(h3attn_plan_t plan, const void* q, const void* k, const void* v,
+                                    int64_t qkv_row_stride, const int32_t* block_idx, const int32_t* block_cnt,
+                                    void* o, int64_t o_row_stride, float softmax_scale, float* lse_out,
+                                    void* cuda_stream);
+
+/* ---- Attention with a shared prefix -----------------------------------------
+ * A batch of documents that all attend to one long prefix besides themselves:
+ * variants of a request over the same reference images, or single queries over
+ * a finished context ([SPARK] step-invariant caches: the prefix's k-hat and v
+ * are computed once per request and block and kept).  Rows of different
+ * documents share the passes over the prefix, so that it is read once per 512
+ * rows of the batch rather than once per document.
+ *
+ * h3attn_plan_set_prefix adds the work list for a prefix of prefix_len >= 1
+ * rows to a plan whose documents are the batch; allocation, capture and "once
+ * per plan" as h3attn_plan_set_sparse (a plan may have both lists).  Partial
+ * results take 520 bytes per (row, head) and pass for rows that share passes.
+ * Errors: EINVAL for a NULL plan, prefix_len < 1, a prefix already set, or
+ * partial results of 2^31 rows or more; ENOMEM / ECUDA from allocation or
+ * upload. */
+h3attn_status h3attn_plan_set_prefix(h3attn_plan_t plan, int32_t prefix_len, void* cuda_stream);
+
+/* For each head and each query row i of document [a, b), with the prefix's
+ * rows k'_0 .. k'_{P-1}, v'_0 .. v'_{P-1} and P = prefix_len:
+ *     o_i = the softmax-weighted sum of v'_0 .. v'_{P-1}, v_a .. v_{b-1}
+ *           with scores softmax_scale <q_i, k'_j> and softmax_scale <q_i, k_j>
+ *     lse[h*S + i] = ln of the sum of the exponentials of all those scores
+ * q, k, v, o, lse_out, strides and errors as h3attn_forward; k_prefix,
+ * v_prefix: bf16 [P,H,128] with prefix_row_stride (>= H*128, a multiple of 8),
+ * 16-byte aligned, not overlapping o or lse_out.  Rows behind the prefix or a
+ * document do not reach o or lse, whatever they hold.  EINVAL also without
+ * h3attn_plan_set_prefix. */
+h3attn_status h3attn_forward_prefix(h3attn_plan_t plan, const void* q, const void* k, const void* v,
+                                    int64_t qkv_row_stride, const void* k_prefix, const void* v_prefix,
+                                    int64_t prefix_row_stride, void* o, int64_t o_row_stride, float softmax_scale,
+                                    float* lse_out, void* cuda_stream);
+
+/* The work lists of the two forwards above for a packed layout, built on the
+ * host alone, as h3attn_work_list_host does for the dense one.
+ *   kind 0 (list walk): p0 = q_block, p1 = max_blocks; kind 1 (prefix walk): p0
+ *   = prefix_len, p1 ignored.
+ * Outputs (host memory; pass units = NULL for the sizes first):
+ *   units    [*n_units][8] int32, grouped by CTA pair: first query row, end of
+ *            the query rows, document begin, document end, head, then for kind 0
+ *            the query block and piece | pieces << 16 (the piece's share of the
+ *            block's list), for kind 1 key tiles [lo, hi) of "the prefix's
+ *            tiles, then the document's"; last the first partial row (-1: the
+ *            segment writes the output itself);
+ *   unit_off [*n_pairs_used + 1] int32: pair p runs units [unit_off[p], unit_off[p + 1]);
+ *   joins    [*n_joins][16] int32, the rows combined from partial rows: rows
+ *            [r0, r1), head, key_lo; then of segment a its first partial row,
+ *            rows, pieces and first query row; the same of segment b (pieces may
+ *            be 0); key_hi (keys [key_lo, key_hi) are attended to by the join
+ *            itself), three zeros.  Row r of piece c is partial row first + c *
+ *            rows + (r - first query row).
+ *   *n_part_rows  partial rows in all.
+ * Errors: EINVAL for NULL cu_seqlens or output counts, the layout errors of
+ * h3attn_work_list_host, parameters that the plan calls refuse, or capacities
+ * (units_cap, joins_cap, in records) too small. */
+h3attn_status h3attn_walk_list_host(int32_t kind, const int32_t* cu_seqlens, int32_t n_docs, int32_t num_heads,
+                                    int32_t p0, int32_t p1, int32_t n_pairs, int32_t* units, int64_t units_cap,
+                                    int32_t* unit_off, int32_t* joins, int64_t joins_cap, int64_t* n_units,
+                                    int32_t* n_pairs_used, int64_t* n_joins, int64_t* n_part_rows);
+
 /* Allocation-free forward.  The pages have no counterpart: this entry point
  * exists for callers that may not allocate device memory -- code whose device
  * memory is owned by a host framework's pool or arena (an engine plugin, a
@@ -316,7 +443,8 @@ h3attn_status h3attn_forward_noalloc(const int32_t* cu_seqlens, int32_t n_docs, 
 /* Synchronises cuda_stream, then reads and clears the plan's device error
  * word.  Returns OK, or ETIMEOUT if a kernel's bounded wait ran out since the
  * last call (the kernel then stopped early and its outputs are invalid), or
- * ECUDA if the stream reports an error. */
+ * EINVAL if a list of h3attn_forward_sparse named a key tile outside its
+ * document (the tile was skipped), or ECUDA if the stream reports an error. */
 h3attn_status h3attn_get_device_error(h3attn_plan_t plan, void* cuda_stream);
 
 /* Launches one CTA that waits on a shared-memory barrier nothing arrives on,

@@ -13,7 +13,9 @@ definitions on the pages:
 * ``oracle.attention``  -- per-document bidirectional softmax attention,
                            evaluated with a two-pass (max, then sum) softmax;
 * ``oracle.fp8``        -- the FP8 (e4m3) variant: quantisers, dequantisation
-                           and the error bound of the kernel's P rounding.
+                           and the error bound of the kernel's P rounding;
+* ``oracle.walks``      -- block selection, block-sparse attention, attention
+                           with a shared prefix.
 
 Pages cited (page title, then section):
   [PR26]   vllm.cpp PR #26 "feat(minimax-h3): port the MiniMax-H3 omni-modal
@@ -22,6 +24,7 @@ Pages cited (page title, then section):
            serving package"
 
 Parity status of each function is recorded in its docstring; every function
-here is pinned by the ``-m "not gpu"`` tests in ``tests/test_oracle_pins.py``.
+here is pinned by the ``-m "not gpu"`` tests in ``tests/test_oracle_pins.py``
+and ``tests/test_oracle_*_pins.py``.
 """
 from . import plan, prologue, attention  # noqa: F401

@@ -98,6 +98,18 @@
 // tile and query tile, P over S, issued by one thread): split into halves,
 // the per-half softmax costs measured slower than the chain they remove.
 //
+// Other key walks (template argument kWalk, bf16): the same pipeline over key
+// tiles that are not "the unit's document, in order".  The list walk
+// (h3attn_forward_sparse) takes the tiles listed for the unit's query block, so
+// the MMAs run at the dense kernel's rate on the listed tiles only; the prefix
+// walk (h3attn_forward_prefix) takes the tiles of a prefix that all documents
+// share (tensor maps of its own), then the document's.  The producer and the
+// softmax warps look each tile up (key_tile); the MMA issuer only counts
+// tiles.  Rows of the V tile past the last valid key are zeroed in shared
+// memory before the PV reads them, so that a NaN or infinity in the rows
+// behind a document or prefix (weight 0) does not reach its output.  A list
+// without a valid tile runs one fully masked tile: o = 0, lse = -inf.
+//
 // Every mbarrier wait is bounded: on expiry the CTA raises an abort flag,
 // records a timeout in the device error word, drains its own copies and MMAs
 // with bounded waits, and leaves through the cluster barrier, where the pair
@@ -177,25 +189,106 @@ struct Bars {
   __device__ uint32_t o_staged(int i) const { return base + 8 * (25 + 2 * kGroups + i); }
 };
 
-struct UnitGeom {
-  int32_t q0, kv0, kv1, head, lo, hi, part, n_st;  // key tiles [lo, hi)
-  int32_t v_off;                                   // FP8: the document's first key in the transposed V
+// Key walks: the unit's own document (the dense forward), the tiles listed for
+// its query block, the shared prefix's tiles and then the document's.
+constexpr int kWalkDoc = 0, kWalkList = 1, kWalkPrefix = 2;
+
+// What a walk needs besides the unit.
+template <int kWalk>
+struct Walk {};
+template <>
+struct Walk<kWalkList> {
+  const int32_t* idx;   // [H, blocks, cap]
+  const int32_t* cnt;   // [H, blocks]
+  int32_t blocks, cap;
+};
+template <>
+struct Walk<kWalkPrefix> {
+  CUtensorMap tm_k, tm_v;   // the prefix's rows
+  int32_t len, tiles;
 };
 
-__device__ __forceinline__ UnitGeom unit_geom(const WorkUnit* units, int u) {
+struct UnitGeom {
+  int32_t q0, kv0, kv1, head, lo, hi, part, n_st;  // key tiles [lo, hi) of the walk
+  int32_t v_off;                                   // FP8: the document's first key in the transposed V
+  int32_t q1;                                      // end of the unit's query rows
+  const int32_t* list;                             // list walk: the query block's tiles (null: none to visit)
+};
+
+template <int kWalk>
+__device__ __forceinline__ UnitGeom unit_geom(const WorkUnit* units, int u, const Walk<kWalk>& walk) {
   const int4 w = __ldg(reinterpret_cast<const int4*>(units) + 2 * u);
   const int4 x = __ldg(reinterpret_cast<const int4*>(units) + 2 * u + 1);
   UnitGeom g;
-  g.q0 = w.x;
-  g.kv0 = w.y;
-  g.kv1 = w.z;
-  g.head = w.w;
-  g.lo = x.x;
-  g.hi = x.y;
-  g.part = x.z;
-  g.v_off = x.w;
-  g.n_st = (w.x + 2 * kTileRows < w.z) ? 2 : 1;  // query tile 1 of the pair holds rows from 256 on
+  if constexpr (kWalk == kWalkDoc) {
+    g.q0 = w.x;
+    g.kv0 = w.y;
+    g.kv1 = w.z;
+    g.head = w.w;
+    g.lo = x.x;
+    g.hi = x.y;
+    g.part = x.z;
+    g.v_off = x.w;
+    g.q1 = w.z;
+    g.list = nullptr;
+    g.n_st = (w.x + 2 * kTileRows < w.z) ? 2 : 1;  // query tile 1 of the pair holds rows from 256 on
+  } else {  // a WalkUnit
+    g.q0 = w.x;
+    g.q1 = w.y;
+    g.kv0 = w.z;
+    g.kv1 = w.w;
+    g.head = x.x;
+    g.part = x.w;
+    g.v_off = 0;
+    g.list = nullptr;
+    g.n_st = (w.x + 2 * kTileRows < w.y) ? 2 : 1;
+    if constexpr (kWalk == kWalkPrefix) {
+      g.lo = x.y;
+      g.hi = x.z;
+    } else {
+      // piece i of m takes entries [n i / m, n (i + 1) / m) of the block's n
+      const int64_t block = (int64_t)x.x * walk.blocks + x.y;
+      const uint32_t i = (uint32_t)x.z & 0xffffu, m = (uint32_t)x.z >> 16;
+      const uint64_t n = (uint64_t)min(max(__ldg(walk.cnt + block), 0), walk.cap);
+      g.lo = m == 1 ? 0 : (int32_t)(n * i / m);
+      g.hi = m == 1 ? (int32_t)n : (int32_t)(n * (i + 1) / m);
+      if (g.hi > g.lo)
+        g.list = walk.idx + block * walk.cap;
+      else
+        g.hi = g.lo + 1;  // nothing listed: one fully masked tile
+    }
+  }
   return g;
+}
+
+// Step j of a unit's walk: the tile's first key row, its valid keys (0 or less:
+// none, 128 or more: all), and whether it lies in the prefix.
+struct KeyTile {
+  int32_t row, rem;
+  bool prefix, bad;
+};
+template <int kWalk>
+__device__ __forceinline__ KeyTile key_tile(const UnitGeom& g, int j, const Walk<kWalk>& walk) {
+  KeyTile t{g.kv0, 0, false, false};
+  if constexpr (kWalk == kWalkDoc) {
+    t.row = g.kv0 + j * kTileRows;
+    t.rem = g.kv1 - t.row;
+  } else if constexpr (kWalk == kWalkPrefix) {
+    t.prefix = j < walk.tiles;
+    t.row = (t.prefix ? j : j - walk.tiles) * kTileRows + (t.prefix ? 0 : g.kv0);
+    t.rem = (t.prefix ? walk.len : g.kv1) - t.row;
+  } else {
+    if (g.list != nullptr) {
+      const int32_t i = __ldg(g.list + j);
+      // a tile outside the document is skipped (and reported by the producer)
+      t.bad = i < 0 || i > (g.kv1 - g.kv0 - 1) / kTileRows;
+      if (!t.bad) {
+        t.row = g.kv0 + i * kTileRows;
+        t.rem = g.kv1 - t.row;
+      }
+    }
+  }
+  return t;
 }
 
 // This CTA's half of a K tile: keys [key0 + 64 rank, +64), all 128 dims (bf16:
@@ -463,11 +556,13 @@ static __device__ __noinline__ void norm_rope_q_row(uint32_t tile, uint32_t r, c
 // kFp8: the FP8 variant -- e4m3 Q, K, V (V transposed, keys contiguous) with
 // scales (per query row, per key tile, per V channel), kind::f8f6f4 MMAs,
 // P rounded to e4m3; everything else as the bf16 kernel.
-template <bool kFp8>
+// kWalk: the key tiles a unit visits (bf16 only where not its own document).
+template <bool kFp8, int kWalk>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-                       ForwardArgs a, int o_tma) {
+                       ForwardArgs a, int o_tma, const __grid_constant__ Walk<kWalk> walk) {
+  static_assert(!kFp8 || kWalk == kWalkDoc, "the FP8 pipeline walks documents");
   using C = Cfg<kFp8>;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = dev::smem_u32(smem_raw);
@@ -513,6 +608,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     dev::tma_prefetch_desc(&tm_q);
     dev::tma_prefetch_desc(&tm_k);
     dev::tma_prefetch_desc(&tm_v);
+    if constexpr (kWalk == kWalkPrefix) {
+      dev::tma_prefetch_desc(&walk.tm_k);
+      dev::tma_prefetch_desc(&walk.tm_v);
+    }
   }
   if (warp == kMmaWarp) {
     dev::tmem_alloc_pair(dev::smem_u32(tmem_slot), kTmemCols);
@@ -536,7 +635,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       int k = 0;
       for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-        const UnitGeom g = unit_geom(a.units, u);
+        const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
 #pragma unroll 1
         for (int s = 0; s < 2 && s < g.n_st; ++s) {
           const int i = 2 * (k & 1) + s;
@@ -550,7 +649,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int w = 0; w < 4; ++w) {
               const int32_t row0 = base_row + 32 * w;
-              if (row0 + 31 >= g.kv1) break;  // (the softmax warps' own test)
+              if (row0 + 31 >= g.q1) break;  // (the softmax warps' own test)
               dev::tma_store_2d(&tm_o, tile + 32u * w * 128u, g.head * kHeadDim, row0);
               dev::tma_store_2d(&tm_o, tile + kQHalfBytes + 32u * w * 128u, g.head * kHeadDim + 64, row0);
               any = true;
@@ -588,9 +687,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ++q_use[i];
         }
       };
+      // the tensor map of a walk's tile
+      auto k_map = [&](const KeyTile& t) {
+        if constexpr (kWalk == kWalkPrefix) return t.prefix ? &walk.tm_k : &tm_k;
+        return &tm_k;
+      };
+      auto v_map = [&](const KeyTile& t) {
+        if constexpr (kWalk == kWalkPrefix) return t.prefix ? &walk.tm_v : &tm_v;
+        return &tm_v;
+      };
       int k = 0;
       for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-        const UnitGeom g = unit_geom(a.units, u);
+        const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
         const bool has_next = u + 1 < u_end;
         // Key/value groups: group 0 is the first unit's first K tile (ring slot
         // 0); group n >= 1 is V(j) with the next K tile -- K(j+1), or the next
@@ -602,33 +710,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = dev::mbar_wait(bars.kv_empty(0), 1, abort_flag, a.err, kTimeoutNs);
           if (!ok) break;
           dev::mbar_arrive_expect_tx(bars.kv_full(0), C::SlotBytes);
-          load_k_half<kFp8>(sbase + C::SmemKV, &tm_k, bars.kv_full(0), g.head, g.kv0 + g.lo * kTileRows, rank,
-                            pol_kv);
+          if constexpr (kWalk == kWalkDoc) {
+            load_k_half<kFp8>(sbase + C::SmemKV, &tm_k, bars.kv_full(0), g.head, g.kv0 + g.lo * kTileRows, rank,
+                              pol_kv);
+          } else {
+            const KeyTile t = key_tile<kWalk>(g, g.lo, walk);
+            load_k_half<kFp8>(sbase + C::SmemKV, k_map(t), bars.kv_full(0), g.head, t.row, rank, pol_kv);
+          }
           grp = 1;
         }
         for (int j = g.lo; ok && j < g.hi; ++j) {
           bool has_k = j + 1 < g.hi;
           int k_head = g.head;
-          int32_t k_row = g.kv0 + (j + 1) * kTileRows;
+          KeyTile vt, kt;
+          if constexpr (kWalk == kWalkDoc) {
+            kt.row = g.kv0 + (j + 1) * kTileRows;
+          } else {
+            vt = key_tile<kWalk>(g, j, walk);
+            if (has_k) kt = key_tile<kWalk>(g, j + 1, walk);
+            if (vt.bad && rank == 0) atomicExch(a.err, kErrBlockIndex);
+          }
           if (!has_k && has_next) {
-            const UnitGeom n = unit_geom(a.units, u + 1);
+            const UnitGeom n = unit_geom<kWalk>(a.units, u + 1, walk);
             has_k = true;
             k_head = n.head;
-            k_row = n.kv0 + n.lo * kTileRows;
+            if constexpr (kWalk == kWalkDoc)
+              kt.row = n.kv0 + n.lo * kTileRows;
+            else
+              kt = key_tile<kWalk>(n, n.lo, walk);
           }
           const uint32_t b = grp % kGroups;
           ok = dev::mbar_wait(bars.kv_empty(b), ((grp / kGroups) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
           if (!ok) break;
           dev::mbar_arrive_expect_tx(bars.kv_full(b), has_k ? 2 * C::SlotBytes : C::SlotBytes);
-          load_v_half<kFp8>(sbase + C::SmemKV + ((2 * grp - 1) % kSlots) * C::SlotBytes, &tm_v, bars.kv_full(b),
-                            g.head, (kFp8 ? g.v_off : g.kv0) + j * kTileRows, rank, pol_kv);
-          if (has_k)
-            load_k_half<kFp8>(sbase + C::SmemKV + ((2 * grp) % kSlots) * C::SlotBytes, &tm_k, bars.kv_full(b),
-                              k_head, k_row, rank, pol_kv);
+          if constexpr (kWalk == kWalkDoc)
+            load_v_half<kFp8>(sbase + C::SmemKV + ((2 * grp - 1) % kSlots) * C::SlotBytes, &tm_v, bars.kv_full(b),
+                              g.head, (kFp8 ? g.v_off : g.kv0) + j * kTileRows, rank, pol_kv);
+          else
+            load_v_half<kFp8>(sbase + C::SmemKV + ((2 * grp - 1) % kSlots) * C::SlotBytes, v_map(vt), bars.kv_full(b),
+                              g.head, vt.row, rank, pol_kv);
+          if (has_k) {
+            if constexpr (kWalk == kWalkDoc)
+              load_k_half<kFp8>(sbase + C::SmemKV + ((2 * grp) % kSlots) * C::SlotBytes, &tm_k, bars.kv_full(b),
+                                k_head, kt.row, rank, pol_kv);
+            else
+              load_k_half<kFp8>(sbase + C::SmemKV + ((2 * grp) % kSlots) * C::SlotBytes, k_map(kt), bars.kv_full(b),
+                                k_head, kt.row, rank, pol_kv);
+          }
           ++grp;
           // the next unit's Q tiles, behind this unit's first group
           if constexpr (kFp8)
-            if (j == g.lo && has_next) load_q(unit_geom(a.units, u + 1), k + 1);
+            if (j == g.lo && has_next) load_q(unit_geom<kWalk>(a.units, u + 1, walk), k + 1);
         }
       }
       if (!ok) {
@@ -655,7 +787,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool issued = false;
         int k = 0;
         for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-          const UnitGeom g = unit_geom(a.units, u);
+          const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
           const uint32_t qb = 2 * (k & 1);
           // Q tiles of this unit, prepared in both CTAs (and, for the first
           // unit, the first K group landed in both)
@@ -748,7 +880,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         issued = true;
       };
       for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-        const UnitGeom g = unit_geom(a.units, u);
+        const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
         const uint32_t qb = 2 * (k & 1);
         if (k == 0) {
           // the pair's first unit: its first K tile is group 0 (ring slot 0),
@@ -767,7 +899,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // unit's last query tile sees S of half 1, so that QK comes after
         // every PV of this unit.
         const bool has_next = u + 1 < u_end;
-        const UnitGeom gn = unit_geom(a.units, has_next ? u + 1 : u);
+        const UnitGeom gn = unit_geom<kWalk>(a.units, has_next ? u + 1 : u, walk);
         const uint32_t qn = 2 * ((k + 1) & 1);
         const bool two = g.n_st == 2;
         // steady state: key tiles with a next key tile in this unit
@@ -838,7 +970,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint64_t pol_q = dev::policy_evict_first();
     int k = 0;
     for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-      const UnitGeom g = unit_geom(a.units, u);
+      const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
 #pragma unroll 1
       for (int s = 0; s < 2 && s < g.n_st; ++s) {
         const int i = 2 * (k & 1) + s;
@@ -864,7 +996,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         good = dev::mbar_wait(bars.q_full(i), q_use[i] & 1, abort_flag, a.err, kTimeoutNs);
         ++q_use[i];
-        if (!kFp8 && good && fuse_q) {
+        if (!kFp8 && kWalk == kWalkDoc && good && fuse_q) {
           const int32_t row0 = g.q0 + s * 2 * kTileRows + (int32_t)rank * kTileRows;
           const float* gain = a.gain_q + (int64_t)g.head * a.gain_head_stride;
 #pragma unroll 1
@@ -910,7 +1042,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // 32-byte output stores when every row start is 32-byte aligned
     const bool o_wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0 && (a.o_stride & 15) == 0;
     for (int u = u_begin; ok && u < u_end; ++u) {
-      const UnitGeom g = unit_geom(a.units, u);
+      const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
       const uint32_t t_unit = t0;
       t0 += g.hi - g.lo;
       if (st >= g.n_st) continue;
@@ -1028,7 +1160,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int j = g.lo; ok && j < g.hi; ++j) {
           const uint32_t t = t_unit + (j - g.lo);  // the pair's running key-tile count
           const float rsc = sl2;  // score scale in log2 units: softmax_scale log2(e)
-          const int rem = g.kv1 - (g.kv0 + j * kTileRows);
+          const int rem = key_tile<kWalk>(g, j, walk).rem;
           const uint32_t kv_bar = bars.kv_full((t + 1) % kGroups), kv_par = ((t + 1) / kGroups) & 1;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -1071,7 +1203,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               alpha = dev::ex2_approx(m_used - m_new);  // 0 on the first half of a unit (m_used = -inf)
               m_used = m_new;
             }
-            const float neg = -m_used;
+            // (a row that has seen no key yet, m_used = -inf: exponents -inf, not NaN)
+            const float neg = kWalk != kWalkDoc && m_used == -INFINITY ? 0.f : -m_used;
             float rs8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             uint32_t p[32];
 #pragma unroll
@@ -1120,6 +1253,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // (a blocking wait and the cluster-address arrive measured faster here
             // than FP8's non-blocking test and local arrive)
             if (h == 0 && checks_kv) ok = dev::mbar_wait(kv_bar, kv_par, abort_flag, a.err, kTimeoutNs) && ok;
+            if constexpr (kWalk != kWalkDoc) {
+              // The tile ends early: the rows of V behind its last valid key (this
+              // CTA's 64 dims, 128 bytes a row) are zeroed before the PV reads
+              // them, by the warp that reports the group landed.
+              if (h == 0 && warp == 0 && rem < kTileRows) {
+                ok = dev::mbar_wait(kv_bar, kv_par, abort_flag, a.err, kTimeoutNs) && ok;
+                const uint32_t v_slot = sbase + C::SmemKV + ((2 * t + 1) % kSlots) * C::SlotBytes;
+                if (ok)
+                  for (uint32_t b = (uint32_t)max(rem, 0) * 128u + lane * 16u; b < C::SlotBytes; b += 512u)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v_slot + b), "r"(0u) : "memory");
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the tensor cores
+                __syncwarp();
+              }
+            }
             if (lane == 0) dev::mbar_arrive_cluster(p_ready_remote[h]);  // P (and O) of the warp's 32 rows
             if (!__all_sync(0xffffffffu, ok)) {
               ok = false;
@@ -1146,19 +1293,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       dev::tc_fence_after();
       const int32_t local = st * 2 * kTileRows + (int32_t)rank * kTileRows + (int32_t)row_in_tile;
       const int32_t row = g.q0 + local;
-      const bool valid = row < g.kv1;
+      const bool valid = row < g.q1;
       if (g.part >= 0) {
         // A piece of a unit split along the keys: unnormalised O row, its
         // reference max (log2 units) and sum, for the merge pass.
         // (the partial buffer is a device allocation: its 512-byte rows are 32-byte aligned)
-        const size_t slot = (size_t)g.part * kUnitRows + local;
+        // (dense: slots of kUnitRows rows; other walks: part is the segment's first partial row)
+        const size_t slot = (kWalk == kWalkDoc ? (size_t)g.part * kUnitRows : (size_t)g.part) + local;
         if constexpr (!kFp8) {
           // bf16: each 32-column chunk of the warp's 32 rows goes through its
           // rows of the unit's Q slot (free: the slot is released only after
           // this warp reports), so that every global store writes whole
           // 128-byte row segments: a store instruction covers 4 rows.
           const uint32_t stage = sbase + C::SmemQ + q_slot * C::QTileBytes + lane_base * 128u;
-          const size_t slot0 = (size_t)g.part * kUnitRows + (size_t)(local - (int32_t)lane);
+          const size_t slot0 = slot - lane;
           const int32_t row_first = g.q0 + local - (int32_t)lane;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -1181,7 +1329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                            : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                            : "r"(stage + r * 128u + ((q ^ (r & 7u)) << 4))
                            : "memory");
-              if (row_first + (int32_t)r < g.kv1)
+              if (row_first + (int32_t)r < g.q1)
                 *reinterpret_cast<uint4*>(a.part_o + (slot0 + r) * kHeadDim + c * 32 + 4 * q) = v;
             }
             __syncwarp();
@@ -1209,7 +1357,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      const float inv = 1.f / l;
+      // (a row that saw no key: O is 0, lse = -inf)
+      const float inv = kWalk != kWalkDoc && l == 0.f ? 0.f : 1.f / l;
       bool staged = false;
       if constexpr (!kFp8) staged = o_tma != 0 && __all_sync(0xffffffffu, valid);
       if (staged) {
@@ -1324,6 +1473,107 @@ __global__ void __launch_bounds__(256, 8) attn_merge_kernel(ForwardArgs a) {
   if (lane == 0 && a.lse != nullptr) a.lse[(int64_t)m.head * a.S + row] = (M + __log2f(l)) * 0.6931471805599453f;
 }
 
+// Output rows of the list and prefix walks that no segment finishes alone: one
+// warp per query row, four dims per lane.  A row's parts are the partial rows
+// of up to two segments' pieces (a split list; the prefix part of rows shared by
+// several documents, and their own document's part) and, for documents of at
+// most kJoinOwnKeys tokens, the softmax over the document's own keys, computed
+// here in fp32 from q, k and v: a segment per such document and head would cost
+// two key-tile periods of a CTA pair for a few keys.  With M the largest part
+// maximum (log2 units): o = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
+struct JoinArgs {
+  const JoinRec* recs;
+  const int2* blocks;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  int64_t stride;
+  __nv_bfloat16* o;
+  int64_t o_stride;
+  float* lse;
+  int64_t S;
+  float scale_log2;
+  const float* part_o;
+  const float2* part_ml;
+};
+
+__device__ __forceinline__ float4 load_bf16x4(const __nv_bfloat16* p) {
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+
+__global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(JoinArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int2 blk = __ldg(a.blocks + blockIdx.x);
+  const JoinRec j = a.recs[blk.x];
+  const int32_t row = blk.y + (int32_t)(threadIdx.x >> 5);
+  if (row >= j.row1) return;
+  // own keys (inputs of the forward: they need not wait for it)
+  float m_own = -INFINITY, l_own = 0.f;
+  float4 o_own = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int n_own = j.key_hi - j.key_lo;
+  if (n_own > 0) {
+    const int64_t col = (int64_t)j.head * kHeadDim + 4 * lane;
+    const float4 q = load_bf16x4(a.q + (int64_t)row * a.stride + col);
+    float s = -INFINITY;  // lane x holds the score of key x (n_own <= 32)
+#pragma unroll 4
+    for (int x = 0; x < n_own; ++x) {
+      const float4 k = load_bf16x4(a.k + (int64_t)(j.key_lo + x) * a.stride + col);
+      float d = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+      if (x == lane) s = d * a.scale_log2;
+    }
+    m_own = s;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m_own = fmaxf(m_own, __shfl_xor_sync(0xffffffffu, m_own, off));
+    const float p = dev::ex2_approx(s - (m_own == -INFINITY ? 0.f : m_own));
+    l_own = p;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) l_own += __shfl_xor_sync(0xffffffffu, l_own, off);
+#pragma unroll 4
+    for (int x = 0; x < n_own; ++x) {
+      const float w = __shfl_sync(0xffffffffu, p, x);
+      const float4 v = load_bf16x4(a.v + (int64_t)(j.key_lo + x) * a.stride + col);
+      o_own.x = fmaf(w, v.x, o_own.x);
+      o_own.y = fmaf(w, v.y, o_own.y);
+      o_own.z = fmaf(w, v.z, o_own.z);
+      o_own.w = fmaf(w, v.w, o_own.w);
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the forward is complete and its writes visible
+  const int64_t ra = (int64_t)j.a_part + (row - j.a_row0), rb = (int64_t)j.b_part + (row - j.b_row0);
+  float M = m_own;
+#pragma unroll 4
+  for (int c = 0; c < j.n_a; ++c) M = fmaxf(M, a.part_ml[ra + (int64_t)c * j.a_rows].x);
+#pragma unroll 4
+  for (int c = 0; c < j.n_b; ++c) M = fmaxf(M, a.part_ml[rb + (int64_t)c * j.b_rows].x);
+  const float ref = M == -INFINITY ? 0.f : M;
+  const float w_own = dev::ex2_approx(m_own - ref);
+  float4 acc = make_float4(w_own * o_own.x, w_own * o_own.y, w_own * o_own.z, w_own * o_own.w);
+  float l = w_own * l_own;
+  const auto add = [&](int64_t r) {
+    const float2 ml = a.part_ml[r];
+    const float w = dev::ex2_approx(ml.x - ref);
+    const float4 o = reinterpret_cast<const float4*>(a.part_o + r * kHeadDim)[lane];
+    acc.x = fmaf(w, o.x, acc.x);
+    acc.y = fmaf(w, o.y, acc.y);
+    acc.z = fmaf(w, o.z, acc.z);
+    acc.w = fmaf(w, o.w, acc.w);
+    l = fmaf(w, ml.y, l);
+  };
+#pragma unroll 4
+  for (int c = 0; c < j.n_a; ++c) add(ra + (int64_t)c * j.a_rows);
+#pragma unroll 4
+  for (int c = 0; c < j.n_b; ++c) add(rb + (int64_t)c * j.b_rows);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  __nv_bfloat16* dst = a.o + (int64_t)row * a.o_stride + j.head * kHeadDim + 4 * lane;
+  *reinterpret_cast<uint2*>(dst) =
+      make_uint2(dev::pack_bf16x2(acc.x * inv, acc.y * inv), dev::pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (lane == 0 && a.lse != nullptr) a.lse[(int64_t)j.head * a.S + row] = (M + __log2f(l)) * 0.6931471805599453f;
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -1360,22 +1610,37 @@ bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType type, uint32
   return true;
 }
 
-template <bool kFp8>
+template <bool kFp8, int kWalk>
 cudaError_t set_smem_attr() {
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(attn_fwd_tc_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    attr = cudaFuncSetAttribute(attn_fwd_tc_kernel<kFp8, kWalk>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)Cfg<kFp8>::SmemAlloc);
   });
   return attr;
+}
+
+// A kernel launched as a programmatic dependent of the forward before it.
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <bool kFp8>
 cudaError_t launch_pairs(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
                          int o_tma, const ForwardArgs& a, int device, int num_sms, cudaStream_t stream,
                          std::string* why) {
-  cudaError_t e = set_smem_attr<kFp8>();
+  cudaError_t e = set_smem_attr<kFp8, kWalkDoc>();
   if (e != cudaSuccess) {
     if (why) *why = "cudaFuncSetAttribute(max dynamic shared memory) failed";
     return e;
@@ -1386,20 +1651,12 @@ cudaError_t launch_pairs(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
     if (why) *why = "the work list has no CTA pairs";
     return cudaErrorInvalidValue;
   }
-  attn_fwd_tc_kernel<kFp8><<<2 * a.n_pairs, kThreads, Cfg<kFp8>::SmemAlloc, stream>>>(mq, mk, mv, mo, a, o_tma);
+  attn_fwd_tc_kernel<kFp8, kWalkDoc>
+      <<<2 * a.n_pairs, kThreads, Cfg<kFp8>::SmemAlloc, stream>>>(mq, mk, mv, mo, a, o_tma, Walk<kWalkDoc>{});
   e = cudaGetLastError();
   if (e != cudaSuccess || a.n_merges == 0) return e;
   const int64_t warps = (int64_t)a.n_merges * kUnitRows;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((warps + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_merge_kernel, a);
+  e = launch_dependent(attn_merge_kernel, (unsigned)((warps + 7) / 8), 256u, stream, a);
   if (e != cudaSuccess && why) *why = "the merge launch failed";
   return e;
 }
@@ -1418,12 +1675,12 @@ int forward_slots(int device, int num_sms) {
     int prev = -1;
     cudaGetDevice(&prev);
     if (prev != device) cudaSetDevice(device);
-    if (set_smem_attr<false>() == cudaSuccess) {
+    if (set_smem_attr<false, kWalkDoc>() == cudaSuccess) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(2 * (num_sms / 2 > 0 ? num_sms / 2 : 1));
       cfg.blockDim = dim3(kThreads);
       cfg.dynamicSmemBytes = Cfg<false>::SmemAlloc;
-      if (cudaOccupancyMaxActiveClusters(&n, attn_fwd_tc_kernel<false>, &cfg) != cudaSuccess) n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, attn_fwd_tc_kernel<false, kWalkDoc>, &cfg) != cudaSuccess) n = 0;
     }
     cudaGetLastError();
     if (prev != device && prev >= 0) cudaSetDevice(prev);
@@ -1432,22 +1689,86 @@ int forward_slots(int device, int num_sms) {
   return slots[device];
 }
 
+namespace {
+
+// Tensor maps of the bf16 forward's q, k, v and o (o_tma: whether O tiles go
+// out by TMA: its rows allow a tensor map, 16-byte aligned base and row stride;
+// otherwise the epilogue stores them directly).
+struct ForwardMaps {
+  CUtensorMap q, k, v, o;
+  int o_tma;
+};
+bool make_forward_maps(const ForwardArgs& a, ForwardMaps* m, std::string* why) {
+  const uint64_t inner = (uint64_t)a.H * kHeadDim, row = (uint64_t)a.qkv_stride * 2;
+  if (!make_map(&m->q, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, a.S, row, kTileRows, why) ||
+      !make_map(&m->k, a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, a.S, row, kTileRows / 2, why) ||
+      !make_map(&m->v, a.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, a.S, row, kTileRows, why))
+    return false;
+  std::memset(&m->o, 0, sizeof(m->o));
+  m->o_tma = (reinterpret_cast<uintptr_t>(a.o) & 15u) == 0 && (a.o_stride & 7) == 0 &&
+             make_map(&m->o, a.o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, a.S, (uint64_t)a.o_stride * 2, 32,
+                      nullptr);
+  return true;
+}
+
+// The forward over another walk, then the join of the rows it left in parts.
+template <int kWalk>
+cudaError_t launch_walk(const ForwardMaps& m, const ForwardArgs& a, const WalkArgs& w, const Walk<kWalk>& walk,
+                        cudaStream_t stream, std::string* why) {
+  cudaError_t e = set_smem_attr<false, kWalk>();
+  if (e != cudaSuccess) {
+    if (why) *why = "cudaFuncSetAttribute(max dynamic shared memory) failed";
+    return e;
+  }
+  attn_fwd_tc_kernel<false, kWalk>
+      <<<2 * a.n_pairs, kThreads, Cfg<false>::SmemAlloc, stream>>>(m.q, m.k, m.v, m.o, a, m.o_tma, walk);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || w.n_join_blocks == 0) return e;
+  const JoinArgs j{w.joins,
+                   w.join_blocks,
+                   static_cast<const __nv_bfloat16*>(a.q),
+                   static_cast<const __nv_bfloat16*>(a.k),
+                   static_cast<const __nv_bfloat16*>(a.v),
+                   a.qkv_stride,
+                   static_cast<__nv_bfloat16*>(a.o),
+                   a.o_stride,
+                   a.lse,
+                   a.S,
+                   a.scale_log2,
+                   a.part_o,
+                   a.part_ml};
+  e = launch_dependent(attn_join_kernel, (unsigned)w.n_join_blocks, 32u * kJoinRows, stream, j);
+  if (e != cudaSuccess && why) *why = "the join launch failed";
+  return e;
+}
+
+}  // namespace
+
 cudaError_t launch_forward(const ForwardArgs& a, int device, int num_sms, cudaStream_t stream, std::string* why) {
   if (a.n_units == 0) return cudaSuccess;
-  CUtensorMap mq, mk, mv;
-  const uint64_t inner = (uint64_t)a.H * kHeadDim, row = (uint64_t)a.qkv_stride * 2;
-  if (!make_map(&mq, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, a.S, row, kTileRows, why) ||
-      !make_map(&mk, a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, a.S, row, kTileRows / 2, why) ||
-      !make_map(&mv, a.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, a.S, row, kTileRows, why))
+  ForwardMaps m;
+  if (!make_forward_maps(a, &m, why)) return cudaErrorInvalidValue;
+  return launch_pairs<false>(m.q, m.k, m.v, m.o, m.o_tma, a, device, num_sms, stream, why);
+}
+
+cudaError_t launch_forward_list(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why) {
+  ForwardMaps m;
+  if (!make_forward_maps(a, &m, why)) return cudaErrorInvalidValue;
+  const Walk<kWalkList> walk{w.block_idx, w.block_cnt, w.n_q_blocks, w.max_blocks};
+  return launch_walk<kWalkList>(m, a, w, walk, stream, why);
+}
+
+cudaError_t launch_forward_prefix(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why) {
+  ForwardMaps m;
+  if (!make_forward_maps(a, &m, why)) return cudaErrorInvalidValue;
+  Walk<kWalkPrefix> walk;
+  walk.len = w.prefix_len;
+  walk.tiles = (int32_t)(((int64_t)w.prefix_len + kTileRows - 1) / kTileRows);
+  const uint64_t inner = (uint64_t)a.H * kHeadDim, row = (uint64_t)w.prefix_stride * 2, n = (uint64_t)w.prefix_len;
+  if (!make_map(&walk.tm_k, w.k_prefix, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, n, row, kTileRows / 2, why) ||
+      !make_map(&walk.tm_v, w.v_prefix, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, n, row, kTileRows, why))
     return cudaErrorInvalidValue;
-  // O tiles go out by TMA when its rows allow a tensor map (16-byte aligned
-  // base and row stride); otherwise the epilogue stores them directly
-  CUtensorMap mo;
-  std::memset(&mo, 0, sizeof(mo));
-  const bool o_tma = (reinterpret_cast<uintptr_t>(a.o) & 15u) == 0 && (a.o_stride & 7) == 0 &&
-                     make_map(&mo, a.o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, a.S, (uint64_t)a.o_stride * 2, 32,
-                              nullptr);
-  return launch_pairs<false>(mq, mk, mv, mo, o_tma ? 1 : 0, a, device, num_sms, stream, why);
+  return launch_walk<kWalkPrefix>(m, a, w, walk, stream, why);
 }
 
 cudaError_t launch_forward_fp8(const ForwardArgs& a, int device, int num_sms, cudaStream_t stream,

@@ -1,6 +1,7 @@
 // The C-ABI entry points: argument validation, plan lifetime, launches.
 // Every function returns a status and never throws; a failing call leaves a
 // message in a thread-local buffer (h3attn_last_error).
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -77,6 +78,39 @@ h3attn_status cuda_fail(cudaError_t e, const char* what) {
   return fail(H3ATTN_ECUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
+void free_walk(WalkPlan* w) {
+  if (w->d_units) cudaFree(w->d_units);
+  if (w->d_joins) cudaFree(w->d_joins);
+  if (w->d_part_o) cudaFree(w->d_part_o);
+  if (w->d_part_ml) cudaFree(w->d_part_ml);
+  w->d_units = nullptr;
+  w->d_joins = nullptr;
+  w->d_part_o = nullptr;
+  w->d_part_ml = nullptr;
+}
+
+// Device copies of a walk's lists, and its partial buffers (enqueued; the caller
+// synchronises the stream before the host lists change).
+cudaError_t upload_walk(WalkPlan* w, cudaStream_t st) {
+  const size_t units = w->units.size() * sizeof(WalkUnit), off = w->unit_off.size() * sizeof(int32_t);
+  const size_t joins = w->joins.size() * sizeof(JoinRec), blocks = w->join_blocks.size() * sizeof(int2);
+  cudaError_t e = cudaMalloc(&w->d_units, units + off);
+  if (e == cudaSuccess && joins > 0) e = cudaMalloc(&w->d_joins, joins + blocks);
+  if (e == cudaSuccess && w->part_rows > 0) {
+    e = cudaMalloc(&w->d_part_o, (size_t)w->part_rows * kHeadDim * sizeof(float));
+    if (e == cudaSuccess) e = cudaMalloc(&w->d_part_ml, (size_t)w->part_rows * sizeof(float2));
+  }
+  if (e == cudaSuccess) e = cudaMemcpyAsync(w->d_units, w->units.data(), units, cudaMemcpyHostToDevice, st);
+  if (e == cudaSuccess)
+    e = cudaMemcpyAsync(w->d_units + w->units.size(), w->unit_off.data(), off, cudaMemcpyHostToDevice, st);
+  if (e == cudaSuccess && joins > 0) {
+    e = cudaMemcpyAsync(w->d_joins, w->joins.data(), joins, cudaMemcpyHostToDevice, st);
+    if (e == cudaSuccess)
+      e = cudaMemcpyAsync(w->d_joins + w->joins.size(), w->join_blocks.data(), blocks, cudaMemcpyHostToDevice, st);
+  }
+  return e;
+}
+
 void free_plan_device(Plan* p) {
   if (p->d_cu) cudaFree(p->d_cu);
   if (p->d_rope) cudaFree(p->d_rope);
@@ -94,6 +128,14 @@ void free_plan_device(Plan* p) {
   p->d_rope = nullptr;
   p->d_units = nullptr;
   p->d_err = nullptr;
+  free_walk(&p->sparse.walk);
+  free_walk(&p->prefix.walk);
+  if (p->sparse.d_groups) cudaFree(p->sparse.d_groups);
+  if (p->sparse.d_q_sum) cudaFree(p->sparse.d_q_sum);
+  if (p->sparse.d_k_mean) cudaFree(p->sparse.d_k_mean);
+  p->sparse.d_groups = nullptr;
+  p->sparse.d_q_sum = nullptr;
+  p->sparse.d_k_mean = nullptr;
 }
 
 // Device copy of the plan's unit_off (stored after the segment list).
@@ -101,8 +143,97 @@ const int32_t* unit_offsets(const Plan* p) {
   return reinterpret_cast<const int32_t*>(p->d_units + p->units_host.size());
 }
 
+// Uploads a walk's lists; `more` allocates and uploads what belongs with them.
+template <class More>
+h3attn_status attach_walk(WalkPlan* w, const char* what, void* cuda_stream, More more) {
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  cudaError_t e = upload_walk(w, st);
+  if (e == cudaSuccess) e = more(st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess) {
+    w->set = true;
+    return H3ATTN_OK;
+  }
+  free_walk(w);
+  return e == cudaErrorMemoryAllocation ? fail(H3ATTN_ENOMEM, "cudaMalloc failed for the plan's %s list", what)
+                                        : cuda_fail(e, what);
+}
+
 h3attn_status check_plan(h3attn_plan_t plan) {
   if (plan == nullptr) return fail(H3ATTN_EINVAL, "plan is NULL");
+  return H3ATTN_OK;
+}
+
+// True when byte ranges [a, a + na) and [b, b + nb) share a byte.
+bool ranges_overlap(const void* a, uintptr_t na, const void* b, uintptr_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks of the forward's tensors shared by h3attn_forward and the forwards
+// over other key walks.
+h3attn_status check_forward_io(const Plan* plan, const void* q, const void* k, const void* v, int64_t qkv_row_stride,
+                               const void* o, int64_t o_row_stride, float softmax_scale, const float* lse_out) {
+  if (!q || !k || !v || !o) return fail(H3ATTN_EINVAL, "NULL q/k/v/o pointer");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o))
+    return fail(H3ATTN_EINVAL, "q/k/v/o must be 16-byte aligned");
+  if (lse_out && !aligned4(lse_out)) return fail(H3ATTN_EINVAL, "lse_out must be 4-byte aligned");
+  const int64_t width = (int64_t)plan->num_heads * kHeadDim;
+  if (qkv_row_stride < width || o_row_stride < width || (qkv_row_stride % 8) || (o_row_stride % 8))
+    return fail(H3ATTN_EINVAL, "row strides must be >= H*128 = %lld and multiples of 8 (got %lld, %lld)",
+                (long long)width, (long long)qkv_row_stride, (long long)o_row_stride);
+  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f))
+    return fail(H3ATTN_EINVAL, "softmax_scale must be finite and > 0");
+  const int64_t S = plan->S;
+  const int32_t H = plan->num_heads;
+  const void* ins[3] = {q, k, v};
+  for (int i = 0; i < 3; ++i)
+    if (may_overlap(o, o_row_stride, ins[i], qkv_row_stride, S, H))
+      return fail(H3ATTN_EINVAL, "o overlaps %c", "qkv"[i]);
+  if (lse_out) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(lse_out), hi = lo + (uintptr_t)S * H * 4;
+    const Extent eo = extent_of(o, S, H, o_row_stride);
+    if (!(hi <= eo.lo || eo.hi <= lo)) return fail(H3ATTN_EINVAL, "lse_out overlaps o");
+  }
+  return H3ATTN_OK;
+}
+
+// lse_out against the inputs that the other walks read while they write it.
+h3attn_status check_lse_inputs(const Plan* plan, const void* q, const void* k, const void* v, int64_t qkv_row_stride,
+                               const float* lse_out) {
+  if (!lse_out) return H3ATTN_OK;
+  const void* ins[3] = {q, k, v};
+  for (int i = 0; i < 3; ++i) {
+    const Extent e = extent_of(ins[i], plan->S, plan->num_heads, qkv_row_stride);
+    if (ranges_overlap(lse_out, (uintptr_t)plan->S * plan->num_heads * 4, ins[i], e.hi - e.lo))
+      return fail(H3ATTN_EINVAL, "lse_out overlaps %c", "qkv"[i]);
+  }
+  return H3ATTN_OK;
+}
+
+// A packed layout given on the host, for the host listings of work.
+h3attn_status check_layout(const int32_t* cu_seqlens, int32_t n_docs, int32_t num_heads, int32_t n_pairs) {
+  if (n_docs < 1) return fail(H3ATTN_EINVAL, "n_docs must be >= 1 (got %d)", n_docs);
+  if (num_heads < 1) return fail(H3ATTN_EINVAL, "num_heads must be >= 1 (got %d)", num_heads);
+  if (n_pairs < 1 || n_pairs > 1024) return fail(H3ATTN_EINVAL, "n_pairs must be in [1, 1024] (got %d)", n_pairs);
+  if (cu_seqlens[0] != 0) return fail(H3ATTN_EINVAL, "cu_seqlens[0] must be 0");
+  for (int32_t d = 0; d < n_docs; ++d)
+    if (cu_seqlens[d + 1] <= cu_seqlens[d])
+      return fail(H3ATTN_EINVAL, "document %d is empty or cu_seqlens is not increasing", d);
+  return H3ATTN_OK;
+}
+
+// Sizes shared by the calls that set a list and the host listing.
+h3attn_status check_list_sizes(int32_t q_block, int32_t max_blocks) {
+  if (q_block != 256 && q_block != 512) return fail(H3ATTN_EINVAL, "q_block must be 256 or 512 (got %d)", q_block);
+  if (max_blocks < 1 || max_blocks > (1 << 20))
+    return fail(H3ATTN_EINVAL, "max_blocks must be in [1, 2^20] (got %d)", max_blocks);
+  return H3ATTN_OK;
+}
+h3attn_status check_prefix_len(int32_t prefix_len) {
+  if (prefix_len < 1) return fail(H3ATTN_EINVAL, "prefix_len must be >= 1 (got %d)", prefix_len);
   return H3ATTN_OK;
 }
 
@@ -313,28 +444,10 @@ static h3attn_status forward_impl(h3attn_plan_t plan, const void* q, const void*
                                   int64_t qkv_row_stride, void* o, int64_t o_row_stride, float softmax_scale,
                                   float* lse_out, const float* gain_q, int64_t gain_head_stride, float eps,
                                   void* cuda_stream) {
-  if (!q || !k || !v || !o) return fail(H3ATTN_EINVAL, "NULL q/k/v/o pointer");
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o))
-    return fail(H3ATTN_EINVAL, "q/k/v/o must be 16-byte aligned");
-  if (lse_out && (reinterpret_cast<uintptr_t>(lse_out) & 3u))
-    return fail(H3ATTN_EINVAL, "lse_out must be 4-byte aligned");
-  const int64_t width = (int64_t)plan->num_heads * kHeadDim;
-  if (qkv_row_stride < width || o_row_stride < width || (qkv_row_stride % 8) || (o_row_stride % 8))
-    return fail(H3ATTN_EINVAL, "row strides must be >= H*128 = %lld and multiples of 8 (got %lld, %lld)",
-                (long long)width, (long long)qkv_row_stride, (long long)o_row_stride);
-  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f))
-    return fail(H3ATTN_EINVAL, "softmax_scale must be finite and > 0");
+  if (h3attn_status st = check_forward_io(plan, q, k, v, qkv_row_stride, o, o_row_stride, softmax_scale, lse_out))
+    return st;
   const int64_t S = plan->S;
   const int32_t H = plan->num_heads;
-  const void* ins[3] = {q, k, v};
-  for (int i = 0; i < 3; ++i)
-    if (may_overlap(o, o_row_stride, ins[i], qkv_row_stride, S, H))
-      return fail(H3ATTN_EINVAL, "o overlaps %c", "qkv"[i]);
-  if (lse_out) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(lse_out), hi = lo + (uintptr_t)S * H * 4;
-    const Extent eo = extent_of(o, S, H, o_row_stride);
-    if (!(hi <= eo.lo || eo.hi <= lo)) return fail(H3ATTN_EINVAL, "lse_out overlaps o");
-  }
   DeviceGuard g;
   cudaError_t e = g.enter(plan->device);
   if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
@@ -464,13 +577,7 @@ h3attn_status h3attn_work_list_host(const int32_t* cu_seqlens, int32_t n_docs, i
                                     int64_t* n_units, int32_t* n_pairs_used) {
   clear_error();
   if (!cu_seqlens || !n_units || !n_pairs_used) return fail(H3ATTN_EINVAL, "NULL cu_seqlens or output count");
-  if (n_docs < 1) return fail(H3ATTN_EINVAL, "n_docs must be >= 1 (got %d)", n_docs);
-  if (num_heads < 1) return fail(H3ATTN_EINVAL, "num_heads must be >= 1 (got %d)", num_heads);
-  if (n_pairs < 1 || n_pairs > 1024) return fail(H3ATTN_EINVAL, "n_pairs must be in [1, 1024] (got %d)", n_pairs);
-  if (cu_seqlens[0] != 0) return fail(H3ATTN_EINVAL, "cu_seqlens[0] must be 0");
-  for (int32_t d = 0; d < n_docs; ++d)
-    if (cu_seqlens[d + 1] <= cu_seqlens[d])
-      return fail(H3ATTN_EINVAL, "document %d is empty or cu_seqlens is not increasing", d);
+  if (h3attn_status s = check_layout(cu_seqlens, n_docs, num_heads, n_pairs)) return s;
   try {
     std::vector<WorkUnit> all, segs;
     std::vector<int32_t> v_off, off;
@@ -547,6 +654,264 @@ h3attn_status h3attn_forward_fp8(h3attn_plan_t plan, const void* q8, const void*
   return H3ATTN_OK;
 }
 
+h3attn_status h3attn_plan_set_sparse(h3attn_plan_t plan, int32_t q_block, int32_t max_blocks, void* cuda_stream) {
+  clear_error();
+  if (h3attn_status s = check_plan(plan)) return s;
+  if (h3attn_status s = check_list_sizes(q_block, max_blocks)) return s;
+  SparsePlan& sp = plan->sparse;
+  if (sp.walk.set) return fail(H3ATTN_EINVAL, "the plan's sparse lists are already set");
+  DeviceGuard g;
+  cudaError_t e = g.enter(plan->device);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+  try {
+    const int32_t* cu = plan->cu_host.data();
+    sp.walk = WalkPlan();
+    const std::string why = build_list_walk(cu, plan->n_docs, plan->num_heads, q_block, max_blocks,
+                                            forward_slots(plan->device, plan->num_sms), sp.walk);
+    if (!why.empty()) return fail(H3ATTN_EINVAL, "%s", why.c_str());
+    sp.q_block = q_block;
+    sp.max_blocks = max_blocks;
+    sp.n_q_blocks = 0;
+    sp.max_tiles = 0;
+    sp.groups.clear();
+    for (int32_t d = 0; d < plan->n_docs; ++d)
+      sp.max_tiles = std::max(sp.max_tiles, (cu[d + 1] - cu[d] + kKeyTile - 1) / kKeyTile);
+    const int32_t warps = select_warps(sp.max_tiles);
+    int32_t tile0 = 0;
+    for (int32_t d = 0; d < plan->n_docs; ++d) {
+      const int32_t L = cu[d + 1] - cu[d], blocks = (L + q_block - 1) / q_block, tiles = (L + kKeyTile - 1) / kKeyTile;
+      for (int32_t i = 0; i < blocks; i += warps)
+        sp.groups.push_back(SelectGroup{sp.n_q_blocks + i, std::min(warps, blocks - i), tile0, tiles, i, {0, 0, 0}});
+      sp.n_q_blocks += blocks;
+      tile0 += tiles;
+    }
+  } catch (const std::bad_alloc&) {
+    return fail(H3ATTN_ENOMEM, "host allocation failed while building the sparse lists");
+  }
+  const size_t rows = (size_t)plan->num_heads * plan->ktiles_host.size() * kHeadDim;
+  const size_t group_bytes = sp.groups.size() * sizeof(SelectGroup);
+  const h3attn_status s = attach_walk(&sp.walk, "sparse", cuda_stream, [&](cudaStream_t st) {
+    cudaError_t m = cudaMalloc(&sp.d_groups, group_bytes);
+    if (m == cudaSuccess) m = cudaMalloc(&sp.d_q_sum, rows * sizeof(float2));
+    if (m == cudaSuccess) m = cudaMalloc(&sp.d_k_mean, rows * sizeof(float));
+    if (m == cudaSuccess) m = cudaMemcpyAsync(sp.d_groups, sp.groups.data(), group_bytes, cudaMemcpyHostToDevice, st);
+    return m;
+  });
+  if (s != H3ATTN_OK) {
+    if (sp.d_groups) cudaFree(sp.d_groups);
+    if (sp.d_q_sum) cudaFree(sp.d_q_sum);
+    if (sp.d_k_mean) cudaFree(sp.d_k_mean);
+    sp = SparsePlan();
+  }
+  return s;
+}
+
+static h3attn_status check_sparse(h3attn_plan_t plan) {
+  if (h3attn_status s = check_plan(plan)) return s;
+  if (!plan->sparse.walk.set) return fail(H3ATTN_EINVAL, "h3attn_plan_set_sparse has not been called on this plan");
+  return H3ATTN_OK;
+}
+
+// The lists' pointers against a tensor of `bytes` bytes at p.
+static bool lists_overlap(const Plan* plan, const int32_t* idx, const int32_t* cnt, const void* p, uintptr_t bytes) {
+  const uintptr_t n = (uintptr_t)plan->num_heads * plan->sparse.n_q_blocks * 4;
+  return ranges_overlap(idx, n * plan->sparse.max_blocks, p, bytes) || ranges_overlap(cnt, n, p, bytes);
+}
+
+h3attn_status h3attn_plan_sparse_info(h3attn_plan_t plan, int32_t* q_block, int32_t* max_blocks, int32_t* n_q_blocks) {
+  clear_error();
+  if (h3attn_status s = check_sparse(plan)) return s;
+  if (q_block) *q_block = plan->sparse.q_block;
+  if (max_blocks) *max_blocks = plan->sparse.max_blocks;
+  if (n_q_blocks) *n_q_blocks = plan->sparse.n_q_blocks;
+  return H3ATTN_OK;
+}
+
+h3attn_status h3attn_block_select(h3attn_plan_t plan, const void* q_hat, const void* k_hat, int64_t qkv_row_stride,
+                                  int32_t keep, int32_t keep_own, int32_t* block_idx, int32_t* block_cnt,
+                                  void* cuda_stream) {
+  clear_error();
+  if (h3attn_status s = check_sparse(plan)) return s;
+  const SparsePlan& sp = plan->sparse;
+  if (!q_hat || !k_hat || !block_idx || !block_cnt) return fail(H3ATTN_EINVAL, "NULL tensor or list pointer");
+  if (!aligned16(q_hat) || !aligned16(k_hat)) return fail(H3ATTN_EINVAL, "q_hat and k_hat must be 16-byte aligned");
+  if (!aligned4(block_idx) || !aligned4(block_cnt)) return fail(H3ATTN_EINVAL, "lists must be 4-byte aligned");
+  const int64_t width = (int64_t)plan->num_heads * kHeadDim;
+  if (qkv_row_stride < width || (qkv_row_stride % 8))
+    return fail(H3ATTN_EINVAL, "row stride must be >= H*128 = %lld and a multiple of 8", (long long)width);
+  if (keep < 1 || keep > sp.max_blocks)
+    return fail(H3ATTN_EINVAL, "keep must be in [1, max_blocks = %d] (got %d)", sp.max_blocks, keep);
+  if (sp.max_tiles > kSelectMaxTiles)
+    return fail(H3ATTN_EUNSUPPORTED, "a document of more than %d tokens cannot be scored", kSelectMaxTiles * kKeyTile);
+  const uintptr_t n = (uintptr_t)plan->num_heads * sp.n_q_blocks * 4;
+  const void* ins[2] = {q_hat, k_hat};
+  for (const void* p : ins) {
+    const Extent e = extent_of(p, plan->S, plan->num_heads, qkv_row_stride);
+    if (lists_overlap(plan, block_idx, block_cnt, p, e.hi - e.lo))
+      return fail(H3ATTN_EINVAL, "a list overlaps q_hat or k_hat");
+  }
+  if (ranges_overlap(block_idx, n * sp.max_blocks, block_cnt, n))
+    return fail(H3ATTN_EINVAL, "block_idx and block_cnt overlap");
+  DeviceGuard g;
+  cudaError_t e = g.enter(plan->device);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+  const SelectArgs a{q_hat, k_hat, qkv_row_stride, plan->num_heads, plan->d_ktiles, (int32_t)plan->ktiles_host.size(),
+                     sp.d_groups, (int32_t)sp.groups.size(), sp.max_tiles, sp.n_q_blocks, sp.q_block / kKeyTile,
+                     sp.d_q_sum, sp.d_k_mean, keep, keep_own, sp.max_blocks, block_idx, block_cnt};
+  e = launch_block_select(a, static_cast<cudaStream_t>(cuda_stream));
+  return e == cudaSuccess ? H3ATTN_OK : cuda_fail(e, "block select launch");
+}
+
+// Arguments of the forward over a walk's work list.
+static ForwardArgs walk_forward_args(const Plan* plan, const WalkPlan& w, const void* q, const void* k, const void* v,
+                                     int64_t qkv_row_stride, void* o, int64_t o_row_stride, float softmax_scale,
+                                     float* lse_out) {
+  return ForwardArgs{q, k, v, o, lse_out, qkv_row_stride, o_row_stride, plan->S, plan->num_heads,
+                     softmax_scale * 1.4426950408889634f, reinterpret_cast<const WorkUnit*>(w.d_units),
+                     (int32_t)w.units.size(), reinterpret_cast<const int32_t*>(w.d_units + w.units.size()), w.n_pairs,
+                     plan->d_err, nullptr, 0, w.d_part_o, w.d_part_ml, nullptr, 0, 0.f, nullptr};
+}
+static WalkArgs walk_args(const WalkPlan& w) {
+  WalkArgs x{};
+  x.joins = w.d_joins;
+  x.join_blocks = reinterpret_cast<const int2*>(w.d_joins + w.joins.size());
+  x.n_join_blocks = (int32_t)w.join_blocks.size();
+  return x;
+}
+
+h3attn_status h3attn_forward_sparse(h3attn_plan_t plan, const void* q, const void* k, const void* v,
+                                    int64_t qkv_row_stride, const int32_t* block_idx, const int32_t* block_cnt,
+                                    void* o, int64_t o_row_stride, float softmax_scale, float* lse_out,
+                                    void* cuda_stream) {
+  clear_error();
+  if (h3attn_status s = check_sparse(plan)) return s;
+  if (h3attn_status s = check_forward_io(plan, q, k, v, qkv_row_stride, o, o_row_stride, softmax_scale, lse_out))
+    return s;
+  if (h3attn_status s = check_lse_inputs(plan, q, k, v, qkv_row_stride, lse_out)) return s;
+  const SparsePlan& sp = plan->sparse;
+  if (!block_idx || !block_cnt) return fail(H3ATTN_EINVAL, "NULL block_idx or block_cnt");
+  if (!aligned4(block_idx) || !aligned4(block_cnt)) return fail(H3ATTN_EINVAL, "lists must be 4-byte aligned");
+  const Extent eo = extent_of(o, plan->S, plan->num_heads, o_row_stride);
+  if (lists_overlap(plan, block_idx, block_cnt, o, eo.hi - eo.lo)) return fail(H3ATTN_EINVAL, "o overlaps a list");
+  if (lse_out && lists_overlap(plan, block_idx, block_cnt, lse_out, (uintptr_t)plan->S * plan->num_heads * 4))
+    return fail(H3ATTN_EINVAL, "lse_out overlaps a list");
+  DeviceGuard g;
+  cudaError_t e = g.enter(plan->device);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+  const ForwardArgs a =
+      walk_forward_args(plan, sp.walk, q, k, v, qkv_row_stride, o, o_row_stride, softmax_scale, lse_out);
+  WalkArgs w = walk_args(sp.walk);
+  w.block_idx = block_idx;
+  w.block_cnt = block_cnt;
+  w.n_q_blocks = sp.n_q_blocks;
+  w.max_blocks = sp.max_blocks;
+  std::string why;
+  e = launch_forward_list(a, w, static_cast<cudaStream_t>(cuda_stream), &why);
+  if (e != cudaSuccess) {
+    if (!why.empty()) return fail(H3ATTN_ECUDA, "sparse forward: %s", why.c_str());
+    return cuda_fail(e, "sparse forward launch");
+  }
+  return H3ATTN_OK;
+}
+
+h3attn_status h3attn_plan_set_prefix(h3attn_plan_t plan, int32_t prefix_len, void* cuda_stream) {
+  clear_error();
+  if (h3attn_status s = check_plan(plan)) return s;
+  if (h3attn_status s = check_prefix_len(prefix_len)) return s;
+  PrefixPlan& pp = plan->prefix;
+  if (pp.walk.set) return fail(H3ATTN_EINVAL, "the plan's prefix is already set");
+  DeviceGuard g;
+  cudaError_t e = g.enter(plan->device);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+  try {
+    pp.walk = WalkPlan();
+    const std::string why = build_prefix_walk(plan->cu_host.data(), plan->n_docs, plan->num_heads, prefix_len,
+                                              forward_slots(plan->device, plan->num_sms), pp.walk);
+    if (!why.empty()) return fail(H3ATTN_EINVAL, "%s", why.c_str());
+    pp.len = prefix_len;
+  } catch (const std::bad_alloc&) {
+    return fail(H3ATTN_ENOMEM, "host allocation failed while building the prefix list");
+  }
+  return attach_walk(&pp.walk, "prefix", cuda_stream, [](cudaStream_t) { return cudaSuccess; });
+}
+
+h3attn_status h3attn_forward_prefix(h3attn_plan_t plan, const void* q, const void* k, const void* v,
+                                    int64_t qkv_row_stride, const void* k_prefix, const void* v_prefix,
+                                    int64_t prefix_row_stride, void* o, int64_t o_row_stride, float softmax_scale,
+                                    float* lse_out, void* cuda_stream) {
+  clear_error();
+  if (h3attn_status s = check_plan(plan)) return s;
+  const PrefixPlan& pp = plan->prefix;
+  if (!pp.walk.set) return fail(H3ATTN_EINVAL, "h3attn_plan_set_prefix has not been called on this plan");
+  if (h3attn_status s = check_forward_io(plan, q, k, v, qkv_row_stride, o, o_row_stride, softmax_scale, lse_out))
+    return s;
+  if (h3attn_status s = check_lse_inputs(plan, q, k, v, qkv_row_stride, lse_out)) return s;
+  if (!k_prefix || !v_prefix) return fail(H3ATTN_EINVAL, "NULL k_prefix or v_prefix");
+  if (!aligned16(k_prefix) || !aligned16(v_prefix))
+    return fail(H3ATTN_EINVAL, "k_prefix and v_prefix must be 16-byte aligned");
+  const int64_t width = (int64_t)plan->num_heads * kHeadDim;
+  if (prefix_row_stride < width || (prefix_row_stride % 8))
+    return fail(H3ATTN_EINVAL, "the prefix's row stride must be >= H*128 = %lld and a multiple of 8 (got %lld)",
+                (long long)width, (long long)prefix_row_stride);
+  const Extent eo = extent_of(o, plan->S, plan->num_heads, o_row_stride);
+  const void* pre[2] = {k_prefix, v_prefix};
+  for (const void* p : pre) {
+    const Extent ep = extent_of(p, pp.len, plan->num_heads, prefix_row_stride);
+    if (ranges_overlap(o, eo.hi - eo.lo, p, ep.hi - ep.lo)) return fail(H3ATTN_EINVAL, "o overlaps the prefix");
+    if (lse_out && ranges_overlap(lse_out, (uintptr_t)plan->S * plan->num_heads * 4, p, ep.hi - ep.lo))
+      return fail(H3ATTN_EINVAL, "lse_out overlaps the prefix");
+  }
+  DeviceGuard g;
+  cudaError_t e = g.enter(plan->device);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+  const ForwardArgs a =
+      walk_forward_args(plan, pp.walk, q, k, v, qkv_row_stride, o, o_row_stride, softmax_scale, lse_out);
+  WalkArgs w = walk_args(pp.walk);
+  w.k_prefix = k_prefix;
+  w.v_prefix = v_prefix;
+  w.prefix_stride = prefix_row_stride;
+  w.prefix_len = pp.len;
+  std::string why;
+  e = launch_forward_prefix(a, w, static_cast<cudaStream_t>(cuda_stream), &why);
+  if (e != cudaSuccess) {
+    if (!why.empty()) return fail(H3ATTN_ECUDA, "prefix forward: %s", why.c_str());
+    return cuda_fail(e, "prefix forward launch");
+  }
+  return H3ATTN_OK;
+}
+
+h3attn_status h3attn_walk_list_host(int32_t kind, const int32_t* cu_seqlens, int32_t n_docs, int32_t num_heads,
+                                    int32_t p0, int32_t p1, int32_t n_pairs, int32_t* units, int64_t units_cap,
+                                    int32_t* unit_off, int32_t* joins, int64_t joins_cap, int64_t* n_units,
+                                    int32_t* n_pairs_used, int64_t* n_joins, int64_t* n_part_rows) {
+  clear_error();
+  if (!cu_seqlens || !n_units || !n_pairs_used || !n_joins || !n_part_rows)
+    return fail(H3ATTN_EINVAL, "NULL cu_seqlens or output count");
+  if (h3attn_status s = check_layout(cu_seqlens, n_docs, num_heads, n_pairs)) return s;
+  if (kind != 0 && kind != 1) return fail(H3ATTN_EINVAL, "kind must be 0 or 1 (got %d)", kind);
+  if (h3attn_status s = kind == 0 ? check_list_sizes(p0, p1) : check_prefix_len(p0)) return s;
+  try {
+    WalkPlan w;
+    const std::string why = kind == 0 ? build_list_walk(cu_seqlens, n_docs, num_heads, p0, p1, n_pairs, w)
+                                      : build_prefix_walk(cu_seqlens, n_docs, num_heads, p0, n_pairs, w);
+    if (!why.empty()) return fail(H3ATTN_EINVAL, "%s", why.c_str());
+    *n_units = (int64_t)w.units.size();
+    *n_pairs_used = w.n_pairs;
+    *n_joins = (int64_t)w.joins.size();
+    *n_part_rows = w.part_rows;
+    if (units == nullptr) return H3ATTN_OK;
+    if (units_cap < *n_units || (joins && joins_cap < *n_joins))
+      return fail(H3ATTN_EINVAL, "capacities %lld, %lld < %lld segments, %lld joins", (long long)units_cap,
+                  (long long)joins_cap, (long long)*n_units, (long long)*n_joins);
+    std::memcpy(units, w.units.data(), w.units.size() * sizeof(WalkUnit));
+    if (unit_off) std::memcpy(unit_off, w.unit_off.data(), w.unit_off.size() * sizeof(int32_t));
+    if (joins && !w.joins.empty()) std::memcpy(joins, w.joins.data(), w.joins.size() * sizeof(JoinRec));
+  } catch (const std::bad_alloc&) {
+    return fail(H3ATTN_ENOMEM, "host allocation failed while building the work list");
+  }
+  return H3ATTN_OK;
+}
+
 h3attn_status h3attn_get_device_error(h3attn_plan_t plan, void* cuda_stream) {
   clear_error();
   if (h3attn_status s = check_plan(plan)) return s;
@@ -562,6 +927,8 @@ h3attn_status h3attn_get_device_error(h3attn_plan_t plan, void* cuda_stream) {
   cudaMemset(plan->d_err, 0, sizeof(word));
   if (word == kErrTimeout)
     return fail(H3ATTN_ETIMEOUT, "a bounded device wait ran out; the outputs of that call are invalid");
+  if (word == kErrBlockIndex)
+    return fail(H3ATTN_EINVAL, "a list of the sparse forward names a key tile outside its document (skipped)");
   return fail(H3ATTN_ECUDA, "device error word 0x%x", word);
 }
 

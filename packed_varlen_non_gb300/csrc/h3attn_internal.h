@@ -21,6 +21,7 @@ constexpr int kUnitRows = 512;      // query rows per attention work unit (a CTA
 // Device error word values (the word is cleared by h3attn_get_device_error).
 constexpr uint32_t kErrNone = 0;
 constexpr uint32_t kErrTimeout = 1;
+constexpr uint32_t kErrBlockIndex = 2;   // a listed key tile outside its document
 
 constexpr int kKeyTile = 128;      // key rows per tile
 
@@ -79,6 +80,146 @@ void build_segments(const std::vector<WorkUnit>& units, int grid, std::vector<Wo
                     std::vector<int32_t>& unit_off, int32_t* n_pairs, std::vector<MergeUnit>& merges,
                     int32_t* n_parts);
 
+// ---- other key walks (h3attn_forward_sparse, h3attn_forward_prefix) ----
+
+// A work segment of a walk other than the unit's own document: query rows
+// [q_row0, q_end) (at most kUnitRows) of one head, and the document [kv_begin,
+// kv_end) they lie in.
+//   list walk:   a = the query block, b = piece | pieces << 16: the segment
+//                takes entries [n i / m, n (i + 1) / m) of the block's n
+//                listed tiles (n is read on the device), i = piece, m = pieces
+//   prefix walk: key tiles [a, b) of the walk "the prefix's tiles, then the
+//                document's"; rows of several documents share a segment only
+//                when b is at most the prefix's tile count
+// part < 0: the segment writes the output; part >= 0: it writes unnormalised
+// rows from row `part` of the partial buffers on, for the join pass.
+struct WalkUnit {
+  int32_t q_row0;
+  int32_t q_end;
+  int32_t kv_begin;
+  int32_t kv_end;
+  int32_t head;
+  int32_t a;
+  int32_t b;
+  int32_t part;
+};
+static_assert(sizeof(WalkUnit) == sizeof(WorkUnit), "read as two 16-byte vectors");
+
+// Rows [row0, row1) of one head whose output the join pass combines from
+// partial rows: n_a pieces of the segment whose first row is a_row0, piece c of
+// row r at partial row a_part + c * a_rows + (r - a_row0); likewise n_b pieces
+// of another one (n_b may be 0); and the keys [key_lo, key_hi) of the rows'
+// document, which the join itself attends to (empty when key_lo == key_hi).
+struct JoinRec {
+  int32_t row0, row1, head, key_lo;
+  int32_t a_part, a_rows, n_a, a_row0;
+  int32_t b_part, b_rows, n_b, b_row0;
+  int32_t key_hi, pad[3];
+};
+static_assert(sizeof(JoinRec) == 64, "JoinRec is read as four 16-byte vectors");
+constexpr int kJoinRows = 8;         // rows per join block (one warp each)
+constexpr int kJoinOwnKeys = 32;     // longest document the join attends to itself
+
+struct WalkPlan {
+  bool set = false;
+  std::vector<WalkUnit> units;         // grouped by CTA pair
+  std::vector<int32_t> unit_off;       // [n_pairs + 1]
+  int32_t n_pairs = 0;
+  std::vector<JoinRec> joins;
+  std::vector<int2> join_blocks;       // (record, first row), kJoinRows rows each
+  int64_t part_rows = 0;               // partial rows of all segments
+
+  WalkUnit* d_units = nullptr;         // units, then unit_off
+  JoinRec* d_joins = nullptr;          // joins, then join_blocks
+  float* d_part_o = nullptr;           // [part_rows, 128] unnormalised O
+  float2* d_part_ml = nullptr;         // [part_rows] (reference max in log2 units, sum)
+};
+
+// The segment lists of the two walks for `grid` CTA pairs (walk_plan.cpp);
+// each returns an empty string or an error.
+std::string build_list_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads, int32_t q_block, int32_t max_blocks,
+                            int grid, WalkPlan& w);
+std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads, int32_t prefix_len, int grid,
+                              WalkPlan& w);
+
+// Up to kSelectWarps query blocks of one document, scored by one thread block.
+struct SelectGroup {
+  int32_t q0, n;          // query blocks [q0, q0 + n)
+  int32_t tile0, tiles;   // the document's key tiles [tile0, tile0 + tiles) of the plan's tile table
+  int32_t first;          // index of q0 within its document
+  int32_t pad[3];
+};
+constexpr int kSelectWarps = 8;
+constexpr int32_t kSelectMaxTiles = 16384;  // key tiles of the longest document that can be scored
+// Query blocks per scoring block: each keeps 8 bytes per key tile in shared memory.
+inline int select_warps(int32_t max_tiles) {
+  const int n = 160 * 1024 / (8 * (max_tiles > 0 ? max_tiles : 1));
+  return n < 1 ? 1 : (n > kSelectWarps ? kSelectWarps : n);
+}
+
+struct SparsePlan {
+  WalkPlan walk;
+  int32_t q_block = 0;
+  int32_t max_blocks = 0;
+  int32_t n_q_blocks = 0;              // over all documents
+  int32_t max_tiles = 0;               // key tiles of the longest document
+  std::vector<SelectGroup> groups;
+  SelectGroup* d_groups = nullptr;
+  float2* d_q_sum = nullptr;           // [H, tiles, 128] sums of q-hat rows (high, low)
+  float* d_k_mean = nullptr;           // [H, tiles, 128] means of k-hat rows
+};
+
+struct PrefixPlan {
+  WalkPlan walk;
+  int32_t len = 0;
+};
+
+// Placement core shared by the lists (plan.cpp): segment i, in list order,
+// goes to the pair with the least load so far, ties to the lower pair.
+template <class Cost>
+void assign_pairs(size_t n, Cost cost, int G, int32_t* pair_of, int64_t* load, int32_t* heap) {
+  // min-heap of pair indices ordered by (load, index); all loads start at 0,
+  // so the identity order is already a heap
+  for (int p = 0; p < G; ++p) {
+    load[p] = 0;
+    heap[p] = p;
+  }
+  auto before = [load](int32_t a, int32_t b) { return load[a] != load[b] ? load[a] < load[b] : a < b; };
+  for (size_t i = 0; i < n; ++i) {
+    const int32_t p = heap[0];
+    pair_of[i] = p;
+    load[p] += cost(i);
+    for (int c = 0;;) {
+      const int l = 2 * c + 1, r = l + 1;
+      int m = c;
+      if (l < G && before(heap[l], heap[m])) m = l;
+      if (r < G && before(heap[r], heap[m])) m = r;
+      if (m == c) break;
+      const int32_t t = heap[c];
+      heap[c] = heap[m];
+      heap[m] = t;
+      c = m;
+    }
+  }
+}
+
+// Pair-major order of placed segments (keeping each pair's list order) into
+// out and unit_off [G + 1]; heap is scratch.  Returns the pairs with work: as
+// every cost is positive and ties go to the lower index, they are the leading
+// ones.
+template <class Unit>
+int32_t group_by_pair(const Unit* segs, size_t n, int G, Unit* out, int32_t* unit_off, const int32_t* pair_of,
+                      int32_t* heap) {
+  for (int p = 0; p <= G; ++p) unit_off[p] = 0;
+  for (size_t i = 0; i < n; ++i) ++unit_off[pair_of[i] + 1];
+  for (int p = 0; p < G; ++p) unit_off[p + 1] += unit_off[p];
+  for (int p = 0; p < G; ++p) heap[p] = unit_off[p];
+  for (size_t i = 0; i < n; ++i) out[heap[pair_of[i]]++] = segs[i];
+  int32_t used = 0;
+  while (used < G && unit_off[used + 1] > unit_off[used]) ++used;
+  return used;
+}
+
 struct Plan {
   int device = -1;
   int num_sms = 0;
@@ -110,6 +251,9 @@ struct Plan {
   float2* d_part_ml = nullptr;       // [n_parts, kUnitRows] (running max in log2 units, sum)
   uint32_t* d_err = nullptr;         // device error word
   int4* d_ktiles = nullptr;
+
+  SparsePlan sparse;                 // h3attn_plan_set_sparse
+  PrefixPlan prefix;                 // h3attn_plan_set_prefix
 };
 
 // Host-side plan construction (plan.cpp); returns an empty string or an error.
@@ -179,6 +323,50 @@ cudaError_t launch_forward(const ForwardArgs& a, int device, int num_sms, cudaSt
                            std::string* why);
 cudaError_t launch_forward_fp8(const ForwardArgs& a, int device, int num_sms, cudaStream_t stream,
                                std::string* why);
+
+// The forward over a list of key tiles per query block, or over a shared prefix
+// and the document (a.units, unit_off, n_pairs, part_o and part_ml are those of
+// the walk plan; a.merges is unused).
+struct WalkArgs {
+  const JoinRec* joins;
+  const int2* join_blocks;
+  int32_t n_join_blocks;
+  // list walk
+  const int32_t* block_idx;    // [H, n_q_blocks, max_blocks]
+  const int32_t* block_cnt;    // [H, n_q_blocks]
+  int32_t n_q_blocks;
+  int32_t max_blocks;
+  // prefix walk
+  const void* k_prefix;
+  const void* v_prefix;
+  int64_t prefix_stride;
+  int32_t prefix_len;
+};
+cudaError_t launch_forward_list(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why);
+cudaError_t launch_forward_prefix(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why);
+
+// Block scores and selection (block_select.cu).
+struct SelectArgs {
+  const void* q_hat;
+  const void* k_hat;
+  int64_t stride;              // row stride (elements)
+  int32_t H;
+  const int4* tiles;           // (begin, end, ...) of every document's 128-key tiles
+  int32_t n_tiles;
+  const SelectGroup* groups;
+  int32_t n_groups;
+  int32_t max_tiles;           // of one document
+  int32_t n_q_blocks;
+  int32_t tiles_per_q_block;
+  float2* q_sum;
+  float* k_mean;
+  int32_t keep;
+  int32_t keep_own;
+  int32_t max_blocks;
+  int32_t* block_idx;          // [H, n_q_blocks, max_blocks]
+  int32_t* block_cnt;          // [H, n_q_blocks]
+};
+cudaError_t launch_block_select(const SelectArgs& a, cudaStream_t stream);
 
 // FP8 (e4m3) quantisation of q-hat, k-hat and v (fp8_quant.cu).
 struct Fp8QuantArgs {

@@ -143,40 +143,8 @@ int64_t segment_cost(const WorkUnit& u) { return (int64_t)(u.tile_hi - u.tile_lo
 int32_t place_pairs(const WorkUnit* segs, size_t n, int grid, WorkUnit* out, int32_t* unit_off,
                     int32_t* pair_of, int64_t* load, int32_t* heap) {
   const int G = grid > 0 ? grid : 1;
-  // min-heap of pair indices ordered by (load, index); all loads start at 0,
-  // so the identity order is already a heap
-  for (int p = 0; p < G; ++p) {
-    load[p] = 0;
-    heap[p] = p;
-  }
-  auto before = [load](int32_t a, int32_t b) { return load[a] != load[b] ? load[a] < load[b] : a < b; };
-  for (size_t i = 0; i < n; ++i) {
-    const int32_t p = heap[0];
-    pair_of[i] = p;
-    load[p] += segment_cost(segs[i]);
-    for (int c = 0;;) {
-      const int l = 2 * c + 1, r = l + 1;
-      int m = c;
-      if (l < G && before(heap[l], heap[m])) m = l;
-      if (r < G && before(heap[r], heap[m])) m = r;
-      if (m == c) break;
-      std::swap(heap[c], heap[m]);
-      c = m;
-    }
-  }
-  // pair-major order (a counting sort that keeps each pair's list order);
-  // heap[] becomes the fill cursor of each pair
-  for (int p = 0; p <= G; ++p) unit_off[p] = 0;
-  for (size_t i = 0; i < n; ++i) ++unit_off[pair_of[i] + 1];
-  for (int p = 0; p < G; ++p) unit_off[p + 1] += unit_off[p];
-  for (int p = 0; p < G; ++p) heap[p] = unit_off[p];
-  for (size_t i = 0; i < n; ++i) out[heap[pair_of[i]]++] = segs[i];
-  // every placement adds a positive cost and ties go to the lower index, so
-  // the first min(n, G) segments open pairs 0, 1, ... in turn: the pairs with
-  // work are exactly the leading ones
-  int32_t used = 0;
-  while (used < G && unit_off[used + 1] > unit_off[used]) ++used;
-  return used;
+  assign_pairs(n, [segs](size_t i) { return segment_cost(segs[i]); }, G, pair_of, load, heap);
+  return group_by_pair(segs, n, G, out, unit_off, pair_of, heap);
 }
 
 void build_segments(const std::vector<WorkUnit>& units, int grid, std::vector<WorkUnit>& segs,

@@ -1,0 +1,271 @@
+// Work lists of the forward's other key walks (host only): attention over a
+// list of key tiles per query block, and over a shared prefix and the row's
+// own document.
+//
+// Both lists consist of segments of at most kUnitRows query rows of one head,
+// placed on the forward's persistent CTA pairs in list order, each on the pair
+// with the least load so far.  Whole segments come first; a tail of them is
+// split along its key tiles into pieces small enough to fill the pairs evenly,
+// and the join pass combines the pieces' partial rows.  How long the tail is
+// and how small its pieces are is chosen by simulating the placement.
+#include <algorithm>
+#include <cstring>
+
+#include "h3attn_internal.h"
+
+namespace h3 {
+
+namespace {
+
+// A segment before placement.
+struct Item {
+  WalkUnit u;
+  int32_t tiles;      // key tiles (list walk: at most this many)
+  bool direct;        // writes the output itself unless it is split
+  int32_t pieces = 1;
+  int32_t part = -1;  // first partial row of piece 0
+  bool partial() const { return !direct || pieces > 1; }
+  int32_t rows() const { return u.q_end - u.q_row0; }
+};
+
+// Rows to combine from the partial rows of items a and b (-1: none) and from
+// the keys [key_lo, key_hi) themselves.
+struct Join {
+  int32_t row0, row1, head;
+  int32_t a, b;
+  int32_t key_lo, key_hi;
+};
+
+// Times in key-tile periods of a CTA pair (about 1.15 us on GB300).  A segment
+// costs its tiles, one period for its start and epilogue, and another where it
+// leaves partial rows; the partial rows are written and read at about 6 TB/s
+// (520 bytes a row), by one pair at a time within a segment (kRowsPerPeriod)
+// and by all of them in the join.
+constexpr int kRowsPerPeriod = 87;
+constexpr double kJoinRowsPerPeriod = 6900.0;
+constexpr double kJoinStart = 2.0;
+
+int64_t piece_cost(int32_t tiles, bool partial) { return (int64_t)tiles + 1 + (partial ? 1 : 0); }
+
+// Splits a tail of the items (in list order) so that the pairs finish together.
+void balance(std::vector<Item>& items, int G) {
+  const size_t U = items.size();
+  std::vector<int32_t> pair_of, heap(G);
+  std::vector<int64_t> load(G), cost;
+  double best = -1.0;
+  std::vector<int32_t> best_pieces(U, 1);
+  std::vector<int64_t> tail_tiles(U + 1, 0);  // tiles of items [i, U)
+  for (size_t i = U; i-- > 0;) tail_tiles[i] = tail_tiles[i + 1] + items[i].tiles;
+  const auto consider = [&](size_t whole, int32_t m) {
+    cost.clear();
+    int64_t rows = 0;
+    for (size_t i = 0; i < U; ++i) {
+      const int32_t n = i < whole ? 1 : std::max<int32_t>(1, (items[i].tiles + m - 1) / m);
+      const bool partial = !items[i].direct || n > 1;
+      for (int32_t c = 0; c < n; ++c) {
+        const int32_t t = (int32_t)((int64_t)items[i].tiles * (c + 1) / n - (int64_t)items[i].tiles * c / n);
+        cost.push_back(piece_cost(t, partial));
+      }
+      if (partial) rows += (int64_t)n * items[i].rows();
+    }
+    pair_of.resize(cost.size());
+    assign_pairs(cost.size(), [&](size_t i) { return cost[i]; }, G, pair_of.data(), load.data(), heap.data());
+    double score = (double)*std::max_element(load.begin(), load.end());
+    if (rows > 0) score += kJoinStart + (double)rows / kJoinRowsPerPeriod;
+    if (best < 0.0 || score < best) {
+      best = score;
+      for (size_t i = 0; i < U; ++i)
+        best_pieces[i] = i < whole ? 1 : std::max<int32_t>(1, (items[i].tiles + m - 1) / m);
+    }
+  };
+  consider(U, 1);
+  const int64_t full = (int64_t)(U / G * G);
+  for (int64_t back : {(int64_t)0, (int64_t)G / 4, (int64_t)G / 2, (int64_t)G, (int64_t)2 * G, full}) {
+    if (back > full) continue;
+    const size_t whole = (size_t)(full - back);
+    if (whole == U) continue;
+    for (int r = 1; r <= 4; ++r) {
+      const int64_t m = (tail_tiles[whole] + (int64_t)G * r - 1) / ((int64_t)G * r);
+      consider(whole, (int32_t)std::max<int64_t>(1, m));
+    }
+  }
+  for (size_t i = 0; i < U; ++i) items[i].pieces = best_pieces[i];
+}
+
+// Pieces, partial rows, placement and join records of the balanced items.
+// make(item, piece) gives a piece's segment (part filled in here).
+template <class Make>
+std::string finish(std::vector<Item>& items, std::vector<Join>& joins, int G, Make make, WalkPlan& w) {
+  int64_t rows = 0;
+  std::vector<WalkUnit> segs;
+  std::vector<int64_t> cost;
+  for (Item& it : items) {
+    if (it.partial()) {
+      it.part = (int32_t)rows;
+      rows += (int64_t)it.pieces * it.rows();
+      if (rows >= (int64_t(1) << 31)) return "the layout needs 2^31 or more partial rows";
+    }
+    for (int32_t c = 0; c < it.pieces; ++c) {
+      WalkUnit s = make(it, c);
+      s.part = it.partial() ? it.part + c * it.rows() : -1;
+      segs.push_back(s);
+      const int32_t t =
+          (int32_t)((int64_t)it.tiles * (c + 1) / it.pieces - (int64_t)it.tiles * c / it.pieces);
+      cost.push_back(piece_cost(t, it.partial()));
+    }
+  }
+  w.part_rows = rows;
+  for (size_t i = 0; i < items.size(); ++i)
+    if (items[i].direct && items[i].pieces > 1)
+      joins.push_back(Join{items[i].u.q_row0, items[i].u.q_end, items[i].u.head, (int32_t)i, -1, 0, 0});
+  w.joins.clear();
+  w.join_blocks.clear();
+  for (const Join& j : joins) {
+    JoinRec r;
+    std::memset(&r, 0, sizeof(r));
+    r.row0 = j.row0;
+    r.row1 = j.row1;
+    r.head = j.head;
+    r.key_lo = j.key_lo;
+    r.key_hi = j.key_hi;
+    const Item& a = items[j.a];
+    r.a_part = a.part;
+    r.a_rows = a.rows();
+    r.n_a = a.pieces;
+    r.a_row0 = a.u.q_row0;
+    if (j.b >= 0) {
+      const Item& b = items[j.b];
+      r.b_part = b.part;
+      r.b_rows = b.rows();
+      r.n_b = b.pieces;
+      r.b_row0 = b.u.q_row0;
+    }
+    for (int32_t x = j.row0; x < j.row1; x += kJoinRows) w.join_blocks.push_back(int2{(int)w.joins.size(), x});
+    w.joins.push_back(r);
+  }
+  w.units.resize(segs.size());
+  w.unit_off.assign((size_t)G + 1, 0);
+  std::vector<int32_t> pair_of(segs.size()), heap(G);
+  std::vector<int64_t> load(G);
+  assign_pairs(segs.size(), [&](size_t i) { return cost[i]; }, G, pair_of.data(), load.data(), heap.data());
+  w.n_pairs = group_by_pair(segs.data(), segs.size(), G, w.units.data(), w.unit_off.data(), pair_of.data(), heap.data());
+  w.unit_off.resize((size_t)w.n_pairs + 1);
+  return "";
+}
+
+}  // namespace
+
+std::string build_list_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads, int32_t q_block, int32_t max_blocks,
+                            int grid, WalkPlan& w) {
+  const int G = grid > 0 ? grid : 1;
+  std::vector<int32_t> order(n_docs), block0(n_docs);
+  int32_t blocks = 0;
+  for (int32_t d = 0; d < n_docs; ++d) {
+    order[d] = d;
+    block0[d] = blocks;
+    blocks += (cu[d + 1] - cu[d] + q_block - 1) / q_block;
+  }
+  // longest documents first, then head, then query block: the pairs running at
+  // one moment read the K and V of one or two heads, which stay in L2
+  std::stable_sort(order.begin(), order.end(),
+                   [cu](int32_t x, int32_t y) { return cu[x + 1] - cu[x] > cu[y + 1] - cu[y]; });
+  std::vector<Item> items;
+  for (int32_t d : order) {
+    const int32_t b = cu[d], e = cu[d + 1];
+    const int32_t tiles = std::min(max_blocks, (e - b + kKeyTile - 1) / kKeyTile);
+    for (int32_t h = 0; h < num_heads; ++h)
+      for (int32_t r = b, i = block0[d]; r < e; ++i) {
+        const int32_t end = (int32_t)std::min<int64_t>((int64_t)r + q_block, e);
+        items.push_back(Item{WalkUnit{r, end, b, e, h, i, 0, -1}, tiles, true});
+        r = end;
+      }
+  }
+  balance(items, G);
+  for (Item& it : items) it.pieces = std::min(it.pieces, 65535);  // the field's width
+  std::vector<Join> joins;
+  return finish(items, joins, G, [](const Item& it, int32_t c) {
+    WalkUnit s = it.u;
+    s.b = (int32_t)((uint32_t)c | ((uint32_t)it.pieces << 16));
+    return s;
+  }, w);
+}
+
+std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads, int32_t prefix_len, int grid,
+                              WalkPlan& w) {
+  const int G = grid > 0 ? grid : 1;
+  const int32_t tp = (int32_t)(((int64_t)prefix_len + kKeyTile - 1) / kKeyTile);
+  // The rows are cut into chunks of up to kUnitRows.  A chunk within one
+  // document walks the prefix's tiles and then the document's and writes the
+  // output.  A chunk over several documents walks the prefix once for all its
+  // rows and leaves partial rows; each document's rows in it walk their own
+  // document in a segment of its own, or, in a document of at most
+  // kJoinOwnKeys tokens, in the join.  A document joins the open chunk of the
+  // documents before it where that is cheaper than chunks of its own.
+  struct Piece {
+    int32_t doc, row0, row1;
+  };
+  std::vector<std::vector<Piece>> chunks;
+  int32_t filled = 0;  // rows of the last chunk
+  const auto tiles_of = [cu](int32_t d) { return (cu[d + 1] - cu[d] + kKeyTile - 1) / kKeyTile; };
+  const auto own_cost = [&](int32_t d, int32_t rows) {
+    return cu[d + 1] - cu[d] <= kJoinOwnKeys ? 0.0 : tiles_of(d) + 1.0 + (double)rows / kRowsPerPeriod;
+  };
+  for (int32_t d = 0; d < n_docs; ++d) {
+    const int32_t L = cu[d + 1] - cu[d];
+    const double whole = (double)tp + tiles_of(d) + 1;  // a chunk of this document alone
+    int32_t at = cu[d];
+    if (filled > 0 && filled < kUnitRows) {
+      const int32_t r = std::min(L, kUnitRows - filled);
+      double cont = (double)r / kRowsPerPeriod + own_cost(d, r) + whole * ((L - r + kUnitRows - 1) / kUnitRows);
+      if (chunks.back().size() == 1) {  // that chunk would no longer write its output itself
+        const int32_t o = chunks.back()[0].doc;
+        cont += (double)filled / kRowsPerPeriod + own_cost(o, filled) - tiles_of(o);
+      }
+      if (cont < whole * ((L + kUnitRows - 1) / kUnitRows)) {
+        chunks.back().push_back(Piece{d, at, at + r});
+        filled += r;
+        at += r;
+      }
+    }
+    while (at < cu[d + 1]) {
+      const int32_t r = std::min(cu[d + 1] - at, kUnitRows);
+      chunks.push_back({Piece{d, at, at + r}});
+      filled = r;
+      at += r;
+    }
+  }
+  // head by head: the pairs running at one moment share a head's prefix in L2
+  std::vector<Item> items;
+  std::vector<Join> joins;
+  for (int32_t h = 0; h < num_heads; ++h) {
+    for (const std::vector<Piece>& c : chunks) {
+      const int32_t q0 = c.front().row0, q1 = c.back().row1;
+      const int32_t b = cu[c[0].doc], e = cu[c[0].doc + 1];
+      if (c.size() == 1) {
+        const int32_t t = tp + tiles_of(c[0].doc);
+        items.push_back(Item{WalkUnit{q0, q1, b, e, h, 0, t, -1}, t, true});
+        continue;
+      }
+      const int32_t pre = (int32_t)items.size();
+      items.push_back(Item{WalkUnit{q0, q1, b, e, h, 0, tp, -1}, tp, false});
+      for (const Piece& p : c) {
+        const int32_t db = cu[p.doc], de = cu[p.doc + 1], t = tiles_of(p.doc);
+        if (de - db <= kJoinOwnKeys) {
+          joins.push_back(Join{p.row0, p.row1, h, pre, -1, db, de});
+        } else {
+          joins.push_back(Join{p.row0, p.row1, h, pre, (int32_t)items.size(), 0, 0});
+          items.push_back(Item{WalkUnit{p.row0, p.row1, db, de, h, tp, tp + t, -1}, t, false});
+        }
+      }
+    }
+  }
+  balance(items, G);
+  return finish(items, joins, G, [](const Item& it, int32_t c) {
+    WalkUnit s = it.u;
+    s.a = it.u.a + (int32_t)((int64_t)it.tiles * c / it.pieces);
+    s.b = it.u.a + (int32_t)((int64_t)it.tiles * (c + 1) / it.pieces);
+    return s;
+  }, w);
+}
+
+}  // namespace h3

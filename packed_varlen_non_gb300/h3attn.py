@@ -68,6 +68,17 @@ _SIGS = {
                            c_int64, c_float, c_void_p, c_void_p],
     "h3attn_forward_noalloc": [c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int64,
                                c_void_p, c_int64, c_float, c_void_p, c_void_p],
+    "h3attn_plan_set_sparse": [c_void_p, c_int32, c_int32, c_void_p],
+    "h3attn_plan_sparse_info": [c_void_p, POINTER(c_int32), POINTER(c_int32), POINTER(c_int32)],
+    "h3attn_block_select": [c_void_p, c_void_p, c_void_p, c_int64, c_int32, c_int32, c_void_p, c_void_p, c_void_p],
+    "h3attn_forward_sparse": [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_int64,
+                              c_float, c_void_p, c_void_p],
+    "h3attn_plan_set_prefix": [c_void_p, c_int32, c_void_p],
+    "h3attn_forward_prefix": [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p,
+                              c_int64, c_float, c_void_p, c_void_p],
+    "h3attn_walk_list_host": [c_int32, c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_int64,
+                              c_void_p, c_void_p, c_int64, POINTER(c_int64), POINTER(c_int32), POINTER(c_int64),
+                              POINTER(c_int64)],
     "h3attn_get_device_error": [c_void_p, c_void_p],
     "h3attn_selftest_bounded_wait": [c_uint64, c_void_p],
 }
@@ -307,6 +318,98 @@ def h3attn_forward_noalloc(cu_seqlens, num_heads: int, q, k, v, o, softmax_scale
                                          _ptr(v), _row_stride(q, qkv_row_stride), _ptr(o),
                                          _row_stride(o, o_row_stride), float(softmax_scale), _ptr(lse),
                                          _stream(stream)), "h3attn_forward_noalloc")
+
+
+# ------------------------------------------------- sparse, shared prefix ----
+
+def _qkv_stride(q, others, given):
+    if given is None and not isinstance(q, int):
+        strides = {int(x.stride(0)) for x in (q, *others)}
+        if len(strides) != 1:
+            raise ValueError(f"tensors of one call must share one row stride (got {sorted(strides)})")
+    return _row_stride(q, given)
+
+
+def _check_lists(plan, block_idx, block_cnt):
+    """The lists are read (or written) by their plan's sizes, so tensors must
+    be int32, contiguous and of those sizes; raw pointers are the caller's."""
+    if isinstance(block_idx, int) or isinstance(block_cnt, int) or block_idx is None or block_cnt is None:
+        return
+    info = h3attn_plan_sparse_info(plan)
+    rows = info["num_heads"] * info["n_q_blocks"]
+    for name, t, n in (("block_idx", block_idx, rows * info["max_blocks"]), ("block_cnt", block_cnt, rows)):
+        if str(t.dtype) != "torch.int32" or not t.is_contiguous() or t.numel() != n:
+            raise ValueError(f"{name} must be a contiguous int32 tensor of {n} elements "
+                             f"(got {tuple(t.shape)}, {t.dtype})")
+
+
+def h3attn_plan_set_sparse(plan, q_block: int, max_blocks: int, stream=None):
+    """Adds the block-sparse work list to a plan (once per plan)."""
+    _check(load().h3attn_plan_set_sparse(plan, int(q_block), int(max_blocks), _stream(stream)),
+           "h3attn_plan_set_sparse")
+
+
+def h3attn_plan_sparse_info(plan) -> dict:
+    qb, mb, nq, nh = c_int32(), c_int32(), c_int32(), c_int32()
+    _check(load().h3attn_plan_sparse_info(plan, ctypes.byref(qb), ctypes.byref(mb), ctypes.byref(nq)),
+           "h3attn_plan_sparse_info")
+    _check(load().h3attn_plan_info(plan, None, None, None, ctypes.byref(nh)), "h3attn_plan_info")
+    return {"q_block": qb.value, "max_blocks": mb.value, "n_q_blocks": nq.value, "num_heads": nh.value}
+
+
+def h3attn_block_select(plan, q_hat, k_hat, keep: int, block_idx, block_cnt, keep_own: bool = True,
+                        qkv_row_stride=None, stream=None):
+    """Scores and keeps key tiles: block_idx int32 [H, n_q_blocks, max_blocks],
+    block_cnt int32 [H, n_q_blocks] (see include/h3attn.h)."""
+    stride = _qkv_stride(q_hat, (k_hat,), qkv_row_stride)
+    _check_lists(plan, block_idx, block_cnt)
+    _check(load().h3attn_block_select(plan, _ptr(q_hat), _ptr(k_hat), stride, int(keep), int(bool(keep_own)),
+                                      _ptr(block_idx), _ptr(block_cnt), _stream(stream)), "h3attn_block_select")
+
+
+def h3attn_forward_sparse(plan, q, k, v, block_idx, block_cnt, o, softmax_scale: float, lse=None,
+                          qkv_row_stride=None, o_row_stride=None, stream=None):
+    """The forward over the listed key tiles of each query block."""
+    stride = _qkv_stride(q, (k, v), qkv_row_stride)
+    _check_lists(plan, block_idx, block_cnt)
+    _check(load().h3attn_forward_sparse(plan, _ptr(q), _ptr(k), _ptr(v), stride, _ptr(block_idx), _ptr(block_cnt),
+                                        _ptr(o), _row_stride(o, o_row_stride), float(softmax_scale), _ptr(lse),
+                                        _stream(stream)), "h3attn_forward_sparse")
+
+
+def h3attn_plan_set_prefix(plan, prefix_len: int, stream=None):
+    """Adds the work list for a shared prefix of prefix_len rows to a plan
+    (once per plan)."""
+    _check(load().h3attn_plan_set_prefix(plan, int(prefix_len), _stream(stream)), "h3attn_plan_set_prefix")
+
+
+def h3attn_forward_prefix(plan, q, k, v, k_prefix, v_prefix, o, softmax_scale: float, lse=None,
+                          qkv_row_stride=None, prefix_row_stride=None, o_row_stride=None, stream=None):
+    """The forward of a batch whose documents all attend to one prefix besides
+    themselves; k_prefix and v_prefix are bf16 [prefix_len, H, 128]-shaped."""
+    stride = _qkv_stride(q, (k, v), qkv_row_stride)
+    _check(load().h3attn_forward_prefix(plan, _ptr(q), _ptr(k), _ptr(v), stride, _ptr(k_prefix), _ptr(v_prefix),
+                                        _qkv_stride(k_prefix, (v_prefix,), prefix_row_stride), _ptr(o),
+                                        _row_stride(o, o_row_stride), float(softmax_scale), _ptr(lse),
+                                        _stream(stream)), "h3attn_forward_prefix")
+
+
+def h3attn_walk_list_host(kind: int, cu_seqlens, num_heads: int, p0: int, p1: int, n_pairs: int):
+    """The work list of the sparse (kind 0: p0 = q_block, p1 = max_blocks) or
+    prefix (kind 1: p0 = prefix_len) forward, built on the host: (units [n, 8],
+    unit_off, joins [m, 16], partial rows); the fields are those of the C call."""
+    cu = np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
+    n, used, nj, rows = c_int64(), c_int32(), c_int64(), c_int64()
+    head = (int(kind), cu.ctypes.data, int(cu.size) - 1, int(num_heads), int(p0), int(p1), int(n_pairs))
+    tail = (ctypes.byref(n), ctypes.byref(used), ctypes.byref(nj), ctypes.byref(rows))
+    lib = load()
+    _check(lib.h3attn_walk_list_host(*head, None, 0, None, None, 0, *tail), "h3attn_walk_list_host")
+    units = np.zeros((n.value, 8), dtype=np.int32)
+    off = np.zeros(used.value + 1, dtype=np.int32)
+    joins = np.zeros((nj.value, 16), dtype=np.int32)
+    _check(lib.h3attn_walk_list_host(*head, units.ctypes.data, n.value, off.ctypes.data, joins.ctypes.data, nj.value,
+                                     *tail), "h3attn_walk_list_host")
+    return units, off, joins, rows.value
 
 
 def h3attn_get_device_error(plan, stream=None):
