@@ -393,7 +393,7 @@ h3attn_status h3attn_forward_prefix(h3attn_plan_t plan, const void* q, const voi
  *            segment writes the output itself);
  *   unit_off [*n_pairs_used + 1] int32: pair p runs units [unit_off[p], unit_off[p + 1]);
  *   joins    [*n_joins][16] int32, the rows combined from partial rows: rows
- *            [r0, r1), head, key_lo; then of segment a its first partial row,
+ *            [r0, r1) (at most 8), head, key_lo; then of segment a its first partial row,
  *            rows, pieces and first query row; the same of segment b (pieces may
  *            be 0); key_hi (keys [key_lo, key_hi) are attended to by the join
  *            itself), three zeros.  Row r of piece c is partial row first + c *

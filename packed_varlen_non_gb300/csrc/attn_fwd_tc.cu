@@ -156,6 +156,13 @@ constexpr uint32_t kKHalfBytes = 64 * 128;             // bf16 K half-tile: one 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kTimeoutNs = 2000000000ull;         // 2 s
 constexpr float kRescaleThreshold = 8.0f;              // log2 units: rescale when max grows by > 2^8
+// The other walks rescale O only when a row's maximum has grown by 2^32: P is
+// bf16, whose range is fp32's, so p up to 2^32 rounds no worse than p up to 2^8,
+// and the sums stay below 2^127 for 2^31 keys and |v| up to 2^64.  A rescale
+// costs a warp two trips of its O rows through registers and a wait for the
+// other half's PV; with scores spread over tens of log2 units some row of a
+// warp crosses 2^8 in most tiles.
+constexpr float kRescaleThresholdWalk = 32.0f;
 constexpr uint16_t kPairMask = 0x3;
 static_assert(kUnitRows == 4 * kTileRows, "a unit is two query tiles in each CTA of the pair");
 
@@ -697,6 +704,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         return &tm_v;
       };
       int k = 0;
+      KeyTile kt;  // the tile whose K was sent last (dense: only its row is used)
       for (int u = u_begin; ok && u < u_end; ++u, ++k) {
         const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
         const bool has_next = u + 1 < u_end;
@@ -714,19 +722,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             load_k_half<kFp8>(sbase + C::SmemKV, &tm_k, bars.kv_full(0), g.head, g.kv0 + g.lo * kTileRows, rank,
                               pol_kv);
           } else {
-            const KeyTile t = key_tile<kWalk>(g, g.lo, walk);
-            load_k_half<kFp8>(sbase + C::SmemKV, k_map(t), bars.kv_full(0), g.head, t.row, rank, pol_kv);
+            kt = key_tile<kWalk>(g, g.lo, walk);
+            load_k_half<kFp8>(sbase + C::SmemKV, k_map(kt), bars.kv_full(0), g.head, kt.row, rank, pol_kv);
           }
           grp = 1;
         }
         for (int j = g.lo; ok && j < g.hi; ++j) {
           bool has_k = j + 1 < g.hi;
           int k_head = g.head;
-          KeyTile vt, kt;
+          const KeyTile vt = kt;  // this step's tile: its K went out a step ago
           if constexpr (kWalk == kWalkDoc) {
             kt.row = g.kv0 + (j + 1) * kTileRows;
           } else {
-            vt = key_tile<kWalk>(g, j, walk);
             if (has_k) kt = key_tile<kWalk>(g, j + 1, walk);
             if (vt.bad && rank == 0) atomicExch(a.err, kErrBlockIndex);
           }
@@ -1157,10 +1164,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       } else {
         // bf16: 64-key halves (see the kernel header).
+        int rem_next = 0;
+        if constexpr (kWalk != kWalkDoc) rem_next = key_tile<kWalk>(g, g.lo, walk).rem;
         for (int j = g.lo; ok && j < g.hi; ++j) {
           const uint32_t t = t_unit + (j - g.lo);  // the pair's running key-tile count
           const float rsc = sl2;  // score scale in log2 units: softmax_scale log2(e)
-          const int rem = key_tile<kWalk>(g, j, walk).rem;
+          int rem;
+          if constexpr (kWalk == kWalkDoc) {
+            rem = key_tile<kWalk>(g, j, walk).rem;
+          } else {  // a list entry is loaded a tile ahead of its use
+            rem = rem_next;
+            if (j + 1 < g.hi) rem_next = key_tile<kWalk>(g, j + 1, walk).rem;
+          }
           const uint32_t kv_bar = bars.kv_full((t + 1) % kGroups), kv_par = ((t + 1) / kGroups) & 1;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -1199,7 +1214,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // The reference max only moves when the row max grows by more than
             // 2^8 (then O and l are rescaled; the final O / l is unchanged).
             float alpha = 1.f;
-            if (m_new > m_used + kRescaleThreshold) {
+            if (m_new > m_used + (kWalk == kWalkDoc ? kRescaleThreshold : kRescaleThresholdWalk)) {
               alpha = dev::ex2_approx(m_used - m_new);  // 0 on the first half of a unit (m_used = -inf)
               m_used = m_new;
             }
@@ -1483,7 +1498,6 @@ __global__ void __launch_bounds__(256, 8) attn_merge_kernel(ForwardArgs a) {
 // maximum (log2 units): o = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
 struct JoinArgs {
   const JoinRec* recs;
-  const int2* blocks;
   const __nv_bfloat16* q;
   const __nv_bfloat16* k;
   const __nv_bfloat16* v;
@@ -1503,11 +1517,13 @@ __device__ __forceinline__ float4 load_bf16x4(const __nv_bfloat16* p) {
                      __uint_as_float(w.y & 0xffff0000u));
 }
 
-__global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(JoinArgs a) {
+// The rows of a record are a block's; parts are read two at a time with their
+// maxima and rows together, in one pass with a running maximum, so that a row
+// waits for memory about once.
+__global__ void __launch_bounds__(32 * kJoinRows, 6) attn_join_kernel(JoinArgs a) {
   const int lane = threadIdx.x & 31;
-  const int2 blk = __ldg(a.blocks + blockIdx.x);
-  const JoinRec j = a.recs[blk.x];
-  const int32_t row = blk.y + (int32_t)(threadIdx.x >> 5);
+  const JoinRec j = a.recs[blockIdx.x];
+  const int32_t row = j.row0 + (int32_t)(threadIdx.x >> 5);
   if (row >= j.row1) return;
   // own keys (inputs of the forward: they need not wait for it)
   float m_own = -INFINITY, l_own = 0.f;
@@ -1544,29 +1560,33 @@ __global__ void __launch_bounds__(32 * kJoinRows) attn_join_kernel(JoinArgs a) {
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the forward is complete and its writes visible
   const int64_t ra = (int64_t)j.a_part + (row - j.a_row0), rb = (int64_t)j.b_part + (row - j.b_row0);
-  float M = m_own;
-#pragma unroll 4
-  for (int c = 0; c < j.n_a; ++c) M = fmaxf(M, a.part_ml[ra + (int64_t)c * j.a_rows].x);
-#pragma unroll 4
-  for (int c = 0; c < j.n_b; ++c) M = fmaxf(M, a.part_ml[rb + (int64_t)c * j.b_rows].x);
-  const float ref = M == -INFINITY ? 0.f : M;
-  const float w_own = dev::ex2_approx(m_own - ref);
-  float4 acc = make_float4(w_own * o_own.x, w_own * o_own.y, w_own * o_own.z, w_own * o_own.w);
-  float l = w_own * l_own;
-  const auto add = [&](int64_t r) {
-    const float2 ml = a.part_ml[r];
-    const float w = dev::ex2_approx(ml.x - ref);
-    const float4 o = reinterpret_cast<const float4*>(a.part_o + r * kHeadDim)[lane];
-    acc.x = fmaf(w, o.x, acc.x);
-    acc.y = fmaf(w, o.y, acc.y);
-    acc.z = fmaf(w, o.z, acc.z);
-    acc.w = fmaf(w, o.w, acc.w);
-    l = fmaf(w, ml.y, l);
-  };
-#pragma unroll 4
-  for (int c = 0; c < j.n_a; ++c) add(ra + (int64_t)c * j.a_rows);
-#pragma unroll 4
-  for (int c = 0; c < j.n_b; ++c) add(rb + (int64_t)c * j.b_rows);
+  float M = m_own, l = l_own;
+  float4 acc = o_own;
+  const int n = j.n_a + j.n_b;
+#pragma unroll 1
+  for (int c = 0; c < n; c += 2) {
+    float2 ml[2];
+    float4 o[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      ml[x] = make_float2(-INFINITY, 0.f);
+      o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c + x < n) {
+        const int64_t r = c + x < j.n_a ? ra + (int64_t)(c + x) * j.a_rows : rb + (int64_t)(c + x - j.n_a) * j.b_rows;
+        ml[x] = a.part_ml[r];
+        o[x] = reinterpret_cast<const float4*>(a.part_o + r * kHeadDim)[lane];
+      }
+    }
+    const float m_new = dev::max3(M, ml[0].x, ml[1].x);
+    const float ref = m_new == -INFINITY ? 0.f : m_new;
+    const float w = dev::ex2_approx(M - ref), w0 = dev::ex2_approx(ml[0].x - ref), w1 = dev::ex2_approx(ml[1].x - ref);
+    acc.x = fmaf(w1, o[1].x, fmaf(w0, o[0].x, w * acc.x));
+    acc.y = fmaf(w1, o[1].y, fmaf(w0, o[0].y, w * acc.y));
+    acc.z = fmaf(w1, o[1].z, fmaf(w0, o[0].z, w * acc.z));
+    acc.w = fmaf(w1, o[1].w, fmaf(w0, o[0].w, w * acc.w));
+    l = fmaf(w1, ml[1].y, fmaf(w0, ml[0].y, w * l));
+    M = m_new;
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   __nv_bfloat16* dst = a.o + (int64_t)row * a.o_stride + j.head * kHeadDim + 4 * lane;
   *reinterpret_cast<uint2*>(dst) =
@@ -1723,9 +1743,8 @@ cudaError_t launch_walk(const ForwardMaps& m, const ForwardArgs& a, const WalkAr
   attn_fwd_tc_kernel<false, kWalk>
       <<<2 * a.n_pairs, kThreads, Cfg<false>::SmemAlloc, stream>>>(m.q, m.k, m.v, m.o, a, m.o_tma, walk);
   e = cudaGetLastError();
-  if (e != cudaSuccess || w.n_join_blocks == 0) return e;
+  if (e != cudaSuccess || w.n_joins == 0) return e;
   const JoinArgs j{w.joins,
-                   w.join_blocks,
                    static_cast<const __nv_bfloat16*>(a.q),
                    static_cast<const __nv_bfloat16*>(a.k),
                    static_cast<const __nv_bfloat16*>(a.v),
@@ -1737,7 +1756,7 @@ cudaError_t launch_walk(const ForwardMaps& m, const ForwardArgs& a, const WalkAr
                    a.scale_log2,
                    a.part_o,
                    a.part_ml};
-  e = launch_dependent(attn_join_kernel, (unsigned)w.n_join_blocks, 32u * kJoinRows, stream, j);
+  e = launch_dependent(attn_join_kernel, (unsigned)w.n_joins, 32u * kJoinRows, stream, j);
   if (e != cudaSuccess && why) *why = "the join launch failed";
   return e;
 }

@@ -7,21 +7,30 @@
 //   ties to the lower tile.
 //
 // Which tiles are kept is a discrete answer: a rounding that swaps two scores
-// changes it.  Sums and scores are therefore carried as unevaluated pairs of
-// fp32 numbers (Knuth's two-sum, and the product's rounding error from one
-// fma: Dekker's and Ogita, Rump and Oishi's error-free transformations), good
-// to about 2^-44 -- not in fp64, whose rate here is a fiftieth of fp32's: the
-// pooling alone would take five times as long as reading its inputs.
+// changes it.  Sums and scores near the border are therefore carried as
+// unevaluated pairs of fp32 numbers (error-free transformations of Knuth,
+// Dekker, and Ogita, Rump and Oishi), good to about 2^-44 -- not in fp64, whose
+// rate here is a fiftieth of fp32's: the pooling alone would take five times as
+// long as reading its inputs.
 //
-// Two kernels.  pool_kernel is HBM-bound: it reads q-hat and k-hat once, one
-// block per (128-row tile, head), every load of the tile in flight at once, and
-// leaves 1.5 KB per tile and head.  Query blocks begin on tile boundaries, so
-// the same tiles serve both.  score_kernel gives a warp to a query block and a
-// lane to a key tile: 32 tiles' means are staged in shared memory, two dims per
-// 8-byte word, and read without conflicts by all warps of the block, which
-// share document and head.  The selection is a bitwise search for the keep-th
-// largest key in 64-bit order-preserving keys (first the high halves, the low
-// ones only among equals), then one ordered pass that writes the kept tiles.
+// pool_kernel is HBM-bound: it reads q-hat and k-hat once, one block per
+// (128-row tile, head, tensor) with all its loads in flight, and leaves 1.5 KB
+// per tile and head.  Query blocks begin on tile boundaries, so the same tiles
+// serve both.  Each thread sums eight rows of eight dims onto an anchor 2^6
+// times above their largest magnitude: every addition then rounds at one fixed
+// place, and its error is two subtractions away (four operations an element
+// where a two-sum of unordered numbers takes seven; with seven, the fp32 pipe
+// took two thirds of the loads' time).
+//
+// score_kernel gives a warp to a query block and a lane to a key tile: 32
+// tiles' means are staged in shared memory, two dims per 8-byte word, and read
+// without conflicts by all warps of the block, which share document and head.
+// Scores are first plain fp32 sums with an error bound E; the keep-th largest
+// of them, T, is found by a bitwise search over order-preserving keys.  A tile
+// above T + 2 E is kept and one below T - 2 E is not, whatever the exact scores
+// are.  Only where more tiles lie between than places are left (a few per cent
+// of the query blocks, and ties) are the scores between computed as pairs and
+// searched again.
 #include "device_common.cuh"
 #include "qk_norm.cuh"
 
@@ -59,69 +68,7 @@ __device__ __forceinline__ float mean_of(const float2& s, float n) {
   return isfinite(q) ? m : q;  // (an infinite sum has no remainder)
 }
 
-// One (tile, head): sums of q-hat's rows as pairs, means of k-hat's.
-__global__ void __launch_bounds__(kPoolThreads) pool_kernel(SelectArgs a) {
-  __shared__ float2 part[2][8][128];
-  const int tile = blockIdx.x, head = blockIdx.y;
-  const int lane16 = threadIdx.x & 15, group = threadIdx.x >> 4, warp = threadIdx.x >> 5;
-  const int4 t = __ldg(a.tiles + tile);
-  const int n = t.y - t.x;
-  const __nv_bfloat16* src[2] = {static_cast<const __nv_bfloat16*>(a.q_hat), static_cast<const __nv_bfloat16*>(a.k_hat)};
-  uint4 raw[2][8];
-#pragma unroll
-  for (int x = 0; x < 2; ++x)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = group + 16 * i;
-      const __nv_bfloat16* p = src[x] + (int64_t)(t.x + r) * a.stride + head * kHeadDim + lane16 * 8;
-      raw[x][i] = r < n ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    float2 s[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v[8];
-      qkn::unpack8(raw[x][i], v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc(s[e].x, s[e].y, v[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {  // the warp's two row groups
-      const float2 o = make_float2(__shfl_xor_sync(0xffffffffu, s[e].x, 16), __shfl_xor_sync(0xffffffffu, s[e].y, 16));
-      acc2(s[e], o);
-      if ((threadIdx.x & 16) == 0) part[x][warp][lane16 * 8 + e] = s[e];
-    }
-  }
-  __syncthreads();
-  const int x = threadIdx.x >> 7, d = threadIdx.x & 127;
-  float2 s = part[x][0][d];
-#pragma unroll
-  for (int w = 1; w < 8; ++w) acc2(s, part[x][w][d]);
-  const int64_t at = ((int64_t)head * a.n_tiles + tile) * kHeadDim + d;
-  if (x == 0)
-    a.q_sum[at] = s;
-  else
-    a.k_mean[at] = mean_of(s, (float)n);
-}
-
-// Order-preserving bits of a float that is not NaN (-0 as +0).
-__device__ __forceinline__ uint32_t ordered(float f) {
-  const uint32_t b = __float_as_uint(f + 0.f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-
-// Packed pairs: (a0 b0, a1 b1) and (a0 - b0, a1 - b1).
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
+// Packed pairs of fp32 numbers (one instruction each).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
   dev::fma2(d.x, d.y, a.x, a.y, b.x, b.y, c.x, c.y);
@@ -134,17 +81,165 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
 
+// Elementwise maximum of two pairs of bf16 numbers (NaN if either is).
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// 1.5 * 2^(e + 6) for a number of exponent e (sums of eight numbers up to it
+// stay in the anchor's binade); no further than the largest exponent.
+__device__ __forceinline__ float anchor_of(uint32_t bits) {
+  const uint32_t e = min(bits & 0x7f800000u, 248u << 23);
+  return __uint_as_float((e + (6u << 23)) | 0x00400000u);
+}
+
+// One (tile, tensor, head): sums of q-hat's rows as pairs, means of k-hat's.
+__global__ void __launch_bounds__(kPoolThreads, 4) pool_kernel(SelectArgs a) {
+  __shared__ float2 part[8][128];
+  const int head = blockIdx.x % a.H, tile = (blockIdx.x / a.H) >> 1;
+  const bool is_k = (blockIdx.x / a.H) & 1;
+  const int lane16 = threadIdx.x & 15, group = threadIdx.x >> 4, warp = threadIdx.x >> 5;
+  const int4 t = __ldg(a.tiles + tile);
+  const int n = t.y - t.x;
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_k ? a.k_hat : a.q_hat) + (int64_t)t.x * a.stride +
+                             head * kHeadDim + lane16 * 8;
+  uint4 raw[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = group + 16 * i;
+    raw[i] = r < n ? __ldg(reinterpret_cast<const uint4*>(src + r * a.stride)) : make_uint4(0, 0, 0, 0);
+  }
+  uint4 m = make_uint4(0, 0, 0, 0);  // largest magnitude of each dim
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    m.x = max_bf16x2(m.x, raw[i].x & 0x7fff7fffu);
+    m.y = max_bf16x2(m.y, raw[i].y & 0x7fff7fffu);
+    m.z = max_bf16x2(m.z, raw[i].z & 0x7fff7fffu);
+    m.w = max_bf16x2(m.w, raw[i].w & 0x7fff7fffu);
+  }
+  const uint32_t mw[4] = {m.x, m.y, m.z, m.w};
+  float2 anchor[4], hi[4], lo[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    anchor[e] = make_float2(anchor_of(mw[e] << 16), anchor_of(mw[e]));
+    hi[e] = anchor[e];
+    lo[e] = make_float2(0.f, 0.f);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float v[8];
+    qkn::unpack8(raw[i], v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 x = make_float2(v[2 * e], v[2 * e + 1]);
+      const float2 s = add2(hi[e], x);
+      lo[e] = add2(lo[e], sub2(x, sub2(s, hi[e])));
+      hi[e] = s;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 h = sub2(hi[e], anchor[e]);
+    const float2 own[2] = {make_float2(h.x, lo[e].x), make_float2(h.y, lo[e].y)};
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {  // the warp's two row groups
+      float2 s = own[c];
+      acc2(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, 16), __shfl_xor_sync(0xffffffffu, s.y, 16)));
+      if ((threadIdx.x & 16) == 0) part[warp][lane16 * 8 + 2 * e + c] = s;
+    }
+  }
+  __syncthreads();
+  const int d = threadIdx.x;
+  if (d >= kHeadDim) return;
+  float2 s = part[0][d];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) acc2(s, part[w][d]);
+  const int64_t at = ((int64_t)head * a.n_tiles + tile) * kHeadDim + d;
+  if (is_k)
+    a.k_mean[at] = mean_of(s, (float)n);
+  else
+    a.q_sum[at] = s;
+}
+
+// Order-preserving bits of a float that is not NaN (-0 as +0).
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t b = __float_as_uint(f + 0.f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// Order-preserving key of the score of query mean q (shared memory) and key
+// mean k to about 2^-44: ordered bits of a normalised pair; 0 for NaN.
+static __device__ __noinline__ uint64_t exact_key(const float2* q, const float2* k) {
+  // even and odd dims apart; each product q k is x + e exactly
+  float2 h = make_float2(0.f, 0.f), l = make_float2(0.f, 0.f);
+#pragma unroll 4
+  for (int p = 0; p < 64; ++p) {
+    const float2 a = q[p], b = __ldg(k + p);
+    const float2 x = mul2(a, b);
+    const float2 e = fma2(a, b, mul2(x, make_float2(-1.f, -1.f)));
+    const float2 s = add2(h, x), bb = sub2(s, h);
+    const float2 err = add2(sub2(h, sub2(s, bb)), sub2(x, bb));
+    h = s;
+    l = add2(l, add2(err, e));
+  }
+  float s, e, hi, lo;
+  two_sum(s, e, h.x, h.y);
+  two_sum(hi, lo, s, __fadd_rn(e, __fadd_rn(l.x, l.y)));
+  // an infinite score has no low part
+  if (!isfinite(hi)) hi = s;
+  if (!isfinite(lo)) lo = 0.f;
+  return isnan(hi) ? 0 : ((uint64_t)ordered(hi) << 32) | ordered(lo);
+}
+
+// The largest x with at least cnt of a warp's keys >= x, and how many keys are
+// above x.  key(j) gives key j of 0 .. n - 1.
+template <class Key>
+__device__ __forceinline__ uint32_t kth_largest(int n, int cnt, int lane, int* above, Key key) {
+  uint32_t th = 0;
+  *above = 0;
+#pragma unroll 1
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t cand = th | (1u << bit);
+    int m = 0;
+    for (int j = lane; j < n; j += 32) m += key(j) >= cand;
+    m = __reduce_add_sync(0xffffffffu, m);
+    if (m >= cnt)
+      th = cand;
+    else
+      *above = m;
+  }
+  return th;
+}
+
 constexpr int kChunk = 32;                       // key tiles staged at a time
 constexpr int kChunkRow = kChunk + 1;            // 8-byte words per pair of dims (padded)
+constexpr uint32_t kOwnKey = 0xffffffffu;        // above every score's key
 
-// Shared memory: km [64][kChunkRow] float2, qm [warps][64] float2, keys
-// [warps][max_tiles] uint64.
+// Bytes of shared memory: km [64][kChunkRow] float2, qm [warps][64] float2,
+// exact keys [warps][max_tiles] uint64, keys [warps][max_tiles] uint32.
+size_t score_smem(int warps, int32_t max_tiles) {
+  return (64 * kChunkRow + (size_t)warps * 64) * sizeof(float2) + (size_t)warps * max_tiles * 12;
+}
+
 __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) {
   extern __shared__ float2 smem[];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float2* km = smem;
   float2* qm = smem + 64 * kChunkRow + warp * 64;
-  uint64_t* keys = reinterpret_cast<uint64_t*>(smem + 64 * kChunkRow + warps * 64) + (int64_t)warp * a.max_tiles;
+  uint64_t* const exact0 = reinterpret_cast<uint64_t*>(smem + 64 * kChunkRow + warps * 64);
+  uint64_t* exact = exact0 + (int64_t)warp * a.max_tiles;
+  uint32_t* keys = reinterpret_cast<uint32_t*>(exact0 + (int64_t)warps * a.max_tiles) + (int64_t)warp * a.max_tiles;
   const int head = blockIdx.y;
   const int4 g0 = __ldg(reinterpret_cast<const int4*>(a.groups + blockIdx.x));
   const int first = __ldg(&a.groups[blockIdx.x].first);
@@ -152,7 +247,10 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
   const bool active = warp < n;
   // this block's own key tiles, relative to the document
   const int own0 = (first + warp) * a.tiles_per_q_block, own1 = min(own0 + a.tiles_per_q_block, tiles);
+  float rows = 1.f;
+  if (active) rows = (float)(__ldg(&a.tiles[tile0 + own1 - 1].y) - __ldg(&a.tiles[tile0 + own0].x));
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the pooled sums are complete
+  float qn = 0.f;  // squared norm of the query block's mean
   if (active) {
     // mean of the query block: four dims per lane, the sums of up to four tiles
     float2 s[4];
@@ -166,93 +264,103 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
       acc2(s[2], make_float2(v.x, v.y));
       acc2(s[3], make_float2(v.z, v.w));
     }
-    const float rows = (float)(__ldg(&a.tiles[tile0 + own1 - 1].y) - __ldg(&a.tiles[tile0 + own0].x));
-    qm[2 * lane] = make_float2(-mean_of(s[0], rows), -mean_of(s[1], rows));  // (negated: see the loop)
-    qm[2 * lane + 1] = make_float2(-mean_of(s[2], rows), -mean_of(s[3], rows));
+    const float2 x = make_float2(mean_of(s[0], rows), mean_of(s[1], rows));
+    const float2 y = make_float2(mean_of(s[2], rows), mean_of(s[3], rows));
+    qm[2 * lane] = x;
+    qm[2 * lane + 1] = y;
+    qn = x.x * x.x + x.y * x.y + (y.x * y.x + y.y * y.y);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) qn += __shfl_xor_sync(0xffffffffu, qn, off);
   }
-  const float* k_mean = a.k_mean + ((int64_t)head * a.n_tiles + tile0) * kHeadDim;
+  const float2* k_mean = reinterpret_cast<const float2*>(a.k_mean + ((int64_t)head * a.n_tiles + tile0) * kHeadDim);
+  float kn = 0.f;      // largest squared norm of this lane's key means
+  bool wild = false;   // a norm that fp32 does not hold (NaN included)
   for (int c0 = 0; c0 < tiles; c0 += kChunk) {
     __syncthreads();  // (also orders qm before its first read)
     for (int i = threadIdx.x; i < kChunk * 64; i += blockDim.x) {
       const int j = i >> 6, p = i & 63;
-      if (c0 + j < tiles)
-        km[p * kChunkRow + j] = __ldg(reinterpret_cast<const float2*>(k_mean + (int64_t)(c0 + j) * kHeadDim) + p);
+      if (c0 + j < tiles) km[p * kChunkRow + j] = __ldg(k_mean + (int64_t)(c0 + j) * 64 + p);
     }
     __syncthreads();
     const int j = c0 + lane;
     if (active && j < tiles) {
-      // -score, even and odd dims apart: each product -q k is x + e exactly
-      float2 h = make_float2(0.f, 0.f), l = make_float2(0.f, 0.f);
-#pragma unroll 8
+      float2 h[2], m[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) h[x] = m[x] = make_float2(0.f, 0.f);
+#pragma unroll 16
       for (int p = 0; p < 64; ++p) {
-        const float2 nq = qm[p], k = km[p * kChunkRow + lane];
-        const float2 x = mul2(nq, k);
-        const float2 e = fma2(nq, k, mul2(x, make_float2(-1.f, -1.f)));
-        const float2 s = add2(h, x), bb = sub2(s, h);
-        const float2 err = add2(sub2(h, sub2(s, bb)), sub2(x, bb));
-        h = s;
-        l = add2(l, add2(err, e));
+        const float2 k = km[p * kChunkRow + lane];
+        h[p & 1] = fma2(qm[p], k, h[p & 1]);
+        m[p & 1] = fma2(k, k, m[p & 1]);
       }
-      float s, e;
-      two_sum(s, e, h.x, h.y);
-      const float low = __fadd_rn(e, __fadd_rn(l.x, l.y));
-      // normalised pair of the score itself; a low part without a value (an
-      // infinite or NaN score) counts as zero
-      float hi, lo;
-      two_sum(hi, lo, -s, -low);
-      if (!isfinite(hi)) hi = -s;
-      if (!isfinite(lo)) lo = 0.f;
-      uint64_t key = ((uint64_t)ordered(hi) << 32) | ordered(lo);
-      if (isnan(hi)) key = 0;                                          // below every number
-      if (a.keep_own && j >= own0 && j < own1) key = ~0ull;
-      keys[j] = key;
+      const float norm = (m[0].x + m[0].y) + (m[1].x + m[1].y);
+      kn = fmaxf(kn, norm);
+      wild = wild || !(norm < INFINITY);
+      const float sum = (h[0].x + h[0].y) + (h[1].x + h[1].y);
+      keys[j] = a.keep_own && j >= own0 && j < own1 ? kOwnKey : (isnan(sum) ? 0u : ordered(sum));
     }
   }
   if (!active) return;
   __syncwarp();
   const int cnt = min(a.keep, tiles);
-  // the largest T with at least cnt keys >= T: high halves first
-  uint32_t th = 0;
-  int above = 0;  // keys whose high half is above th
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t cand = th | (1u << bit);
-    int m = 0;
-    for (int j = lane; j < tiles; j += 32) m += (uint32_t)(keys[j] >> 32) >= cand;
-    m = __reduce_add_sync(0xffffffffu, m);
-    if (m >= cnt) th = cand;
-    else above = m;
-  }
-  int equal = 0;
-  for (int j = lane; j < tiles; j += 32) equal += (uint32_t)(keys[j] >> 32) == th;
-  equal = __reduce_add_sync(0xffffffffu, equal);
-  uint64_t T = (uint64_t)th << 32;
-  int ties = cnt - above;  // of the keys equal to T, the lowest tiles taken
-  if (above + equal > cnt) {
-    // low halves among the keys whose high half is th
-    uint32_t tl = 0;
-    int more = 0;
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t cand = tl | (1u << bit);
-      int m = 0;
-      for (int j = lane; j < tiles; j += 32) m += (uint32_t)(keys[j] >> 32) == th && (uint32_t)keys[j] >= cand;
-      m = __reduce_add_sync(0xffffffffu, m);
-      if (above + m >= cnt) tl = cand;
-      else more = m;
-    }
-    T |= tl;
-    ties = cnt - above - more;
-  } else {
-    ties = 0;  // every key with high half th is kept: keys >= T
-    T -= T > 0 ? 1 : 0;
-    if (th == 0) ties = tiles;  // T = 0: keys equal to 0 are kept as well
-  }
   const int64_t block = (int64_t)head * a.n_q_blocks + q0 + warp;
   int32_t* out = a.block_idx + block * a.max_blocks;
+  for (int j = cnt + lane; j < a.max_blocks; j += 32) out[j] = -1;
+  if (lane == 0) a.block_cnt[block] = cnt;
+  const unsigned below = (1u << lane) - 1;
+
+  int above;
+  const uint32_t th = kth_largest(tiles, cnt, lane, &above, [&](int j) { return keys[j]; });
+  // A score is a sum of at most 16 fused products and 3 additions in each of
+  // four parts, off by less than 20 * 2^-24 |q| |k| (Cauchy-Schwarz); E has six
+  // times that for the norms' own rounding, and a term for underflow.
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) kn = fmaxf(kn, __shfl_xor_sync(0xffffffffu, kn, off));
+  wild = __any_sync(0xffffffffu, wild);
+  const float E = 0x1p-17f * sqrtf(qn) * sqrtf(kn) + 0x1p-120f;
+  uint32_t key_lo = 0, key_hi = kOwnKey - 1;  // all scores, unless E bounds them
+  if (th == kOwnKey) {
+    key_lo = kOwnKey;  // the block's own tiles fill every place
+  } else if (!wild && E < 0x1p100f) {
+    const float T = __uint_as_float((th & 0x80000000u) ? th & 0x7fffffffu : ~th);
+    key_lo = ordered(__fsub_rd(T, 2.f * E));
+    key_hi = ordered(__fadd_ru(T, 2.f * E));
+  }
+  int ge = 0;
+  for (int j = lane; j < tiles; j += 32) ge += keys[j] >= key_lo;
+  ge = __reduce_add_sync(0xffffffffu, ge);
+  if (ge == cnt) {  // the tiles around T are exactly the places left
+    int at = 0;
+    for (int c0 = 0; c0 < tiles; c0 += 32) {
+      const int j = c0 + lane;
+      const bool in = j < tiles && keys[j] >= key_lo;
+      const unsigned mask = __ballot_sync(0xffffffffu, in);
+      if (in) out[at + __popc(mask & below)] = j;
+      at += __popc(mask);
+    }
+    return;
+  }
+  // Exact keys of the tiles around T: those above come first, those below last.
+  for (int j = lane; j < tiles; j += 32) {
+    const uint32_t x = keys[j];
+    exact[j] = x > key_hi ? ~0ull : (x >= key_lo ? exact_key(qm, k_mean + (int64_t)j * 64) : 0);
+  }
+  __syncwarp();
+  const uint32_t high = kth_largest(tiles, cnt, lane, &above, [&](int j) { return (uint32_t)(exact[j] >> 32); });
+  int more;
+  const uint32_t low = kth_largest(tiles, cnt - above, lane, &more, [&](int j) {
+    return (uint32_t)(exact[j] >> 32) == high ? (uint32_t)exact[j] : 0u;
+  });
+  // (low keys of numbers are above 0, so the zeros of other high halves never count)
+  const uint64_t T = ((uint64_t)high << 32) | low;
+  int ties = cnt;  // places left for keys equal to T, the lowest tiles first
+  int greater = 0;
+  for (int j = lane; j < tiles; j += 32) greater += exact[j] > T;
+  ties -= __reduce_add_sync(0xffffffffu, greater);
   int at = 0, taken = 0;
   for (int c0 = 0; c0 < tiles; c0 += 32) {
     const int j = c0 + lane;
-    const uint64_t key = j < tiles ? keys[j] : 0;
-    const unsigned below = (1u << lane) - 1;
+    const uint64_t key = j < tiles ? exact[j] : 0;
     const bool tie = j < tiles && key == T;
     const unsigned tie_mask = __ballot_sync(0xffffffffu, tie);
     const bool in = j < tiles && (key > T || (tie && taken + __popc(tie_mask & below) < ties));
@@ -261,18 +369,16 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
     at += __popc(mask);
     taken += __popc(tie_mask);
   }
-  for (int j = cnt + lane; j < a.max_blocks; j += 32) out[j] = -1;
-  if (lane == 0) a.block_cnt[block] = cnt;
 }
 
 }  // namespace
 
 cudaError_t launch_block_select(const SelectArgs& a, cudaStream_t stream) {
-  pool_kernel<<<dim3(a.n_tiles, a.H), kPoolThreads, 0, stream>>>(a);
+  pool_kernel<<<2u * (unsigned)a.n_tiles * (unsigned)a.H, kPoolThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int warps = select_warps(a.max_tiles);
-  const size_t smem = (64 * kChunkRow + warps * 64) * sizeof(float2) + (size_t)warps * a.max_tiles * sizeof(uint64_t);
+  const size_t smem = score_smem(warps, a.max_tiles);
   if (smem > 48 * 1024) {
     e = cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;

@@ -93,9 +93,9 @@ void free_walk(WalkPlan* w) {
 // synchronises the stream before the host lists change).
 cudaError_t upload_walk(WalkPlan* w, cudaStream_t st) {
   const size_t units = w->units.size() * sizeof(WalkUnit), off = w->unit_off.size() * sizeof(int32_t);
-  const size_t joins = w->joins.size() * sizeof(JoinRec), blocks = w->join_blocks.size() * sizeof(int2);
+  const size_t joins = w->joins.size() * sizeof(JoinRec);
   cudaError_t e = cudaMalloc(&w->d_units, units + off);
-  if (e == cudaSuccess && joins > 0) e = cudaMalloc(&w->d_joins, joins + blocks);
+  if (e == cudaSuccess && joins > 0) e = cudaMalloc(&w->d_joins, joins);
   if (e == cudaSuccess && w->part_rows > 0) {
     e = cudaMalloc(&w->d_part_o, (size_t)w->part_rows * kHeadDim * sizeof(float));
     if (e == cudaSuccess) e = cudaMalloc(&w->d_part_ml, (size_t)w->part_rows * sizeof(float2));
@@ -103,11 +103,8 @@ cudaError_t upload_walk(WalkPlan* w, cudaStream_t st) {
   if (e == cudaSuccess) e = cudaMemcpyAsync(w->d_units, w->units.data(), units, cudaMemcpyHostToDevice, st);
   if (e == cudaSuccess)
     e = cudaMemcpyAsync(w->d_units + w->units.size(), w->unit_off.data(), off, cudaMemcpyHostToDevice, st);
-  if (e == cudaSuccess && joins > 0) {
+  if (e == cudaSuccess && joins > 0)
     e = cudaMemcpyAsync(w->d_joins, w->joins.data(), joins, cudaMemcpyHostToDevice, st);
-    if (e == cudaSuccess)
-      e = cudaMemcpyAsync(w->d_joins + w->joins.size(), w->join_blocks.data(), blocks, cudaMemcpyHostToDevice, st);
-  }
   return e;
 }
 
@@ -774,8 +771,7 @@ static ForwardArgs walk_forward_args(const Plan* plan, const WalkPlan& w, const 
 static WalkArgs walk_args(const WalkPlan& w) {
   WalkArgs x{};
   x.joins = w.d_joins;
-  x.join_blocks = reinterpret_cast<const int2*>(w.d_joins + w.joins.size());
-  x.n_join_blocks = (int32_t)w.join_blocks.size();
+  x.n_joins = (int32_t)w.joins.size();
   return x;
 }
 

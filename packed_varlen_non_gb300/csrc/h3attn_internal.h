@@ -105,8 +105,8 @@ struct WalkUnit {
 };
 static_assert(sizeof(WalkUnit) == sizeof(WorkUnit), "read as two 16-byte vectors");
 
-// Rows [row0, row1) of one head whose output the join pass combines from
-// partial rows: n_a pieces of the segment whose first row is a_row0, piece c of
+// Rows [row0, row1) of one head (at most kJoinRows: a block of the join, one warp
+// each) whose output the join pass combines from partial rows: n_a pieces of the segment whose first row is a_row0, piece c of
 // row r at partial row a_part + c * a_rows + (r - a_row0); likewise n_b pieces
 // of another one (n_b may be 0); and the keys [key_lo, key_hi) of the rows'
 // document, which the join itself attends to (empty when key_lo == key_hi).
@@ -126,11 +126,10 @@ struct WalkPlan {
   std::vector<int32_t> unit_off;       // [n_pairs + 1]
   int32_t n_pairs = 0;
   std::vector<JoinRec> joins;
-  std::vector<int2> join_blocks;       // (record, first row), kJoinRows rows each
   int64_t part_rows = 0;               // partial rows of all segments
 
   WalkUnit* d_units = nullptr;         // units, then unit_off
-  JoinRec* d_joins = nullptr;          // joins, then join_blocks
+  JoinRec* d_joins = nullptr;
   float* d_part_o = nullptr;           // [part_rows, 128] unnormalised O
   float2* d_part_ml = nullptr;         // [part_rows] (reference max in log2 units, sum)
 };
@@ -151,9 +150,9 @@ struct SelectGroup {
 };
 constexpr int kSelectWarps = 8;
 constexpr int32_t kSelectMaxTiles = 16384;  // key tiles of the longest document that can be scored
-// Query blocks per scoring block: each keeps 8 bytes per key tile in shared memory.
+// Query blocks per scoring block: each keeps 12 bytes per key tile in shared memory.
 inline int select_warps(int32_t max_tiles) {
-  const int n = 160 * 1024 / (8 * (max_tiles > 0 ? max_tiles : 1));
+  const int n = 192 * 1024 / (12 * (max_tiles > 0 ? max_tiles : 1));
   return n < 1 ? 1 : (n > kSelectWarps ? kSelectWarps : n);
 }
 
@@ -329,8 +328,7 @@ cudaError_t launch_forward_fp8(const ForwardArgs& a, int device, int num_sms, cu
 // the walk plan; a.merges is unused).
 struct WalkArgs {
   const JoinRec* joins;
-  const int2* join_blocks;
-  int32_t n_join_blocks;
+  int32_t n_joins;
   // list walk
   const int32_t* block_idx;    // [H, n_q_blocks, max_blocks]
   const int32_t* block_cnt;    // [H, n_q_blocks]

@@ -119,12 +119,9 @@ std::string finish(std::vector<Item>& items, std::vector<Join>& joins, int G, Ma
     if (items[i].direct && items[i].pieces > 1)
       joins.push_back(Join{items[i].u.q_row0, items[i].u.q_end, items[i].u.head, (int32_t)i, -1, 0, 0});
   w.joins.clear();
-  w.join_blocks.clear();
   for (const Join& j : joins) {
     JoinRec r;
     std::memset(&r, 0, sizeof(r));
-    r.row0 = j.row0;
-    r.row1 = j.row1;
     r.head = j.head;
     r.key_lo = j.key_lo;
     r.key_hi = j.key_hi;
@@ -140,8 +137,11 @@ std::string finish(std::vector<Item>& items, std::vector<Join>& joins, int G, Ma
       r.n_b = b.pieces;
       r.b_row0 = b.u.q_row0;
     }
-    for (int32_t x = j.row0; x < j.row1; x += kJoinRows) w.join_blocks.push_back(int2{(int)w.joins.size(), x});
-    w.joins.push_back(r);
+    for (int32_t x = j.row0; x < j.row1; x += kJoinRows) {
+      r.row0 = x;
+      r.row1 = std::min(x + kJoinRows, j.row1);
+      w.joins.push_back(r);
+    }
   }
   w.units.resize(segs.size());
   w.unit_off.assign((size_t)G + 1, 0);
@@ -150,6 +150,7 @@ std::string finish(std::vector<Item>& items, std::vector<Join>& joins, int G, Ma
   assign_pairs(segs.size(), [&](size_t i) { return cost[i]; }, G, pair_of.data(), load.data(), heap.data());
   w.n_pairs = group_by_pair(segs.data(), segs.size(), G, w.units.data(), w.unit_off.data(), pair_of.data(), heap.data());
   w.unit_off.resize((size_t)w.n_pairs + 1);
+  if (w.joins.size() >= (size_t(1) << 31)) return "the layout needs 2^31 or more join records";
   return "";
 }
 
