@@ -274,8 +274,15 @@ struct KeyTile {
   int32_t row, rem;
   bool prefix, bad;
 };
+// entry: list walk: the list's entry j (list_entry), so that it can be loaded
+// well before its use.
 template <int kWalk>
-__device__ __forceinline__ KeyTile key_tile(const UnitGeom& g, int j, const Walk<kWalk>& walk) {
+__device__ __forceinline__ int32_t list_entry(const UnitGeom& g, int j) {
+  if constexpr (kWalk == kWalkList) return g.list != nullptr ? __ldg(g.list + j) : -1;
+  return 0;
+}
+template <int kWalk>
+__device__ __forceinline__ KeyTile key_tile(const UnitGeom& g, int j, int32_t entry, const Walk<kWalk>& walk) {
   KeyTile t{g.kv0, 0, false, false};
   if constexpr (kWalk == kWalkDoc) {
     t.row = g.kv0 + j * kTileRows;
@@ -285,15 +292,13 @@ __device__ __forceinline__ KeyTile key_tile(const UnitGeom& g, int j, const Walk
     t.row = (t.prefix ? j : j - walk.tiles) * kTileRows + (t.prefix ? 0 : g.kv0);
     t.rem = (t.prefix ? walk.len : g.kv1) - t.row;
   } else {
-    if (g.list != nullptr) {
-      const int32_t i = __ldg(g.list + j);
-      // a tile outside the document is skipped (and reported by the producer)
-      t.bad = i < 0 || i > (g.kv1 - g.kv0 - 1) / kTileRows;
-      if (!t.bad) {
-        t.row = g.kv0 + i * kTileRows;
-        t.rem = g.kv1 - t.row;
-      }
+    // a tile outside the document is skipped (and reported by the producer)
+    const bool in = (uint32_t)entry <= (uint32_t)(g.kv1 - g.kv0 - 1) / kTileRows;
+    if (in) {
+      t.row = g.kv0 + entry * kTileRows;
+      t.rem = g.kv1 - t.row;
     }
+    t.bad = !in && g.list != nullptr;
   }
   return t;
 }
@@ -722,7 +727,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             load_k_half<kFp8>(sbase + C::SmemKV, &tm_k, bars.kv_full(0), g.head, g.kv0 + g.lo * kTileRows, rank,
                               pol_kv);
           } else {
-            kt = key_tile<kWalk>(g, g.lo, walk);
+            kt = key_tile<kWalk>(g, g.lo, list_entry<kWalk>(g, g.lo), walk);
             load_k_half<kFp8>(sbase + C::SmemKV, k_map(kt), bars.kv_full(0), g.head, kt.row, rank, pol_kv);
           }
           grp = 1;
@@ -734,7 +739,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if constexpr (kWalk == kWalkDoc) {
             kt.row = g.kv0 + (j + 1) * kTileRows;
           } else {
-            if (has_k) kt = key_tile<kWalk>(g, j + 1, walk);
+            if (has_k) kt = key_tile<kWalk>(g, j + 1, list_entry<kWalk>(g, j + 1), walk);
             if (vt.bad && rank == 0) atomicExch(a.err, kErrBlockIndex);
           }
           if (!has_k && has_next) {
@@ -744,7 +749,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if constexpr (kWalk == kWalkDoc)
               kt.row = n.kv0 + n.lo * kTileRows;
             else
-              kt = key_tile<kWalk>(n, n.lo, walk);
+              kt = key_tile<kWalk>(n, n.lo, list_entry<kWalk>(n, n.lo), walk);
           }
           const uint32_t b = grp % kGroups;
           ok = dev::mbar_wait(bars.kv_empty(b), ((grp / kGroups) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
@@ -1057,7 +1062,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ring bookkeeping by one lane of one warp per CTA
       const bool releases = lead_lane && st == g.n_st - 1;
       const bool checks_kv = lead_lane && st == 0;
-      float m_used = -INFINITY, l = 0.f;
+      // (other walks: finite, so that the exponents of a row that sees no key are -inf, not NaN)
+      float m_used = kWalk == kWalkDoc ? -INFINITY : -3.402823466e38f, l = 0.f;
       // fp8: this row's q scale (1 for rows past the tensor, never stored)
       float sq_row = 1.f;
       if constexpr (kFp8) {
@@ -1164,18 +1170,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       } else {
         // bf16: 64-key halves (see the kernel header).
-        int rem_next = 0;
-        if constexpr (kWalk != kWalkDoc) rem_next = key_tile<kWalk>(g, g.lo, walk).rem;
+        int32_t entry_next = list_entry<kWalk>(g, g.lo);  // a list entry is loaded a tile ahead of its use
         for (int j = g.lo; ok && j < g.hi; ++j) {
           const uint32_t t = t_unit + (j - g.lo);  // the pair's running key-tile count
           const float rsc = sl2;  // score scale in log2 units: softmax_scale log2(e)
-          int rem;
-          if constexpr (kWalk == kWalkDoc) {
-            rem = key_tile<kWalk>(g, j, walk).rem;
-          } else {  // a list entry is loaded a tile ahead of its use
-            rem = rem_next;
-            if (j + 1 < g.hi) rem_next = key_tile<kWalk>(g, j + 1, walk).rem;
-          }
+          const int rem = key_tile<kWalk>(g, j, entry_next, walk).rem;
+          if (kWalk == kWalkList && j + 1 < g.hi) entry_next = list_entry<kWalk>(g, j + 1);
           const uint32_t kv_bar = bars.kv_full((t + 1) % kGroups), kv_par = ((t + 1) / kGroups) & 1;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -1218,8 +1218,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               alpha = dev::ex2_approx(m_used - m_new);  // 0 on the first half of a unit (m_used = -inf)
               m_used = m_new;
             }
-            // (a row that has seen no key yet, m_used = -inf: exponents -inf, not NaN)
-            const float neg = kWalk != kWalkDoc && m_used == -INFINITY ? 0.f : -m_used;
+            const float neg = -m_used;
             float rs8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             uint32_t p[32];
 #pragma unroll

@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(kPoolThreads, 4) pool_kernel(SelectArgs a) {
   const int head = blockIdx.x % a.H, tile = (blockIdx.x / a.H) >> 1;
   const bool is_k = (blockIdx.x / a.H) & 1;
   const int lane16 = threadIdx.x & 15, group = threadIdx.x >> 4, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.launch_dependents;");  // (the scoring blocks wait for this grid's end)
   const int4 t = __ldg(a.tiles + tile);
   const int n = t.y - t.x;
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_k ? a.k_hat : a.q_hat) + (int64_t)t.x * a.stride +
@@ -178,52 +179,94 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
-// Order-preserving key of the score of query mean q (shared memory) and key
-// mean k to about 2^-44: ordered bits of a normalised pair; 0 for NaN.
-static __device__ __noinline__ uint64_t exact_key(const float2* q, const float2* k) {
-  // even and odd dims apart; each product q k is x + e exactly
-  float2 h = make_float2(0.f, 0.f), l = make_float2(0.f, 0.f);
-#pragma unroll 4
-  for (int p = 0; p < 64; ++p) {
-    const float2 a = q[p], b = __ldg(k + p);
-    const float2 x = mul2(a, b);
-    const float2 e = fma2(a, b, mul2(x, make_float2(-1.f, -1.f)));
-    const float2 s = add2(h, x), bb = sub2(s, h);
-    const float2 err = add2(sub2(h, sub2(s, bb)), sub2(x, bb));
-    h = s;
-    l = add2(l, add2(err, e));
-  }
-  float s, e, hi, lo;
-  two_sum(s, e, h.x, h.y);
-  two_sum(hi, lo, s, __fadd_rn(e, __fadd_rn(l.x, l.y)));
-  // an infinite score has no low part
-  if (!isfinite(hi)) hi = s;
+// (hi, lo) += q k for two dims at once, even and odd dims apart: each product is
+// x + e exactly, and so is each sum.
+__device__ __forceinline__ void acc_product(float2& h, float2& l, float2 q, float2 k) {
+  const float2 x = mul2(q, k);
+  const float2 e = fma2(q, k, mul2(x, make_float2(-1.f, -1.f)));
+  const float2 s = add2(h, x), bb = sub2(s, h);
+  const float2 err = add2(sub2(h, sub2(s, bb)), sub2(x, bb));
+  h = s;
+  l = add2(l, add2(err, e));
+}
+
+// Order-preserving key of the score s.x + s.y (a normalised pair's ordered bits;
+// 0 for NaN, an infinite score has no low part).
+__device__ __forceinline__ uint64_t pair_key(float2 s) {
+  float hi, lo;
+  two_sum(hi, lo, s.x, s.y);
+  if (!isfinite(hi)) hi = s.x;
   if (!isfinite(lo)) lo = 0.f;
   return isnan(hi) ? 0 : ((uint64_t)ordered(hi) << 32) | ordered(lo);
 }
 
-// The largest x with at least cnt of a warp's keys >= x, and how many keys are
-// above x.  key(j) gives key j of 0 .. n - 1.
+// The exact key of one tile by one lane: q (shared memory), k: 64 float2 each.
+__device__ __noinline__ uint64_t exact_key_lane(const float2* q, const float2* k) {
+  float2 h = make_float2(0.f, 0.f), l = make_float2(0.f, 0.f);
+#pragma unroll 8
+  for (int p = 0; p < 64; ++p) acc_product(h, l, q[p], __ldg(k + p));
+  float2 s = make_float2(h.x, l.x + l.y);
+  acc(s.x, s.y, h.y);
+  return pair_key(s);
+}
+
+// The same by a whole warp (every lane gets it): four dims per lane.
+__device__ __forceinline__ uint64_t exact_key_warp(const float2* q, const float2* k, int lane) {
+  const float4 kk = __ldg(reinterpret_cast<const float4*>(k) + lane);
+  float2 h = make_float2(0.f, 0.f), l = make_float2(0.f, 0.f);
+  acc_product(h, l, q[2 * lane], make_float2(kk.x, kk.y));
+  acc_product(h, l, q[2 * lane + 1], make_float2(kk.z, kk.w));
+  float2 s = make_float2(h.x, l.x + l.y);
+  acc(s.x, s.y, h.y);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+    acc2(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, off), __shfl_xor_sync(0xffffffffu, s.y, off)));
+  return pair_key(make_float2(__shfl_sync(0xffffffffu, s.x, 0), __shfl_sync(0xffffffffu, s.y, 0)));
+}
+
+// The cnt-th largest of a warp's keys 0 .. n - 1 (key(j), called for j of this
+// lane: lane, lane + 32, ...) and how many are above it.  Bitwise from the
+// first bit in which keys differ; it ends as soon as a candidate has exactly
+// cnt keys at or above it, after about log2(n) bits.
 template <class Key>
 __device__ __forceinline__ uint32_t kth_largest(int n, int cnt, int lane, int* above, Key key) {
-  uint32_t th = 0;
+  uint32_t any = 0, all = ~0u;
+  for (int j = lane; j < n; j += 32) {
+    any |= key(j);
+    all &= key(j);
+  }
+  any = __reduce_or_sync(0xffffffffu, any);
+  all = __reduce_and_sync(0xffffffffu, all);
+  uint32_t th = all;  // the common leading bits; below them, bits that every key has do not matter
   *above = 0;
+  const uint32_t differ = any ^ all;
+  if (differ == 0) return all;
+  const int top = 31 - __clz(differ);
+  th &= ~((2u << top) - 1);
 #pragma unroll 1
-  for (int bit = 31; bit >= 0; --bit) {
+  for (int bit = top; bit >= 0; --bit) {
     const uint32_t cand = th | (1u << bit);
     int m = 0;
     for (int j = lane; j < n; j += 32) m += key(j) >= cand;
     m = __reduce_add_sync(0xffffffffu, m);
-    if (m >= cnt)
-      th = cand;
-    else
-      *above = m;
+    if (m >= cnt) th = cand;
+    else *above = m;
+    if (m == cnt) break;
   }
-  return th;
+  // the smallest key at or above th is the cnt-th largest
+  uint32_t least = ~0u;
+  for (int j = lane; j < n; j += 32)
+    if (key(j) >= th) least = min(least, key(j));
+  least = __reduce_min_sync(0xffffffffu, least);
+  int greater = 0;
+  for (int j = lane; j < n; j += 32) greater += key(j) > least;
+  *above = __reduce_add_sync(0xffffffffu, greater);
+  return least;
 }
 
 constexpr int kChunk = 32;                       // key tiles staged at a time
 constexpr int kChunkRow = kChunk + 1;            // 8-byte words per pair of dims (padded)
+constexpr int kStage = kChunk * 64 / (32 * kSelectWarps);  // words per thread of a full block
 constexpr uint32_t kOwnKey = 0xffffffffu;        // above every score's key
 
 // Bytes of shared memory: km [64][kChunkRow] float2, qm [warps][64] float2,
@@ -275,11 +318,31 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
   const float2* k_mean = reinterpret_cast<const float2*>(a.k_mean + ((int64_t)head * a.n_tiles + tile0) * kHeadDim);
   float kn = 0.f;      // largest squared norm of this lane's key means
   bool wild = false;   // a norm that fp32 does not hold (NaN included)
+  // The next chunk's means are on their way while this one's are used.
+  float2 next[kStage];
+  const auto fetch = [&](int c0) {
+#pragma unroll
+    for (int x = 0; x < kStage; ++x) {
+      const int i = threadIdx.x + x * (int)blockDim.x, j = i >> 6;
+      if (i < kChunk * 64 && c0 + j < tiles) next[x] = __ldg(k_mean + (int64_t)(c0 + j) * 64 + (i & 63));
+    }
+  };
+  const bool staged = blockDim.x == 32 * kSelectWarps;  // (smaller blocks load as they store)
+  if (staged) fetch(0);
   for (int c0 = 0; c0 < tiles; c0 += kChunk) {
     __syncthreads();  // (also orders qm before its first read)
-    for (int i = threadIdx.x; i < kChunk * 64; i += blockDim.x) {
-      const int j = i >> 6, p = i & 63;
-      if (c0 + j < tiles) km[p * kChunkRow + j] = __ldg(k_mean + (int64_t)(c0 + j) * 64 + p);
+    if (staged) {
+#pragma unroll
+      for (int x = 0; x < kStage; ++x) {
+        const int i = threadIdx.x + x * 32 * kSelectWarps;
+        km[(i & 63) * kChunkRow + (i >> 6)] = next[x];
+      }
+      fetch(c0 + kChunk);
+    } else {
+      for (int i = threadIdx.x; i < kChunk * 64; i += blockDim.x) {
+        const int j = i >> 6, p = i & 63;
+        if (c0 + j < tiles) km[p * kChunkRow + j] = __ldg(k_mean + (int64_t)(c0 + j) * 64 + p);
+      }
     }
     __syncthreads();
     const int j = c0 + lane;
@@ -319,8 +382,9 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
   wild = __any_sync(0xffffffffu, wild);
   const float E = 0x1p-17f * sqrtf(qn) * sqrtf(kn) + 0x1p-120f;
   uint32_t key_lo = 0, key_hi = kOwnKey - 1;  // all scores, unless E bounds them
-  if (th == kOwnKey) {
-    key_lo = kOwnKey;  // the block's own tiles fill every place
+  const bool own_only = th == kOwnKey;
+  if (own_only) {
+    key_lo = key_hi = kOwnKey;  // the block's own tiles fill every place, the lowest first
   } else if (!wild && E < 0x1p100f) {
     const float T = __uint_as_float((th & 0x80000000u) ? th & 0x7fffffffu : ~th);
     key_lo = ordered(__fsub_rd(T, 2.f * E));
@@ -340,10 +404,49 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
     }
     return;
   }
-  // Exact keys of the tiles around T: those above come first, those below last.
+  int n_in = 0;
+  for (int j = lane; j < tiles; j += 32) n_in += keys[j] > key_hi;
+  n_in = __reduce_add_sync(0xffffffffu, n_in);
+  const int band = ge - n_in, places = cnt - n_in;
+  if (band <= 32) {
+    // few tiles around T: lane i takes the i-th of them and ranks its exact key
+    int mine = -1, at = 0;
+    for (int c0 = 0; c0 < tiles; c0 += 32) {
+      const int j = c0 + lane;
+      unsigned mask = __ballot_sync(0xffffffffu, j < tiles && keys[j] >= key_lo && keys[j] <= key_hi);
+      const int here = __popc(mask);
+      if (lane >= at && lane < at + here) mine = c0 + (int)__fns(mask, 0, lane - at + 1);
+      at += here;
+    }
+    uint64_t key = 0;
+    for (int i = 0; i < band; ++i) {
+      if (own_only) break;
+      const uint64_t x = exact_key_warp(qm, k_mean + (int64_t)__shfl_sync(0xffffffffu, mine, i) * 64, lane);
+      if (i == lane) key = x;
+    }
+    int rank = 0;
+    for (int i = 0; i < band; ++i) {
+      const uint64_t x = __shfl_sync(0xffffffffu, key, i);
+      rank += x > key || (x == key && i < lane);
+    }
+    // a place each: the tile's key moves above or below the band
+    if (lane < band) keys[mine] = rank < places ? kOwnKey : 0u;
+    __syncwarp();
+    at = 0;
+    const uint32_t floor = key_hi == kOwnKey ? kOwnKey : key_hi + 1;
+    for (int c0 = 0; c0 < tiles; c0 += 32) {
+      const int j = c0 + lane;
+      const bool in = j < tiles && keys[j] >= floor;
+      const unsigned mask = __ballot_sync(0xffffffffu, in);
+      if (in) out[at + __popc(mask & below)] = j;
+      at += __popc(mask);
+    }
+    return;
+  }
+  // Many (ties): the exact keys of all of them, searched again.
   for (int j = lane; j < tiles; j += 32) {
     const uint32_t x = keys[j];
-    exact[j] = x > key_hi ? ~0ull : (x >= key_lo ? exact_key(qm, k_mean + (int64_t)j * 64) : 0);
+    exact[j] = x > key_hi ? ~0ull : (x >= key_lo ? exact_key_lane(qm, k_mean + (int64_t)j * 64) : 0);
   }
   __syncwarp();
   const uint32_t high = kth_largest(tiles, cnt, lane, &above, [&](int j) { return (uint32_t)(exact[j] >> 32); });
