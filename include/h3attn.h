@@ -328,7 +328,7 @@ h3attn_status h3attn_plan_sparse_info(h3attn_plan_t plan, int32_t* q_block, int3
  * Errors: EINVAL for NULL or misaligned (tensors 16, lists 4 bytes) pointers, a
  * bad stride, keep outside [1, max_blocks], lists that overlap the tensors or
  * each other, or without h3attn_plan_set_sparse; EUNSUPPORTED for a document of
- * more than 2,097,152 tokens. */
+ * more than 1,572,864 tokens. */
 h3attn_status h3attn_block_select(h3attn_plan_t plan, const void* q_hat, const void* k_hat, int64_t qkv_row_stride,
                                   int32_t keep, int32_t keep_own, int32_t* block_idx, int32_t* block_cnt,
                                   void* cuda_stream);

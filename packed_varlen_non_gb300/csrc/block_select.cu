@@ -22,15 +22,17 @@
 // where a two-sum of unordered numbers takes seven; with seven, the fp32 pipe
 // took two thirds of the loads' time).
 //
-// score_kernel gives a warp to a query block and a lane to a key tile: 32
-// tiles' means are staged in shared memory, two dims per 8-byte word, and read
-// without conflicts by all warps of the block, which share document and head.
-// Scores are first plain fp32 sums with an error bound E; the keep-th largest
-// of them, T, is found by a bitwise search over order-preserving keys.  A tile
-// above T + 2 E is kept and one below T - 2 E is not, whatever the exact scores
-// are.  Only where more tiles lie between than places are left (a few per cent
-// of the query blocks, and ties) are the scores between computed as pairs and
-// searched again.
+// score_kernel takes eight query blocks of one document and head.  Its warps
+// score 32 dims of 32 tiles at a time, a tile to a lane, against all eight: the
+// key means, tiles innermost, are read once per block and straight into
+// registers, the query means come from shared memory as broadcasts (with a warp per query
+// block and the key means in shared memory, that memory's bandwidth bound it:
+// 22 us for 160 tiles).  Then each warp selects for one query block.  Scores are
+// first plain fp32 sums with an error bound E; the keep-th largest of them, T,
+// is found by a bitwise search over order-preserving keys.  A tile above T + 2 E
+// is kept and one below T - 2 E is not, whatever the exact scores are.  Only
+// where more tiles lie between than places are left (a few per cent of the
+// query blocks, and ties) are the scores between computed as pairs and ranked.
 #include "device_common.cuh"
 #include "qk_norm.cuh"
 
@@ -157,11 +159,10 @@ __global__ void __launch_bounds__(kPoolThreads, 4) pool_kernel(SelectArgs a) {
   float2 s = part[0][d];
 #pragma unroll
   for (int w = 1; w < 8; ++w) acc2(s, part[w][d]);
-  const int64_t at = ((int64_t)head * a.n_tiles + tile) * kHeadDim + d;
-  if (is_k)
-    a.k_mean[at] = mean_of(s, (float)n);
+  if (is_k)  // tiles innermost, two dims a word: a warp's lanes score consecutive tiles
+    reinterpret_cast<float*>(a.k_mean + ((int64_t)head * 64 + (d >> 1)) * a.n_tiles + tile)[d & 1] = mean_of(s, (float)n);
   else
-    a.q_sum[at] = s;
+    a.q_sum[((int64_t)head * a.n_tiles + tile) * kHeadDim + d] = s;
 }
 
 // Order-preserving bits of a float that is not NaN (-0 as +0).
@@ -200,22 +201,23 @@ __device__ __forceinline__ uint64_t pair_key(float2 s) {
   return isnan(hi) ? 0 : ((uint64_t)ordered(hi) << 32) | ordered(lo);
 }
 
-// The exact key of one tile by one lane: q (shared memory), k: 64 float2 each.
-__device__ __noinline__ uint64_t exact_key_lane(const float2* q, const float2* k) {
+// The exact key of one tile by one lane: q (shared memory, kSelectWarps words
+// apart) and k (`row` words apart), 64 words each.
+__device__ __noinline__ uint64_t exact_key_lane(const float2* q, const float2* k, int64_t row) {
   float2 h = make_float2(0.f, 0.f), l = make_float2(0.f, 0.f);
 #pragma unroll 8
-  for (int p = 0; p < 64; ++p) acc_product(h, l, q[p], __ldg(k + p));
+  for (int p = 0; p < 64; ++p) acc_product(h, l, q[p * kSelectWarps], __ldg(k + p * row));
   float2 s = make_float2(h.x, l.x + l.y);
   acc(s.x, s.y, h.y);
   return pair_key(s);
 }
 
 // The same by a whole warp (every lane gets it): four dims per lane.
-__device__ __forceinline__ uint64_t exact_key_warp(const float2* q, const float2* k, int lane) {
-  const float4 kk = __ldg(reinterpret_cast<const float4*>(k) + lane);
+__device__ __forceinline__ uint64_t exact_key_warp(const float2* q, const float2* k, int64_t row, int lane) {
+  const float2 k0 = __ldg(k + 2 * lane * row), k1 = __ldg(k + (2 * lane + 1) * row);
   float2 h = make_float2(0.f, 0.f), l = make_float2(0.f, 0.f);
-  acc_product(h, l, q[2 * lane], make_float2(kk.x, kk.y));
-  acc_product(h, l, q[2 * lane + 1], make_float2(kk.z, kk.w));
+  acc_product(h, l, q[2 * lane * kSelectWarps], k0);
+  acc_product(h, l, q[(2 * lane + 1) * kSelectWarps], k1);
   float2 s = make_float2(h.x, l.x + l.y);
   acc(s.x, s.y, h.y);
 #pragma unroll
@@ -264,107 +266,113 @@ __device__ __forceinline__ uint32_t kth_largest(int n, int cnt, int lane, int* a
   return least;
 }
 
-constexpr int kChunk = 32;                       // key tiles staged at a time
-constexpr int kChunkRow = kChunk + 1;            // 8-byte words per pair of dims (padded)
-constexpr int kStage = kChunk * 64 / (32 * kSelectWarps);  // words per thread of a full block
 constexpr uint32_t kOwnKey = 0xffffffffu;        // above every score's key
 
-// Bytes of shared memory: km [64][kChunkRow] float2, qm [warps][64] float2,
-// exact keys [warps][max_tiles] uint64, keys [warps][max_tiles] uint32.
+constexpr int kParts = 4;                        // parts of a score, 32 dims each
+
+// Bytes of shared memory: qm [64][kSelectWarps] float2, then for each query block
+// its scores' parts [kParts][max_tiles] float, which become its keys (uint32, the
+// first part's place) and exact keys (uint64, the last two parts').
 size_t score_smem(int warps, int32_t max_tiles) {
-  return (64 * kChunkRow + (size_t)warps * 64) * sizeof(float2) + (size_t)warps * max_tiles * 12;
+  return 64 * kSelectWarps * sizeof(float2) + (size_t)warps * max_tiles * (kParts * sizeof(float));
 }
 
 __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) {
   extern __shared__ float2 smem[];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float2* km = smem;
-  float2* qm = smem + 64 * kChunkRow + warp * 64;
-  uint64_t* const exact0 = reinterpret_cast<uint64_t*>(smem + 64 * kChunkRow + warps * 64);
-  uint64_t* exact = exact0 + (int64_t)warp * a.max_tiles;
-  uint32_t* keys = reinterpret_cast<uint32_t*>(exact0 + (int64_t)warps * a.max_tiles) + (int64_t)warp * a.max_tiles;
+  __shared__ uint32_t kn_of[kParts];  // largest squared norms of the key means' parts (bits of floats >= 0)
+  float2* qm = smem + warp;  // word p at qm[p * kSelectWarps]
+  float* const parts0 = reinterpret_cast<float*>(smem + 64 * kSelectWarps);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(parts0 + (int64_t)warp * kParts * a.max_tiles);
+  uint64_t* exact = reinterpret_cast<uint64_t*>(keys + 2 * (int64_t)a.max_tiles);
   const int head = blockIdx.y;
   const int4 g0 = __ldg(reinterpret_cast<const int4*>(a.groups + blockIdx.x));
-  const int first = __ldg(&a.groups[blockIdx.x].first);
-  const int q0 = g0.x, n = g0.y, tile0 = g0.z, tiles = g0.w;
+  const int2 g1 = __ldg(reinterpret_cast<const int2*>(a.groups + blockIdx.x) + 2);
+  const int q0 = g0.x, n = g0.y, tile0 = g0.z, tiles = g0.w, first = g1.x;
   const bool active = warp < n;
-  // this block's own key tiles, relative to the document
+  // this block's own key tiles, relative to the document, and its rows
   const int own0 = (first + warp) * a.tiles_per_q_block, own1 = min(own0 + a.tiles_per_q_block, tiles);
-  float rows = 1.f;
-  if (active) rows = (float)(__ldg(&a.tiles[tile0 + own1 - 1].y) - __ldg(&a.tiles[tile0 + own0].x));
+  const float rows = (float)(min(own1 * kKeyTile, g1.y) - own0 * kKeyTile);
+  if (threadIdx.x < kParts) kn_of[threadIdx.x] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the pooled sums are complete
   float qn = 0.f;  // squared norm of the query block's mean
   if (active) {
     // mean of the query block: four dims per lane, the sums of up to four tiles
+    const float4* p = reinterpret_cast<const float4*>(a.q_sum + ((int64_t)head * a.n_tiles + tile0 + own0) * kHeadDim + 4 * lane);
+    float4 u[4], v[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      u[t] = v[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (own0 + t < own1) {
+        u[t] = p[64 * t];
+        v[t] = p[64 * t + 1];
+      }
+    }
     float2 s[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] = make_float2(0.f, 0.f);
-    for (int t = own0; t < own1; ++t) {
-      const float4* p = reinterpret_cast<const float4*>(a.q_sum + ((int64_t)head * a.n_tiles + tile0 + t) * kHeadDim + 4 * lane);
-      const float4 u = p[0], v = p[1];
-      acc2(s[0], make_float2(u.x, u.y));
-      acc2(s[1], make_float2(u.z, u.w));
-      acc2(s[2], make_float2(v.x, v.y));
-      acc2(s[3], make_float2(v.z, v.w));
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      acc2(s[0], make_float2(u[t].x, u[t].y));
+      acc2(s[1], make_float2(u[t].z, u[t].w));
+      acc2(s[2], make_float2(v[t].x, v[t].y));
+      acc2(s[3], make_float2(v[t].z, v[t].w));
     }
     const float2 x = make_float2(mean_of(s[0], rows), mean_of(s[1], rows));
     const float2 y = make_float2(mean_of(s[2], rows), mean_of(s[3], rows));
-    qm[2 * lane] = x;
-    qm[2 * lane + 1] = y;
+    qm[2 * lane * kSelectWarps] = x;
+    qm[(2 * lane + 1) * kSelectWarps] = y;
     qn = x.x * x.x + x.y * x.y + (y.x * y.x + y.y * y.y);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) qn += __shfl_xor_sync(0xffffffffu, qn, off);
   }
-  const float2* k_mean = reinterpret_cast<const float2*>(a.k_mean + ((int64_t)head * a.n_tiles + tile0) * kHeadDim);
-  float kn = 0.f;      // largest squared norm of this lane's key means
-  bool wild = false;   // a norm that fp32 does not hold (NaN included)
-  // The next chunk's means are on their way while this one's are used.
-  float2 next[kStage];
-  const auto fetch = [&](int c0) {
+  __syncthreads();
+  // Scores: a warp takes a part (32 dims) of 32 tiles' scores against all the
+  // block's query blocks, so that each word of the key means is read once per
+  // block, with one wait.
+  const int64_t row = a.n_tiles;
+  const float2* k_mean = a.k_mean + (int64_t)head * 64 * row + tile0;
+  const int items = (tiles + 31) / 32 * kParts;
+  for (int i = warp; i < items; i += warps) {
+    const int j = i / kParts * 32 + lane, part = i % kParts;
+    const float2* kp = k_mean + min(j, tiles - 1) + part * (64 / kParts) * row;
+    const float4* q = reinterpret_cast<const float4*>(smem + part * (64 / kParts) * kSelectWarps);
+    float2 k[64 / kParts];
 #pragma unroll
-    for (int x = 0; x < kStage; ++x) {
-      const int i = threadIdx.x + x * (int)blockDim.x, j = i >> 6;
-      if (i < kChunk * 64 && c0 + j < tiles) next[x] = __ldg(k_mean + (int64_t)(c0 + j) * 64 + (i & 63));
-    }
-  };
-  const bool staged = blockDim.x == 32 * kSelectWarps;  // (smaller blocks load as they store)
-  if (staged) fetch(0);
-  for (int c0 = 0; c0 < tiles; c0 += kChunk) {
-    __syncthreads();  // (also orders qm before its first read)
-    if (staged) {
+    for (int p = 0; p < 64 / kParts; ++p) k[p] = __ldg(kp + p * row);
+    float2 h[kSelectWarps], m = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int x = 0; x < kStage; ++x) {
-        const int i = threadIdx.x + x * 32 * kSelectWarps;
-        km[(i & 63) * kChunkRow + (i >> 6)] = next[x];
-      }
-      fetch(c0 + kChunk);
-    } else {
-      for (int i = threadIdx.x; i < kChunk * 64; i += blockDim.x) {
-        const int j = i >> 6, p = i & 63;
-        if (c0 + j < tiles) km[p * kChunkRow + j] = __ldg(k_mean + (int64_t)(c0 + j) * 64 + p);
+    for (int x = 0; x < kSelectWarps; ++x) h[x] = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int p = 0; p < 64 / kParts; ++p) {
+      m = fma2(k[p], k[p], m);
+#pragma unroll
+      for (int x = 0; x < kSelectWarps / 2; ++x) {
+        const float4 qq = q[p * (kSelectWarps / 2) + x];
+        h[2 * x] = fma2(make_float2(qq.x, qq.y), k[p], h[2 * x]);
+        h[2 * x + 1] = fma2(make_float2(qq.z, qq.w), k[p], h[2 * x + 1]);
       }
     }
-    __syncthreads();
-    const int j = c0 + lane;
-    if (active && j < tiles) {
-      float2 h[2], m[2];
+    const float norm = m.x + m.y;  // (infinite for one that fp32 does not hold)
+    const uint32_t kn = __reduce_max_sync(0xffffffffu, __float_as_uint(norm < INFINITY ? norm : INFINITY));
+    if (lane == 0) atomicMax(&kn_of[part], kn);
+    if (j < tiles) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) h[x] = m[x] = make_float2(0.f, 0.f);
-#pragma unroll 16
-      for (int p = 0; p < 64; ++p) {
-        const float2 k = km[p * kChunkRow + lane];
-        h[p & 1] = fma2(qm[p], k, h[p & 1]);
-        m[p & 1] = fma2(k, k, m[p & 1]);
-      }
-      const float norm = (m[0].x + m[0].y) + (m[1].x + m[1].y);
-      kn = fmaxf(kn, norm);
-      wild = wild || !(norm < INFINITY);
-      const float sum = (h[0].x + h[0].y) + (h[1].x + h[1].y);
-      keys[j] = a.keep_own && j >= own0 && j < own1 ? kOwnKey : (isnan(sum) ? 0u : ordered(sum));
+      for (int x = 0; x < kSelectWarps; ++x)
+        if (x < n) parts0[((int64_t)x * kParts + part) * a.max_tiles + j] = h[x].x + h[x].y;
     }
   }
+  __syncthreads();
   if (!active) return;
+  const float* parts = reinterpret_cast<const float*>(keys);
+  for (int j = lane; j < tiles; j += 32) {
+    const float sum = (parts[j] + parts[a.max_tiles + j]) + (parts[2 * a.max_tiles + j] + parts[3 * a.max_tiles + j]);
+    keys[j] = a.keep_own && j >= own0 && j < own1 ? kOwnKey : (isnan(sum) ? 0u : ordered(sum));
+  }
   __syncwarp();
+  float kn = 0.f;  // (at least the largest squared norm of a key mean)
+#pragma unroll
+  for (int p = 0; p < kParts; ++p) kn += __uint_as_float(kn_of[p]);
   const int cnt = min(a.keep, tiles);
   const int64_t block = (int64_t)head * a.n_q_blocks + q0 + warp;
   int32_t* out = a.block_idx + block * a.max_blocks;
@@ -374,18 +382,15 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
 
   int above;
   const uint32_t th = kth_largest(tiles, cnt, lane, &above, [&](int j) { return keys[j]; });
-  // A score is a sum of at most 16 fused products and 3 additions in each of
-  // four parts, off by less than 20 * 2^-24 |q| |k| (Cauchy-Schwarz); E has six
-  // times that for the norms' own rounding, and a term for underflow.
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) kn = fmaxf(kn, __shfl_xor_sync(0xffffffffu, kn, off));
-  wild = __any_sync(0xffffffffu, wild);
+  // A score is eight sums of 16 fused products and seven additions, off by at
+  // most 24 * 2^-24 |q| |k| (Cauchy-Schwarz).  E has five times that, for the
+  // norms' own rounding too, and a term for underflow.
   const float E = 0x1p-17f * sqrtf(qn) * sqrtf(kn) + 0x1p-120f;
   uint32_t key_lo = 0, key_hi = kOwnKey - 1;  // all scores, unless E bounds them
   const bool own_only = th == kOwnKey;
   if (own_only) {
     key_lo = key_hi = kOwnKey;  // the block's own tiles fill every place, the lowest first
-  } else if (!wild && E < 0x1p100f) {
+  } else if (E < 0x1p100f) {
     const float T = __uint_as_float((th & 0x80000000u) ? th & 0x7fffffffu : ~th);
     key_lo = ordered(__fsub_rd(T, 2.f * E));
     key_hi = ordered(__fadd_ru(T, 2.f * E));
@@ -421,7 +426,7 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
     uint64_t key = 0;
     for (int i = 0; i < band; ++i) {
       if (own_only) break;
-      const uint64_t x = exact_key_warp(qm, k_mean + (int64_t)__shfl_sync(0xffffffffu, mine, i) * 64, lane);
+      const uint64_t x = exact_key_warp(qm, k_mean + __shfl_sync(0xffffffffu, mine, i), row, lane);
       if (i == lane) key = x;
     }
     int rank = 0;
@@ -446,7 +451,7 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
   // Many (ties): the exact keys of all of them, searched again.
   for (int j = lane; j < tiles; j += 32) {
     const uint32_t x = keys[j];
-    exact[j] = x > key_hi ? ~0ull : (x >= key_lo ? exact_key_lane(qm, k_mean + (int64_t)j * 64) : 0);
+    exact[j] = x > key_hi ? ~0ull : (x >= key_lo ? exact_key_lane(qm, k_mean + j, row) : 0);
   }
   __syncwarp();
   const uint32_t high = kth_largest(tiles, cnt, lane, &above, [&](int j) { return (uint32_t)(exact[j] >> 32); });

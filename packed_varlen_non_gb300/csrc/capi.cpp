@@ -678,19 +678,19 @@ h3attn_status h3attn_plan_set_sparse(h3attn_plan_t plan, int32_t q_block, int32_
     for (int32_t d = 0; d < plan->n_docs; ++d) {
       const int32_t L = cu[d + 1] - cu[d], blocks = (L + q_block - 1) / q_block, tiles = (L + kKeyTile - 1) / kKeyTile;
       for (int32_t i = 0; i < blocks; i += warps)
-        sp.groups.push_back(SelectGroup{sp.n_q_blocks + i, std::min(warps, blocks - i), tile0, tiles, i, {0, 0, 0}});
+        sp.groups.push_back(SelectGroup{sp.n_q_blocks + i, std::min(warps, blocks - i), tile0, tiles, i, L, {0, 0}});
       sp.n_q_blocks += blocks;
       tile0 += tiles;
     }
   } catch (const std::bad_alloc&) {
     return fail(H3ATTN_ENOMEM, "host allocation failed while building the sparse lists");
   }
-  const size_t rows = (size_t)plan->num_heads * plan->ktiles_host.size() * kHeadDim;
+  const size_t words = (size_t)plan->num_heads * plan->ktiles_host.size() * kHeadDim;
   const size_t group_bytes = sp.groups.size() * sizeof(SelectGroup);
   const h3attn_status s = attach_walk(&sp.walk, "sparse", cuda_stream, [&](cudaStream_t st) {
     cudaError_t m = cudaMalloc(&sp.d_groups, group_bytes);
-    if (m == cudaSuccess) m = cudaMalloc(&sp.d_q_sum, rows * sizeof(float2));
-    if (m == cudaSuccess) m = cudaMalloc(&sp.d_k_mean, rows * sizeof(float));
+    if (m == cudaSuccess) m = cudaMalloc(&sp.d_q_sum, words * sizeof(float2));
+    if (m == cudaSuccess) m = cudaMalloc(&sp.d_k_mean, words / 2 * sizeof(float2));
     if (m == cudaSuccess) m = cudaMemcpyAsync(sp.d_groups, sp.groups.data(), group_bytes, cudaMemcpyHostToDevice, st);
     return m;
   });

@@ -146,13 +146,15 @@ struct SelectGroup {
   int32_t q0, n;          // query blocks [q0, q0 + n)
   int32_t tile0, tiles;   // the document's key tiles [tile0, tile0 + tiles) of the plan's tile table
   int32_t first;          // index of q0 within its document
-  int32_t pad[3];
+  int32_t len;            // the document's tokens
+  int32_t pad[2];
 };
+static_assert(sizeof(SelectGroup) == 32, "SelectGroup is read as vectors");
 constexpr int kSelectWarps = 8;
-constexpr int32_t kSelectMaxTiles = 16384;  // key tiles of the longest document that can be scored
-// Query blocks per scoring block: each keeps 12 bytes per key tile in shared memory.
+constexpr int32_t kSelectMaxTiles = 12288;  // key tiles of the longest document that can be scored
+// Query blocks per scoring block: each keeps 16 bytes per key tile in shared memory.
 inline int select_warps(int32_t max_tiles) {
-  const int n = 192 * 1024 / (12 * (max_tiles > 0 ? max_tiles : 1));
+  const int n = 192 * 1024 / (16 * (max_tiles > 0 ? max_tiles : 1));
   return n < 1 ? 1 : (n > kSelectWarps ? kSelectWarps : n);
 }
 
@@ -165,7 +167,7 @@ struct SparsePlan {
   std::vector<SelectGroup> groups;
   SelectGroup* d_groups = nullptr;
   float2* d_q_sum = nullptr;           // [H, tiles, 128] sums of q-hat rows (high, low)
-  float* d_k_mean = nullptr;           // [H, tiles, 128] means of k-hat rows
+  float2* d_k_mean = nullptr;          // [H, 64, tiles] means of k-hat rows, two dims a word
 };
 
 struct PrefixPlan {
@@ -357,7 +359,7 @@ struct SelectArgs {
   int32_t n_q_blocks;
   int32_t tiles_per_q_block;
   float2* q_sum;
-  float* k_mean;
+  float2* k_mean;
   int32_t keep;
   int32_t keep_own;
   int32_t max_blocks;

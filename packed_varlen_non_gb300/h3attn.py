@@ -120,7 +120,7 @@ def _check(status: int, fn: str):
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream or None
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None
@@ -169,6 +169,7 @@ def h3attn_plan_create(docs, num_heads: int, rope_base: float = 10000.0, head_di
 
 
 def h3attn_plan_destroy(plan):
+    _list_sizes.pop(plan, None)
     _check(load().h3attn_plan_destroy(plan), "h3attn_plan_destroy")
 
 
@@ -324,10 +325,15 @@ def h3attn_forward_noalloc(cu_seqlens, num_heads: int, q, k, v, o, softmax_scale
 
 def _qkv_stride(q, others, given):
     if given is None and not isinstance(q, int):
-        strides = {int(x.stride(0)) for x in (q, *others)}
-        if len(strides) != 1:
-            raise ValueError(f"tensors of one call must share one row stride (got {sorted(strides)})")
+        given = q.stride(0)
+        for x in others:
+            if x.stride(0) != given:
+                raise ValueError(f"tensors of one call must share one row stride (got {given}, {x.stride(0)})")
     return _row_stride(q, given)
+
+
+# Sizes of the lists of the plans that have them (fixed once set).
+_list_sizes: dict = {}
 
 
 def _check_lists(plan, block_idx, block_cnt):
@@ -335,18 +341,22 @@ def _check_lists(plan, block_idx, block_cnt):
     be int32, contiguous and of those sizes; raw pointers are the caller's."""
     if isinstance(block_idx, int) or isinstance(block_cnt, int) or block_idx is None or block_cnt is None:
         return
-    info = h3attn_plan_sparse_info(plan)
-    rows = info["num_heads"] * info["n_q_blocks"]
-    for name, t, n in (("block_idx", block_idx, rows * info["max_blocks"]), ("block_cnt", block_cnt, rows)):
-        if str(t.dtype) != "torch.int32" or not t.is_contiguous() or t.numel() != n:
-            raise ValueError(f"{name} must be a contiguous int32 tensor of {n} elements "
-                             f"(got {tuple(t.shape)}, {t.dtype})")
+    sizes = _list_sizes.get(plan)
+    if sizes is None:
+        return  # the call itself refuses a plan without lists
+    for t, n in ((block_idx, sizes[0]), (block_cnt, sizes[1])):
+        if t.numel() != n or t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous():
+            raise ValueError("block_idx and block_cnt must be contiguous int32 tensors of "
+                             f"{sizes[0]} and {sizes[1]} elements (got {tuple(t.shape)}, {t.dtype})")
 
 
 def h3attn_plan_set_sparse(plan, q_block: int, max_blocks: int, stream=None):
     """Adds the block-sparse work list to a plan (once per plan)."""
     _check(load().h3attn_plan_set_sparse(plan, int(q_block), int(max_blocks), _stream(stream)),
            "h3attn_plan_set_sparse")
+    info = h3attn_plan_sparse_info(plan)
+    rows = info["num_heads"] * info["n_q_blocks"]
+    _list_sizes[plan] = (rows * info["max_blocks"], rows)
 
 
 def h3attn_plan_sparse_info(plan) -> dict:
