@@ -16,7 +16,7 @@
 // pool_kernel is HBM-bound: it reads q-hat and k-hat once, one block per
 // (128-row tile, head, tensor) with all its loads in flight, and leaves 1.5 KB
 // per tile and head.  Query blocks begin on tile boundaries, so the same tiles
-// serve both.  Each thread sums eight rows of eight dims onto an anchor 2^6
+// serve both.  Each thread sums sixteen rows of eight dims onto an anchor 2^6
 // times above their largest magnitude: every addition then rounds at one fixed
 // place, and its error is two subtractions away (four operations an element
 // where a two-sum of unordered numbers takes seven; with seven, the fp32 pipe
@@ -40,7 +40,8 @@ namespace h3 {
 
 namespace {
 
-constexpr int kPoolThreads = 256;
+constexpr int kPoolThreads = 128;
+constexpr int kPoolRows = 16 * kKeyTile / kPoolThreads;  // rows per thread (16 lanes a row)
 
 // s + err = a + b exactly (Knuth).
 __device__ __forceinline__ void two_sum(float& s, float& err, float a, float b) {
@@ -83,23 +84,26 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
 
-// Elementwise maximum of two pairs of bf16 numbers (NaN if either is).
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+// Elementwise larger magnitude of two pairs of bf16 numbers (NaN if either is),
+// under a sign that means nothing.
+__device__ __forceinline__ uint32_t max_mag_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
-// 1.5 * 2^(e + 6) for a number of exponent e (sums of eight numbers up to it
+// 1.5 * 2^(e + 6) for a number of exponent e (sums of kPoolRows numbers up to it
 // stay in the anchor's binade); no further than the largest exponent.
 __device__ __forceinline__ float anchor_of(uint32_t bits) {
   const uint32_t e = min(bits & 0x7f800000u, 248u << 23);
   return __uint_as_float((e + (6u << 23)) | 0x00400000u);
 }
 
+static_assert(kPoolRows <= 16, "2^(e + 1) * kPoolRows <= 2^(e + 5)");
+
 // One (tile, tensor, head): sums of q-hat's rows as pairs, means of k-hat's.
-__global__ void __launch_bounds__(kPoolThreads, 4) pool_kernel(SelectArgs a) {
-  __shared__ float2 part[8][128];
+__global__ void __launch_bounds__(kPoolThreads, 5) pool_kernel(SelectArgs a) {
+  __shared__ float2 part[kPoolThreads / 32][128];
   const int head = blockIdx.x % a.H, tile = (blockIdx.x / a.H) >> 1;
   const bool is_k = (blockIdx.x / a.H) & 1;
   const int lane16 = threadIdx.x & 15, group = threadIdx.x >> 4, warp = threadIdx.x >> 5;
@@ -108,19 +112,19 @@ __global__ void __launch_bounds__(kPoolThreads, 4) pool_kernel(SelectArgs a) {
   const int n = t.y - t.x;
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_k ? a.k_hat : a.q_hat) + (int64_t)t.x * a.stride +
                              head * kHeadDim + lane16 * 8;
-  uint4 raw[8];
+  uint4 raw[kPoolRows];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = group + 16 * i;
+  for (int i = 0; i < kPoolRows; ++i) {
+    const int r = group + kPoolThreads / 16 * i;
     raw[i] = r < n ? __ldg(reinterpret_cast<const uint4*>(src + r * a.stride)) : make_uint4(0, 0, 0, 0);
   }
-  uint4 m = make_uint4(0, 0, 0, 0);  // largest magnitude of each dim
+  uint4 m = raw[0];  // largest magnitude of each dim
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    m.x = max_bf16x2(m.x, raw[i].x & 0x7fff7fffu);
-    m.y = max_bf16x2(m.y, raw[i].y & 0x7fff7fffu);
-    m.z = max_bf16x2(m.z, raw[i].z & 0x7fff7fffu);
-    m.w = max_bf16x2(m.w, raw[i].w & 0x7fff7fffu);
+  for (int i = 1; i < kPoolRows; ++i) {
+    m.x = max_mag_bf16x2(m.x, raw[i].x);
+    m.y = max_mag_bf16x2(m.y, raw[i].y);
+    m.z = max_mag_bf16x2(m.z, raw[i].z);
+    m.w = max_mag_bf16x2(m.w, raw[i].w);
   }
   const uint32_t mw[4] = {m.x, m.y, m.z, m.w};
   float2 anchor[4], hi[4], lo[4];
@@ -131,7 +135,7 @@ __global__ void __launch_bounds__(kPoolThreads, 4) pool_kernel(SelectArgs a) {
     lo[e] = make_float2(0.f, 0.f);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < kPoolRows; ++i) {
     float v[8];
     qkn::unpack8(raw[i], v);
 #pragma unroll
@@ -154,11 +158,11 @@ __global__ void __launch_bounds__(kPoolThreads, 4) pool_kernel(SelectArgs a) {
     }
   }
   __syncthreads();
+  static_assert(kPoolThreads == kHeadDim, "a thread per dim");
   const int d = threadIdx.x;
-  if (d >= kHeadDim) return;
   float2 s = part[0][d];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) acc2(s, part[w][d]);
+  for (int w = 1; w < kPoolThreads / 32; ++w) acc2(s, part[w][d]);
   if (is_k)  // tiles innermost, two dims a word: a warp's lanes score consecutive tiles
     reinterpret_cast<float*>(a.k_mean + ((int64_t)head * 64 + (d >> 1)) * a.n_tiles + tile)[d & 1] = mean_of(s, (float)n);
   else
@@ -267,6 +271,79 @@ __device__ __forceinline__ uint32_t kth_largest(int n, int cnt, int lane, int* a
 }
 
 constexpr uint32_t kOwnKey = 0xffffffffu;        // above every score's key
+
+// Keys [*lo, *hi] of the scores within 2 E of the one whose key is th (all
+// scores where E does not bound them; the own tiles where they fill every place).
+__device__ __forceinline__ void border(uint32_t th, float E, uint32_t* lo, uint32_t* hi) {
+  *lo = 0;
+  *hi = kOwnKey - 1;
+  if (th == kOwnKey) {
+    *lo = *hi = kOwnKey;
+  } else if (E < 0x1p100f) {
+    const float T = __uint_as_float((th & 0x80000000u) ? th & 0x7fffffffu : ~th);
+    *lo = ordered(__fsub_rd(T, 2.f * E));
+    *hi = ordered(__fadd_ru(T, 2.f * E));
+  }
+}
+
+// The selection where the keys fit in R registers a lane and no exact score is
+// needed; false where one is, or where E bounds nothing.  *th: the cnt-th
+// largest key.
+template <int R>
+__device__ __forceinline__ bool pick_few(const uint32_t* keys, int tiles, int cnt, int lane, float E, int32_t* out,
+                                         uint32_t* kth) {
+  uint32_t r[R];
+  uint32_t any = 0, all = ~0u;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int j = 32 * i + lane;
+    r[i] = j < tiles ? keys[j] : 0;
+    any |= r[i];
+    all &= j < tiles ? r[i] : ~0u;
+  }
+  any = __reduce_or_sync(0xffffffffu, any);
+  all = __reduce_and_sync(0xffffffffu, all);
+  const uint32_t differ = any ^ all;
+  uint32_t th = all;
+  if (differ != 0) {
+    const int top = 31 - __clz(differ);
+    th &= ~((2u << top) - 1);
+#pragma unroll 1
+    for (int bit = top; bit >= 0; --bit) {
+      const uint32_t cand = th | (1u << bit);
+      int m = 0;
+#pragma unroll
+      for (int i = 0; i < R; ++i) m += r[i] >= cand;
+      m = __reduce_add_sync(0xffffffffu, m);
+      if (m >= cnt) th = cand;
+      if (m == cnt) break;
+    }
+    uint32_t least = ~0u;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (r[i] >= th) least = min(least, r[i]);
+    th = __reduce_min_sync(0xffffffffu, least);
+  }
+  *kth = th;
+  uint32_t lo, hi;
+  border(th, E, &lo, &hi);
+  if (lo == 0) return false;  // (0 also stands behind the last tile)
+  unsigned mask[R];
+  int ge = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    mask[i] = __ballot_sync(0xffffffffu, r[i] >= lo);
+    ge += __popc(mask[i]);
+  }
+  if (ge != cnt) return false;
+  int at = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    if (r[i] >= lo) out[at + __popc(mask[i] & ((1u << lane) - 1))] = 32 * i + lane;
+    at += __popc(mask[i]);
+  }
+  return true;
+}
 
 constexpr int kParts = 4;                        // parts of a score, 32 dims each
 
@@ -380,21 +457,20 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
   if (lane == 0) a.block_cnt[block] = cnt;
   const unsigned below = (1u << lane) - 1;
 
-  int above;
-  const uint32_t th = kth_largest(tiles, cnt, lane, &above, [&](int j) { return keys[j]; });
   // A score is eight sums of 16 fused products and seven additions, off by at
-  // most 24 * 2^-24 |q| |k| (Cauchy-Schwarz).  E has five times that, for the
+  // most 24 * 2^-24 |q| |k| (Cauchy-Schwarz).  E has 2.6 times that, for the
   // norms' own rounding too, and a term for underflow.
-  const float E = 0x1p-17f * sqrtf(qn) * sqrtf(kn) + 0x1p-120f;
-  uint32_t key_lo = 0, key_hi = kOwnKey - 1;  // all scores, unless E bounds them
-  const bool own_only = th == kOwnKey;
-  if (own_only) {
-    key_lo = key_hi = kOwnKey;  // the block's own tiles fill every place, the lowest first
-  } else if (E < 0x1p100f) {
-    const float T = __uint_as_float((th & 0x80000000u) ? th & 0x7fffffffu : ~th);
-    key_lo = ordered(__fsub_rd(T, 2.f * E));
-    key_hi = ordered(__fadd_ru(T, 2.f * E));
-  }
+  const float E = 0x1p-18f * sqrtf(qn) * sqrtf(kn) + 0x1p-120f;
+  uint32_t th;
+  if (tiles <= 32 ? pick_few<1>(keys, tiles, cnt, lane, E, out, &th)
+      : tiles <= 96 ? pick_few<3>(keys, tiles, cnt, lane, E, out, &th)
+                    : tiles <= 256 && pick_few<8>(keys, tiles, cnt, lane, E, out, &th))
+    return;
+  int above;
+  if (tiles > 256) th = kth_largest(tiles, cnt, lane, &above, [&](int j) { return keys[j]; });
+  const bool own_only = th == kOwnKey;  // the block's own tiles fill every place, the lowest first
+  uint32_t key_lo, key_hi;
+  border(th, E, &key_lo, &key_hi);
   int ge = 0;
   for (int j = lane; j < tiles; j += 32) ge += keys[j] >= key_lo;
   ge = __reduce_add_sync(0xffffffffu, ge);
@@ -415,14 +491,17 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
   const int band = ge - n_in, places = cnt - n_in;
   if (band <= 32) {
     // few tiles around T: lane i takes the i-th of them and ranks its exact key
-    int mine = -1, at = 0;
+    int at = 0;
+    int* list = reinterpret_cast<int*>(exact);
     for (int c0 = 0; c0 < tiles; c0 += 32) {
       const int j = c0 + lane;
-      unsigned mask = __ballot_sync(0xffffffffu, j < tiles && keys[j] >= key_lo && keys[j] <= key_hi);
-      const int here = __popc(mask);
-      if (lane >= at && lane < at + here) mine = c0 + (int)__fns(mask, 0, lane - at + 1);
-      at += here;
+      const bool in = j < tiles && keys[j] >= key_lo && keys[j] <= key_hi;
+      const unsigned mask = __ballot_sync(0xffffffffu, in);
+      if (in) list[at + __popc(mask & below)] = j;
+      at += __popc(mask);
     }
+    __syncwarp();
+    const int mine = lane < band ? list[lane] : 0;
     uint64_t key = 0;
     for (int i = 0; i < band; ++i) {
       if (own_only) break;
