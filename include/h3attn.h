@@ -391,6 +391,8 @@ h3attn_status h3attn_forward_prefix(h3attn_plan_t plan, const void* q, const voi
  *            block's list), for kind 1 key tiles [lo, hi) of "the prefix's
  *            tiles, then the document's"; last the first partial row (-1: the
  *            segment writes the output itself);
+ *            With q_block 256, a pair runs its segments two at a time, side by
+ *            side;
  *   unit_off [*n_pairs_used + 1] int32: pair p runs units [unit_off[p], unit_off[p + 1]);
  *   joins    [*n_joins][16] int32, the rows combined from partial rows: rows
  *            [r0, r1) (at most 8), head, key_lo; then of segment a its first partial row,

@@ -133,21 +133,23 @@ constexpr int kMmaWarp = 8;
 constexpr int kTmaWarp = 9;
 constexpr int kQWarp = 10;
 constexpr int kTileRows = 128;
-constexpr int kSlots = 6;                              // ring slots (16 KB each)
-constexpr int kGroups = kSlots / 2;                    // key/value groups in flight
-// barriers: q_full[4] q_empty[4] q_ready[4] kv_full[G] kv_empty[G] s_ready[2][2] p_ready[2][2] pv_done[2][2] drain o_staged[4]
-constexpr int kNumBars = 12 + 2 * kGroups + 4 + 4 + 4 + 1 + 4;
 // Shared-memory layout: 2 buffers x 2 query tiles, then the ring.  bf16: a Q
 // tile is 128 rows x 128 dims in two 16 KB halves of 64 dims, a slot 16 KB;
 // fp8 (e4m3): a Q tile is one 16 KB block of 128-byte rows, a slot 8 KB.
-template <bool kFp8>
+// kPair (two query blocks side by side): three Q tiles and eight ring slots.
+template <bool kFp8, bool kPair = false>
 struct Cfg {
+  static constexpr int Slots = kPair ? 8 : 6;          // ring slots
+  static constexpr int Groups = Slots / 2;             // key/value groups in flight
+  static constexpr int QTiles = kPair ? 3 : 4;
+  // q_full[4] q_empty[4] q_ready[4] kv_full[G] kv_empty[G] s_ready[2][2] p_ready[2][2] pv_done[2][2] drain o_staged[4]
+  static constexpr int NumBars = 12 + 2 * Groups + 4 + 4 + 4 + 1 + 4;
   static constexpr uint32_t QTileBytes = kFp8 ? 128 * 128 : 128 * 128 * 2;
   static constexpr uint32_t SlotBytes = kFp8 ? 64 * 128 : 64 * 128 * 2;
   static constexpr uint32_t SmemQ = 0;
-  static constexpr uint32_t SmemKV = 4 * QTileBytes;
-  static constexpr uint32_t SmemBar = SmemKV + kSlots * SlotBytes;
-  static constexpr uint32_t SmemMisc = SmemBar + kNumBars * 8;
+  static constexpr uint32_t SmemKV = QTiles * QTileBytes;
+  static constexpr uint32_t SmemBar = SmemKV + Slots * SlotBytes;
+  static constexpr uint32_t SmemMisc = SmemBar + NumBars * 8;
   static constexpr size_t SmemAlloc = SmemMisc + 16 + 1024;  // slack to align the base to 1 KB
   static_assert(SmemAlloc <= 227 * 1024, "shared memory per CTA");
 };
@@ -176,7 +178,13 @@ constexpr uint32_t kIdescPV = kIdescBf16 | ((128u >> 3) << 17) | (1u << 16);
 // both K-major (the FP8 pipeline takes whole 128-key tiles)
 constexpr uint32_t kIdescF8 = (1u << 4) | ((128u >> 3) << 17) | ((256u >> 4) << 24);
 
-// Q slot i = 2 * buffer + query tile; the unit with ordinal k (per pair) uses buffer k & 1.
+// Q slot i = 2 * buffer + query tile; the unit with ordinal k (per pair) uses
+// buffer k & 1.  With kPair the three Q tiles rotate.
+template <bool kPair>
+__device__ __forceinline__ int q_slot_of(int k, int s) {
+  return kPair ? (2 * k + s) % 3 : 2 * (k & 1) + s;
+}
+template <int kGroups>
 struct Bars {
   uint32_t base;
   __device__ uint32_t q_full(int i) const { return base + 8 * i; }
@@ -200,6 +208,18 @@ struct Bars {
 // its query block, the shared prefix's tiles and then the document's.
 constexpr int kWalkDoc = 0, kWalkList = 1, kWalkPrefix = 2;
 
+// kPair (list walk, query blocks of 256 rows): a unit is two segments of up to
+// 256 rows, each with a walk of its own -- two query blocks with different
+// lists, of any documents and heads.  Query tile s of both CTAs (rows q0 + 128
+// rank + i) belongs to segment s.  The two run in lockstep: a unit has as many
+// steps as the longer list, the other one's last steps are masked tiles.  Every
+// step needs a K and a V tile per query tile, twice the L2 traffic per MMA of
+// the shared walk, and two groups of the ring, so the ring has eight slots (the
+// fourth group is what lets a group be loaded a whole step ahead of its use) at
+// the cost of the fourth Q tile.  Group 0 holds both query tiles' first K tiles;
+// group 1 + 2 t + s holds V(t) and K(t + 1) of query tile s, t counting the
+// pair's steps.
+
 // What a walk needs besides the unit.
 template <int kWalk>
 struct Walk {};
@@ -219,14 +239,38 @@ struct UnitGeom {
   int32_t q0, kv0, kv1, head, lo, hi, part, n_st;  // key tiles [lo, hi) of the walk
   int32_t v_off;                                   // FP8: the document's first key in the transposed V
   int32_t q1;                                      // end of the unit's query rows
-  const int32_t* list;                             // list walk: the query block's tiles (null: none to visit)
+  const int32_t* list;                             // list walk: the segment's tiles, step j's at list[j] (null: none)
+  int32_t n;                                       // list walk: entries of the list; the steps after them are masked
 };
 
-template <int kWalk>
-__device__ __forceinline__ UnitGeom unit_geom(const WorkUnit* units, int u, const Walk<kWalk>& walk) {
-  const int4 w = __ldg(reinterpret_cast<const int4*>(units) + 2 * u);
-  const int4 x = __ldg(reinterpret_cast<const int4*>(units) + 2 * u + 1);
+// First row of this CTA's query tile s of a unit.
+template <bool kPair>
+__device__ __forceinline__ int32_t tile_row(const UnitGeom& g, int s, uint32_t rank) {
+  return g.q0 + (kPair ? 0 : s * 2 * kTileRows) + (int32_t)rank * kTileRows;
+}
+
+// Entries [*lo, *hi) of its query block's list that a segment (its record's
+// second half) visits: piece i of m takes [n i / m, n (i + 1) / m) of the n.
+__device__ __forceinline__ int64_t list_range(const int4& x, const Walk<kWalkList>& walk, int32_t* lo, int32_t* hi) {
+  *lo = *hi = 0;
+  if (x.y < 0) return 0;  // no segment
+  const int64_t block = (int64_t)x.x * walk.blocks + x.y;
+  const uint32_t i = (uint32_t)x.z & 0xffffu, m = (uint32_t)x.z >> 16;
+  const uint64_t n = (uint64_t)min(max(__ldg(walk.cnt + block), 0), walk.cap);
+  *lo = m == 1 ? 0 : (int32_t)(n * i / m);
+  *hi = m == 1 ? (int32_t)n : (int32_t)(n * (i + 1) / m);
+  return block * walk.cap;
+}
+
+// Unit u (kPair: its segment s).
+template <int kWalk, bool kPair = false>
+__device__ __forceinline__ UnitGeom unit_geom(const WorkUnit* units, int u, const Walk<kWalk>& walk, int s = 0) {
+  const int r = kPair ? 2 * u + s : u;
+  const int4 w = __ldg(reinterpret_cast<const int4*>(units) + 2 * r);
+  const int4 x = __ldg(reinterpret_cast<const int4*>(units) + 2 * r + 1);
   UnitGeom g;
+  g.list = nullptr;
+  g.n = 0;
   if constexpr (kWalk == kWalkDoc) {
     g.q0 = w.x;
     g.kv0 = w.y;
@@ -237,7 +281,6 @@ __device__ __forceinline__ UnitGeom unit_geom(const WorkUnit* units, int u, cons
     g.part = x.z;
     g.v_off = x.w;
     g.q1 = w.z;
-    g.list = nullptr;
     g.n_st = (w.x + 2 * kTileRows < w.z) ? 2 : 1;  // query tile 1 of the pair holds rows from 256 on
   } else {  // a WalkUnit
     g.q0 = w.x;
@@ -247,22 +290,23 @@ __device__ __forceinline__ UnitGeom unit_geom(const WorkUnit* units, int u, cons
     g.head = x.x;
     g.part = x.w;
     g.v_off = 0;
-    g.list = nullptr;
-    g.n_st = (w.x + 2 * kTileRows < w.y) ? 2 : 1;
+    g.n_st = kPair || (w.x + 2 * kTileRows < w.y) ? 2 : 1;
     if constexpr (kWalk == kWalkPrefix) {
       g.lo = x.y;
       g.hi = x.z;
     } else {
-      // piece i of m takes entries [n i / m, n (i + 1) / m) of the block's n
-      const int64_t block = (int64_t)x.x * walk.blocks + x.y;
-      const uint32_t i = (uint32_t)x.z & 0xffffu, m = (uint32_t)x.z >> 16;
-      const uint64_t n = (uint64_t)min(max(__ldg(walk.cnt + block), 0), walk.cap);
-      g.lo = m == 1 ? 0 : (int32_t)(n * i / m);
-      g.hi = m == 1 ? (int32_t)n : (int32_t)(n * (i + 1) / m);
-      if (g.hi > g.lo)
-        g.list = walk.idx + block * walk.cap;
-      else
-        g.hi = g.lo + 1;  // nothing listed: one fully masked tile
+      int32_t lo, hi;
+      const int64_t at = list_range(x, walk, &lo, &hi);
+      g.n = hi - lo;
+      if (g.n > 0) g.list = walk.idx + at + lo;
+      int32_t steps = g.n;
+      if constexpr (kPair) {
+        const int4 y = __ldg(reinterpret_cast<const int4*>(units) + 2 * (2 * u + 1 - s) + 1);
+        list_range(y, walk, &lo, &hi);
+        steps = max(steps, hi - lo);
+      }
+      g.lo = 0;
+      g.hi = max(steps, 1);  // nothing listed: one fully masked tile
     }
   }
   return g;
@@ -278,7 +322,7 @@ struct KeyTile {
 // well before its use.
 template <int kWalk>
 __device__ __forceinline__ int32_t list_entry(const UnitGeom& g, int j) {
-  if constexpr (kWalk == kWalkList) return g.list != nullptr ? __ldg(g.list + j) : -1;
+  if constexpr (kWalk == kWalkList) return j < g.n ? __ldg(g.list + j) : -1;
   return 0;
 }
 template <int kWalk>
@@ -298,7 +342,7 @@ __device__ __forceinline__ KeyTile key_tile(const UnitGeom& g, int j, int32_t en
       t.row = g.kv0 + entry * kTileRows;
       t.rem = g.kv1 - t.row;
     }
-    t.bad = !in && g.list != nullptr;
+    t.bad = !in && j < g.n;
   }
   return t;
 }
@@ -569,18 +613,20 @@ static __device__ __noinline__ void norm_rope_q_row(uint32_t tile, uint32_t r, c
 // scales (per query row, per key tile, per V channel), kind::f8f6f4 MMAs,
 // P rounded to e4m3; everything else as the bf16 kernel.
 // kWalk: the key tiles a unit visits (bf16 only where not its own document).
-template <bool kFp8, int kWalk>
+template <bool kFp8, int kWalk, bool kPair>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                        ForwardArgs a, int o_tma, const __grid_constant__ Walk<kWalk> walk) {
   static_assert(!kFp8 || kWalk == kWalkDoc, "the FP8 pipeline walks documents");
-  using C = Cfg<kFp8>;
+  static_assert(!kPair || kWalk == kWalkList, "two segments side by side: the list walk");
+  using C = Cfg<kFp8, kPair>;
+  constexpr int kSlots = C::Slots, kGroups = C::Groups;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = dev::smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   unsigned char* smem = smem_raw + (sbase - raw);
-  const Bars bars{sbase + C::SmemBar};
+  const Bars<kGroups> bars{sbase + C::SmemBar};
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SmemMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::SmemMisc + 4);
 
@@ -647,16 +693,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       int k = 0;
       for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-        const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
+        UnitGeom g = unit_geom<kWalk, kPair>(a.units, u, walk);
 #pragma unroll 1
         for (int s = 0; s < 2 && s < g.n_st; ++s) {
-          const int i = 2 * (k & 1) + s;
+          const int i = q_slot_of<kPair>(k, s);
+          if (kPair && s == 1) g = unit_geom<kWalk, kPair>(a.units, u, walk, 1);
           ok = dev::mbar_wait(bars.o_staged(i), use[i] & 1, abort_flag, a.err, kTimeoutNs);
           ++use[i];
           if (!ok) break;
           if (o_tma != 0 && g.part < 0) {
             const uint32_t tile = sbase + C::SmemQ + i * C::QTileBytes;
-            const int32_t base_row = g.q0 + s * 2 * kTileRows + (int32_t)rank * kTileRows;
+            const int32_t base_row = tile_row<kPair>(g, s, rank);
             bool any = false;
 #pragma unroll 1
             for (int w = 0; w < 4; ++w) {
@@ -708,10 +755,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if constexpr (kWalk == kWalkPrefix) return t.prefix ? &walk.tm_v : &tm_v;
         return &tm_v;
       };
+      if constexpr (kPair) {
+        // group 0: both query tiles' first K tiles; then, per step and query tile,
+        // a group of its V tile and its next K tile (see kPair)
+        int k = 0;
+        int32_t next[2] = {-1, -1};  // entries of the tiles whose K was sent last
+        for (int u = u_begin; ok && u < u_end; ++u, ++k) {
+          const UnitGeom g[2] = {unit_geom<kWalk, kPair>(a.units, u, walk, 0), unit_geom<kWalk, kPair>(a.units, u, walk, 1)};
+          const bool has_next = u + 1 < u_end;
+          if (k == 0) {
+            ok = dev::mbar_wait(bars.kv_empty(0), 1, abort_flag, a.err, kTimeoutNs);
+            if (!ok) break;
+            dev::mbar_arrive_expect_tx(bars.kv_full(0), 2 * C::SlotBytes);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              next[s] = list_entry<kWalk>(g[s], 0);
+              const KeyTile t = key_tile<kWalk>(g[s], 0, next[s], walk);
+              load_k_half<kFp8>(sbase + C::SmemKV + s * C::SlotBytes, &tm_k, bars.kv_full(0), g[s].head, t.row, rank, pol_kv);
+            }
+            grp = 1;
+          }
+          for (int j = 0; ok && j < g[0].hi; ++j) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              const KeyTile vt = key_tile<kWalk>(g[s], j, next[s], walk);
+              KeyTile kt = vt;
+              int k_head = g[s].head;
+              const bool has_k = j + 1 < g[s].hi || has_next;
+              if (j + 1 < g[s].hi) {
+                next[s] = list_entry<kWalk>(g[s], j + 1);
+                kt = key_tile<kWalk>(g[s], j + 1, next[s], walk);
+              } else if (has_next) {
+                const UnitGeom n = unit_geom<kWalk, kPair>(a.units, u + 1, walk, s);
+                next[s] = list_entry<kWalk>(n, 0);
+                kt = key_tile<kWalk>(n, 0, next[s], walk);
+                k_head = n.head;
+              }
+              if (vt.bad && rank == 0) atomicExch(a.err, kErrBlockIndex);
+              const uint32_t b = grp % kGroups;
+              ok = dev::mbar_wait(bars.kv_empty(b), ((grp / kGroups) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
+              if (!ok) break;
+              const uint32_t slot = sbase + C::SmemKV + ((2 * grp) % kSlots) * C::SlotBytes;
+              dev::mbar_arrive_expect_tx(bars.kv_full(b), has_k ? 2 * C::SlotBytes : C::SlotBytes);
+              load_v_half<kFp8>(slot, &tm_v, bars.kv_full(b), g[s].head, vt.row, rank, pol_kv);
+              if (has_k) load_k_half<kFp8>(slot + C::SlotBytes, &tm_k, bars.kv_full(b), k_head, kt.row, rank, pol_kv);
+              ++grp;
+            }
+          }
+        }
+      } else {
       int k = 0;
       KeyTile kt;  // the tile whose K was sent last (dense: only its row is used)
       for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-        const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
+        const UnitGeom g = unit_geom<kWalk, kPair>(a.units, u, walk);
         const bool has_next = u + 1 < u_end;
         // Key/value groups: group 0 is the first unit's first K tile (ring slot
         // 0); group n >= 1 is V(j) with the next K tile -- K(j+1), or the next
@@ -743,7 +839,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (vt.bad && rank == 0) atomicExch(a.err, kErrBlockIndex);
           }
           if (!has_k && has_next) {
-            const UnitGeom n = unit_geom<kWalk>(a.units, u + 1, walk);
+            const UnitGeom n = unit_geom<kWalk, kPair>(a.units, u + 1, walk);
             has_k = true;
             k_head = n.head;
             if constexpr (kWalk == kWalkDoc)
@@ -772,8 +868,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ++grp;
           // the next unit's Q tiles, behind this unit's first group
           if constexpr (kFp8)
-            if (j == g.lo && has_next) load_q(unit_geom<kWalk>(a.units, u + 1, walk), k + 1);
+            if (j == g.lo && has_next) load_q(unit_geom<kWalk, kPair>(a.units, u + 1, walk), k + 1);
         }
+      }
       }
       if (!ok) {
         // drain: wait (bounded) for every copy this thread issued into the ring and Q
@@ -799,7 +896,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool issued = false;
         int k = 0;
         for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-          const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
+          const UnitGeom g = unit_geom<kWalk, kPair>(a.units, u, walk);
           const uint32_t qb = 2 * (k & 1);
           // Q tiles of this unit, prepared in both CTAs (and, for the first
           // unit, the first K group landed in both)
@@ -878,27 +975,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t vb = sbase + C::SmemKV + vs * C::SlotBytes;
         issue_pv(d, pt, vb + 4096 * h, acc);
       };
-      // The first QK (half h) of query tile s of unit gg: Q slot qbase + s (its
-      // readiness in both CTAs is awaited before half 0), K in ring slot ks.
-      auto first_qk = [&](const UnitGeom& gg, uint32_t qbase, uint32_t ks, int s, int h) {
+      // The first QK (half h) of query tile s of a unit: Q slot qs (its readiness
+      // in both CTAs is awaited before half 0), K in ring slot ks.
+      auto first_qk = [&](uint32_t qs, uint32_t ks, int s, int h) {
         if (h == 0) {
           ok = __all_sync(0xffffffffu,
-                          dev::mbar_wait(bars.q_ready(qbase + s), q_use[qbase + s] & 1, abort_flag, a.err, kTimeoutNs));
-          ++q_use[qbase + s];
+                          dev::mbar_wait(bars.q_ready(qs), q_use[qs] & 1, abort_flag, a.err, kTimeoutNs));
+          ++q_use[qs];
           if (!ok) return;
           dev::tc_fence_after();
         }
-        qk_half(s, qbase + s, ks, h);
+        qk_half(s, qs, ks, h);
         issued = true;
       };
+      // Ring slots of query tile s's V and next K in this step (kPair: group
+      // 1 + 2 t + s, slots 2 (1 + 2 t + s) and the one after it, mod 8)
+      auto v_at = [&](int s) { return kPair ? (vslot + 2 * s) % kSlots : vslot; };
+      auto k_at = [&](int s) { return kPair ? (vslot + 2 * s + 1) % kSlots : kslot; };
+      auto advance = [&]() {
+        if constexpr (kPair) {
+          vslot = (vslot + 4) % kSlots;
+        } else {
+          vslot = vslot + 2 >= (uint32_t)kSlots ? vslot + 2 - kSlots : vslot + 2;
+          kslot = kslot + 2 >= (uint32_t)kSlots ? kslot + 2 - kSlots : kslot + 2;
+        }
+      };
+      if constexpr (kPair) vslot = 2;
       for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-        const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
-        const uint32_t qb = 2 * (k & 1);
+        const UnitGeom g = unit_geom<kWalk, kPair>(a.units, u, walk);
+        const uint32_t q_at[2] = {(uint32_t)q_slot_of<kPair>(k, 0), (uint32_t)q_slot_of<kPair>(k, 1)};
         if (k == 0) {
-          // the pair's first unit: its first K tile is group 0 (ring slot 0),
-          // and Q-ready also covers that group's arrival in both CTAs
-          for (int h = 0; ok && h < 2; ++h)
-            for (int s = 0; ok && s < g.n_st; ++s) first_qk(g, qb, 0, s, h);
+          // the pair's first unit: its first K tile is group 0 (ring slot 0;
+          // kPair: slot s for query tile s), and Q-ready also covers that group's
+          // arrival in both CTAs
+          if constexpr (kPair) {
+            for (int s = 0; ok && s < 2; ++s)
+              for (int h = 0; ok && h < 2; ++h) first_qk(q_at[s], s, s, h);
+          } else {
+            for (int h = 0; ok && h < 2; ++h)
+              for (int s = 0; ok && s < g.n_st; ++s) first_qk(q_at[s], 0, s, h);
+          }
           if (!ok) break;
         }
         // Per key tile j and half h, for each query tile s: wait for P(s, j, h),
@@ -911,8 +1027,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // unit's last query tile sees S of half 1, so that QK comes after
         // every PV of this unit.
         const bool has_next = u + 1 < u_end;
-        const UnitGeom gn = unit_geom<kWalk>(a.units, has_next ? u + 1 : u, walk);
-        const uint32_t qn = 2 * ((k + 1) & 1);
+        const UnitGeom gn = unit_geom<kWalk, kPair>(a.units, has_next ? u + 1 : u, walk);
         const bool two = g.n_st == 2;
         // steady state: key tiles with a next key tile in this unit
         for (int j = g.lo; ok && j + 1 < g.hi; ++j) {
@@ -929,13 +1044,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (!ok) break;
               ++p_it[s][h];
               dev::tc_fence_after();
-              pv_half(s, vslot, h, acc0 || h == 1);
-              qk_half(s, qb + s, kslot, h);
+              pv_half(s, v_at(s), h, acc0 || h == 1);
+              qk_half(s, q_at[s], k_at(s), h);
             }
             if (!ok) break;
           }
-          vslot = vslot + 2 >= (uint32_t)kSlots ? vslot + 2 - kSlots : vslot + 2;
-          kslot = kslot + 2 >= (uint32_t)kSlots ? kslot + 2 - kSlots : kslot + 2;
+          advance();
         }
         if (!ok) break;
         // the last key tile: each PV is followed by "PV done" of its half (the
@@ -951,16 +1065,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (!ok) break;
               ++p_it[s][h];
               dev::tc_fence_after();
-              pv_half(s, vslot, h, acc0 || h == 1);
+              pv_half(s, v_at(s), h, acc0 || h == 1);
               commit_pair_elect(bars.pv_done(s, h));
             }
           }
           if (has_next) {
-            for (int h = 0; ok && h < 2; ++h)
-              for (int s = 0; ok && s < gn.n_st; ++s) first_qk(gn, qn, kslot, s, h);
+            if constexpr (kPair) {
+              // (query tile 1's Q slot is the one this unit's query tile 0 leaves in
+              // its epilogue, so query tile 0 goes first)
+              for (int s = 0; ok && s < 2; ++s)
+                for (int h = 0; ok && h < 2; ++h) first_qk(q_slot_of<kPair>(k + 1, s), k_at(s), s, h);
+            } else {
+              for (int h = 0; ok && h < 2; ++h)
+                for (int s = 0; ok && s < gn.n_st; ++s) first_qk(q_slot_of<kPair>(k + 1, s), kslot, s, h);
+            }
           }
-          vslot = vslot + 2 >= (uint32_t)kSlots ? vslot + 2 - kSlots : vslot + 2;
-          kslot = kslot + 2 >= (uint32_t)kSlots ? kslot + 2 - kSlots : kslot + 2;
+          advance();
         }
       }
       if (!ok && issued) {
@@ -982,10 +1102,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint64_t pol_q = dev::policy_evict_first();
     int k = 0;
     for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-      const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
+      UnitGeom g = unit_geom<kWalk, kPair>(a.units, u, walk);
 #pragma unroll 1
       for (int s = 0; s < 2 && s < g.n_st; ++s) {
-        const int i = 2 * (k & 1) + s;
+        const int i = q_slot_of<kPair>(k, s);
+        if (kPair && s == 1) g = unit_geom<kWalk, kPair>(a.units, u, walk, 1);
         bool good = true;
         if constexpr (!kFp8) {
           // bf16: this warp loads the tile once its slot is free (the
@@ -994,7 +1115,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             good = dev::mbar_wait(bars.q_empty(i), (q_use[i] & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
             if (good) {
               const uint32_t dst = sbase + C::SmemQ + i * C::QTileBytes;
-              const int32_t row = g.q0 + s * 2 * kTileRows + (int32_t)rank * kTileRows;
+              const int32_t row = tile_row<kPair>(g, s, rank);
               dev::mbar_arrive_expect_tx(bars.q_full(i), C::QTileBytes);
               dev::tma_load_2d(dst, &tm_q, bars.q_full(i), g.head * 128, row, pol_q);
               dev::tma_load_2d(dst + kQHalfBytes, &tm_q, bars.q_full(i), g.head * 128 + 64, row, pol_q);
@@ -1054,14 +1175,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // 32-byte output stores when every row start is 32-byte aligned
     const bool o_wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0 && (a.o_stride & 15) == 0;
     for (int u = u_begin; ok && u < u_end; ++u) {
-      const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
+      const UnitGeom g = unit_geom<kWalk, kPair>(a.units, u, walk, kPair ? st : 0);
       const uint32_t t_unit = t0;
       t0 += g.hi - g.lo;
       if (st >= g.n_st) continue;
-      const uint32_t q_slot = 2 * ((u - u_begin) & 1) + st;  // this unit's Q tile of this query tile
+      const uint32_t q_slot = q_slot_of<kPair>(u - u_begin, st);  // this unit's Q tile of this query tile
       // ring bookkeeping by one lane of one warp per CTA
-      const bool releases = lead_lane && st == g.n_st - 1;
-      const bool checks_kv = lead_lane && st == 0;
+      // (kPair: each query tile has groups of its own)
+      const bool releases = lead_lane && (kPair || st == g.n_st - 1);
+      const bool checks_kv = lead_lane && (kPair || st == 0);
       // (other walks: finite, so that the exponents of a row that sees no key are -inf, not NaN)
       float m_used = kWalk == kWalkDoc ? -INFINITY : -3.402823466e38f, l = 0.f;
       // fp8: this row's q scale (1 for rows past the tensor, never stored)
@@ -1176,7 +1298,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const float rsc = sl2;  // score scale in log2 units: softmax_scale log2(e)
           const int rem = key_tile<kWalk>(g, j, entry_next, walk).rem;
           if (kWalk == kWalkList && j + 1 < g.hi) entry_next = list_entry<kWalk>(g, j + 1);
-          const uint32_t kv_bar = bars.kv_full((t + 1) % kGroups), kv_par = ((t + 1) / kGroups) & 1;
+          // the group holding V(t) and K(t + 1), and the one holding K(t)
+          const uint32_t grp = kPair ? 2 * t + 1 + st : t + 1, grp_k = kPair ? grp - 2 : t;
+          const uint32_t kv_bar = bars.kv_full(grp % kGroups), kv_par = (grp / kGroups) & 1;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             // (no lane leaves here: a failed wait only clears ok, and the
@@ -1185,7 +1309,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ++s_it[h];
             // S half 1 of the last query tile is ready: every MMA before its QK is
             // done, so the group holding K(t) (and V(t-1)) is free in this CTA
-            if (releases && h == 1) dev::mbar_arrive(bars.kv_empty(t % kGroups));
+            // (kPair: group 0 holds both query tiles' first K; tile 1's QK comes last)
+            if (releases && h == 1 && !(kPair && t == 0 && st == 0)) dev::mbar_arrive(bars.kv_empty(grp_k % kGroups));
             __syncwarp();  // lanes leave the wait separately; the TMEM loads are warp-collective
             dev::tc_fence_after();
             const uint32_t t_sh = t_s + 64 * h;  // this half's S, then its P
@@ -1271,9 +1396,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               // The tile ends early: the rows of V behind its last valid key (this
               // CTA's 64 dims, 128 bytes a row) are zeroed before the PV reads
               // them, by the warp that reports the group landed.
-              if (h == 0 && warp == 0 && rem < kTileRows) {
+              if (h == 0 && (kPair ? (warp & 3) == 0 : warp == 0) && rem < kTileRows) {
                 ok = dev::mbar_wait(kv_bar, kv_par, abort_flag, a.err, kTimeoutNs) && ok;
-                const uint32_t v_slot = sbase + C::SmemKV + ((2 * t + 1) % kSlots) * C::SlotBytes;
+                const uint32_t v_slot = sbase + C::SmemKV + ((kPair ? 2 * grp : 2 * grp - 1) % kSlots) * C::SlotBytes;
                 if (ok)
                   for (uint32_t b = (uint32_t)max(rem, 0) * 128u + lane * 16u; b < C::SlotBytes; b += 512u)
                     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v_slot + b), "r"(0u) : "memory");
@@ -1305,7 +1430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       dev::tc_fence_after();
-      const int32_t local = st * 2 * kTileRows + (int32_t)rank * kTileRows + (int32_t)row_in_tile;
+      const int32_t local = (kPair ? 0 : st * 2 * kTileRows) + (int32_t)rank * kTileRows + (int32_t)row_in_tile;
       const int32_t row = g.q0 + local;
       const bool valid = row < g.q1;
       if (g.part >= 0) {
@@ -1629,13 +1754,13 @@ bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType type, uint32
   return true;
 }
 
-template <bool kFp8, int kWalk>
+template <bool kFp8, int kWalk, bool kPair = false>
 cudaError_t set_smem_attr() {
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(attn_fwd_tc_kernel<kFp8, kWalk>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)Cfg<kFp8>::SmemAlloc);
+    attr = cudaFuncSetAttribute(attn_fwd_tc_kernel<kFp8, kWalk, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)Cfg<kFp8, kPair>::SmemAlloc);
   });
   return attr;
 }
@@ -1670,7 +1795,7 @@ cudaError_t launch_pairs(const CUtensorMap& mq, const CUtensorMap& mk, const CUt
     if (why) *why = "the work list has no CTA pairs";
     return cudaErrorInvalidValue;
   }
-  attn_fwd_tc_kernel<kFp8, kWalkDoc>
+  attn_fwd_tc_kernel<kFp8, kWalkDoc, false>
       <<<2 * a.n_pairs, kThreads, Cfg<kFp8>::SmemAlloc, stream>>>(mq, mk, mv, mo, a, o_tma, Walk<kWalkDoc>{});
   e = cudaGetLastError();
   if (e != cudaSuccess || a.n_merges == 0) return e;
@@ -1699,7 +1824,7 @@ int forward_slots(int device, int num_sms) {
       cfg.gridDim = dim3(2 * (num_sms / 2 > 0 ? num_sms / 2 : 1));
       cfg.blockDim = dim3(kThreads);
       cfg.dynamicSmemBytes = Cfg<false>::SmemAlloc;
-      if (cudaOccupancyMaxActiveClusters(&n, attn_fwd_tc_kernel<false, kWalkDoc>, &cfg) != cudaSuccess) n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, attn_fwd_tc_kernel<false, kWalkDoc, false>, &cfg) != cudaSuccess) n = 0;
     }
     cudaGetLastError();
     if (prev != device && prev >= 0) cudaSetDevice(prev);
@@ -1731,16 +1856,16 @@ bool make_forward_maps(const ForwardArgs& a, ForwardMaps* m, std::string* why) {
 }
 
 // The forward over another walk, then the join of the rows it left in parts.
-template <int kWalk>
+template <int kWalk, bool kPair>
 cudaError_t launch_walk(const ForwardMaps& m, const ForwardArgs& a, const WalkArgs& w, const Walk<kWalk>& walk,
                         cudaStream_t stream, std::string* why) {
-  cudaError_t e = set_smem_attr<false, kWalk>();
+  cudaError_t e = set_smem_attr<false, kWalk, kPair>();
   if (e != cudaSuccess) {
     if (why) *why = "cudaFuncSetAttribute(max dynamic shared memory) failed";
     return e;
   }
-  attn_fwd_tc_kernel<false, kWalk>
-      <<<2 * a.n_pairs, kThreads, Cfg<false>::SmemAlloc, stream>>>(m.q, m.k, m.v, m.o, a, m.o_tma, walk);
+  attn_fwd_tc_kernel<false, kWalk, kPair>
+      <<<2 * a.n_pairs, kThreads, Cfg<false, kPair>::SmemAlloc, stream>>>(m.q, m.k, m.v, m.o, a, m.o_tma, walk);
   e = cudaGetLastError();
   if (e != cudaSuccess || w.n_joins == 0) return e;
   const JoinArgs j{w.joins,
@@ -1773,7 +1898,8 @@ cudaError_t launch_forward_list(const ForwardArgs& a, const WalkArgs& w, cudaStr
   ForwardMaps m;
   if (!make_forward_maps(a, &m, why)) return cudaErrorInvalidValue;
   const Walk<kWalkList> walk{w.block_idx, w.block_cnt, w.n_q_blocks, w.max_blocks};
-  return launch_walk<kWalkList>(m, a, w, walk, stream, why);
+  return w.pair ? launch_walk<kWalkList, true>(m, a, w, walk, stream, why)
+                : launch_walk<kWalkList, false>(m, a, w, walk, stream, why);
 }
 
 cudaError_t launch_forward_prefix(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why) {
@@ -1786,7 +1912,7 @@ cudaError_t launch_forward_prefix(const ForwardArgs& a, const WalkArgs& w, cudaS
   if (!make_map(&walk.tm_k, w.k_prefix, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, n, row, kTileRows / 2, why) ||
       !make_map(&walk.tm_v, w.v_prefix, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, n, row, kTileRows, why))
     return cudaErrorInvalidValue;
-  return launch_walk<kWalkPrefix>(m, a, w, walk, stream, why);
+  return launch_walk<kWalkPrefix, false>(m, a, w, walk, stream, why);
 }
 
 cudaError_t launch_forward_fp8(const ForwardArgs& a, int device, int num_sms, cudaStream_t stream,

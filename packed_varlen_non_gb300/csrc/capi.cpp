@@ -772,6 +772,7 @@ static WalkArgs walk_args(const WalkPlan& w) {
   WalkArgs x{};
   x.joins = w.d_joins;
   x.n_joins = (int32_t)w.joins.size();
+  x.pair = w.segs == 2;
   return x;
 }
 
@@ -891,7 +892,15 @@ h3attn_status h3attn_walk_list_host(int32_t kind, const int32_t* cu_seqlens, int
     const std::string why = kind == 0 ? build_list_walk(cu_seqlens, n_docs, num_heads, p0, p1, n_pairs, w)
                                       : build_prefix_walk(cu_seqlens, n_docs, num_heads, p0, n_pairs, w);
     if (!why.empty()) return fail(H3ATTN_EINVAL, "%s", why.c_str());
-    *n_units = (int64_t)w.units.size();
+    // segments, without the empty ones that fill up a unit
+    std::vector<WalkUnit> segs;
+    std::vector<int32_t> off(1, 0);
+    for (int32_t p = 0; p < w.n_pairs; ++p) {
+      for (int32_t i = w.unit_off[p] * w.segs; i < w.unit_off[p + 1] * w.segs; ++i)
+        if (w.units[i].q_row0 < w.units[i].q_end) segs.push_back(w.units[i]);
+      off.push_back((int32_t)segs.size());
+    }
+    *n_units = (int64_t)segs.size();
     *n_pairs_used = w.n_pairs;
     *n_joins = (int64_t)w.joins.size();
     *n_part_rows = w.part_rows;
@@ -899,8 +908,8 @@ h3attn_status h3attn_walk_list_host(int32_t kind, const int32_t* cu_seqlens, int
     if (units_cap < *n_units || (joins && joins_cap < *n_joins))
       return fail(H3ATTN_EINVAL, "capacities %lld, %lld < %lld segments, %lld joins", (long long)units_cap,
                   (long long)joins_cap, (long long)*n_units, (long long)*n_joins);
-    std::memcpy(units, w.units.data(), w.units.size() * sizeof(WalkUnit));
-    if (unit_off) std::memcpy(unit_off, w.unit_off.data(), w.unit_off.size() * sizeof(int32_t));
+    std::memcpy(units, segs.data(), segs.size() * sizeof(WalkUnit));
+    if (unit_off) std::memcpy(unit_off, off.data(), off.size() * sizeof(int32_t));
     if (joins && !w.joins.empty()) std::memcpy(joins, w.joins.data(), w.joins.size() * sizeof(JoinRec));
   } catch (const std::bad_alloc&) {
     return fail(H3ATTN_ENOMEM, "host allocation failed while building the work list");

@@ -122,8 +122,9 @@ constexpr int kJoinOwnKeys = 32;     // longest document the join attends to its
 
 struct WalkPlan {
   bool set = false;
-  std::vector<WalkUnit> units;         // grouped by CTA pair
-  std::vector<int32_t> unit_off;       // [n_pairs + 1]
+  int segs = 1;                        // segments of a unit: 2 run side by side on a CTA pair
+  std::vector<WalkUnit> units;         // segments, unit by unit, grouped by CTA pair (q_row0 = q_end: none)
+  std::vector<int32_t> unit_off;       // [n_pairs + 1], in units
   int32_t n_pairs = 0;
   std::vector<JoinRec> joins;
   int64_t part_rows = 0;               // partial rows of all segments
@@ -331,6 +332,7 @@ cudaError_t launch_forward_fp8(const ForwardArgs& a, int device, int num_sms, cu
 struct WalkArgs {
   const JoinRec* joins;
   int32_t n_joins;
+  bool pair;                   // units of two segments
   // list walk
   const int32_t* block_idx;    // [H, n_q_blocks, max_blocks]
   const int32_t* block_cnt;    // [H, n_q_blocks]

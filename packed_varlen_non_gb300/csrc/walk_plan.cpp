@@ -47,8 +47,17 @@ constexpr double kJoinStart = 2.0;
 
 int64_t piece_cost(int32_t tiles, bool partial) { return (int64_t)tiles + 1 + (partial ? 1 : 0); }
 
+// Costs of units of `segs` consecutive pieces that run in lockstep: the largest's.
+std::vector<int64_t> unit_costs(const std::vector<int64_t>& pieces, int segs) {
+  std::vector<int64_t> out;
+  out.reserve((pieces.size() + segs - 1) / segs);
+  for (size_t i = 0; i < pieces.size(); i += segs)
+    out.push_back(*std::max_element(pieces.begin() + i, pieces.begin() + std::min(pieces.size(), i + segs)));
+  return out;
+}
+
 // Splits a tail of the items (in list order) so that the pairs finish together.
-void balance(std::vector<Item>& items, int G) {
+void balance(std::vector<Item>& items, int G, int segs) {
   const size_t U = items.size();
   std::vector<int32_t> pair_of, heap(G);
   std::vector<int64_t> load(G), cost;
@@ -68,6 +77,7 @@ void balance(std::vector<Item>& items, int G) {
       }
       if (partial) rows += (int64_t)n * items[i].rows();
     }
+    if (segs > 1) cost = unit_costs(cost, segs);
     pair_of.resize(cost.size());
     assign_pairs(cost.size(), [&](size_t i) { return cost[i]; }, G, pair_of.data(), load.data(), heap.data());
     double score = (double)*std::max_element(load.begin(), load.end());
@@ -79,13 +89,13 @@ void balance(std::vector<Item>& items, int G) {
     }
   };
   consider(U, 1);
-  const int64_t full = (int64_t)(U / G * G);
-  for (int64_t back : {(int64_t)0, (int64_t)G / 4, (int64_t)G / 2, (int64_t)G, (int64_t)2 * G, full}) {
+  const int64_t round = (int64_t)G * segs, full = (int64_t)U / round * round;
+  for (int64_t back : {(int64_t)0, round / 4, round / 2, round, 2 * round, full}) {
     if (back > full) continue;
     const size_t whole = (size_t)(full - back);
     if (whole == U) continue;
     for (int r = 1; r <= 4; ++r) {
-      const int64_t m = (tail_tiles[whole] + (int64_t)G * r - 1) / ((int64_t)G * r);
+      const int64_t m = (tail_tiles[whole] + round * r - 1) / (round * r);
       consider(whole, (int32_t)std::max<int64_t>(1, m));
     }
   }
@@ -97,6 +107,7 @@ void balance(std::vector<Item>& items, int G) {
 template <class Make>
 std::string finish(std::vector<Item>& items, std::vector<Join>& joins, int G, Make make, WalkPlan& w) {
   int64_t rows = 0;
+  const int per = w.segs;
   std::vector<WalkUnit> segs;
   std::vector<int64_t> cost;
   for (Item& it : items) {
@@ -143,12 +154,23 @@ std::string finish(std::vector<Item>& items, std::vector<Join>& joins, int G, Ma
       w.joins.push_back(r);
     }
   }
+  // an odd last unit's second segment: no rows, no list
+  while (segs.size() % per != 0) segs.push_back(WalkUnit{0, 0, 0, 1, 0, -1, 1 << 16, -1});
+  if (per > 1) cost = unit_costs(cost, per);
+  struct Unit {
+    WalkUnit seg[2];
+  };
   w.units.resize(segs.size());
   w.unit_off.assign((size_t)G + 1, 0);
-  std::vector<int32_t> pair_of(segs.size()), heap(G);
+  std::vector<int32_t> pair_of(cost.size()), heap(G);
   std::vector<int64_t> load(G);
-  assign_pairs(segs.size(), [&](size_t i) { return cost[i]; }, G, pair_of.data(), load.data(), heap.data());
-  w.n_pairs = group_by_pair(segs.data(), segs.size(), G, w.units.data(), w.unit_off.data(), pair_of.data(), heap.data());
+  assign_pairs(cost.size(), [&](size_t i) { return cost[i]; }, G, pair_of.data(), load.data(), heap.data());
+  if (per == 1)
+    w.n_pairs =
+        group_by_pair(segs.data(), cost.size(), G, w.units.data(), w.unit_off.data(), pair_of.data(), heap.data());
+  else
+    w.n_pairs = group_by_pair(reinterpret_cast<const Unit*>(segs.data()), cost.size(), G,
+                              reinterpret_cast<Unit*>(w.units.data()), w.unit_off.data(), pair_of.data(), heap.data());
   w.unit_off.resize((size_t)w.n_pairs + 1);
   if (w.joins.size() >= (size_t(1) << 31)) return "the layout needs 2^31 or more join records";
   return "";
@@ -181,7 +203,8 @@ std::string build_list_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads
         r = end;
       }
   }
-  balance(items, G);
+  w.segs = q_block == kUnitRows ? 1 : 2;
+  balance(items, G, w.segs);
   for (Item& it : items) it.pieces = std::min(it.pieces, 65535);  // the field's width
   std::vector<Join> joins;
   return finish(items, joins, G, [](const Item& it, int32_t c) {
@@ -260,7 +283,7 @@ std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_hea
       }
     }
   }
-  balance(items, G);
+  balance(items, G, w.segs);
   return finish(items, joins, G, [](const Item& it, int32_t c) {
     WalkUnit s = it.u;
     s.a = it.u.a + (int32_t)((int64_t)it.tiles * c / it.pieces);
