@@ -300,7 +300,7 @@ h3attn_status h3attn_forward_fp8(h3attn_plan_t plan, const void* q8, const void*
  *
  * h3attn_plan_set_sparse adds the work list to a plan: q_block is 512 (the
  * forward's unit of work: the rate of the dense forward on the listed tiles)
- * or 256 (a finer selection, at about half that rate); max_blocks >= 1 is the
+ * or 256 (a finer selection, at about 85 % of that rate); max_blocks >= 1 is the
  * width of the lists and what the work is balanced for.  It allocates and
  * synchronises cuda_stream, must not be called while a stream is captured, and
  * may be called once per plan, so that no later call invalidates a captured
@@ -389,25 +389,30 @@ h3attn_status h3attn_forward_prefix(h3attn_plan_t plan, const void* q, const voi
  *            the query rows, document begin, document end, head, then for kind 0
  *            the query block and piece | pieces << 16 (the piece's share of the
  *            block's list), for kind 1 key tiles [lo, hi) of "the prefix's
- *            tiles, then the document's"; last the first partial row (-1: the
+ *            tiles, then the document's" -- with document end = -n for a segment
+ *            over several documents, whose n own tiles are entries [document
+ *            begin, document begin + n) of own; last the first partial row (-1: the
  *            segment writes the output itself);
  *            With q_block 256, a pair runs its segments two at a time, side by
  *            side;
  *   unit_off [*n_pairs_used + 1] int32: pair p runs units [unit_off[p], unit_off[p + 1]);
- *   joins    [*n_joins][16] int32, the rows combined from partial rows: rows
- *            [r0, r1) (at most 8), head, key_lo; then of segment a its first partial row,
- *            rows, pieces and first query row; the same of segment b (pieces may
- *            be 0); key_hi (keys [key_lo, key_hi) are attended to by the join
- *            itself), three zeros.  Row r of piece c is partial row first + c *
- *            rows + (r - first query row).
+ *   joins    [*n_joins][12] int32, the rows combined from partial rows: rows
+ *            [r0, r1) (at most 8), head, and of their segment the first query
+ *            row, the first partial row, its rows and its pieces (row r of piece
+ *            c is partial row first + c * rows + (r - first query row)); keys
+ *            [key_lo, key_hi) that the join itself attends to; three zeros;
+ *   own      [*n_own][20] int32: a key tile's first row, its valid keys, the
+ *            segment's rows [lo, hi) that see it, counted from its first, and
+ *            two times 8 words of the lanes of O that it leaves alone;
  *   *n_part_rows  partial rows in all.
  * Errors: EINVAL for NULL cu_seqlens or output counts, the layout errors of
  * h3attn_work_list_host, parameters that the plan calls refuse, or capacities
- * (units_cap, joins_cap, in records) too small. */
+ * (units_cap, joins_cap, own_cap, in records) too small. */
 h3attn_status h3attn_walk_list_host(int32_t kind, const int32_t* cu_seqlens, int32_t n_docs, int32_t num_heads,
                                     int32_t p0, int32_t p1, int32_t n_pairs, int32_t* units, int64_t units_cap,
-                                    int32_t* unit_off, int32_t* joins, int64_t joins_cap, int64_t* n_units,
-                                    int32_t* n_pairs_used, int64_t* n_joins, int64_t* n_part_rows);
+                                    int32_t* unit_off, int32_t* joins, int64_t joins_cap, int32_t* own,
+                                    int64_t own_cap, int64_t* n_units, int32_t* n_pairs_used, int64_t* n_joins,
+                                    int64_t* n_own, int64_t* n_part_rows);
 
 /* Allocation-free forward.  The pages have no counterpart: this entry point
  * exists for callers that may not allocate device memory -- code whose device

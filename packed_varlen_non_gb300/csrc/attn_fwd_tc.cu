@@ -232,6 +232,7 @@ struct Walk<kWalkList> {
 template <>
 struct Walk<kWalkPrefix> {
   CUtensorMap tm_k, tm_v;   // the prefix's rows
+  const OwnTile* own;       // own tiles of segments over several documents
   int32_t len, tiles;
 };
 
@@ -241,6 +242,7 @@ struct UnitGeom {
   int32_t q1;                                      // end of the unit's query rows
   const int32_t* list;                             // list walk: the segment's tiles, step j's at list[j] (null: none)
   int32_t n;                                       // list walk: entries of the list; the steps after them are masked
+                                                   // prefix walk: own tiles of a segment over several documents
 };
 
 // First row of this CTA's query tile s of a unit.
@@ -294,6 +296,7 @@ __device__ __forceinline__ UnitGeom unit_geom(const WorkUnit* units, int u, cons
     if constexpr (kWalk == kWalkPrefix) {
       g.lo = x.y;
       g.hi = x.z;
+      g.n = max(-w.w, 0);  // kv0: the first of them in the table
     } else {
       int32_t lo, hi;
       const int64_t at = list_range(x, walk, &lo, &hi);
@@ -312,22 +315,29 @@ __device__ __forceinline__ UnitGeom unit_geom(const WorkUnit* units, int u, cons
   return g;
 }
 
+// What a walk looks up for its step j, a tile ahead of its use: the list's entry
+// (x), or an own tile's key row, valid keys and query rows.
+template <int kWalk>
+__device__ __forceinline__ int4 walk_entry(const UnitGeom& g, int j, const Walk<kWalk>& walk) {
+  int4 e = make_int4(-1, 0, 0, 0);
+  if constexpr (kWalk == kWalkList) {
+    if (j < g.n) e.x = __ldg(g.list + j);
+  } else if constexpr (kWalk == kWalkPrefix) {
+    if (g.n > 0 && j >= walk.tiles) e = __ldg(reinterpret_cast<const int4*>(walk.own + g.kv0 + (j - walk.tiles)));
+  }
+  return e;
+}
+
 // Step j of a unit's walk: the tile's first key row, its valid keys (0 or less:
-// none, 128 or more: all), and whether it lies in the prefix.
+// none, 128 or more: all), the unit's rows [lo, hi) that see it, and whether it
+// lies in the prefix.
 struct KeyTile {
-  int32_t row, rem;
+  int32_t row, rem, lo, hi;
   bool prefix, bad;
 };
-// entry: list walk: the list's entry j (list_entry), so that it can be loaded
-// well before its use.
 template <int kWalk>
-__device__ __forceinline__ int32_t list_entry(const UnitGeom& g, int j) {
-  if constexpr (kWalk == kWalkList) return j < g.n ? __ldg(g.list + j) : -1;
-  return 0;
-}
-template <int kWalk>
-__device__ __forceinline__ KeyTile key_tile(const UnitGeom& g, int j, int32_t entry, const Walk<kWalk>& walk) {
-  KeyTile t{g.kv0, 0, false, false};
+__device__ __forceinline__ KeyTile key_tile(const UnitGeom& g, int j, const int4& entry, const Walk<kWalk>& walk) {
+  KeyTile t{g.kv0, 0, 0, kUnitRows, false, false};
   if constexpr (kWalk == kWalkDoc) {
     t.row = g.kv0 + j * kTileRows;
     t.rem = g.kv1 - t.row;
@@ -335,11 +345,17 @@ __device__ __forceinline__ KeyTile key_tile(const UnitGeom& g, int j, int32_t en
     t.prefix = j < walk.tiles;
     t.row = (t.prefix ? j : j - walk.tiles) * kTileRows + (t.prefix ? 0 : g.kv0);
     t.rem = (t.prefix ? walk.len : g.kv1) - t.row;
+    if (g.n > 0 && !t.prefix) {
+      t.row = entry.x;
+      t.rem = entry.y;
+      t.lo = entry.z;
+      t.hi = entry.w;
+    }
   } else {
     // a tile outside the document is skipped (and reported by the producer)
-    const bool in = (uint32_t)entry <= (uint32_t)(g.kv1 - g.kv0 - 1) / kTileRows;
+    const bool in = (uint32_t)entry.x <= (uint32_t)(g.kv1 - g.kv0 - 1) / kTileRows;
     if (in) {
-      t.row = g.kv0 + entry * kTileRows;
+      t.row = g.kv0 + entry.x * kTileRows;
       t.rem = g.kv1 - t.row;
     }
     t.bad = !in && j < g.n;
@@ -441,6 +457,29 @@ __device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint3
       "add.u32 t, %1, 24;\n\tadd.u32 y, %2, 640;\n\tmov.b64 b, {y, %3};\n\t"
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [t], b, %5, p1;\n\t}" ::"r"(d_tmem),
       "r"(p_tmem), "r"(vb), "r"(kDescHi), "r"(acc ? 1u : 0u), "r"(kIdescPV)
+      : "memory");
+}
+
+// The same, leaving the lanes of O whose bits are set in skip (a, b: 8 words, the
+// even CTA's 128 lanes first) as they are: rows of other documents than the
+// tile's, whose P is 0 but whose O a NaN in V would reach.
+__device__ __forceinline__ void issue_pv_skip(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_smem, bool acc, const uint4& a,
+                                              const uint4& b) {
+  const uint32_t vb = desc_lo(v_smem, Cfg<false>::SlotBytes);
+  asm volatile(
+      "{\n\t.reg .pred p0, p1, e;\n\telect.sync _|e, 0xffffffff;\n\t.reg .b64 b;\n\t.reg .b32 t, y;\n\t"
+      "setp.ne.u32 p0, %4, 0;\n\t"
+      "setp.eq.u32 p1, %4, %4;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %5, {%6, %7, %8, %9, %10, %11, %12, %13}, p0;\n\t"
+      "add.u32 t, %1, 8;\n\tadd.u32 y, %2, 128;\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [t], b, %5, {%6, %7, %8, %9, %10, %11, %12, %13}, p1;\n\t"
+      "add.u32 t, %1, 16;\n\tadd.u32 y, %2, 512;\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [t], b, %5, {%6, %7, %8, %9, %10, %11, %12, %13}, p1;\n\t"
+      "add.u32 t, %1, 24;\n\tadd.u32 y, %2, 640;\n\tmov.b64 b, {y, %3};\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [t], b, %5, {%6, %7, %8, %9, %10, %11, %12, %13}, p1;\n\t}" ::"r"(d_tmem),
+      "r"(p_tmem), "r"(vb), "r"(kDescHi), "r"(acc ? 1u : 0u), "r"(kIdescPV), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+      "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
       : "memory");
 }
 
@@ -759,7 +798,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // group 0: both query tiles' first K tiles; then, per step and query tile,
         // a group of its V tile and its next K tile (see kPair)
         int k = 0;
-        int32_t next[2] = {-1, -1};  // entries of the tiles whose K was sent last
+        int4 next[2] = {};  // entries of the tiles whose K was sent last
         for (int u = u_begin; ok && u < u_end; ++u, ++k) {
           const UnitGeom g[2] = {unit_geom<kWalk, kPair>(a.units, u, walk, 0), unit_geom<kWalk, kPair>(a.units, u, walk, 1)};
           const bool has_next = u + 1 < u_end;
@@ -769,7 +808,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             dev::mbar_arrive_expect_tx(bars.kv_full(0), 2 * C::SlotBytes);
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-              next[s] = list_entry<kWalk>(g[s], 0);
+              next[s] = walk_entry<kWalk>(g[s], 0, walk);
               const KeyTile t = key_tile<kWalk>(g[s], 0, next[s], walk);
               load_k_half<kFp8>(sbase + C::SmemKV + s * C::SlotBytes, &tm_k, bars.kv_full(0), g[s].head, t.row, rank, pol_kv);
             }
@@ -783,11 +822,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               int k_head = g[s].head;
               const bool has_k = j + 1 < g[s].hi || has_next;
               if (j + 1 < g[s].hi) {
-                next[s] = list_entry<kWalk>(g[s], j + 1);
+                next[s] = walk_entry<kWalk>(g[s], j + 1, walk);
                 kt = key_tile<kWalk>(g[s], j + 1, next[s], walk);
               } else if (has_next) {
                 const UnitGeom n = unit_geom<kWalk, kPair>(a.units, u + 1, walk, s);
-                next[s] = list_entry<kWalk>(n, 0);
+                next[s] = walk_entry<kWalk>(n, 0, walk);
                 kt = key_tile<kWalk>(n, 0, next[s], walk);
                 k_head = n.head;
               }
@@ -823,7 +862,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             load_k_half<kFp8>(sbase + C::SmemKV, &tm_k, bars.kv_full(0), g.head, g.kv0 + g.lo * kTileRows, rank,
                               pol_kv);
           } else {
-            kt = key_tile<kWalk>(g, g.lo, list_entry<kWalk>(g, g.lo), walk);
+            kt = key_tile<kWalk>(g, g.lo, walk_entry<kWalk>(g, g.lo, walk), walk);
             load_k_half<kFp8>(sbase + C::SmemKV, k_map(kt), bars.kv_full(0), g.head, kt.row, rank, pol_kv);
           }
           grp = 1;
@@ -835,7 +874,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if constexpr (kWalk == kWalkDoc) {
             kt.row = g.kv0 + (j + 1) * kTileRows;
           } else {
-            if (has_k) kt = key_tile<kWalk>(g, j + 1, list_entry<kWalk>(g, j + 1), walk);
+            if (has_k) kt = key_tile<kWalk>(g, j + 1, walk_entry<kWalk>(g, j + 1, walk), walk);
             if (vt.bad && rank == 0) atomicExch(a.err, kErrBlockIndex);
           }
           if (!has_k && has_next) {
@@ -845,7 +884,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if constexpr (kWalk == kWalkDoc)
               kt.row = n.kv0 + n.lo * kTileRows;
             else
-              kt = key_tile<kWalk>(n, n.lo, list_entry<kWalk>(n, n.lo), walk);
+              kt = key_tile<kWalk>(n, n.lo, walk_entry<kWalk>(n, n.lo, walk), walk);
           }
           const uint32_t b = grp % kGroups;
           ok = dev::mbar_wait(bars.kv_empty(b), ((grp / kGroups) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
@@ -975,6 +1014,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t vb = sbase + C::SmemKV + vs * C::SlotBytes;
         issue_pv(d, pt, vb + 4096 * h, acc);
       };
+      // Prefix walk: the same for an own tile of a segment over several documents,
+      // which leaves the other documents' rows alone: their lanes, for query tile
+      // s in skip[2 s] and skip[2 s + 1], loaded a tile ahead.
+      uint4 skip[4];
+      auto load_skip = [&](const UnitGeom& g, int j) {
+        if constexpr (kWalk == kWalkPrefix) {
+          const uint4* p = reinterpret_cast<const uint4*>(walk.own[g.kv0 + (j - walk.tiles)].skip);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) skip[x] = __ldg(p + x);
+        }
+      };
+      auto pv_half_skip = [&](int s, uint32_t vs, int h) {
+        const uint32_t d = tmem + 256 + s * 128, pt = tmem + s * 128 + h * 64;
+        const uint32_t vb = sbase + C::SmemKV + vs * C::SlotBytes;
+        issue_pv_skip(d, pt, vb + 4096 * h, true, s == 0 ? skip[0] : skip[2], s == 0 ? skip[1] : skip[3]);
+      };
       // The first QK (half h) of query tile s of a unit: Q slot qs (its readiness
       // in both CTAs is awaited before half 0), K in ring slot ks.
       auto first_qk = [&](uint32_t qs, uint32_t ks, int s, int h) {
@@ -1030,7 +1085,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const UnitGeom gn = unit_geom<kWalk, kPair>(a.units, has_next ? u + 1 : u, walk);
         const bool two = g.n_st == 2;
         // steady state: key tiles with a next key tile in this unit
-        for (int j = g.lo; ok && j + 1 < g.hi; ++j) {
+        // (prefix walk: those before the own tiles of a segment over several
+        // documents, which a loop of their own takes: selecting between the two
+        // PVs here cost the steady state 10 %)
+        int j_own = g.hi;
+        if constexpr (kWalk == kWalkPrefix)
+          if (g.n > 0) j_own = walk.tiles;
+        const int j_end = min(g.hi - 1, j_own);
+        for (int j = g.lo; ok && j < j_end; ++j) {
           const bool acc0 = j > g.lo;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -1051,6 +1113,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           advance();
         }
+        if constexpr (kWalk == kWalkPrefix) {
+          if (g.hi > j_own) load_skip(g, j_own);
+#pragma unroll 1
+          for (int j = j_own; ok && j + 1 < g.hi; ++j) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+              for (int s = 0; s < 2; ++s) {
+                if (s == 1 && !two) break;
+                ok = __all_sync(0xffffffffu,
+                                dev::mbar_wait(bars.p_ready(s, h), p_it[s][h] & 1, abort_flag, a.err, kTimeoutNs));
+                if (!ok) break;
+                ++p_it[s][h];
+                dev::tc_fence_after();
+                pv_half_skip(s, v_at(s), h);
+                qk_half(s, q_at[s], k_at(s), h);
+              }
+              if (!ok) break;
+            }
+            load_skip(g, j + 1);
+            advance();
+          }
+        }
         if (!ok) break;
         // the last key tile: each PV is followed by "PV done" of its half (the
         // epilogue waits for both halves); the next unit's first QKs follow
@@ -1065,7 +1150,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (!ok) break;
               ++p_it[s][h];
               dev::tc_fence_after();
-              pv_half(s, v_at(s), h, acc0 || h == 1);
+              if (kWalk == kWalkPrefix && g.hi > j_own)
+                pv_half_skip(s, v_at(s), h);
+              else
+                pv_half(s, v_at(s), h, acc0 || h == 1);
               commit_pair_elect(bars.pv_done(s, h));
             }
           }
@@ -1160,6 +1248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------- softmax ----
     const int st = warp >> 2;            // query tile of this warpgroup
     const uint32_t row_in_tile = threadIdx.x & 127;
+    const uint32_t row_in_unit = st * 2 * kTileRows + rank * kTileRows + row_in_tile;  // (not kPair)
     const uint32_t lane_base = (warp & 3) * 32;
     const uint32_t t_s = tmem + (lane_base << 16) + st * 128;        // S_s / P_s
     const uint32_t t_o = tmem + (lane_base << 16) + 256 + st * 128;  // O_s
@@ -1292,12 +1381,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       } else {
         // bf16: 64-key halves (see the kernel header).
-        int32_t entry_next = list_entry<kWalk>(g, g.lo);  // a list entry is loaded a tile ahead of its use
+        int4 entry_next = walk_entry<kWalk>(g, g.lo, walk);  // an entry is loaded a tile ahead of its use
         for (int j = g.lo; ok && j < g.hi; ++j) {
           const uint32_t t = t_unit + (j - g.lo);  // the pair's running key-tile count
           const float rsc = sl2;  // score scale in log2 units: softmax_scale log2(e)
-          const int rem = key_tile<kWalk>(g, j, entry_next, walk).rem;
-          if (kWalk == kWalkList && j + 1 < g.hi) entry_next = list_entry<kWalk>(g, j + 1);
+          const KeyTile tile = key_tile<kWalk>(g, j, entry_next, walk);
+          if (kWalk != kWalkDoc && j + 1 < g.hi && (kWalk == kWalkList || g.n > 0))
+            entry_next = walk_entry<kWalk>(g, j + 1, walk);
+          const int rem_tile = tile.rem;
+          // this row's valid keys: none of another document's tile
+          int rem = tile.rem;
+          if (kWalk == kWalkPrefix && g.n > 0 && ((int32_t)row_in_unit < tile.lo || (int32_t)row_in_unit >= tile.hi)) rem = 0;
           // the group holding V(t) and K(t + 1), and the one holding K(t)
           const uint32_t grp = kPair ? 2 * t + 1 + st : t + 1, grp_k = kPair ? grp - 2 : t;
           const uint32_t kv_bar = bars.kv_full(grp % kGroups), kv_par = (grp / kGroups) & 1;
@@ -1396,11 +1490,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               // The tile ends early: the rows of V behind its last valid key (this
               // CTA's 64 dims, 128 bytes a row) are zeroed before the PV reads
               // them, by the warp that reports the group landed.
-              if (h == 0 && (kPair ? (warp & 3) == 0 : warp == 0) && rem < kTileRows) {
+              if (h == 0 && (kPair ? (warp & 3) == 0 : warp == 0) && rem_tile < kTileRows) {
                 ok = dev::mbar_wait(kv_bar, kv_par, abort_flag, a.err, kTimeoutNs) && ok;
                 const uint32_t v_slot = sbase + C::SmemKV + ((kPair ? 2 * grp : 2 * grp - 1) % kSlots) * C::SlotBytes;
                 if (ok)
-                  for (uint32_t b = (uint32_t)max(rem, 0) * 128u + lane * 16u; b < C::SlotBytes; b += 512u)
+                  for (uint32_t b = (uint32_t)max(rem_tile, 0) * 128u + lane * 16u; b < C::SlotBytes; b += 512u)
                     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v_slot + b), "r"(0u) : "memory");
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the tensor cores
                 __syncwarp();
@@ -1613,12 +1707,11 @@ __global__ void __launch_bounds__(256, 8) attn_merge_kernel(ForwardArgs a) {
 }
 
 // Output rows of the list and prefix walks that no segment finishes alone: one
-// warp per query row, four dims per lane.  A row's parts are the partial rows
-// of up to two segments' pieces (a split list; the prefix part of rows shared by
-// several documents, and their own document's part) and, for documents of at
-// most kJoinOwnKeys tokens, the softmax over the document's own keys, computed
-// here in fp32 from q, k and v: a segment per such document and head would cost
-// two key-tile periods of a CTA pair for a few keys.  With M the largest part
+// warp per query row, four dims per lane.  A row's parts are the partial rows of
+// its segment's pieces and, for small documents that share a segment with many
+// others, the softmax over the document's own keys (at most kJoinOwnKeys),
+// computed here in fp32 from q, k and v: a tile of the segment's walk each would
+// cost a key-tile period of a CTA pair for a few keys.  With M the largest part
 // maximum (log2 units): o = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c.
 struct JoinArgs {
   const JoinRec* recs;
@@ -1683,20 +1776,19 @@ __global__ void __launch_bounds__(32 * kJoinRows, 6) attn_join_kernel(JoinArgs a
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the forward is complete and its writes visible
-  const int64_t ra = (int64_t)j.a_part + (row - j.a_row0), rb = (int64_t)j.b_part + (row - j.b_row0);
+  const int64_t r0 = (int64_t)j.part + (row - j.q_row0);
   float M = m_own, l = l_own;
   float4 acc = o_own;
-  const int n = j.n_a + j.n_b;
 #pragma unroll 1
-  for (int c = 0; c < n; c += 2) {
+  for (int c = 0; c < j.n; c += 2) {
     float2 ml[2];
     float4 o[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       ml[x] = make_float2(-INFINITY, 0.f);
       o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c + x < n) {
-        const int64_t r = c + x < j.n_a ? ra + (int64_t)(c + x) * j.a_rows : rb + (int64_t)(c + x - j.n_a) * j.b_rows;
+      if (c + x < j.n) {
+        const int64_t r = r0 + (int64_t)(c + x) * j.rows;
         ml[x] = a.part_ml[r];
         o[x] = reinterpret_cast<const float4*>(a.part_o + r * kHeadDim)[lane];
       }
@@ -1906,6 +1998,7 @@ cudaError_t launch_forward_prefix(const ForwardArgs& a, const WalkArgs& w, cudaS
   ForwardMaps m;
   if (!make_forward_maps(a, &m, why)) return cudaErrorInvalidValue;
   Walk<kWalkPrefix> walk;
+  walk.own = w.own;
   walk.len = w.prefix_len;
   walk.tiles = (int32_t)(((int64_t)w.prefix_len + kTileRows - 1) / kTileRows);
   const uint64_t inner = (uint64_t)a.H * kHeadDim, row = (uint64_t)w.prefix_stride * 2, n = (uint64_t)w.prefix_len;

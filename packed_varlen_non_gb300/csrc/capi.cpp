@@ -80,10 +80,12 @@ h3attn_status cuda_fail(cudaError_t e, const char* what) {
 
 void free_walk(WalkPlan* w) {
   if (w->d_units) cudaFree(w->d_units);
+  if (w->d_own) cudaFree(w->d_own);
   if (w->d_joins) cudaFree(w->d_joins);
   if (w->d_part_o) cudaFree(w->d_part_o);
   if (w->d_part_ml) cudaFree(w->d_part_ml);
   w->d_units = nullptr;
+  w->d_own = nullptr;
   w->d_joins = nullptr;
   w->d_part_o = nullptr;
   w->d_part_ml = nullptr;
@@ -93,9 +95,10 @@ void free_walk(WalkPlan* w) {
 // synchronises the stream before the host lists change).
 cudaError_t upload_walk(WalkPlan* w, cudaStream_t st) {
   const size_t units = w->units.size() * sizeof(WalkUnit), off = w->unit_off.size() * sizeof(int32_t);
-  const size_t joins = w->joins.size() * sizeof(JoinRec);
+  const size_t joins = w->joins.size() * sizeof(JoinRec), own = w->own.size() * sizeof(OwnTile);
   cudaError_t e = cudaMalloc(&w->d_units, units + off);
   if (e == cudaSuccess && joins > 0) e = cudaMalloc(&w->d_joins, joins);
+  if (e == cudaSuccess && own > 0) e = cudaMalloc(&w->d_own, own);
   if (e == cudaSuccess && w->part_rows > 0) {
     e = cudaMalloc(&w->d_part_o, (size_t)w->part_rows * kHeadDim * sizeof(float));
     if (e == cudaSuccess) e = cudaMalloc(&w->d_part_ml, (size_t)w->part_rows * sizeof(float2));
@@ -103,6 +106,7 @@ cudaError_t upload_walk(WalkPlan* w, cudaStream_t st) {
   if (e == cudaSuccess) e = cudaMemcpyAsync(w->d_units, w->units.data(), units, cudaMemcpyHostToDevice, st);
   if (e == cudaSuccess)
     e = cudaMemcpyAsync(w->d_units + w->units.size(), w->unit_off.data(), off, cudaMemcpyHostToDevice, st);
+  if (e == cudaSuccess && own > 0) e = cudaMemcpyAsync(w->d_own, w->own.data(), own, cudaMemcpyHostToDevice, st);
   if (e == cudaSuccess && joins > 0)
     e = cudaMemcpyAsync(w->d_joins, w->joins.data(), joins, cudaMemcpyHostToDevice, st);
   return e;
@@ -868,6 +872,7 @@ h3attn_status h3attn_forward_prefix(h3attn_plan_t plan, const void* q, const voi
   w.v_prefix = v_prefix;
   w.prefix_stride = prefix_row_stride;
   w.prefix_len = pp.len;
+  w.own = pp.walk.d_own;
   std::string why;
   e = launch_forward_prefix(a, w, static_cast<cudaStream_t>(cuda_stream), &why);
   if (e != cudaSuccess) {
@@ -879,10 +884,11 @@ h3attn_status h3attn_forward_prefix(h3attn_plan_t plan, const void* q, const voi
 
 h3attn_status h3attn_walk_list_host(int32_t kind, const int32_t* cu_seqlens, int32_t n_docs, int32_t num_heads,
                                     int32_t p0, int32_t p1, int32_t n_pairs, int32_t* units, int64_t units_cap,
-                                    int32_t* unit_off, int32_t* joins, int64_t joins_cap, int64_t* n_units,
-                                    int32_t* n_pairs_used, int64_t* n_joins, int64_t* n_part_rows) {
+                                    int32_t* unit_off, int32_t* joins, int64_t joins_cap, int32_t* own,
+                                    int64_t own_cap, int64_t* n_units, int32_t* n_pairs_used, int64_t* n_joins,
+                                    int64_t* n_own, int64_t* n_part_rows) {
   clear_error();
-  if (!cu_seqlens || !n_units || !n_pairs_used || !n_joins || !n_part_rows)
+  if (!cu_seqlens || !n_units || !n_pairs_used || !n_joins || !n_own || !n_part_rows)
     return fail(H3ATTN_EINVAL, "NULL cu_seqlens or output count");
   if (h3attn_status s = check_layout(cu_seqlens, n_docs, num_heads, n_pairs)) return s;
   if (kind != 0 && kind != 1) return fail(H3ATTN_EINVAL, "kind must be 0 or 1 (got %d)", kind);
@@ -903,14 +909,17 @@ h3attn_status h3attn_walk_list_host(int32_t kind, const int32_t* cu_seqlens, int
     *n_units = (int64_t)segs.size();
     *n_pairs_used = w.n_pairs;
     *n_joins = (int64_t)w.joins.size();
+    *n_own = (int64_t)w.own.size();
     *n_part_rows = w.part_rows;
     if (units == nullptr) return H3ATTN_OK;
-    if (units_cap < *n_units || (joins && joins_cap < *n_joins))
-      return fail(H3ATTN_EINVAL, "capacities %lld, %lld < %lld segments, %lld joins", (long long)units_cap,
-                  (long long)joins_cap, (long long)*n_units, (long long)*n_joins);
+    if (units_cap < *n_units || (joins && joins_cap < *n_joins) || (own && own_cap < *n_own))
+      return fail(H3ATTN_EINVAL, "capacities %lld, %lld, %lld < %lld segments, %lld joins, %lld own tiles",
+                  (long long)units_cap, (long long)joins_cap, (long long)own_cap, (long long)*n_units,
+                  (long long)*n_joins, (long long)*n_own);
     std::memcpy(units, segs.data(), segs.size() * sizeof(WalkUnit));
     if (unit_off) std::memcpy(unit_off, off.data(), off.size() * sizeof(int32_t));
     if (joins && !w.joins.empty()) std::memcpy(joins, w.joins.data(), w.joins.size() * sizeof(JoinRec));
+    if (own && !w.own.empty()) std::memcpy(own, w.own.data(), w.own.size() * sizeof(OwnTile));
   } catch (const std::bad_alloc&) {
     return fail(H3ATTN_ENOMEM, "host allocation failed while building the work list");
   }

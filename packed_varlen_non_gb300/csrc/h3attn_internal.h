@@ -89,8 +89,10 @@ void build_segments(const std::vector<WorkUnit>& units, int grid, std::vector<Wo
 //                takes entries [n i / m, n (i + 1) / m) of the block's n
 //                listed tiles (n is read on the device), i = piece, m = pieces
 //   prefix walk: key tiles [a, b) of the walk "the prefix's tiles, then the
-//                document's"; rows of several documents share a segment only
-//                when b is at most the prefix's tile count
+//                document's".  A segment whose rows belong to several documents
+//                has kv_end = -n < 0: n own tiles, entries [kv_begin, kv_begin +
+//                n) of the walk's table, follow the prefix; its a lies in the
+//                prefix.
 // part < 0: the segment writes the output; part >= 0: it writes unnormalised
 // rows from row `part` of the partial buffers on, for the join pass.
 struct WalkUnit {
@@ -105,20 +107,29 @@ struct WalkUnit {
 };
 static_assert(sizeof(WalkUnit) == sizeof(WorkUnit), "read as two 16-byte vectors");
 
+// A key tile of one document in a segment over several: its first key row and
+// valid keys, the segment's rows [lo, hi) (counted from q_row0) that belong to
+// the document, and for each query tile s of the pair the lanes of O that the
+// tile's PV must leave alone (bit i of word w: row 256 s + 32 w + i).
+struct OwnTile {
+  int32_t row, rem, lo, hi;
+  uint32_t skip[2][8];
+};
+static_assert(sizeof(OwnTile) == 80, "OwnTile is read as five 16-byte vectors");
+
 // Rows [row0, row1) of one head (at most kJoinRows: a block of the join, one warp
-// each) whose output the join pass combines from partial rows: n_a pieces of the segment whose first row is a_row0, piece c of
-// row r at partial row a_part + c * a_rows + (r - a_row0); likewise n_b pieces
-// of another one (n_b may be 0); and the keys [key_lo, key_hi) of the rows'
-// document, which the join itself attends to (empty when key_lo == key_hi).
+// each) whose output the join pass combines from n partial rows each, piece c of
+// row r at partial row part + c * rows + (r - q_row0), and from the keys [key_lo,
+// key_hi) of the rows' document, which the join itself attends to (none when
+// key_lo == key_hi).
 struct JoinRec {
-  int32_t row0, row1, head, key_lo;
-  int32_t a_part, a_rows, n_a, a_row0;
-  int32_t b_part, b_rows, n_b, b_row0;
+  int32_t row0, row1, head, q_row0;
+  int32_t part, rows, n, key_lo;
   int32_t key_hi, pad[3];
 };
-static_assert(sizeof(JoinRec) == 64, "JoinRec is read as four 16-byte vectors");
+static_assert(sizeof(JoinRec) == 48, "JoinRec is read as three 16-byte vectors");
 constexpr int kJoinRows = 8;         // rows per join block (one warp each)
-constexpr int kJoinOwnKeys = 32;     // longest document the join attends to itself
+constexpr int kJoinOwnKeys = 32;     // longest document the join may attend to itself
 
 struct WalkPlan {
   bool set = false;
@@ -126,10 +137,12 @@ struct WalkPlan {
   std::vector<WalkUnit> units;         // segments, unit by unit, grouped by CTA pair (q_row0 = q_end: none)
   std::vector<int32_t> unit_off;       // [n_pairs + 1], in units
   int32_t n_pairs = 0;
+  std::vector<OwnTile> own;            // prefix walk
   std::vector<JoinRec> joins;
   int64_t part_rows = 0;               // partial rows of all segments
 
   WalkUnit* d_units = nullptr;         // units, then unit_off
+  OwnTile* d_own = nullptr;
   JoinRec* d_joins = nullptr;
   float* d_part_o = nullptr;           // [part_rows, 128] unnormalised O
   float2* d_part_ml = nullptr;         // [part_rows] (reference max in log2 units, sum)
@@ -343,6 +356,7 @@ struct WalkArgs {
   const void* v_prefix;
   int64_t prefix_stride;
   int32_t prefix_len;
+  const OwnTile* own;
 };
 cudaError_t launch_forward_list(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why);
 cudaError_t launch_forward_prefix(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why);

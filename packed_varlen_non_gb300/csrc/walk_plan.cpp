@@ -21,18 +21,28 @@ namespace {
 struct Item {
   WalkUnit u;
   int32_t tiles;      // key tiles (list walk: at most this many)
+  int32_t limit;      // every piece begins below this tile
   bool direct;        // writes the output itself unless it is split
   int32_t pieces = 1;
   int32_t part = -1;  // first partial row of piece 0
   bool partial() const { return !direct || pieces > 1; }
   int32_t rows() const { return u.q_end - u.q_row0; }
+  // pieces of at most m tiles
+  int32_t split(int32_t m) const { return std::max(1, std::min((tiles + m - 1) / m, limit)); }
 };
 
-// Rows to combine from the partial rows of items a and b (-1: none) and from
-// the keys [key_lo, key_hi) themselves.
+// First tile of piece c of n (c = n: the end): even shares, but every piece
+// begins below the item's limit.
+int32_t bound(const Item& it, int32_t c, int32_t n) {
+  if (c == n) return it.tiles;
+  return (int32_t)std::min<int64_t>((int64_t)it.tiles * c / n, it.limit - (n - c));
+}
+
+// Rows to combine from the partial rows of an item and from the keys [key_lo,
+// key_hi) themselves.
 struct Join {
   int32_t row0, row1, head;
-  int32_t a, b;
+  int32_t item;
   int32_t key_lo, key_hi;
 };
 
@@ -69,12 +79,10 @@ void balance(std::vector<Item>& items, int G, int segs) {
     cost.clear();
     int64_t rows = 0;
     for (size_t i = 0; i < U; ++i) {
-      const int32_t n = i < whole ? 1 : std::max<int32_t>(1, (items[i].tiles + m - 1) / m);
+      const int32_t n = i < whole ? 1 : items[i].split(m);
       const bool partial = !items[i].direct || n > 1;
-      for (int32_t c = 0; c < n; ++c) {
-        const int32_t t = (int32_t)((int64_t)items[i].tiles * (c + 1) / n - (int64_t)items[i].tiles * c / n);
-        cost.push_back(piece_cost(t, partial));
-      }
+      for (int32_t c = 0; c < n; ++c)
+        cost.push_back(piece_cost(bound(items[i], c + 1, n) - bound(items[i], c, n), partial));
       if (partial) rows += (int64_t)n * items[i].rows();
     }
     if (segs > 1) cost = unit_costs(cost, segs);
@@ -85,7 +93,7 @@ void balance(std::vector<Item>& items, int G, int segs) {
     if (best < 0.0 || score < best) {
       best = score;
       for (size_t i = 0; i < U; ++i)
-        best_pieces[i] = i < whole ? 1 : std::max<int32_t>(1, (items[i].tiles + m - 1) / m);
+        best_pieces[i] = i < whole ? 1 : items[i].split(m);
     }
   };
   consider(U, 1);
@@ -120,15 +128,13 @@ std::string finish(std::vector<Item>& items, std::vector<Join>& joins, int G, Ma
       WalkUnit s = make(it, c);
       s.part = it.partial() ? it.part + c * it.rows() : -1;
       segs.push_back(s);
-      const int32_t t =
-          (int32_t)((int64_t)it.tiles * (c + 1) / it.pieces - (int64_t)it.tiles * c / it.pieces);
-      cost.push_back(piece_cost(t, it.partial()));
+      cost.push_back(piece_cost(bound(it, c + 1, it.pieces) - bound(it, c, it.pieces), it.partial()));
     }
   }
   w.part_rows = rows;
   for (size_t i = 0; i < items.size(); ++i)
     if (items[i].direct && items[i].pieces > 1)
-      joins.push_back(Join{items[i].u.q_row0, items[i].u.q_end, items[i].u.head, (int32_t)i, -1, 0, 0});
+      joins.push_back(Join{items[i].u.q_row0, items[i].u.q_end, items[i].u.head, (int32_t)i, 0, 0});
   w.joins.clear();
   for (const Join& j : joins) {
     JoinRec r;
@@ -136,18 +142,11 @@ std::string finish(std::vector<Item>& items, std::vector<Join>& joins, int G, Ma
     r.head = j.head;
     r.key_lo = j.key_lo;
     r.key_hi = j.key_hi;
-    const Item& a = items[j.a];
-    r.a_part = a.part;
-    r.a_rows = a.rows();
-    r.n_a = a.pieces;
-    r.a_row0 = a.u.q_row0;
-    if (j.b >= 0) {
-      const Item& b = items[j.b];
-      r.b_part = b.part;
-      r.b_rows = b.rows();
-      r.n_b = b.pieces;
-      r.b_row0 = b.u.q_row0;
-    }
+    const Item& it = items[j.item];
+    r.part = it.part;
+    r.rows = it.rows();
+    r.n = it.pieces;
+    r.q_row0 = it.u.q_row0;
     for (int32_t x = j.row0; x < j.row1; x += kJoinRows) {
       r.row0 = x;
       r.row1 = std::min(x + kJoinRows, j.row1);
@@ -199,7 +198,7 @@ std::string build_list_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads
     for (int32_t h = 0; h < num_heads; ++h)
       for (int32_t r = b, i = block0[d]; r < e; ++i) {
         const int32_t end = (int32_t)std::min<int64_t>((int64_t)r + q_block, e);
-        items.push_back(Item{WalkUnit{r, end, b, e, h, i, 0, -1}, tiles, true});
+        items.push_back(Item{WalkUnit{r, end, b, e, h, i, 0, -1}, tiles, tiles, true});
         r = end;
       }
   }
@@ -218,34 +217,21 @@ std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_hea
                               WalkPlan& w) {
   const int G = grid > 0 ? grid : 1;
   const int32_t tp = (int32_t)(((int64_t)prefix_len + kKeyTile - 1) / kKeyTile);
-  // The rows are cut into chunks of up to kUnitRows.  A chunk within one
-  // document walks the prefix's tiles and then the document's and writes the
-  // output.  A chunk over several documents walks the prefix once for all its
-  // rows and leaves partial rows; each document's rows in it walk their own
-  // document in a segment of its own, or, in a document of at most
-  // kJoinOwnKeys tokens, in the join.  A document joins the open chunk of the
-  // documents before it where that is cheaper than chunks of its own.
+  // The rows are cut into chunks of up to kUnitRows, which walk the prefix once
+  // for all their rows and then their documents' own tiles.  A document joins the
+  // open chunk of the documents before it unless that costs it a chunk more.
   struct Piece {
     int32_t doc, row0, row1;
   };
   std::vector<std::vector<Piece>> chunks;
   int32_t filled = 0;  // rows of the last chunk
   const auto tiles_of = [cu](int32_t d) { return (cu[d + 1] - cu[d] + kKeyTile - 1) / kKeyTile; };
-  const auto own_cost = [&](int32_t d, int32_t rows) {
-    return cu[d + 1] - cu[d] <= kJoinOwnKeys ? 0.0 : tiles_of(d) + 1.0 + (double)rows / kRowsPerPeriod;
-  };
   for (int32_t d = 0; d < n_docs; ++d) {
     const int32_t L = cu[d + 1] - cu[d];
-    const double whole = (double)tp + tiles_of(d) + 1;  // a chunk of this document alone
     int32_t at = cu[d];
     if (filled > 0 && filled < kUnitRows) {
       const int32_t r = std::min(L, kUnitRows - filled);
-      double cont = (double)r / kRowsPerPeriod + own_cost(d, r) + whole * ((L - r + kUnitRows - 1) / kUnitRows);
-      if (chunks.back().size() == 1) {  // that chunk would no longer write its output itself
-        const int32_t o = chunks.back()[0].doc;
-        cont += (double)filled / kRowsPerPeriod + own_cost(o, filled) - tiles_of(o);
-      }
-      if (cont < whole * ((L + kUnitRows - 1) / kUnitRows)) {
+      if ((L - r + kUnitRows - 1) / kUnitRows < (L - 1) / kUnitRows + 1) {
         chunks.back().push_back(Piece{d, at, at + r});
         filled += r;
         at += r;
@@ -258,36 +244,70 @@ std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_hea
       at += r;
     }
   }
+  // What a chunk over several documents walks after the prefix.  Documents of
+  // at most kJoinOwnKeys tokens take a whole tile each, for a few keys: where
+  // there are more of them than the chunk's partial rows cost (kRowsPerPeriod),
+  // the chunk leaves partial rows and the join attends to them.
+  struct Own {
+    int32_t first = 0, n = 0;
+    bool join = false;
+  };
+  std::vector<Own> own(chunks.size());
+  w.own.clear();
+  const auto small = [cu](int32_t d) { return cu[d + 1] - cu[d] <= kJoinOwnKeys; };
+  for (size_t c = 0; c < chunks.size(); ++c) {
+    if (chunks[c].size() == 1) continue;
+    const int32_t q0 = chunks[c].front().row0, rows = chunks[c].back().row1 - q0;
+    int32_t tiny = 0;
+    for (const Piece& p : chunks[c]) tiny += small(p.doc);
+    own[c].first = (int32_t)w.own.size();
+    own[c].join = tiny > 2 + rows / kRowsPerPeriod;
+    for (const Piece& p : chunks[c]) {
+      if (own[c].join && small(p.doc)) continue;
+      for (int32_t t = cu[p.doc]; t < cu[p.doc + 1]; t += kKeyTile) {
+        OwnTile o;
+        o.row = t;
+        o.rem = cu[p.doc + 1] - t;
+        o.lo = p.row0 - q0;
+        o.hi = p.row1 - q0;
+        for (int32_t r = 0; r < kUnitRows; r += 32) {
+          uint32_t skip = 0;
+          for (int32_t i = 0; i < 32; ++i) skip |= (uint32_t)(r + i < o.lo || r + i >= o.hi) << i;
+          o.skip[r / 256][r % 256 / 32] = skip;
+        }
+        w.own.push_back(o);
+      }
+    }
+    own[c].n = (int32_t)w.own.size() - own[c].first;
+    if (w.own.size() >= (size_t(1) << 31) / sizeof(OwnTile)) return "the layout needs too large a table of own tiles";
+  }
+  // (a split chunk's pieces beyond the direct ones are joined by finish)
   // head by head: the pairs running at one moment share a head's prefix in L2
   std::vector<Item> items;
   std::vector<Join> joins;
   for (int32_t h = 0; h < num_heads; ++h) {
-    for (const std::vector<Piece>& c : chunks) {
+    for (size_t x = 0; x < chunks.size(); ++x) {
+      const std::vector<Piece>& c = chunks[x];
       const int32_t q0 = c.front().row0, q1 = c.back().row1;
-      const int32_t b = cu[c[0].doc], e = cu[c[0].doc + 1];
       if (c.size() == 1) {
         const int32_t t = tp + tiles_of(c[0].doc);
-        items.push_back(Item{WalkUnit{q0, q1, b, e, h, 0, t, -1}, t, true});
+        items.push_back(Item{WalkUnit{q0, q1, cu[c[0].doc], cu[c[0].doc + 1], h, 0, t, -1}, t, t, true});
         continue;
       }
-      const int32_t pre = (int32_t)items.size();
-      items.push_back(Item{WalkUnit{q0, q1, b, e, h, 0, tp, -1}, tp, false});
-      for (const Piece& p : c) {
-        const int32_t db = cu[p.doc], de = cu[p.doc + 1], t = tiles_of(p.doc);
-        if (de - db <= kJoinOwnKeys) {
-          joins.push_back(Join{p.row0, p.row1, h, pre, -1, db, de});
-        } else {
-          joins.push_back(Join{p.row0, p.row1, h, pre, (int32_t)items.size(), 0, 0});
-          items.push_back(Item{WalkUnit{p.row0, p.row1, db, de, h, tp, tp + t, -1}, t, false});
-        }
-      }
+      // (n = 0: a chunk of small documents walks the prefix alone)
+      const int32_t t = tp + own[x].n;
+      if (own[x].join)
+        for (const Piece& p : c)
+          joins.push_back(Join{p.row0, p.row1, h, (int32_t)items.size(), small(p.doc) ? cu[p.doc] : 0,
+                               small(p.doc) ? cu[p.doc + 1] : 0});
+      items.push_back(Item{WalkUnit{q0, q1, own[x].first, -own[x].n, h, 0, t, -1}, t, tp, !own[x].join});
     }
   }
   balance(items, G, w.segs);
   return finish(items, joins, G, [](const Item& it, int32_t c) {
     WalkUnit s = it.u;
-    s.a = it.u.a + (int32_t)((int64_t)it.tiles * c / it.pieces);
-    s.b = it.u.a + (int32_t)((int64_t)it.tiles * (c + 1) / it.pieces);
+    s.a = bound(it, c, it.pieces);
+    s.b = bound(it, c + 1, it.pieces);
     return s;
   }, w);
 }

@@ -77,8 +77,8 @@ _SIGS = {
     "h3attn_forward_prefix": [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p,
                               c_int64, c_float, c_void_p, c_void_p],
     "h3attn_walk_list_host": [c_int32, c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_int64,
-                              c_void_p, c_void_p, c_int64, POINTER(c_int64), POINTER(c_int32), POINTER(c_int64),
-                              POINTER(c_int64)],
+                              c_void_p, c_void_p, c_int64, c_void_p, c_int64, POINTER(c_int64), POINTER(c_int32),
+                              POINTER(c_int64), POINTER(c_int64), POINTER(c_int64)],
     "h3attn_get_device_error": [c_void_p, c_void_p],
     "h3attn_selftest_bounded_wait": [c_uint64, c_void_p],
 }
@@ -407,19 +407,21 @@ def h3attn_forward_prefix(plan, q, k, v, k_prefix, v_prefix, o, softmax_scale: f
 def h3attn_walk_list_host(kind: int, cu_seqlens, num_heads: int, p0: int, p1: int, n_pairs: int):
     """The work list of the sparse (kind 0: p0 = q_block, p1 = max_blocks) or
     prefix (kind 1: p0 = prefix_len) forward, built on the host: (units [n, 8],
-    unit_off, joins [m, 16], partial rows); the fields are those of the C call."""
+    unit_off, joins [m, 12], own tiles [t, 20], partial rows); the fields are
+    those of the C call."""
     cu = np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
-    n, used, nj, rows = c_int64(), c_int32(), c_int64(), c_int64()
+    n, used, nj, no, rows = c_int64(), c_int32(), c_int64(), c_int64(), c_int64()
     head = (int(kind), cu.ctypes.data, int(cu.size) - 1, int(num_heads), int(p0), int(p1), int(n_pairs))
-    tail = (ctypes.byref(n), ctypes.byref(used), ctypes.byref(nj), ctypes.byref(rows))
+    tail = [ctypes.byref(x) for x in (n, used, nj, no, rows)]
     lib = load()
-    _check(lib.h3attn_walk_list_host(*head, None, 0, None, None, 0, *tail), "h3attn_walk_list_host")
+    _check(lib.h3attn_walk_list_host(*head, None, 0, None, None, 0, None, 0, *tail), "h3attn_walk_list_host")
     units = np.zeros((n.value, 8), dtype=np.int32)
     off = np.zeros(used.value + 1, dtype=np.int32)
-    joins = np.zeros((nj.value, 16), dtype=np.int32)
+    joins = np.zeros((nj.value, 12), dtype=np.int32)
+    own = np.zeros((no.value, 20), dtype=np.int32)
     _check(lib.h3attn_walk_list_host(*head, units.ctypes.data, n.value, off.ctypes.data, joins.ctypes.data, nj.value,
-                                     *tail), "h3attn_walk_list_host")
-    return units, off, joins, rows.value
+                                     own.ctypes.data, no.value, *tail), "h3attn_walk_list_host")
+    return units, off, joins, own, rows.value
 
 
 def h3attn_get_device_error(plan, stream=None):

@@ -24,9 +24,9 @@ def tiles(n):
     return math.ceil(n / 128)
 
 
-def check_rows(lens, heads, units, off, joins, part_rows, walk_of, share_of):
-    """walk_of(row) -> number of steps of the row's walk; share_of(segment) ->
-    its steps of that walk as a (lo, hi) range."""
+def check_rows(lens, heads, units, off, joins, part_rows, steps_of, share_of):
+    """steps_of(segment) -> steps of its whole walk; share_of(segment) -> those it
+    takes, as a (lo, hi) range.  Returns (row, head) -> keys the join attends to."""
     S = sum(lens)
     assert off[0] == 0 and off[-1] == len(units) and np.all(np.diff(off) >= 1)
     done = np.zeros((heads, S), dtype=np.int32)
@@ -37,30 +37,28 @@ def check_rows(lens, heads, units, off, joins, part_rows, walk_of, share_of):
         assert 0 <= q0 < q1 <= S and q1 - q0 <= 512 and 0 <= h < heads
         if part < 0:
             done[h, q0:q1] += 1
-            assert share_of(s) == (0, walk_of(q0)) and walk_of(q0) == walk_of(q1 - 1)
+            assert share_of(s) == (0, steps_of(s))
         else:
             used[part:part + q1 - q0] += 1
             by_part[part] = s
     assert np.all(used == 1)
-    for r0, r1, h, key_lo, a_part, a_rows, n_a, a_q0, b_part, b_rows, n_b, b_q0, key_hi, *_ in joins.tolist():
-        assert 0 <= r0 < r1 <= S
+    inline = {}
+    for r0, r1, h, q0, part, rows, n, key_lo, key_hi, *rest in joins.tolist():
+        assert 0 <= r0 < r1 <= S and r1 - r0 <= 8 and n >= 1 and rest == [0, 0, 0]
         done[h, r0:r1] += 1
         spans = []
-        for part, rows, n, q0 in ((a_part, a_rows, n_a, a_q0), (b_part, b_rows, n_b, b_q0)):
-            for c in range(n):
-                s = by_part[part + c * rows]
-                assert int(s[0]) == q0 and int(s[1]) - q0 == rows and int(s[4]) == h
-                assert q0 <= r0 and r1 <= q0 + rows
-                spans.append(share_of(s))
-        if key_hi > key_lo:  # the join attends to the document itself
-            cu = np.concatenate([[0], np.cumsum(lens)])
-            d = int(np.searchsorted(cu, r0, side="right")) - 1
-            assert (key_lo, key_hi) == (cu[d], cu[d + 1]) and key_hi - key_lo <= 32
-            spans.append((walk_of(r0) - tiles(key_hi - key_lo), walk_of(r0)))
-        spans.sort()
-        assert spans[0][0] == 0 and spans[-1][1] == walk_of(r0) == walk_of(r1 - 1)
+        for c in range(n):
+            s = by_part[part + c * rows]
+            assert int(s[0]) == q0 and int(s[1]) - q0 == rows and int(s[4]) == h
+            assert q0 <= r0 and r1 <= q0 + rows
+            spans.append(share_of(s))
+        assert spans[0][0] == 0 and spans[-1][1] == steps_of(s)
         assert all(x[1] == y[0] for x, y in zip(spans, spans[1:]))
+        if key_hi > key_lo:
+            for r in range(r0, r1):
+                inline[h, r] = (key_lo, key_hi)
     assert np.all(done == 1)
+    return inline
 
 
 @pytest.mark.parametrize("lens,heads", LAYOUTS)
@@ -68,7 +66,7 @@ def check_rows(lens, heads, units, off, joins, part_rows, walk_of, share_of):
 @pytest.mark.parametrize("pairs", [76, 5])
 def test_list_walk_covers_every_row(lib, lens, heads, q_block, max_blocks, pairs):
     cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
-    units, off, joins, part_rows = H.h3attn_walk_list_host(0, cu, heads, q_block, max_blocks, pairs)
+    units, off, joins, own, part_rows = H.h3attn_walk_list_host(0, cu, heads, q_block, max_blocks, pairs)
     blocks = [(r, min(r + q_block, b), a, b) for a, b in zip(cu[:-1], cu[1:]) for r in range(a, b, q_block)]
     for s in units:
         q0, q1, b, e, _, block, _, _ = (int(x) for x in s)
@@ -80,7 +78,7 @@ def test_list_walk_covers_every_row(lib, lens, heads, q_block, max_blocks, pairs
         i, m = int(s[6]) & 0xffff, (int(s[6]) >> 16) & 0xffff
         assert 0 <= i < m
         return n * i // m, n * (i + 1) // m
-    check_rows(lens, heads, units, off, joins, part_rows, lambda row: n, share)
+    assert not check_rows(lens, heads, units, off, joins, part_rows, lambda s: n, share) and len(own) == 0
 
 
 @pytest.mark.parametrize("lens,heads", LAYOUTS)
@@ -88,16 +86,41 @@ def test_list_walk_covers_every_row(lib, lens, heads, q_block, max_blocks, pairs
 @pytest.mark.parametrize("pairs", [76, 5])
 def test_prefix_walk_covers_every_row(lib, lens, heads, prefix, pairs):
     cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
-    units, off, joins, part_rows = H.h3attn_walk_list_host(1, cu, heads, prefix, 0, pairs)
+    units, off, joins, own, part_rows = H.h3attn_walk_list_host(1, cu, heads, prefix, 0, pairs)
     tp = tiles(prefix)
     doc = np.repeat(np.arange(len(lens)), lens)
-    steps = tp + np.array([tiles(n) for n in lens])[doc]
+
+    def steps(s):
+        return tp + (tiles(int(s[3]) - int(s[2])) if s[3] > 0 else -int(s[3]))
+    inline = check_rows(lens, heads, units, off, joins, part_rows, steps, lambda s: (int(s[5]), int(s[6])))
+    for h, r in inline:
+        assert inline[h, r] == (cu[doc[r]], cu[doc[r] + 1]) and lens[doc[r]] <= 32
+    seen = set()
     for s in units:
-        q0, q1, b, e, _, lo, hi, _ = (int(x) for x in s)
-        assert 0 <= lo < hi
-        if hi > tp:  # own tiles: rows of one document, whose bounds the segment has
+        q0, q1, b, e, h, lo, hi, part = (int(x) for x in s)
+        assert 0 <= lo < hi <= steps(s)
+        if e > 0:  # rows of one document, whose bounds the segment has
             assert doc[q0] == doc[q1 - 1] and (b, e) == (cu[doc[q0]], cu[doc[q0] + 1])
-    check_rows(lens, heads, units, off, joins, part_rows, lambda row: int(steps[row]), lambda s: (int(s[5]), int(s[6])))
+            continue
+        assert lo < tp  # every piece begins in the prefix
+        if (h, q0) in seen:
+            continue
+        seen.add((h, q0))
+        # the own tiles are exactly those of each row's document, unless the join has it
+        want, at = [], q0
+        while at < q1:
+            d = doc[at]
+            end = min(int(cu[d + 1]), q1)
+            if (h, at) not in inline:
+                want += [(t, int(cu[d + 1]) - t, at - q0, end - q0) for t in range(cu[d], cu[d + 1], 128)]
+            at = end
+        table = own[b:b - e]
+        assert [tuple(x) for x in table[:, :4].tolist()] == want
+        for t in table:  # lanes of the other documents' rows, 32 a word
+            rows = np.arange(512)
+            skip = (rows < t[2]) | (rows >= t[3])
+            words = t[4:].astype(np.uint32)
+            assert np.array_equal((words[rows // 32] >> (rows % 32).astype(np.uint32)) & 1, skip)
 
 
 def cost(s, lo, hi):
@@ -107,12 +130,11 @@ def cost(s, lo, hi):
 @pytest.mark.parametrize("lens,heads,prefix", [([4096] * 3, 21, 2430), ([1] * 32, 21, 5033), ([20423], 21, 405)])
 def test_prefix_passes_are_shared_and_pairs_evenly_loaded(lib, lens, heads, prefix):
     cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
-    units, off, _, _ = H.h3attn_walk_list_host(1, cu, heads, prefix, 0, 76)
+    units, off, _, _, _ = H.h3attn_walk_list_host(1, cu, heads, prefix, 0, 76)
     tp = tiles(prefix)
-    # steps over the prefix: no more than one pass per 512 rows of a head, rounded up per document of 512 or more
+    # steps over the prefix: one pass per 512 rows of a head
     steps = sum(min(int(s[6]), tp) - min(int(s[5]), tp) for s in units)
-    passes = math.ceil(sum(lens) / 512) if max(lens) < 512 else sum(math.ceil(n / 512) for n in lens)
-    assert steps <= heads * passes * tp
+    assert steps == heads * math.ceil(sum(lens) / 512) * tp
     loads = [sum(cost(s, int(s[5]), int(s[6])) for s in units[off[p]:off[p + 1]]) for p in range(len(off) - 1)]
     assert max(loads) <= 1.15 * sum(loads) / 76 + 2
 
