@@ -1734,7 +1734,9 @@ __device__ __forceinline__ float4 load_bf16x4(const __nv_bfloat16* p) {
                      __uint_as_float(w.y & 0xffff0000u));
 }
 
-// The rows of a record are a block's; parts are read two at a time with their
+constexpr int kAtOnce = 4;
+
+// The rows of a record are a block's; parts are read kAtOnce at a time with their
 // maxima and rows together, in one pass with a running maximum, so that a row
 // waits for memory about once.
 __global__ void __launch_bounds__(32 * kJoinRows, 6) attn_join_kernel(JoinArgs a) {
@@ -1780,11 +1782,11 @@ __global__ void __launch_bounds__(32 * kJoinRows, 6) attn_join_kernel(JoinArgs a
   float M = m_own, l = l_own;
   float4 acc = o_own;
 #pragma unroll 1
-  for (int c = 0; c < j.n; c += 2) {
-    float2 ml[2];
-    float4 o[2];
+  for (int c = 0; c < j.n; c += kAtOnce) {
+    float2 ml[kAtOnce];
+    float4 o[kAtOnce];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < kAtOnce; ++x) {
       ml[x] = make_float2(-INFINITY, 0.f);
       o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c + x < j.n) {
@@ -1793,14 +1795,22 @@ __global__ void __launch_bounds__(32 * kJoinRows, 6) attn_join_kernel(JoinArgs a
         o[x] = reinterpret_cast<const float4*>(a.part_o + r * kHeadDim)[lane];
       }
     }
-    const float m_new = dev::max3(M, ml[0].x, ml[1].x);
+    float m_new = M;
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) m_new = fmaxf(m_new, ml[x].x);
     const float ref = m_new == -INFINITY ? 0.f : m_new;
-    const float w = dev::ex2_approx(M - ref), w0 = dev::ex2_approx(ml[0].x - ref), w1 = dev::ex2_approx(ml[1].x - ref);
-    acc.x = fmaf(w1, o[1].x, fmaf(w0, o[0].x, w * acc.x));
-    acc.y = fmaf(w1, o[1].y, fmaf(w0, o[0].y, w * acc.y));
-    acc.z = fmaf(w1, o[1].z, fmaf(w0, o[0].z, w * acc.z));
-    acc.w = fmaf(w1, o[1].w, fmaf(w0, o[0].w, w * acc.w));
-    l = fmaf(w1, ml[1].y, fmaf(w0, ml[0].y, w * l));
+    const float w = dev::ex2_approx(M - ref);
+    acc = make_float4(w * acc.x, w * acc.y, w * acc.z, w * acc.w);
+    l *= w;
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) {
+      const float wx = dev::ex2_approx(ml[x].x - ref);
+      acc.x = fmaf(wx, o[x].x, acc.x);
+      acc.y = fmaf(wx, o[x].y, acc.y);
+      acc.z = fmaf(wx, o[x].z, acc.z);
+      acc.w = fmaf(wx, o[x].w, acc.w);
+      l = fmaf(wx, ml[x].y, l);
+    }
     M = m_new;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1947,19 +1957,9 @@ bool make_forward_maps(const ForwardArgs& a, ForwardMaps* m, std::string* why) {
   return true;
 }
 
-// The forward over another walk, then the join of the rows it left in parts.
-template <int kWalk, bool kPair>
-cudaError_t launch_walk(const ForwardMaps& m, const ForwardArgs& a, const WalkArgs& w, const Walk<kWalk>& walk,
-                        cudaStream_t stream, std::string* why) {
-  cudaError_t e = set_smem_attr<false, kWalk, kPair>();
-  if (e != cudaSuccess) {
-    if (why) *why = "cudaFuncSetAttribute(max dynamic shared memory) failed";
-    return e;
-  }
-  attn_fwd_tc_kernel<false, kWalk, kPair>
-      <<<2 * a.n_pairs, kThreads, Cfg<false, kPair>::SmemAlloc, stream>>>(m.q, m.k, m.v, m.o, a, m.o_tma, walk);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || w.n_joins == 0) return e;
+// The join of the rows that a walk left in parts.
+cudaError_t launch_join(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why) {
+  if (w.n_joins == 0) return cudaSuccess;
   const JoinArgs j{w.joins,
                    static_cast<const __nv_bfloat16*>(a.q),
                    static_cast<const __nv_bfloat16*>(a.k),
@@ -1972,9 +1972,24 @@ cudaError_t launch_walk(const ForwardMaps& m, const ForwardArgs& a, const WalkAr
                    a.scale_log2,
                    a.part_o,
                    a.part_ml};
-  e = launch_dependent(attn_join_kernel, (unsigned)w.n_joins, 32u * kJoinRows, stream, j);
+  const cudaError_t e = launch_dependent(attn_join_kernel, (unsigned)w.n_joins, 32u * kJoinRows, stream, j);
   if (e != cudaSuccess && why) *why = "the join launch failed";
   return e;
+}
+
+// The forward over another walk, then the join.
+template <int kWalk, bool kPair>
+cudaError_t launch_walk(const ForwardMaps& m, const ForwardArgs& a, const WalkArgs& w, const Walk<kWalk>& walk,
+                        cudaStream_t stream, std::string* why) {
+  cudaError_t e = set_smem_attr<false, kWalk, kPair>();
+  if (e != cudaSuccess) {
+    if (why) *why = "cudaFuncSetAttribute(max dynamic shared memory) failed";
+    return e;
+  }
+  attn_fwd_tc_kernel<false, kWalk, kPair>
+      <<<2 * a.n_pairs, kThreads, Cfg<false, kPair>::SmemAlloc, stream>>>(m.q, m.k, m.v, m.o, a, m.o_tma, walk);
+  e = cudaGetLastError();
+  return e != cudaSuccess ? e : launch_join(a, w, stream, why);
 }
 
 }  // namespace
@@ -1995,6 +2010,20 @@ cudaError_t launch_forward_list(const ForwardArgs& a, const WalkArgs& w, cudaStr
 }
 
 cudaError_t launch_forward_prefix(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why) {
+  if (w.rows) {
+    const RowsArgs r{static_cast<const __nv_bfloat16*>(a.q),
+                     static_cast<const __nv_bfloat16*>(w.k_prefix),
+                     static_cast<const __nv_bfloat16*>(w.v_prefix),
+                     a.qkv_stride,
+                     w.prefix_stride,
+                     w.prefix_len,
+                     reinterpret_cast<const WalkUnit*>(a.units),
+                     a.scale_log2,
+                     a.part_o,
+                     a.part_ml};
+    const cudaError_t e = launch_attn_rows(r, a.n_units, a.S < kRowsTile ? (int)a.S : kRowsTile, stream);
+    return e != cudaSuccess ? e : launch_join(a, w, stream, why);
+  }
   ForwardMaps m;
   if (!make_forward_maps(a, &m, why)) return cudaErrorInvalidValue;
   Walk<kWalkPrefix> walk;

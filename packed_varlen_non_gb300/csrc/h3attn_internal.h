@@ -2,6 +2,7 @@
 // C-ABI layer) and the kernel launchers.  Nothing here is part of the ABI.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -131,8 +132,14 @@ static_assert(sizeof(JoinRec) == 48, "JoinRec is read as three 16-byte vectors")
 constexpr int kJoinRows = 8;         // rows per join block (one warp each)
 constexpr int kJoinOwnKeys = 32;     // longest document the join may attend to itself
 
+// A few short documents over a prefix (attn_rows.cu): at most kRowsMax rows in
+// all, kRowsTile of them and one head to a segment, a block each.
+constexpr int kRowsTile = 32;
+constexpr int kRowsMax = 64;
+
 struct WalkPlan {
   bool set = false;
+  bool rows = false;                   // prefix walk of a few short documents: unit_off is not used
   int segs = 1;                        // segments of a unit: 2 run side by side on a CTA pair
   std::vector<WalkUnit> units;         // segments, unit by unit, grouped by CTA pair (q_row0 = q_end: none)
   std::vector<int32_t> unit_off;       // [n_pairs + 1], in units
@@ -346,6 +353,7 @@ struct WalkArgs {
   const JoinRec* joins;
   int32_t n_joins;
   bool pair;                   // units of two segments
+  bool rows;                   // attn_rows.cu's segments
   // list walk
   const int32_t* block_idx;    // [H, n_q_blocks, max_blocks]
   const int32_t* block_cnt;    // [H, n_q_blocks]
@@ -358,6 +366,19 @@ struct WalkArgs {
   int32_t prefix_len;
   const OwnTile* own;
 };
+struct RowsArgs {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k_prefix;
+  const __nv_bfloat16* v_prefix;
+  int64_t q_stride, prefix_stride;
+  int32_t prefix_len;
+  const WalkUnit* units;
+  float scale_log2;
+  float* part_o;
+  float2* part_ml;
+};
+cudaError_t launch_attn_rows(const RowsArgs& a, int n_units, int max_rows, cudaStream_t stream);
+
 cudaError_t launch_forward_list(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why);
 cudaError_t launch_forward_prefix(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why);
 

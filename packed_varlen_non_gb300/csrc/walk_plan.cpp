@@ -213,10 +213,40 @@ std::string build_list_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads
   }, w);
 }
 
+static WalkUnit prefix_piece(const Item& it, int32_t c) {
+  WalkUnit s = it.u;
+  s.a = bound(it, c, it.pieces);
+  s.b = bound(it, c + 1, it.pieces);
+  return s;
+}
+
 std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads, int32_t prefix_len, int grid,
                               WalkPlan& w) {
   const int G = grid > 0 ? grid : 1;
   const int32_t tp = (int32_t)(((int64_t)prefix_len + kKeyTile - 1) / kKeyTile);
+  // Up to kRowsMax rows of documents that the join can attend to: bound by
+  // reading the prefix, a block per SM half (attn_rows.cu).
+  int32_t longest = 0;
+  for (int32_t d = 0; d < n_docs; ++d) longest = std::max(longest, cu[d + 1] - cu[d]);
+  if (cu[n_docs] <= kRowsMax && longest <= kJoinOwnKeys) {
+    w.rows = true;
+    std::vector<Item> items;
+    std::vector<Join> joins;
+    const int32_t tiles = (cu[n_docs] + kRowsTile - 1) / kRowsTile;
+    const int32_t blocks = std::max(1, 4 * G / std::max(1, tiles * num_heads));  // two per SM
+    for (int32_t q0 = 0; q0 < cu[n_docs]; q0 += kRowsTile)
+      for (int32_t h = 0; h < num_heads; ++h) {
+        const int32_t q1 = std::min(q0 + kRowsTile, cu[n_docs]);
+        for (int32_t d = 0; d < n_docs; ++d) {
+          const int32_t r0 = std::max(cu[d], q0), r1 = std::min(cu[d + 1], q1);
+          if (r0 < r1) joins.push_back(Join{r0, r1, h, (int32_t)items.size(), cu[d], cu[d + 1]});
+        }
+        Item it{WalkUnit{q0, q1, 0, 0, h, 0, tp, -1}, tp, tp, false};
+        it.pieces = std::min(blocks, tp);
+        items.push_back(it);
+      }
+    return finish(items, joins, (int)std::min<size_t>(items.size() * items[0].pieces, size_t(1) << 20), prefix_piece, w);
+  }
   // The rows are cut into chunks of up to kUnitRows, which walk the prefix once
   // for all their rows and then their documents' own tiles.  A document joins the
   // open chunk of the documents before it unless that costs it a chunk more.
@@ -304,12 +334,7 @@ std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_hea
     }
   }
   balance(items, G, w.segs);
-  return finish(items, joins, G, [](const Item& it, int32_t c) {
-    WalkUnit s = it.u;
-    s.a = bound(it, c, it.pieces);
-    s.b = bound(it, c + 1, it.pieces);
-    return s;
-  }, w);
+  return finish(items, joins, G, prefix_piece, w);
 }
 
 }  // namespace h3

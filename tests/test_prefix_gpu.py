@@ -15,6 +15,8 @@ pytestmark = pytest.mark.gpu
 LAYOUTS = [
     ([1], 1), ([1] * 5, 2), ([1] * 70, 1), ([32, 33, 31, 1, 2], 2), ([129, 40, 300, 7], 3), ([512], 1), ([513, 5], 2),
     ([700, 3, 3, 600], 2), ([40] * 30, 2), ([500, 20, 100, 530, 1], 4),
+    # (at most 64 rows of documents of at most 32 tokens: the few-rows kernel)
+    ([32, 31, 1], 2), ([3, 20, 30], 3), ([1] * 33, 2), ([16], 5),
 ]
 
 
@@ -44,7 +46,7 @@ def test_forward_matches_the_oracle(lib, lens, heads, prefix):
     W.check(o, lse, t[0], [t[1], t[3]], oracle(p, t), f"{lens} P={prefix}")
 
 
-@pytest.mark.parametrize("lens,heads,prefix", [([1], 21, 20423), ([2000, 2000], 8, 4096), ([31] * 40, 21, 640),
+@pytest.mark.parametrize("lens,heads,prefix", [([1], 21, 20423), ([1] * 64, 21, 5033), ([2000, 2000], 8, 4096), ([31] * 40, 21, 640),
                                                ([300] * 12, 56, 1215)])
 def test_larger_batches(lib, lens, heads, prefix):
     p = W.Prefix(lens, heads, prefix)
