@@ -46,16 +46,18 @@ struct Join {
   int32_t key_lo, key_hi;
 };
 
-// Times in key-tile periods of a CTA pair (about 1.15 us on GB300).  A segment
-// costs its tiles, one period for its start and epilogue, and another where it
-// leaves partial rows; the partial rows are written and read at about 6 TB/s
-// (520 bytes a row), by one pair at a time within a segment (kRowsPerPeriod)
-// and by all of them in the join.
+// Times in key-tile periods of a CTA pair (1.28 us on GB300).  A segment costs
+// its tiles and three periods (4 us, measured for segments of 1 to 16 tiles on
+// every walk: the pipeline runs empty at its end, and the tensor pipe resumes
+// at a third of its rate for a while), and another one where it leaves partial
+// rows.  The join takes kJoinStart, and a period for kJoinRowsPerPeriod partial
+// rows (141,658 of them measured 33 us); in a chunk of the prefix walk, a
+// period for kRowsPerPeriod of its rows, written and read by its pair's share.
 constexpr int kRowsPerPeriod = 87;
-constexpr double kJoinRowsPerPeriod = 6900.0;
-constexpr double kJoinStart = 2.0;
+constexpr double kJoinRowsPerPeriod = 5500.0;
+constexpr double kJoinStart = 2.5;
 
-int64_t piece_cost(int32_t tiles, bool partial) { return (int64_t)tiles + 1 + (partial ? 1 : 0); }
+int64_t piece_cost(int32_t tiles, bool partial) { return (int64_t)tiles + 3 + (partial ? 1 : 0); }
 
 // Costs of units of `segs` consecutive pieces that run in lockstep: the largest's.
 std::vector<int64_t> unit_costs(const std::vector<int64_t>& pieces, int segs) {
