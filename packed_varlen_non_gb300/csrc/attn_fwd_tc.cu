@@ -723,7 +723,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == kTmaWarp) {
     // ------------------------------------------------------ TMA producer ----
-    if (!kFp8 && lane == 1) {
+    if (!kFp8 && !kPair && lane == 1) {
       // bf16 O stores: as the four softmax warps of a query tile finish a
       // unit's epilogue, send the rows they staged in its Q slot (every warp
       // whose 32 rows lie in the document) with TMA tile stores, wait until
@@ -732,11 +732,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       int k = 0;
       for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-        UnitGeom g = unit_geom<kWalk, kPair>(a.units, u, walk);
+        const UnitGeom g = unit_geom<kWalk, kPair>(a.units, u, walk);
 #pragma unroll 1
         for (int s = 0; s < 2 && s < g.n_st; ++s) {
           const int i = q_slot_of<kPair>(k, s);
-          if (kPair && s == 1) g = unit_geom<kWalk, kPair>(a.units, u, walk, 1);
           ok = dev::mbar_wait(bars.o_staged(i), use[i] & 1, abort_flag, a.err, kTimeoutNs);
           ++use[i];
           if (!ok) break;
@@ -1001,12 +1000,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool issued = false;
       int k = 0;
       // QK of half h of the key tile in ring slot ks for query tile s (Q slot qs)
-      auto qk_half = [&](int s, uint32_t qs, uint32_t ks, int h) {
+      // (last: kPair, the segment's last QK: its Q slot is free once it completes)
+      auto qk_half = [&](int s, uint32_t qs, uint32_t ks, int h, bool last) {
         const uint32_t d = tmem + s * 128 + h * 64;
         const uint32_t qa = sbase + C::SmemQ + qs * C::QTileBytes;
         const uint32_t kb = sbase + C::SmemKV + ks * C::SlotBytes + h * kHalfKeyRowsBytes;
         issue_qk(d, qa, kb);
         commit_pair_elect(bars.s_ready(s, h));
+        if (kPair && last && h == 1) commit_pair_elect(bars.q_empty(qs));
       };
       // PV of half h of the key tile whose V is in ring slot vs, query tile s
       auto pv_half = [&](int s, uint32_t vs, int h, bool acc) {
@@ -1032,7 +1033,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       // The first QK (half h) of query tile s of a unit: Q slot qs (its readiness
       // in both CTAs is awaited before half 0), K in ring slot ks.
-      auto first_qk = [&](uint32_t qs, uint32_t ks, int s, int h) {
+      auto first_qk = [&](const UnitGeom& gg, uint32_t qs, uint32_t ks, int s, int h) {
         if (h == 0) {
           ok = __all_sync(0xffffffffu,
                           dev::mbar_wait(bars.q_ready(qs), q_use[qs] & 1, abort_flag, a.err, kTimeoutNs));
@@ -1040,7 +1041,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!ok) return;
           dev::tc_fence_after();
         }
-        qk_half(s, qs, ks, h);
+        qk_half(s, qs, ks, h, gg.hi - gg.lo == 1);
         issued = true;
       };
       // Ring slots of query tile s's V and next K in this step (kPair: group
@@ -1065,10 +1066,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // arrival in both CTAs
           if constexpr (kPair) {
             for (int s = 0; ok && s < 2; ++s)
-              for (int h = 0; ok && h < 2; ++h) first_qk(q_at[s], s, s, h);
+              for (int h = 0; ok && h < 2; ++h) first_qk(g, q_at[s], s, s, h);
           } else {
             for (int h = 0; ok && h < 2; ++h)
-              for (int s = 0; ok && s < g.n_st; ++s) first_qk(q_at[s], 0, s, h);
+              for (int s = 0; ok && s < g.n_st; ++s) first_qk(g, q_at[s], 0, s, h);
           }
           if (!ok) break;
         }
@@ -1107,7 +1108,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               ++p_it[s][h];
               dev::tc_fence_after();
               pv_half(s, v_at(s), h, acc0 || h == 1);
-              qk_half(s, q_at[s], k_at(s), h);
+              qk_half(s, q_at[s], k_at(s), h, j + 2 == g.hi);
             }
             if (!ok) break;
           }
@@ -1128,7 +1129,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ++p_it[s][h];
                 dev::tc_fence_after();
                 pv_half_skip(s, v_at(s), h);
-                qk_half(s, q_at[s], k_at(s), h);
+                qk_half(s, q_at[s], k_at(s), h, j + 2 == g.hi);
               }
               if (!ok) break;
             }
@@ -1159,13 +1160,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (has_next) {
             if constexpr (kPair) {
-              // (query tile 1's Q slot is the one this unit's query tile 0 leaves in
-              // its epilogue, so query tile 0 goes first)
               for (int s = 0; ok && s < 2; ++s)
-                for (int h = 0; ok && h < 2; ++h) first_qk(q_slot_of<kPair>(k + 1, s), k_at(s), s, h);
+                for (int h = 0; ok && h < 2; ++h) first_qk(gn, q_slot_of<kPair>(k + 1, s), k_at(s), s, h);
             } else {
               for (int h = 0; ok && h < 2; ++h)
-                for (int s = 0; ok && s < gn.n_st; ++s) first_qk(q_slot_of<kPair>(k + 1, s), kslot, s, h);
+                for (int s = 0; ok && s < gn.n_st; ++s) first_qk(gn, q_slot_of<kPair>(k + 1, s), kslot, s, h);
             }
           }
           advance();
@@ -1533,7 +1532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // (the partial buffer is a device allocation: its 512-byte rows are 32-byte aligned)
         // (dense: slots of kUnitRows rows; other walks: part is the segment's first partial row)
         const size_t slot = (kWalk == kWalkDoc ? (size_t)g.part * kUnitRows : (size_t)g.part) + local;
-        if constexpr (!kFp8) {
+        if constexpr (!kFp8 && !kPair) {
           // bf16: each 32-column chunk of the warp's 32 rows goes through its
           // rows of the unit's Q slot (free: the slot is released only after
           // this warp reports), so that every global store writes whole
@@ -1574,7 +1573,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t ov[32];
             dev::tmem_ld32(t_o + c * 32, ov);
             dev::tmem_wait_ld();
-            scale_by_channel(ov, a.sv + g.head * kHeadDim + c * 32);
+            if constexpr (kFp8) scale_by_channel(ov, a.sv + g.head * kHeadDim + c * 32);
             if (valid) {
 #pragma unroll
               for (int e = 0; e < 4; ++e)
@@ -1584,7 +1583,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         if (valid) a.part_ml[slot] = make_float2(m_used, l);
-        if constexpr (!kFp8) {
+        if constexpr (!kFp8 && !kPair) {
           __syncwarp();
           if (lane == 0) dev::mbar_arrive(bars.o_staged(q_slot));
         }
@@ -1593,7 +1592,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // (a row that saw no key: O is 0, lse = -inf)
       const float inv = kWalk != kWalkDoc && l == 0.f ? 0.f : 1.f / l;
       bool staged = false;
-      if constexpr (!kFp8) staged = o_tma != 0 && __all_sync(0xffffffffu, valid);
+      if constexpr (!kFp8 && !kPair) staged = o_tma != 0 && __all_sync(0xffffffffu, valid);
       if (staged) {
         // The warp's 32 rows, bf16, into its rows of the unit's Q slot (free:
         // every MMA of the unit is done) in the tile's 128-byte swizzled
@@ -1644,7 +1643,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if constexpr (!kFp8) {
+        if constexpr (!kFp8 && !kPair) {
           __syncwarp();
           if (lane == 0) dev::mbar_arrive(bars.o_staged(q_slot));
         }
