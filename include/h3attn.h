@@ -393,8 +393,8 @@ h3attn_status h3attn_forward_prefix(h3attn_plan_t plan, const void* q, const voi
  *            over several documents, whose n own tiles are entries [document
  *            begin, document begin + n) of own; last the first partial row (-1: the
  *            segment writes the output itself);
- *            With q_block 256, a pair runs its segments two at a time, side by
- *            side;
+ *            With q_block 256, a pair runs two streams of segments side by side
+ *            (the first one's come first here);
  *   unit_off [*n_pairs_used + 1] int32: pair p runs units [unit_off[p], unit_off[p + 1]);
  *   joins    [*n_joins][12] int32, the rows combined from partial rows: rows
  *            [r0, r1) (at most 8), head, and of their segment the first query

@@ -136,12 +136,12 @@ constexpr int kTileRows = 128;
 // Shared-memory layout: 2 buffers x 2 query tiles, then the ring.  bf16: a Q
 // tile is 128 rows x 128 dims in two 16 KB halves of 64 dims, a slot 16 KB;
 // fp8 (e4m3): a Q tile is one 16 KB block of 128-byte rows, a slot 8 KB.
-// kPair (two query blocks side by side): three Q tiles and eight ring slots.
+// kPair (two streams of segments side by side): two Q tiles and eight ring slots.
 template <bool kFp8, bool kPair = false>
 struct Cfg {
   static constexpr int Slots = kPair ? 8 : 6;          // ring slots
   static constexpr int Groups = Slots / 2;             // key/value groups in flight
-  static constexpr int QTiles = kPair ? 3 : 4;
+  static constexpr int QTiles = kPair ? 2 : 4;
   // q_full[4] q_empty[4] q_ready[4] kv_full[G] kv_empty[G] s_ready[2][2] p_ready[2][2] pv_done[2][2] drain o_staged[4]
   static constexpr int NumBars = 12 + 2 * Groups + 4 + 4 + 4 + 1 + 4;
   static constexpr uint32_t QTileBytes = kFp8 ? 128 * 128 : 128 * 128 * 2;
@@ -150,7 +150,8 @@ struct Cfg {
   static constexpr uint32_t SmemKV = QTiles * QTileBytes;
   static constexpr uint32_t SmemBar = SmemKV + Slots * SlotBytes;
   static constexpr uint32_t SmemMisc = SmemBar + NumBars * 8;
-  static constexpr size_t SmemAlloc = SmemMisc + 16 + 1024;  // slack to align the base to 1 KB
+  static constexpr uint32_t SmemSteps = SmemMisc + 16;  // kPair: steps of each stream's segments [2][4]
+  static constexpr size_t SmemAlloc = SmemSteps + (kPair ? 32 : 0) + 1024;  // slack to align the base to 1 KB
   static_assert(SmemAlloc <= 227 * 1024, "shared memory per CTA");
 };
 constexpr uint32_t kQHalfBytes = 128 * 128;            // bf16 Q tile: one half (64 dims)
@@ -179,10 +180,10 @@ constexpr uint32_t kIdescPV = kIdescBf16 | ((128u >> 3) << 17) | (1u << 16);
 constexpr uint32_t kIdescF8 = (1u << 4) | ((128u >> 3) << 17) | ((256u >> 4) << 24);
 
 // Q slot i = 2 * buffer + query tile; the unit with ordinal k (per pair) uses
-// buffer k & 1.  With kPair the three Q tiles rotate.
+// buffer k & 1.  (kPair: stream s has Q slot s.)
 template <bool kPair>
 __device__ __forceinline__ int q_slot_of(int k, int s) {
-  return kPair ? (2 * k + s) % 3 : 2 * (k & 1) + s;
+  return kPair ? s : 2 * (k & 1) + s;
 }
 template <int kGroups>
 struct Bars {
@@ -208,17 +209,21 @@ struct Bars {
 // its query block, the shared prefix's tiles and then the document's.
 constexpr int kWalkDoc = 0, kWalkList = 1, kWalkPrefix = 2;
 
-// kPair (list walk, query blocks of 256 rows): a unit is two segments of up to
-// 256 rows, each with a walk of its own -- two query blocks with different
-// lists, of any documents and heads.  Query tile s of both CTAs (rows q0 + 128
-// rank + i) belongs to segment s.  The two run in lockstep: a unit has as many
-// steps as the longer list, the other one's last steps are masked tiles.  Every
-// step needs a K and a V tile per query tile, twice the L2 traffic per MMA of
-// the shared walk, and two groups of the ring, so the ring has eight slots (the
-// fourth group is what lets a group be loaded a whole step ahead of its use) at
-// the cost of the fourth Q tile.  Group 0 holds both query tiles' first K tiles;
-// group 1 + 2 t + s holds V(t) and K(t + 1) of query tile s, t counting the
-// pair's steps.
+// kPair (list walk, query blocks of 256 rows): a CTA pair runs two streams of
+// segments of up to 256 rows, each with walks of its own -- query blocks with
+// different lists, of any documents and heads.  Query tile s of both CTAs (rows
+// q0 + 128 rank + i) belongs to stream s.  The streams share nothing but the
+// tensor cores: the issuer takes whichever stream's next P is ready, and stream
+// 1 begins half a segment after stream 0, so that one stream's segment boundary
+// (the pipeline running empty, the epilogue, the next Q and first softmax) falls
+// into the middle of the other's segment.  Every step needs a K and a V tile per
+// query tile, twice the L2 traffic per MMA of a shared walk, and each stream has
+// two groups of the ring: group n of stream s, ring slots 4 s + 2 (n & 1) and the
+// one after it, holds V(n - 1) and K(n), n counting the stream's steps.  A Q
+// slot is free once its segment's last QK is done, a step before the segment
+// ends, so one per stream is enough; O rows are stored directly.
+// Warp 9 loads stream 0 and warp 10 stream 1: lane 0 Q, K and V in the order the
+// stream needs them, lane 1 reports each Q tile landed.
 
 // What a walk needs besides the unit.
 template <int kWalk>
@@ -255,7 +260,6 @@ __device__ __forceinline__ int32_t tile_row(const UnitGeom& g, int s, uint32_t r
 // second half) visits: piece i of m takes [n i / m, n (i + 1) / m) of the n.
 __device__ __forceinline__ int64_t list_range(const int4& x, const Walk<kWalkList>& walk, int32_t* lo, int32_t* hi) {
   *lo = *hi = 0;
-  if (x.y < 0) return 0;  // no segment
   const int64_t block = (int64_t)x.x * walk.blocks + x.y;
   const uint32_t i = (uint32_t)x.z & 0xffffu, m = (uint32_t)x.z >> 16;
   const uint64_t n = (uint64_t)min(max(__ldg(walk.cnt + block), 0), walk.cap);
@@ -264,12 +268,10 @@ __device__ __forceinline__ int64_t list_range(const int4& x, const Walk<kWalkLis
   return block * walk.cap;
 }
 
-// Unit u (kPair: its segment s).
-template <int kWalk, bool kPair = false>
-__device__ __forceinline__ UnitGeom unit_geom(const WorkUnit* units, int u, const Walk<kWalk>& walk, int s = 0) {
-  const int r = kPair ? 2 * u + s : u;
-  const int4 w = __ldg(reinterpret_cast<const int4*>(units) + 2 * r);
-  const int4 x = __ldg(reinterpret_cast<const int4*>(units) + 2 * r + 1);
+template <int kWalk>
+__device__ __forceinline__ UnitGeom unit_geom(const WorkUnit* units, int u, const Walk<kWalk>& walk) {
+  const int4 w = __ldg(reinterpret_cast<const int4*>(units) + 2 * u);
+  const int4 x = __ldg(reinterpret_cast<const int4*>(units) + 2 * u + 1);
   UnitGeom g;
   g.list = nullptr;
   g.n = 0;
@@ -292,7 +294,7 @@ __device__ __forceinline__ UnitGeom unit_geom(const WorkUnit* units, int u, cons
     g.head = x.x;
     g.part = x.w;
     g.v_off = 0;
-    g.n_st = kPair || (w.x + 2 * kTileRows < w.y) ? 2 : 1;
+    g.n_st = (w.x + 2 * kTileRows < w.y) ? 2 : 1;
     if constexpr (kWalk == kWalkPrefix) {
       g.lo = x.y;
       g.hi = x.z;
@@ -302,14 +304,8 @@ __device__ __forceinline__ UnitGeom unit_geom(const WorkUnit* units, int u, cons
       const int64_t at = list_range(x, walk, &lo, &hi);
       g.n = hi - lo;
       if (g.n > 0) g.list = walk.idx + at + lo;
-      int32_t steps = g.n;
-      if constexpr (kPair) {
-        const int4 y = __ldg(reinterpret_cast<const int4*>(units) + 2 * (2 * u + 1 - s) + 1);
-        list_range(y, walk, &lo, &hi);
-        steps = max(steps, hi - lo);
-      }
       g.lo = 0;
-      g.hi = max(steps, 1);  // nothing listed: one fully masked tile
+      g.hi = max(g.n, 1);  // nothing listed: one fully masked tile
     }
   }
   return g;
@@ -673,8 +669,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t lane = threadIdx.x & 31;
   const uint32_t rank = dev::cluster_ctarank();   // 0: issues the pair's MMAs
   const int pair = (int)(blockIdx.x >> 1);
-  // this pair's segments, in order
-  const int u_begin = __ldg(a.unit_off + pair), u_end = __ldg(a.unit_off + pair + 1);
+  // this pair's segments, in order (kPair: stream s's first and last in unit_off[4 pair + 2 s] and after it)
+  const int u_begin = kPair ? 0 : __ldg(a.unit_off + pair), u_end = kPair ? 0 : __ldg(a.unit_off + pair + 1);
+  const auto stream_begin = [&](int s) { return __ldg(a.unit_off + 4 * pair + 2 * s); };
+  const auto stream_end = [&](int s) { return __ldg(a.unit_off + 4 * pair + 2 * s + 1); };
+  volatile int* const steps_of = reinterpret_cast<volatile int*>(smem + C::SmemSteps);  // kPair: [s][ordinal & 3]
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -721,9 +720,84 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   dev::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == kTmaWarp) {
+  if (kPair && (warp == kTmaWarp || warp == kQWarp)) {
+    // ------------------------------------------- kPair: a stream's loads ----
+    if constexpr (kPair) {
+      const int st = warp == kQWarp ? 1 : 0;
+      const int ub = stream_begin(st), ue = stream_end(st);
+      if (lane == 0) {
+        const uint64_t pol_q = dev::policy_evict_first(), pol_kv = dev::policy_evict_last();
+        bool ok = true;
+        uint32_t n = 0;      // groups loaded
+        int loaded_q = 0;
+        int4 entry = {};     // of the tile whose K was sent last
+        for (int u = ub; ok && u < ue; ++u) {
+          const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
+          // Q: free since the last QK of the segment before (whose last group,
+          // with this segment's first K, is on its way)
+          ok = dev::mbar_wait(bars.q_empty(st), ((u - ub) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
+          if (!ok) break;
+          steps_of[4 * st + ((u - ub) & 3)] = g.hi;  // (the issuer reads it after Q-ready)
+          const uint32_t dst = sbase + C::SmemQ + st * C::QTileBytes;
+          const int32_t row = tile_row<kPair>(g, st, rank);
+          dev::mbar_arrive_expect_tx(bars.q_full(st), C::QTileBytes);
+          dev::tma_load_2d(dst, &tm_q, bars.q_full(st), g.head * 128, row, pol_q);
+          dev::tma_load_2d(dst + kQHalfBytes, &tm_q, bars.q_full(st), g.head * 128 + 64, row, pol_q);
+          ++loaded_q;
+          if (u == ub) {
+            ok = dev::mbar_wait(bars.kv_empty(2 * st), 1, abort_flag, a.err, kTimeoutNs);
+            if (!ok) break;
+            entry = walk_entry<kWalk>(g, 0, walk);
+            dev::mbar_arrive_expect_tx(bars.kv_full(2 * st), C::SlotBytes);
+            load_k_half<kFp8>(sbase + C::SmemKV + (4 * st + 1) * C::SlotBytes, &tm_k, bars.kv_full(2 * st), g.head,
+                              key_tile<kWalk>(g, 0, entry, walk).row, rank, pol_kv);
+            n = 1;
+          }
+          for (int j = 0; ok && j < g.hi; ++j) {
+            const KeyTile vt = key_tile<kWalk>(g, j, entry, walk);
+            KeyTile kt = vt;
+            int k_head = g.head;
+            const bool has_k = j + 1 < g.hi || u + 1 < ue;
+            if (j + 1 < g.hi) {
+              entry = walk_entry<kWalk>(g, j + 1, walk);
+              kt = key_tile<kWalk>(g, j + 1, entry, walk);
+            } else if (has_k) {
+              const UnitGeom gn = unit_geom<kWalk>(a.units, u + 1, walk);
+              entry = walk_entry<kWalk>(gn, 0, walk);
+              kt = key_tile<kWalk>(gn, 0, entry, walk);
+              k_head = gn.head;
+            }
+            if (vt.bad && rank == 0) atomicExch(a.err, kErrBlockIndex);
+            const uint32_t b = 2 * st + (n & 1);
+            ok = dev::mbar_wait(bars.kv_empty(b), ((n >> 1) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
+            if (!ok) break;
+            const uint32_t slot = sbase + C::SmemKV + (4 * st + 2 * (n & 1)) * C::SlotBytes;
+            dev::mbar_arrive_expect_tx(bars.kv_full(b), has_k ? 2 * C::SlotBytes : C::SlotBytes);
+            load_v_half<kFp8>(slot, &tm_v, bars.kv_full(b), g.head, vt.row, rank, pol_kv);
+            if (has_k) load_k_half<kFp8>(slot + C::SlotBytes, &tm_k, bars.kv_full(b), k_head, kt.row, rank, pol_kv);
+            ++n;
+          }
+        }
+        if (!ok) {  // drain: wait (bounded) for the copies on their way
+          for (uint32_t x = 1; x <= 2 && x <= n; ++x)
+            dev::mbar_wait_bounded(bars.kv_full(2 * st + ((n - x) & 1)), ((n - x) >> 1) & 1, nullptr, nullptr, kTimeoutNs);
+          if (loaded_q) dev::mbar_wait_bounded(bars.q_full(st), (loaded_q - 1) & 1, nullptr, nullptr, kTimeoutNs);
+        }
+      } else if (lane == 1) {
+        // Q-ready counts one arrival per CTA; before the first one, the stream's
+        // first K tile must have landed too
+        bool ok = true;
+        for (int u = ub; ok && u < ue; ++u) {
+          ok = dev::mbar_wait(bars.q_full(st), (u - ub) & 1, abort_flag, a.err, kTimeoutNs);
+          if (ok && u == ub) ok = dev::mbar_wait(bars.kv_full(2 * st), 0, abort_flag, a.err, kTimeoutNs);
+          if (ok) dev::mbar_arrive_cluster(dev::mapa_shared(bars.q_ready(st), 0));
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp == kTmaWarp) {
     // ------------------------------------------------------ TMA producer ----
-    if (!kFp8 && !kPair && lane == 1) {
+    if (!kFp8 && lane == 1) {
       // bf16 O stores: as the four softmax warps of a query tile finish a
       // unit's epilogue, send the rows they staged in its Q slot (every warp
       // whose 32 rows lie in the document) with TMA tile stores, wait until
@@ -732,7 +806,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       int k = 0;
       for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-        const UnitGeom g = unit_geom<kWalk, kPair>(a.units, u, walk);
+        const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
 #pragma unroll 1
         for (int s = 0; s < 2 && s < g.n_st; ++s) {
           const int i = q_slot_of<kPair>(k, s);
@@ -793,59 +867,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if constexpr (kWalk == kWalkPrefix) return t.prefix ? &walk.tm_v : &tm_v;
         return &tm_v;
       };
-      if constexpr (kPair) {
-        // group 0: both query tiles' first K tiles; then, per step and query tile,
-        // a group of its V tile and its next K tile (see kPair)
-        int k = 0;
-        int4 next[2] = {};  // entries of the tiles whose K was sent last
-        for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-          const UnitGeom g[2] = {unit_geom<kWalk, kPair>(a.units, u, walk, 0), unit_geom<kWalk, kPair>(a.units, u, walk, 1)};
-          const bool has_next = u + 1 < u_end;
-          if (k == 0) {
-            ok = dev::mbar_wait(bars.kv_empty(0), 1, abort_flag, a.err, kTimeoutNs);
-            if (!ok) break;
-            dev::mbar_arrive_expect_tx(bars.kv_full(0), 2 * C::SlotBytes);
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              next[s] = walk_entry<kWalk>(g[s], 0, walk);
-              const KeyTile t = key_tile<kWalk>(g[s], 0, next[s], walk);
-              load_k_half<kFp8>(sbase + C::SmemKV + s * C::SlotBytes, &tm_k, bars.kv_full(0), g[s].head, t.row, rank, pol_kv);
-            }
-            grp = 1;
-          }
-          for (int j = 0; ok && j < g[0].hi; ++j) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              const KeyTile vt = key_tile<kWalk>(g[s], j, next[s], walk);
-              KeyTile kt = vt;
-              int k_head = g[s].head;
-              const bool has_k = j + 1 < g[s].hi || has_next;
-              if (j + 1 < g[s].hi) {
-                next[s] = walk_entry<kWalk>(g[s], j + 1, walk);
-                kt = key_tile<kWalk>(g[s], j + 1, next[s], walk);
-              } else if (has_next) {
-                const UnitGeom n = unit_geom<kWalk, kPair>(a.units, u + 1, walk, s);
-                next[s] = walk_entry<kWalk>(n, 0, walk);
-                kt = key_tile<kWalk>(n, 0, next[s], walk);
-                k_head = n.head;
-              }
-              if (vt.bad && rank == 0) atomicExch(a.err, kErrBlockIndex);
-              const uint32_t b = grp % kGroups;
-              ok = dev::mbar_wait(bars.kv_empty(b), ((grp / kGroups) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
-              if (!ok) break;
-              const uint32_t slot = sbase + C::SmemKV + ((2 * grp) % kSlots) * C::SlotBytes;
-              dev::mbar_arrive_expect_tx(bars.kv_full(b), has_k ? 2 * C::SlotBytes : C::SlotBytes);
-              load_v_half<kFp8>(slot, &tm_v, bars.kv_full(b), g[s].head, vt.row, rank, pol_kv);
-              if (has_k) load_k_half<kFp8>(slot + C::SlotBytes, &tm_k, bars.kv_full(b), k_head, kt.row, rank, pol_kv);
-              ++grp;
-            }
-          }
-        }
-      } else {
       int k = 0;
       KeyTile kt;  // the tile whose K was sent last (dense: only its row is used)
       for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-        const UnitGeom g = unit_geom<kWalk, kPair>(a.units, u, walk);
+        const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
         const bool has_next = u + 1 < u_end;
         // Key/value groups: group 0 is the first unit's first K tile (ring slot
         // 0); group n >= 1 is V(j) with the next K tile -- K(j+1), or the next
@@ -877,7 +902,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (vt.bad && rank == 0) atomicExch(a.err, kErrBlockIndex);
           }
           if (!has_k && has_next) {
-            const UnitGeom n = unit_geom<kWalk, kPair>(a.units, u + 1, walk);
+            const UnitGeom n = unit_geom<kWalk>(a.units, u + 1, walk);
             has_k = true;
             k_head = n.head;
             if constexpr (kWalk == kWalkDoc)
@@ -906,9 +931,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ++grp;
           // the next unit's Q tiles, behind this unit's first group
           if constexpr (kFp8)
-            if (j == g.lo && has_next) load_q(unit_geom<kWalk, kPair>(a.units, u + 1, walk), k + 1);
+            if (j == g.lo && has_next) load_q(unit_geom<kWalk>(a.units, u + 1, walk), k + 1);
         }
-      }
       }
       if (!ok) {
         // drain: wait (bounded) for every copy this thread issued into the ring and Q
@@ -934,7 +958,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool issued = false;
         int k = 0;
         for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-          const UnitGeom g = unit_geom<kWalk, kPair>(a.units, u, walk);
+          const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
           const uint32_t qb = 2 * (k & 1);
           // Q tiles of this unit, prepared in both CTAs (and, for the first
           // unit, the first K group landed in both)
@@ -989,6 +1013,98 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           dev::mbar_wait_bounded(bars.drain(), 0, nullptr, nullptr, kTimeoutNs);
         }
       }
+    } else if constexpr (kPair) {
+      if (rank == 0) {
+        // Two streams: the whole warp runs the loop, one lane polls the stream's
+        // next barrier without blocking, and the warp takes the stream if it is
+        // ready.  Per stream: its segments' steps are awaited as in the other
+        // issuer, so the order of a stream's MMAs (PV, then the next QK into the
+        // same columns) is the same.
+        int u[2], ue[2], hi[2] = {0, 0}, j[2] = {0, 0}, h[2] = {0, 0};
+        uint32_t t[2] = {0, 0}, k[2] = {0, 0};  // steps and segments of the stream so far
+        bool first[2] = {true, true};           // the next barrier is Q-ready
+        bool ok = true, issued = false;
+        for (int s = 0; s < 2; ++s) {
+          u[s] = stream_begin(s);
+          ue[s] = stream_end(s);
+        }
+        bool hold = ue[0] - u[0] > 1;           // stream 1 waits for the middle of stream 0's first segment
+        uint64_t since = 0;                     // when nothing has been ready from
+        uint32_t idle = 0;
+        while (ok && (u[0] < ue[0] || u[1] < ue[1])) {
+          bool any = false;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (u[s] >= ue[s] || (s == 1 && hold)) continue;
+            const uint32_t bar = first[s] ? bars.q_ready(s) : (h[s] ? bars.p_ready(s, 1) : bars.p_ready(s, 0));
+            const uint32_t par = (first[s] ? k[s] : t[s]) & 1;
+            bool good = true;
+            if (lane == 0) good = dev::mbar_test_wait(bar, par);
+            good = __shfl_sync(0xffffffffu, good, 0);
+            if (!good) continue;
+            any = true;
+            dev::tc_fence_after();
+            const uint32_t d = tmem + s * 128, qa = sbase + C::SmemQ + s * C::QTileBytes;
+            // K(t) lies in group t, V(t) and K(t + 1) in group t + 1
+            const uint32_t ring = sbase + C::SmemKV + 4 * s * C::SlotBytes;
+            if (first[s]) {
+              const uint32_t kb = ring + (2 * (t[s] & 1) + 1) * C::SlotBytes;
+              hi[s] = steps_of[4 * s + (k[s] & 3)];
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                issue_qk(d + 64 * x, qa, kb + x * kHalfKeyRowsBytes);
+                commit_pair_elect(bars.s_ready(s, x));
+              }
+              if (hi[s] == 1) commit_pair_elect(bars.q_empty(s));
+              ++k[s];
+              first[s] = false;
+              issued = true;
+            } else {
+              const uint32_t vb = ring + 2 * ((t[s] + 1) & 1) * C::SlotBytes;
+              issue_pv(tmem + 256 + s * 128, d + 64 * h[s], vb + 4096 * h[s], j[s] > 0 || h[s] == 1);
+              if (j[s] + 1 < hi[s]) {
+                issue_qk(d + 64 * h[s], qa, vb + C::SlotBytes + h[s] * kHalfKeyRowsBytes);
+                commit_pair_elect(h[s] ? bars.s_ready(s, 1) : bars.s_ready(s, 0));
+                if (h[s] == 1 && j[s] + 2 == hi[s]) commit_pair_elect(bars.q_empty(s));
+              } else {
+                commit_pair_elect(h[s] ? bars.pv_done(s, 1) : bars.pv_done(s, 0));
+              }
+              if (h[s] == 1) {
+                ++t[s];
+                if (++j[s] == hi[s]) {
+                  j[s] = 0;
+                  ++u[s];
+                  first[s] = true;
+                }
+              }
+              h[s] ^= 1;
+            }
+          }
+          hold = hold && u[0] < ue[0] && (t[0] == 0 || 2 * t[0] < (uint32_t)hi[0]);
+          if (any) {
+            idle = 0;
+          } else if ((++idle & 63u) == 0) {  // bounded: two seconds of nothing, or another thread's abort
+            const uint64_t now = dev::globaltimer_ns();
+            if (idle == 64) since = now;
+            bool stop = false;
+            if (lane == 0) {
+              stop = *abort_flag != 0;
+              if (!stop && now - since > kTimeoutNs) {
+                *abort_flag = 1;
+                atomicExch(a.err, kErrTimeout);
+                stop = true;
+              }
+            }
+            ok = !__shfl_sync(0xffffffffu, stop, 0);
+          }
+        }
+        if (!ok && issued) {
+          // drain: every MMA issued so far must finish before TMEM is freed
+          __syncwarp();
+          commit_pair_local_elect(bars.drain());
+          dev::mbar_wait_bounded(bars.drain(), 0, nullptr, nullptr, kTimeoutNs);
+        }
+      }
     } else if (rank == 0) {
     // bf16: the whole warp runs the loop (its values stay warp-uniform); every
     // tcgen05 MMA and commit is issued by one elected lane.
@@ -1000,14 +1116,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool issued = false;
       int k = 0;
       // QK of half h of the key tile in ring slot ks for query tile s (Q slot qs)
-      // (last: kPair, the segment's last QK: its Q slot is free once it completes)
-      auto qk_half = [&](int s, uint32_t qs, uint32_t ks, int h, bool last) {
+      auto qk_half = [&](int s, uint32_t qs, uint32_t ks, int h) {
         const uint32_t d = tmem + s * 128 + h * 64;
         const uint32_t qa = sbase + C::SmemQ + qs * C::QTileBytes;
         const uint32_t kb = sbase + C::SmemKV + ks * C::SlotBytes + h * kHalfKeyRowsBytes;
         issue_qk(d, qa, kb);
         commit_pair_elect(bars.s_ready(s, h));
-        if (kPair && last && h == 1) commit_pair_elect(bars.q_empty(qs));
       };
       // PV of half h of the key tile whose V is in ring slot vs, query tile s
       auto pv_half = [&](int s, uint32_t vs, int h, bool acc) {
@@ -1033,7 +1147,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       // The first QK (half h) of query tile s of a unit: Q slot qs (its readiness
       // in both CTAs is awaited before half 0), K in ring slot ks.
-      auto first_qk = [&](const UnitGeom& gg, uint32_t qs, uint32_t ks, int s, int h) {
+      auto first_qk = [&](uint32_t qs, uint32_t ks, int s, int h) {
         if (h == 0) {
           ok = __all_sync(0xffffffffu,
                           dev::mbar_wait(bars.q_ready(qs), q_use[qs] & 1, abort_flag, a.err, kTimeoutNs));
@@ -1041,36 +1155,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!ok) return;
           dev::tc_fence_after();
         }
-        qk_half(s, qs, ks, h, gg.hi - gg.lo == 1);
+        qk_half(s, qs, ks, h);
         issued = true;
       };
-      // Ring slots of query tile s's V and next K in this step (kPair: group
-      // 1 + 2 t + s, slots 2 (1 + 2 t + s) and the one after it, mod 8)
-      auto v_at = [&](int s) { return kPair ? (vslot + 2 * s) % kSlots : vslot; };
-      auto k_at = [&](int s) { return kPair ? (vslot + 2 * s + 1) % kSlots : kslot; };
       auto advance = [&]() {
-        if constexpr (kPair) {
-          vslot = (vslot + 4) % kSlots;
-        } else {
-          vslot = vslot + 2 >= (uint32_t)kSlots ? vslot + 2 - kSlots : vslot + 2;
-          kslot = kslot + 2 >= (uint32_t)kSlots ? kslot + 2 - kSlots : kslot + 2;
-        }
+        vslot = vslot + 2 >= (uint32_t)kSlots ? vslot + 2 - kSlots : vslot + 2;
+        kslot = kslot + 2 >= (uint32_t)kSlots ? kslot + 2 - kSlots : kslot + 2;
       };
-      if constexpr (kPair) vslot = 2;
       for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-        const UnitGeom g = unit_geom<kWalk, kPair>(a.units, u, walk);
+        const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
         const uint32_t q_at[2] = {(uint32_t)q_slot_of<kPair>(k, 0), (uint32_t)q_slot_of<kPair>(k, 1)};
         if (k == 0) {
-          // the pair's first unit: its first K tile is group 0 (ring slot 0;
-          // kPair: slot s for query tile s), and Q-ready also covers that group's
-          // arrival in both CTAs
-          if constexpr (kPair) {
-            for (int s = 0; ok && s < 2; ++s)
-              for (int h = 0; ok && h < 2; ++h) first_qk(g, q_at[s], s, s, h);
-          } else {
-            for (int h = 0; ok && h < 2; ++h)
-              for (int s = 0; ok && s < g.n_st; ++s) first_qk(g, q_at[s], 0, s, h);
-          }
+          // the pair's first unit: its first K tile is group 0 (ring slot 0),
+          // and Q-ready also covers that group's arrival in both CTAs
+          for (int h = 0; ok && h < 2; ++h)
+            for (int s = 0; ok && s < g.n_st; ++s) first_qk(q_at[s], 0, s, h);
           if (!ok) break;
         }
         // Per key tile j and half h, for each query tile s: wait for P(s, j, h),
@@ -1083,7 +1182,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // unit's last query tile sees S of half 1, so that QK comes after
         // every PV of this unit.
         const bool has_next = u + 1 < u_end;
-        const UnitGeom gn = unit_geom<kWalk, kPair>(a.units, has_next ? u + 1 : u, walk);
+        const UnitGeom gn = unit_geom<kWalk>(a.units, has_next ? u + 1 : u, walk);
         const bool two = g.n_st == 2;
         // steady state: key tiles with a next key tile in this unit
         // (prefix walk: those before the own tiles of a segment over several
@@ -1107,8 +1206,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (!ok) break;
               ++p_it[s][h];
               dev::tc_fence_after();
-              pv_half(s, v_at(s), h, acc0 || h == 1);
-              qk_half(s, q_at[s], k_at(s), h, j + 2 == g.hi);
+              pv_half(s, vslot, h, acc0 || h == 1);
+              qk_half(s, q_at[s], kslot, h);
             }
             if (!ok) break;
           }
@@ -1128,8 +1227,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 ++p_it[s][h];
                 dev::tc_fence_after();
-                pv_half_skip(s, v_at(s), h);
-                qk_half(s, q_at[s], k_at(s), h, j + 2 == g.hi);
+                pv_half_skip(s, vslot, h);
+                qk_half(s, q_at[s], kslot, h);
               }
               if (!ok) break;
             }
@@ -1152,20 +1251,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               ++p_it[s][h];
               dev::tc_fence_after();
               if (kWalk == kWalkPrefix && g.hi > j_own)
-                pv_half_skip(s, v_at(s), h);
+                pv_half_skip(s, vslot, h);
               else
-                pv_half(s, v_at(s), h, acc0 || h == 1);
+                pv_half(s, vslot, h, acc0 || h == 1);
               commit_pair_elect(bars.pv_done(s, h));
             }
           }
           if (has_next) {
-            if constexpr (kPair) {
-              for (int s = 0; ok && s < 2; ++s)
-                for (int h = 0; ok && h < 2; ++h) first_qk(gn, q_slot_of<kPair>(k + 1, s), k_at(s), s, h);
-            } else {
-              for (int h = 0; ok && h < 2; ++h)
-                for (int s = 0; ok && s < gn.n_st; ++s) first_qk(gn, q_slot_of<kPair>(k + 1, s), kslot, s, h);
-            }
+            for (int h = 0; ok && h < 2; ++h)
+              for (int s = 0; ok && s < gn.n_st; ++s) first_qk(q_slot_of<kPair>(k + 1, s), kslot, s, h);
           }
           advance();
         }
@@ -1189,11 +1283,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint64_t pol_q = dev::policy_evict_first();
     int k = 0;
     for (int u = u_begin; ok && u < u_end; ++u, ++k) {
-      UnitGeom g = unit_geom<kWalk, kPair>(a.units, u, walk);
+      const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
 #pragma unroll 1
       for (int s = 0; s < 2 && s < g.n_st; ++s) {
         const int i = q_slot_of<kPair>(k, s);
-        if (kPair && s == 1) g = unit_geom<kWalk, kPair>(a.units, u, walk, 1);
         bool good = true;
         if constexpr (!kFp8) {
           // bf16: this warp loads the tile once its slot is free (the
@@ -1262,12 +1355,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __nv_bfloat16* og = static_cast<__nv_bfloat16*>(a.o);
     // 32-byte output stores when every row start is 32-byte aligned
     const bool o_wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0 && (a.o_stride & 15) == 0;
-    for (int u = u_begin; ok && u < u_end; ++u) {
-      const UnitGeom g = unit_geom<kWalk, kPair>(a.units, u, walk, kPair ? st : 0);
+    const int us = kPair ? stream_begin(st) : u_begin, ue = kPair ? stream_end(st) : u_end;
+    for (int u = us; ok && u < ue; ++u) {
+      const UnitGeom g = unit_geom<kWalk>(a.units, u, walk);
       const uint32_t t_unit = t0;
       t0 += g.hi - g.lo;
-      if (st >= g.n_st) continue;
-      const uint32_t q_slot = q_slot_of<kPair>(u - u_begin, st);  // this unit's Q tile of this query tile
+      if (!kPair && st >= g.n_st) continue;
+      const uint32_t q_slot = q_slot_of<kPair>(u - us, st);  // this unit's Q tile of this query tile
       // ring bookkeeping by one lane of one warp per CTA
       // (kPair: each query tile has groups of its own)
       const bool releases = lead_lane && (kPair || st == g.n_st - 1);
@@ -1392,8 +1486,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           int rem = tile.rem;
           if (kWalk == kWalkPrefix && g.n > 0 && ((int32_t)row_in_unit < tile.lo || (int32_t)row_in_unit >= tile.hi)) rem = 0;
           // the group holding V(t) and K(t + 1), and the one holding K(t)
-          const uint32_t grp = kPair ? 2 * t + 1 + st : t + 1, grp_k = kPair ? grp - 2 : t;
-          const uint32_t kv_bar = bars.kv_full(grp % kGroups), kv_par = (grp / kGroups) & 1;
+          const uint32_t grp = kPair ? 2 * st + ((t + 1) & 1) : (t + 1) % kGroups;
+          const uint32_t grp_k = kPair ? 2 * st + (t & 1) : t % kGroups;
+          const uint32_t kv_bar = bars.kv_full(grp), kv_par = ((t + 1) / (kPair ? 2 : kGroups)) & 1;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             // (no lane leaves here: a failed wait only clears ok, and the
@@ -1402,8 +1497,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ++s_it[h];
             // S half 1 of the last query tile is ready: every MMA before its QK is
             // done, so the group holding K(t) (and V(t-1)) is free in this CTA
-            // (kPair: group 0 holds both query tiles' first K; tile 1's QK comes last)
-            if (releases && h == 1 && !(kPair && t == 0 && st == 0)) dev::mbar_arrive(bars.kv_empty(grp_k % kGroups));
+            if (releases && h == 1) dev::mbar_arrive(bars.kv_empty(grp_k));
             __syncwarp();  // lanes leave the wait separately; the TMEM loads are warp-collective
             dev::tc_fence_after();
             const uint32_t t_sh = t_s + 64 * h;  // this half's S, then its P
@@ -1491,7 +1585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               // them, by the warp that reports the group landed.
               if (h == 0 && (kPair ? (warp & 3) == 0 : warp == 0) && rem_tile < kTileRows) {
                 ok = dev::mbar_wait(kv_bar, kv_par, abort_flag, a.err, kTimeoutNs) && ok;
-                const uint32_t v_slot = sbase + C::SmemKV + ((kPair ? 2 * grp : 2 * grp - 1) % kSlots) * C::SlotBytes;
+                const uint32_t v_slot = sbase + C::SmemKV + (kPair ? 2 * grp : (2 * t + 1) % kSlots) * C::SlotBytes;
                 if (ok)
                   for (uint32_t b = (uint32_t)max(rem_tile, 0) * 128u + lane * 16u; b < C::SlotBytes; b += 512u)
                     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v_slot + b), "r"(0u) : "memory");

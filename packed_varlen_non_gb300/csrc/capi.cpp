@@ -776,7 +776,7 @@ static WalkArgs walk_args(const WalkPlan& w) {
   WalkArgs x{};
   x.joins = w.d_joins;
   x.n_joins = (int32_t)w.joins.size();
-  x.pair = w.segs == 2;
+  x.pair = w.streams == 2;
   x.rows = w.rows;
   return x;
 }
@@ -899,12 +899,14 @@ h3attn_status h3attn_walk_list_host(int32_t kind, const int32_t* cu_seqlens, int
     const std::string why = kind == 0 ? build_list_walk(cu_seqlens, n_docs, num_heads, p0, p1, n_pairs, w)
                                       : build_prefix_walk(cu_seqlens, n_docs, num_heads, p0, n_pairs, w);
     if (!why.empty()) return fail(H3ATTN_EINVAL, "%s", why.c_str());
-    // segments, without the empty ones that fill up a unit
+    // pair by pair (of two streams, the first one's segments before the second's)
     std::vector<WalkUnit> segs;
     std::vector<int32_t> off(1, 0);
     for (int32_t p = 0; p < w.n_pairs; ++p) {
-      for (int32_t i = w.unit_off[p] * w.segs; i < w.unit_off[p + 1] * w.segs; ++i)
-        if (w.units[i].q_row0 < w.units[i].q_end) segs.push_back(w.units[i]);
+      for (int x = 0; x < w.streams; ++x) {
+        const int32_t* r = w.streams == 1 ? &w.unit_off[p] : &w.unit_off[4 * p + 2 * x];
+        segs.insert(segs.end(), w.units.begin() + r[0], w.units.begin() + r[1]);
+      }
       off.push_back((int32_t)segs.size());
     }
     *n_units = (int64_t)segs.size();

@@ -140,9 +140,9 @@ constexpr int kRowsMax = 64;
 struct WalkPlan {
   bool set = false;
   bool rows = false;                   // prefix walk of a few short documents: unit_off is not used
-  int segs = 1;                        // segments of a unit: 2 run side by side on a CTA pair
-  std::vector<WalkUnit> units;         // segments, unit by unit, grouped by CTA pair (q_row0 = q_end: none)
-  std::vector<int32_t> unit_off;       // [n_pairs + 1], in units
+  int streams = 1;                     // streams of segments that a CTA pair runs side by side
+  std::vector<WalkUnit> units;         // grouped by CTA pair
+  std::vector<int32_t> unit_off;       // [n_pairs + 1]; two streams: [n_pairs][2] (first, end)
   int32_t n_pairs = 0;
   std::vector<OwnTile> own;            // prefix walk
   std::vector<JoinRec> joins;
@@ -352,7 +352,7 @@ cudaError_t launch_forward_fp8(const ForwardArgs& a, int device, int num_sms, cu
 struct WalkArgs {
   const JoinRec* joins;
   int32_t n_joins;
-  bool pair;                   // units of two segments
+  bool pair;                   // two streams of segments on a CTA pair
   bool rows;                   // attn_rows.cu's segments
   // list walk
   const int32_t* block_idx;    // [H, n_q_blocks, max_blocks]

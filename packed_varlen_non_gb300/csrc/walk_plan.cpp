@@ -59,17 +59,8 @@ constexpr double kJoinStart = 2.5;
 
 int64_t piece_cost(int32_t tiles, bool partial) { return (int64_t)tiles + 3 + (partial ? 1 : 0); }
 
-// Costs of units of `segs` consecutive pieces that run in lockstep: the largest's.
-std::vector<int64_t> unit_costs(const std::vector<int64_t>& pieces, int segs) {
-  std::vector<int64_t> out;
-  out.reserve((pieces.size() + segs - 1) / segs);
-  for (size_t i = 0; i < pieces.size(); i += segs)
-    out.push_back(*std::max_element(pieces.begin() + i, pieces.begin() + std::min(pieces.size(), i + segs)));
-  return out;
-}
-
 // Splits a tail of the items (in list order) so that the pairs finish together.
-void balance(std::vector<Item>& items, int G, int segs) {
+void balance(std::vector<Item>& items, int G) {
   const size_t U = items.size();
   std::vector<int32_t> pair_of, heap(G);
   std::vector<int64_t> load(G), cost;
@@ -87,7 +78,6 @@ void balance(std::vector<Item>& items, int G, int segs) {
         cost.push_back(piece_cost(bound(items[i], c + 1, n) - bound(items[i], c, n), partial));
       if (partial) rows += (int64_t)n * items[i].rows();
     }
-    if (segs > 1) cost = unit_costs(cost, segs);
     pair_of.resize(cost.size());
     assign_pairs(cost.size(), [&](size_t i) { return cost[i]; }, G, pair_of.data(), load.data(), heap.data());
     double score = (double)*std::max_element(load.begin(), load.end());
@@ -99,7 +89,7 @@ void balance(std::vector<Item>& items, int G, int segs) {
     }
   };
   consider(U, 1);
-  const int64_t round = (int64_t)G * segs, full = (int64_t)U / round * round;
+  const int64_t round = G, full = (int64_t)U / round * round;
   for (int64_t back : {(int64_t)0, round / 4, round / 2, round, 2 * round, full}) {
     if (back > full) continue;
     const size_t whole = (size_t)(full - back);
@@ -117,7 +107,6 @@ void balance(std::vector<Item>& items, int G, int segs) {
 template <class Make>
 std::string finish(std::vector<Item>& items, std::vector<Join>& joins, int G, Make make, WalkPlan& w) {
   int64_t rows = 0;
-  const int per = w.segs;
   std::vector<WalkUnit> segs;
   std::vector<int64_t> cost;
   for (Item& it : items) {
@@ -155,24 +144,25 @@ std::string finish(std::vector<Item>& items, std::vector<Join>& joins, int G, Ma
       w.joins.push_back(r);
     }
   }
-  // an odd last unit's second segment: no rows, no list
-  while (segs.size() % per != 0) segs.push_back(WalkUnit{0, 0, 0, 1, 0, -1, 1 << 16, -1});
-  if (per > 1) cost = unit_costs(cost, per);
-  struct Unit {
-    WalkUnit seg[2];
-  };
+  // two streams a pair: twice the bins, the first of every pair before the second
+  const int bins = w.streams * G;
   w.units.resize(segs.size());
-  w.unit_off.assign((size_t)G + 1, 0);
-  std::vector<int32_t> pair_of(cost.size()), heap(G);
-  std::vector<int64_t> load(G);
-  assign_pairs(cost.size(), [&](size_t i) { return cost[i]; }, G, pair_of.data(), load.data(), heap.data());
-  if (per == 1)
-    w.n_pairs =
-        group_by_pair(segs.data(), cost.size(), G, w.units.data(), w.unit_off.data(), pair_of.data(), heap.data());
-  else
-    w.n_pairs = group_by_pair(reinterpret_cast<const Unit*>(segs.data()), cost.size(), G,
-                              reinterpret_cast<Unit*>(w.units.data()), w.unit_off.data(), pair_of.data(), heap.data());
-  w.unit_off.resize((size_t)w.n_pairs + 1);
+  std::vector<int32_t> off((size_t)bins + 1), pair_of(segs.size()), heap(bins);
+  std::vector<int64_t> load(bins);
+  assign_pairs(segs.size(), [&](size_t i) { return cost[i]; }, bins, pair_of.data(), load.data(), heap.data());
+  const int32_t used =
+      group_by_pair(segs.data(), segs.size(), bins, w.units.data(), off.data(), pair_of.data(), heap.data());
+  w.n_pairs = std::min(used, G);
+  w.unit_off.clear();
+  if (w.streams == 1) {
+    w.unit_off.assign(off.begin(), off.begin() + w.n_pairs + 1);
+  } else {
+    for (int32_t p = 0; p < w.n_pairs; ++p)
+      for (int32_t b : {p, p + G}) {
+        w.unit_off.push_back(off[b]);
+        w.unit_off.push_back(off[b + 1]);
+      }
+  }
   if (w.joins.size() >= (size_t(1) << 31)) return "the layout needs 2^31 or more join records";
   return "";
 }
@@ -204,8 +194,8 @@ std::string build_list_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads
         r = end;
       }
   }
-  w.segs = q_block == kUnitRows ? 1 : 2;
-  balance(items, G, w.segs);
+  w.streams = q_block == kUnitRows ? 1 : 2;
+  balance(items, w.streams * G);
   for (Item& it : items) it.pieces = std::min(it.pieces, 65535);  // the field's width
   std::vector<Join> joins;
   return finish(items, joins, G, [](const Item& it, int32_t c) {
@@ -335,7 +325,7 @@ std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_hea
       items.push_back(Item{WalkUnit{q0, q1, own[x].first, -own[x].n, h, 0, t, -1}, t, tp, !own[x].join});
     }
   }
-  balance(items, G, w.segs);
+  balance(items, G);
   return finish(items, joins, G, prefix_piece, w);
 }
 
