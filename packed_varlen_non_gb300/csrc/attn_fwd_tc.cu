@@ -1015,73 +1015,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     } else if constexpr (kPair) {
       if (rank == 0) {
-        // Two streams: the whole warp runs the loop, one lane polls the stream's
-        // next barrier without blocking, and the warp takes the stream if it is
-        // ready.  Per stream: its segments' steps are awaited as in the other
-        // issuer, so the order of a stream's MMAs (PV, then the next QK into the
-        // same columns) is the same.
-        int u[2], ue[2], hi[2] = {0, 0}, j[2] = {0, 0}, h[2] = {0, 0};
+        // Two streams: the whole warp runs the loop; lane s polls stream s's next
+        // barrier without blocking, and the warp serves the streams that are ready.
+        // Per stream, its segments' steps are awaited as in the other issuer, so the
+        // order of a stream's MMAs (PV, then the next QK into the same columns) is
+        // the same.
+        int left[2], hi[2] = {0, 0}, j[2] = {0, 0}, h[2] = {0, 0};  // segments to go; steps, step and half of this one
         uint32_t t[2] = {0, 0}, k[2] = {0, 0};  // steps and segments of the stream so far
         bool first[2] = {true, true};           // the next barrier is Q-ready
         bool ok = true, issued = false;
-        for (int s = 0; s < 2; ++s) {
-          u[s] = stream_begin(s);
-          ue[s] = stream_end(s);
-        }
-        bool hold = ue[0] - u[0] > 1;           // stream 1 waits for the middle of stream 0's first segment
+#pragma unroll
+        for (int s = 0; s < 2; ++s) left[s] = stream_end(s) - stream_begin(s);
+        bool hold = left[0] > 1;                // stream 1 waits for the middle of stream 0's first segment
         uint64_t since = 0;                     // when nothing has been ready from
         uint32_t idle = 0;
-        while (ok && (u[0] < ue[0] || u[1] < ue[1])) {
-          bool any = false;
+        // serves stream s
+        auto serve = [&](const int s) {
+          dev::tc_fence_after();
+          const uint32_t d = tmem + s * 128, qa = sbase + C::SmemQ + s * C::QTileBytes;
+          // K(t) lies in group t, V(t) and K(t + 1) in group t + 1
+          const uint32_t ring = sbase + C::SmemKV + 4 * s * C::SlotBytes;
+          if (first[s]) {
+            const uint32_t kb = ring + (2 * (t[s] & 1) + 1) * C::SlotBytes;
+            hi[s] = steps_of[4 * s + (k[s] & 3)];
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (u[s] >= ue[s] || (s == 1 && hold)) continue;
-            const uint32_t bar = first[s] ? bars.q_ready(s) : (h[s] ? bars.p_ready(s, 1) : bars.p_ready(s, 0));
-            const uint32_t par = (first[s] ? k[s] : t[s]) & 1;
-            bool good = true;
-            if (lane == 0) good = dev::mbar_test_wait(bar, par);
-            good = __shfl_sync(0xffffffffu, good, 0);
-            if (!good) continue;
-            any = true;
-            dev::tc_fence_after();
-            const uint32_t d = tmem + s * 128, qa = sbase + C::SmemQ + s * C::QTileBytes;
-            // K(t) lies in group t, V(t) and K(t + 1) in group t + 1
-            const uint32_t ring = sbase + C::SmemKV + 4 * s * C::SlotBytes;
-            if (first[s]) {
-              const uint32_t kb = ring + (2 * (t[s] & 1) + 1) * C::SlotBytes;
-              hi[s] = steps_of[4 * s + (k[s] & 3)];
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                issue_qk(d + 64 * x, qa, kb + x * kHalfKeyRowsBytes);
-                commit_pair_elect(bars.s_ready(s, x));
-              }
-              if (hi[s] == 1) commit_pair_elect(bars.q_empty(s));
-              ++k[s];
-              first[s] = false;
-              issued = true;
-            } else {
-              const uint32_t vb = ring + 2 * ((t[s] + 1) & 1) * C::SlotBytes;
-              issue_pv(tmem + 256 + s * 128, d + 64 * h[s], vb + 4096 * h[s], j[s] > 0 || h[s] == 1);
-              if (j[s] + 1 < hi[s]) {
-                issue_qk(d + 64 * h[s], qa, vb + C::SlotBytes + h[s] * kHalfKeyRowsBytes);
-                commit_pair_elect(h[s] ? bars.s_ready(s, 1) : bars.s_ready(s, 0));
-                if (h[s] == 1 && j[s] + 2 == hi[s]) commit_pair_elect(bars.q_empty(s));
-              } else {
-                commit_pair_elect(h[s] ? bars.pv_done(s, 1) : bars.pv_done(s, 0));
-              }
-              if (h[s] == 1) {
-                ++t[s];
-                if (++j[s] == hi[s]) {
-                  j[s] = 0;
-                  ++u[s];
-                  first[s] = true;
-                }
-              }
-              h[s] ^= 1;
+            for (int x = 0; x < 2; ++x) {
+              issue_qk(d + 64 * x, qa, kb + x * kHalfKeyRowsBytes);
+              commit_pair_elect(bars.s_ready(s, x));
+            }
+            if (hi[s] == 1) commit_pair_elect(bars.q_empty(s));
+            ++k[s];
+            first[s] = false;
+            issued = true;
+            return;
+          }
+          const uint32_t vb = ring + 2 * ((t[s] + 1) & 1) * C::SlotBytes;
+          issue_pv(tmem + 256 + s * 128, d + 64 * h[s], vb + 4096 * h[s], j[s] > 0 || h[s] == 1);
+          if (j[s] + 1 < hi[s]) {
+            issue_qk(d + 64 * h[s], qa, vb + C::SlotBytes + h[s] * kHalfKeyRowsBytes);
+            commit_pair_elect(bars.s_ready(s, 0) + 8 * h[s]);
+            if (h[s] == 1 && j[s] + 2 == hi[s]) commit_pair_elect(bars.q_empty(s));
+          } else {
+            commit_pair_elect(bars.pv_done(s, 0) + 8 * h[s]);
+          }
+          if (h[s] == 1) {
+            ++t[s];
+            if (++j[s] == hi[s]) {
+              j[s] = 0;
+              --left[s];
+              first[s] = true;
             }
           }
-          hold = hold && u[0] < ue[0] && (t[0] == 0 || 2 * t[0] < (uint32_t)hi[0]);
-          if (any) {
+          h[s] ^= 1;
+        };
+        while (ok && (left[0] > 0 || left[1] > 0)) {
+          bool good = false;
+          if (lane < 2) {
+            const bool one = lane == 1;
+            const bool f = one ? first[1] : first[0];
+            const uint32_t hh = one ? h[1] : h[0], n = f ? (one ? k[1] : k[0]) : (one ? t[1] : t[0]);
+            if ((one ? left[1] : left[0]) > 0 && !(one && hold))
+              good = dev::mbar_test_wait(f ? bars.q_ready((int)lane) : bars.p_ready((int)lane, 0) + 8 * hh, n & 1);
+          }
+          const unsigned ready = __ballot_sync(0xffffffffu, good);
+          if (ready & 1u) serve(0);
+          if (ready & 2u) serve(1);
+          hold = hold && left[0] > 0 && (t[0] == 0 || 2 * t[0] < (uint32_t)hi[0]);
+          if (ready != 0) {
             idle = 0;
           } else if ((++idle & 63u) == 0) {  // bounded: two seconds of nothing, or another thread's abort
             const uint64_t now = dev::globaltimer_ns();
