@@ -1827,12 +1827,12 @@ __device__ __forceinline__ float4 load_bf16x4(const __nv_bfloat16* p) {
                      __uint_as_float(w.y & 0xffff0000u));
 }
 
-constexpr int kAtOnce = 4;
+constexpr int kAtOnce = 8;
 
 // The rows of a record are a block's; parts are read kAtOnce at a time with their
 // maxima and rows together, in one pass with a running maximum, so that a row
 // waits for memory about once.
-__global__ void __launch_bounds__(32 * kJoinRows, 6) attn_join_kernel(JoinArgs a) {
+__global__ void __launch_bounds__(32 * kJoinRows, 4) attn_join_kernel(JoinArgs a) {
   const int lane = threadIdx.x & 31;
   const JoinRec j = a.recs[blockIdx.x];
   const int32_t row = j.row0 + (int32_t)(threadIdx.x >> 5);
@@ -2103,18 +2103,20 @@ cudaError_t launch_forward_list(const ForwardArgs& a, const WalkArgs& w, cudaStr
 }
 
 cudaError_t launch_forward_prefix(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why) {
-  if (w.rows) {
+  if (w.pieces > 0) {
     const RowsArgs r{static_cast<const __nv_bfloat16*>(a.q),
                      static_cast<const __nv_bfloat16*>(w.k_prefix),
                      static_cast<const __nv_bfloat16*>(w.v_prefix),
                      a.qkv_stride,
                      w.prefix_stride,
                      w.prefix_len,
-                     reinterpret_cast<const WalkUnit*>(a.units),
+                     (int32_t)a.S,
+                     (int32_t)(((int64_t)w.prefix_len + kTileRows - 1) / kTileRows),
+                     w.pieces,
                      a.scale_log2,
                      a.part_o,
                      a.part_ml};
-    const cudaError_t e = launch_attn_rows(r, a.n_units, a.S < kRowsTile ? (int)a.S : kRowsTile, stream);
+    const cudaError_t e = launch_attn_rows(r, a.H, stream);
     return e != cudaSuccess ? e : launch_join(a, w, stream, why);
   }
   ForwardMaps m;

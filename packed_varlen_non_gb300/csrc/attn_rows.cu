@@ -66,10 +66,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(RowsArgs a) {
   const uint32_t base = dev::smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;  // fragment row and column group
-  const int4 u = __ldg(reinterpret_cast<const int4*>(a.units) + 2 * blockIdx.x);
-  const int4 w = __ldg(reinterpret_cast<const int4*>(a.units) + 2 * blockIdx.x + 1);
-  const int q0 = u.x, rows = u.y - u.x, head = w.x;
-  const int key0 = w.y * kKeyTile, key1 = min((int64_t)w.z * kKeyTile, (int64_t)a.prefix_len);
+  // the segment, as the plan lists it (computed: a load would delay the first copies)
+  const int piece = blockIdx.x, head = blockIdx.y, q0 = blockIdx.z * kRowsTile, rows = min(kRowsTile, a.S - q0);
+  const int key0 = (int)((int64_t)a.tiles * piece / a.pieces) * kKeyTile;
+  const int key1 = (int)min((int64_t)a.tiles * (piece + 1) / a.pieces * kKeyTile, (int64_t)a.prefix_len);
   const int64_t col = (int64_t)head * kHeadDim;
   const __nv_bfloat16* kp = a.k_prefix + col;
   const __nv_bfloat16* vp = a.v_prefix + col;
@@ -238,25 +238,26 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(RowsArgs a) {
       sum.w = fmaf(f, v.w, sum.w);
       total = fmaf(f, ml_of[x][r].y, total);
     }
-    const int64_t at = (int64_t)w.w + r;
+    const int64_t at = ((int64_t)q0 * gridDim.y + (int64_t)head * rows) * a.pieces + piece * rows + r;
     reinterpret_cast<float4*>(a.part_o + at * kHeadDim)[lane] = sum;
     if (lane == 0) a.part_ml[at] = make_float2(M, total);
   }
 }
 
 template <int kM>
-cudaError_t launch(const RowsArgs& a, int n_units, cudaStream_t stream) {
+cudaError_t launch(const RowsArgs& a, int heads, cudaStream_t stream) {
   // (asked on every call: the attribute belongs to the current device)
   cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<kM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
-  attn_rows_kernel<kM><<<n_units, kThreads, kSmem, stream>>>(a);
+  const dim3 grid((unsigned)a.pieces, (unsigned)heads, (unsigned)((a.S + kRowsTile - 1) / kRowsTile));
+  attn_rows_kernel<kM><<<grid, kThreads, kSmem, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attn_rows(const RowsArgs& a, int n_units, int max_rows, cudaStream_t stream) {
-  return max_rows <= 16 ? launch<1>(a, n_units, stream) : launch<2>(a, n_units, stream);
+cudaError_t launch_attn_rows(const RowsArgs& a, int heads, cudaStream_t stream) {
+  return a.S <= 16 ? launch<1>(a, heads, stream) : launch<2>(a, heads, stream);
 }
 
 }  // namespace h3

@@ -777,7 +777,7 @@ static WalkArgs walk_args(const WalkPlan& w) {
   x.joins = w.d_joins;
   x.n_joins = (int32_t)w.joins.size();
   x.pair = w.streams == 2;
-  x.rows = w.rows;
+  x.pieces = w.pieces;
   return x;
 }
 

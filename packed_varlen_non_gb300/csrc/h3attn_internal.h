@@ -139,7 +139,8 @@ constexpr int kRowsMax = 64;
 
 struct WalkPlan {
   bool set = false;
-  bool rows = false;                   // prefix walk of a few short documents: unit_off is not used
+  int32_t pieces = 0;                  // > 0: prefix walk of a few short documents, so many blocks for each head and
+                                       // kRowsTile rows (attn_rows.cu, which computes its segments itself)
   int streams = 1;                     // streams of segments that a CTA pair runs side by side
   std::vector<WalkUnit> units;         // grouped by CTA pair
   std::vector<int32_t> unit_off;       // [n_pairs + 1]; two streams: [n_pairs][2] (first, end)
@@ -353,7 +354,7 @@ struct WalkArgs {
   const JoinRec* joins;
   int32_t n_joins;
   bool pair;                   // two streams of segments on a CTA pair
-  bool rows;                   // attn_rows.cu's segments
+  int32_t pieces;              // > 0: attn_rows.cu's
   // list walk
   const int32_t* block_idx;    // [H, n_q_blocks, max_blocks]
   const int32_t* block_cnt;    // [H, n_q_blocks]
@@ -372,12 +373,12 @@ struct RowsArgs {
   const __nv_bfloat16* v_prefix;
   int64_t q_stride, prefix_stride;
   int32_t prefix_len;
-  const WalkUnit* units;
+  int32_t S, tiles, pieces;    // query rows; the prefix's tiles, cut into pieces for each head and kRowsTile rows
   float scale_log2;
   float* part_o;
   float2* part_ml;
 };
-cudaError_t launch_attn_rows(const RowsArgs& a, int n_units, int max_rows, cudaStream_t stream);
+cudaError_t launch_attn_rows(const RowsArgs& a, int heads, cudaStream_t stream);
 
 cudaError_t launch_forward_list(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why);
 cudaError_t launch_forward_prefix(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why);

@@ -231,7 +231,6 @@ std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_hea
   int32_t longest = 0;
   for (int32_t d = 0; d < n_docs; ++d) longest = std::max(longest, cu[d + 1] - cu[d]);
   if (cu[n_docs] <= kRowsMax && longest <= kJoinOwnKeys) {
-    w.rows = true;
     std::vector<Item> items;
     std::vector<Join> joins;
     const int32_t tiles = (cu[n_docs] + kRowsTile - 1) / kRowsTile;
@@ -244,7 +243,7 @@ std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_hea
           if (r0 < r1) joins.push_back(Join{r0, r1, h, (int32_t)items.size(), cu[d], cu[d + 1]});
         }
         Item it{WalkUnit{q0, q1, 0, 0, h, 0, tp, -1}, tp, tp, false};
-        it.pieces = std::min(blocks, tp);
+        it.pieces = w.pieces = std::min(blocks, tp);
         items.push_back(it);
       }
     return finish(items, joins, (int)std::min<size_t>(items.size() * items[0].pieces, size_t(1) << 20), prefix_piece, w);
