@@ -29,14 +29,16 @@ constexpr uint32_t kTensorBytes = kStageKeys * 256;       // K or V of a stage: 
 constexpr uint32_t kStageBytes = 2 * kTensorBytes;
 constexpr uint32_t kSmem = kStages * kStageBytes;
 constexpr float kRescale = 32.0f;                         // log2 units (see attn_fwd_tc.cu)
-static_assert(kSmem >= kWarps * kRowsTile * 512, "the joined O rows reuse the ring");
+constexpr int kORow = 136;  // floats between the joined O rows (eight rows' same dims in different banks)
+static_assert(kSmem >= kWarps * kRowsTile * kORow * 4, "the joined O rows reuse the ring");
+static_assert(kStageBytes >= kRowsTile * 256, "Q passes through a stage");
 
 // Byte offset of 16-byte chunk c of row r of a stage's K or V (chunks swizzled
 // by the row, so that eight rows' same chunk lie in different banks).
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) { return (uint32_t)(r * 256 + ((c ^ (r & 7)) << 4)); }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
-  const int n = in ? 16 : 0;  // (0: the 16 bytes are filled with zeros)
+// n = 0: the 16 bytes are filled with zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n = 16) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -74,18 +76,36 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(RowsArgs a) {
   const __nv_bfloat16* kp = a.k_prefix + col;
   const __nv_bfloat16* vp = a.v_prefix + col;
   const int steps = (key1 - key0 + kStageKeys - 1) / kStageKeys;
+  // This thread copies 16-byte chunk c of rows r0, r0 + 8, ... of a stage (eight
+  // rows apart, a chunk keeps its place in the swizzle).
+  const int r0 = threadIdx.x >> 4, c = threadIdx.x & 15;
+  const uint32_t to = base + chunk_at(r0, c);
+  const int64_t from = (int64_t)(key0 + r0) * a.prefix_stride + 8 * c, rows8 = 8 * a.prefix_stride;
   const auto load = [&](int step) {
-    const uint32_t dst = base + (step % kStages) * kStageBytes;
-    const int k0 = key0 + step * kStageKeys;
+    const uint32_t dst = to + (step % kStages) * kStageBytes;
+    const int64_t at = from + (int64_t)step * (kStageKeys / 8) * rows8;
+    const __nv_bfloat16 *ks = kp + at, *vs = vp + at;
+    const int n = key1 - (key0 + step * kStageKeys + r0);  // keys from row r0 to the end
+    if (n > kStageKeys - 8) {
 #pragma unroll
-    for (int i = 0; i < kStageKeys * 16 / kThreads; ++i) {
-      const int r = (threadIdx.x >> 4) + i * (kThreads / 16), c = threadIdx.x & 15;
-      const bool in = k0 + r < key1;
-      const int64_t at = (int64_t)(in ? k0 + r : key0) * a.prefix_stride + 8 * c;
-      copy16(dst + chunk_at(r, c), kp + at, in);
-      copy16(dst + kTensorBytes + chunk_at(r, c), vp + at, in);
+      for (int i = 0; i < kStageKeys / 8; ++i) {
+        copy16(dst + i * 2048, ks + i * rows8);
+        copy16(dst + kTensorBytes + i * 2048, vs + i * rows8);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kStageKeys / 8; ++i) {
+        const bool in = 8 * i < n;
+        copy16(dst + i * 2048, in ? ks + i * rows8 : kp, in ? 16 : 0);
+        copy16(dst + kTensorBytes + i * 2048, in ? vs + i * rows8 : vp, in ? 16 : 0);
+      }
     }
   };
+  // Q through the last stage, which is loaded only once the first step begins
+  const uint32_t qs = base + (kStages - 1) * kStageBytes;
+  for (int r = r0; r < 16 * kM; r += 8)
+    copy16(qs + chunk_at(r, c), a.q + (int64_t)(q0 + min(r, rows - 1)) * a.q_stride + col + 8 * c, r < rows ? 16 : 0);
+  asm volatile("cp.async.commit_group;" ::: "memory");
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
     if (s < steps) load(s);
@@ -93,20 +113,16 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(RowsArgs a) {
   }
   asm volatile("griddepcontrol.launch_dependents;");  // (the join waits for this grid's end)
 
-  // Q as A fragments, 8 steps of 16 dims
+  // Q as A fragments, 8 steps of 16 dims: matrices (rows 0-7, 8-15) x (dims 0-7, 8-15)
+  const int mat = lane >> 3, in_mat = lane & 7;
   uint32_t q[kM][8][4];
+  asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+  __syncthreads();
 #pragma unroll
   for (int m = 0; m < kM; ++m)
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int r = 16 * m + 8 * half + g;
-      const uint32_t* p = reinterpret_cast<const uint32_t*>(a.q + (int64_t)(q0 + min(r, rows - 1)) * a.q_stride + col);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        q[m][k][half] = __ldg(p + 8 * k + t);
-        q[m][k][2 + half] = __ldg(p + 8 * k + 4 + t);
-      }
-    }
+    for (int k = 0; k < 8; ++k)
+      ldsm4(q[m][k], qs + (chunk_at(16 * m + (mat & 1) * 8 + in_mat, mat >> 1) ^ (32 * k)));
   float o[kM][16][4], mx[kM][2], l[kM][2];
 #pragma unroll
   for (int m = 0; m < kM; ++m) {
@@ -120,9 +136,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(RowsArgs a) {
 
   // ldmatrix rows of this lane: K: matrices (keys 0-7, 8-15) x (dims 0-7, 8-15);
   // V, transposed: the same with keys innermost
-  const int mat = lane >> 3, in_mat = lane & 7;
-  const int k_row = 16 * warp + (mat >> 1) * 8 + in_mat, k_chunk = mat & 1;
-  const int v_row = 16 * warp + (mat & 1) * 8 + in_mat, v_chunk = mat >> 1;
+  // (a row's chunk c lies at c ^ (row & 7): the bytes of step k's chunks differ
+  // from the first one's by an exclusive or)
+  const uint32_t k_at = chunk_at(16 * warp + (mat >> 1) * 8 + in_mat, mat & 1);
+  const uint32_t v_at = chunk_at(16 * warp + (mat & 1) * 8 + in_mat, mat >> 1);
 
 #pragma unroll 1
   for (int step = 0; step < steps; ++step) {
@@ -141,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(RowsArgs a) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       uint32_t b[4];
-      ldsm4(b, ks + chunk_at(k_row, 2 * k + k_chunk));
+      ldsm4(b, ks + (k_at ^ (32 * k)));
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
         mma(s[m][0], q[m][k], b[0], b[1]);
@@ -149,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(RowsArgs a) {
       }
     }
     const int k0 = key0 + step * kStageKeys + 16 * warp + 2 * t;  // key of s[.][0][0]
+    const bool last = step + 1 == steps;
     uint32_t p[kM][4];
 #pragma unroll
     for (int m = 0; m < kM; ++m) {
@@ -156,8 +174,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(RowsArgs a) {
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const bool in = k0 + 8 * n + (e & 1) < key1;
-          s[m][n][e] = in ? s[m][n][e] * a.scale_log2 : -INFINITY;
+          s[m][n][e] *= a.scale_log2;
+          if (last && k0 + 8 * n + (e & 1) >= key1) s[m][n][e] = -INFINITY;
         }
       bool grow = false;
       float next[2];
@@ -194,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(RowsArgs a) {
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
       uint32_t b[4];
-      ldsm4_t(b, vs + chunk_at(v_row, 2 * n + v_chunk));
+      ldsm4_t(b, vs + (v_at ^ (32 * n)));
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
         mma(o[m][2 * n], p[m], b[0], b[1]);
@@ -218,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(RowsArgs a) {
       if (t == 0) ml_of[warp][r] = make_float2(mx[m][h], sum);
 #pragma unroll
       for (int n = 0; n < 16; ++n)
-        *reinterpret_cast<float2*>(os + (warp * kRowsTile + r) * kHeadDim + 8 * n + 2 * t) =
+        *reinterpret_cast<float2*>(os + (warp * kRowsTile + r) * kORow + 8 * n + 2 * t) =
             make_float2(o[m][n][2 * h], o[m][n][2 * h + 1]);
     }
   __syncthreads();
@@ -231,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(RowsArgs a) {
 #pragma unroll
     for (int x = 0; x < kWarps; ++x) {
       const float f = dev::ex2_approx(ml_of[x][r].x - M);
-      const float4 v = reinterpret_cast<const float4*>(os + (x * kRowsTile + r) * kHeadDim)[lane];
+      const float4 v = reinterpret_cast<const float4*>(os + (x * kRowsTile + r) * kORow)[lane];
       sum.x = fmaf(f, v.x, sum.x);
       sum.y = fmaf(f, v.y, sum.y);
       sum.z = fmaf(f, v.z, sum.z);
