@@ -1837,43 +1837,52 @@ __global__ void __launch_bounds__(32 * kJoinRows, 4) attn_join_kernel(JoinArgs a
   const JoinRec j = a.recs[blockIdx.x];
   const int32_t row = j.row0 + (int32_t)(threadIdx.x >> 5);
   if (row >= j.row1) return;
-  // own keys (inputs of the forward: they need not wait for it)
-  float m_own = -INFINITY, l_own = 0.f;
-  float4 o_own = make_float4(0.f, 0.f, 0.f, 0.f);
+  // own keys (inputs of the forward: they need not wait for it), four at a time
+  // with their values
+  float M = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const int n_own = j.key_hi - j.key_lo;
   if (n_own > 0) {
     const int64_t col = (int64_t)j.head * kHeadDim + 4 * lane;
     const float4 q = load_bf16x4(a.q + (int64_t)row * a.stride + col);
-    float s = -INFINITY;  // lane x holds the score of key x (n_own <= 32)
-#pragma unroll 4
-    for (int x = 0; x < n_own; ++x) {
-      const float4 k = load_bf16x4(a.k + (int64_t)(j.key_lo + x) * a.stride + col);
-      float d = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, q.w * k.w)));
+#pragma unroll 1
+    for (int x0 = 0; x0 < n_own; x0 += 4) {
+      float s[4];
+      float4 k[4], v[4];
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-      if (x == lane) s = d * a.scale_log2;
-    }
-    m_own = s;
+      for (int x = 0; x < 4; ++x) {
+        const int64_t at = (int64_t)(j.key_lo + min(x0 + x, n_own - 1)) * a.stride + col;
+        k[x] = load_bf16x4(a.k + at);
+        v[x] = load_bf16x4(a.v + at);
+      }
+      float m_new = M;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m_own = fmaxf(m_own, __shfl_xor_sync(0xffffffffu, m_own, off));
-    const float p = dev::ex2_approx(s - (m_own == -INFINITY ? 0.f : m_own));
-    l_own = p;
+      for (int x = 0; x < 4; ++x) {
+        float d = fmaf(q.x, k[x].x, fmaf(q.y, k[x].y, fmaf(q.z, k[x].z, q.w * k[x].w)));
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) l_own += __shfl_xor_sync(0xffffffffu, l_own, off);
-#pragma unroll 4
-    for (int x = 0; x < n_own; ++x) {
-      const float w = __shfl_sync(0xffffffffu, p, x);
-      const float4 v = load_bf16x4(a.v + (int64_t)(j.key_lo + x) * a.stride + col);
-      o_own.x = fmaf(w, v.x, o_own.x);
-      o_own.y = fmaf(w, v.y, o_own.y);
-      o_own.z = fmaf(w, v.z, o_own.z);
-      o_own.w = fmaf(w, v.w, o_own.w);
+        for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+        s[x] = x0 + x < n_own ? d * a.scale_log2 : -INFINITY;
+        m_new = fmaxf(m_new, s[x]);
+      }
+      const float ref = m_new == -INFINITY ? 0.f : m_new;
+      const float w = dev::ex2_approx(M - ref);
+      acc = make_float4(w * acc.x, w * acc.y, w * acc.z, w * acc.w);
+      l *= w;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        if (x0 + x >= n_own) break;
+        const float p = dev::ex2_approx(s[x] - ref);
+        acc.x = fmaf(p, v[x].x, acc.x);
+        acc.y = fmaf(p, v[x].y, acc.y);
+        acc.z = fmaf(p, v[x].z, acc.z);
+        acc.w = fmaf(p, v[x].w, acc.w);
+        l += p;
+      }
+      M = m_new;
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the forward is complete and its writes visible
   const int64_t r0 = (int64_t)j.part + (row - j.q_row0);
-  float M = m_own, l = l_own;
-  float4 acc = o_own;
 #pragma unroll 1
   for (int c = 0; c < j.n; c += kAtOnce) {
     float2 ml[kAtOnce];
