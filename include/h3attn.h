@@ -328,7 +328,8 @@ h3attn_status h3attn_plan_sparse_info(h3attn_plan_t plan, int32_t* q_block, int3
  * Errors: EINVAL for NULL or misaligned (tensors 16, lists 4 bytes) pointers, a
  * bad stride, keep outside [1, max_blocks], lists that overlap the tensors or
  * each other, or without h3attn_plan_set_sparse; EUNSUPPORTED for a document of
- * more than 1,572,864 tokens. */
+ * more than 1,572,864 tokens, more than 65,535 heads, or 2^30 or more key tiles
+ * times heads. */
 h3attn_status h3attn_block_select(h3attn_plan_t plan, const void* q_hat, const void* k_hat, int64_t qkv_row_stride,
                                   int32_t keep, int32_t keep_own, int32_t* block_idx, int32_t* block_cnt,
                                   void* cuda_stream);
@@ -340,7 +341,8 @@ h3attn_status h3attn_block_select(h3attn_plan_t plan, const void* q_hat, const v
  * and o_i = 0, lse = -inf where J is empty.  A listed tile outside the
  * document is skipped and reported by h3attn_get_device_error (EINVAL).  Keys
  * that are not visited, among them the rows behind a document's end, do not
- * reach o or lse, whatever they hold (NaN included).  Tensors, strides and
+ * reach o or lse, whatever they hold (NaN included).  |v| may be up
+ * to 2^64.  The lists must not change while the call runs.  Tensors, strides and
  * errors as h3attn_forward; block_idx, block_cnt: as above, 4-byte aligned, not
  * overlapping o or lse_out; EINVAL without h3attn_plan_set_sparse. */
 h3attn_status h3attn_forward_sparse(h3attn_plan_t plan, const void* q, const void* k, const void* v,
@@ -373,7 +375,8 @@ h3attn_status h3attn_plan_set_prefix(h3attn_plan_t plan, int32_t prefix_len, voi
  * q, k, v, o, lse_out, strides and errors as h3attn_forward; k_prefix,
  * v_prefix: bf16 [P,H,128] with prefix_row_stride (>= H*128, a multiple of 8),
  * 16-byte aligned, not overlapping o or lse_out.  Rows behind the prefix or a
- * document do not reach o or lse, whatever they hold.  EINVAL also without
+ * document do not reach o or lse, whatever they hold.  |v| may be up to 2^64.
+ * EINVAL also without
  * h3attn_plan_set_prefix. */
 h3attn_status h3attn_forward_prefix(h3attn_plan_t plan, const void* q, const void* k, const void* v,
                                     int64_t qkv_row_stride, const void* k_prefix, const void* v_prefix,

@@ -1960,13 +1960,8 @@ bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType type, uint32
 
 template <bool kFp8, int kWalk, bool kPair = false>
 cudaError_t set_smem_attr() {
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(attn_fwd_tc_kernel<kFp8, kWalk, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)Cfg<kFp8, kPair>::SmemAlloc);
-  });
-  return attr;
+  static SmemAttr attr;
+  return attr.set(attn_fwd_tc_kernel<kFp8, kWalk, kPair>, (int)Cfg<kFp8, kPair>::SmemAlloc);
 }
 
 // A kernel launched as a programmatic dependent of the forward before it.

@@ -264,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_rows_kernel(RowsArgs a) {
 
 template <int kM>
 cudaError_t launch(const RowsArgs& a, int heads, cudaStream_t stream) {
-  // (asked on every call: the attribute belongs to the current device)
-  cudaError_t e = cudaFuncSetAttribute(attn_rows_kernel<kM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  static SmemAttr attr;
+  const cudaError_t e = attr.set(attn_rows_kernel<kM>, (int)kSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)a.pieces, (unsigned)heads, (unsigned)((a.S + kRowsTile - 1) / kRowsTile));
   attn_rows_kernel<kM><<<grid, kThreads, kSmem, stream>>>(a);

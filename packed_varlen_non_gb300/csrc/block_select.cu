@@ -566,9 +566,9 @@ cudaError_t launch_block_select(const SelectArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int warps = select_warps(a.max_tiles);
   const size_t smem = score_smem(warps, a.max_tiles);
-  if (smem > 48 * 1024) {
-    e = cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {  // (more than 334 tiles)
+    static SmemAttr attr;
+    if ((e = attr.set(score_kernel, (int)score_smem(1, kSelectMaxTiles))) != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.n_groups, (unsigned)a.H);

@@ -6,6 +6,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <exception>
 #include <new>
 
 #include "h3attn_internal.h"
@@ -686,7 +687,7 @@ h3attn_status h3attn_plan_set_sparse(h3attn_plan_t plan, int32_t q_block, int32_
       sp.n_q_blocks += blocks;
       tile0 += tiles;
     }
-  } catch (const std::bad_alloc&) {
+  } catch (const std::exception&) {
     return fail(H3ATTN_ENOMEM, "host allocation failed while building the sparse lists");
   }
   const size_t words = (size_t)plan->num_heads * plan->ktiles_host.size() * kHeadDim;
@@ -742,6 +743,8 @@ h3attn_status h3attn_block_select(h3attn_plan_t plan, const void* q_hat, const v
     return fail(H3ATTN_EINVAL, "row stride must be >= H*128 = %lld and a multiple of 8", (long long)width);
   if (keep < 1 || keep > sp.max_blocks)
     return fail(H3ATTN_EINVAL, "keep must be in [1, max_blocks = %d] (got %d)", sp.max_blocks, keep);
+  if (plan->num_heads > 65535 || 2 * (int64_t)plan->ktiles_host.size() * plan->num_heads >= (int64_t(1) << 31))
+    return fail(H3ATTN_EUNSUPPORTED, "too many heads or tokens to score");
   if (sp.max_tiles > kSelectMaxTiles)
     return fail(H3ATTN_EUNSUPPORTED, "a document of more than %d tokens cannot be scored", kSelectMaxTiles * kKeyTile);
   const uintptr_t n = (uintptr_t)plan->num_heads * sp.n_q_blocks * 4;
@@ -831,7 +834,7 @@ h3attn_status h3attn_plan_set_prefix(h3attn_plan_t plan, int32_t prefix_len, voi
                                               forward_slots(plan->device, plan->num_sms), pp.walk);
     if (!why.empty()) return fail(H3ATTN_EINVAL, "%s", why.c_str());
     pp.len = prefix_len;
-  } catch (const std::bad_alloc&) {
+  } catch (const std::exception&) {
     return fail(H3ATTN_ENOMEM, "host allocation failed while building the prefix list");
   }
   return attach_walk(&pp.walk, "prefix", cuda_stream, [](cudaStream_t) { return cudaSuccess; });
@@ -923,7 +926,7 @@ h3attn_status h3attn_walk_list_host(int32_t kind, const int32_t* cu_seqlens, int
     if (unit_off) std::memcpy(unit_off, off.data(), off.size() * sizeof(int32_t));
     if (joins && !w.joins.empty()) std::memcpy(joins, w.joins.data(), w.joins.size() * sizeof(JoinRec));
     if (own && !w.own.empty()) std::memcpy(own, w.own.data(), w.own.size() * sizeof(OwnTile));
-  } catch (const std::bad_alloc&) {
+  } catch (const std::exception&) {
     return fail(H3ATTN_ENOMEM, "host allocation failed while building the work list");
   }
   return H3ATTN_OK;

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
 #include <string>
 #include <vector>
 
@@ -287,6 +288,24 @@ std::string build_plan_host(const h3attn_doc* docs, int32_t n_docs, const h3attn
 // Error reporting for the C-ABI layer.
 h3attn_status fail(h3attn_status s, const char* fmt, ...);
 void clear_error();
+
+// The maximum dynamic shared memory of a kernel, set once per kernel and device
+// (the attribute belongs to the current device's copy of the kernel).
+struct SmemAttr {
+  std::once_flag once[64];
+  cudaError_t result[64] = {};
+  template <class Kernel>
+  cudaError_t set(Kernel* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    std::call_once(once[dev], [&] {
+      result[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    });
+    return result[dev];
+  }
+};
 
 // Kernel launchers.
 struct PrologueArgs {

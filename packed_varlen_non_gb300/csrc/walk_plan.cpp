@@ -230,7 +230,7 @@ std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_hea
   // reading the prefix, a block per SM half (attn_rows.cu).
   int32_t longest = 0;
   for (int32_t d = 0; d < n_docs; ++d) longest = std::max(longest, cu[d + 1] - cu[d]);
-  if (cu[n_docs] <= kRowsMax && longest <= kJoinOwnKeys) {
+  if (cu[n_docs] <= kRowsMax && longest <= kJoinOwnKeys && num_heads <= 65535) {
     std::vector<Item> items;
     std::vector<Join> joins;
     const int32_t tiles = (cu[n_docs] + kRowsTile - 1) / kRowsTile;

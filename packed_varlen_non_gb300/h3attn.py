@@ -169,7 +169,8 @@ def h3attn_plan_create(docs, num_heads: int, rope_base: float = 10000.0, head_di
 
 
 def h3attn_plan_destroy(plan):
-    _list_sizes.pop(plan, None)
+    for known in (_list_sizes, _plan_rows, _prefix_rows):
+        known.pop(plan, None)
     _check(load().h3attn_plan_destroy(plan), "h3attn_plan_destroy")
 
 
@@ -323,13 +324,27 @@ def h3attn_forward_noalloc(cu_seqlens, num_heads: int, q, k, v, o, softmax_scale
 
 # ------------------------------------------------- sparse, shared prefix ----
 
-def _qkv_stride(q, others, given):
+# Rows that the walks' calls read or write: a plan's tokens, and its prefix.
+_plan_rows: dict = {}
+_prefix_rows: dict = {}
+
+
+def _qkv_stride(q, others, given, rows=None):
+    """Row stride shared by tensors of at least `rows` rows on the device."""
     if given is None and not isinstance(q, int):
         given = q.stride(0)
         for x in others:
             if x.stride(0) != given:
                 raise ValueError(f"tensors of one call must share one row stride (got {given}, {x.stride(0)})")
+    if rows is not None:
+        for x in (q, *others):
+            _check_rows(x, rows)
     return _row_stride(q, given)
+
+
+def _check_rows(x, rows):
+    if x is not None and not isinstance(x, int) and (x.shape[0] < rows or not x.is_cuda):
+        raise ValueError(f"a tensor on the device with at least {rows} rows is needed (got {tuple(x.shape)}, {x.device})")
 
 
 # Sizes of the lists of the plans that have them (fixed once set).
@@ -345,9 +360,9 @@ def _check_lists(plan, block_idx, block_cnt):
     if sizes is None:
         return  # the call itself refuses a plan without lists
     for t, n in ((block_idx, sizes[0]), (block_cnt, sizes[1])):
-        if t.numel() != n or t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous():
-            raise ValueError("block_idx and block_cnt must be contiguous int32 tensors of "
-                             f"{sizes[0]} and {sizes[1]} elements (got {tuple(t.shape)}, {t.dtype})")
+        if t.numel() != n or t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous() or not t.is_cuda:
+            raise ValueError("block_idx and block_cnt must be contiguous int32 tensors on the device of "
+                             f"{sizes[0]} and {sizes[1]} elements (got {tuple(t.shape)}, {t.dtype}, {t.device})")
 
 
 def h3attn_plan_set_sparse(plan, q_block: int, max_blocks: int, stream=None):
@@ -357,6 +372,7 @@ def h3attn_plan_set_sparse(plan, q_block: int, max_blocks: int, stream=None):
     info = h3attn_plan_sparse_info(plan)
     rows = info["num_heads"] * info["n_q_blocks"]
     _list_sizes[plan] = (rows * info["max_blocks"], rows)
+    _plan_rows[plan] = h3attn_plan_info(plan)["S"]
 
 
 def h3attn_plan_sparse_info(plan) -> dict:
@@ -371,7 +387,7 @@ def h3attn_block_select(plan, q_hat, k_hat, keep: int, block_idx, block_cnt, kee
                         qkv_row_stride=None, stream=None):
     """Scores and keeps key tiles: block_idx int32 [H, n_q_blocks, max_blocks],
     block_cnt int32 [H, n_q_blocks] (see include/h3attn.h)."""
-    stride = _qkv_stride(q_hat, (k_hat,), qkv_row_stride)
+    stride = _qkv_stride(q_hat, (k_hat,), qkv_row_stride, _plan_rows.get(plan))
     _check_lists(plan, block_idx, block_cnt)
     _check(load().h3attn_block_select(plan, _ptr(q_hat), _ptr(k_hat), stride, int(keep), int(bool(keep_own)),
                                       _ptr(block_idx), _ptr(block_cnt), _stream(stream)), "h3attn_block_select")
@@ -380,7 +396,10 @@ def h3attn_block_select(plan, q_hat, k_hat, keep: int, block_idx, block_cnt, kee
 def h3attn_forward_sparse(plan, q, k, v, block_idx, block_cnt, o, softmax_scale: float, lse=None,
                           qkv_row_stride=None, o_row_stride=None, stream=None):
     """The forward over the listed key tiles of each query block."""
-    stride = _qkv_stride(q, (k, v), qkv_row_stride)
+    rows = _plan_rows.get(plan)
+    stride = _qkv_stride(q, (k, v), qkv_row_stride, rows)
+    if rows is not None:
+        _check_rows(o, rows)
     _check_lists(plan, block_idx, block_cnt)
     _check(load().h3attn_forward_sparse(plan, _ptr(q), _ptr(k), _ptr(v), stride, _ptr(block_idx), _ptr(block_cnt),
                                         _ptr(o), _row_stride(o, o_row_stride), float(softmax_scale), _ptr(lse),
@@ -391,15 +410,21 @@ def h3attn_plan_set_prefix(plan, prefix_len: int, stream=None):
     """Adds the work list for a shared prefix of prefix_len rows to a plan
     (once per plan)."""
     _check(load().h3attn_plan_set_prefix(plan, int(prefix_len), _stream(stream)), "h3attn_plan_set_prefix")
+    _prefix_rows[plan] = int(prefix_len)
+    _plan_rows[plan] = h3attn_plan_info(plan)["S"]
 
 
 def h3attn_forward_prefix(plan, q, k, v, k_prefix, v_prefix, o, softmax_scale: float, lse=None,
                           qkv_row_stride=None, prefix_row_stride=None, o_row_stride=None, stream=None):
     """The forward of a batch whose documents all attend to one prefix besides
     themselves; k_prefix and v_prefix are bf16 [prefix_len, H, 128]-shaped."""
-    stride = _qkv_stride(q, (k, v), qkv_row_stride)
+    rows = _plan_rows.get(plan)
+    stride = _qkv_stride(q, (k, v), qkv_row_stride, rows)
+    if rows is not None:
+        _check_rows(o, rows)
+    prefix_stride = _qkv_stride(k_prefix, (v_prefix,), prefix_row_stride, _prefix_rows.get(plan))
     _check(load().h3attn_forward_prefix(plan, _ptr(q), _ptr(k), _ptr(v), stride, _ptr(k_prefix), _ptr(v_prefix),
-                                        _qkv_stride(k_prefix, (v_prefix,), prefix_row_stride), _ptr(o),
+                                        prefix_stride, _ptr(o),
                                         _row_stride(o, o_row_stride), float(softmax_scale), _ptr(lse),
                                         _stream(stream)), "h3attn_forward_prefix")
 

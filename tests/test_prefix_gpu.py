@@ -95,6 +95,17 @@ def test_nan_in_other_documents_and_behind_the_prefix_reaches_nothing(lib, lens)
     assert torch.equal(o2[1:], o[1:])
 
 
+@pytest.mark.parametrize("lens", [[1] * 9, [300, 40, 5], [1100]])
+@pytest.mark.parametrize("spread,size", [(8.0, 1.0), (3.0, 2.0 ** 60), (0.0, 1.0)])
+def test_wide_scores_and_large_values(lib, lens, spread, size):
+    p = W.Prefix(lens, 2, 700)
+    t = tensors(lens, 2, 700, 110)
+    t[0] = (t[0].float() * spread).to(torch.bfloat16)
+    t[2], t[4] = ((x.float() * size).to(torch.bfloat16) for x in (t[2], t[4]))
+    o, lse = p.forward(*t)
+    W.check(o, lse, t[0], [t[1], t[3]], oracle(p, t))
+
+
 def test_strides_guards_and_no_lse(lib):
     lens, heads, P = [5, 333, 64], 2, 150
     p = W.Prefix(lens, heads, P)
@@ -201,4 +212,9 @@ def test_refusals(lib):
             assert status(lambda: fwd(**kw)) == E, kw
         with pytest.raises(ValueError):
             H.h3attn_forward_prefix(p, *t[:3], t[3], W.strided(t[4].view(100, 2, 128), 512), o, 0.1)
+        # a prefix or batch that is too short, or not on the device
+        for bad in (dict(k_prefix=t[3][:99], v_prefix=t[4][:99]), dict(q=t[0][:299]), dict(v_prefix=t[4].cpu())):
+            with pytest.raises(ValueError):
+                H.h3attn_forward_prefix(**{**dict(plan=p, q=t[0], k=t[1], v=t[2], k_prefix=t[3], v_prefix=t[4], o=o,
+                                                  softmax_scale=0.1), **bad})
         torch.cuda.synchronize()

@@ -223,6 +223,20 @@ def test_nan_in_unlisted_keys_reaches_nothing(lib):
             assert bool(fine) == (e != d)
 
 
+@pytest.mark.parametrize("q_block,max_blocks", [(256, 6), (512, 6), (512, 14)])
+@pytest.mark.parametrize("spread,size", [(8.0, 1.0), (3.0, 2.0 ** 60), (0.0, 1.0)])
+def test_wide_scores_and_large_values(lib, q_block, max_blocks, spread, size):
+    # scores spread over hundreds of log2 units (maxima that grow past the rescale
+    # threshold), over tens with large values (no rescale), and all equal
+    s = W.Sparse([1700, 300], 2, q_block, max_blocks)
+    q, k = W.rows(s.S, 2, 130, spread), W.rows(s.S, 2, 131)
+    v = W.rows(s.S, 2, 132, size)
+    idx, cnt = random_lists(s, np.random.default_rng(3), "shuffled")
+    s.lists(idx, cnt)
+    o, lse = s.forward(q, k, v)
+    W.check(o, lse, q, [k], walks.sparse_attention(W.f64(q), W.f64(k), W.f64(v), s.cu, q_block, idx, cnt, W.SCALE))
+
+
 def test_strides_guards_and_no_lse(lib):
     lens, heads = [333, 64], 2
     s = W.Sparse(lens, heads, 256, 3)
@@ -354,4 +368,9 @@ def test_refusals(lib):
                 H.h3attn_forward_sparse(p, *f, bad, cnt, o, 0.1)
         with pytest.raises(ValueError):
             H.h3attn_block_select(p, f[0], f[1], 2, idx, cnt[:1])
+        # tensors that are too short, or not on the device
+        for bad in (dict(q=f[0][:299]), dict(o=o[:299]), dict(v=f[2].cpu()), dict(block_idx=idx.cpu())):
+            with pytest.raises(ValueError):
+                H.h3attn_forward_sparse(**{**dict(plan=p, q=f[0], k=f[1], v=f[2], block_idx=idx, block_cnt=cnt, o=o,
+                                                  softmax_scale=0.1), **bad})
         torch.cuda.synchronize()
