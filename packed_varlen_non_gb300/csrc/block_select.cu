@@ -346,6 +346,21 @@ __device__ __forceinline__ bool pick_few(const uint32_t* keys, int tiles, int cn
 }
 
 constexpr int kParts = 4;                        // parts of a score, 32 dims each
+constexpr int kPartWords = 64 / kParts;
+
+// Loads that keep their order, so that a batch is in flight at once (scheduled
+// by the compiler they went out as their values were needed: an item's scores
+// took 5,000 cycles instead of the one wait).
+__device__ __forceinline__ float2 load_ordered(const float2* p) {
+  float2 v;
+  asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float4 load_ordered(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
 
 // Bytes of shared memory: qm [64][kSelectWarps] float2, then for each query block
 // its scores' parts [kParts][max_tiles] float, which become its keys (uint32, the
@@ -378,13 +393,14 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
     const float4* p = reinterpret_cast<const float4*>(a.q_sum + ((int64_t)head * a.n_tiles + tile0 + own0) * kHeadDim + 4 * lane);
     float4 u[4], v[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      u[t] = v[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (own0 + t < own1) {
-        u[t] = p[64 * t];
-        v[t] = p[64 * t + 1];
-      }
+    for (int t = 0; t < 4; ++t) {  // (a tile that the block does not have: the first one's, times zero)
+      const int x = own0 + t < own1 ? 64 * t : 0;
+      u[t] = load_ordered(p + x);
+      v[t] = load_ordered(p + x + 1);
     }
+#pragma unroll
+    for (int t = 1; t < 4; ++t)
+      if (own0 + t >= own1) u[t] = v[t] = make_float4(0.f, 0.f, 0.f, 0.f);
     float2 s[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] = make_float2(0.f, 0.f);
@@ -403,25 +419,31 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) qn += __shfl_xor_sync(0xffffffffu, qn, off);
   }
-  __syncthreads();
   // Scores: a warp takes a part (32 dims) of 32 tiles' scores against all the
   // block's query blocks, so that each word of the key means is read once per
   // block, with one wait.
   const int64_t row = a.n_tiles;
   const float2* k_mean = a.k_mean + (int64_t)head * 64 * row + tile0;
   const int items = (tiles + 31) / 32 * kParts;
+  const auto fetch = [&](int i, float2 (&k)[kPartWords]) {
+    const float2* kp = k_mean + min(i / kParts * 32 + lane, tiles - 1) + i % kParts * kPartWords * row;
+#pragma unroll
+    for (int p = 0; p < kPartWords; ++p) k[p] = load_ordered(kp + p * row);
+  };
+  float2 k[kPartWords];
+  if (warp < items) fetch(warp, k);
+  __syncthreads();  // the query means
+#pragma unroll 1
   for (int i = warp; i < items; i += warps) {
     const int j = i / kParts * 32 + lane, part = i % kParts;
-    const float2* kp = k_mean + min(j, tiles - 1) + part * (64 / kParts) * row;
-    const float4* q = reinterpret_cast<const float4*>(smem + part * (64 / kParts) * kSelectWarps);
-    float2 k[64 / kParts];
-#pragma unroll
-    for (int p = 0; p < 64 / kParts; ++p) k[p] = __ldg(kp + p * row);
+    const float4* q = reinterpret_cast<const float4*>(smem + part * kPartWords * kSelectWarps);
+    float2 next[kPartWords];  // the next item's words, on their way
+    if (i + warps < items) fetch(i + warps, next);
     float2 h[kSelectWarps], m = make_float2(0.f, 0.f);
 #pragma unroll
     for (int x = 0; x < kSelectWarps; ++x) h[x] = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int p = 0; p < 64 / kParts; ++p) {
+    for (int p = 0; p < kPartWords; ++p) {
       m = fma2(k[p], k[p], m);
 #pragma unroll
       for (int x = 0; x < kSelectWarps / 2; ++x) {
@@ -436,8 +458,10 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
     if (j < tiles) {
 #pragma unroll
       for (int x = 0; x < kSelectWarps; ++x)
-        if (x < n) parts0[((int64_t)x * kParts + part) * a.max_tiles + j] = h[x].x + h[x].y;
+        if (x < n) parts0[(x * kParts + part) * a.max_tiles + j] = h[x].x + h[x].y;
     }
+#pragma unroll
+    for (int p = 0; p < kPartWords; ++p) k[p] = next[p];
   }
   __syncthreads();
   if (!active) return;
