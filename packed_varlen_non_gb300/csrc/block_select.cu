@@ -92,6 +92,15 @@ __device__ __forceinline__ uint32_t max_mag_bf16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
+// 16 bytes read once by the SM, the rows' 256 bytes together from DRAM.
+__device__ __forceinline__ uint4 load_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // 1.5 * 2^(e + 6) for a number of exponent e (sums of kPoolRows numbers up to it
 // stay in the anchor's binade); no further than the largest exponent.
 __device__ __forceinline__ float anchor_of(uint32_t bits) {
@@ -116,7 +125,7 @@ __global__ void __launch_bounds__(kPoolThreads, 5) pool_kernel(SelectArgs a) {
 #pragma unroll
   for (int i = 0; i < kPoolRows; ++i) {
     const int r = group + kPoolThreads / 16 * i;
-    raw[i] = r < n ? __ldg(reinterpret_cast<const uint4*>(src + r * a.stride)) : make_uint4(0, 0, 0, 0);
+    raw[i] = r < n ? load_once(src + r * a.stride) : make_uint4(0, 0, 0, 0);
   }
   uint4 m = raw[0];  // largest magnitude of each dim
 #pragma unroll
