@@ -300,7 +300,7 @@ h3attn_status h3attn_forward_fp8(h3attn_plan_t plan, const void* q8, const void*
  *
  * h3attn_plan_set_sparse adds the work list to a plan: q_block is 512 (the
  * forward's unit of work: the rate of the dense forward on the listed tiles)
- * or 256 (a finer selection, at about 85 % of that rate); max_blocks >= 1 is the
+ * or 256 (a finer selection, at about nine tenths of that rate); max_blocks >= 1 is the
  * width of the lists and what the work is balanced for.  It allocates and
  * synchronises cuda_stream, must not be called while a stream is captured, and
  * may be called once per plan, so that no later call invalidates a captured

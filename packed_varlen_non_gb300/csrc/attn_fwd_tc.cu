@@ -100,15 +100,26 @@
 //
 // Other key walks (template argument kWalk, bf16): the same pipeline over key
 // tiles that are not "the unit's document, in order".  The list walk
-// (h3attn_forward_sparse) takes the tiles listed for the unit's query block, so
-// the MMAs run at the dense kernel's rate on the listed tiles only; the prefix
-// walk (h3attn_forward_prefix) takes the tiles of a prefix that all documents
-// share (tensor maps of its own), then the document's.  The producer and the
-// softmax warps look each tile up (key_tile); the MMA issuer only counts
-// tiles.  Rows of the V tile past the last valid key are zeroed in shared
-// memory before the PV reads them, so that a NaN or infinity in the rows
-// behind a document or prefix (weight 0) does not reach its output.  A list
-// without a valid tile runs one fully masked tile: o = 0, lse = -inf.
+// (h3attn_forward_sparse) takes the tiles listed for a query block, the prefix
+// walk (h3attn_forward_prefix) the tiles of a prefix that all documents share
+// (tensor maps of its own) and then the rows' own documents.  The producer and
+// the softmax warps look each tile up (walk_entry, a tile ahead, and key_tile);
+// the MMA issuer only counts tiles.  Three things keep rows apart that share
+// MMAs or tiles:
+//   - keys a row may not see are masked to -inf after the QK, as above;
+//   - the rows of a V tile behind its last valid key are zeroed in shared memory
+//     before the PV reads them, so that a NaN or infinity behind a document or
+//     prefix (weight 0) does not reach its output;
+//   - a segment over several documents (prefix walk) runs each one's own tiles
+//     for all its rows, but their PVs leave the lanes of O of the other
+//     documents' rows alone (the MMA's lane mask).
+// A list without a valid tile runs one fully masked tile: o = 0, lse = -inf.
+// Bound by the tensor pipe for long walks (1.28 us a tile and CTA pair, 512 rows,
+// which is the dense forward's rate: 682 us for 1.12e12 flops in a loop, 1,640
+// TFLOP/s; 628 us alone); a segment costs another 4 us for its boundary, where
+// the pipeline runs empty (measured for segments of 1 to 16 tiles).  For short
+// lists and 256-row query blocks that boundary is hidden by a second stream of
+// segments (kPair, below).
 //
 // Every mbarrier wait is bounded: on expiry the CTA raises an abort flag,
 // records a timeout in the device error word, drains its own copies and MMAs
@@ -209,9 +220,9 @@ struct Bars {
 // its query block, the shared prefix's tiles and then the document's.
 constexpr int kWalkDoc = 0, kWalkList = 1, kWalkPrefix = 2;
 
-// kPair (list walk, query blocks of 256 rows): a CTA pair runs two streams of
-// segments of up to 256 rows, each with walks of its own -- query blocks with
-// different lists, of any documents and heads.  Query tile s of both CTAs (rows
+// kPair (list walk, 256-row segments: 256-row query blocks, and the halves of
+// 512-row ones with short lists): a CTA pair runs two streams of segments, each
+// with walks of its own -- different lists, of any documents and heads.  Query tile s of both CTAs (rows
 // q0 + 128 rank + i) belongs to stream s.  The streams share nothing but the
 // tensor cores: the issuer takes whichever stream's next P is ready, and stream
 // 1 begins half a segment after stream 0, so that one stream's segment boundary
@@ -224,6 +235,9 @@ constexpr int kWalkDoc = 0, kWalkList = 1, kWalkPrefix = 2;
 // ends, so one per stream is enough; O rows are stored directly.
 // Warp 9 loads stream 0 and warp 10 stream 1: lane 0 Q, K and V in the order the
 // stream needs them, lane 1 reports each Q tile landed.
+// Measured, us for 512 rows of a head (two segments) and 2 / 4 / 8 / 16 tiles: one
+// 256-row segment at a time with the other query tile idle 13.5 / 18 / 28 / 49;
+// two in lockstep 7.5 / 9.7 / 14.8 / 25.1; two streams 5.4 / 7.7 / 13.0 / 24.1.
 
 // What a walk needs besides the unit.
 template <int kWalk>
@@ -1831,7 +1845,8 @@ constexpr int kAtOnce = 8;
 
 // The rows of a record are a block's; parts are read kAtOnce at a time with their
 // maxima and rows together, in one pass with a running maximum, so that a row
-// waits for memory about once.
+// waits for memory about once (two passes over the maxima and then the rows, and
+// a lookup of the record: 52 us for 95,000 rows of 142,000 parts; so 33 us).
 __global__ void __launch_bounds__(32 * kJoinRows, 4) attn_join_kernel(JoinArgs a) {
   const int lane = threadIdx.x & 31;
   const JoinRec j = a.recs[blockIdx.x];

@@ -4,7 +4,9 @@
 //
 // The tensor-core kernel of attn_fwd_tc.cu takes 512 query rows at a time and
 // key tiles of 128 one after the other; with 32 rows its softmax chain, not
-// the memory, set the time (27 us for 54 MB).  Here a block takes up to 32 rows
+// the memory, set the time (25 us for 54 MB, 32 rows and 21 heads; this one 14
+// us, 4 TB/s, from DRAM or from L2: what is left is the latency of six steps, the
+// first copies and the exchange of the results).  Here a block takes up to 32 rows
 // of one head over its share of the prefix, two blocks an SM: K and V stream
 // through a three-stage ring of asynchronous copies (96 KB a block in flight),
 // each of the four warps takes 16 of a stage's 64 keys for all rows -- the

@@ -19,20 +19,23 @@
 // serve both.  Each thread sums sixteen rows of eight dims onto an anchor 2^6
 // times above their largest magnitude: every addition then rounds at one fixed
 // place, and its error is two subtractions away (four operations an element
-// where a two-sum of unordered numbers takes seven; with seven, the fp32 pipe
-// took two thirds of the loads' time).
+// where a two-sum of unordered numbers takes seven: 55 us for 220 MB, q-hat and
+// k-hat of 20,423 tokens and 21 heads; so 40 us, 5.5 TB/s).
 //
 // score_kernel takes eight query blocks of one document and head.  Its warps
 // score 32 dims of 32 tiles at a time, a tile to a lane, against all eight: the
 // key means, tiles innermost, are read once per block and straight into
-// registers, the query means come from shared memory as broadcasts (with a warp per query
-// block and the key means in shared memory, that memory's bandwidth bound it:
-// 22 us for 160 tiles).  Then each warp selects for one query block.  Scores are
-// first plain fp32 sums with an error bound E; the keep-th largest of them, T,
-// is found by a bitwise search over order-preserving keys.  A tile above T + 2 E
-// is kept and one below T - 2 E is not, whatever the exact scores are.  Only
-// where more tiles lie between than places are left (a few per cent of the
-// query blocks, and ties) are the scores between computed as pairs and ranked.
+// registers, a batch of loads ahead, the query means come from shared memory as
+// broadcasts (with a warp per query block and the key means in shared memory,
+// that memory's bandwidth bound it).  Then each warp selects for one query block.
+// Scores are first plain fp32 sums with an error bound E; the keep-th largest of
+// them, T, is found by a bitwise search over order-preserving keys.  A tile
+// above T + 2 E is kept and one below T - 2 E is not, whatever the exact scores
+// are.  Only where more tiles lie between than places are left (3 of 1,680 query
+// blocks with 160 tiles, and ties) are the scores between computed as pairs and
+// ranked.  It is a chain of waits: 10 us after the pooling for 80 query blocks of
+// 160 tiles and 21 heads, half of it hidden behind the pooling's tail (its launch
+// is a programmatic dependent one).
 #include "device_common.cuh"
 #include "qk_norm.cuh"
 
