@@ -161,8 +161,8 @@ struct Cfg {
   static constexpr uint32_t SmemKV = QTiles * QTileBytes;
   static constexpr uint32_t SmemBar = SmemKV + Slots * SlotBytes;
   static constexpr uint32_t SmemMisc = SmemBar + NumBars * 8;
-  static constexpr uint32_t SmemSteps = SmemMisc + 16;  // kPair: steps of each stream's segments [2][4]
-  static constexpr size_t SmemAlloc = SmemSteps + (kPair ? 32 : 0) + 1024;  // slack to align the base to 1 KB
+  static constexpr uint32_t SmemSteps = SmemMisc + 16;  // kPair: of each stream's last segments [2][4][4] (see steps_of)
+  static constexpr size_t SmemAlloc = SmemSteps + (kPair ? 128 : 0) + 1024;  // slack to align the base to 1 KB
   static_assert(SmemAlloc <= 227 * 1024, "shared memory per CTA");
 };
 constexpr uint32_t kQHalfBytes = 128 * 128;            // bf16 Q tile: one half (64 dims)
@@ -220,9 +220,9 @@ struct Bars {
 // its query block, the shared prefix's tiles and then the document's.
 constexpr int kWalkDoc = 0, kWalkList = 1, kWalkPrefix = 2;
 
-// kPair (list walk, 256-row segments: 256-row query blocks, and the halves of
-// 512-row ones with short lists): a CTA pair runs two streams of segments, each
-// with walks of its own -- different lists, of any documents and heads.  Query tile s of both CTAs (rows
+// kPair (the other walks, segments of up to 256 rows: 256-row query blocks, and
+// where the walks are short): a CTA pair runs two streams of segments, each with
+// walks of its own -- different lists, of any documents and heads.  Query tile s of both CTAs (rows
 // q0 + 128 rank + i) belongs to stream s.  The streams share nothing but the
 // tensor cores: the issuer takes whichever stream's next P is ready, and stream
 // 1 begins half a segment after stream 0, so that one stream's segment boundary
@@ -232,7 +232,9 @@ constexpr int kWalkDoc = 0, kWalkList = 1, kWalkPrefix = 2;
 // two groups of the ring: group n of stream s, ring slots 4 s + 2 (n & 1) and the
 // one after it, holds V(n - 1) and K(n), n counting the stream's steps.  A Q
 // slot is free once its segment's last QK is done, a step before the segment
-// ends, so one per stream is enough; O rows are stored directly.
+// ends, so one per stream is enough; O rows are stored directly.  (The extra
+// tiles cost a step 11 %: with the operands' reads they fill shared memory's
+// bandwidth; the step's time does not depend on where in L2 the tiles lie.)
 // Warp 9 loads stream 0 and warp 10 stream 1: lane 0 Q, K and V in the order the
 // stream needs them, lane 1 reports each Q tile landed.
 // Measured, us for 512 rows of a head (two segments) and 2 / 4 / 8 / 16 tiles: one
@@ -668,7 +670,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                        ForwardArgs a, int o_tma, const __grid_constant__ Walk<kWalk> walk) {
   static_assert(!kFp8 || kWalk == kWalkDoc, "the FP8 pipeline walks documents");
-  static_assert(!kPair || kWalk == kWalkList, "two segments side by side: the list walk");
+  static_assert(!kPair || kWalk != kWalkDoc, "two streams: the other walks");
   using C = Cfg<kFp8, kPair>;
   constexpr int kSlots = C::Slots, kGroups = C::Groups;
   extern __shared__ unsigned char smem_raw[];
@@ -687,7 +689,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int u_begin = kPair ? 0 : __ldg(a.unit_off + pair), u_end = kPair ? 0 : __ldg(a.unit_off + pair + 1);
   const auto stream_begin = [&](int s) { return __ldg(a.unit_off + 4 * pair + 2 * s); };
   const auto stream_end = [&](int s) { return __ldg(a.unit_off + 4 * pair + 2 * s + 1); };
-  volatile int* const steps_of = reinterpret_cast<volatile int*>(smem + C::SmemSteps);  // kPair: [s][ordinal & 3]
+  // kPair: at 4 (4 s + (ordinal & 3)): a segment's steps, the first of its steps
+  // over a table's own tile (prefix walk; none: the steps), and that entry
+  volatile int* const steps_of = reinterpret_cast<volatile int*>(smem + C::SmemSteps);
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -734,6 +738,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   dev::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // the tensor map of a walk's tile
+  const auto k_map = [&](const KeyTile& t) {
+    if constexpr (kWalk == kWalkPrefix) return t.prefix ? &walk.tm_k : &tm_k;
+    return &tm_k;
+  };
+  const auto v_map = [&](const KeyTile& t) {
+    if constexpr (kWalk == kWalkPrefix) return t.prefix ? &walk.tm_v : &tm_v;
+    return &tm_v;
+  };
+
   if (kPair && (warp == kTmaWarp || warp == kQWarp)) {
     // ------------------------------------------- kPair: a stream's loads ----
     if constexpr (kPair) {
@@ -751,7 +765,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // with this segment's first K, is on its way)
           ok = dev::mbar_wait(bars.q_empty(st), ((u - ub) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
           if (!ok) break;
-          steps_of[4 * st + ((u - ub) & 3)] = g.hi;  // (the issuer reads it after Q-ready)
+          volatile int* const info = steps_of + 4 * (4 * st + ((u - ub) & 3));  // (the issuer reads it after Q-ready)
+          info[0] = g.hi - g.lo;
+          info[1] = g.hi - g.lo;
+          if constexpr (kWalk == kWalkPrefix)
+            if (g.n > 0) {
+              info[1] = walk.tiles - g.lo;
+              info[2] = g.kv0;
+            }
           const uint32_t dst = sbase + C::SmemQ + st * C::QTileBytes;
           const int32_t row = tile_row<kPair>(g, st, rank);
           dev::mbar_arrive_expect_tx(bars.q_full(st), C::QTileBytes);
@@ -761,13 +782,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (u == ub) {
             ok = dev::mbar_wait(bars.kv_empty(2 * st), 1, abort_flag, a.err, kTimeoutNs);
             if (!ok) break;
-            entry = walk_entry<kWalk>(g, 0, walk);
+            entry = walk_entry<kWalk>(g, g.lo, walk);
+            const KeyTile t = key_tile<kWalk>(g, g.lo, entry, walk);
             dev::mbar_arrive_expect_tx(bars.kv_full(2 * st), C::SlotBytes);
-            load_k_half<kFp8>(sbase + C::SmemKV + (4 * st + 1) * C::SlotBytes, &tm_k, bars.kv_full(2 * st), g.head,
-                              key_tile<kWalk>(g, 0, entry, walk).row, rank, pol_kv);
+            load_k_half<kFp8>(sbase + C::SmemKV + (4 * st + 1) * C::SlotBytes, k_map(t), bars.kv_full(2 * st), g.head,
+                              t.row, rank, pol_kv);
             n = 1;
           }
-          for (int j = 0; ok && j < g.hi; ++j) {
+          for (int j = g.lo; ok && j < g.hi; ++j) {
             const KeyTile vt = key_tile<kWalk>(g, j, entry, walk);
             KeyTile kt = vt;
             int k_head = g.head;
@@ -777,8 +799,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               kt = key_tile<kWalk>(g, j + 1, entry, walk);
             } else if (has_k) {
               const UnitGeom gn = unit_geom<kWalk>(a.units, u + 1, walk);
-              entry = walk_entry<kWalk>(gn, 0, walk);
-              kt = key_tile<kWalk>(gn, 0, entry, walk);
+              entry = walk_entry<kWalk>(gn, gn.lo, walk);
+              kt = key_tile<kWalk>(gn, gn.lo, entry, walk);
               k_head = gn.head;
             }
             if (vt.bad && rank == 0) atomicExch(a.err, kErrBlockIndex);
@@ -787,8 +809,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok) break;
             const uint32_t slot = sbase + C::SmemKV + (4 * st + 2 * (n & 1)) * C::SlotBytes;
             dev::mbar_arrive_expect_tx(bars.kv_full(b), has_k ? 2 * C::SlotBytes : C::SlotBytes);
-            load_v_half<kFp8>(slot, &tm_v, bars.kv_full(b), g.head, vt.row, rank, pol_kv);
-            if (has_k) load_k_half<kFp8>(slot + C::SlotBytes, &tm_k, bars.kv_full(b), k_head, kt.row, rank, pol_kv);
+            load_v_half<kFp8>(slot, v_map(vt), bars.kv_full(b), g.head, vt.row, rank, pol_kv);
+            if (has_k) load_k_half<kFp8>(slot + C::SlotBytes, k_map(kt), bars.kv_full(b), k_head, kt.row, rank, pol_kv);
             ++n;
           }
         }
@@ -871,15 +893,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             dev::tma_load_2d(dst + kQHalfBytes, &tm_q, bars.q_full(i), g.head * 128 + 64, row, pol_q);
           ++q_use[i];
         }
-      };
-      // the tensor map of a walk's tile
-      auto k_map = [&](const KeyTile& t) {
-        if constexpr (kWalk == kWalkPrefix) return t.prefix ? &walk.tm_k : &tm_k;
-        return &tm_k;
-      };
-      auto v_map = [&](const KeyTile& t) {
-        if constexpr (kWalk == kWalkPrefix) return t.prefix ? &walk.tm_v : &tm_v;
-        return &tm_v;
       };
       int k = 0;
       KeyTile kt;  // the tile whose K was sent last (dense: only its row is used)
@@ -1037,6 +1050,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int left[2], hi[2] = {0, 0}, j[2] = {0, 0}, h[2] = {0, 0};  // segments to go; steps, step and half of this one
         uint32_t t[2] = {0, 0}, k[2] = {0, 0};  // steps and segments of the stream so far
         bool first[2] = {true, true};           // the next barrier is Q-ready
+        int own_from[2] = {0, 0}, own0[2] = {0, 0};  // prefix walk: first step over an own tile, and its entry
+        uint4 skip[2][2];                       // lanes that the own tile's PV leaves alone, loaded a step ahead
         bool ok = true, issued = false;
 #pragma unroll
         for (int s = 0; s < 2; ++s) left[s] = stream_end(s) - stream_begin(s);
@@ -1051,7 +1066,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t ring = sbase + C::SmemKV + 4 * s * C::SlotBytes;
           if (first[s]) {
             const uint32_t kb = ring + (2 * (t[s] & 1) + 1) * C::SlotBytes;
-            hi[s] = steps_of[4 * s + (k[s] & 3)];
+            const volatile int* const info = steps_of + 4 * (4 * s + (k[s] & 3));
+            hi[s] = info[0];
+            if constexpr (kWalk == kWalkPrefix) {
+              own_from[s] = info[1];
+              own0[s] = info[2];
+            }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               issue_qk(d + 64 * x, qa, kb + x * kHalfKeyRowsBytes);
@@ -1064,7 +1084,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             return;
           }
           const uint32_t vb = ring + 2 * ((t[s] + 1) & 1) * C::SlotBytes;
-          issue_pv(tmem + 256 + s * 128, d + 64 * h[s], vb + 4096 * h[s], j[s] > 0 || h[s] == 1);
+          if (kWalk == kWalkPrefix && j[s] >= own_from[s])
+            issue_pv_skip(tmem + 256 + s * 128, d + 64 * h[s], vb + 4096 * h[s], true, skip[s][0], skip[s][1]);
+          else
+            issue_pv(tmem + 256 + s * 128, d + 64 * h[s], vb + 4096 * h[s], j[s] > 0 || h[s] == 1);
           if (j[s] + 1 < hi[s]) {
             issue_qk(d + 64 * h[s], qa, vb + C::SlotBytes + h[s] * kHalfKeyRowsBytes);
             commit_pair_elect(bars.s_ready(s, 0) + 8 * h[s]);
@@ -1078,6 +1101,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               j[s] = 0;
               --left[s];
               first[s] = true;
+            } else if constexpr (kWalk == kWalkPrefix) {
+              if (j[s] >= own_from[s]) {
+                const uint4* p = reinterpret_cast<const uint4*>(walk.own[own0[s] + j[s] - own_from[s]].skip[0]);
+                skip[s][0] = __ldg(p);
+                skip[s][1] = __ldg(p + 1);
+              }
             }
           }
           h[s] ^= 1;
@@ -1354,7 +1383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------- softmax ----
     const int st = warp >> 2;            // query tile of this warpgroup
     const uint32_t row_in_tile = threadIdx.x & 127;
-    const uint32_t row_in_unit = st * 2 * kTileRows + rank * kTileRows + row_in_tile;  // (not kPair)
+    const uint32_t row_in_unit = (kPair ? 0 : st * 2 * kTileRows) + rank * kTileRows + row_in_tile;
     const uint32_t lane_base = (warp & 3) * 32;
     const uint32_t t_s = tmem + (lane_base << 16) + st * 128;        // S_s / P_s
     const uint32_t t_o = tmem + (lane_base << 16) + 256 + st * 128;  // O_s
@@ -2148,7 +2177,8 @@ cudaError_t launch_forward_prefix(const ForwardArgs& a, const WalkArgs& w, cudaS
   if (!make_map(&walk.tm_k, w.k_prefix, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, n, row, kTileRows / 2, why) ||
       !make_map(&walk.tm_v, w.v_prefix, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, inner, n, row, kTileRows, why))
     return cudaErrorInvalidValue;
-  return launch_walk<kWalkPrefix, false>(m, a, w, walk, stream, why);
+  return w.pair ? launch_walk<kWalkPrefix, true>(m, a, w, walk, stream, why)
+                : launch_walk<kWalkPrefix, false>(m, a, w, walk, stream, why);
 }
 
 cudaError_t launch_forward_fp8(const ForwardArgs& a, int device, int num_sms, cudaStream_t stream,

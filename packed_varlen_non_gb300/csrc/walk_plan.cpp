@@ -46,29 +46,29 @@ struct Join {
   int32_t key_lo, key_hi;
 };
 
-// Times in key-tile periods of a CTA pair (1.28 us on GB300).  A segment costs
-// its tiles and three periods (4 us, measured for segments of 1 to 16 tiles on
-// every walk: the pipeline runs empty at its end, and the tensor pipe resumes
-// at a third of its rate for a while), and another one where it leaves partial
-// rows.  The join takes kJoinStart, and a period for kJoinRowsPerPeriod partial
-// rows (141,658 of them measured 33 us); in a chunk of the prefix walk, a
-// period for kRowsPerPeriod of its rows, written and read by its pair's share.
-constexpr int kRowsPerPeriod = 87;
-constexpr double kJoinRowsPerPeriod = 5500.0;
-constexpr double kJoinStart = 2.5;
+// Times in hundredths of a microsecond, as measured on GB300 for segments of 1 to
+// 32 tiles.  A CTA pair runs one segment of up to kUnitRows rows at a time (1.28
+// us a tile, and 4 us for its boundary, where the pipeline runs empty), or two
+// streams of segments of half as many rows (1.50 us for a tile of each: every
+// segment's K and V tiles come from L2 for half the rows, and with them shared
+// memory's bandwidth runs short; but a boundary costs 1.7 us, as the other stream
+// goes on).  So streams suit short walks, and rows of many documents, whose own
+// tiles then take half as many rows along: 100 documents of 100 tokens over 512
+// prefix rows 93 against 119 us, three of 4,096 over 2,430 rows 559 against 512.
+// Partial rows cost a segment 1.3 us, and the join kJoinStart and kJoinRow for
+// each (142,000 of them measured 33 us).
+int64_t piece_cost(int32_t tiles, bool partial, int streams) {
+  return (streams == 2 ? (int64_t)150 * tiles + 170 : (int64_t)128 * tiles + 400) + (partial ? 130 : 0);
+}
+constexpr double kJoinStart = 320.0;
+constexpr double kJoinRow = 0.0233;
+// Rows of a chunk of the prefix walk whose partial rows cost a tile's time.
+constexpr int kRowsPerTile = 87;
 
-// Query blocks of 512 rows with lists of at most this many tiles run as two
-// segments of 256 in the two streams of a pair rather than as one of 512: the
-// streams hide each other's segment boundaries, the one segment reads every K
-// and V tile once.  Measured per 512 rows and head on a CTA pair, us, for lists
-// of 2 / 4 / 8 / 16 tiles: two streams 5.4 / 7.7 / 13.0 / 24.1, one 6.8 / 9.1 /
-// 14.2 / 24.5; a tile more costs 1.4 against 1.28.
-constexpr int32_t kTwoStreamTiles = 12;
-
-int64_t piece_cost(int32_t tiles, bool partial) { return (int64_t)tiles + 3 + (partial ? 1 : 0); }
-
-// Splits a tail of the items (in list order) so that the pairs finish together.
-void balance(std::vector<Item>& items, int G) {
+// Splits a tail of the items (in list order) so that the pairs finish together;
+// returns the estimated time.
+double balance(std::vector<Item>& items, int pairs, int streams) {
+  const int G = pairs * streams;
   const size_t U = items.size();
   std::vector<int32_t> pair_of, heap(G);
   std::vector<int64_t> load(G), cost;
@@ -83,13 +83,13 @@ void balance(std::vector<Item>& items, int G) {
       const int32_t n = i < whole ? 1 : items[i].split(m);
       const bool partial = !items[i].direct || n > 1;
       for (int32_t c = 0; c < n; ++c)
-        cost.push_back(piece_cost(bound(items[i], c + 1, n) - bound(items[i], c, n), partial));
+        cost.push_back(piece_cost(bound(items[i], c + 1, n) - bound(items[i], c, n), partial, streams));
       if (partial) rows += (int64_t)n * items[i].rows();
     }
     pair_of.resize(cost.size());
     assign_pairs(cost.size(), [&](size_t i) { return cost[i]; }, G, pair_of.data(), load.data(), heap.data());
     double score = (double)*std::max_element(load.begin(), load.end());
-    if (rows > 0) score += kJoinStart + (double)rows / kJoinRowsPerPeriod;
+    if (rows > 0) score += kJoinStart + (double)rows * kJoinRow;
     if (best < 0.0 || score < best) {
       best = score;
       for (size_t i = 0; i < U; ++i)
@@ -108,6 +108,7 @@ void balance(std::vector<Item>& items, int G) {
     }
   }
   for (size_t i = 0; i < U; ++i) items[i].pieces = best_pieces[i];
+  return best;
 }
 
 // Pieces, partial rows, placement and join records of the balanced items.
@@ -127,7 +128,7 @@ std::string finish(std::vector<Item>& items, std::vector<Join>& joins, int G, Ma
       WalkUnit s = make(it, c);
       s.part = it.partial() ? it.part + c * it.rows() : -1;
       segs.push_back(s);
-      cost.push_back(piece_cost(bound(it, c + 1, it.pieces) - bound(it, c, it.pieces), it.partial()));
+      cost.push_back(piece_cost(bound(it, c + 1, it.pieces) - bound(it, c, it.pieces), it.partial(), w.streams));
     }
   }
   w.part_rows = rows;
@@ -191,21 +192,29 @@ std::string build_list_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads
   // one moment read the K and V of one or two heads, which stay in L2
   std::stable_sort(order.begin(), order.end(),
                    [cu](int32_t x, int32_t y) { return cu[x + 1] - cu[x] > cu[y + 1] - cu[y]; });
-  // 256-row segments in two streams a pair, or 512-row ones in one
-  w.streams = q_block == kUnitRows && max_blocks > kTwoStreamTiles ? 1 : 2;
-  const int32_t seg_rows = w.streams == 2 ? kUnitRows / 2 : kUnitRows;
+  // 256-row segments in two streams a pair, or, where the blocks allow it,
+  // 512-row ones in one: whichever is estimated to finish first
   std::vector<Item> items;
-  for (int32_t d : order) {
-    const int32_t b = cu[d], e = cu[d + 1];
-    const int32_t tiles = std::min(max_blocks, (e - b + kKeyTile - 1) / kKeyTile);
-    for (int32_t h = 0; h < num_heads; ++h)
-      for (int32_t r = b; r < e;) {
-        const int32_t end = (int32_t)std::min<int64_t>((int64_t)r + seg_rows, e);
-        items.push_back(Item{WalkUnit{r, end, b, e, h, block0[d] + (r - b) / q_block, 0, -1}, tiles, tiles, true});
-        r = end;
-      }
+  double best = -1.0;
+  for (int streams = q_block == kUnitRows ? 1 : 2; streams <= 2; ++streams) {
+    std::vector<Item> list;
+    for (int32_t d : order) {
+      const int32_t b = cu[d], e = cu[d + 1];
+      const int32_t tiles = std::min(max_blocks, (e - b + kKeyTile - 1) / kKeyTile);
+      for (int32_t h = 0; h < num_heads; ++h)
+        for (int32_t r = b; r < e;) {
+          const int32_t end = (int32_t)std::min<int64_t>((int64_t)r + kUnitRows / streams, e);
+          list.push_back(Item{WalkUnit{r, end, b, e, h, block0[d] + (r - b) / q_block, 0, -1}, tiles, tiles, true});
+          r = end;
+        }
+    }
+    const double time = balance(list, G, streams);
+    if (best < 0.0 || time < best) {
+      best = time;
+      w.streams = streams;
+      items.swap(list);
+    }
   }
-  balance(items, w.streams * G);
   for (Item& it : items) it.pieces = std::min(it.pieces, 65535);  // the field's width
   std::vector<Join> joins;
   return finish(items, joins, G, [](const Item& it, int32_t c) {
@@ -220,6 +229,97 @@ static WalkUnit prefix_piece(const Item& it, int32_t c) {
   s.a = bound(it, c, it.pieces);
   s.b = bound(it, c + 1, it.pieces);
   return s;
+}
+
+// The prefix walk's segments of up to kUnitRows / streams rows, not yet balanced.
+static std::string prefix_items(const int32_t* cu, int32_t n_docs, int32_t num_heads, int32_t tp, int streams,
+                                std::vector<OwnTile>& own_tiles, std::vector<Item>& items, std::vector<Join>& joins) {
+  const int32_t most = kUnitRows / streams;
+  // The rows are cut into chunks of up to `most` rows, which walk the prefix once
+  // for all their rows and then their documents' own tiles.  A document joins the
+  // open chunk of the documents before it unless that costs it a chunk more.
+  struct Piece {
+    int32_t doc, row0, row1;
+  };
+  std::vector<std::vector<Piece>> chunks;
+  int32_t filled = 0;  // rows of the last chunk
+  const auto tiles_of = [cu](int32_t d) { return (cu[d + 1] - cu[d] + kKeyTile - 1) / kKeyTile; };
+  for (int32_t d = 0; d < n_docs; ++d) {
+    const int32_t L = cu[d + 1] - cu[d];
+    int32_t at = cu[d];
+    if (filled > 0 && filled < most) {
+      const int32_t r = std::min(L, most - filled);
+      if ((L - r + most - 1) / most < (L - 1) / most + 1) {
+        chunks.back().push_back(Piece{d, at, at + r});
+        filled += r;
+        at += r;
+      }
+    }
+    while (at < cu[d + 1]) {
+      const int32_t r = std::min(cu[d + 1] - at, most);
+      chunks.push_back({Piece{d, at, at + r}});
+      filled = r;
+      at += r;
+    }
+  }
+  // What a chunk over several documents walks after the prefix.  Documents of
+  // at most kJoinOwnKeys tokens take a whole tile each, for a few keys: where
+  // there are more of them than the chunk's partial rows cost (kRowsPerTile),
+  // the chunk leaves partial rows and the join attends to them.
+  struct Own {
+    int32_t first = 0, n = 0;
+    bool join = false;
+  };
+  std::vector<Own> own(chunks.size());
+  own_tiles.clear();
+  const auto small = [cu](int32_t d) { return cu[d + 1] - cu[d] <= kJoinOwnKeys; };
+  for (size_t c = 0; c < chunks.size(); ++c) {
+    if (chunks[c].size() == 1) continue;
+    const int32_t q0 = chunks[c].front().row0, rows = chunks[c].back().row1 - q0;
+    int32_t tiny = 0;
+    for (const Piece& p : chunks[c]) tiny += small(p.doc);
+    own[c].first = (int32_t)own_tiles.size();
+    own[c].join = tiny > 2 + rows / kRowsPerTile;
+    for (const Piece& p : chunks[c]) {
+      if (own[c].join && small(p.doc)) continue;
+      for (int32_t t = cu[p.doc]; t < cu[p.doc + 1]; t += kKeyTile) {
+        OwnTile o;
+        o.row = t;
+        o.rem = cu[p.doc + 1] - t;
+        o.lo = p.row0 - q0;
+        o.hi = p.row1 - q0;
+        for (int32_t r = 0; r < kUnitRows; r += 32) {
+          uint32_t skip = 0;
+          for (int32_t i = 0; i < 32; ++i) skip |= (uint32_t)(r + i < o.lo || r + i >= o.hi) << i;
+          o.skip[r / 256][r % 256 / 32] = skip;
+        }
+        own_tiles.push_back(o);
+      }
+    }
+    own[c].n = (int32_t)own_tiles.size() - own[c].first;
+    if (own_tiles.size() >= (size_t(1) << 31) / sizeof(OwnTile)) return "the layout needs too large a table of own tiles";
+  }
+  // (a split chunk's pieces beyond the direct ones are joined by finish)
+  // head by head: the pairs running at one moment share a head's prefix in L2
+  for (int32_t h = 0; h < num_heads; ++h) {
+    for (size_t x = 0; x < chunks.size(); ++x) {
+      const std::vector<Piece>& c = chunks[x];
+      const int32_t q0 = c.front().row0, q1 = c.back().row1;
+      if (c.size() == 1) {
+        const int32_t t = tp + tiles_of(c[0].doc);
+        items.push_back(Item{WalkUnit{q0, q1, cu[c[0].doc], cu[c[0].doc + 1], h, 0, t, -1}, t, t, true});
+        continue;
+      }
+      // (n = 0: a chunk of small documents walks the prefix alone)
+      const int32_t t = tp + own[x].n;
+      if (own[x].join)
+        for (const Piece& p : c)
+          joins.push_back(Join{p.row0, p.row1, h, (int32_t)items.size(), small(p.doc) ? cu[p.doc] : 0,
+                               small(p.doc) ? cu[p.doc + 1] : 0});
+      items.push_back(Item{WalkUnit{q0, q1, own[x].first, -own[x].n, h, 0, t, -1}, t, tp, !own[x].join});
+    }
+  }
+  return "";
 }
 
 std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads, int32_t prefix_len, int grid,
@@ -248,93 +348,26 @@ std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_hea
       }
     return finish(items, joins, (int)std::min<size_t>(items.size() * items[0].pieces, size_t(1) << 20), prefix_piece, w);
   }
-  // The rows are cut into chunks of up to kUnitRows, which walk the prefix once
-  // for all their rows and then their documents' own tiles.  A document joins the
-  // open chunk of the documents before it unless that costs it a chunk more.
-  struct Piece {
-    int32_t doc, row0, row1;
-  };
-  std::vector<std::vector<Piece>> chunks;
-  int32_t filled = 0;  // rows of the last chunk
-  const auto tiles_of = [cu](int32_t d) { return (cu[d + 1] - cu[d] + kKeyTile - 1) / kKeyTile; };
-  for (int32_t d = 0; d < n_docs; ++d) {
-    const int32_t L = cu[d + 1] - cu[d];
-    int32_t at = cu[d];
-    if (filled > 0 && filled < kUnitRows) {
-      const int32_t r = std::min(L, kUnitRows - filled);
-      if ((L - r + kUnitRows - 1) / kUnitRows < (L - 1) / kUnitRows + 1) {
-        chunks.back().push_back(Piece{d, at, at + r});
-        filled += r;
-        at += r;
-      }
-    }
-    while (at < cu[d + 1]) {
-      const int32_t r = std::min(cu[d + 1] - at, kUnitRows);
-      chunks.push_back({Piece{d, at, at + r}});
-      filled = r;
-      at += r;
-    }
-  }
-  // What a chunk over several documents walks after the prefix.  Documents of
-  // at most kJoinOwnKeys tokens take a whole tile each, for a few keys: where
-  // there are more of them than the chunk's partial rows cost (kRowsPerPeriod),
-  // the chunk leaves partial rows and the join attends to them.
-  struct Own {
-    int32_t first = 0, n = 0;
-    bool join = false;
-  };
-  std::vector<Own> own(chunks.size());
-  w.own.clear();
-  const auto small = [cu](int32_t d) { return cu[d + 1] - cu[d] <= kJoinOwnKeys; };
-  for (size_t c = 0; c < chunks.size(); ++c) {
-    if (chunks[c].size() == 1) continue;
-    const int32_t q0 = chunks[c].front().row0, rows = chunks[c].back().row1 - q0;
-    int32_t tiny = 0;
-    for (const Piece& p : chunks[c]) tiny += small(p.doc);
-    own[c].first = (int32_t)w.own.size();
-    own[c].join = tiny > 2 + rows / kRowsPerPeriod;
-    for (const Piece& p : chunks[c]) {
-      if (own[c].join && small(p.doc)) continue;
-      for (int32_t t = cu[p.doc]; t < cu[p.doc + 1]; t += kKeyTile) {
-        OwnTile o;
-        o.row = t;
-        o.rem = cu[p.doc + 1] - t;
-        o.lo = p.row0 - q0;
-        o.hi = p.row1 - q0;
-        for (int32_t r = 0; r < kUnitRows; r += 32) {
-          uint32_t skip = 0;
-          for (int32_t i = 0; i < 32; ++i) skip |= (uint32_t)(r + i < o.lo || r + i >= o.hi) << i;
-          o.skip[r / 256][r % 256 / 32] = skip;
-        }
-        w.own.push_back(o);
-      }
-    }
-    own[c].n = (int32_t)w.own.size() - own[c].first;
-    if (w.own.size() >= (size_t(1) << 31) / sizeof(OwnTile)) return "the layout needs too large a table of own tiles";
-  }
-  // (a split chunk's pieces beyond the direct ones are joined by finish)
-  // head by head: the pairs running at one moment share a head's prefix in L2
+  // Longer batches: chunks of 512 rows, or of 256 in two streams a pair, whichever
+  // is estimated to finish first.
   std::vector<Item> items;
   std::vector<Join> joins;
-  for (int32_t h = 0; h < num_heads; ++h) {
-    for (size_t x = 0; x < chunks.size(); ++x) {
-      const std::vector<Piece>& c = chunks[x];
-      const int32_t q0 = c.front().row0, q1 = c.back().row1;
-      if (c.size() == 1) {
-        const int32_t t = tp + tiles_of(c[0].doc);
-        items.push_back(Item{WalkUnit{q0, q1, cu[c[0].doc], cu[c[0].doc + 1], h, 0, t, -1}, t, t, true});
-        continue;
-      }
-      // (n = 0: a chunk of small documents walks the prefix alone)
-      const int32_t t = tp + own[x].n;
-      if (own[x].join)
-        for (const Piece& p : c)
-          joins.push_back(Join{p.row0, p.row1, h, (int32_t)items.size(), small(p.doc) ? cu[p.doc] : 0,
-                               small(p.doc) ? cu[p.doc + 1] : 0});
-      items.push_back(Item{WalkUnit{q0, q1, own[x].first, -own[x].n, h, 0, t, -1}, t, tp, !own[x].join});
+  double best = -1.0;
+  for (int streams = 1; streams <= 2; ++streams) {
+    std::vector<Item> list;
+    std::vector<Join> list_joins;
+    std::vector<OwnTile> own;
+    const std::string why = prefix_items(cu, n_docs, num_heads, tp, streams, own, list, list_joins);
+    if (!why.empty()) return why;
+    const double time = balance(list, G, streams);
+    if (best < 0.0 || time < best) {
+      best = time;
+      w.streams = streams;
+      w.own.swap(own);
+      items.swap(list);
+      joins.swap(list_joins);
     }
   }
-  balance(items, G);
   return finish(items, joins, G, prefix_piece, w);
 }
 
