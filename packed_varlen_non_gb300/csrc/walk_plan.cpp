@@ -86,10 +86,17 @@ double balance(std::vector<Item>& items, int pairs, int streams) {
         cost.push_back(piece_cost(bound(items[i], c + 1, n) - bound(items[i], c, n), partial, streams));
       if (partial) rows += (int64_t)n * items[i].rows();
     }
+    const double join = rows > 0 ? kJoinStart + (double)rows * kJoinRow : 0.0;
+    // (no placement finishes before the mean load or the largest piece)
+    int64_t sum = 0, most = 0;
+    for (int64_t c : cost) {
+      sum += c;
+      most = std::max(most, c);
+    }
+    if (best >= 0.0 && std::max((double)sum / G, (double)most) + join >= best) return;
     pair_of.resize(cost.size());
     assign_pairs(cost.size(), [&](size_t i) { return cost[i]; }, G, pair_of.data(), load.data(), heap.data());
-    double score = (double)*std::max_element(load.begin(), load.end());
-    if (rows > 0) score += kJoinStart + (double)rows * kJoinRow;
+    const double score = (double)*std::max_element(load.begin(), load.end()) + join;
     if (best < 0.0 || score < best) {
       best = score;
       for (size_t i = 0; i < U; ++i)
@@ -97,15 +104,23 @@ double balance(std::vector<Item>& items, int pairs, int streams) {
     }
   };
   consider(U, 1);
+  int32_t longest = 0;
+  for (const Item& it : items) longest = std::max(longest, it.tiles);
   const int64_t round = G, full = (int64_t)U / round * round;
+  std::vector<std::pair<size_t, int32_t>> tried;
+  const auto consider_once = [&](size_t whole, int64_t m) {
+    const std::pair<size_t, int32_t> way(whole, (int32_t)std::max<int64_t>(1, m));
+    if (way.second >= longest || std::find(tried.begin(), tried.end(), way) != tried.end()) return;
+    tried.push_back(way);
+    consider(whole, way.second);
+  };
   for (int64_t back : {(int64_t)0, round / 4, round / 2, round, 2 * round, full}) {
     if (back > full) continue;
     const size_t whole = (size_t)(full - back);
     if (whole == U) continue;
-    for (int r = 1; r <= 4; ++r) {
-      const int64_t m = (tail_tiles[whole] + round * r - 1) / (round * r);
-      consider(whole, (int32_t)std::max<int64_t>(1, m));
-    }
+    // pieces that give every pair 1 .. 4 of them, or cut the longest in 2, 3, 4
+    for (int r = 1; r <= 4; ++r) consider_once(whole, (tail_tiles[whole] + round * r - 1) / (round * r));
+    for (int n = 2; n <= 4; ++n) consider_once(whole, (longest + n - 1) / n);
   }
   for (size_t i = 0; i < U; ++i) items[i].pieces = best_pieces[i];
   return best;
@@ -232,8 +247,11 @@ static WalkUnit prefix_piece(const Item& it, int32_t c) {
 }
 
 // The prefix walk's segments of up to kUnitRows / streams rows, not yet balanced.
+// mix_long: documents longer than a chunk share chunks too, which saves passes
+// over the prefix but makes segments that walk several long documents and cannot
+// be split there.
 static std::string prefix_items(const int32_t* cu, int32_t n_docs, int32_t num_heads, int32_t tp, int streams,
-                                std::vector<OwnTile>& own_tiles, std::vector<Item>& items, std::vector<Join>& joins) {
+                                bool mix_long, std::vector<OwnTile>& own_tiles, std::vector<Item>& items, std::vector<Join>& joins) {
   const int32_t most = kUnitRows / streams;
   // The rows are cut into chunks of up to `most` rows, which walk the prefix once
   // for all their rows and then their documents' own tiles.  A document joins the
@@ -246,8 +264,9 @@ static std::string prefix_items(const int32_t* cu, int32_t n_docs, int32_t num_h
   const auto tiles_of = [cu](int32_t d) { return (cu[d + 1] - cu[d] + kKeyTile - 1) / kKeyTile; };
   for (int32_t d = 0; d < n_docs; ++d) {
     const int32_t L = cu[d + 1] - cu[d];
+    const bool alone = L > most && !mix_long;
     int32_t at = cu[d];
-    if (filled > 0 && filled < most) {
+    if (filled > 0 && filled < most && !alone) {
       const int32_t r = std::min(L, most - filled);
       if ((L - r + most - 1) / most < (L - 1) / most + 1) {
         chunks.back().push_back(Piece{d, at, at + r});
@@ -258,7 +277,7 @@ static std::string prefix_items(const int32_t* cu, int32_t n_docs, int32_t num_h
     while (at < cu[d + 1]) {
       const int32_t r = std::min(cu[d + 1] - at, most);
       chunks.push_back({Piece{d, at, at + r}});
-      filled = r;
+      filled = alone ? most : r;
       at += r;
     }
   }
@@ -348,16 +367,19 @@ std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_hea
       }
     return finish(items, joins, (int)std::min<size_t>(items.size() * items[0].pieces, size_t(1) << 20), prefix_piece, w);
   }
-  // Longer batches: chunks of 512 rows, or of 256 in two streams a pair, whichever
-  // is estimated to finish first.
+  // Longer batches: chunks of 512 rows, or of 256 in two streams a pair, long
+  // documents sharing chunks or not, whichever is estimated to finish first.
   std::vector<Item> items;
   std::vector<Join> joins;
   double best = -1.0;
-  for (int streams = 1; streams <= 2; ++streams) {
+  for (int way = 0; way < 4; ++way) {
+    const int streams = 1 + way / 2;
+    const bool mix_long = way % 2 == 0;
+    if (!mix_long && longest <= kUnitRows / streams) continue;
     std::vector<Item> list;
     std::vector<Join> list_joins;
     std::vector<OwnTile> own;
-    const std::string why = prefix_items(cu, n_docs, num_heads, tp, streams, own, list, list_joins);
+    const std::string why = prefix_items(cu, n_docs, num_heads, tp, streams, mix_long, own, list, list_joins);
     if (!why.empty()) return why;
     const double time = balance(list, G, streams);
     if (best < 0.0 || time < best) {
