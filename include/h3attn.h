@@ -355,8 +355,8 @@ h3attn_status h3attn_forward_sparse(h3attn_plan_t plan, const void* q, const voi
  * variants of a request over the same reference images, or single queries over
  * a finished context ([SPARK] step-invariant caches: the prefix's k-hat and v
  * are computed once per request and block and kept).  Rows of different
- * documents share the passes over the prefix, so that it is read once per 512
- * rows of the batch rather than once per document.
+ * documents share the passes over the prefix, so that it is read once per 256
+ * or 512 rows of the batch rather than once per document.
  *
  * h3attn_plan_set_prefix adds the work list for a prefix of prefix_len >= 1
  * rows to a plan whose documents are the batch; allocation, capture and "once
@@ -396,8 +396,10 @@ h3attn_status h3attn_forward_prefix(h3attn_plan_t plan, const void* q, const voi
  *            over several documents, whose n own tiles are entries [document
  *            begin, document begin + n) of own; last the first partial row (-1: the
  *            segment writes the output itself);
- *            With q_block 256, a pair runs two streams of segments side by side
- *            (the first one's come first here);
+ *            where segments have at most 256 rows, a pair may run two streams of
+ *            them side by side (the first one's come first here); for kind 1 and at
+ *            most 64 rows in documents of at most 32 tokens each segment is a
+ *            thread block's, and there are as many "pairs" as segments;
  *   unit_off [*n_pairs_used + 1] int32: pair p runs units [unit_off[p], unit_off[p + 1]);
  *   joins    [*n_joins][12] int32, the rows combined from partial rows: rows
  *            [r0, r1) (at most 8), head, and of their segment the first query

@@ -318,7 +318,6 @@ static std::string prefix_items(const int32_t* cu, int32_t n_docs, int32_t num_h
     own[c].n = (int32_t)own_tiles.size() - own[c].first;
     if (own_tiles.size() >= (size_t(1) << 31) / sizeof(OwnTile)) return "the layout needs too large a table of own tiles";
   }
-  // (a split chunk's pieces beyond the direct ones are joined by finish)
   // head by head: the pairs running at one moment share a head's prefix in L2
   for (int32_t h = 0; h < num_heads; ++h) {
     for (size_t x = 0; x < chunks.size(); ++x) {
