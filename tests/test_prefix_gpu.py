@@ -146,6 +146,20 @@ def test_offsets_past_32_bits(lib):
     assert torch.equal(o2, o) and torch.equal(lse2, lse)
 
 
+@pytest.mark.parametrize("lens", [[1, 20], [1] * 33])
+def test_few_rows_offsets_past_32_bits(lib, lens):
+    stride, P, heads = 1 << 20, 2200, 1
+    p = W.Prefix(lens, heads, P)
+    t = tensors(lens, heads, P, 51)
+    o, lse = p.forward(*t)
+    big = torch.empty(P, stride, dtype=torch.bfloat16, device="cuda")
+    kp, vp = (big[:P, 256 * i:256 * i + 128] for i in (3, 4))
+    for dst, src in zip((kp, vp), t[3:]):
+        dst.copy_(W.flat(src))
+    o2, lse2 = p.forward(*t[:3], kp, vp)
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)
+
+
 def test_captured_and_replayed_on_new_inputs(lib):
     lens, heads, P = [1, 600, 20, 50], 3, 900
     p = W.Prefix(lens, heads, P)
