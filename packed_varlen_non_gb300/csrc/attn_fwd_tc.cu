@@ -1843,7 +1843,7 @@ __global__ void __launch_bounds__(256, 8) attn_merge_kernel(ForwardArgs a) {
 }
 
 // Output rows of the list and prefix walks that no segment finishes alone: one
-// warp per query row, four dims per lane.  A row's parts are the partial rows of
+// to eight warps per query row, four dims per lane.  A row's parts are the partial rows of
 // its segment's pieces and, for small documents that share a segment with many
 // others, the softmax over the document's own keys (at most kJoinOwnKeys),
 // computed here in fp32 from q, k and v: a tile of the segment's walk each would
@@ -1870,22 +1870,31 @@ __device__ __forceinline__ float4 load_bf16x4(const __nv_bfloat16* p) {
                      __uint_as_float(w.y & 0xffff0000u));
 }
 
-constexpr int kAtOnce = 8;
+constexpr int kAtOnce = kJoinParts;
 
 // The rows of a record are a block's; parts are read kAtOnce at a time with their
 // maxima and rows together, in one pass with a running maximum, so that a row
 // waits for memory about once (two passes over the maxima and then the rows, and
-// a lookup of the record: 52 us for 95,000 rows of 142,000 parts; so 33 us).
+// a lookup of the record: 52 us for 95,000 rows of 142,000 parts; so 33 us).  A
+// row of more parts has several warps, whose sums meet in shared memory, in the
+// warps' order (eight single queries over 12,000 rows, two heads: 94 parts a row,
+// 19 us with one warp, 7 with eight).
 __global__ void __launch_bounds__(32 * kJoinRows, 4) attn_join_kernel(JoinArgs a) {
-  const int lane = threadIdx.x & 31;
+  __shared__ float4 o_of[kJoinRows][32];
+  __shared__ float2 ml_of[kJoinRows];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const JoinRec j = a.recs[blockIdx.x];
-  const int32_t row = j.row0 + (int32_t)(threadIdx.x >> 5);
-  if (row >= j.row1) return;
+  const int rows = j.row1 - j.row0;
+  const int shift = join_warps_log2(rows, j.n);  // a row has 1 << shift warps
+  const int w = warp & ((1 << shift) - 1);                           // this one of them
+  const int32_t row = j.row0 + (warp >> shift);
+  const bool active = row < j.row1;
   // own keys (inputs of the forward: they need not wait for it), four at a time
   // with their values
   float M = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int n_own = j.key_hi - j.key_lo;
+  const int n_keys = active ? j.key_hi - j.key_lo : 0;
+  const int key0 = j.key_lo + (n_keys * w >> shift), n_own = (n_keys * (w + 1) >> shift) - (n_keys * w >> shift);
   if (n_own > 0) {
     const int64_t col = (int64_t)j.head * kHeadDim + 4 * lane;
     const float4 q = load_bf16x4(a.q + (int64_t)row * a.stride + col);
@@ -1895,7 +1904,7 @@ __global__ void __launch_bounds__(32 * kJoinRows, 4) attn_join_kernel(JoinArgs a
       float4 k[4], v[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const int64_t at = (int64_t)(j.key_lo + min(x0 + x, n_own - 1)) * a.stride + col;
+        const int64_t at = (int64_t)(key0 + min(x0 + x, n_own - 1)) * a.stride + col;
         k[x] = load_bf16x4(a.k + at);
         v[x] = load_bf16x4(a.v + at);
       }
@@ -1927,15 +1936,17 @@ __global__ void __launch_bounds__(32 * kJoinRows, 4) attn_join_kernel(JoinArgs a
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the forward is complete and its writes visible
   const int64_t r0 = (int64_t)j.part + (row - j.q_row0);
+  const int n_parts = active ? j.n : 0;
+  const int c0 = (int)((int64_t)n_parts * w >> shift), c1 = (int)((int64_t)n_parts * (w + 1) >> shift);
 #pragma unroll 1
-  for (int c = 0; c < j.n; c += kAtOnce) {
+  for (int c = c0; c < c1; c += kAtOnce) {
     float2 ml[kAtOnce];
     float4 o[kAtOnce];
 #pragma unroll
     for (int x = 0; x < kAtOnce; ++x) {
       ml[x] = make_float2(-INFINITY, 0.f);
       o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c + x < j.n) {
+      if (c + x < c1) {
         const int64_t r = r0 + (int64_t)(c + x) * j.rows;
         ml[x] = a.part_ml[r];
         o[x] = reinterpret_cast<const float4*>(a.part_o + r * kHeadDim)[lane];
@@ -1958,6 +1969,31 @@ __global__ void __launch_bounds__(32 * kJoinRows, 4) attn_join_kernel(JoinArgs a
       l = fmaf(wx, ml[x].y, l);
     }
     M = m_new;
+  }
+  if (shift > 0) {
+    if (lane == 0) ml_of[warp] = make_float2(M, l);
+    o_of[warp][lane] = acc;
+    __syncthreads();
+    if (w > 0 || !active) return;
+    const int n = 1 << shift;
+    float m_all = M;
+    for (int x = 1; x < n; ++x) m_all = fmaxf(m_all, ml_of[warp + x].x);
+    const float ref = m_all == -INFINITY ? 0.f : m_all;
+    const float own = dev::ex2_approx(M - ref);
+    acc = make_float4(own * acc.x, own * acc.y, own * acc.z, own * acc.w);
+    l *= own;
+    for (int x = 1; x < n; ++x) {
+      const float wx = dev::ex2_approx(ml_of[warp + x].x - ref);
+      const float4 o = o_of[warp + x][lane];
+      acc.x = fmaf(wx, o.x, acc.x);
+      acc.y = fmaf(wx, o.y, acc.y);
+      acc.z = fmaf(wx, o.z, acc.z);
+      acc.w = fmaf(wx, o.w, acc.w);
+      l = fmaf(wx, ml_of[warp + x].y, l);
+    }
+    M = m_all;
+  } else if (!active) {
+    return;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   __nv_bfloat16* dst = a.o + (int64_t)row * a.o_stride + j.head * kHeadDim + 4 * lane;
@@ -2113,7 +2149,7 @@ cudaError_t launch_join(const ForwardArgs& a, const WalkArgs& w, cudaStream_t st
                    a.scale_log2,
                    a.part_o,
                    a.part_ml};
-  const cudaError_t e = launch_dependent(attn_join_kernel, (unsigned)w.n_joins, 32u * kJoinRows, stream, j);
+  const cudaError_t e = launch_dependent(attn_join_kernel, (unsigned)w.n_joins, 32u * (unsigned)w.join_warps, stream, j);
   if (e != cudaSuccess && why) *why = "the join launch failed";
   return e;
 }

@@ -779,6 +779,7 @@ static WalkArgs walk_args(const WalkPlan& w) {
   WalkArgs x{};
   x.joins = w.d_joins;
   x.n_joins = (int32_t)w.joins.size();
+  x.join_warps = w.join_warps;
   x.pair = w.streams == 2;
   x.pieces = w.pieces;
   return x;

@@ -119,8 +119,8 @@ struct OwnTile {
 };
 static_assert(sizeof(OwnTile) == 80, "OwnTile is read as five 16-byte vectors");
 
-// Rows [row0, row1) of one head (at most kJoinRows: a block of the join, one warp
-// each) whose output the join pass combines from n partial rows each, piece c of
+// Rows [row0, row1) of one head (a block of the join: at most kJoinRows, a warp
+// each; fewer where a row has so many parts that several warps share them) whose output the join pass combines from n partial rows each, piece c of
 // row r at partial row part + c * rows + (r - q_row0), and from the keys [key_lo,
 // key_hi) of the rows' document, which the join itself attends to (none when
 // key_lo == key_hi).
@@ -130,13 +130,25 @@ struct JoinRec {
   int32_t key_hi, pad[3];
 };
 static_assert(sizeof(JoinRec) == 48, "JoinRec is read as three 16-byte vectors");
-constexpr int kJoinRows = 8;         // rows per join block (one warp each)
+constexpr int kJoinRows = 8;         // warps of a join block, and its most rows
+constexpr int kJoinParts = 8;        // parts that a warp of the join reads at once
+
+// log2 of the warps that a row of a join record has: enough to read its n parts
+// at once, as far as kJoinRows warps go round its rows.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int join_warps_log2(int32_t rows, int32_t n) {
+  int s = 0;
+  while ((rows << (s + 1)) <= kJoinRows && (kJoinParts << s) < n) ++s;
+  return s;
+}
 constexpr int kJoinOwnKeys = 32;     // longest document the join may attend to itself
 
-// A few short documents over a prefix (attn_rows.cu): at most kRowsMax rows in
-// all, kRowsTile of them and one head to a segment, a block each.
+// A few short documents over a prefix (attn_rows.cu): kRowsTile rows and one head
+// to a segment, a block each; never more than kRowsMax rows in all.
 constexpr int kRowsTile = 32;
-constexpr int kRowsMax = 64;
+constexpr int kRowsMax = 1024;
 
 struct WalkPlan {
   bool set = false;
@@ -148,6 +160,7 @@ struct WalkPlan {
   int32_t n_pairs = 0;
   std::vector<OwnTile> own;            // prefix walk
   std::vector<JoinRec> joins;
+  int32_t join_warps = 0;              // warps of a join block: the most that a record needs
   int64_t part_rows = 0;               // partial rows of all segments
 
   WalkUnit* d_units = nullptr;         // units, then unit_off
@@ -371,7 +384,7 @@ cudaError_t launch_forward_fp8(const ForwardArgs& a, int device, int num_sms, cu
 // the walk plan; a.merges is unused).
 struct WalkArgs {
   const JoinRec* joins;
-  int32_t n_joins;
+  int32_t n_joins, join_warps;
   bool pair;                   // two streams of segments on a CTA pair
   int32_t pieces;              // > 0: attn_rows.cu's
   // list walk

@@ -65,6 +65,15 @@ constexpr double kJoinRow = 0.0233;
 // Rows of a chunk of the prefix walk whose partial rows cost a tile's time.
 constexpr int kRowsPerTile = 87;
 
+// The same for the few-rows kernel's blocks of `tiles` tiles each, two to an SM: a
+// step of 64 keys takes a block 0.65 us alone on its SM (0.44 with up to 16 rows)
+// and two of them 0.95 us.  Its launch with the join takes 2.5 us less than the
+// tensor-core kernel's.
+double rows_cost(int32_t tiles, int64_t blocks, int pairs, int32_t S) {
+  const double step = blocks > 2 * pairs ? 95.0 : S > 16 ? 65.0 : 44.0;
+  return kJoinStart - 250.0 + 2.0 * tiles * step * (double)((blocks + 4 * pairs - 1) / (4 * pairs));
+}
+
 // Splits a tail of the items (in list order) so that the pairs finish together;
 // returns the estimated time.
 double balance(std::vector<Item>& items, int pairs, int streams) {
@@ -151,6 +160,7 @@ std::string finish(std::vector<Item>& items, std::vector<Join>& joins, int G, Ma
     if (items[i].direct && items[i].pieces > 1)
       joins.push_back(Join{items[i].u.q_row0, items[i].u.q_end, items[i].u.head, (int32_t)i, 0, 0});
   w.joins.clear();
+  w.join_warps = 0;
   for (const Join& j : joins) {
     JoinRec r;
     std::memset(&r, 0, sizeof(r));
@@ -162,9 +172,12 @@ std::string finish(std::vector<Item>& items, std::vector<Join>& joins, int G, Ma
     r.rows = it.rows();
     r.n = it.pieces;
     r.q_row0 = it.u.q_row0;
-    for (int32_t x = j.row0; x < j.row1; x += kJoinRows) {
+    int32_t most = kJoinRows;  // rows that leave each its warps
+    while (most > 1 && kJoinParts * (kJoinRows / most) < r.n) most /= 2;
+    for (int32_t x = j.row0; x < j.row1; x += most) {
       r.row0 = x;
-      r.row1 = std::min(x + kJoinRows, j.row1);
+      r.row1 = std::min(x + most, j.row1);
+      w.join_warps = std::max(w.join_warps, (r.row1 - r.row0) << join_warps_log2(r.row1 - r.row0, r.n));
       w.joins.push_back(r);
     }
   }
@@ -344,30 +357,10 @@ std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_hea
                               WalkPlan& w) {
   const int G = grid > 0 ? grid : 1;
   const int32_t tp = (int32_t)(((int64_t)prefix_len + kKeyTile - 1) / kKeyTile);
-  // Up to kRowsMax rows of documents that the join can attend to: bound by
-  // reading the prefix, a block per SM half (attn_rows.cu).
   int32_t longest = 0;
   for (int32_t d = 0; d < n_docs; ++d) longest = std::max(longest, cu[d + 1] - cu[d]);
-  if (cu[n_docs] <= kRowsMax && longest <= kJoinOwnKeys && num_heads <= 65535) {
-    std::vector<Item> items;
-    std::vector<Join> joins;
-    const int32_t tiles = (cu[n_docs] + kRowsTile - 1) / kRowsTile;
-    const int32_t blocks = std::max(1, 4 * G / std::max(1, tiles * num_heads));  // two per SM
-    for (int32_t q0 = 0; q0 < cu[n_docs]; q0 += kRowsTile)
-      for (int32_t h = 0; h < num_heads; ++h) {
-        const int32_t q1 = std::min(q0 + kRowsTile, cu[n_docs]);
-        for (int32_t d = 0; d < n_docs; ++d) {
-          const int32_t r0 = std::max(cu[d], q0), r1 = std::min(cu[d + 1], q1);
-          if (r0 < r1) joins.push_back(Join{r0, r1, h, (int32_t)items.size(), cu[d], cu[d + 1]});
-        }
-        Item it{WalkUnit{q0, q1, 0, 0, h, 0, tp, -1}, tp, tp, false};
-        it.pieces = w.pieces = std::min(blocks, tp);
-        items.push_back(it);
-      }
-    return finish(items, joins, (int)std::min<size_t>(items.size() * items[0].pieces, size_t(1) << 20), prefix_piece, w);
-  }
-  // Longer batches: chunks of 512 rows, or of 256 in two streams a pair, long
-  // documents sharing chunks or not, whichever is estimated to finish first.
+  // Chunks of 512 rows, or of 256 in two streams a pair, long documents sharing
+  // chunks or not, whichever is estimated to finish first.
   std::vector<Item> items;
   std::vector<Join> joins;
   double best = -1.0;
@@ -387,6 +380,38 @@ std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_hea
       w.own.swap(own);
       items.swap(list);
       joins.swap(list_joins);
+    }
+  }
+  // A few rows of documents that the join can attend to: bound by reading the
+  // prefix, a block per SM half (attn_rows.cu), where that is quicker.  Measured in
+  // us, this and the tensor-core kernel: single queries, 21 heads over 5,033 rows
+  // 64 17.9 / 19.7, 96 24.7 / 20.9; 8 heads 128 15.9 / 17.3, 256 24.9 / 18.5; 21
+  // heads over 300 rows 256 13.1 / 14.4.
+  const int32_t S = cu[n_docs], row_tiles = (S + kRowsTile - 1) / kRowsTile;
+  if (S <= kRowsMax && longest <= kJoinOwnKeys && num_heads <= 65535) {
+    const int64_t segs = (int64_t)row_tiles * num_heads;
+    // equal pieces that fill the blocks' places once; no more than the join reads at once
+    const int32_t most = (int32_t)std::min<int64_t>(std::max<int64_t>(1, 4 * G / segs), kJoinRows * kJoinParts);
+    const int32_t each = (tp + most - 1) / most, pieces = (tp + each - 1) / each;
+    const double time = rows_cost(each, segs * pieces, G, S) + (double)S * num_heads * pieces * kJoinRow;
+    if (time <= best) {
+      items.clear();
+      joins.clear();
+      w.own.clear();
+      w.streams = 1;
+      w.pieces = pieces;
+      for (int32_t q0 = 0; q0 < S; q0 += kRowsTile)
+        for (int32_t h = 0; h < num_heads; ++h) {
+          const int32_t q1 = std::min(q0 + kRowsTile, S);
+          for (int32_t d = 0; d < n_docs; ++d) {
+            const int32_t r0 = std::max(cu[d], q0), r1 = std::min(cu[d + 1], q1);
+            if (r0 < r1) joins.push_back(Join{r0, r1, h, (int32_t)items.size(), cu[d], cu[d + 1]});
+          }
+          Item it{WalkUnit{q0, q1, 0, 0, h, 0, tp, -1}, tp, tp, false};
+          it.pieces = pieces;
+          items.push_back(it);
+        }
+      return finish(items, joins, (int)std::min<size_t>(items.size() * pieces, size_t(1) << 20), prefix_piece, w);
     }
   }
   return finish(items, joins, G, prefix_piece, w);

@@ -47,7 +47,9 @@ def test_forward_matches_the_oracle(lib, lens, heads, prefix):
 
 
 @pytest.mark.parametrize("lens,heads,prefix", [([1], 21, 20423), ([1] * 64, 21, 5033), ([2000, 2000], 8, 4096), ([31] * 40, 21, 640),
-                                               ([300] * 12, 56, 1215)])
+                                               ([300] * 12, 56, 1215), ([1] * 200, 21, 2430), ([1] * 128, 2, 1200),
+                                               ([1] * 200, 1, 12000), ([32] * 9, 8, 300), ([30, 32, 31, 7, 1] * 5, 3, 5000),
+                                               ([2] * 50, 2, 12000)])
 def test_larger_batches(lib, lens, heads, prefix):
     p = W.Prefix(lens, heads, prefix)
     t = tensors(lens, heads, prefix, 10)

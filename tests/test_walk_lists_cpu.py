@@ -15,7 +15,7 @@ from packed_varlen_non_gb300 import h3attn as H
 
 VARLEN = [1400, 2576, 2400, 488, 3416, 1512, 3168, 1600, 1928, 1248, 3440, 800, 2088, 1760, 2328, 2616]
 LAYOUTS = [
-    ([1], 1), ([1] * 40, 3), ([32, 30, 2], 7), ([20423], 21), ([64, 80], 2), (VARLEN, 21), ([31, 32, 33, 1, 511, 512, 513, 2], 2),
+    ([1], 1), ([1] * 40, 3), ([1] * 200, 2), ([32, 1, 7, 30] * 6, 3), ([1] * 300, 21), ([32, 30, 2], 7), ([20423], 21), ([64, 80], 2), (VARLEN, 21), ([31, 32, 33, 1, 511, 512, 513, 2], 2),
     ([600] * 30, 5), ([1, 2672, 2210, 4, 2379], 2), ([700, 5, 5000, 3, 3, 129], 4), ([4096, 4096, 4096], 21), ([16320, 5033], 56),
 ]
 
