@@ -397,9 +397,9 @@ h3attn_status h3attn_forward_prefix(h3attn_plan_t plan, const void* q, const voi
  *            begin, document begin + n) of own; last the first partial row (-1: the
  *            segment writes the output itself);
  *            where segments have at most 256 rows, a pair may run two streams of
- *            them side by side (the first one's come first here); for kind 1 and at
- *            most 64 rows in documents of at most 32 tokens each segment is a
- *            thread block's, and there are as many "pairs" as segments;
+ *            them side by side (the first one's come first here); for kind 1 and a
+ *            few rows of documents of at most 32 tokens a segment of up to 32 rows may
+ *            be a thread block's, and there are as many "pairs" as segments;
  *   unit_off [*n_pairs_used + 1] int32: pair p runs units [unit_off[p], unit_off[p + 1]);
  *   joins    [*n_joins][12] int32, the rows combined from partial rows: rows
  *            [r0, r1) (at most 8), head, and of their segment the first query

@@ -1,6 +1,8 @@
 // The shared-prefix forward of a few short documents (single queries over a long
-// prefix): up to kRowsMax query rows in all, so a pass over the prefix does
-// 512 flops x rows per 512 bytes of K and V and is bound by reading them.
+// prefix): a pass over the prefix for up to 32 rows does 512 flops x rows per 512
+// bytes of K and V and is bound by reading them.  The plan takes this kernel where
+// it estimates it to be quicker than the tensor-core kernel's segments: for up to
+// 64 to 256 rows, by heads and prefix.
 //
 // The tensor-core kernel of attn_fwd_tc.cu takes 512 query rows at a time and
 // key tiles of 128 one after the other; with 32 rows its softmax chain, not
