@@ -13,14 +13,19 @@
 // rate here is a fiftieth of fp32's: the pooling alone would take five times as
 // long as reading its inputs.
 //
-// pool_kernel is HBM-bound: it reads q-hat and k-hat once, one block per
-// (128-row tile, head, tensor) with all its loads in flight, and leaves 1.5 KB
-// per tile and head.  Query blocks begin on tile boundaries, so the same tiles
+// pool_kernel is HBM-bound: it reads q-hat and k-hat once and leaves 1.5 KB per
+// tile and head.  Four blocks per SM take one (128-row tile, head, tensor) after
+// another, the next one's 32 KB on its way to shared memory while this one's are
+// summed from registers (a block for each, with its loads straight into registers,
+// leaves the memory idle while it sums: 43 us against 37 for 220 MB, 65 against 57
+// for 352 MB; the copies alone take 34 and 52.  Three blocks with two stages 39 and
+// 61, five with one 39 and 58: the sums' chain needs the warps, and the copies need
+// the shared memory).  Query blocks begin on tile boundaries, so the same tiles
 // serve both.  Each thread sums sixteen rows of eight dims onto an anchor 2^6
 // times above their largest magnitude: every addition then rounds at one fixed
 // place, and its error is two subtractions away (four operations an element
-// where a two-sum of unordered numbers takes seven: 55 us for 220 MB, q-hat and
-// k-hat of 20,423 tokens and 21 heads; so 40 us, 5.5 TB/s).
+// where a two-sum of unordered numbers takes seven: 55 against 40 us for 220 MB,
+// q-hat and k-hat of 20,423 tokens and 21 heads, before the copies ran ahead).
 //
 // score_kernel takes eight query blocks of one document and head.  Its warps
 // score 32 dims of 32 tiles at a time, a tile to a lane, against all eight: the
@@ -36,6 +41,8 @@
 // ranked.  It is a chain of waits: 10 us after the pooling for 80 query blocks of
 // 160 tiles and 21 heads, half of it hidden behind the pooling's tail (its launch
 // is a programmatic dependent one).
+#include <algorithm>
+
 #include "device_common.cuh"
 #include "qk_norm.cuh"
 
@@ -45,6 +52,9 @@ namespace {
 
 constexpr int kPoolThreads = 128;
 constexpr int kPoolRows = 16 * kKeyTile / kPoolThreads;  // rows per thread (16 lanes a row)
+constexpr int kPoolBlocks = 4;                          // per SM
+constexpr int kPoolStages = 1;                          // of a tile's 32 KB each
+constexpr uint32_t kPoolStage = kKeyTile * kHeadDim * 2;
 
 // s + err = a + b exactly (Knuth).
 __device__ __forceinline__ void two_sum(float& s, float& err, float a, float b) {
@@ -95,13 +105,12 @@ __device__ __forceinline__ uint32_t max_mag_bf16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// 16 bytes read once by the SM, the rows' 256 bytes together from DRAM.
-__device__ __forceinline__ uint4 load_once(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+// 16 bytes copied to shared memory, the rows' 256 bytes together from DRAM; zeros
+// where `in` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint.L2::256B [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+               "r"(in ? 16 : 0), "l"(policy)
+               : "memory");
 }
 
 // 1.5 * 2^(e + 6) for a number of exponent e (sums of kPoolRows numbers up to it
@@ -113,72 +122,110 @@ __device__ __forceinline__ float anchor_of(uint32_t bits) {
 
 static_assert(kPoolRows <= 16, "2^(e + 1) * kPoolRows <= 2^(e + 5)");
 
-// One (tile, tensor, head): sums of q-hat's rows as pairs, means of k-hat's.
-__global__ void __launch_bounds__(kPoolThreads, 5) pool_kernel(SelectArgs a) {
-  __shared__ float2 part[kPoolThreads / 32][128];
-  const int head = blockIdx.x % a.H, tile = (blockIdx.x / a.H) >> 1;
-  const bool is_k = (blockIdx.x / a.H) & 1;
+// Items, one (tile, tensor, head) each: sums of q-hat's rows as pairs, means of
+// k-hat's.  A block takes every gridDim.x-th item and copies kPoolStages
+// ahead; a thread reads what it copied itself, so the copies need no barrier.
+__global__ void __launch_bounds__(kPoolThreads, kPoolBlocks) pool_kernel(SelectArgs a) {
+  extern __shared__ float2 smem[];
+  __shared__ float2 part_of[2][kPoolThreads / 32][128];
   const int lane16 = threadIdx.x & 15, group = threadIdx.x >> 4, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.launch_dependents;");  // (the scoring blocks wait for this grid's end)
-  const int4 t = __ldg(a.tiles + tile);
-  const int n = t.y - t.x;
-  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_k ? a.k_hat : a.q_hat) + (int64_t)t.x * a.stride +
-                             head * kHeadDim + lane16 * 8;
-  uint4 raw[kPoolRows];
+  // (q-hat and k-hat were most likely written just before: lines read here that
+  // leave L2 first keep the written ones from being written back meanwhile; with
+  // the default policy 70 instead of 65 us after the prologue for 32,768 tokens)
+  const uint64_t policy = dev::policy_evict_first();
+  const uint32_t own = dev::smem_u32(smem) + threadIdx.x * 16;  // this thread's chunks, kPoolThreads apart
+  const uint32_t H = a.H, step = gridDim.x, items = 2u * a.n_tiles * H;  // (items below 2^31)
+  const auto rows_of = [&](uint32_t item) {  // (the launch has at most `items` blocks)
+    return __ldg(reinterpret_cast<const int2*>(a.tiles + ((min(item, items - 1) / H) >> 1)));
+  };
+  const auto copy = [&](uint32_t item, int stage, const int2& t) {
+    if (item < items) {
+      const bool k = (item / H) & 1;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(k ? a.k_hat : a.q_hat) +
+                                 (int64_t)(t.x + group) * a.stride + item % H * kHeadDim + lane16 * 8;
+      const uint32_t dst = own + stage * kPoolStage;
 #pragma unroll
-  for (int i = 0; i < kPoolRows; ++i) {
-    const int r = group + kPoolThreads / 16 * i;
-    raw[i] = r < n ? load_once(src + r * a.stride) : make_uint4(0, 0, 0, 0);
-  }
-  uint4 m = raw[0];  // largest magnitude of each dim
+      for (int i = 0; i < kPoolRows; ++i) {
+        const bool in = group + kPoolThreads / 16 * i < t.y - t.x;
+        copy16(dst + i * kPoolThreads * 16, in ? src + i * (kPoolThreads / 16) * a.stride : src, in, policy);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int2 t[kPoolStages + 1];
 #pragma unroll
-  for (int i = 1; i < kPoolRows; ++i) {
-    m.x = max_mag_bf16x2(m.x, raw[i].x);
-    m.y = max_mag_bf16x2(m.y, raw[i].y);
-    m.z = max_mag_bf16x2(m.z, raw[i].z);
-    m.w = max_mag_bf16x2(m.w, raw[i].w);
-  }
-  const uint32_t mw[4] = {m.x, m.y, m.z, m.w};
-  float2 anchor[4], hi[4], lo[4];
+  for (int x = 0; x <= kPoolStages; ++x) t[x] = rows_of(blockIdx.x + x * step);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    anchor[e] = make_float2(anchor_of(mw[e] << 16), anchor_of(mw[e]));
-    hi[e] = anchor[e];
-    lo[e] = make_float2(0.f, 0.f);
-  }
+  for (int x = 0; x < kPoolStages; ++x) copy(blockIdx.x + x * step, x, t[x]);
+#pragma unroll 1
+  for (uint32_t item = blockIdx.x, k = 0; item < items; item += step, ++k) {
+    const uint32_t stage = k % kPoolStages;
+    const int head = item % H, tile = (item / H) >> 1, n = t[0].y - t[0].x;
+    const bool is_k = (item / H) & 1;
+    float2(*const part)[128] = part_of[k & 1];
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPoolStages - 1) : "memory");
+    uint4 raw[kPoolRows];
 #pragma unroll
-  for (int i = 0; i < kPoolRows; ++i) {
-    float v[8];
-    qkn::unpack8(raw[i], v);
+    for (int i = 0; i < kPoolRows; ++i)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(raw[i].x), "=r"(raw[i].y), "=r"(raw[i].z), "=r"(raw[i].w)
+                   : "r"(own + stage * kPoolStage + i * kPoolThreads * 16)
+                   : "memory");
+#pragma unroll
+    for (int x = 0; x < kPoolStages; ++x) t[x] = t[x + 1];
+    t[kPoolStages] = rows_of(item + (kPoolStages + 1) * step);
+    copy(item + kPoolStages * step, stage, t[kPoolStages - 1]);
+    uint4 m = raw[0];  // largest magnitude of each dim
+#pragma unroll
+    for (int i = 1; i < kPoolRows; ++i) {
+      m.x = max_mag_bf16x2(m.x, raw[i].x);
+      m.y = max_mag_bf16x2(m.y, raw[i].y);
+      m.z = max_mag_bf16x2(m.z, raw[i].z);
+      m.w = max_mag_bf16x2(m.w, raw[i].w);
+    }
+    const uint32_t mw[4] = {m.x, m.y, m.z, m.w};
+    float2 anchor[4], hi[4], lo[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 x = make_float2(v[2 * e], v[2 * e + 1]);
-      const float2 s = add2(hi[e], x);
-      lo[e] = add2(lo[e], sub2(x, sub2(s, hi[e])));
-      hi[e] = s;
+      anchor[e] = make_float2(anchor_of(mw[e] << 16), anchor_of(mw[e]));
+      hi[e] = anchor[e];
+      lo[e] = make_float2(0.f, 0.f);
     }
-  }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 h = sub2(hi[e], anchor[e]);
-    const float2 own[2] = {make_float2(h.x, lo[e].x), make_float2(h.y, lo[e].y)};
+    for (int i = 0; i < kPoolRows; ++i) {
+      float v[8];
+      qkn::unpack8(raw[i], v);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {  // the warp's two row groups
-      float2 s = own[c];
-      acc2(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, 16), __shfl_xor_sync(0xffffffffu, s.y, 16)));
-      if ((threadIdx.x & 16) == 0) part[warp][lane16 * 8 + 2 * e + c] = s;
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = make_float2(v[2 * e], v[2 * e + 1]);
+        const float2 s = add2(hi[e], x);
+        lo[e] = add2(lo[e], sub2(x, sub2(s, hi[e])));
+        hi[e] = s;
+      }
     }
-  }
-  __syncthreads();
-  static_assert(kPoolThreads == kHeadDim, "a thread per dim");
-  const int d = threadIdx.x;
-  float2 s = part[0][d];
 #pragma unroll
-  for (int w = 1; w < kPoolThreads / 32; ++w) acc2(s, part[w][d]);
-  if (is_k)  // tiles innermost, two dims a word: a warp's lanes score consecutive tiles
-    reinterpret_cast<float*>(a.k_mean + ((int64_t)head * 64 + (d >> 1)) * a.n_tiles + tile)[d & 1] = mean_of(s, (float)n);
-  else
-    a.q_sum[((int64_t)head * a.n_tiles + tile) * kHeadDim + d] = s;
+    for (int e = 0; e < 4; ++e) {
+      const float2 h = sub2(hi[e], anchor[e]);
+      const float2 own[2] = {make_float2(h.x, lo[e].x), make_float2(h.y, lo[e].y)};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {  // the warp's two row groups
+        float2 s = own[c];
+        acc2(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, 16), __shfl_xor_sync(0xffffffffu, s.y, 16)));
+        if ((threadIdx.x & 16) == 0) part[warp][lane16 * 8 + 2 * e + c] = s;
+      }
+    }
+    __syncthreads();
+    static_assert(kPoolThreads == kHeadDim, "a thread per dim");
+    const int d = threadIdx.x;
+    float2 s = part[0][d];
+#pragma unroll
+    for (int w = 1; w < kPoolThreads / 32; ++w) acc2(s, part[w][d]);
+    if (is_k)  // tiles innermost, two dims a word: a warp's lanes score consecutive tiles
+      reinterpret_cast<float*>(a.k_mean + ((int64_t)head * 64 + (d >> 1)) * a.n_tiles + tile)[d & 1] = mean_of(s, (float)n);
+    else
+      a.q_sum[((int64_t)head * a.n_tiles + tile) * kHeadDim + d] = s;
+  }
 }
 
 // Order-preserving bits of a float that is not NaN (-0 as +0).
@@ -597,8 +644,12 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
 }  // namespace
 
 cudaError_t launch_block_select(const SelectArgs& a, cudaStream_t stream) {
-  pool_kernel<<<2u * (unsigned)a.n_tiles * (unsigned)a.H, kPoolThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
+  static SmemAttr pool_attr;
+  cudaError_t e = pool_attr.set(pool_kernel, (int)(kPoolStages * kPoolStage));
+  if (e != cudaSuccess) return e;
+  const unsigned blocks = std::min(2u * (unsigned)a.n_tiles * (unsigned)a.H, (unsigned)(kPoolBlocks * a.num_sms));
+  pool_kernel<<<blocks, kPoolThreads, kPoolStages * kPoolStage, stream>>>(a);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int warps = select_warps(a.max_tiles);
   const size_t smem = score_smem(warps, a.max_tiles);

@@ -761,7 +761,7 @@ h3attn_status h3attn_block_select(h3attn_plan_t plan, const void* q_hat, const v
   if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
   const SelectArgs a{q_hat, k_hat, qkv_row_stride, plan->num_heads, plan->d_ktiles, (int32_t)plan->ktiles_host.size(),
                      sp.d_groups, (int32_t)sp.groups.size(), sp.max_tiles, sp.n_q_blocks, sp.q_block / kKeyTile,
-                     sp.d_q_sum, sp.d_k_mean, keep, keep_own, sp.max_blocks, block_idx, block_cnt};
+                     sp.d_q_sum, sp.d_k_mean, keep, keep_own, sp.max_blocks, block_idx, block_cnt, plan->num_sms};
   e = launch_block_select(a, static_cast<cudaStream_t>(cuda_stream));
   return e == cudaSuccess ? H3ATTN_OK : cuda_fail(e, "block select launch");
 }

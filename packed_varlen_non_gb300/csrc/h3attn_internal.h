@@ -435,6 +435,7 @@ struct SelectArgs {
   int32_t max_blocks;
   int32_t* block_idx;          // [H, n_q_blocks, max_blocks]
   int32_t* block_cnt;          // [H, n_q_blocks]
+  int32_t num_sms;
 };
 cudaError_t launch_block_select(const SelectArgs& a, cudaStream_t stream);
 
