@@ -644,19 +644,18 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
 }  // namespace
 
 cudaError_t launch_block_select(const SelectArgs& a, cudaStream_t stream) {
-  static SmemAttr pool_attr;
+  // (both limits before the first launch, so that a refusal leaves nothing launched; the second one for every
+  // size: dynamic and static bytes count together against the default of 48 KB)
+  static SmemAttr pool_attr, score_attr;
   cudaError_t e = pool_attr.set(pool_kernel, (int)(kPoolStages * kPoolStage));
+  if (e == cudaSuccess) e = score_attr.set(score_kernel, (int)score_smem(1, kSelectMaxTiles));
   if (e != cudaSuccess) return e;
   const unsigned blocks = std::min(2u * (unsigned)a.n_tiles * (unsigned)a.H, (unsigned)(kPoolBlocks * a.num_sms));
   pool_kernel<<<blocks, kPoolThreads, kPoolStages * kPoolStage, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int warps = select_warps(a.max_tiles);
-  const size_t smem = score_smem(warps, a.max_tiles);
-  if (smem > 48 * 1024) {  // (more than 334 tiles)
-    static SmemAttr attr;
-    if ((e = attr.set(score_kernel, (int)score_smem(1, kSelectMaxTiles))) != cudaSuccess) return e;
-  }
+  const size_t smem = score_smem(warps, a.max_tiles);  // (at most score_smem(1, kSelectMaxTiles), see select_warps)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.n_groups, (unsigned)a.H);
   cfg.blockDim = dim3(32u * (unsigned)warps);
