@@ -318,9 +318,10 @@ h3attn_status h3attn_plan_sparse_info(h3attn_plan_t plan, int32_t* q_block, int3
  * block i and km_j the mean of the k-hat rows of key tile j of its document
  * (each mean rounded once to fp32), score_ij = <qm_i, km_j>; per head, block i
  * keeps the min(keep, tiles of the document) tiles with the largest scores,
- * ties to the lower tile.  Sums and scores are carried to about 2^-44, so that
- * the answer does not depend on the order of summation; a NaN score ranks
- * below every number, and one beyond fp32's range as infinite.  keep_own != 0
+ * ties to the lower tile.  The sums of rows are carried to about 2^-44 and
+ * scores are compared as sums of exact products in fp64 (good to 2^-46 |qm| |km|),
+ * so that the answer does not depend on the order of summation; a NaN score ranks
+ * below every number.  Finite rows may hold numbers from 0 to 2^112.  keep_own != 0
  * puts the tiles that overlap the query block before all others.  Writes the
  * kept tiles in ascending order, -1 behind them up to max_blocks, and their
  * number.  q_hat, k_hat: bf16 [S,H,128] with qkv_row_stride; block_idx,

@@ -7,11 +7,12 @@
 //   ties to the lower tile.
 //
 // Which tiles are kept is a discrete answer: a rounding that swaps two scores
-// changes it.  Sums and scores near the border are therefore carried as
-// unevaluated pairs of fp32 numbers (error-free transformations of Knuth,
-// Dekker, and Ogita, Rump and Oishi), good to about 2^-44 -- not in fp64, whose
-// rate here is a fiftieth of fp32's: the pooling alone would take five times as
-// long as reading its inputs.
+// changes it.  Sums of rows are therefore carried as unevaluated pairs of fp32
+// numbers (error-free transformations of Knuth and Dekker), good to about 2^-44
+// -- not in fp64, whose rate here is a fiftieth of fp32's: the pooling alone
+// would take five times as long as reading its inputs.  The few scores that fp32
+// leaves open are taken in fp64, where the product of two means is exact, the sum
+// is good to 2^-46 |qm| |km|, and nothing overflows or vanishes.
 //
 // pool_kernel is HBM-bound: it reads q-hat and k-hat once and leaves 1.5 KB per
 // tile and head.  Four blocks per SM take one (128-row tile, head, tensor) after
@@ -37,7 +38,7 @@
 // them, T, is found by a bitwise search over order-preserving keys.  A tile
 // above T + 2 E is kept and one below T - 2 E is not, whatever the exact scores
 // are.  Only where more tiles lie between than places are left (3 of 1,680 query
-// blocks with 160 tiles, and ties) are the scores between computed as pairs and
+// blocks with 160 tiles, and ties) are the scores between computed in fp64 and
 // ranked.  It is a chain of waits: 10 us after the pooling for 80 query blocks of
 // 160 tiles and 21 heads, half of it hidden behind the pooling's tail (its launch
 // is a programmatic dependent one).
@@ -234,59 +235,39 @@ __device__ __forceinline__ uint32_t ordered(float f) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-      "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
+// Order-preserving key of a score in fp64 (0 for NaN, below every number's).
+__device__ __forceinline__ uint64_t score_key(double s) {
+  const uint64_t b = (uint64_t)__double_as_longlong(s + 0.0);
+  return isnan(s) ? 0 : (b >> 63) ? ~b : (b | (1ull << 63));
 }
 
-// (hi, lo) += q k for two dims at once, even and odd dims apart: each product is
-// x + e exactly, and so is each sum.
-__device__ __forceinline__ void acc_product(float2& h, float2& l, float2 q, float2 k) {
-  const float2 x = mul2(q, k);
-  const float2 e = fma2(q, k, mul2(x, make_float2(-1.f, -1.f)));
-  const float2 s = add2(h, x), bb = sub2(s, h);
-  const float2 err = add2(sub2(h, sub2(s, bb)), sub2(x, bb));
-  h = s;
-  l = add2(l, add2(err, e));
-}
-
-// Order-preserving key of the score s.x + s.y (a normalised pair's ordered bits;
-// 0 for NaN, an infinite score has no low part).
-__device__ __forceinline__ uint64_t pair_key(float2 s) {
-  float hi, lo;
-  two_sum(hi, lo, s.x, s.y);
-  if (!isfinite(hi)) hi = s.x;
-  if (!isfinite(lo)) lo = 0.f;
-  return isnan(hi) ? 0 : ((uint64_t)ordered(hi) << 32) | ordered(lo);
-}
-
-// The exact key of one tile by one lane: q (shared memory, kSelectWarps words
-// apart) and k (`row` words apart), 64 words each.
+// The score of one tile by one lane, in fp64: the products are exact, and whatever
+// the means' magnitudes are, nothing overflows or vanishes.  (All tiles of every
+// block tied, which takes equal tiles or a zero query block: 20,423 tokens and 21
+// heads 315 us for the whole call, 51 for inputs without ties; pairs of fp32
+// numbers took 70, but lose their low parts for products below 2^-100 and their
+// high ones above 2^127.)  q (shared memory, kSelectWarps words apart) and k (`row`
+// words apart), 64 words each.
 __device__ __noinline__ uint64_t exact_key_lane(const float2* q, const float2* k, int64_t row) {
-  float2 h = make_float2(0.f, 0.f), l = make_float2(0.f, 0.f);
+  double x = 0.0, y = 0.0;
 #pragma unroll 8
-  for (int p = 0; p < 64; ++p) acc_product(h, l, q[p * kSelectWarps], __ldg(k + p * row));
-  float2 s = make_float2(h.x, l.x + l.y);
-  acc(s.x, s.y, h.y);
-  return pair_key(s);
+  for (int p = 0; p < 64; ++p) {
+    const float2 qq = q[p * kSelectWarps], kk = __ldg(k + p * row);
+    x = fma((double)qq.x, (double)kk.x, x);
+    y = fma((double)qq.y, (double)kk.y, y);
+  }
+  return score_key(x + y);
 }
 
 // The same by a whole warp (every lane gets it): four dims per lane.
 __device__ __forceinline__ uint64_t exact_key_warp(const float2* q, const float2* k, int64_t row, int lane) {
   const float2 k0 = __ldg(k + 2 * lane * row), k1 = __ldg(k + (2 * lane + 1) * row);
-  float2 h = make_float2(0.f, 0.f), l = make_float2(0.f, 0.f);
-  acc_product(h, l, q[2 * lane * kSelectWarps], k0);
-  acc_product(h, l, q[(2 * lane + 1) * kSelectWarps], k1);
-  float2 s = make_float2(h.x, l.x + l.y);
-  acc(s.x, s.y, h.y);
+  const float2 q0 = q[2 * lane * kSelectWarps], q1 = q[(2 * lane + 1) * kSelectWarps];
+  double s = fma((double)q0.x, (double)k0.x, (double)q0.y * (double)k0.y) +
+             fma((double)q1.x, (double)k1.x, (double)q1.y * (double)k1.y);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1)
-    acc2(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, off), __shfl_xor_sync(0xffffffffu, s.y, off)));
-  return pair_key(make_float2(__shfl_sync(0xffffffffu, s.x, 0), __shfl_sync(0xffffffffu, s.y, 0)));
+  for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  return score_key(__shfl_sync(0xffffffffu, s, 0));
 }
 
 // The cnt-th largest of a warp's keys 0 .. n - 1 (key(j), called for j of this
@@ -542,8 +523,10 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
 
   // A score is eight sums of 16 fused products and seven additions, off by at
   // most 24 * 2^-24 |q| |k| (Cauchy-Schwarz).  E has 2.6 times that, for the
-  // norms' own rounding too, and a term for underflow.
-  const float E = 0x1p-18f * sqrtf(qn) * sqrtf(kn) + 0x1p-120f;
+  // norms' own rounding too, and terms for underflow: 2^-120 for the products',
+  // 2^-70 for the squares' (128 of them, each off by at most 2^-149, hide no more
+  // than 2^-71 of a norm).
+  const float E = 0x1p-18f * (sqrtf(qn) + 0x1p-70f) * (sqrtf(kn) + 0x1p-70f) + 0x1p-120f;
   uint32_t th;
   if (tiles <= 32 ? pick_few<1>(keys, tiles, cnt, lane, E, out, &th)
       : tiles <= 96 ? pick_few<3>(keys, tiles, cnt, lane, E, out, &th)
@@ -621,7 +604,7 @@ __global__ void __launch_bounds__(32 * kSelectWarps) score_kernel(SelectArgs a) 
   const uint32_t low = kth_largest(tiles, cnt - above, lane, &more, [&](int j) {
     return (uint32_t)(exact[j] >> 32) == high ? (uint32_t)exact[j] : 0u;
   });
-  // (low keys of numbers are above 0, so the zeros of other high halves never count)
+  // (at least cnt - above keys have this high half: the zeros of the others change nothing)
   const uint64_t T = ((uint64_t)high << 32) | low;
   int ties = cnt;  // places left for keys equal to T, the lowest tiles first
   int greater = 0;
