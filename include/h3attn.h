@@ -457,7 +457,7 @@ h3attn_status h3attn_forward_noalloc(const int32_t* cu_seqlens, int32_t n_docs, 
  * word.  Returns OK, or ETIMEOUT if a kernel's bounded wait ran out since the
  * last call (the kernel then stopped early and its outputs are invalid), or
  * EINVAL if a list of h3attn_forward_sparse named a key tile outside its
- * document (the tile was skipped), or ECUDA if the stream reports an error. */
+ * document (the tile was skipped) and no wait ran out, or ECUDA if the stream reports an error. */
 h3attn_status h3attn_get_device_error(h3attn_plan_t plan, void* cuda_stream);
 
 /* Launches one CTA that waits on a shared-memory barrier nothing arrives on,
@@ -467,6 +467,11 @@ h3attn_status h3attn_get_device_error(h3attn_plan_t plan, void* cuda_stream);
  * (OK would mean the bound is broken).  Exercises failure detection without
  * faulting or hanging the GPU. */
 h3attn_status h3attn_selftest_bounded_wait(uint64_t timeout_ns, void* cuda_stream);
+
+/* The same wait, recorded in the plan's device error word as a forward's would
+ * be, where h3attn_get_device_error finds it.  Asynchronous on cuda_stream.
+ * Errors: EINVAL for a NULL plan or a limit out of range. */
+h3attn_status h3attn_selftest_plan_wait(h3attn_plan_t plan, uint64_t timeout_ns, void* cuda_stream);
 
 /* Message for the last failing call on this host thread ("" if none). */
 const char* h3attn_last_error(void);

@@ -809,7 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               kt = key_tile<kWalk>(gn, gn.lo, entry, walk);
               k_head = gn.head;
             }
-            if (vt.bad && rank == 0) atomicExch(a.err, kErrBlockIndex);
+            if (vt.bad && rank == 0) dev::report_bad_tile(a.err);
             const uint32_t b = 2 * st + (n & 1);
             ok = dev::mbar_wait(bars.kv_empty(b), ((n >> 1) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
             if (!ok) break;
@@ -932,7 +932,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             kt.row = g.kv0 + (j + 1) * kTileRows;
           } else {
             if (has_k) kt = key_tile<kWalk>(g, j + 1, walk_entry<kWalk>(g, j + 1, walk), walk);
-            if (vt.bad && rank == 0) atomicExch(a.err, kErrBlockIndex);
+            if (vt.bad && rank == 0) dev::report_bad_tile(a.err);
           }
           if (!has_k && has_next) {
             const UnitGeom n = unit_geom<kWalk>(a.units, u + 1, walk);

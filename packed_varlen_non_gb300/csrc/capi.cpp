@@ -227,6 +227,12 @@ h3attn_status check_layout(const int32_t* cu_seqlens, int32_t n_docs, int32_t nu
   return H3ATTN_OK;
 }
 
+h3attn_status check_wait_limit(uint64_t timeout_ns) {
+  if (timeout_ns < 1000ull || timeout_ns > 10000000000ull)
+    return fail(H3ATTN_EINVAL, "timeout_ns must be in [1e3, 1e10]");
+  return H3ATTN_OK;
+}
+
 // Sizes shared by the calls that set a list and the host listing.
 h3attn_status check_list_sizes(int32_t q_block, int32_t max_blocks) {
   if (q_block != 256 && q_block != 512) return fail(H3ATTN_EINVAL, "q_block must be 256 or 512 (got %d)", q_block);
@@ -955,8 +961,7 @@ h3attn_status h3attn_get_device_error(h3attn_plan_t plan, void* cuda_stream) {
 
 h3attn_status h3attn_selftest_bounded_wait(uint64_t timeout_ns, void* cuda_stream) {
   clear_error();
-  if (timeout_ns < 1000ull || timeout_ns > 10000000000ull)
-    return fail(H3ATTN_EINVAL, "timeout_ns must be in [1e3, 1e10]");
+  if (h3attn_status s = check_wait_limit(timeout_ns)) return s;
   uint32_t* d_flag = nullptr;
   cudaError_t e = cudaMalloc(&d_flag, sizeof(uint32_t));
   if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc");
@@ -970,6 +975,17 @@ h3attn_status h3attn_selftest_bounded_wait(uint64_t timeout_ns, void* cuda_strea
   if (e != cudaSuccess) return cuda_fail(e, "selftest");
   if (word == kErrTimeout) return fail(H3ATTN_ETIMEOUT, "bounded wait ran out (expected)");
   return fail(H3ATTN_ECUDA, "bounded wait did not report a timeout (word 0x%x)", word);
+}
+
+h3attn_status h3attn_selftest_plan_wait(h3attn_plan_t plan, uint64_t timeout_ns, void* cuda_stream) {
+  clear_error();
+  if (h3attn_status s = check_plan(plan)) return s;
+  if (h3attn_status s = check_wait_limit(timeout_ns)) return s;
+  DeviceGuard g;
+  cudaError_t e = g.enter(plan->device);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+  e = launch_selftest_bounded_wait(timeout_ns, plan->d_err, static_cast<cudaStream_t>(cuda_stream));
+  return e == cudaSuccess ? H3ATTN_OK : cuda_fail(e, "selftest launch");
 }
 
 }  // extern "C"

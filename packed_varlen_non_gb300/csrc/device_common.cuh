@@ -127,6 +127,10 @@ static __device__ __noinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t par
   }
 }
 
+// Records that a list named a tile outside its document.  A word that already
+// says something stays: a timeout's outputs are invalid, a skipped tile's are not.
+__device__ __forceinline__ void report_bad_tile(uint32_t* err_word) { atomicCAS(err_word, kErrNone, kErrBlockIndex); }
+
 // Inline fast path for the hot waits: one try_wait before falling back to the
 // out-of-line bounded wait.  Calling the bounded wait on an already-complete
 // phase costs ~450-600 cycles in the MMA-issuing thread on GB300 (an inline

@@ -81,6 +81,7 @@ _SIGS = {
                               POINTER(c_int64), POINTER(c_int64), POINTER(c_int64)],
     "h3attn_get_device_error": [c_void_p, c_void_p],
     "h3attn_selftest_bounded_wait": [c_uint64, c_void_p],
+    "h3attn_selftest_plan_wait": [c_void_p, c_uint64, c_void_p],
 }
 
 _lib = None
@@ -456,6 +457,11 @@ def h3attn_get_device_error(plan, stream=None):
 def h3attn_selftest_bounded_wait(timeout_ns: int, stream=None) -> int:
     """Returns the raw status (ETIMEOUT is the expected outcome)."""
     return int(load().h3attn_selftest_bounded_wait(int(timeout_ns), _stream(stream)))
+
+
+def h3attn_selftest_plan_wait(plan, timeout_ns: int, stream=None):
+    """A wait that runs out, recorded in the plan's device error word."""
+    _check(load().h3attn_selftest_plan_wait(plan, int(timeout_ns), _stream(stream)), "h3attn_selftest_plan_wait")
 
 
 class Plan:
