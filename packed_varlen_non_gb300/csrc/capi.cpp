@@ -25,7 +25,13 @@ h3attn_status fail(h3attn_status s, const char* fmt, ...) {
   return s;
 }
 
-void clear_error() { g_last_error.clear(); }
+// Every call begins with it.  The runtime keeps a failed call's error until it is
+// asked for, and launches are checked by asking: without the second line a refused
+// allocation came back as the next call's failed launch.
+void clear_error() {
+  g_last_error.clear();
+  cudaGetLastError();
+}
 
 }  // namespace h3
 
