@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_uint64, c_void_p
 
 import numpy as np
@@ -118,13 +119,27 @@ def _check(status: int, fn: str):
         raise H3AttnError(status, fn, h3attn_last_error())
 
 
-def _stream(stream) -> int | None:
+def _torch():
+    return sys.modules["torch"]  # (whoever passes tensors has it)
+
+
+def _stream(stream, device=None) -> int | None:
+    """The stream's handle; for None the current one of `device` (None: of the
+    current device)."""
     if stream is None:
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None
+
+
+# The device that was current when a plan was created.
+_plan_device: dict = {}
+
+
+def _plan_stream(plan, stream):
+    return _stream(stream, _plan_device.get(plan))
 
 
 def _ptr(x) -> int | None:
@@ -166,11 +181,13 @@ def h3attn_plan_create(docs, num_heads: int, rope_base: float = 10000.0, head_di
     st = _stream(stream) if stream is not False else None
     _check(load().h3attn_plan_create(cdocs, len(docs), ctypes.byref(opts), st, ctypes.byref(out)),
            "h3attn_plan_create")
+    if "torch" in sys.modules:
+        _plan_device[out.value] = _torch().cuda.current_device()
     return out.value
 
 
 def h3attn_plan_destroy(plan):
-    for known in (_list_sizes, _plan_rows, _prefix_rows):
+    for known in (_list_sizes, _plan_rows, _prefix_rows, _plan_device):
         known.pop(plan, None)
     _check(load().h3attn_plan_destroy(plan), "h3attn_plan_destroy")
 
@@ -325,55 +342,94 @@ def h3attn_forward_noalloc(cu_seqlens, num_heads: int, q, k, v, o, softmax_scale
 
 # ------------------------------------------------- sparse, shared prefix ----
 
-# Rows that the walks' calls read or write: a plan's tokens, and its prefix.
+# What the tensors of the walks' calls must be, of the plans that have them (fixed
+# once set): (tokens, heads * 128, device), the prefix's rows, the lists' elements.
 _plan_rows: dict = {}
 _prefix_rows: dict = {}
-
-
-def _qkv_stride(q, others, given, rows=None):
-    """Row stride shared by tensors of at least `rows` rows on the device."""
-    if given is None and not isinstance(q, int):
-        given = q.stride(0)
-        for x in others:
-            if x.stride(0) != given:
-                raise ValueError(f"tensors of one call must share one row stride (got {given}, {x.stride(0)})")
-    if rows is not None:
-        for x in (q, *others):
-            _check_rows(x, rows)
-    return _row_stride(q, given)
-
-
-def _check_rows(x, rows):
-    if x is not None and not isinstance(x, int) and (x.shape[0] < rows or not x.is_cuda):
-        raise ValueError(f"a tensor on the device with at least {rows} rows is needed (got {tuple(x.shape)}, {x.device})")
-
-
-# Sizes of the lists of the plans that have them (fixed once set).
 _list_sizes: dict = {}
+
+
+def _known(plan):
+    """Notes the sizes of a plan that has just got a list."""
+    info = h3attn_plan_info(plan)
+    _plan_rows[plan] = (info["S"], info["num_heads"] * 128, _plan_device.get(plan))
+
+
+def _on(x, device):
+    """Whether a tensor lies on the given device (None: on any GPU)."""
+    at = x.get_device()
+    return at >= 0 if device is None else at == device
+
+
+def _rows(tensors, given, rows, sizes):
+    """The row stride shared by bf16 tensors of at least `rows` rows of
+    heads * 128 contiguous elements on the plan's device; raw pointers among them
+    are the caller's, with the given stride."""
+    if sizes is None:  # the call itself refuses a plan without lists
+        return _row_stride(tensors[0], given)
+    _, width, device = sizes
+    bf16 = _torch().bfloat16
+    stride, shape, step, fits = given, None, None, False
+    for x in tensors:
+        if x is None or isinstance(x, int):
+            continue
+        last, shape, last_step, step = shape, x.shape, step, x.stride()
+        if shape != last or step != last_step:  # (most calls' tensors are alike)
+            n = len(shape)
+            if n == 2:
+                fits = step[1] == 1 and shape[1] >= width
+            else:
+                fits = n == 3 and step[2] == 1 and (step[1] == shape[2] or shape[1] == 1) and shape[1] * shape[2] >= width
+            fits = fits and shape[0] >= rows
+        at = x.get_device()
+        if not fits or x.dtype is not bf16 or at < 0 or (device is not None and at != device):
+            raise ValueError(f"a bfloat16 tensor of at least {rows} rows of {width} contiguous elements on the plan's "
+                             f"device is needed (got {tuple(shape)}, strides {tuple(step)}, {x.dtype}, {x.device})")
+        if rows == 1:
+            continue  # (one row has no stride)
+        if stride is None:
+            stride = step[0]
+        elif step[0] != stride:
+            raise ValueError(f"tensors of one call must share one row stride (got {stride}, {step[0]})")
+    if stride is None:
+        if any(isinstance(x, int) for x in tensors):
+            raise ValueError("a row stride is required when passing raw pointers")
+        stride = width
+    return int(stride)
+
+
+def _check_lse(lse, sizes):
+    if lse is None or isinstance(lse, int) or sizes is None:
+        return
+    n = sizes[0] * (sizes[1] // 128)
+    if lse.dtype is not _torch().float32 or lse.numel() != n or not lse.is_contiguous() or not _on(lse, sizes[2]):
+        raise ValueError(f"lse must be a contiguous float32 tensor of {n} elements on the plan's device "
+                         f"(got {tuple(lse.shape)}, {lse.dtype}, {lse.device})")
 
 
 def _check_lists(plan, block_idx, block_cnt):
     """The lists are read (or written) by their plan's sizes, so tensors must
     be int32, contiguous and of those sizes; raw pointers are the caller's."""
-    if isinstance(block_idx, int) or isinstance(block_cnt, int) or block_idx is None or block_cnt is None:
-        return
     sizes = _list_sizes.get(plan)
     if sizes is None:
         return  # the call itself refuses a plan without lists
+    device = _plan_rows[plan][2]
     for t, n in ((block_idx, sizes[0]), (block_cnt, sizes[1])):
-        if t.numel() != n or t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous() or not t.is_cuda:
-            raise ValueError("block_idx and block_cnt must be contiguous int32 tensors on the device of "
+        if t is None or isinstance(t, int):
+            continue
+        if t.numel() != n or t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous() or not _on(t, device):
+            raise ValueError("block_idx and block_cnt must be contiguous int32 tensors on the plan's device of "
                              f"{sizes[0]} and {sizes[1]} elements (got {tuple(t.shape)}, {t.dtype}, {t.device})")
 
 
 def h3attn_plan_set_sparse(plan, q_block: int, max_blocks: int, stream=None):
     """Adds the block-sparse work list to a plan (once per plan)."""
-    _check(load().h3attn_plan_set_sparse(plan, int(q_block), int(max_blocks), _stream(stream)),
+    _check(load().h3attn_plan_set_sparse(plan, int(q_block), int(max_blocks), _plan_stream(plan, stream)),
            "h3attn_plan_set_sparse")
     info = h3attn_plan_sparse_info(plan)
     rows = info["num_heads"] * info["n_q_blocks"]
+    _known(plan)
     _list_sizes[plan] = (rows * info["max_blocks"], rows)
-    _plan_rows[plan] = h3attn_plan_info(plan)["S"]
 
 
 def h3attn_plan_sparse_info(plan) -> dict:
@@ -388,46 +444,50 @@ def h3attn_block_select(plan, q_hat, k_hat, keep: int, block_idx, block_cnt, kee
                         qkv_row_stride=None, stream=None):
     """Scores and keeps key tiles: block_idx int32 [H, n_q_blocks, max_blocks],
     block_cnt int32 [H, n_q_blocks] (see include/h3attn.h)."""
-    stride = _qkv_stride(q_hat, (k_hat,), qkv_row_stride, _plan_rows.get(plan))
+    sizes = _plan_rows.get(plan)
+    stride = _rows((q_hat, k_hat), qkv_row_stride, sizes[0] if sizes else 0, sizes)
     _check_lists(plan, block_idx, block_cnt)
     _check(load().h3attn_block_select(plan, _ptr(q_hat), _ptr(k_hat), stride, int(keep), int(bool(keep_own)),
-                                      _ptr(block_idx), _ptr(block_cnt), _stream(stream)), "h3attn_block_select")
+                                      _ptr(block_idx), _ptr(block_cnt), _plan_stream(plan, stream)),
+           "h3attn_block_select")
 
 
 def h3attn_forward_sparse(plan, q, k, v, block_idx, block_cnt, o, softmax_scale: float, lse=None,
                           qkv_row_stride=None, o_row_stride=None, stream=None):
     """The forward over the listed key tiles of each query block."""
-    rows = _plan_rows.get(plan)
-    stride = _qkv_stride(q, (k, v), qkv_row_stride, rows)
-    if rows is not None:
-        _check_rows(o, rows)
+    sizes = _plan_rows.get(plan)
+    rows = sizes[0] if sizes else 0
+    stride = _rows((q, k, v), qkv_row_stride, rows, sizes)
+    o_stride = _rows((o,), o_row_stride, rows, sizes)
+    _check_lse(lse, sizes)
     _check_lists(plan, block_idx, block_cnt)
     _check(load().h3attn_forward_sparse(plan, _ptr(q), _ptr(k), _ptr(v), stride, _ptr(block_idx), _ptr(block_cnt),
-                                        _ptr(o), _row_stride(o, o_row_stride), float(softmax_scale), _ptr(lse),
-                                        _stream(stream)), "h3attn_forward_sparse")
+                                        _ptr(o), o_stride, float(softmax_scale), _ptr(lse),
+                                        _plan_stream(plan, stream)), "h3attn_forward_sparse")
 
 
 def h3attn_plan_set_prefix(plan, prefix_len: int, stream=None):
     """Adds the work list for a shared prefix of prefix_len rows to a plan
     (once per plan)."""
-    _check(load().h3attn_plan_set_prefix(plan, int(prefix_len), _stream(stream)), "h3attn_plan_set_prefix")
+    _check(load().h3attn_plan_set_prefix(plan, int(prefix_len), _plan_stream(plan, stream)),
+           "h3attn_plan_set_prefix")
+    _known(plan)
     _prefix_rows[plan] = int(prefix_len)
-    _plan_rows[plan] = h3attn_plan_info(plan)["S"]
 
 
 def h3attn_forward_prefix(plan, q, k, v, k_prefix, v_prefix, o, softmax_scale: float, lse=None,
                           qkv_row_stride=None, prefix_row_stride=None, o_row_stride=None, stream=None):
     """The forward of a batch whose documents all attend to one prefix besides
     themselves; k_prefix and v_prefix are bf16 [prefix_len, H, 128]-shaped."""
-    rows = _plan_rows.get(plan)
-    stride = _qkv_stride(q, (k, v), qkv_row_stride, rows)
-    if rows is not None:
-        _check_rows(o, rows)
-    prefix_stride = _qkv_stride(k_prefix, (v_prefix,), prefix_row_stride, _prefix_rows.get(plan))
+    sizes, prefix_len = _plan_rows.get(plan), _prefix_rows.get(plan)
+    rows = sizes[0] if sizes else 0
+    stride = _rows((q, k, v), qkv_row_stride, rows, sizes)
+    prefix_stride = _rows((k_prefix, v_prefix), prefix_row_stride, prefix_len, sizes if prefix_len else None)
+    o_stride = _rows((o,), o_row_stride, rows, sizes)
+    _check_lse(lse, sizes)
     _check(load().h3attn_forward_prefix(plan, _ptr(q), _ptr(k), _ptr(v), stride, _ptr(k_prefix), _ptr(v_prefix),
-                                        prefix_stride, _ptr(o),
-                                        _row_stride(o, o_row_stride), float(softmax_scale), _ptr(lse),
-                                        _stream(stream)), "h3attn_forward_prefix")
+                                        prefix_stride, _ptr(o), o_stride, float(softmax_scale), _ptr(lse),
+                                        _plan_stream(plan, stream)), "h3attn_forward_prefix")
 
 
 def h3attn_walk_list_host(kind: int, cu_seqlens, num_heads: int, p0: int, p1: int, n_pairs: int):
@@ -451,7 +511,7 @@ def h3attn_walk_list_host(kind: int, cu_seqlens, num_heads: int, p0: int, p1: in
 
 
 def h3attn_get_device_error(plan, stream=None):
-    _check(load().h3attn_get_device_error(plan, _stream(stream)), "h3attn_get_device_error")
+    _check(load().h3attn_get_device_error(plan, _plan_stream(plan, stream)), "h3attn_get_device_error")
 
 
 def h3attn_selftest_bounded_wait(timeout_ns: int, stream=None) -> int:
@@ -461,7 +521,7 @@ def h3attn_selftest_bounded_wait(timeout_ns: int, stream=None) -> int:
 
 def h3attn_selftest_plan_wait(plan, timeout_ns: int, stream=None):
     """A wait that runs out, recorded in the plan's device error word."""
-    _check(load().h3attn_selftest_plan_wait(plan, int(timeout_ns), _stream(stream)), "h3attn_selftest_plan_wait")
+    _check(load().h3attn_selftest_plan_wait(plan, int(timeout_ns), _plan_stream(plan, stream)), "h3attn_selftest_plan_wait")
 
 
 class Plan:
