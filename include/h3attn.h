@@ -306,7 +306,8 @@ h3attn_status h3attn_forward_fp8(h3attn_plan_t plan, const void* q8, const void*
  * may be called once per plan, so that no later call invalidates a captured
  * graph.
  * Errors: EINVAL for a NULL plan, another q_block, max_blocks outside
- * [1, 2^20], lists already set, lists or partial results of 2^31 rows or more;
+ * [1, 2^20], lists already set, more than 2^31 - 513 tokens, lists or partial
+ * results of 2^31 rows or more;
  * ENOMEM / ECUDA from allocation or upload. */
 h3attn_status h3attn_plan_set_sparse(h3attn_plan_t plan, int32_t q_block, int32_t max_blocks, void* cuda_stream);
 
@@ -363,8 +364,8 @@ h3attn_status h3attn_forward_sparse(h3attn_plan_t plan, const void* q, const voi
  * rows to a plan whose documents are the batch; allocation, capture and "once
  * per plan" as h3attn_plan_set_sparse (a plan may have both lists).  Partial
  * results take 520 bytes per (row, head) and pass for rows that share passes.
- * Errors: EINVAL for a NULL plan, prefix_len < 1, a prefix already set, or
- * partial results of 2^31 rows or more; ENOMEM / ECUDA from allocation or
+ * Errors: EINVAL for a NULL plan, prefix_len < 1, a prefix already set, more
+ * than 2^31 - 513 tokens, or partial results of 2^31 rows or more; ENOMEM / ECUDA from allocation or
  * upload. */
 h3attn_status h3attn_plan_set_prefix(h3attn_plan_t plan, int32_t prefix_len, void* cuda_stream);
 

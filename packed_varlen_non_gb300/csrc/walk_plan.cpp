@@ -80,6 +80,10 @@ double rows_cost(int32_t tiles, int64_t blocks, int pairs, int32_t S) {
   return kJoinStart - 250.0 + 2.0 * tiles * step * (double)((blocks + 4 * pairs - 1) / (4 * pairs));
 }
 
+// Row numbers are 32-bit, and the walks' go up to a segment past the last row.
+bool too_long(const int32_t* cu, int32_t n_docs) { return cu[n_docs] > INT32_MAX - kUnitRows; }
+constexpr char kTooLong[] = "too many tokens for a list of the sparse or prefix forward";
+
 // Splits a tail of the items (in list order) so that the pairs finish together;
 // returns the estimated time.
 double balance(std::vector<Item>& items, int pairs, int streams) {
@@ -216,6 +220,7 @@ std::string finish(std::vector<Item>& items, std::vector<Join>& joins, int G, Ma
 
 std::string build_list_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads, int32_t q_block, int32_t max_blocks,
                             int grid, WalkPlan& w) {
+  if (too_long(cu, n_docs)) return kTooLong;
   const int G = grid > 0 ? grid : 1;
   std::vector<int32_t> order(n_docs), block0(n_docs);
   int32_t blocks = 0;
@@ -363,6 +368,7 @@ static std::string prefix_items(const int32_t* cu, int32_t n_docs, int32_t num_h
 
 std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads, int32_t prefix_len, int grid,
                               WalkPlan& w) {
+  if (too_long(cu, n_docs)) return kTooLong;
   const int G = grid > 0 ? grid : 1;
   const int32_t tp = (int32_t)(((int64_t)prefix_len + kKeyTile - 1) / kKeyTile);
   int32_t longest = 0;
