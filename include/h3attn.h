@@ -362,7 +362,9 @@ h3attn_status h3attn_forward_sparse(h3attn_plan_t plan, const void* q, const voi
  *
  * h3attn_plan_set_prefix adds the work list for a prefix of prefix_len >= 1
  * rows to a plan whose documents are the batch; allocation, capture and "once
- * per plan" as h3attn_plan_set_sparse (a plan may have both lists).  Partial
+ * per plan" as h3attn_plan_set_sparse (a plan may have both lists).  A prefix
+ * that grows needs a plan for each length (about half a millisecond for a few
+ * single tokens).  Partial
  * results take 520 bytes per (row, head) and pass for rows that share passes.
  * Errors: EINVAL for a NULL plan, prefix_len < 1, a prefix already set, more
  * than 2^31 - 513 tokens, or partial results of 2^31 rows or more; ENOMEM / ECUDA from allocation or

@@ -238,9 +238,11 @@ constexpr int kWalkDoc = 0, kWalkList = 1, kWalkPrefix = 2;
 // two groups of the ring: group n of stream s, ring slots 4 s + 2 (n & 1) and the
 // one after it, holds V(n - 1) and K(n), n counting the stream's steps.  A Q
 // slot is free once its segment's last QK is done, a step before the segment
-// ends, so one per stream is enough; O rows are stored directly.  (The extra
-// tiles cost a step 11 %: with the operands' reads they fill shared memory's
-// bandwidth; the step's time does not depend on where in L2 the tiles lie.)
+// ends, so one per stream is enough; O rows are stored directly.  (A step of
+// both streams takes 1.50 us, one of 512 rows in one stream 1.28.  What makes the
+// difference is not known: it does not depend on where in L2 the tiles lie, and no
+// unit is full -- over 20 listed tiles a segment the tensor pipe is active 70 % of
+// cycles, with its operands' fetches 83 %, against 77 and 90 % in one stream over 40.)
 // Warp 9 loads stream 0 and warp 10 stream 1: lane 0 Q, K and V in the order the
 // stream needs them, lane 1 reports each Q tile landed.
 // Measured, us for 512 rows of a head (two segments) and 2 / 4 / 8 / 16 tiles: one

@@ -10,8 +10,9 @@
 // us, 4 TB/s, from DRAM or from L2: what is left is the latency of six steps, the
 // first copies and the exchange of the results).  Here a block takes up to 32 rows
 // of one head over its share of the prefix, two blocks an SM: K and V stream
-// through a three-stage ring of asynchronous copies (96 KB a block in flight),
-// each of the four warps takes 16 of a stage's 64 keys for all rows -- the
+// through a three-stage ring of asynchronous copies (one 32 KB stage in use, two
+// on their way; Q passes through the third, so the first copies are two stages
+// too), each of the four warps takes 16 of a stage's 64 keys for all rows -- the
 // scores, the softmax with a running maximum of its own and PV as m16n8k16
 // products on registers (at 32 rows their rate is not the limit, and they need
 // none of the set-up of the tcgen05 path) -- and the four partial results are

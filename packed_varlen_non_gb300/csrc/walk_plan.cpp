@@ -49,10 +49,9 @@ struct Join {
 // Times in hundredths of a microsecond, as measured on GB300 for segments of 1 to
 // 32 tiles.  A CTA pair runs one segment of up to kUnitRows rows at a time (1.28
 // us a tile, and 4 us for its boundary, where the pipeline runs empty), or two
-// streams of segments of half as many rows (1.50 us for a tile of each: every
-// segment's K and V tiles come from L2 for half the rows, and with them shared
-// memory's bandwidth runs short; but a boundary costs 1.7 us, as the other stream
-// goes on).  So streams suit short walks, and rows of many documents, whose own
+// streams of segments of half as many rows (1.50 us for a tile of each: the same
+// products with twice the K and V tiles; but a boundary costs 1.7 us, as the other
+// stream goes on).  So streams suit short walks, and rows of many documents, whose own
 // tiles then take half as many rows along: 100 documents of 100 tokens over 512
 // prefix rows 93 against 119 us, three of 4,096 over 2,430 rows 559 against 512.
 // Partial rows cost a segment 1.3 us, and the join kJoinStart and kJoinRow for
