@@ -25,13 +25,9 @@ h3attn_status fail(h3attn_status s, const char* fmt, ...) {
   return s;
 }
 
-// Every call begins with it.  The runtime keeps a failed call's error until it is
-// asked for, and launches are checked by asking: without the second line a refused
-// allocation came back as the next call's failed launch.
-void clear_error() {
-  g_last_error.clear();
-  cudaGetLastError();
-}
+void clear_error() { g_last_error.clear(); }
+
+void clear_runtime_error() { cudaGetLastError(); }
 
 }  // namespace h3
 
@@ -68,6 +64,7 @@ struct DeviceGuard {
   int prev = -1;
   bool switched = false;
   cudaError_t enter(int dev) {
+    clear_runtime_error();
     cudaError_t e = cudaGetDevice(&prev);
     if (e != cudaSuccess) return e;
     if (prev != dev) {
@@ -290,6 +287,7 @@ h3attn_status h3attn_plan_create(const h3attn_doc* docs, int32_t n_docs,
   h3attn_plan* p = new (std::nothrow) h3attn_plan();
   if (p == nullptr) return fail(H3ATTN_ENOMEM, "host allocation failed");
 
+  clear_runtime_error();
   cudaError_t e = cudaGetDevice(&p->device);
   if (e != cudaSuccess) {
     delete p;
@@ -968,6 +966,7 @@ h3attn_status h3attn_get_device_error(h3attn_plan_t plan, void* cuda_stream) {
 h3attn_status h3attn_selftest_bounded_wait(uint64_t timeout_ns, void* cuda_stream) {
   clear_error();
   if (h3attn_status s = check_wait_limit(timeout_ns)) return s;
+  clear_runtime_error();
   uint32_t* d_flag = nullptr;
   cudaError_t e = cudaMalloc(&d_flag, sizeof(uint32_t));
   if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc");

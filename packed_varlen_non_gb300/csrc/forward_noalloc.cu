@@ -125,6 +125,7 @@ extern "C" h3attn_status h3attn_forward_noalloc(const int32_t* cu_seqlens, int32
   }
 
   int dev = 0;
+  clear_runtime_error();
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return fail(H3ATTN_ECUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
   if (dev < 0 || dev >= kMaxDevices) return fail(H3ATTN_EUNSUPPORTED, "device index %d", dev);

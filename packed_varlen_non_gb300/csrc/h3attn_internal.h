@@ -301,6 +301,12 @@ std::string build_plan_host(const h3attn_doc* docs, int32_t n_docs, const h3attn
 // Error reporting for the C-ABI layer.
 h3attn_status fail(h3attn_status s, const char* fmt, ...);
 void clear_error();
+// Every call that goes to the device begins there with it.  The runtime keeps a
+// failed call's error until it is asked for, and launches are checked by asking:
+// without it a refused allocation came back as the next call's failed launch.
+// (Not in calls that stay on the host: it initialises the driver, after which a
+// process may not fork ones that use it.)
+void clear_runtime_error();
 
 // The maximum dynamic shared memory of a kernel, set once per kernel and device
 // (the attribute belongs to the current device's copy of the kernel).
