@@ -423,6 +423,120 @@ h3attn_status h3attn_walk_list_host(int32_t kind, const int32_t* cu_seqlens, int
                                     int64_t own_cap, int64_t* n_units, int32_t* n_pairs_used, int64_t* n_joins,
                                     int64_t* n_own, int64_t* n_part_rows);
 
+/* ---- Rotary positions -------------------------------------------------------
+ * Positions of a text tower and of long contexts ([PR26] "The device-resident
+ * forward (W2b)" and the device-encoder commit name the rotation and M-RoPE; the
+ * DiT's own 3D positions are h3attn_qk_prologue's).  A head's first rope_dims
+ * dims are pairs (a_j, b_j), j < rope_dims / 2: dims (j, j + rope_dims/2), or (2j,
+ * 2j + 1) where interleaved.  A token at p turns pair j by t = p[axis_j] f_j:
+ *     a' = A (a cos t - b sin t),   b' = A (b cos t + a sin t)
+ * and the other dims pass through.  Frequencies, with d = rope_dims:
+ *     PLAIN     f_j = base^(-2j/d)
+ *     LINEAR    f_j / factor
+ *     NTK       f_j of the base  base factor^(d/(d-2))
+ *     BY_PARTS  f_j (g + (1 - g)/factor),  g = clamp((original_len f_j/(2 pi) -
+ *               beta_slow)/(beta_fast - beta_slow), 0, 1)
+ * A = amplitude, or where that is 0: 0.1 ln(factor) + 1 BY_PARTS, else 1.  axis:
+ * the position axis of each pair (rope_dims/2 bytes below n_axes), NULL for axis
+ * 0; so (t, h, w) positions may take sections or every third pair.
+ * An angle is found in turns, by integer arithmetic modulo one turn, from the
+ * frequency as a 64-bit fraction of a turn: a position p, negative ones among
+ * them, costs no more than |p| 2^-53 turns. */
+typedef enum {
+  H3ATTN_ROPE_PLAIN = 0,
+  H3ATTN_ROPE_LINEAR = 1,
+  H3ATTN_ROPE_NTK = 2,
+  H3ATTN_ROPE_BY_PARTS = 3
+} h3attn_rope_scaling;
+
+typedef struct {
+  int32_t rope_dims;     /* a multiple of 16 in [16, 128] */
+  int32_t interleaved;   /* 0 or 1 */
+  double base;           /* > 1 */
+  int32_t scaling;       /* h3attn_rope_scaling */
+  double factor;         /* >= 1 (ignored where PLAIN) */
+  double original_len;   /* BY_PARTS: > 0 */
+  double beta_fast, beta_slow;  /* BY_PARTS: beta_fast > beta_slow >= 0 (usually 32 and 1) */
+  double amplitude;      /* > 0, or 0 for the default */
+  int32_t n_axes;        /* 1 to 3 */
+  const uint8_t* axis;   /* host, [rope_dims / 2] or NULL */
+} h3attn_rope_opts;
+
+/* What the rotary calls need of it: plain data of the caller's, read by each
+ * call before it returns. */
+typedef struct {
+  int32_t rope_dims, interleaved, n_axes;
+  float amplitude;
+  uint64_t turns[64];    /* f_j / (2 pi) as a fraction of 2^64 */
+  uint8_t axis[64];
+} h3attn_rope;
+
+/* Fills a h3attn_rope on the host (no device and no CUDA call is needed).
+ * Errors: EINVAL for NULL pointers and values outside the ranges above;
+ * EUNSUPPORTED for rope_dims that are not a multiple of 16 in [16, 128]. */
+h3attn_status h3attn_rope_init(const h3attn_rope_opts* opts, h3attn_rope* out);
+
+/* Rotates q (num_heads heads) and k (num_kv_heads) of n_tokens tokens:
+ * positions int32 [n_axes, n_tokens] on the device; rows as everywhere, bf16, 128
+ * dims a head, every tensor with a row stride of its own; fp32 arithmetic, one
+ * rounding.  inverse != 0 turns by -t, with the same amplitude: the rotation's
+ * gradient, and with A = 1 its undoing.  Outputs may be their own input (equal pointers and strides; in
+ * place).  k_in and k_out may both be NULL (num_kv_heads is then ignored), or
+ * q_in and q_out.  n_tokens = 0 is allowed.
+ * There is no plan: the call runs on the current device, which must be the
+ * tensors'.  Calls may overlap each other.
+ * Errors: EINVAL for a NULL rope or positions, only one of an input and its
+ * output NULL, all NULL, misaligned pointers (positions 4 bytes), bad strides,
+ * n_tokens < 0 or >= 2^31, heads < 1, a h3attn_rope that h3attn_rope_init did
+ * not fill, an output that overlaps another tensor other than exactly in place. */
+h3attn_status h3attn_rotary(const h3attn_rope* rope, const int32_t* positions, int64_t n_tokens, const void* q_in,
+                            int64_t q_in_stride, void* q_out, int64_t q_out_stride, int32_t num_heads, const void* k_in,
+                            int64_t k_in_stride, void* k_out, int64_t k_out_stride, int32_t num_kv_heads,
+                            int32_t inverse, void* cuda_stream);
+
+/* ---- A paged cache of keys and values -----------------------------------------
+ * The caller's device memory, described by plain data: k and v are bf16
+ * [n_pages, page_size, num_kv_heads, 128], element (page, token, head, dim) at
+ * page*page_stride + token*token_stride + head*head_stride + dim, so that a page
+ * may hold a token's heads together or a head's tokens.  Strides (elements, the same for k
+ * and v) are multiples of 8, rows must not share elements; 16-byte aligned.
+ * A slot is a row of the cache: page * page_size + token, below 2^31 in all. */
+typedef struct {
+  void* k;
+  void* v;
+  int32_t n_pages, page_size, num_kv_heads;
+  int64_t page_stride, token_stride, head_stride;
+} h3attn_cache;
+
+/* The step's rotation with the rows' way into the cache: rotates q into q_out
+ * (both NULL: no q), k into the cache's k and copies v into its v, token i's rows
+ * to slot slots[i] (int32 [n_tokens] on the device).  A token whose slot is not a
+ * row of the cache (negative: padding) is not stored.  Slots should be distinct: of
+ * tokens with one slot the row may hold any one, or parts of several.  k_in, v_in:
+ * kv_row_stride.  Otherwise as h3attn_rotary.
+ * Errors: as there; EINVAL for a NULL or misaligned slots, k_in or v_in, for a
+ * cache with NULL or misaligned tensors, sizes < 1, 2^31 or more slots, bad
+ * strides or rows that share elements, and for tensors that share a range of bytes
+ * with the cache's k or v. */
+h3attn_status h3attn_rotary_store(const h3attn_rope* rope, const int32_t* positions, int64_t n_tokens, const void* q_in,
+                                  int64_t q_in_stride, void* q_out, int64_t q_out_stride, int32_t num_heads,
+                                  const void* k_in, const void* v_in, int64_t kv_row_stride, const h3attn_cache* cache,
+                                  const int32_t* slots, void* cuda_stream);
+
+/* Moves rows within the cache, k and v alike: group g copies the rows src[g][i]
+ * to dst[g][i], i < width (int32 [n_groups, width] on the device).  All of a
+ * group's sources are read before its first destination is written, so accepted
+ * drafts move up past one another, rows change places and pages are forked; a
+ * pair with a slot that is not a row of the cache is left out (padding: -1).  A
+ * slot may be a source any number of times.  No group may write a slot that another one names, and of
+ * equal destinations any one may stay.  n_groups = 0 is allowed.  Runs on the
+ * current device, as h3attn_rotary.
+ * Errors: EINVAL for a bad cache (above), NULL or misaligned lists, n_groups < 0
+ * or above 2^31 - 1, lists that overlap the cache; EUNSUPPORTED for width outside [1, 256] or more
+ * than 32,767 heads. */
+h3attn_status h3attn_cache_move(const h3attn_cache* cache, const int32_t* src, const int32_t* dst, int64_t n_groups,
+                                int32_t width, void* cuda_stream);
+
 /* Allocation-free forward.  The pages have no counterpart: this entry point
  * exists for callers that may not allocate device memory -- code whose device
  * memory is owned by a host framework's pool or arena (an engine plugin, a

@@ -943,6 +943,273 @@ h3attn_status h3attn_walk_list_host(int32_t kind, const int32_t* cu_seqlens, int
   return H3ATTN_OK;
 }
 
+// ------------------------------------------- rotary positions, the cache ----
+
+h3attn_status h3attn_rope_init(const h3attn_rope_opts* opts, h3attn_rope* out) {
+  clear_error();
+  if (opts == nullptr || out == nullptr) return fail(H3ATTN_EINVAL, "opts or out is NULL");
+  const int32_t d = opts->rope_dims;
+  if (d < 16 || d > kHeadDim || d % 16)
+    return fail(H3ATTN_EUNSUPPORTED, "rope_dims must be a multiple of 16 in [16, 128] (got %d)", d);
+  if (opts->interleaved != 0 && opts->interleaved != 1) return fail(H3ATTN_EINVAL, "interleaved must be 0 or 1");
+  if (!std::isfinite(opts->base) || !(opts->base > 1.0)) return fail(H3ATTN_EINVAL, "base must be finite and > 1");
+  if (opts->scaling < H3ATTN_ROPE_PLAIN || opts->scaling > H3ATTN_ROPE_BY_PARTS)
+    return fail(H3ATTN_EINVAL, "scaling must be a h3attn_rope_scaling (got %d)", opts->scaling);
+  const double s = opts->scaling == H3ATTN_ROPE_PLAIN ? 1.0 : opts->factor;
+  if (!std::isfinite(s) || !(s >= 1.0)) return fail(H3ATTN_EINVAL, "factor must be finite and >= 1");
+  const bool parts = opts->scaling == H3ATTN_ROPE_BY_PARTS;
+  if (parts && (!std::isfinite(opts->original_len) || !(opts->original_len > 0.0) || !std::isfinite(opts->beta_fast) ||
+                !(opts->beta_slow >= 0.0) || !(opts->beta_fast > opts->beta_slow)))
+    return fail(H3ATTN_EINVAL, "scaling by parts needs original_len > 0 and beta_fast > beta_slow >= 0");
+  if (!std::isfinite(opts->amplitude) || opts->amplitude < 0.0 || opts->amplitude > 1e30)
+    return fail(H3ATTN_EINVAL, "amplitude must be 0 (the default) or in (0, 1e30]");
+  if (opts->n_axes < 1 || opts->n_axes > 3) return fail(H3ATTN_EINVAL, "n_axes must be in [1, 3] (got %d)", opts->n_axes);
+  for (int32_t j = 0; opts->axis != nullptr && j < d / 2; ++j)
+    if (opts->axis[j] >= opts->n_axes) return fail(H3ATTN_EINVAL, "axis[%d] = %d is no axis", j, (int)opts->axis[j]);
+  const double two_pi = 6.283185307179586476925;
+  const double base = opts->scaling == H3ATTN_ROPE_NTK ? opts->base * std::pow(s, (double)d / (d - 2)) : opts->base;
+  if (!std::isfinite(base)) return fail(H3ATTN_EINVAL, "base and factor are too large");
+  h3attn_rope r;
+  std::memset(&r, 0, sizeof(r));
+  r.rope_dims = d;
+  r.interleaved = opts->interleaved;
+  r.n_axes = opts->n_axes;
+  r.amplitude = (float)(opts->amplitude != 0.0 ? opts->amplitude : parts ? 0.1 * std::log(s) + 1.0 : 1.0);
+  for (int32_t j = 0; j < d / 2; ++j) {
+    double f = std::pow(base, -2.0 * j / d);
+    if (opts->scaling == H3ATTN_ROPE_LINEAR) f /= s;
+    if (parts) {
+      double g = (opts->original_len * f / two_pi - opts->beta_slow) / (opts->beta_fast - opts->beta_slow);
+      g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
+      f *= g + (1.0 - g) / s;
+    }
+    r.turns[j] = (uint64_t)std::ldexp(f / two_pi, 64);  // (f <= 1: below 2^62)
+    r.axis[j] = opts->axis != nullptr ? opts->axis[j] : 0;
+  }
+  *out = r;
+  return H3ATTN_OK;
+}
+
+namespace {
+
+h3attn_status check_rope(const h3attn_rope* rope, const int32_t* positions, int64_t n_tokens) {
+  if (!rope || (!positions && n_tokens != 0)) return fail(H3ATTN_EINVAL, "NULL rope or positions");
+  bool good = rope->rope_dims >= 16 && rope->rope_dims <= kHeadDim && rope->rope_dims % 16 == 0 &&
+              (rope->interleaved == 0 || rope->interleaved == 1) && rope->n_axes >= 1 && rope->n_axes <= 3;
+  for (int j = 0; good && j < 64; ++j) good = rope->axis[j] < rope->n_axes;
+  if (!good) return fail(H3ATTN_EINVAL, "rope was not filled by h3attn_rope_init");
+  if (!aligned4(positions)) return fail(H3ATTN_EINVAL, "positions must be 4-byte aligned");
+  if (n_tokens < 0 || n_tokens > INT32_MAX) return fail(H3ATTN_EINVAL, "n_tokens must be in [0, 2^31) (got %lld)", (long long)n_tokens);
+  return H3ATTN_OK;
+}
+
+// Rows of a call without a plan: bf16 [n, heads, 128].
+struct Rows {
+  const char* name;
+  const void* p;
+  int64_t stride;
+  int32_t heads;
+  int64_t width() const { return (int64_t)heads * kHeadDim; }
+  uintptr_t bytes(int64_t n) const { return n > 0 ? (uintptr_t)((n - 1) * stride + width()) * 2 : 0; }
+};
+
+h3attn_status check_rows(const Rows& r, int64_t n) {
+  if (!r.p) return fail(H3ATTN_EINVAL, "NULL %s", r.name);
+  if (!aligned16(r.p)) return fail(H3ATTN_EINVAL, "%s must be 16-byte aligned", r.name);
+  if (r.heads < 1 || r.heads > (1 << 20)) return fail(H3ATTN_EINVAL, "%s: heads must be in [1, 2^20] (got %d)", r.name, r.heads);
+  if (r.stride < r.width() || r.stride % 8 || (n > 1 && r.stride > (int64_t(1) << 60) / n))
+    return fail(H3ATTN_EINVAL, "%s: its row stride must be >= %lld and a multiple of 8 (got %lld)", r.name,
+                (long long)r.width(), (long long)r.stride);
+  return H3ATTN_OK;
+}
+
+// True when two tensors of n rows can share an element: with equal strides their
+// column windows are compared, otherwise any byte counts.
+bool rows_overlap(const Rows& a, const Rows& b, int64_t n) {
+  if (!ranges_overlap(a.p, a.bytes(n), b.p, b.bytes(n))) return false;
+  if (a.stride != b.stride) return true;
+  const int64_t delta = ((int64_t)reinterpret_cast<uintptr_t>(b.p) - (int64_t)reinterpret_cast<uintptr_t>(a.p)) / 2;
+  int64_t r = delta % a.stride;
+  if (r < 0) r += a.stride;
+  return r < a.width() || r + b.width() > a.stride;
+}
+
+h3attn_status check_cache(const h3attn_cache* c) {
+  if (!c || !c->k || !c->v) return fail(H3ATTN_EINVAL, "NULL cache or cache tensor");
+  if (!aligned16(c->k) || !aligned16(c->v)) return fail(H3ATTN_EINVAL, "the cache's tensors must be 16-byte aligned");
+  if (c->n_pages < 1 || c->page_size < 1 || c->num_kv_heads < 1)
+    return fail(H3ATTN_EINVAL, "the cache's sizes must be >= 1 (got %d pages of %d, %d heads)", c->n_pages, c->page_size,
+                c->num_kv_heads);
+  if ((int64_t)c->n_pages * c->page_size > INT32_MAX) return fail(H3ATTN_EINVAL, "the cache has 2^31 or more slots");
+  // rows share no element where every stride reaches past what the smaller ones span
+  struct Dim {
+    int64_t n, stride;
+  } d[3] = {{c->n_pages, c->page_stride}, {c->page_size, c->token_stride}, {c->num_kv_heads, c->head_stride}};
+  std::sort(d, d + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+  int64_t span = kHeadDim;
+  for (const Dim& x : d) {
+    if (x.stride < 0 || x.stride % 8) return fail(H3ATTN_EINVAL, "the cache's strides must be multiples of 8 (got %lld)", (long long)x.stride);
+    if (x.n == 1) continue;
+    if (x.stride < span || x.stride > (int64_t(1) << 38))
+      return fail(H3ATTN_EINVAL, "the cache's rows share elements, or lie too far apart (stride %lld)", (long long)x.stride);
+    span += (x.n - 1) * x.stride;
+  }
+  if (c->k == c->v) return fail(H3ATTN_EINVAL, "the cache's k and v are the same");
+  return H3ATTN_OK;
+}
+
+// Bytes that the cache's k (or v) spans.
+uintptr_t cache_bytes(const h3attn_cache* c) {
+  return (uintptr_t)((c->n_pages - 1) * c->page_stride + (c->page_size - 1) * c->token_stride +
+                     (c->num_kv_heads - 1) * c->head_stride + kHeadDim) * 2;
+}
+bool overlaps_cache(const h3attn_cache* c, const void* p, uintptr_t bytes) {
+  const uintptr_t n = cache_bytes(c);
+  return ranges_overlap(c->k, n, p, bytes) || ranges_overlap(c->v, n, p, bytes);
+}
+
+cudaError_t current_sms(int* sms) {
+  clear_runtime_error();
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
+h3attn_status launch_rotary_args(const RotaryArgs& a, void* cuda_stream) {
+  int sms = 0;
+  cudaError_t e = current_sms(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  e = launch_rotary(a, sms, static_cast<cudaStream_t>(cuda_stream));
+  return e == cudaSuccess ? H3ATTN_OK : cuda_fail(e, "rotary launch");
+}
+
+}  // namespace
+
+h3attn_status h3attn_rotary(const h3attn_rope* rope, const int32_t* positions, int64_t n_tokens, const void* q_in,
+                            int64_t q_in_stride, void* q_out, int64_t q_out_stride, int32_t num_heads, const void* k_in,
+                            int64_t k_in_stride, void* k_out, int64_t k_out_stride, int32_t num_kv_heads,
+                            int32_t inverse, void* cuda_stream) {
+  clear_error();
+  if (h3attn_status s = check_rope(rope, positions, n_tokens)) return s;
+  if (n_tokens == 0) return H3ATTN_OK;
+  const bool with_q = q_in || q_out, with_k = k_in || k_out;
+  if (!with_q && !with_k) return fail(H3ATTN_EINVAL, "NULL q and k");
+  const Rows in[2] = {{"q_in", q_in, q_in_stride, num_heads}, {"k_in", k_in, k_in_stride, num_kv_heads}};
+  const Rows out[2] = {{"q_out", q_out, q_out_stride, num_heads}, {"k_out", k_out, k_out_stride, num_kv_heads}};
+  const bool with[2] = {with_q, with_k};
+  for (int i = 0; i < 2; ++i)
+    if (with[i]) {
+      if (h3attn_status s = check_rows(in[i], n_tokens)) return s;
+      if (h3attn_status s = check_rows(out[i], n_tokens)) return s;
+    }
+  for (int i = 0; i < 2; ++i) {
+    if (!with[i]) continue;
+    if (ranges_overlap(out[i].p, out[i].bytes(n_tokens), positions, (uintptr_t)n_tokens * rope->n_axes * 4))
+      return fail(H3ATTN_EINVAL, "%s overlaps positions", out[i].name);
+    for (int j = 0; j < 2; ++j) {
+      if (!with[j]) continue;
+      const bool in_place = i == j && in[j].p == out[i].p && in[j].stride == out[i].stride;
+      if (!in_place && rows_overlap(out[i], in[j], n_tokens))
+        return fail(H3ATTN_EINVAL, "%s overlaps %s other than exactly in place", out[i].name, in[j].name);
+    }
+  }
+  if (with_q && with_k && rows_overlap(out[0], out[1], n_tokens)) return fail(H3ATTN_EINVAL, "q_out and k_out overlap");
+  RotaryArgs a{};
+  a.rope = *rope;
+  a.positions = positions;
+  a.n = n_tokens;
+  a.q_in = static_cast<const __nv_bfloat16*>(q_in);
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.q_in_stride = q_in_stride;
+  a.q_out_stride = q_out_stride;
+  a.k_in = static_cast<const __nv_bfloat16*>(k_in);
+  a.k_in_stride = k_in_stride;
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.k_out_stride = k_out_stride;
+  a.k_out_head_stride = kHeadDim;
+  a.H = with_q ? num_heads : 0;
+  a.Hk = with_k ? num_kv_heads : 0;
+  a.inverse = inverse != 0;
+  return launch_rotary_args(a, cuda_stream);
+}
+
+h3attn_status h3attn_rotary_store(const h3attn_rope* rope, const int32_t* positions, int64_t n_tokens, const void* q_in,
+                                  int64_t q_in_stride, void* q_out, int64_t q_out_stride, int32_t num_heads,
+                                  const void* k_in, const void* v_in, int64_t kv_row_stride, const h3attn_cache* cache,
+                                  const int32_t* slots, void* cuda_stream) {
+  clear_error();
+  if (h3attn_status s = check_rope(rope, positions, n_tokens)) return s;
+  if (h3attn_status s = check_cache(cache)) return s;
+  if (n_tokens == 0) return H3ATTN_OK;
+  if (!slots || !aligned4(slots)) return fail(H3ATTN_EINVAL, "slots must be a 4-byte aligned list");
+  const bool with_q = q_in || q_out;
+  const Rows q[2] = {{"q_in", q_in, q_in_stride, num_heads}, {"q_out", q_out, q_out_stride, num_heads}};
+  const Rows kv[2] = {{"k_in", k_in, kv_row_stride, cache->num_kv_heads}, {"v_in", v_in, kv_row_stride, cache->num_kv_heads}};
+  const uintptr_t n = (uintptr_t)n_tokens;
+  for (int i = 0; i < 2; ++i) {
+    if (h3attn_status s = check_rows(kv[i], n_tokens)) return s;
+    if (overlaps_cache(cache, kv[i].p, kv[i].bytes(n_tokens))) return fail(H3ATTN_EINVAL, "%s overlaps the cache", kv[i].name);
+    if (!with_q) continue;
+    if (h3attn_status s = check_rows(q[i], n_tokens)) return s;
+    if (overlaps_cache(cache, q[i].p, q[i].bytes(n_tokens))) return fail(H3ATTN_EINVAL, "%s overlaps the cache", q[i].name);
+  }
+  if (overlaps_cache(cache, positions, n * rope->n_axes * 4) || overlaps_cache(cache, slots, n * 4))
+    return fail(H3ATTN_EINVAL, "positions or slots overlap the cache");
+  if (with_q) {
+    if (ranges_overlap(q_out, q[1].bytes(n_tokens), positions, n * rope->n_axes * 4) ||
+        ranges_overlap(q_out, q[1].bytes(n_tokens), slots, n * 4))
+      return fail(H3ATTN_EINVAL, "q_out overlaps positions or slots");
+    if (!(q_in == q_out && q_in_stride == q_out_stride) && rows_overlap(q[1], q[0], n_tokens))
+      return fail(H3ATTN_EINVAL, "q_out overlaps q_in other than exactly in place");
+    for (const Rows& r : kv)
+      if (rows_overlap(q[1], r, n_tokens)) return fail(H3ATTN_EINVAL, "q_out overlaps %s", r.name);
+  }
+  RotaryArgs a{};
+  a.rope = *rope;
+  a.positions = positions;
+  a.n = n_tokens;
+  a.q_in = static_cast<const __nv_bfloat16*>(q_in);
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.q_in_stride = q_in_stride;
+  a.q_out_stride = q_out_stride;
+  a.k_in = static_cast<const __nv_bfloat16*>(k_in);
+  a.v_in = static_cast<const __nv_bfloat16*>(v_in);
+  a.k_in_stride = kv_row_stride;
+  a.k_out = static_cast<__nv_bfloat16*>(cache->k);
+  a.v_out = static_cast<__nv_bfloat16*>(cache->v);
+  a.k_out_stride = cache->token_stride;
+  a.k_out_head_stride = cache->head_stride;
+  a.slots = slots;
+  a.page_stride = cache->page_stride;
+  a.page_size = cache->page_size;
+  a.n_slots = cache->n_pages * cache->page_size;
+  a.H = with_q ? num_heads : 0;
+  a.Hk = a.Hv = cache->num_kv_heads;
+  return launch_rotary_args(a, cuda_stream);
+}
+
+h3attn_status h3attn_cache_move(const h3attn_cache* cache, const int32_t* src, const int32_t* dst, int64_t n_groups,
+                                int32_t width, void* cuda_stream) {
+  clear_error();
+  if (h3attn_status s = check_cache(cache)) return s;
+  if (n_groups == 0) return H3ATTN_OK;
+  if (!src || !dst || !aligned4(src) || !aligned4(dst)) return fail(H3ATTN_EINVAL, "src and dst must be 4-byte aligned lists");
+  if (n_groups < 0 || n_groups > INT32_MAX) return fail(H3ATTN_EINVAL, "n_groups must be in [0, 2^31) (got %lld)", (long long)n_groups);
+  if (width < 1 || width > 256) return fail(H3ATTN_EUNSUPPORTED, "width must be in [1, 256] (got %d)", width);
+  if (cache->num_kv_heads > 32767) return fail(H3ATTN_EUNSUPPORTED, "more than 32767 key heads");
+  const uintptr_t bytes = (uintptr_t)n_groups * width * 4;
+  if (overlaps_cache(cache, src, bytes) || overlaps_cache(cache, dst, bytes))
+    return fail(H3ATTN_EINVAL, "a list overlaps the cache");
+  int sms = 0;
+  cudaError_t e = current_sms(&sms);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const CacheMoveArgs a{static_cast<__nv_bfloat16*>(cache->k), static_cast<__nv_bfloat16*>(cache->v), src, dst, n_groups,
+                        width, cache->page_size, cache->n_pages * cache->page_size, cache->page_stride,
+                        cache->token_stride, cache->head_stride};
+  e = launch_cache_move(a, cache->num_kv_heads, static_cast<cudaStream_t>(cuda_stream));
+  return e == cudaSuccess ? H3ATTN_OK : cuda_fail(e, "cache move launch");
+}
+
 h3attn_status h3attn_get_device_error(h3attn_plan_t plan, void* cuda_stream) {
   clear_error();
   if (h3attn_status s = check_plan(plan)) return s;

@@ -468,6 +468,43 @@ cudaError_t launch_fp8_quantize(const Fp8QuantArgs& a, int num_sms, cudaStream_t
 // v and the FP8 outputs), then the v quantisation (fp8_quant.cu).
 cudaError_t launch_prologue_fp8(const PrologueArgs& p, const Fp8QuantArgs& a, cudaStream_t stream);
 
+// Rotary positions (rotary.cu): q rows (H of them a token), k rows (Hk) and v rows
+// (Hv, copied only); k and v go to rows of their own or, with slots, into a cache.
+struct RotaryArgs {
+  h3attn_rope rope;
+  const int32_t* positions;    // [n_axes, n]
+  int64_t n;
+  const __nv_bfloat16* q_in;
+  __nv_bfloat16* q_out;
+  int64_t q_in_stride, q_out_stride;
+  const __nv_bfloat16* k_in;
+  const __nv_bfloat16* v_in;
+  int64_t k_in_stride;         // v's too
+  __nv_bfloat16* k_out;
+  __nv_bfloat16* v_out;
+  int64_t k_out_stride;        // of a token's rows, or of a token in its page
+  int64_t k_out_head_stride;
+  const int32_t* slots;        // [n], or null: rows of their own
+  int64_t page_stride;
+  int32_t page_size, n_slots;
+  int32_t H, Hk, Hv;
+  int32_t inverse;
+  int32_t block_tokens;        // (the launcher's)
+};
+cudaError_t launch_rotary(const RotaryArgs& a, int num_sms, cudaStream_t stream);
+
+// Row moves within a cache (cache_move.cu).
+struct CacheMoveArgs {
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;
+  const int32_t* src;          // [n_groups, width]
+  const int32_t* dst;
+  int64_t n_groups;
+  int32_t width, page_size, n_slots;
+  int64_t page_stride, token_stride, head_stride;
+};
+cudaError_t launch_cache_move(const CacheMoveArgs& a, int heads, cudaStream_t stream);
+
 cudaError_t launch_selftest_bounded_wait(uint64_t timeout_ns, uint32_t* d_flag,
                                          cudaStream_t stream);
 

@@ -42,6 +42,22 @@ class h3attn_plan_opts(ctypes.Structure):
                 ("rope_base", c_double)]
 
 
+class h3attn_rope_opts(ctypes.Structure):
+    _fields_ = [("rope_dims", c_int32), ("interleaved", c_int32), ("base", c_double), ("scaling", c_int32),
+                ("factor", c_double), ("original_len", c_double), ("beta_fast", c_double), ("beta_slow", c_double),
+                ("amplitude", c_double), ("n_axes", c_int32), ("axis", c_void_p)]
+
+
+class h3attn_rope(ctypes.Structure):
+    _fields_ = [("rope_dims", c_int32), ("interleaved", c_int32), ("n_axes", c_int32), ("amplitude", c_float),
+                ("turns", c_uint64 * 64), ("axis", ctypes.c_uint8 * 64)]
+
+
+class h3attn_cache(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("n_pages", c_int32), ("page_size", c_int32),
+                ("num_kv_heads", c_int32), ("page_stride", c_int64), ("token_stride", c_int64), ("head_stride", c_int64)]
+
+
 _SIGS = {
     "h3attn_plan_create": [POINTER(h3attn_doc), c_int32, POINTER(h3attn_plan_opts), c_void_p,
                            POINTER(c_void_p)],
@@ -80,6 +96,12 @@ _SIGS = {
     "h3attn_walk_list_host": [c_int32, c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_int64,
                               c_void_p, c_void_p, c_int64, c_void_p, c_int64, POINTER(c_int64), POINTER(c_int32),
                               POINTER(c_int64), POINTER(c_int64), POINTER(c_int64)],
+    "h3attn_rope_init": [POINTER(h3attn_rope_opts), POINTER(h3attn_rope)],
+    "h3attn_rotary": [POINTER(h3attn_rope), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int32, c_void_p,
+                      c_int64, c_void_p, c_int64, c_int32, c_int32, c_void_p],
+    "h3attn_rotary_store": [POINTER(h3attn_rope), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int32,
+                            c_void_p, c_void_p, c_int64, POINTER(h3attn_cache), c_void_p, c_void_p],
+    "h3attn_cache_move": [POINTER(h3attn_cache), c_void_p, c_void_p, c_int64, c_int32, c_void_p],
     "h3attn_get_device_error": [c_void_p, c_void_p],
     "h3attn_selftest_bounded_wait": [c_uint64, c_void_p],
     "h3attn_selftest_plan_wait": [c_void_p, c_uint64, c_void_p],
@@ -508,6 +530,126 @@ def h3attn_walk_list_host(kind: int, cu_seqlens, num_heads: int, p0: int, p1: in
     _check(lib.h3attn_walk_list_host(*head, units.ctypes.data, n.value, off.ctypes.data, joins.ctypes.data, nj.value,
                                      own.ctypes.data, no.value, *tail), "h3attn_walk_list_host")
     return units, off, joins, own, rows.value
+
+
+# ------------------------------------------------ positions, paged cache ----
+
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
+
+
+def h3attn_rope_init(rope_dims: int = 128, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                     factor: float = 1.0, original_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                     amplitude: float = 0.0, axes=None, n_axes=None) -> h3attn_rope:
+    """Frequencies of a rotary embedding (host data for the rotary calls); scaling is "none",
+    "linear", "ntk" or "parts", axes the position axis of each of the rope_dims / 2 pairs."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_SCALINGS)} (got {scaling!r})")
+    axis = None
+    if axes is not None:
+        if len(axes) != int(rope_dims) // 2:
+            raise ValueError(f"axes must name the axis of each of {int(rope_dims) // 2} pairs (got {len(axes)})")
+        if any(not 0 <= int(x) < 3 for x in axes):
+            raise ValueError("axes must be 0, 1 or 2")
+        axis = np.asarray([int(x) for x in axes], dtype=np.uint8)
+        n_axes = int(axis.max()) + 1 if n_axes is None and axis.size else n_axes
+    opts = h3attn_rope_opts(int(rope_dims), int(bool(interleaved)), float(base), _SCALINGS[scaling], float(factor),
+                            float(original_len), float(beta_fast), float(beta_slow), float(amplitude), int(n_axes or 1),
+                            axis.ctypes.data if axis is not None else None)
+    out = h3attn_rope()
+    _check(load().h3attn_rope_init(ctypes.byref(opts), ctypes.byref(out)), "h3attn_rope_init")
+    return out
+
+
+class Cache:
+    """The caller's cache: bf16 tensors k and v of [pages, tokens of a page, heads, 128], of any
+    strides but the last (a head-major one is a transposed view)."""
+
+    def __init__(self, k, v):
+        for x in (k, v):
+            if (x.dtype is not _torch().bfloat16 or x.dim() != 4 or x.shape[3] != 128 or x.stride(3) != 1
+                    or x.get_device() < 0 or x.shape != k.shape or x.stride() != k.stride() or x.device != k.device):
+                raise ValueError("a cache is two bfloat16 tensors [pages, tokens, heads, 128] on one GPU with equal strides "
+                                 f"and a contiguous last dimension (got {tuple(x.shape)}, strides {x.stride()}, "
+                                 f"{x.dtype}, {x.device})")
+        self.k, self.v, self.device = k, v, k.get_device()
+        self.num_kv_heads = k.shape[2]
+        self.c = h3attn_cache(k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[1], k.shape[2], k.stride(0), k.stride(1),
+                              k.stride(2))
+
+
+def _heads(x, name, n, device):
+    """(pointer, row stride, heads) of bf16 rows [n, heads, 128] on the device."""
+    if (x.dtype is not _torch().bfloat16 or x.dim() != 3 or x.shape[2] != 128 or x.shape[0] != n or x.stride(2) != 1
+            or (x.stride(1) != 128 and x.shape[1] != 1) or x.get_device() != device):
+        raise ValueError(f"{name} must be a bfloat16 tensor [{n}, heads, 128] with contiguous heads on GPU {device} "
+                         f"(got {tuple(x.shape)}, strides {x.stride()}, {x.dtype}, {x.device})")
+    heads = x.shape[1]
+    return x.data_ptr(), (x.stride(0) if n > 1 else 128 * heads), heads
+
+
+def _ints(x, name, shape, device):
+    """The pointer of a contiguous int32 tensor of the given shape on the device."""
+    if x.dtype is not _torch().int32 or tuple(x.shape) != tuple(shape) or not x.is_contiguous() or x.get_device() != device:
+        raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on GPU {device} "
+                         f"(got {tuple(x.shape)}, {x.dtype}, {x.device})")
+    return x.data_ptr()
+
+
+def _positions(rope, positions, n, device):
+    if rope.n_axes == 1 and positions.dim() == 1:
+        return _ints(positions, "positions", (n,), device)
+    return _ints(positions, "positions", (rope.n_axes, n), device)
+
+
+def _call_on(device, fn, name, *args, stream):
+    """The call without a plan, with the tensors' device current."""
+    torch = _torch()
+    if torch.cuda.current_device() == device:
+        _check(fn(*args, _stream(stream, device)), name)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream, device)), name)
+
+
+def h3attn_rotary(rope, positions, q_in, q_out, k_in=None, k_out=None, inverse: bool = False, stream=None):
+    """Rotates q (and k): bf16 tensors [n, heads, 128], each with a row stride of its own; positions
+    int32 [n_axes, n] ([n] for one axis).  q_in and q_out, or k_in and k_out, may both be None."""
+    first = q_in if q_in is not None else k_in
+    if first is None or (q_in is None) != (q_out is None) or (k_in is None) != (k_out is None):
+        raise ValueError("an input and its output go together, and one pair is needed")
+    n, device = first.shape[0], first.get_device()
+    none = (None, 0, 0)
+    q = [_heads(x, name, n, device) if x is not None else none for x, name in ((q_in, "q_in"), (q_out, "q_out"))]
+    k = [_heads(x, name, n, device) if x is not None else none for x, name in ((k_in, "k_in"), (k_out, "k_out"))]
+    if q[0][2] != q[1][2] or k[0][2] != k[1][2]:
+        raise ValueError("an input and its output must have the same heads")
+    _call_on(device, load().h3attn_rotary, "h3attn_rotary", rope, _positions(rope, positions, n, device), n, q[0][0], q[0][1],
+             q[1][0], q[1][1], q[0][2], k[0][0], k[0][1], k[1][0], k[1][1], k[0][2], int(bool(inverse)), stream=stream)
+
+
+def h3attn_rotary_store(rope, positions, q_in, q_out, k_in, v_in, cache: Cache, slots, stream=None):
+    """Rotates q into q_out (both may be None) and k into the cache, and copies v beside it; slots
+    int32 [n]."""
+    if (q_in is None) != (q_out is None):
+        raise ValueError("q_in and q_out go together")
+    n, device = k_in.shape[0], cache.device
+    none = (None, 0, 0)
+    q = [_heads(x, name, n, device) if x is not None else none for x, name in ((q_in, "q_in"), (q_out, "q_out"))]
+    k, v = _heads(k_in, "k_in", n, device), _heads(v_in, "v_in", n, device)
+    if q[0][2] != q[1][2] or k[2] != cache.num_kv_heads or v[2] != cache.num_kv_heads:
+        raise ValueError("q_in and q_out must have the same heads, and k_in and v_in the cache's")
+    if k[1] != v[1]:
+        raise ValueError(f"k_in and v_in must share one row stride (got {k[1]}, {v[1]})")
+    _call_on(device, load().h3attn_rotary_store, "h3attn_rotary_store", rope, _positions(rope, positions, n, device), n, q[0][0],
+             q[0][1], q[1][0], q[1][1], q[0][2], k[0], v[0], k[1], cache.c, _ints(slots, "slots", (n,), device), stream=stream)
+
+
+def h3attn_cache_move(cache: Cache, src, dst, stream=None):
+    """Copies rows of the cache to other slots: src, dst int32 [groups, width]."""
+    if src.dim() != 2:
+        raise ValueError(f"src and dst are [groups, width] (got {tuple(src.shape)})")
+    _call_on(cache.device, load().h3attn_cache_move, "h3attn_cache_move", cache.c, _ints(src, "src", src.shape, cache.device),
+             _ints(dst, "dst", src.shape, cache.device), src.shape[0], src.shape[1], stream=stream)
 
 
 def h3attn_get_device_error(plan, stream=None):
