@@ -33,8 +33,8 @@
  *   - All compute calls are asynchronous on the given CUDA stream
  *     (a cudaStream_t passed as void*; NULL = the legacy default stream) and
  *     may be issued on any stream.  The library allocates no device memory on
- *     the compute path; only h3attn_plan_create, h3attn_plan_set_sparse and
- *     h3attn_plan_set_prefix allocate, and h3attn_plan_destroy frees.
+ *     the compute path; only h3attn_plan_create and the h3attn_plan_set_ calls
+ *     allocate, and h3attn_plan_destroy frees.
  *   - Functions never throw across the boundary.  Arguments are validated
  *     before anything is launched; on failure nothing is launched, the
  *     status says why, and h3attn_last_error() holds a message.
@@ -387,10 +387,11 @@ h3attn_status h3attn_forward_prefix(h3attn_plan_t plan, const void* q, const voi
                                     int64_t prefix_row_stride, void* o, int64_t o_row_stride, float softmax_scale,
                                     float* lse_out, void* cuda_stream);
 
-/* The work lists of the two forwards above for a packed layout, built on the
- * host alone, as h3attn_work_list_host does for the dense one.
+/* The work lists of the two forwards above and of h3attn_forward_causal for a
+ * packed layout, built on the host alone, as h3attn_work_list_host does for the
+ * dense one.
  *   kind 0 (list walk): p0 = q_block, p1 = max_blocks; kind 1 (prefix walk): p0
- *   = prefix_len, p1 ignored.
+ *   = prefix_len, p1 ignored; kind 2 (causal walk): p0 = num_kv_heads, p1 ignored.
  * Outputs (host memory; pass units = NULL for the sizes first):
  *   units    [*n_units][8] int32, grouped by CTA pair: first query row, end of
  *            the query rows, document begin, document end, head, then for kind 0
@@ -398,8 +399,11 @@ h3attn_status h3attn_forward_prefix(h3attn_plan_t plan, const void* q, const voi
  *            block's list), for kind 1 key tiles [lo, hi) of "the prefix's
  *            tiles, then the document's" -- with document end = -n for a segment
  *            over several documents, whose n own tiles are entries [document
- *            begin, document begin + n) of own; last the first partial row (-1: the
- *            segment writes the output itself);
+ *            begin, document begin + n) of own; for kind 2 key tiles [lo, hi) of the
+ *            document, the rows being those of `pack` heads from the head on, pack the
+ *            largest divisor up to 16 of num_heads / num_kv_heads; last the first
+ *            partial row (-1: the segment writes the output itself; kind 2: row r of head
+ *            h is at first + (h - head) * rows + r - first query row);
  *            where segments have at most 256 rows, a pair may run two streams of
  *            them side by side (the first one's come first here); for kind 1 and a
  *            few rows of documents of at most 32 tokens a segment of up to 32 rows may
@@ -536,6 +540,33 @@ h3attn_status h3attn_rotary_store(const h3attn_rope* rope, const int32_t* positi
  * than 32,767 heads. */
 h3attn_status h3attn_cache_move(const h3attn_cache* cache, const int32_t* src, const int32_t* dst, int64_t n_groups,
                                 int32_t width, void* cuda_stream);
+
+/* ---- Causal attention over whole prompts, grouped heads -------------------------
+ * The text tower's attention: documents are prompts, row i of document [a, b)
+ * attends to its rows a .. i, and query head h reads key head h / (num_heads /
+ * num_kv_heads).  num_heads is the plan's.
+ *
+ * h3attn_plan_set_causal adds the work list to a plan; allocation, capture and
+ * "once per plan" as h3attn_plan_set_sparse (a plan may have every list).
+ * Errors: EINVAL for a NULL plan, num_kv_heads < 1 or not a divisor of num_heads,
+ * heads already set, more than 2^31 - 513 tokens, or partial results of 2^31 rows or more;
+ * ENOMEM / ECUDA from allocation or upload. */
+h3attn_status h3attn_plan_set_causal(h3attn_plan_t plan, int32_t num_kv_heads, void* cuda_stream);
+
+/* For each head h and each query row i of document [a, b), with g = h /
+ * (num_heads / num_kv_heads):
+ *     o_i = sum_{j = a..i} softmax_j(softmax_scale <q_i, k_j,g>) v_j,g
+ *     lse[h*S + i] = ln sum_{j = a..i} exp(softmax_scale <q_i, k_j,g>)
+ * q bf16 [S,H,128] with q_row_stride, k and v bf16 [S,num_kv_heads,128] with
+ * kv_row_stride (all may lie in one fused buffer), o and lse_out as
+ * h3attn_forward.  Rows of other documents reach nothing, whatever they hold; a
+ * NaN or an infinity in v of a later row of the same document may reach the rows
+ * up to 511 before it.  |v| may be up to 2^64.
+ * Errors: as h3attn_forward; EINVAL without h3attn_plan_set_causal, and for
+ * lse_out that overlaps q, k or v. */
+h3attn_status h3attn_forward_causal(h3attn_plan_t plan, const void* q, int64_t q_row_stride, const void* k, const void* v,
+                                    int64_t kv_row_stride, void* o, int64_t o_row_stride, float softmax_scale,
+                                    float* lse_out, void* cuda_stream);
 
 /* Allocation-free forward.  The pages have no counterpart: this entry point
  * exists for callers that may not allocate device memory -- code whose device

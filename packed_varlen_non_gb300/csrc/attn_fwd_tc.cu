@@ -114,6 +114,12 @@
 //     for all its rows, but their PVs leave the lanes of O of the other
 //     documents' rows alone (the MMA's lane mask).
 // A list without a valid tile runs one fully masked tile: o = 0, lse = -inf.
+// The causal walk (h3attn_forward_causal) is the document walk up to a segment's
+// last token, with every row's own end of the keys.  The query heads that share a key
+// head share segments too: a tile's rows are (token, head of the pack) pairs, token
+// by token, which one box of a three-dimensional tensor map fetches in that order.
+// So a segment spans fewer tokens (4 x 128 / pack), whose keys end at nearly the same
+// place, and K and V pass once for all of them.
 // Bound by the tensor pipe for long walks (1.28 us a tile and CTA pair, 512 rows,
 // which is the dense forward's rate: 682 us for 1.12e12 flops in a loop, 1,640
 // TFLOP/s; 628 us alone); a segment costs another 4 us for its boundary, where
@@ -223,8 +229,9 @@ struct Bars {
 };
 
 // Key walks: the unit's own document (the dense forward), the tiles listed for
-// its query block, the shared prefix's tiles and then the document's.
-constexpr int kWalkDoc = 0, kWalkList = 1, kWalkPrefix = 2;
+// its query block, the shared prefix's tiles and then the document's, the document's
+// up to each row itself.
+constexpr int kWalkDoc = 0, kWalkList = 1, kWalkPrefix = 2, kWalkCausal = 3;
 
 // kPair (the other walks, segments of up to 256 rows: 256-row query blocks, and
 // where the walks are short): a CTA pair runs two streams of segments, each with
@@ -265,19 +272,34 @@ struct Walk<kWalkPrefix> {
   int32_t len, tiles;
 };
 
+template <>
+struct Walk<kWalkCausal> {
+  int32_t pack, toks;   // heads and tokens of a query tile (pack * toks <= 128 rows)
+  uint32_t recip;       // row / pack = row * recip >> 16 for rows below 128
+  int32_t group;        // query heads of a key head
+};
+
 struct UnitGeom {
   int32_t q0, kv0, kv1, head, lo, hi, part, n_st;  // key tiles [lo, hi) of the walk
   int32_t v_off;                                   // FP8: the document's first key in the transposed V
+                                                   // causal walk: the key head
   int32_t q1;                                      // end of the unit's query rows
   const int32_t* list;                             // list walk: the segment's tiles, step j's at list[j] (null: none)
   int32_t n;                                       // list walk: entries of the list; the steps after them are masked
                                                    // prefix walk: own tiles of a segment over several documents
 };
 
-// First row of this CTA's query tile s of a unit.
-template <bool kPair>
-__device__ __forceinline__ int32_t tile_row(const UnitGeom& g, int s, uint32_t rank) {
+// First row (token) of this CTA's query tile s of a unit.
+template <int kWalk, bool kPair>
+__device__ __forceinline__ int32_t tile_row(const UnitGeom& g, int s, uint32_t rank, const Walk<kWalk>& walk) {
+  if constexpr (kWalk == kWalkCausal) return g.q0 + ((kPair ? 0 : 2 * s) + (int32_t)rank) * walk.toks;
   return g.q0 + (kPair ? 0 : s * 2 * kTileRows) + (int32_t)rank * kTileRows;
+}
+
+// The head whose keys and values a unit reads.
+template <int kWalk>
+__device__ __forceinline__ int32_t key_head(const UnitGeom& g) {
+  return kWalk == kWalkCausal ? g.v_off : g.head;
 }
 
 // Entries [*lo, *hi) of its query block's list that a segment (its record's
@@ -319,7 +341,12 @@ __device__ __forceinline__ UnitGeom unit_geom(const WorkUnit* units, int u, cons
     g.part = x.w;
     g.v_off = 0;
     g.n_st = (w.x + 2 * kTileRows < w.y) ? 2 : 1;
-    if constexpr (kWalk == kWalkPrefix) {
+    if constexpr (kWalk == kWalkCausal) {
+      g.lo = x.y;
+      g.hi = x.z;
+      g.v_off = x.x / walk.group;
+      g.n_st = (w.x + 2 * walk.toks < w.y) ? 2 : 1;
+    } else if constexpr (kWalk == kWalkPrefix) {
       g.lo = x.y;
       g.hi = x.z;
       g.n = max(-w.w, 0);  // kv0: the first of them in the table
@@ -358,7 +385,7 @@ struct KeyTile {
 template <int kWalk>
 __device__ __forceinline__ KeyTile key_tile(const UnitGeom& g, int j, const int4& entry, const Walk<kWalk>& walk) {
   KeyTile t{g.kv0, 0, 0, kUnitRows, false, false};
-  if constexpr (kWalk == kWalkDoc) {
+  if constexpr (kWalk == kWalkDoc || kWalk == kWalkCausal) {
     t.row = g.kv0 + j * kTileRows;
     t.rem = g.kv1 - t.row;
   } else if constexpr (kWalk == kWalkPrefix) {
@@ -381,6 +408,21 @@ __device__ __forceinline__ KeyTile key_tile(const UnitGeom& g, int j, const int4
     t.bad = !in && j < g.n;
   }
   return t;
+}
+
+// A bf16 query tile whose first row is `row`, in two halves of 64 dims.
+template <int kWalk>
+__device__ __forceinline__ void load_q_tile(uint32_t dst, const CUtensorMap* tm, uint32_t bar, int32_t head, int32_t row,
+                                            uint64_t pol, const Walk<kWalk>& walk) {
+  if constexpr (kWalk == kWalkCausal) {
+    dev::mbar_arrive_expect_tx(bar, 256u * (uint32_t)(walk.pack * walk.toks));
+    dev::tma_load_3d(dst, tm, bar, 0, head, row, pol);
+    dev::tma_load_3d(dst + kQHalfBytes, tm, bar, 64, head, row, pol);
+  } else {
+    dev::mbar_arrive_expect_tx(bar, Cfg<false>::QTileBytes);
+    dev::tma_load_2d(dst, tm, bar, head * 128, row, pol);
+    dev::tma_load_2d(dst + kQHalfBytes, tm, bar, head * 128 + 64, row, pol);
+  }
 }
 
 // This CTA's half of a K tile: keys [key0 + 64 rank, +64), all 128 dims (bf16:
@@ -782,10 +824,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               info[2] = g.kv0;
             }
           const uint32_t dst = sbase + C::SmemQ + st * C::QTileBytes;
-          const int32_t row = tile_row<kPair>(g, st, rank);
-          dev::mbar_arrive_expect_tx(bars.q_full(st), C::QTileBytes);
-          dev::tma_load_2d(dst, &tm_q, bars.q_full(st), g.head * 128, row, pol_q);
-          dev::tma_load_2d(dst + kQHalfBytes, &tm_q, bars.q_full(st), g.head * 128 + 64, row, pol_q);
+          const int32_t row = tile_row<kWalk, kPair>(g, st, rank, walk);
+          load_q_tile<kWalk>(dst, &tm_q, bars.q_full(st), g.head, row, pol_q, walk);
           ++loaded_q;
           if (u == ub) {
             ok = dev::mbar_wait(bars.kv_empty(2 * st), 1, abort_flag, a.err, kTimeoutNs);
@@ -793,14 +833,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             entry = walk_entry<kWalk>(g, g.lo, walk);
             const KeyTile t = key_tile<kWalk>(g, g.lo, entry, walk);
             dev::mbar_arrive_expect_tx(bars.kv_full(2 * st), C::SlotBytes);
-            load_k_half<kFp8>(sbase + C::SmemKV + (4 * st + 1) * C::SlotBytes, k_map(t), bars.kv_full(2 * st), g.head,
-                              t.row, rank, pol_kv);
+            load_k_half<kFp8>(sbase + C::SmemKV + (4 * st + 1) * C::SlotBytes, k_map(t), bars.kv_full(2 * st),
+                              key_head<kWalk>(g), t.row, rank, pol_kv);
             n = 1;
           }
           for (int j = g.lo; ok && j < g.hi; ++j) {
             const KeyTile vt = key_tile<kWalk>(g, j, entry, walk);
             KeyTile kt = vt;
-            int k_head = g.head;
+            int k_head = key_head<kWalk>(g);
             const bool has_k = j + 1 < g.hi || u + 1 < ue;
             if (j + 1 < g.hi) {
               entry = walk_entry<kWalk>(g, j + 1, walk);
@@ -809,7 +849,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               const UnitGeom gn = unit_geom<kWalk>(a.units, u + 1, walk);
               entry = walk_entry<kWalk>(gn, gn.lo, walk);
               kt = key_tile<kWalk>(gn, gn.lo, entry, walk);
-              k_head = gn.head;
+              k_head = key_head<kWalk>(gn);
             }
             if (vt.bad && rank == 0) dev::report_bad_tile(a.err);
             const uint32_t b = 2 * st + (n & 1);
@@ -817,7 +857,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!ok) break;
             const uint32_t slot = sbase + C::SmemKV + (4 * st + 2 * (n & 1)) * C::SlotBytes;
             dev::mbar_arrive_expect_tx(bars.kv_full(b), has_k ? 2 * C::SlotBytes : C::SlotBytes);
-            load_v_half<kFp8>(slot, v_map(vt), bars.kv_full(b), g.head, vt.row, rank, pol_kv);
+            load_v_half<kFp8>(slot, v_map(vt), bars.kv_full(b), key_head<kWalk>(g), vt.row, rank, pol_kv);
             if (has_k) load_k_half<kFp8>(slot + C::SlotBytes, k_map(kt), bars.kv_full(b), k_head, kt.row, rank, pol_kv);
             ++n;
           }
@@ -859,14 +899,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!ok) break;
           if (o_tma != 0 && g.part < 0) {
             const uint32_t tile = sbase + C::SmemQ + i * C::QTileBytes;
-            const int32_t base_row = tile_row<kPair>(g, s, rank);
+            const int32_t base_row = tile_row<kWalk, kPair>(g, s, rank, walk);
             bool any = false;
+            int warp_toks = 32;  // rows (tokens) of a warp
+            if constexpr (kWalk == kWalkCausal) warp_toks = walk.toks / 4;
 #pragma unroll 1
             for (int w = 0; w < 4; ++w) {
-              const int32_t row0 = base_row + 32 * w;
-              if (row0 + 31 >= g.q1) break;  // (the softmax warps' own test)
-              dev::tma_store_2d(&tm_o, tile + 32u * w * 128u, g.head * kHeadDim, row0);
-              dev::tma_store_2d(&tm_o, tile + kQHalfBytes + 32u * w * 128u, g.head * kHeadDim + 64, row0);
+              const int32_t row0 = base_row + warp_toks * w;
+              if (row0 + warp_toks - 1 >= g.q1) break;  // (the softmax warps' own test)
+              if constexpr (kWalk == kWalkCausal) {
+                dev::tma_store_3d(&tm_o, tile + 32u * w * 128u, 0, g.head, row0);
+                dev::tma_store_3d(&tm_o, tile + kQHalfBytes + 32u * w * 128u, 64, g.head, row0);
+              } else {
+                dev::tma_store_2d(&tm_o, tile + 32u * w * 128u, g.head * kHeadDim, row0);
+                dev::tma_store_2d(&tm_o, tile + kQHalfBytes + 32u * w * 128u, g.head * kHeadDim + 64, row0);
+              }
               any = true;
             }
             if (any) {
@@ -922,13 +969,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                               pol_kv);
           } else {
             kt = key_tile<kWalk>(g, g.lo, walk_entry<kWalk>(g, g.lo, walk), walk);
-            load_k_half<kFp8>(sbase + C::SmemKV, k_map(kt), bars.kv_full(0), g.head, kt.row, rank, pol_kv);
+            load_k_half<kFp8>(sbase + C::SmemKV, k_map(kt), bars.kv_full(0), key_head<kWalk>(g), kt.row, rank, pol_kv);
           }
           grp = 1;
         }
         for (int j = g.lo; ok && j < g.hi; ++j) {
           bool has_k = j + 1 < g.hi;
-          int k_head = g.head;
+          int k_head = key_head<kWalk>(g);
           const KeyTile vt = kt;  // this step's tile: its K went out a step ago
           if constexpr (kWalk == kWalkDoc) {
             kt.row = g.kv0 + (j + 1) * kTileRows;
@@ -939,7 +986,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!has_k && has_next) {
             const UnitGeom n = unit_geom<kWalk>(a.units, u + 1, walk);
             has_k = true;
-            k_head = n.head;
+            k_head = key_head<kWalk>(n);
             if constexpr (kWalk == kWalkDoc)
               kt.row = n.kv0 + n.lo * kTileRows;
             else
@@ -954,7 +1001,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                               g.head, (kFp8 ? g.v_off : g.kv0) + j * kTileRows, rank, pol_kv);
           else
             load_v_half<kFp8>(sbase + C::SmemKV + ((2 * grp - 1) % kSlots) * C::SlotBytes, v_map(vt), bars.kv_full(b),
-                              g.head, vt.row, rank, pol_kv);
+                              key_head<kWalk>(g), vt.row, rank, pol_kv);
           if (has_k) {
             if constexpr (kWalk == kWalkDoc)
               load_k_half<kFp8>(sbase + C::SmemKV + ((2 * grp) % kSlots) * C::SlotBytes, &tm_k, bars.kv_full(b),
@@ -1346,10 +1393,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             good = dev::mbar_wait(bars.q_empty(i), (q_use[i] & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
             if (good) {
               const uint32_t dst = sbase + C::SmemQ + i * C::QTileBytes;
-              const int32_t row = tile_row<kPair>(g, s, rank);
-              dev::mbar_arrive_expect_tx(bars.q_full(i), C::QTileBytes);
-              dev::tma_load_2d(dst, &tm_q, bars.q_full(i), g.head * 128, row, pol_q);
-              dev::tma_load_2d(dst + kQHalfBytes, &tm_q, bars.q_full(i), g.head * 128 + 64, row, pol_q);
+              const int32_t row = tile_row<kWalk, kPair>(g, s, rank, walk);
+              load_q_tile<kWalk>(dst, &tm_q, bars.q_full(i), g.head, row, pol_q, walk);
             }
           }
           good = __shfl_sync(0xffffffffu, good, 0);
@@ -1525,6 +1570,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       } else {
         // bf16: 64-key halves (see the kernel header).
+        int32_t q_end = 0;  // causal walk: the end of this row's keys
+        if constexpr (kWalk == kWalkCausal)
+          q_end = tile_row<kWalk, kPair>(g, st, rank, walk) + (int32_t)(row_in_tile * walk.recip >> 16) + 1;
         int4 entry_next = walk_entry<kWalk>(g, g.lo, walk);  // an entry is loaded a tile ahead of its use
         for (int j = g.lo; ok && j < g.hi; ++j) {
           const uint32_t t = t_unit + (j - g.lo);  // the pair's running key-tile count
@@ -1536,6 +1584,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // this row's valid keys: none of another document's tile
           int rem = tile.rem;
           if (kWalk == kWalkPrefix && g.n > 0 && ((int32_t)row_in_unit < tile.lo || (int32_t)row_in_unit >= tile.hi)) rem = 0;
+          if constexpr (kWalk == kWalkCausal) rem = min(rem, q_end - tile.row);
           // the group holding V(t) and K(t + 1), and the one holding K(t)
           const uint32_t grp = kPair ? 2 * st + ((t + 1) & 1) : (t + 1) % kGroups;
           const uint32_t grp_k = kPair ? 2 * st + (t & 1) : t % kGroups;
@@ -1669,14 +1718,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       dev::tc_fence_after();
       const int32_t local = (kPair ? 0 : st * 2 * kTileRows) + (int32_t)rank * kTileRows + (int32_t)row_in_tile;
-      const int32_t row = g.q0 + local;
-      const bool valid = row < g.q1;
+      int32_t row = g.q0 + local, head = g.head;
+      bool valid = row < g.q1;
+      // causal walk: token and head of a row of this tile, and its partial row (a head's tokens together)
+      [[maybe_unused]] const int32_t tile0 = tile_row<kWalk, kPair>(g, st, rank, walk);
+      [[maybe_unused]] const auto packed = [&](uint32_t r, int32_t* tok, int32_t* sub) {
+        if constexpr (kWalk == kWalkCausal) {
+          const int32_t t = (int32_t)(r * walk.recip >> 16);
+          *tok = tile0 + t;
+          *sub = (int32_t)r - t * walk.pack;
+          return t < walk.toks && *tok < g.q1;
+        }
+        return false;
+      };
+      if constexpr (kWalk == kWalkCausal) {
+        int32_t sub;
+        valid = packed(row_in_tile, &row, &sub);
+        head += sub;
+      }
       if (g.part >= 0) {
         // A piece of a unit split along the keys: unnormalised O row, its
         // reference max (log2 units) and sum, for the merge pass.
         // (the partial buffer is a device allocation: its 512-byte rows are 32-byte aligned)
         // (dense: slots of kUnitRows rows; other walks: part is the segment's first partial row)
-        const size_t slot = (kWalk == kWalkDoc ? (size_t)g.part * kUnitRows : (size_t)g.part) + local;
+        size_t slot = (kWalk == kWalkDoc ? (size_t)g.part * kUnitRows : (size_t)g.part) + local;
+        if constexpr (kWalk == kWalkCausal) slot = (size_t)g.part + (head - g.head) * (g.q1 - g.q0) + (row - g.q0);
         if constexpr (!kFp8 && !kPair) {
           // bf16: each 32-column chunk of the warp's 32 rows goes through its
           // rows of the unit's Q slot (free: the slot is released only after
@@ -1706,8 +1772,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                            : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                            : "r"(stage + r * 128u + ((q ^ (r & 7u)) << 4))
                            : "memory");
-              if (row_first + (int32_t)r < g.q1)
+              if constexpr (kWalk == kWalkCausal) {
+                int32_t tok, sub;
+                if (packed(lane_base + r, &tok, &sub))
+                  *reinterpret_cast<uint4*>(a.part_o + ((size_t)g.part + sub * (g.q1 - g.q0) + (tok - g.q0)) * kHeadDim +
+                                            c * 32 + 4 * q) = v;
+              } else if (row_first + (int32_t)r < g.q1) {
                 *reinterpret_cast<uint4*>(a.part_o + (slot0 + r) * kHeadDim + c * 32 + 4 * q) = v;
+              }
             }
             __syncwarp();
           }
@@ -1766,7 +1838,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) dev::mbar_arrive(bars.o_staged(q_slot));  // the store thread sends them
       } else {
-        __nv_bfloat16* dst = og + (int64_t)row * a.o_stride + g.head * kHeadDim;
+        __nv_bfloat16* dst = og + (int64_t)row * a.o_stride + head * kHeadDim;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t ov[32];
@@ -1794,7 +1866,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (valid && a.lse != nullptr)
-        a.lse[(int64_t)g.head * a.S + row] = (m_used + __log2f(l)) * 0.6931471805599453f;
+        a.lse[(int64_t)head * a.S + row] = (m_used + __log2f(l)) * 0.6931471805599453f;
     }
   }
 
@@ -2046,6 +2118,29 @@ bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType type, uint32
   return true;
 }
 
+// 3D tensor map of bf16 rows [outer, heads, 128], 128-byte swizzle: boxes of 64
+// dims of box_heads heads of box_rows rows.
+bool make_map_heads(CUtensorMap* m, const void* base, uint64_t heads, uint64_t outer, uint64_t row_bytes, uint32_t box_heads,
+                    uint32_t box_rows, std::string* why) {
+  auto fn = encode_fn();
+  if (fn == nullptr) {
+    if (why) *why = "cuTensorMapEncodeTiled is unavailable";
+    return false;
+  }
+  cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)heads, (cuuint64_t)outer};
+  cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)row_bytes};
+  cuuint32_t box[3] = {64, box_heads, box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    if (why) *why = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string((int)r);
+    return false;
+  }
+  return true;
+}
+
 template <bool kFp8, int kWalk, bool kPair = false>
 cudaError_t set_smem_attr() {
   static SmemAttr attr;
@@ -2192,6 +2287,26 @@ cudaError_t launch_forward_list(const ForwardArgs& a, const WalkArgs& w, cudaStr
   const Walk<kWalkList> walk{w.block_idx, w.block_cnt, w.n_q_blocks, w.max_blocks};
   return w.pair ? launch_walk<kWalkList, true>(m, a, w, walk, stream, why)
                 : launch_walk<kWalkList, false>(m, a, w, walk, stream, why);
+}
+
+cudaError_t launch_forward_causal(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why) {
+  Walk<kWalkCausal> walk;
+  walk.pack = w.pack;
+  walk.toks = kTileRows / w.pack;
+  walk.recip = (65536u + (uint32_t)w.pack - 1) / (uint32_t)w.pack;
+  walk.group = a.H / w.kv_heads;
+  ForwardMaps m;
+  const uint64_t S = (uint64_t)a.S, kv_width = (uint64_t)w.kv_heads * kHeadDim, kv_row = (uint64_t)w.kv_stride * 2;
+  if (!make_map_heads(&m.q, a.q, (uint64_t)a.H, S, (uint64_t)a.qkv_stride * 2, (uint32_t)walk.pack, (uint32_t)walk.toks, why) ||
+      !make_map(&m.k, a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kv_width, S, kv_row, kTileRows / 2, why) ||
+      !make_map(&m.v, a.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kv_width, S, kv_row, kTileRows, why))
+    return cudaErrorInvalidValue;
+  std::memset(&m.o, 0, sizeof(m.o));
+  // (O tiles go out by TMA where a warp's 32 rows are whole tokens)
+  m.o_tma = 32 % walk.pack == 0 && make_map_heads(&m.o, a.o, (uint64_t)a.H, S, (uint64_t)a.o_stride * 2, (uint32_t)walk.pack,
+                                                  32u / (uint32_t)walk.pack, nullptr);
+  return w.pair ? launch_walk<kWalkCausal, true>(m, a, w, walk, stream, why)
+                : launch_walk<kWalkCausal, false>(m, a, w, walk, stream, why);
 }
 
 cudaError_t launch_forward_prefix(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why) {

@@ -135,6 +135,7 @@ void free_plan_device(Plan* p) {
   p->d_err = nullptr;
   free_walk(&p->sparse.walk);
   free_walk(&p->prefix.walk);
+  free_walk(&p->causal.walk);
   if (p->sparse.d_groups) cudaFree(p->sparse.d_groups);
   if (p->sparse.d_q_sum) cudaFree(p->sparse.d_q_sum);
   if (p->sparse.d_k_mean) cudaFree(p->sparse.d_k_mean);
@@ -241,6 +242,11 @@ h3attn_status check_list_sizes(int32_t q_block, int32_t max_blocks) {
   if (q_block != 256 && q_block != 512) return fail(H3ATTN_EINVAL, "q_block must be 256 or 512 (got %d)", q_block);
   if (max_blocks < 1 || max_blocks > (1 << 20))
     return fail(H3ATTN_EINVAL, "max_blocks must be in [1, 2^20] (got %d)", max_blocks);
+  return H3ATTN_OK;
+}
+h3attn_status check_kv_heads(int32_t num_heads, int32_t num_kv_heads) {
+  if (num_kv_heads < 1 || num_heads % num_kv_heads)
+    return fail(H3ATTN_EINVAL, "num_kv_heads must be a divisor of num_heads = %d (got %d)", num_heads, num_kv_heads);
   return H3ATTN_OK;
 }
 h3attn_status check_prefix_len(int32_t prefix_len) {
@@ -906,12 +912,14 @@ h3attn_status h3attn_walk_list_host(int32_t kind, const int32_t* cu_seqlens, int
   if (!cu_seqlens || !n_units || !n_pairs_used || !n_joins || !n_own || !n_part_rows)
     return fail(H3ATTN_EINVAL, "NULL cu_seqlens or output count");
   if (h3attn_status s = check_layout(cu_seqlens, n_docs, num_heads, n_pairs)) return s;
-  if (kind != 0 && kind != 1) return fail(H3ATTN_EINVAL, "kind must be 0 or 1 (got %d)", kind);
-  if (h3attn_status s = kind == 0 ? check_list_sizes(p0, p1) : check_prefix_len(p0)) return s;
+  if (kind < 0 || kind > 2) return fail(H3ATTN_EINVAL, "kind must be 0, 1 or 2 (got %d)", kind);
+  if (h3attn_status s = kind == 0 ? check_list_sizes(p0, p1) : kind == 1 ? check_prefix_len(p0) : check_kv_heads(num_heads, p0))
+    return s;
   try {
     WalkPlan w;
-    const std::string why = kind == 0 ? build_list_walk(cu_seqlens, n_docs, num_heads, p0, p1, n_pairs, w)
-                                      : build_prefix_walk(cu_seqlens, n_docs, num_heads, p0, n_pairs, w);
+    const std::string why = kind == 0   ? build_list_walk(cu_seqlens, n_docs, num_heads, p0, p1, n_pairs, w)
+                            : kind == 1 ? build_prefix_walk(cu_seqlens, n_docs, num_heads, p0, n_pairs, w)
+                                        : build_causal_walk(cu_seqlens, n_docs, num_heads, p0, n_pairs, w);
     if (!why.empty()) return fail(H3ATTN_EINVAL, "%s", why.c_str());
     // pair by pair (of two streams, the first one's segments before the second's)
     std::vector<WalkUnit> segs;
@@ -1208,6 +1216,85 @@ h3attn_status h3attn_cache_move(const h3attn_cache* cache, const int32_t* src, c
                         cache->token_stride, cache->head_stride};
   e = launch_cache_move(a, cache->num_kv_heads, static_cast<cudaStream_t>(cuda_stream));
   return e == cudaSuccess ? H3ATTN_OK : cuda_fail(e, "cache move launch");
+}
+
+// ------------------------------------------------------ causal attention ----
+
+h3attn_status h3attn_plan_set_causal(h3attn_plan_t plan, int32_t num_kv_heads, void* cuda_stream) {
+  clear_error();
+  if (h3attn_status s = check_plan(plan)) return s;
+  if (h3attn_status s = check_kv_heads(plan->num_heads, num_kv_heads)) return s;
+  CausalPlan& cp = plan->causal;
+  if (cp.walk.set) return fail(H3ATTN_EINVAL, "the plan's causal list is already set");
+  DeviceGuard g;
+  cudaError_t e = g.enter(plan->device);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+  try {
+    cp.walk = WalkPlan();
+    const std::string why = build_causal_walk(plan->cu_host.data(), plan->n_docs, plan->num_heads, num_kv_heads,
+                                              forward_slots(plan->device, plan->num_sms), cp.walk);
+    if (!why.empty()) return fail(H3ATTN_EINVAL, "%s", why.c_str());
+    cp.kv_heads = num_kv_heads;
+  } catch (const std::exception&) {
+    return fail(H3ATTN_ENOMEM, "host allocation failed while building the causal list");
+  }
+  return attach_walk(&cp.walk, "causal", cuda_stream, [](cudaStream_t) { return cudaSuccess; });
+}
+
+namespace {
+
+// Checks of q, o, softmax_scale and lse_out where k and v have heads of their own.
+h3attn_status check_grouped_io(const Plan* plan, const void* q, int64_t q_row_stride, const void* o, int64_t o_row_stride,
+                               float softmax_scale, const float* lse_out) {
+  const int64_t S = plan->S;
+  const Rows rq{"q", q, q_row_stride, plan->num_heads}, ro{"o", o, o_row_stride, plan->num_heads};
+  if (h3attn_status s = check_rows(rq, S)) return s;
+  if (h3attn_status s = check_rows(ro, S)) return s;
+  if (lse_out && !aligned4(lse_out)) return fail(H3ATTN_EINVAL, "lse_out must be 4-byte aligned");
+  if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f))
+    return fail(H3ATTN_EINVAL, "softmax_scale must be finite and > 0");
+  if (rows_overlap(ro, rq, S)) return fail(H3ATTN_EINVAL, "o overlaps q");
+  if (lse_out) {
+    const uintptr_t n = (uintptr_t)S * plan->num_heads * 4;
+    if (ranges_overlap(lse_out, n, o, ro.bytes(S))) return fail(H3ATTN_EINVAL, "lse_out overlaps o");
+    if (ranges_overlap(lse_out, n, q, rq.bytes(S))) return fail(H3ATTN_EINVAL, "lse_out overlaps q");
+  }
+  return H3ATTN_OK;
+}
+
+}  // namespace
+
+h3attn_status h3attn_forward_causal(h3attn_plan_t plan, const void* q, int64_t q_row_stride, const void* k, const void* v,
+                                    int64_t kv_row_stride, void* o, int64_t o_row_stride, float softmax_scale,
+                                    float* lse_out, void* cuda_stream) {
+  clear_error();
+  if (h3attn_status s = check_plan(plan)) return s;
+  const CausalPlan& cp = plan->causal;
+  if (!cp.walk.set) return fail(H3ATTN_EINVAL, "h3attn_plan_set_causal has not been called on this plan");
+  if (h3attn_status s = check_grouped_io(plan, q, q_row_stride, o, o_row_stride, softmax_scale, lse_out)) return s;
+  const int64_t S = plan->S;
+  const Rows ro{"o", o, o_row_stride, plan->num_heads};
+  for (const Rows& r : {Rows{"k", k, kv_row_stride, cp.kv_heads}, Rows{"v", v, kv_row_stride, cp.kv_heads}}) {
+    if (h3attn_status s = check_rows(r, S)) return s;
+    if (rows_overlap(ro, r, S)) return fail(H3ATTN_EINVAL, "o overlaps %s", r.name);
+    if (lse_out && ranges_overlap(lse_out, (uintptr_t)S * plan->num_heads * 4, r.p, r.bytes(S)))
+      return fail(H3ATTN_EINVAL, "lse_out overlaps %s", r.name);
+  }
+  DeviceGuard g;
+  cudaError_t e = g.enter(plan->device);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+  const ForwardArgs a = walk_forward_args(plan, cp.walk, q, k, v, q_row_stride, o, o_row_stride, softmax_scale, lse_out);
+  WalkArgs w = walk_args(cp.walk);
+  w.kv_heads = cp.kv_heads;
+  w.kv_stride = kv_row_stride;
+  w.pack = causal_pack(plan->num_heads / cp.kv_heads);
+  std::string why;
+  e = launch_forward_causal(a, w, static_cast<cudaStream_t>(cuda_stream), &why);
+  if (e != cudaSuccess) {
+    if (!why.empty()) return fail(H3ATTN_ECUDA, "causal forward: %s", why.c_str());
+    return cuda_fail(e, "causal forward launch");
+  }
+  return H3ATTN_OK;
 }
 
 h3attn_status h3attn_get_device_error(h3attn_plan_t plan, void* cuda_stream) {

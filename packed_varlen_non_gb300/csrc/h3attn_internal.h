@@ -95,6 +95,8 @@ void build_segments(const std::vector<WorkUnit>& units, int grid, std::vector<Wo
 //                has kv_end = -n < 0: n own tiles, entries [kv_begin, kv_begin +
 //                n) of the walk's table, follow the prefix; its a lies in the
 //                prefix.
+//   causal walk: key tiles [a, b) of the document; the rows are tokens, of `pack`
+//                query heads from `head` on
 // part < 0: the segment writes the output; part >= 0: it writes unnormalised
 // rows from row `part` of the partial buffers on, for the join pass.
 struct WalkUnit {
@@ -177,6 +179,17 @@ std::string build_list_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads
 std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads, int32_t prefix_len, int grid,
                               WalkPlan& w);
 
+// Causal walk: query heads that share a segment, for `group` query heads of a key
+// head: the largest divisor up to 16, so that a tile's 128 rows hold whole tokens and
+// few stay empty (none for powers of two, 2 of 128 for six or seven heads).
+inline int32_t causal_pack(int32_t group) {
+  for (int32_t p = 16; p > 1; --p)
+    if (group % p == 0) return p;
+  return 1;
+}
+std::string build_causal_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads, int32_t num_kv_heads, int grid,
+                              WalkPlan& w);
+
 // Up to kSelectWarps query blocks of one document, scored by one thread block.
 struct SelectGroup {
   int32_t q0, n;          // query blocks [q0, q0 + n)
@@ -209,6 +222,11 @@ struct SparsePlan {
 struct PrefixPlan {
   WalkPlan walk;
   int32_t len = 0;
+};
+
+struct CausalPlan {
+  WalkPlan walk;
+  int32_t kv_heads = 0;
 };
 
 // Placement core shared by the lists (plan.cpp): segment i, in list order,
@@ -291,6 +309,7 @@ struct Plan {
 
   SparsePlan sparse;                 // h3attn_plan_set_sparse
   PrefixPlan prefix;                 // h3attn_plan_set_prefix
+  CausalPlan causal;                 // h3attn_plan_set_causal
 };
 
 // Host-side plan construction (plan.cpp); returns an empty string or an error.
@@ -404,6 +423,9 @@ struct WalkArgs {
   int64_t prefix_stride;
   int32_t prefix_len;
   const OwnTile* own;
+  // causal walk
+  int32_t kv_heads, pack;
+  int64_t kv_stride;
 };
 struct RowsArgs {
   const __nv_bfloat16* q;
@@ -420,6 +442,8 @@ cudaError_t launch_attn_rows(const RowsArgs& a, int heads, cudaStream_t stream);
 
 cudaError_t launch_forward_list(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why);
 cudaError_t launch_forward_prefix(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why);
+
+cudaError_t launch_forward_causal(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why);
 
 // Block scores and selection (block_select.cu).
 struct SelectArgs {

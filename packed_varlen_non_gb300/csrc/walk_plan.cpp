@@ -25,8 +25,9 @@ struct Item {
   bool direct;        // writes the output itself unless it is split
   int32_t pieces = 1;
   int32_t part = -1;  // first partial row of piece 0
+  int32_t pack = 1;   // causal walk: query heads of its rows
   bool partial() const { return !direct || pieces > 1; }
-  int32_t rows() const { return u.q_end - u.q_row0; }
+  int32_t rows() const { return pack * (u.q_end - u.q_row0); }
   // pieces of at most m tiles
   int32_t split(int32_t m) const { return std::max(1, std::min((tiles + m - 1) / m, limit)); }
 };
@@ -44,6 +45,7 @@ struct Join {
   int32_t row0, row1, head;
   int32_t item;
   int32_t key_lo, key_hi;
+  int32_t shift = 0;  // of the head's partial rows in the item's
 };
 
 // Times in hundredths of a microsecond, as measured on GB300 for segments of 1 to
@@ -169,7 +171,10 @@ std::string finish(std::vector<Item>& items, std::vector<Join>& joins, int G, Ma
   w.part_rows = rows;
   for (size_t i = 0; i < items.size(); ++i)
     if (items[i].direct && items[i].pieces > 1)
-      joins.push_back(Join{items[i].u.q_row0, items[i].u.q_end, items[i].u.head, (int32_t)i, 0, 0});
+      for (int32_t h = 0; h < items[i].pack; ++h) {
+        const WalkUnit& u = items[i].u;
+        joins.push_back(Join{u.q_row0, u.q_end, u.head + h, (int32_t)i, 0, 0, h * (u.q_end - u.q_row0)});
+      }
   w.joins.clear();
   w.join_warps = 0;
   for (const Join& j : joins) {
@@ -179,7 +184,7 @@ std::string finish(std::vector<Item>& items, std::vector<Join>& joins, int G, Ma
     r.key_lo = j.key_lo;
     r.key_hi = j.key_hi;
     const Item& it = items[j.item];
-    r.part = it.part;
+    r.part = it.part + j.shift;
     r.rows = it.rows();
     r.n = it.pieces;
     r.q_row0 = it.u.q_row0;
@@ -427,6 +432,62 @@ std::string build_prefix_walk(const int32_t* cu, int32_t n_docs, int32_t num_hea
       return finish(items, joins, (int)std::min<size_t>(items.size() * pieces, size_t(1) << 20), prefix_piece, w);
     }
   }
+  return finish(items, joins, G, prefix_piece, w);
+}
+
+// Keys and values that the causal walk's segments in work share, in bytes: heads
+// are taken in batches of about so much (the L2 holds 129 MB).
+constexpr int64_t kCausalBatch = 48 << 20;
+
+std::string build_causal_walk(const int32_t* cu, int32_t n_docs, int32_t num_heads, int32_t num_kv_heads, int grid,
+                              WalkPlan& w) {
+  if (too_long(cu, n_docs)) return kTooLong;
+  const int G = grid > 0 ? grid : 1;
+  const int32_t pack = causal_pack(num_heads / num_kv_heads), toks = kKeyTile / pack;
+  std::vector<int32_t> order(n_docs);
+  for (int32_t d = 0; d < n_docs; ++d) order[d] = d;
+  std::stable_sort(order.begin(), order.end(),
+                   [cu](int32_t x, int32_t y) { return cu[x + 1] - cu[x] > cu[y + 1] - cu[y]; });
+  // Segments of four query tiles, or of two in two streams a pair, whichever is
+  // estimated to finish first; longest first within a batch of (document, key head)
+  // pairs whose keys and values the L2 holds together.
+  std::vector<Item> items;
+  double best = -1.0;
+  for (int streams = 1; streams <= 2; ++streams) {
+    const int32_t most = 4 / streams * toks;
+    std::vector<Item> list;
+    size_t batch = 0;
+    int64_t bytes = 0;
+    const auto close = [&] {
+      std::stable_sort(list.begin() + batch, list.end(), [](const Item& x, const Item& y) { return x.tiles > y.tiles; });
+      batch = list.size();
+      bytes = 0;
+    };
+    for (int32_t d : order) {
+      const int32_t b = cu[d], e = cu[d + 1];
+      for (int32_t g = 0; g < num_kv_heads; ++g) {
+        for (int32_t h = num_heads / num_kv_heads * g; h < num_heads / num_kv_heads * (g + 1); h += pack)
+          for (int32_t r = b; r < e;) {
+            const int32_t end = (int32_t)std::min<int64_t>((int64_t)r + most, e);
+            const int32_t tiles = (end - b + kKeyTile - 1) / kKeyTile;
+            list.push_back(Item{WalkUnit{r, end, b, e, h, 0, tiles, -1}, tiles, tiles, true});
+            list.back().pack = pack;
+            r = end;
+            if (list.size() >= (size_t(1) << 30)) return "too many work units";
+          }
+        bytes += (int64_t)(e - b) * kHeadDim * 4;
+        if (bytes >= kCausalBatch) close();
+      }
+    }
+    close();
+    const double time = balance(list, G, streams);
+    if (best < 0.0 || time < best) {
+      best = time;
+      w.streams = streams;
+      items.swap(list);
+    }
+  }
+  std::vector<Join> joins;
   return finish(items, joins, G, prefix_piece, w);
 }
 

@@ -96,6 +96,9 @@ _SIGS = {
     "h3attn_walk_list_host": [c_int32, c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_int64,
                               c_void_p, c_void_p, c_int64, c_void_p, c_int64, POINTER(c_int64), POINTER(c_int32),
                               POINTER(c_int64), POINTER(c_int64), POINTER(c_int64)],
+    "h3attn_plan_set_causal": [c_void_p, c_int32, c_void_p],
+    "h3attn_forward_causal": [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_float, c_void_p,
+                              c_void_p],
     "h3attn_rope_init": [POINTER(h3attn_rope_opts), POINTER(h3attn_rope)],
     "h3attn_rotary": [POINTER(h3attn_rope), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int32, c_void_p,
                       c_int64, c_void_p, c_int64, c_int32, c_int32, c_void_p],
@@ -209,7 +212,7 @@ def h3attn_plan_create(docs, num_heads: int, rope_base: float = 10000.0, head_di
 
 
 def h3attn_plan_destroy(plan):
-    for known in (_list_sizes, _plan_rows, _prefix_rows, _plan_device):
+    for known in (_list_sizes, _plan_rows, _prefix_rows, _causal_heads, _plan_device):
         known.pop(plan, None)
     _check(load().h3attn_plan_destroy(plan), "h3attn_plan_destroy")
 
@@ -513,8 +516,8 @@ def h3attn_forward_prefix(plan, q, k, v, k_prefix, v_prefix, o, softmax_scale: f
 
 
 def h3attn_walk_list_host(kind: int, cu_seqlens, num_heads: int, p0: int, p1: int, n_pairs: int):
-    """The work list of the sparse (kind 0: p0 = q_block, p1 = max_blocks) or
-    prefix (kind 1: p0 = prefix_len) forward, built on the host: (units [n, 8],
+    """The work list of the sparse (kind 0: p0 = q_block, p1 = max_blocks), prefix
+    (kind 1: p0 = prefix_len) or causal (kind 2: p0 = num_kv_heads) forward, built on the host: (units [n, 8],
     unit_off, joins [m, 12], own tiles [t, 20], partial rows); the fields are
     those of the C call."""
     cu = np.ascontiguousarray(np.asarray(cu_seqlens, dtype=np.int32))
@@ -530,6 +533,32 @@ def h3attn_walk_list_host(kind: int, cu_seqlens, num_heads: int, p0: int, p1: in
     _check(lib.h3attn_walk_list_host(*head, units.ctypes.data, n.value, off.ctypes.data, joins.ctypes.data, nj.value,
                                      own.ctypes.data, no.value, *tail), "h3attn_walk_list_host")
     return units, off, joins, own, rows.value
+
+
+# ------------------------------------------------------ causal, grouped ----
+
+_causal_heads: dict = {}  # key heads of the plans that have a causal list
+
+
+def h3attn_plan_set_causal(plan, num_kv_heads: int, stream=None):
+    """Adds the causal work list to a plan (once per plan)."""
+    _check(load().h3attn_plan_set_causal(plan, int(num_kv_heads), _plan_stream(plan, stream)), "h3attn_plan_set_causal")
+    _known(plan)
+    _causal_heads[plan] = int(num_kv_heads)
+
+
+def h3attn_forward_causal(plan, q, k, v, o, softmax_scale: float, lse=None, q_row_stride=None, kv_row_stride=None,
+                          o_row_stride=None, stream=None):
+    """Causal attention over the plan's documents with grouped heads: q, o bf16 [S, H, 128]-shaped, k and v
+    [S, num_kv_heads, 128]-shaped, each side with a row stride of its own."""
+    sizes, kv = _plan_rows.get(plan), _causal_heads.get(plan)
+    rows = sizes[0] if sizes else 0
+    q_stride = _rows((q,), q_row_stride, rows, sizes)
+    kv_stride = _rows((k, v), kv_row_stride, rows, (rows, 128 * kv, sizes[2]) if kv else None)
+    o_stride = _rows((o,), o_row_stride, rows, sizes)
+    _check_lse(lse, sizes)
+    _check(load().h3attn_forward_causal(plan, _ptr(q), q_stride, _ptr(k), _ptr(v), kv_stride, _ptr(o), o_stride,
+                                        float(softmax_scale), _ptr(lse), _plan_stream(plan, stream)), "h3attn_forward_causal")
 
 
 # ------------------------------------------------ positions, paged cache ----
