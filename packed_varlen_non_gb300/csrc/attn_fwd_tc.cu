@@ -768,6 +768,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     dev::mbar_init(bars.drain(), 1);
     dev::fence_barrier_init();
   }
+  if constexpr (kWalk == kWalkCausal) {
+    // Rows of a tile that no load fills, where the pack does not divide 128.  (Left as
+    // they were, their scores could be anything, and every new maximum among them made
+    // the warp rescale O: 1,836 against 1,683 us for 20,423 tokens, packs of seven.)
+    if (walk.pack * walk.toks < kTileRows) {
+      for (uint32_t i = threadIdx.x * 16u; i < C::SmemKV; i += kThreads * 16u)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sbase + C::SmemQ + i), "r"(0u) : "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+  }
   if (warp == kTmaWarp && lane == 0) {
     dev::tma_prefetch_desc(&tm_q);
     dev::tma_prefetch_desc(&tm_k);
