@@ -568,6 +568,45 @@ h3attn_status h3attn_forward_causal(h3attn_plan_t plan, const void* q, int64_t q
                                     int64_t kv_row_stride, void* o, int64_t o_row_stride, float softmax_scale,
                                     float* lse_out, void* cuda_stream);
 
+/* ---- Attention for trees of drafted tokens over a cache --------------------------
+ * Answering from a context that grows: documents are the drafted tokens of one
+ * sequence each, 1 to 64 of them (1: the single-token step), whose keys and
+ * values the cache already holds behind the sequence's context.  Lengths, pages
+ * and trees lie on the device, so one plan, and one captured graph, serves the
+ * sequences as they grow.
+ *
+ * h3attn_plan_set_tree adds the workspace to a plan; allocation, capture and
+ * "once per plan" as h3attn_plan_set_sparse.
+ * (Partial rows: 80 MB at most.)  Errors: EINVAL for a NULL plan, num_kv_heads < 1
+ * or not a divisor of num_heads, workspace already set; EUNSUPPORTED for a document
+ * of more than 64 tokens, more than 4,096 documents or 2^31 rows (tokens times heads);
+ * ENOMEM / ECUDA. */
+h3attn_status h3attn_plan_set_tree(h3attn_plan_t plan, int32_t num_kv_heads, void* cuda_stream);
+
+/* Sequence b (document [a, a + T) of the plan) has ctx_lens[b] context tokens,
+ * its n-th row (context, then drafts) in page page_table[b*table_width + n /
+ * page_size].  Draft i sees the context and the drafts j < T whose bit j is set in
+ * tree_mask[a + i] (itself only if bit i is); tree_mask = NULL: the drafts j <= i.
+ *     o_{a+i} = sum softmax(softmax_scale <q_{a+i}, k>) v over those rows, key
+ *               head h / (num_heads / num_kv_heads); 0 where there are none
+ *     lse[h*S + a + i] = ln of the sum of their exponentials; -inf
+ * q bf16 [S,H,128], o, lse_out as h3attn_forward; cache: above, page_size a
+ * multiple of 8; page_table int32 [n_docs, table_width], ctx_lens int32 [n_docs],
+ * tree_mask uint64 [S], all on the device.  Rows of the cache behind a sequence's
+ * last draft reach nothing, whatever they hold; a NaN or an infinity in v of a draft
+ * reaches the whole tree.  |v| may be up to 2^64.  A page outside the cache is read as rows of zeros, a
+ * length outside [0, table_width * page_size - T] as the nearest one inside, and
+ * both are reported by h3attn_get_device_error (EINVAL).
+ * Errors: as h3attn_forward; EINVAL without h3attn_plan_set_tree, for a bad cache
+ * or one of other key heads than the plan's, NULL or misaligned (tree_mask 8, the
+ * others 4 bytes) lists, a table too narrow for the drafts or of 2^31 - 128 rows or more,
+ * and for o or lse_out that overlaps the cache, a list or q; EUNSUPPORTED for
+ * another page_size. */
+h3attn_status h3attn_forward_tree(h3attn_plan_t plan, const void* q, int64_t q_row_stride, const h3attn_cache* cache,
+                                  const int32_t* page_table, int32_t table_width, const int32_t* ctx_lens,
+                                  const uint64_t* tree_mask, void* o, int64_t o_row_stride, float softmax_scale,
+                                  float* lse_out, void* cuda_stream);
+
 /* Allocation-free forward.  The pages have no counterpart: this entry point
  * exists for callers that may not allocate device memory -- code whose device
  * memory is owned by a host framework's pool or arena (an engine plugin, a
@@ -605,7 +644,9 @@ h3attn_status h3attn_forward_noalloc(const int32_t* cu_seqlens, int32_t n_docs, 
  * word.  Returns OK, or ETIMEOUT if a kernel's bounded wait ran out since the
  * last call (the kernel then stopped early and its outputs are invalid), or
  * EINVAL if a list of h3attn_forward_sparse named a key tile outside its
- * document (the tile was skipped) and no wait ran out, or ECUDA if the stream reports an error. */
+ * document (the tile was skipped) or a sequence of h3attn_forward_tree a page
+ * outside the cache or a length outside its table, and no wait ran out, or ECUDA
+ * if the stream reports an error. */
 h3attn_status h3attn_get_device_error(h3attn_plan_t plan, void* cuda_stream);
 
 /* Launches one CTA that waits on a shared-memory barrier nothing arrives on,

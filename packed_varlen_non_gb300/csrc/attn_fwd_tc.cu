@@ -133,12 +133,11 @@
 // frees its TMEM together.
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cudaTypedefs.h>
 
 #include <cstring>
-#include <mutex>
 
 #include "device_common.cuh"
+#include "launch_common.cuh"
 #include "qk_norm.cuh"
 
 namespace h3 {
@@ -2092,20 +2091,6 @@ __global__ void __launch_bounds__(32 * kJoinRows, 4) attn_join_kernel(JoinArgs a
   if (lane == 0 && a.lse != nullptr) a.lse[(int64_t)j.head * a.S + row] = (M + __log2f(l)) * 0.6931471805599453f;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
 // 2D tensor map, 128-byte swizzle: inner extent `inner` elements of `esize`
 // bytes (the tile box is 128 bytes wide), `outer` rows `row_bytes` apart.
 bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType type, uint32_t esize, uint64_t inner,
@@ -2155,21 +2140,6 @@ template <bool kFp8, int kWalk, bool kPair = false>
 cudaError_t set_smem_attr() {
   static SmemAttr attr;
   return attr.set(attn_fwd_tc_kernel<kFp8, kWalk, kPair>, (int)Cfg<kFp8, kPair>::SmemAlloc);
-}
-
-// A kernel launched as a programmatic dependent of the forward before it.
-template <class... P, class... A>
-cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <bool kFp8>

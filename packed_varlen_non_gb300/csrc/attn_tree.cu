@@ -1,0 +1,881 @@
+// Attention for trees of drafted tokens (a single token among them) over a paged
+// cache, heads grouped: include/h3attn.h, h3attn_forward_tree.
+//
+// Pages: "h3-spark" model card, "What this config does" (caches that outlive a
+// step).  The mathematics is the online softmax over key tiles: per query row a
+// running reference m and sum l, p = 2^(s - m), O += P V, o = O / l.
+//
+// What bounds it: reading the cache.  A sequence's T drafts and the G query heads of
+// a key head are G T rows over the same keys, 512 flops a row for 512 bytes of K and
+// V; up to about 256 rows the tensor cores keep up with HBM.  So the rows of a key head
+// fill the 128 lanes of a query tile (packed (token, head) as the causal walk does),
+// one or two such tiles share a pass over the keys, and the work is cut by keys, not
+// by rows:
+//   - a step is one 128-key tile of one (sequence, key head, up to two query tiles);
+//     the steps of all sequences, in order, are cut into equal ranges, one per SM.
+//     Lengths are on the device, so each block adds them up itself and finds its
+//     range; no list is built on the host and one captured graph serves growing
+//     sequences.
+//   - a range's pieces of items that other blocks share leave partial rows (m, l, O),
+//     at most two pieces a block; attn_tree_join_kernel combines them in the order of the
+//     keys, so results do not depend on which block ends first.
+// Per block (one an SM), 11 warps:
+//   warps 0..3, 4..7  softmax of stream 0 and 1, a thread a row;
+//   warp 8            issues the MMAs: S_s = Q K^T (128 x 128 fp32 in TMEM), O_s += P V with
+//                     P (bf16) in S's columns;
+//   warp 9            K and V tiles through a ring of five 32 KB slots (160 KB on their way an SM);
+//                     a lane a page box: gcd(page_size, 128) rows each;
+//   warp 10           Q tiles.
+// Two streams hide the chain S -> softmax -> PV: with two query tiles a stream is a
+// query tile; with one, the streams take the key tiles in turn, each with a running
+// maximum and O of its own, and the block joins the two at the piece's end.
+// Rows behind a sequence's last draft: their scores are masked, their V rows are
+// zeroed in shared memory before the PV reads them (0 times a stranger's NaN is not 0).
+// Every wait is bounded, as in the forward (attn_fwd_tc.cu).
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <cstring>
+
+#include "device_common.cuh"
+#include "launch_common.cuh"
+
+namespace h3 {
+
+namespace {
+
+constexpr int kThreads = 352;
+constexpr int kMmaWarp = 8, kKvWarp = 9, kQWarp = 10;
+constexpr int kRows = 128;                          // of a query tile, and of a key tile
+constexpr int kSlots = 5;
+constexpr uint32_t kTileBytes = 128 * 256;          // two halves of 64 dims, 128-byte rows
+constexpr uint32_t kHalfBytes = kTileBytes / 2;
+constexpr uint32_t kSmemQ = 0;
+constexpr uint32_t kSmemKV = 2 * kTileBytes;
+constexpr uint32_t kSmemBar = kSmemKV + kSlots * kTileBytes;
+constexpr int kNumBars = 4 + 2 * kSlots + 6 + 2;
+constexpr uint32_t kSmemMl = kSmemBar + kNumBars * 8;   // float2 [2][128]
+constexpr uint32_t kSmemMisc = kSmemMl + 2 * 128 * 8;
+constexpr uint32_t kSlack = 512;                        // the base is 1 KB aligned (declared so; checked in the kernel)
+constexpr size_t kSmemAlloc = kSmemMisc + 64 + kSlack;
+static_assert(kSmemAlloc <= 227 * 1024, "shared memory per CTA");
+static_assert(kSmemMl % 16 == 0, "alignment");
+constexpr uint32_t kTmemCols = 512;                 // S0 S1 O0 O1, 128 columns each
+constexpr uint64_t kTimeoutNs = 2000000000ull;      // 2 s
+constexpr float kRescale = 32.0f;                   // log2 units (see attn_fwd_tc.cu)
+constexpr float kLowest = -3.402823466e38f;
+
+// kind::f16: fp32 accumulator, bf16 A and B, M = 128, N = 128
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+constexpr uint32_t kIdescPV = kIdesc | (1u << 16);  // B (V) MN-major
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
+}
+
+struct Bars {
+  uint32_t base;
+  __device__ uint32_t q_full(int i) const { return base + 8 * i; }
+  __device__ uint32_t q_empty(int i) const { return base + 8 * (2 + i); }
+  __device__ uint32_t full(int i) const { return base + 8 * (4 + i); }
+  __device__ uint32_t empty(int i) const { return base + 8 * (4 + kSlots + i); }
+  __device__ uint32_t s_ready(int s) const { return base + 8 * (4 + 2 * kSlots + s); }
+  __device__ uint32_t p_ready(int s) const { return base + 8 * (6 + 2 * kSlots + s); }
+  __device__ uint32_t pv_done(int s) const { return base + 8 * (8 + 2 * kSlots + s); }
+  __device__ uint32_t drain() const { return base + 8 * (10 + 2 * kSlots); }
+  __device__ uint32_t joined() const { return base + 8 * (11 + 2 * kSlots); }  // both streams' softmax warps
+};
+
+// S (TMEM) = Q * K^T, 8 MMAs of 16 dims, issued by one elected lane of the warp.
+__device__ __forceinline__ void issue_qk(uint32_t d_tmem, uint32_t q_smem, uint32_t k_smem) {
+  const uint32_t qa = desc_lo(q_smem, 16), kb = desc_lo(k_smem, 16);
+#define H3_QK(off, pred)                                                                 \
+  "add.u32 x, %1, " off ";\n\tadd.u32 y, %2, " off ";\n\tmov.b64 a, {x, %3};\n\tmov.b64 b, {y, %3};\n\t" \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, " pred ";\n\t"
+  asm volatile(
+      "{\n\t.reg .pred p0, p1, e;\n\telect.sync _|e, 0xffffffff;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t"
+      "setp.ne.u32 p0, %4, %4;\n\tsetp.eq.u32 p1, %4, %4;\n\t"
+      H3_QK("0", "p0") H3_QK("2", "p1") H3_QK("4", "p1") H3_QK("6", "p1")
+      H3_QK("1024", "p1") H3_QK("1026", "p1") H3_QK("1028", "p1") H3_QK("1030", "p1")
+      "}" ::"r"(d_tmem), "r"(qa), "r"(kb), "r"(kDescHi), "r"(0u), "r"(kIdesc)
+      : "memory");
+#undef H3_QK
+}
+
+// O (TMEM) (+)= P (TMEM, bf16 pairs) * V, 8 MMAs of 16 keys (2 KB of each half apart).
+__device__ __forceinline__ void issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint32_t v_smem, bool acc) {
+  const uint32_t vb = desc_lo(v_smem, kHalfBytes);
+#define H3_PV(p, v, pred)                                                      \
+  "add.u32 t, %1, " p ";\n\tadd.u32 y, %2, " v ";\n\tmov.b64 b, {y, %3};\n\t" \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %5, " pred ";\n\t"
+  asm volatile(
+      "{\n\t.reg .pred p0, p1, e;\n\telect.sync _|e, 0xffffffff;\n\t.reg .b64 b;\n\t.reg .b32 t, y;\n\t"
+      "setp.ne.u32 p0, %4, 0;\n\tsetp.eq.u32 p1, %4, %4;\n\t"
+      H3_PV("0", "0", "p0") H3_PV("8", "128", "p1") H3_PV("16", "256", "p1") H3_PV("24", "384", "p1")
+      H3_PV("32", "512", "p1") H3_PV("40", "640", "p1") H3_PV("48", "768", "p1") H3_PV("56", "896", "p1")
+      "}" ::"r"(d_tmem), "r"(p_tmem), "r"(vb), "r"(kDescHi), "r"(acc ? 1u : 0u), "r"(kIdescPV)
+      : "memory");
+#undef H3_PV
+}
+
+__device__ __forceinline__ void commit_elect(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+
+// A sequence: its drafts [row0, row0 + T), context, key tiles, and items (key head, unit of up to two query tiles).
+struct Doc {
+  int32_t row0, T, ctx, tiles, qtiles, units;
+  bool bad;
+};
+__device__ __forceinline__ Doc doc_of(const TreeArgs& a, int b) {
+  Doc d;
+  d.row0 = __ldg(a.cu + b);
+  d.T = __ldg(a.cu + b + 1) - d.row0;
+  const int32_t given = __ldg(a.ctx_lens + b);
+  const int64_t most = (int64_t)a.table_width * a.page_size - d.T;  // (not negative, and below 2^31: checked by the caller)
+  d.ctx = max(0, (int32_t)min((int64_t)given, most));
+  d.bad = d.ctx != given;
+  d.tiles = (int32_t)(((int64_t)d.ctx + d.T + kRows - 1) / kRows);
+  d.qtiles = a.packs * ((d.T + a.toks - 1) / a.toks);
+  d.units = (d.qtiles + 1) / 2;
+  return d;
+}
+
+// A block's share of one item: key tiles [lo, hi).
+struct Piece {
+  int32_t b, kvh, lo, hi;
+  int32_t qt, n_qt;    // its first query tile, and how many (1 or 2)
+  bool whole;
+  bool first;          // of the block's pieces
+  int32_t at;          // steps of the block before it
+};
+// Walks a block's range piece by piece; every role runs its own.
+struct Walk {
+  int32_t b, item, lo;
+  int32_t left, at;
+  bool first;
+  Doc d;
+  __device__ void begin(const TreeArgs& a, int32_t b_, int64_t off, int32_t steps) {
+    b = b_;
+    left = steps;
+    at = 0;
+    first = true;
+    d = doc_of(a, b);
+    item = (int32_t)(off / d.tiles);
+    lo = (int32_t)(off - (int64_t)item * d.tiles);
+  }
+  // the next piece; false at the end
+  __device__ bool next(const TreeArgs& a, Piece* p) {
+    if (left <= 0) return false;
+    if (item == a.kv_heads * d.units) {
+      item = 0;
+      d = doc_of(a, ++b);
+    }
+    p->b = b;
+    p->kvh = item / d.units;
+    p->qt = 2 * (item - p->kvh * d.units);
+    p->n_qt = min(2, d.qtiles - p->qt);
+    p->lo = lo;
+    p->hi = min(d.tiles, lo + left);
+    p->whole = lo == 0 && p->hi == d.tiles;
+    p->first = first;
+    p->at = at;
+    first = false;
+    at += p->hi - lo;
+    left -= p->hi - lo;
+    lo = p->hi;
+    if (lo == d.tiles) {
+      lo = 0;
+      ++item;
+    }
+    return true;
+  }
+};
+
+// Ring entries in the order of their loads: K of the first tile, then K of every
+// tile before V of the one before it.
+__device__ __forceinline__ uint32_t k_entry(int32_t t) { return t == 0 ? 0u : 2u * t - 1; }
+__device__ __forceinline__ uint32_t v_entry(int32_t t, int32_t steps) { return t + 1 < steps ? 2u * t + 2 : 2u * t + 1; }
+
+// A query tile's tokens and first head.
+struct QTile {
+  int32_t tok0, n_tok, head;
+};
+__device__ __forceinline__ QTile q_tile(const TreeArgs& a, const Doc& d, int32_t kvh, int32_t qt) {
+  const int32_t block = qt / a.packs, first = block * a.toks;
+  return QTile{d.row0 + first, min(a.toks, d.T - first), kvh * a.group + (qt - block * a.packs) * a.pack};
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeArgs a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  const uint32_t raw = dev::smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  if (sbase - raw > kSlack) {
+    if (threadIdx.x == 0) atomicExch(a.err, kErrTimeout);  // (outputs are invalid)
+    return;
+  }
+  unsigned char* smem = smem_raw + (sbase - raw);
+  const Bars bars{sbase + kSmemBar};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kSmemMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kSmemMisc + 4);
+  // the block's range: first sequence, offset in its steps, steps
+  volatile int32_t* const range = reinterpret_cast<volatile int32_t*>(smem + kSmemMisc + 8);
+  volatile int64_t* const range_off = reinterpret_cast<volatile int64_t*>(smem + kSmemMisc + 16);
+  const uint32_t warp = dev::warp_id_uniform();
+  const uint32_t lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.launch_dependents;");  // (the join waits for this grid's end)
+  {
+    // every thread a run of sequences: steps before them, and in all
+    int64_t* const sums = reinterpret_cast<int64_t*>(smem + kSmemMl);
+    const int per = (a.n_docs + kThreads - 1) / kThreads;
+    const int b0 = min((int)threadIdx.x * per, a.n_docs), b1 = min(b0 + per, a.n_docs);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Doc d = doc_of(a, b);
+      mine += (int64_t)d.tiles * d.units * a.kv_heads;
+      if (d.bad && blockIdx.x == 0) dev::report_bad_page(a.err);
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if ((int)lane >= o) incl += x;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < (int)warp) before += sums[w];
+      total += sums[w];
+    }
+    const int64_t grid = min((int64_t)gridDim.x, total);
+    const int64_t c = blockIdx.x;
+    const int64_t s0 = c < grid ? total * c / grid : total, s1 = c < grid ? total * (c + 1) / grid : total;
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[a.n_docs] = total;
+    for (int b = b0; b < b1; ++b) {
+      const Doc d = doc_of(a, b);
+      const int64_t n = (int64_t)d.tiles * d.units * a.kv_heads;
+      if (blockIdx.x == 0) a.prefix[b] = before;
+      if (s0 >= before && s0 < before + n) {
+        range[0] = b;
+        range[1] = (int32_t)(s1 - s0);
+        range_off[0] = s0 - before;
+      }
+      before += n;
+    }
+    if (c >= grid) return;  // (the whole block)
+    __syncthreads();
+  }
+  const int32_t steps = range[1];
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < 2; ++i) {
+      dev::mbar_init(bars.q_full(i), 1);
+      dev::mbar_init(bars.q_empty(i), 1);
+      dev::mbar_init(bars.s_ready(i), 1);
+      dev::mbar_init(bars.p_ready(i), 4);
+      dev::mbar_init(bars.pv_done(i), 1);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      dev::mbar_init(bars.full(i), 1);
+      dev::mbar_init(bars.empty(i), 1);
+    }
+    dev::mbar_init(bars.drain(), 1);
+    dev::mbar_init(bars.joined(), 8);
+    dev::fence_barrier_init();
+  }
+  if (a.pack * a.toks < kRows) {
+    // rows of a query tile that no load fills (their scores must not be anything: see attn_fwd_tc.cu)
+    for (uint32_t i = threadIdx.x * 16u; i < 2 * kTileBytes; i += kThreads * 16u)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sbase + kSmemQ + i), "r"(0u) : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    dev::tmem_alloc(dev::smem_u32(tmem_slot), kTmemCols);
+    dev::tmem_relinquish();
+  }
+  dev::tc_fence_before();
+  __syncthreads();
+  dev::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Walk walk;
+  walk.begin(a, range[0], range_off[0], steps);
+  Piece p;
+
+  if (warp == kKvWarp) {
+    // ---------------------------------------------------- K and V tiles ----
+    // (tiles that other units read too should stay in L2)
+    const uint64_t pol_once = dev::policy_evict_first(), pol_shared = dev::policy_evict_last();
+    const int n_box = kRows / a.box;  // boxes of a tile, a lane each
+    uint32_t loaded = 0;
+    bool ok = true;
+    // a tile's box of this lane: whether it holds rows, its page and row; the tile's key head and bytes
+    struct Tile {
+      bool in;
+      int32_t page, row, kvh;
+      uint32_t bytes;
+      uint64_t pol;
+    };
+    const auto load = [&](const CUtensorMap* tm, const Tile& t) {
+      const uint32_t slot = loaded % kSlots;
+      bool good = true;
+      if (lane == 0) good = dev::mbar_wait(bars.empty(slot), ((loaded / kSlots) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
+      ok = __shfl_sync(0xffffffffu, good, 0);
+      if (!ok) return;
+      if (lane == 0) dev::mbar_arrive_expect_tx(bars.full(slot), t.bytes);
+      __syncwarp();
+      if (t.in) {
+        const uint32_t dst = sbase + kSmemKV + slot * kTileBytes + lane * (uint32_t)a.box * 128u;
+        const int32_t c1 = a.heads_first ? t.kvh : t.row, c2 = a.heads_first ? t.row : t.kvh;
+        dev::tma_load_4d(dst, tm, bars.full(slot), 0, c1, c2, t.page, t.pol);
+        dev::tma_load_4d(dst + kHalfBytes, tm, bars.full(slot), 64, c1, c2, t.page, t.pol);
+      }
+      ++loaded;
+    };
+    Tile prev{};
+    bool any = false;
+    while (ok && walk.next(a, &p)) {
+      const int32_t total = walk.d.ctx + walk.d.T;
+      const int32_t* table = a.page_table + (int64_t)p.b * a.table_width;
+      const auto page_of = [&](int32_t t) {
+        const uint32_t key = (uint32_t)t * kRows + lane * (uint32_t)a.box;
+        return (int)lane < n_box && t < p.hi && key < (uint32_t)total ? __ldg(table + key / (uint32_t)a.page_size) : 0;
+      };
+      int32_t page = page_of(p.lo);
+      for (int32_t t = p.lo; ok && t < p.hi; ++t) {
+        const uint32_t key = (uint32_t)t * kRows + lane * (uint32_t)a.box;
+        Tile cur;
+        cur.in = (int)lane < n_box && key < (uint32_t)total;
+        cur.page = page;
+        page = page_of(t + 1);  // a tile ahead of its use
+        cur.row = (int32_t)(key % (uint32_t)a.page_size);
+        cur.kvh = p.kvh;
+        cur.pol = walk.d.units > 1 ? pol_shared : pol_once;
+        const int32_t boxes = min(n_box, (total - t * kRows + a.box - 1) / a.box);
+        cur.bytes = (uint32_t)boxes * (uint32_t)a.box * 256u;
+        if (cur.in && (uint32_t)cur.page >= (uint32_t)a.n_pages) {
+          dev::report_bad_page(a.err);
+          cur.page = a.n_pages;  // outside the tensor map: zeros
+        }
+        load(&tm_k, cur);
+        if (ok && any) load(&tm_v, prev);
+        prev = cur;
+        any = true;
+      }
+    }
+    if (ok && any) load(&tm_v, prev);
+    if (!ok && lane == 0) {  // drain: wait (bounded) for the copies on their way
+      for (uint32_t r = 1; r <= (uint32_t)kSlots && r <= loaded; ++r)
+        dev::mbar_wait_bounded(bars.full((loaded - r) % kSlots), ((loaded - r) / kSlots) & 1, nullptr, nullptr, kTimeoutNs);
+    }
+    __syncwarp();
+  } else if (warp == kQWarp) {
+    // ----------------------------------------------------------- Q tiles ----
+    if (lane == 0) {
+      const uint64_t pol = dev::policy_evict_first();
+      uint32_t n = 0;
+      bool ok = true;
+      while (ok && walk.next(a, &p)) {
+        for (int i = 0; ok && i < p.n_qt; ++i) {
+          ok = dev::mbar_wait(bars.q_empty(n & 1), ((n >> 1) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
+          if (!ok) break;
+          const QTile q = q_tile(a, walk.d, p.kvh, p.qt + i);
+          const uint32_t dst = sbase + kSmemQ + (n & 1) * kTileBytes, bar = bars.q_full(n & 1);
+          dev::mbar_arrive_expect_tx(bar, 256u * (uint32_t)(a.pack * a.toks));
+          dev::tma_load_3d(dst, &tm_q, bar, 0, q.head, q.tok0, pol);
+          dev::tma_load_3d(dst + kHalfBytes, &tm_q, bar, 64, q.head, q.tok0, pol);
+          ++n;
+        }
+      }
+      if (!ok)
+        for (uint32_t r = 1; r <= 2 && r <= n; ++r)
+          dev::mbar_wait_bounded(bars.q_full((n - r) & 1), ((n - r) >> 1) & 1, nullptr, nullptr, kTimeoutNs);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // -------------------------------------------------------- MMA issuer ----
+    // (the whole warp; one lane polls, one elected lane issues)
+    uint32_t n_q = 0, p_it[2] = {0, 0};
+    bool ok = true, issued = false;
+    const auto wait = [&](uint32_t bar, uint32_t parity) {
+      bool good = true;
+      if (lane == 0) good = dev::mbar_wait(bar, parity, abort_flag, a.err, kTimeoutNs);
+      ok = ok && __shfl_sync(0xffffffffu, good, 0);
+      dev::tc_fence_after();
+      return ok;
+    };
+    const auto landed = [&](uint32_t entry) { return wait(bars.full(entry % kSlots), (entry / kSlots) & 1); };
+    const auto slot_of = [&](uint32_t entry) { return sbase + kSmemKV + (entry % kSlots) * kTileBytes; };
+    const auto release = [&](uint32_t entry) { commit_elect(bars.empty(entry % kSlots)); };
+    const auto qk = [&](int s, uint32_t q, uint32_t entry) {
+      issue_qk(tmem + s * 128, sbase + kSmemQ + q * kTileBytes, slot_of(entry));
+      commit_elect(bars.s_ready(s));
+      issued = true;
+    };
+    const auto pv = [&](int s, uint32_t entry, bool acc) { issue_pv(tmem + 256 + s * 128, tmem + s * 128, slot_of(entry), acc); };
+    while (ok && walk.next(a, &p)) {
+      const int32_t n = p.hi - p.lo, t0 = p.at;
+      const uint32_t q0 = n_q & 1, q1 = q0 ^ 1;
+      wait(bars.q_full(q0), (n_q >> 1) & 1);
+      ++n_q;
+      if (p.n_qt == 2) {
+        // stream s: query tile s over every key tile
+        wait(bars.q_full(q1), (n_q >> 1) & 1);
+        ++n_q;
+        if (!landed(k_entry(t0))) break;
+        qk(0, q0, k_entry(t0));
+        qk(1, q1, k_entry(t0));
+        release(k_entry(t0));
+        if (n == 1) {
+          commit_elect(bars.q_empty(q0));
+          commit_elect(bars.q_empty(q1));
+        }
+        for (int32_t j = 0; ok && j < n; ++j) {
+          const uint32_t ve = v_entry(t0 + j, steps), ke = k_entry(t0 + j + 1);
+          const bool more = j + 1 < n;
+          for (int s = 0; s < 2; ++s) {
+            if (!wait(bars.p_ready(s), p_it[s] & 1)) break;
+            ++p_it[s];
+            if (s == 0 && (!landed(ve) || (more && !landed(ke)))) break;
+            pv(s, ve, j > 0);
+            if (more)
+              qk(s, s == 0 ? q0 : q1, ke);
+            else
+              commit_elect(bars.pv_done(s));
+          }
+          if (!ok) break;
+          release(ve);
+          if (more) release(ke);
+          if (j + 2 == n) {
+            commit_elect(bars.q_empty(q0));
+            commit_elect(bars.q_empty(q1));
+          }
+        }
+      } else {
+        // stream s: the one query tile over the key tiles s, s + 2, ...
+        for (int s = 0; s < 2 && s < n; ++s) {
+          if (!landed(k_entry(t0 + s))) break;
+          qk(s, q0, k_entry(t0 + s));
+          release(k_entry(t0 + s));
+        }
+        if (!ok) break;
+        if (n <= 2) commit_elect(bars.q_empty(q0));
+        for (int32_t j = 0; ok && j < n; ++j) {
+          const int s = j & 1;
+          const uint32_t ve = v_entry(t0 + j, steps);
+          if (!wait(bars.p_ready(s), (s == 0 ? p_it[0] : p_it[1]) & 1)) break;
+          if (s == 0)
+            ++p_it[0];
+          else
+            ++p_it[1];
+          if (!landed(ve)) break;
+          pv(s, ve, j >= 2);
+          release(ve);
+          if (j + 2 < n) {
+            const uint32_t ke = k_entry(t0 + j + 2);
+            if (!landed(ke)) break;
+            qk(s, q0, ke);
+            release(ke);
+            if (j + 3 == n) commit_elect(bars.q_empty(q0));
+          } else {
+            commit_elect(bars.pv_done(s));
+          }
+        }
+      }
+    }
+    if (!ok && issued) {
+      // drain: every MMA issued so far must finish before TMEM is freed
+      __syncwarp();
+      commit_elect(bars.drain());
+      dev::mbar_wait_bounded(bars.drain(), 0, nullptr, nullptr, kTimeoutNs);
+    }
+  } else {
+    // ----------------------------------------------------------- softmax ----
+    const int st = warp >> 2;                     // stream
+    const uint32_t row = threadIdx.x & 127;       // TMEM lane, row of the query tile
+    const uint32_t lane_base = (warp & 3) * 32;
+    const uint32_t t_s = tmem + (lane_base << 16) + st * 128;
+    const uint32_t t_o = tmem + (lane_base << 16) + 256;  // O_0; O_1 128 columns on
+    float2* const ml_of = reinterpret_cast<float2*>(smem + kSmemMl);
+    const uint32_t tok_in = row * a.recip >> 16, sub = row - tok_in * (uint32_t)a.pack;
+    uint32_t s_it = 0, done[2] = {0, 0}, joined = 0;
+    bool ok = true;
+    // stream s's last PV of the piece; every warp sees every phase, so that none waits for one that
+    // another has followed
+    const auto finished = [&](int s) {
+      ok = dev::mbar_wait(bars.pv_done(s), (s == 0 ? done[0] : done[1]) & 1, abort_flag, a.err, kTimeoutNs) && ok;
+      if (s == 0)
+        ++done[0];
+      else
+        ++done[1];
+    };
+    while (ok && walk.next(a, &p)) {
+      const bool two = p.n_qt == 2;
+      const Doc& d = walk.d;
+      const QTile q = q_tile(a, d, p.kvh, p.qt + (two ? st : 0));
+      const bool valid = tok_in < (uint32_t)q.n_tok;  // (rows past pack * toks have larger tok_in)
+      const bool busy = (int32_t)(lane_base * a.recip >> 16) < q.n_tok;  // any row of this warp
+      const int32_t n = p.hi - p.lo;
+      // the drafts that this row sees
+      uint64_t word = 0;
+      if (valid) {
+        const int32_t i = q.tok0 + (int32_t)tok_in - d.row0;
+        word = a.tree_mask != nullptr ? __ldg(reinterpret_cast<const unsigned long long*>(a.tree_mask) + d.row0 + i) : ~0ull >> (63 - i);
+        word &= ~0ull >> (64 - d.T);
+      }
+      float m = kLowest, l = 0.f;
+      for (int32_t j = two ? 0 : st; ok && j < n; j += two ? 1 : 2) {
+        const int32_t t = p.lo + j;
+        ok = dev::mbar_wait(bars.s_ready(st), s_it & 1, abort_flag, a.err, kTimeoutNs);
+        ++s_it;
+        __syncwarp();  // lanes leave the wait separately; the TMEM loads are warp-collective
+        dev::tc_fence_after();
+        if (busy) {
+          uint32_t r[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) dev::tmem_ld32(t_s + c * 32, r[c]);
+          dev::tmem_wait_ld();
+          float* sv = reinterpret_cast<float*>(&r[0][0]);
+          const int32_t base = t * kRows - d.ctx;  // draft of the tile's first key (negative: context)
+          if (base + kRows > 0) {
+            uint64_t lo = ~0ull, hi = 0;           // keys that the row sees
+            if (base >= 0) {
+              lo = word >> base;                   // (the last tile begins before the last draft: below 64)
+            } else if (base > -64) {
+              lo = (word << -base) | ((1ull << -base) - 1);
+              hi = word >> (64 + base);
+            } else if (base == -64) {
+              hi = word;
+            } else {
+              hi = (word << (-base - 64)) | ((1ull << (-base - 64)) - 1);
+            }
+            const uint32_t w[4] = {(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (!((w[c >> 5] >> (c & 31)) & 1u)) sv[c] = -INFINITY;
+          }
+          float mx[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mx[i] = fmaxf(sv[i], sv[8 + i]);
+#pragma unroll
+          for (int c = 16; c < 128; c += 16)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mx[i] = dev::max3(mx[i], sv[c + i], sv[c + 8 + i]);
+          const float m_new =
+              dev::max3(dev::max3(mx[0], mx[1], mx[2]), dev::max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * a.scale_log2;
+          float alpha = 1.f;
+          if (m_new > m + kRescale) {
+            alpha = dev::ex2_approx(m - m_new);
+            m = m_new;
+          }
+          const float neg = -m;
+          float rs8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pr[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              float x0, x1;
+              dev::fma2(x0, x1, sv[64 * h + 2 * c], sv[64 * h + 2 * c + 1], a.scale_log2, a.scale_log2, neg, neg);
+              const float p0 = dev::ex2_approx(x0), p1 = dev::ex2_approx(x1);
+              const int ai = 2 * (c & 3);
+              dev::add2(rs8[ai], rs8[ai + 1], rs8[ai], rs8[ai + 1], p0, p1);
+              // bf16, as the operand of the tensor cores: half a step of each weight, the sum keeps fp32
+              pr[c] = dev::pack_bf16x2(p0, p1);
+            }
+            dev::tmem_st32(t_s + 32 * h, pr);
+          }
+          const float rs = ((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7]));
+          l = l * alpha + rs;
+          // (every PV of this stream so far completed before the QK whose S was just read)
+          if (j >= (two ? 1 : 2) && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t ov[16];
+              dev::tmem_ld16(t_o + st * 128 + c * 16, ov);
+              dev::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+              dev::tmem_st16(t_o + st * 128 + c * 16, ov);
+            }
+          }
+          dev::tmem_wait_st();
+        }
+        dev::tc_fence_before();
+        // the tile ends early: zero the rows of V behind it, a quarter a warp (two query
+        // tiles: the first one's warps, whose PV goes first)
+        const int32_t rem = d.ctx + d.T - t * kRows;
+        if (rem < kRows && (!two || st == 0)) {
+          const uint32_t ve = v_entry(p.at + j, steps);
+          ok = dev::mbar_wait(bars.full(ve % kSlots), (ve / kSlots) & 1, abort_flag, a.err, kTimeoutNs) && ok;
+          const uint32_t v = sbase + kSmemKV + (ve % kSlots) * kTileBytes;
+          if (ok)
+            for (uint32_t x = (uint32_t)rem * 128u + threadIdx.x % 128 * 16u; x < kHalfBytes; x += 2048u)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + h * kHalfBytes + x), "r"(0u) : "memory");
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the tensor cores
+        }
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(bars.p_ready(st));
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (!ok) break;
+      if (two) {
+        finished(st);
+      } else {
+        finished(0);
+        if (n > 1) finished(1);
+      }
+      float w0 = 1.f, w1 = 0.f;
+      const bool both = !two && n > 1;
+      if (!two) {
+        // exchange with the other stream's row: o = (w0 O_0 + w1 O_1) / l
+        ml_of[st * 128 + row] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(bars.joined());
+        ok = dev::mbar_wait(bars.joined(), joined & 1, abort_flag, a.err, kTimeoutNs) && ok;
+        ++joined;
+        const float2 x0 = ml_of[row], x1 = ml_of[128 + row];
+        m = fmaxf(x0.x, x1.x);
+        w0 = dev::ex2_approx(x0.x - m);
+        w1 = dev::ex2_approx(x1.x - m);
+        l = w0 * x0.y + w1 * x1.y;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      dev::tc_fence_after();
+      if (busy) {
+        // two query tiles: all dims of the row; one: half of them in each stream's warps
+        const int c0 = two ? 0 : 2 * st, c1 = two ? 4 : 2 * st + 2;
+        const int32_t tok = q.tok0 + (int32_t)tok_in, head = q.head + (int32_t)sub;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t part = (int64_t)(2 * blockIdx.x + (p.first ? 0 : 1)) * a.slot_rows + (two ? st * kRows : 0) + row;
+#pragma unroll 1
+        for (int c = c0; c < c1; ++c) {
+          uint32_t ov[32];
+          dev::tmem_ld32(t_o + (two ? st * 128 : 0) + c * 32, ov);
+          dev::tmem_wait_ld();
+          if (!two) {
+            uint32_t o1[32];
+            if (both) {
+              dev::tmem_ld32(t_o + 128 + c * 32, o1);
+              dev::tmem_wait_ld();
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float x = w0 * __uint_as_float(ov[e]);
+              ov[e] = __float_as_uint(both ? fmaf(w1, __uint_as_float(o1[e]), x) : x);
+            }
+          }
+          if (valid && p.whole) {
+            __nv_bfloat16* const dst = a.o + (int64_t)tok * a.o_stride + (int64_t)head * kHeadDim + c * 32;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                w[x] = dev::pack_bf16x2(__uint_as_float(ov[8 * e + 2 * x]) * inv, __uint_as_float(ov[8 * e + 2 * x + 1]) * inv);
+              *reinterpret_cast<uint4*>(dst + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else if (valid) {
+            float* const dst = a.part_o + part * kHeadDim + c * 32;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dev::st_global_v8(dst + 8 * e, ov[8 * e], ov[8 * e + 1], ov[8 * e + 2], ov[8 * e + 3], ov[8 * e + 4],
+                                ov[8 * e + 5], ov[8 * e + 6], ov[8 * e + 7]);
+          }
+        }
+        if (valid && (two || st == 0)) {
+          if (!p.whole)
+            a.part_ml[part] = make_float2(m, l);
+          else if (a.lse != nullptr)
+            a.lse[(int64_t)head * a.S + tok] = (m + __log2f(l)) * 0.6931471805599453f;
+        }
+      }
+      dev::tc_fence_before();
+      if (two) {
+        finished(st ^ 1);
+        ok = __all_sync(0xffffffffu, ok);
+      } else {
+        // neither stream's next PV may overwrite an O that the other's warps still read
+        // (nor its next row the other's m and l)
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(bars.joined());
+        ok = dev::mbar_wait(bars.joined(), joined & 1, abort_flag, a.err, kTimeoutNs);
+        ++joined;
+        ok = __all_sync(0xffffffffu, ok);
+      }
+    }
+  }
+
+  dev::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    dev::tc_fence_after();
+    dev::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Rows whose item several blocks shared: o = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c -
+// M) l_c over the pieces in the order of their keys.  A warp a row, four dims a lane;
+// the eight warps of a block share out the pieces of rows that have many.
+constexpr int kJoinWarps = 8;
+constexpr int kAtOnce = 8;     // partial rows that a warp has on their way
+constexpr int kAlone = 16;     // pieces that a warp combines by itself
+
+struct Acc {
+  float m, l;
+  float4 o;
+};
+__device__ __forceinline__ Acc nothing() { return Acc{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)}; }
+__device__ __forceinline__ void add(Acc& x, float m, float l, const float4& o) {
+  const float top = fmaxf(x.m, m), ref = top == -INFINITY ? 0.f : top;
+  const float wx = dev::ex2_approx(x.m - ref), w = dev::ex2_approx(m - ref);
+  x.o = make_float4(fmaf(w, o.x, wx * x.o.x), fmaf(w, o.y, wx * x.o.y), fmaf(w, o.z, wx * x.o.z), fmaf(w, o.w, wx * x.o.w));
+  x.l = fmaf(w, l, wx * x.l);
+  x.m = top;
+}
+
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_tree_join_kernel(const __grid_constant__ TreeArgs a) {
+  __shared__ Acc shared[kJoinWarps][32];
+  __shared__ int4 info[kJoinWarps];  // of each warp's row: first block, pieces, row of the partial tile, its first slot
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t id = (int64_t)blockIdx.x * kJoinWarps + warp;
+  const bool real = id < a.S * a.H;
+  const int32_t tok = real ? (int32_t)(id / a.H) : 0, head = real ? (int32_t)(id - (int64_t)tok * a.H) : 0;
+  const int32_t b = __ldg(a.doc_of + tok), row0 = __ldg(a.cu + b), T = __ldg(a.cu + b + 1) - row0;
+  const int32_t kvh = head / a.group, in = head - kvh * a.group, pk = in / a.pack, blk = (tok - row0) / a.toks;
+  const int32_t qt = blk * a.packs + pk;
+  const int32_t units = (a.packs * ((T + a.toks - 1) / a.toks) + 1) / 2;
+  const int32_t row = (qt & 1) * kRows + ((tok - row0) - blk * a.toks) * a.pack + (in - pk * a.pack);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the forward is complete and its writes visible
+  const int64_t total = a.prefix[a.n_docs], first = a.prefix[b], tiles = (a.prefix[b + 1] - first) / ((int64_t)units * a.kv_heads);
+  const int64_t grid = min((int64_t)a.grid, total);
+  const int64_t s0 = first + ((int64_t)kvh * units + qt / 2) * tiles, s1 = s0 + tiles;  // the item's steps
+  // block c has steps [total c / grid, total (c + 1) / grid)
+  const int32_t c0 = (int32_t)(((s0 + 1) * grid - 1) / total), c1 = (int32_t)((s1 * grid - 1) / total);
+  const int32_t n = real && c1 > c0 ? c1 - c0 + 1 : 0;  // (a block's whole items are written by it)
+  // the piece of the first block is its last one unless the item begins there; the others' is their first
+  const int32_t slot0 = 2 * c0 + (total * c0 / grid < s0 ? 1 : 0);
+  if (lane == 0) info[warp] = make_int4(c0, n, row, slot0);
+  __syncthreads();
+  const auto part_row = [&](const int4& x, int32_t i) {
+    return (int64_t)(i == 0 ? x.w : 2 * (x.x + i)) * a.slot_rows + x.z;
+  };
+  const auto run = [&](const int4& x, int32_t i0, int32_t i1, Acc& acc) {
+#pragma unroll 1
+    for (int32_t i = i0; i < i1; i += kAtOnce) {
+      float2 ml[kAtOnce];
+      float4 o[kAtOnce];
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e)
+        if (i + e < i1) {
+          const int64_t r = part_row(x, i + e);
+          ml[e] = a.part_ml[r];
+          o[e] = reinterpret_cast<const float4*>(a.part_o + r * kHeadDim)[lane];
+        }
+#pragma unroll
+      for (int e = 0; e < kAtOnce; ++e)
+        if (i + e < i1) add(acc, ml[e].x, ml[e].y, o[e]);
+    }
+  };
+  const auto finish = [&](const Acc& acc, int64_t row_id) {
+    const int32_t t = (int32_t)(row_id / a.H), h = (int32_t)(row_id - (int64_t)t * a.H);
+    const float inv = acc.l == 0.f ? 0.f : 1.f / acc.l;
+    __nv_bfloat16* const dst = a.o + (int64_t)t * a.o_stride + (int64_t)h * kHeadDim + 4 * lane;
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(dev::pack_bf16x2(acc.o.x * inv, acc.o.y * inv), dev::pack_bf16x2(acc.o.z * inv, acc.o.w * inv));
+    if (lane == 0 && a.lse != nullptr) a.lse[(int64_t)h * a.S + t] = (acc.m + __log2f(acc.l)) * 0.6931471805599453f;
+  };
+  if (n > 0 && n <= kAlone) {
+    Acc acc = nothing();
+    run(info[warp], 0, n, acc);
+    finish(acc, id);
+  }
+#pragma unroll 1
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const int4 x = info[w];
+    if (x.y <= kAlone) continue;  // (the same for the whole block)
+    Acc acc = nothing();
+    run(x, x.y * warp / kJoinWarps, x.y * (warp + 1) / kJoinWarps, acc);
+    shared[warp][lane] = acc;
+    __syncthreads();
+    if (warp == w) {
+      Acc all = nothing();
+      for (int i = 0; i < kJoinWarps; ++i) add(all, shared[i][lane].m, shared[i][lane].l, shared[i][lane].o);
+      finish(all, (int64_t)blockIdx.x * kJoinWarps + w);
+    }
+    __syncthreads();
+  }
+}
+
+bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+            std::string* why) {
+  auto fn = encode_fn();
+  if (fn == nullptr) {
+    *why = "cuTensorMapEncodeTiled is unavailable";
+    return false;
+  }
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, one,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    *why = "cuTensorMapEncodeTiled failed with CUresult " + std::to_string((int)r);
+    return false;
+  }
+  return true;
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tree(const TreeArgs& args, const void* q, int64_t q_stride, const h3attn_cache& c, cudaStream_t stream,
+                             std::string* why) {
+  static SmemAttr attr;
+  cudaError_t e = attr.set(attn_tree_kernel, (int)kSmemAlloc);
+  if (e != cudaSuccess) {
+    *why = "cudaFuncSetAttribute(max dynamic shared memory) failed";
+    return e;
+  }
+  TreeArgs a = args;
+  a.recip = (65536u + (uint32_t)a.pack - 1) / (uint32_t)a.pack;
+  a.page_size = c.page_size;
+  a.n_pages = c.n_pages;
+  a.box = c.page_size & -c.page_size;  // gcd(page_size, 128), of a multiple of 8
+  if (a.box > kRows) a.box = kRows;
+  CUtensorMap mq, mk, mv;
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)a.H, (cuuint64_t)a.S};
+    const cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.pack, (cuuint32_t)a.toks};
+    if (!encode(&mq, q, 3, dims, strides, box, why)) return cudaErrorInvalidValue;
+  }
+  // the smaller stride first; a dimension of one may have any
+  const int64_t tok = c.page_size > 1 ? c.token_stride : kHeadDim, hd = c.num_kv_heads > 1 ? c.head_stride : kHeadDim;
+  a.heads_first = hd < tok;
+  const cuuint64_t kv_dims[4] = {(cuuint64_t)kHeadDim, (cuuint64_t)(a.heads_first ? c.num_kv_heads : c.page_size),
+                                 (cuuint64_t)(a.heads_first ? c.page_size : c.num_kv_heads), (cuuint64_t)c.n_pages};
+  const cuuint64_t kv_strides[3] = {(cuuint64_t)(a.heads_first ? hd : tok) * 2, (cuuint64_t)(a.heads_first ? tok : hd) * 2,
+                                    (cuuint64_t)(c.n_pages > 1 ? c.page_stride : kHeadDim) * 2};
+  const cuuint32_t kv_box[4] = {64, a.heads_first ? 1u : (cuuint32_t)a.box, a.heads_first ? (cuuint32_t)a.box : 1u, 1};
+  if (!encode(&mk, c.k, 4, kv_dims, kv_strides, kv_box, why) || !encode(&mv, c.v, 4, kv_dims, kv_strides, kv_box, why))
+    return cudaErrorInvalidValue;
+  attn_tree_kernel<<<(unsigned)a.grid, kThreads, kSmemAlloc, stream>>>(mq, mk, mv, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = (a.S * a.H + kJoinWarps - 1) / kJoinWarps;
+  e = launch_dependent(attn_tree_join_kernel, (unsigned)blocks, 32u * kJoinWarps, stream, a);
+  if (e != cudaSuccess) *why = "the join launch failed";
+  return e;
+}
+
+}  // namespace h3

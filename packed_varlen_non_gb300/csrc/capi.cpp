@@ -95,6 +95,14 @@ void free_walk(WalkPlan* w) {
   w->d_part_ml = nullptr;
 }
 
+void free_tree(TreePlan* t) {
+  if (t->d_doc) cudaFree(t->d_doc);
+  if (t->d_prefix) cudaFree(t->d_prefix);
+  if (t->d_part_o) cudaFree(t->d_part_o);
+  if (t->d_part_ml) cudaFree(t->d_part_ml);
+  *t = TreePlan();
+}
+
 // Device copies of a walk's lists, and its partial buffers (enqueued; the caller
 // synchronises the stream before the host lists change).
 cudaError_t upload_walk(WalkPlan* w, cudaStream_t st) {
@@ -136,6 +144,7 @@ void free_plan_device(Plan* p) {
   free_walk(&p->sparse.walk);
   free_walk(&p->prefix.walk);
   free_walk(&p->causal.walk);
+  free_tree(&p->tree);
   if (p->sparse.d_groups) cudaFree(p->sparse.d_groups);
   if (p->sparse.d_q_sum) cudaFree(p->sparse.d_q_sum);
   if (p->sparse.d_k_mean) cudaFree(p->sparse.d_k_mean);
@@ -1297,6 +1306,126 @@ h3attn_status h3attn_forward_causal(h3attn_plan_t plan, const void* q, int64_t q
   return H3ATTN_OK;
 }
 
+// ------------------------------------------------------- tree attention ----
+
+h3attn_status h3attn_plan_set_tree(h3attn_plan_t plan, int32_t num_kv_heads, void* cuda_stream) {
+  clear_error();
+  if (h3attn_status s = check_plan(plan)) return s;
+  if (h3attn_status s = check_kv_heads(plan->num_heads, num_kv_heads)) return s;
+  TreePlan& tp = plan->tree;
+  if (tp.set) return fail(H3ATTN_EINVAL, "the plan's tree workspace is already set");
+  if (plan->max_seqlen > kTreeMax)
+    return fail(H3ATTN_EUNSUPPORTED, "a document of more than %d drafted tokens (%d)", kTreeMax, plan->max_seqlen);
+  if (plan->n_docs > kTreeDocs) return fail(H3ATTN_EUNSUPPORTED, "more than %d documents (%d)", kTreeDocs, plan->n_docs);
+  if (plan->S * plan->num_heads >= (int64_t(1) << 31)) return fail(H3ATTN_EUNSUPPORTED, "2^31 or more rows");
+  DeviceGuard g;
+  cudaError_t e = g.enter(plan->device);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+  TreePlan t;
+  t.kv_heads = num_kv_heads;
+  const int32_t group = plan->num_heads / num_kv_heads;
+  for (int32_t p = 1; p <= kKeyTile; ++p)
+    if (group % p == 0) t.pack = p;
+  t.toks = std::min(kKeyTile / t.pack, plan->max_seqlen);
+  t.max_len = plan->max_seqlen;
+  const int32_t qtiles = group / t.pack * ((plan->max_seqlen + t.toks - 1) / t.toks);
+  t.slot_rows = qtiles > 1 ? 2 * kKeyTile : kKeyTile;
+  t.grid = plan->num_sms;
+  const size_t rows = (size_t)2 * t.grid * t.slot_rows;
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  std::vector<int32_t> doc;
+  try {
+    doc.resize((size_t)plan->S);
+  } catch (const std::exception&) {
+    return fail(H3ATTN_ENOMEM, "host allocation failed for the tree workspace");
+  }
+  for (int32_t d = 0; d < plan->n_docs; ++d)
+    std::fill(doc.begin() + plan->cu_host[d], doc.begin() + plan->cu_host[d + 1], d);
+  e = cudaMalloc(&t.d_doc, doc.size() * sizeof(int32_t));
+  if (e == cudaSuccess) e = cudaMalloc(&t.d_prefix, ((size_t)plan->n_docs + 1) * sizeof(int64_t));
+  if (e == cudaSuccess) e = cudaMalloc(&t.d_part_o, rows * kHeadDim * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&t.d_part_ml, rows * sizeof(float2));
+  if (e == cudaSuccess) e = cudaMemcpyAsync(t.d_doc, doc.data(), doc.size() * sizeof(int32_t), cudaMemcpyHostToDevice, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) {
+    free_tree(&t);
+    return e == cudaErrorMemoryAllocation ? fail(H3ATTN_ENOMEM, "cudaMalloc failed for the plan's tree workspace")
+                                          : cuda_fail(e, "tree");
+  }
+  t.set = true;
+  tp = t;
+  return H3ATTN_OK;
+}
+
+h3attn_status h3attn_forward_tree(h3attn_plan_t plan, const void* q, int64_t q_row_stride, const h3attn_cache* cache,
+                                  const int32_t* page_table, int32_t table_width, const int32_t* ctx_lens,
+                                  const uint64_t* tree_mask, void* o, int64_t o_row_stride, float softmax_scale,
+                                  float* lse_out, void* cuda_stream) {
+  clear_error();
+  if (h3attn_status s = check_plan(plan)) return s;
+  const TreePlan& tp = plan->tree;
+  if (!tp.set) return fail(H3ATTN_EINVAL, "h3attn_plan_set_tree has not been called on this plan");
+  if (h3attn_status s = check_grouped_io(plan, q, q_row_stride, o, o_row_stride, softmax_scale, lse_out)) return s;
+  if (h3attn_status s = check_cache(cache)) return s;
+  if (cache->num_kv_heads != tp.kv_heads)
+    return fail(H3ATTN_EINVAL, "the cache has %d key heads, the plan %d", cache->num_kv_heads, tp.kv_heads);
+  if (!page_table || !ctx_lens || !aligned4(page_table) || !aligned4(ctx_lens) ||
+      (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
+    return fail(H3ATTN_EINVAL, "page_table and ctx_lens must be 4-byte aligned, tree_mask 8-byte aligned lists");
+  if (table_width < 1 || (int64_t)table_width * cache->page_size > INT32_MAX - kKeyTile ||
+      (int64_t)table_width * cache->page_size < tp.max_len)
+    return fail(H3ATTN_EINVAL, "table_width must hold the drafts and less than 2^31 - 128 rows (got %d pages of %d)", table_width,
+                cache->page_size);
+  const int64_t S = plan->S;
+  const uintptr_t o_bytes = Rows{"o", o, o_row_stride, plan->num_heads}.bytes(S), lse_bytes = (uintptr_t)S * plan->num_heads * 4;
+  struct List {
+    const void* p;
+    uintptr_t bytes;
+  };
+  for (const List& x : {List{page_table, (uintptr_t)plan->n_docs * table_width * 4}, List{ctx_lens, (uintptr_t)plan->n_docs * 4},
+                        List{tree_mask, tree_mask ? (uintptr_t)S * 8 : 0}})
+    if (x.p && (ranges_overlap(o, o_bytes, x.p, x.bytes) || (lse_out && ranges_overlap(lse_out, lse_bytes, x.p, x.bytes))))
+      return fail(H3ATTN_EINVAL, "o or lse_out overlaps a list");
+  if (overlaps_cache(cache, o, o_bytes) || (lse_out && overlaps_cache(cache, lse_out, lse_bytes)))
+    return fail(H3ATTN_EINVAL, "o or lse_out overlaps the cache");
+  if (cache->page_size % 8) return fail(H3ATTN_EUNSUPPORTED, "page_size must be a multiple of 8 (got %d)", cache->page_size);
+  DeviceGuard g;
+  cudaError_t e = g.enter(plan->device);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+  TreeArgs a{};
+  a.cu = plan->d_cu;
+  a.doc_of = tp.d_doc;
+  a.ctx_lens = ctx_lens;
+  a.page_table = page_table;
+  a.tree_mask = tree_mask;
+  a.S = S;
+  a.n_docs = plan->n_docs;
+  a.H = plan->num_heads;
+  a.kv_heads = tp.kv_heads;
+  a.group = plan->num_heads / tp.kv_heads;
+  a.table_width = table_width;
+  a.pack = tp.pack;
+  a.toks = tp.toks;
+  a.packs = a.group / tp.pack;
+  a.slot_rows = tp.slot_rows;
+  a.grid = tp.grid;
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.o_stride = o_row_stride;
+  a.lse = lse_out;
+  a.prefix = tp.d_prefix;
+  a.part_o = tp.d_part_o;
+  a.part_ml = tp.d_part_ml;
+  a.err = plan->d_err;
+  std::string why;
+  e = launch_attn_tree(a, q, q_row_stride, *cache, static_cast<cudaStream_t>(cuda_stream), &why);
+  if (e != cudaSuccess) {
+    if (!why.empty()) return fail(H3ATTN_ECUDA, "tree forward: %s", why.c_str());
+    return cuda_fail(e, "tree forward launch");
+  }
+  return H3ATTN_OK;
+}
+
 h3attn_status h3attn_get_device_error(h3attn_plan_t plan, void* cuda_stream) {
   clear_error();
   if (h3attn_status s = check_plan(plan)) return s;
@@ -1312,6 +1441,8 @@ h3attn_status h3attn_get_device_error(h3attn_plan_t plan, void* cuda_stream) {
   cudaMemset(plan->d_err, 0, sizeof(word));
   if (word == kErrTimeout)
     return fail(H3ATTN_ETIMEOUT, "a bounded device wait ran out; the outputs of that call are invalid");
+  if (word == kErrPage)
+    return fail(H3ATTN_EINVAL, "a sequence of the tree forward names a page outside the cache, or a length outside its table");
   if (word == kErrBlockIndex)
     return fail(H3ATTN_EINVAL, "a list of the sparse forward names a key tile outside its document (skipped)");
   return fail(H3ATTN_ECUDA, "device error word 0x%x", word);

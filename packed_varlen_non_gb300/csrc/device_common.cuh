@@ -131,6 +131,10 @@ static __device__ __noinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t par
 // says something stays: a timeout's outputs are invalid, a skipped tile's are not.
 __device__ __forceinline__ void report_bad_tile(uint32_t* err_word) { atomicCAS(err_word, kErrNone, kErrBlockIndex); }
 
+// Records that a sequence named a page outside the cache, or had a length that
+// does not fit its table.
+__device__ __forceinline__ void report_bad_page(uint32_t* err_word) { atomicCAS(err_word, kErrNone, kErrPage); }
+
 // Inline fast path for the hot waits: one try_wait before falling back to the
 // out-of-line bounded wait.  Calling the bounded wait on an already-complete
 // phase costs ~450-600 cycles in the MMA-issuing thread on GB300 (an inline
@@ -173,6 +177,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* desc, uint
       "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
       " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(desc)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "l"(cache_hint)
+      : "memory");
+}
+
+// 4D tiled load: c0 the inner (element) coordinate.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* desc, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3, uint64_t cache_hint) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(desc)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(cache_hint)
       : "memory");
 }
 

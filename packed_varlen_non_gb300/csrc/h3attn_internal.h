@@ -24,6 +24,7 @@ constexpr int kUnitRows = 512;      // query rows per attention work unit (a CTA
 constexpr uint32_t kErrNone = 0;
 constexpr uint32_t kErrTimeout = 1;
 constexpr uint32_t kErrBlockIndex = 2;   // a listed key tile outside its document
+constexpr uint32_t kErrPage = 3;         // a page outside the cache, or a length outside its table
 
 constexpr int kKeyTile = 128;      // key rows per tile
 
@@ -224,6 +225,23 @@ struct PrefixPlan {
   int32_t len = 0;
 };
 
+// Workspace of the tree forward.
+struct TreePlan {
+  bool set = false;
+  int32_t kv_heads = 0;
+  int32_t pack = 1;                    // query heads in a query tile (a divisor of the group), and tokens
+  int32_t toks = 1;
+  int32_t slot_rows = 0;               // rows of a partial slot: of one query tile, or of two
+  int32_t grid = 0;                    // blocks, two partial slots each
+  int32_t max_len = 0;                 // drafts of the longest document
+  int32_t* d_doc = nullptr;            // [S] document of a token
+  int64_t* d_prefix = nullptr;         // [n_docs + 1] steps before each sequence (written by the forward)
+  float* d_part_o = nullptr;           // [2 grid slot_rows, 128]
+  float2* d_part_ml = nullptr;         // [2 grid slot_rows]
+};
+constexpr int32_t kTreeMax = 64;       // drafts of a document
+constexpr int32_t kTreeDocs = 4096;
+
 struct CausalPlan {
   WalkPlan walk;
   int32_t kv_heads = 0;
@@ -310,6 +328,7 @@ struct Plan {
   SparsePlan sparse;                 // h3attn_plan_set_sparse
   PrefixPlan prefix;                 // h3attn_plan_set_prefix
   CausalPlan causal;                 // h3attn_plan_set_causal
+  TreePlan tree;                     // h3attn_plan_set_tree
 };
 
 // Host-side plan construction (plan.cpp); returns an empty string or an error.
@@ -444,6 +463,34 @@ cudaError_t launch_forward_list(const ForwardArgs& a, const WalkArgs& w, cudaStr
 cudaError_t launch_forward_prefix(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why);
 
 cudaError_t launch_forward_causal(const ForwardArgs& a, const WalkArgs& w, cudaStream_t stream, std::string* why);
+
+// Trees of drafts over a paged cache (attn_tree.cu).
+struct TreeArgs {
+  const int32_t* cu;           // [n_docs + 1]
+  const int32_t* doc_of;       // [S]
+  const int32_t* ctx_lens;     // [n_docs]
+  const int32_t* page_table;   // [n_docs, table_width]
+  const uint64_t* tree_mask;   // [S] or null
+  int64_t S;
+  int32_t n_docs, H, kv_heads, group, table_width;
+  int32_t pack, toks, packs;   // heads and tokens of a query tile, query tiles that a token's group takes
+  int32_t slot_rows, grid;
+  float scale_log2;
+  __nv_bfloat16* o;
+  int64_t o_stride;
+  float* lse;
+  int64_t* prefix;
+  float* part_o;
+  float2* part_ml;
+  uint32_t* err;
+  // (the launcher's)
+  uint32_t recip;              // row / pack = row * recip >> 16
+  int32_t page_size, n_pages;
+  int32_t box;                 // rows of the cache that a copy takes: gcd(page_size, 128)
+  int32_t heads_first;         // the cache's heads lie closer together than its tokens
+};
+cudaError_t launch_attn_tree(const TreeArgs& a, const void* q, int64_t q_stride, const h3attn_cache& cache, cudaStream_t stream,
+                             std::string* why);
 
 // Block scores and selection (block_select.cu).
 struct SelectArgs {

@@ -99,6 +99,9 @@ _SIGS = {
     "h3attn_plan_set_causal": [c_void_p, c_int32, c_void_p],
     "h3attn_forward_causal": [c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_float, c_void_p,
                               c_void_p],
+    "h3attn_plan_set_tree": [c_void_p, c_int32, c_void_p],
+    "h3attn_forward_tree": [c_void_p, c_void_p, c_int64, POINTER(h3attn_cache), c_void_p, c_int32, c_void_p, c_void_p, c_void_p,
+                            c_int64, c_float, c_void_p, c_void_p],
     "h3attn_rope_init": [POINTER(h3attn_rope_opts), POINTER(h3attn_rope)],
     "h3attn_rotary": [POINTER(h3attn_rope), c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int32, c_void_p,
                       c_int64, c_void_p, c_int64, c_int32, c_int32, c_void_p],
@@ -212,7 +215,7 @@ def h3attn_plan_create(docs, num_heads: int, rope_base: float = 10000.0, head_di
 
 
 def h3attn_plan_destroy(plan):
-    for known in (_list_sizes, _plan_rows, _prefix_rows, _causal_heads, _plan_device):
+    for known in (_list_sizes, _plan_rows, _prefix_rows, _causal_heads, _tree_docs, _plan_device):
         known.pop(plan, None)
     _check(load().h3attn_plan_destroy(plan), "h3attn_plan_destroy")
 
@@ -679,6 +682,44 @@ def h3attn_cache_move(cache: Cache, src, dst, stream=None):
         raise ValueError(f"src and dst are [groups, width] (got {tuple(src.shape)})")
     _call_on(cache.device, load().h3attn_cache_move, "h3attn_cache_move", cache.c, _ints(src, "src", src.shape, cache.device),
              _ints(dst, "dst", src.shape, cache.device), src.shape[0], src.shape[1], stream=stream)
+
+
+_tree_docs: dict = {}  # documents of the plans that have a tree workspace
+
+
+def h3attn_plan_set_tree(plan, num_kv_heads: int, stream=None):
+    """Adds the tree forward's workspace to a plan whose documents are trees of drafts (once per plan)."""
+    _check(load().h3attn_plan_set_tree(plan, int(num_kv_heads), _plan_stream(plan, stream)), "h3attn_plan_set_tree")
+    _known(plan)
+    _tree_docs[plan] = h3attn_plan_info(plan)["n_docs"]
+
+
+def h3attn_forward_tree(plan, q, cache: Cache, page_table, ctx_lens, o, softmax_scale: float, lse=None, tree_mask=None,
+                        q_row_stride=None, o_row_stride=None, stream=None):
+    """Attention of drafted tokens over their sequences' pages: q, o bf16 [S, H, 128]-shaped, page_table int32
+    [n_docs, width], ctx_lens int32 [n_docs], tree_mask int64 or uint64 [S] (None: each draft sees those before it)."""
+    sizes, docs = _plan_rows.get(plan), _tree_docs.get(plan)
+    rows = sizes[0] if sizes else 0
+    q_stride = _rows((q,), q_row_stride, rows, sizes)
+    o_stride = _rows((o,), o_row_stride, rows, sizes)
+    _check_lse(lse, sizes)
+    if docs is None:  # the call itself refuses a plan without a workspace
+        width, table, ctx = 1, 0, 0
+    else:
+        if page_table.dim() != 2:
+            raise ValueError(f"page_table is [n_docs, width] (got {tuple(page_table.shape)})")
+        width = page_table.shape[1]
+        table = _ints(page_table, "page_table", (docs, width), cache.device)
+        ctx = _ints(ctx_lens, "ctx_lens", (docs,), cache.device)
+        if sizes[2] is not None and cache.device != sizes[2]:
+            raise ValueError(f"the cache lies on GPU {cache.device}, the plan on {sizes[2]}")
+        if tree_mask is not None and not isinstance(tree_mask, int) and (
+                tree_mask.dtype not in (_torch().int64, _torch().uint64) or not tree_mask.is_contiguous()
+                or tuple(tree_mask.shape) != (rows,) or tree_mask.get_device() != cache.device):
+            raise ValueError(f"tree_mask must be a contiguous int64 or uint64 tensor ({rows},) on GPU {cache.device} "
+                             f"(got {tuple(tree_mask.shape)}, {tree_mask.dtype}, {tree_mask.device})")
+    _check(load().h3attn_forward_tree(plan, _ptr(q), q_stride, cache.c, table, width, ctx, _ptr(tree_mask), _ptr(o), o_stride,
+                                      float(softmax_scale), _ptr(lse), _plan_stream(plan, stream)), "h3attn_forward_tree")
 
 
 def h3attn_get_device_error(plan, stream=None):

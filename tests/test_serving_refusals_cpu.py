@@ -112,3 +112,8 @@ def test_move(lib):
     for kw in (dict(width=0), dict(width=257), dict(c=cache(num_kv_heads=32768, token_stride=1 << 22, page_stride=1 << 25))):
         assert move(**kw) == U, kw
     assert move(n=0, src=None, dst=None) == H.H3ATTN_OK
+
+
+def test_the_tree_calls_refuse_a_null_plan(lib):
+    assert status(lambda: H.h3attn_plan_set_tree(None, 1, stream=0)) == E
+    assert lib.load().h3attn_forward_tree(None, Q, 512, ctypes.byref(cache()), POS, 4, LIST, None, Q2, 512, 0.1, None, None) == E
