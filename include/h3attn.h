@@ -579,8 +579,8 @@ h3attn_status h3attn_forward_causal(h3attn_plan_t plan, const void* q, int64_t q
  * "once per plan" as h3attn_plan_set_sparse.
  * (Partial rows: 80 MB at most.)  Errors: EINVAL for a NULL plan, num_kv_heads < 1
  * or not a divisor of num_heads, workspace already set; EUNSUPPORTED for a document
- * of more than 64 tokens, more than 4,096 documents or 2^31 rows (tokens times heads);
- * ENOMEM / ECUDA. */
+ * of more than 64 tokens, more than 4,096 documents, 2^31 rows (tokens times heads) or 2^24 items (documents times
+ * key heads times pairs of 128-row tiles) or more; ENOMEM / ECUDA. */
 h3attn_status h3attn_plan_set_tree(h3attn_plan_t plan, int32_t num_kv_heads, void* cuda_stream);
 
 /* Sequence b (document [a, a + T) of the plan) has ctx_lens[b] context tokens,

@@ -11,21 +11,26 @@
 // fill the 128 lanes of a query tile (packed (token, head) as the causal walk does),
 // one or two such tiles share a pass over the keys, and the work is cut by keys, not
 // by rows:
-//   - a step is one 128-key tile of one (sequence, key head, up to two query tiles);
-//     the steps of all sequences, in order, are cut into equal ranges, one per SM.
+//   - a step is one 128-key tile of one item (sequence, key head, up to two query
+//     tiles).  Where there are no more items than SMs, every item is cut into equal
+//     pieces of at most L tiles, one block each, L the smallest for which there are
+//     blocks enough; otherwise the steps of all items, in order, are cut into equal ranges,
+//     one per SM, which may hold pieces of several items.  (A second piece costs a block
+//     4 us: its first loads and its first step wait for the first one's end.)
 //     Lengths are on the device, so each block adds them up itself and finds its
-//     range; no list is built on the host and one captured graph serves growing
+//     part; no list is built on the host and one captured graph serves growing
 //     sequences.
-//   - a range's pieces of items that other blocks share leave partial rows (m, l, O),
-//     at most two pieces a block; attn_tree_join_kernel combines them in the order of the
+//   - pieces of items that other blocks share leave partial rows (m, l, O), at most two
+//     of them a block; attn_tree_join_kernel combines them in the order of the
 //     keys, so results do not depend on which block ends first.
-// Per block (one an SM), 11 warps:
+// Per block (one an SM), 12 warps:
 //   warps 0..3, 4..7  softmax of stream 0 and 1, a thread a row;
 //   warp 8            issues the MMAs: S_s = Q K^T (128 x 128 fp32 in TMEM), O_s += P V with
 //                     P (bf16) in S's columns;
-//   warp 9            K and V tiles through a ring of five 32 KB slots (160 KB on their way an SM);
-//                     a lane a page box: gcd(page_size, 128) rows each;
-//   warp 10           Q tiles.
+//   warp 9            Q tiles;
+//   warps 10, 11      K tiles and V tiles, through one ring of five 32 KB slots (160 KB on their way
+//                     an SM); a lane a page box: gcd(page_size, 128) rows each.  (A warp issues a
+//                     copy in about 100 cycles: pages of 16 take 32 of them a step.)
 // Two streams hide the chain S -> softmax -> PV: with two query tiles a stream is a
 // query tile; with one, the streams take the key tiles in turn, each with a running
 // maximum and O of its own, and the block joins the two at the piece's end.
@@ -44,8 +49,9 @@ namespace h3 {
 
 namespace {
 
-constexpr int kThreads = 352;
-constexpr int kMmaWarp = 8, kKvWarp = 9, kQWarp = 10;
+constexpr int kThreads = 384;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMmaWarp = 8, kQWarp = 9, kKWarp = 10, kVWarp = 11;
 constexpr int kRows = 128;                          // of a query tile, and of a key tile
 constexpr int kSlots = 5;
 constexpr uint32_t kTileBytes = 128 * 256;          // two halves of 64 dims, 128-byte rows
@@ -128,20 +134,23 @@ __device__ __forceinline__ void commit_elect(uint32_t bar) {
 // A sequence: its drafts [row0, row0 + T), context, key tiles, and items (key head, unit of up to two query tiles).
 struct Doc {
   int32_t row0, T, ctx, tiles, qtiles, units;
-  bool bad;
 };
-__device__ __forceinline__ Doc doc_of(const TreeArgs& a, int b) {
+__device__ __forceinline__ int32_t context(const TreeArgs& a, int32_t T, int32_t given) {
+  const int64_t most = (int64_t)a.table_width * a.page_size - T;  // (not negative, and below 2^31: checked by the caller)
+  return max(0, (int32_t)min((int64_t)given, most));
+}
+__device__ __forceinline__ Doc make_doc(const TreeArgs& a, int32_t row0, int32_t row1, int32_t given) {
   Doc d;
-  d.row0 = __ldg(a.cu + b);
-  d.T = __ldg(a.cu + b + 1) - d.row0;
-  const int32_t given = __ldg(a.ctx_lens + b);
-  const int64_t most = (int64_t)a.table_width * a.page_size - d.T;  // (not negative, and below 2^31: checked by the caller)
-  d.ctx = max(0, (int32_t)min((int64_t)given, most));
-  d.bad = d.ctx != given;
+  d.row0 = row0;
+  d.T = row1 - row0;
+  d.ctx = context(a, d.T, given);
   d.tiles = (int32_t)(((int64_t)d.ctx + d.T + kRows - 1) / kRows);
   d.qtiles = a.packs * ((d.T + a.toks - 1) / a.toks);
   d.units = (d.qtiles + 1) / 2;
   return d;
+}
+__device__ __forceinline__ Doc doc_of(const TreeArgs& a, int b) {
+  return make_doc(a, __ldg(a.cu + b), __ldg(a.cu + b + 1), __ldg(a.ctx_lens + b));
 }
 
 // A block's share of one item: key tiles [lo, hi).
@@ -152,27 +161,40 @@ struct Piece {
   bool first;          // of the block's pieces
   int32_t at;          // steps of the block before it
 };
+// Where a block's range begins (found once, for all roles).
+struct Start {
+  int32_t b, steps, item, lo, row0, row1, given;
+};
 // Walks a block's range piece by piece; every role runs its own.
 struct Walk {
   int32_t b, item, lo;
   int32_t left, at;
   bool first;
   Doc d;
-  __device__ void begin(const TreeArgs& a, int32_t b_, int64_t off, int32_t steps) {
-    b = b_;
-    left = steps;
+  int32_t row2, given;  // of the next sequence: its end and length, on their way while this one runs
+  __device__ void ahead(const TreeArgs& a) {
+    const int n = min(b + 1, a.n_docs - 1);
+    row2 = __ldg(a.cu + n + 1);
+    given = __ldg(a.ctx_lens + n);
+  }
+  __device__ void begin(const TreeArgs& a, const volatile Start& s) {
+    b = s.b;
+    left = s.steps;
     at = 0;
     first = true;
-    d = doc_of(a, b);
-    item = (int32_t)(off / d.tiles);
-    lo = (int32_t)(off - (int64_t)item * d.tiles);
+    item = s.item;
+    lo = s.lo;
+    ahead(a);
+    d = make_doc(a, s.row0, s.row1, s.given);
   }
   // the next piece; false at the end
   __device__ bool next(const TreeArgs& a, Piece* p) {
     if (left <= 0) return false;
     if (item == a.kv_heads * d.units) {
       item = 0;
-      d = doc_of(a, ++b);
+      ++b;
+      d = make_doc(a, d.row0 + d.T, row2, given);
+      ahead(a);
     }
     p->b = b;
     p->kvh = item / d.units;
@@ -223,58 +245,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Bars bars{sbase + kSmemBar};
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kSmemMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kSmemMisc + 4);
-  // the block's range: first sequence, offset in its steps, steps
-  volatile int32_t* const range = reinterpret_cast<volatile int32_t*>(smem + kSmemMisc + 8);
-  volatile int64_t* const range_off = reinterpret_cast<volatile int64_t*>(smem + kSmemMisc + 16);
+  volatile Start& start = *reinterpret_cast<volatile Start*>(smem + kSmemMisc + 8);
   const uint32_t warp = dev::warp_id_uniform();
   const uint32_t lane = threadIdx.x & 31;
 
   asm volatile("griddepcontrol.launch_dependents;");  // (the join waits for this grid's end)
-  {
-    // every thread a run of sequences: steps before them, and in all
-    int64_t* const sums = reinterpret_cast<int64_t*>(smem + kSmemMl);
-    const int per = (a.n_docs + kThreads - 1) / kThreads;
-    const int b0 = min((int)threadIdx.x * per, a.n_docs), b1 = min(b0 + per, a.n_docs);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) {
-      const Doc d = doc_of(a, b);
-      mine += (int64_t)d.tiles * d.units * a.kv_heads;
-      if (d.bad && blockIdx.x == 0) dev::report_bad_page(a.err);
-    }
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-      if ((int)lane >= o) incl += x;
-    }
-    if (lane == 31) sums[warp] = incl;
-    __syncthreads();
-    int64_t before = incl - mine, total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < (int)warp) before += sums[w];
-      total += sums[w];
-    }
-    const int64_t grid = min((int64_t)gridDim.x, total);
-    const int64_t c = blockIdx.x;
-    const int64_t s0 = c < grid ? total * c / grid : total, s1 = c < grid ? total * (c + 1) / grid : total;
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.prefix[a.n_docs] = total;
-    for (int b = b0; b < b1; ++b) {
-      const Doc d = doc_of(a, b);
-      const int64_t n = (int64_t)d.tiles * d.units * a.kv_heads;
-      if (blockIdx.x == 0) a.prefix[b] = before;
-      if (s0 >= before && s0 < before + n) {
-        range[0] = b;
-        range[1] = (int32_t)(s1 - s0);
-        range_off[0] = s0 - before;
-      }
-      before += n;
-    }
-    if (c >= grid) return;  // (the whole block)
-    __syncthreads();
-  }
-  const int32_t steps = range[1];
-
+  if (warp == kKWarp && lane < 3) dev::tma_prefetch_desc(lane == 0 ? &tm_k : lane == 1 ? &tm_v : &tm_q);
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < 2; ++i) {
@@ -292,6 +268,92 @@ __global__ void __launch_bounds__(kThreads, 1)
     dev::mbar_init(bars.joined(), 8);
     dev::fence_barrier_init();
   }
+
+  // What this block does.  Every thread adds up a run of sequences.
+  const int per = (a.n_docs + kThreads - 1) / kThreads;
+  const int b0 = min((int)threadIdx.x * per, a.n_docs), b1 = min(b0 + per, a.n_docs);
+  int64_t* const sums = reinterpret_cast<int64_t*>(smem + kSmemMl);
+  // the sum over all threads, and over those before this one
+  const auto scan = [&](int64_t mine, int64_t* before) {
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if ((int)lane >= o) incl += x;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int64_t total = 0;
+    *before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < (int)warp) *before += sums[w];
+      total += sums[w];
+    }
+    return total;
+  };
+  Doc d0 = {};  // (the thread's sequence, where there is one to a thread)
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    d0 = doc_of(a, b);
+    mine += (int64_t)d0.tiles * d0.units * a.kv_heads;
+  }
+  int64_t before, total = scan(mine, &before);
+  int32_t most = 0;  // tiles of a piece; 0: ranges
+  if (a.items <= (int)gridDim.x) {
+    // (so there is a thread to every sequence) candidates: a lane each, from the even share on
+    int32_t* const pieces_of = reinterpret_cast<int32_t*>(smem + kSmemMl);  // [kWarps][32]
+    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+    const int32_t cand = (int32_t)min(share + lane, (int64_t)INT32_MAX / 2);
+    int32_t n = 0;
+    for (int b = warp; b < a.n_docs; b += kWarps) {
+      const Doc d = doc_of(a, b);
+      n += d.units * a.kv_heads * ((d.tiles + cand - 1) / cand);
+    }
+    __syncthreads();
+    pieces_of[warp * 32 + lane] = n;
+    __syncthreads();
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) n += pieces_of[w * 32 + lane];
+    const unsigned fits = __ballot_sync(0xffffffffu, n <= (int)gridDim.x);
+    __syncthreads();
+    // (three tiles more than the even share are quicker than a second piece)
+    if (fits != 0 && __ffs(fits) - 1 <= 3) most = (int32_t)share + __ffs(fits) - 1;
+    if (most > 0) total = scan(b0 < b1 ? (int64_t)d0.units * a.kv_heads * ((d0.tiles + most - 1) / most) : 0, &before);
+  }
+  const int64_t grid = min((int64_t)gridDim.x, total);
+  const int64_t c = blockIdx.x;
+  if (c >= grid) return;  // (the whole block)
+  const int64_t s0 = most > 0 ? c : total * c / grid, s1 = most > 0 ? c + 1 : total * (c + 1) / grid;
+  if (s1 - s0 > INT32_MAX) {  // (hours of work: lengths of 2^31 in thousands of sequences)
+    if (threadIdx.x == 0) dev::report_bad_page(a.err);
+    return;
+  }
+  for (int b = b0; b < b1; ++b) {
+    const Doc d = per == 1 ? d0 : doc_of(a, b);
+    const int32_t cut = most > 0 ? (d.tiles + most - 1) / most : d.tiles;  // pieces (steps) of an item
+    const int64_t n = (int64_t)cut * d.units * a.kv_heads;
+    if (s0 >= before && s0 < before + n) {
+      const int32_t item = (int32_t)((s0 - before) / cut), i = (int32_t)((s0 - before) - (int64_t)item * cut);
+      start.b = b;
+      start.item = item;
+      start.lo = most > 0 ? (int32_t)((int64_t)d.tiles * i / cut) : i;
+      start.steps = most > 0 ? (int32_t)((int64_t)d.tiles * (i + 1) / cut) - (int32_t)((int64_t)d.tiles * i / cut) : (int32_t)(s1 - s0);
+      start.row0 = d.row0;
+      start.row1 = d.row0 + d.T;
+      start.given = d.ctx;
+    }
+    if (c == 0) {  // for the join
+      a.prefix[b] = before;
+      if (b + 1 == a.n_docs) {
+        a.prefix[b + 1] = total;
+        a.prefix[b + 2] = most;
+      }
+      if (__ldg(a.ctx_lens + b) != d.ctx) dev::report_bad_page(a.err);
+    }
+    before += n;
+  }
   if (a.pack * a.toks < kRows) {
     // rows of a query tile that no load fills (their scores must not be anything: see attn_fwd_tc.cu)
     for (uint32_t i = threadIdx.x * 16u; i < 2 * kTileBytes; i += kThreads * 16u)
@@ -306,75 +368,69 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   dev::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const int32_t steps = start.steps;
   Walk walk;
-  walk.begin(a, range[0], range_off[0], steps);
+  walk.begin(a, start);
   Piece p;
 
-  if (warp == kKvWarp) {
-    // ---------------------------------------------------- K and V tiles ----
+  if (warp == kKWarp || warp == kVWarp) {
+    // ------------------------------------------------------ K or V tiles ----
+    const bool is_v = warp == kVWarp;
+    const CUtensorMap* const tm = is_v ? &tm_v : &tm_k;
     // (tiles that other units read too should stay in L2)
     const uint64_t pol_once = dev::policy_evict_first(), pol_shared = dev::policy_evict_last();
-    const int n_box = kRows / a.box;  // boxes of a tile, a lane each
-    uint32_t loaded = 0;
+    const int n_box = kRows / a.box;             // boxes of a tile, a lane each
+    const int32_t tiles_at_once = 32 / n_box;
+    const uint32_t dst0 = sbase + kSmemKV + lane * (uint32_t)a.box * 128u;
+    int32_t loaded = 0;                          // tiles
     bool ok = true;
-    // a tile's box of this lane: whether it holds rows, its page and row; the tile's key head and bytes
-    struct Tile {
-      bool in;
-      int32_t page, row, kvh;
-      uint32_t bytes;
-      uint64_t pol;
-    };
-    const auto load = [&](const CUtensorMap* tm, const Tile& t) {
-      const uint32_t slot = loaded % kSlots;
-      bool good = true;
-      if (lane == 0) good = dev::mbar_wait(bars.empty(slot), ((loaded / kSlots) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
-      ok = __shfl_sync(0xffffffffu, good, 0);
-      if (!ok) return;
-      if (lane == 0) dev::mbar_arrive_expect_tx(bars.full(slot), t.bytes);
-      __syncwarp();
-      if (t.in) {
-        const uint32_t dst = sbase + kSmemKV + slot * kTileBytes + lane * (uint32_t)a.box * 128u;
-        const int32_t c1 = a.heads_first ? t.kvh : t.row, c2 = a.heads_first ? t.row : t.kvh;
-        dev::tma_load_4d(dst, tm, bars.full(slot), 0, c1, c2, t.page, t.pol);
-        dev::tma_load_4d(dst + kHalfBytes, tm, bars.full(slot), 64, c1, c2, t.page, t.pol);
-      }
-      ++loaded;
-    };
-    Tile prev{};
-    bool any = false;
     while (ok && walk.next(a, &p)) {
       const int32_t total = walk.d.ctx + walk.d.T;
       const int32_t* table = a.page_table + (int64_t)p.b * a.table_width;
-      const auto page_of = [&](int32_t t) {
-        const uint32_t key = (uint32_t)t * kRows + lane * (uint32_t)a.box;
-        return (int)lane < n_box && t < p.hi && key < (uint32_t)total ? __ldg(table + key / (uint32_t)a.page_size) : 0;
+      const uint64_t pol = walk.d.units > 1 ? pol_shared : pol_once;
+      // Page numbers a window of 32 boxes at a time, a lane each, the next window on
+      // its way (a lookup a tile, though asked for a tile ahead, paced the loads: 1,000 cycles a tile).
+      const auto pages_from = [&](int32_t t) {
+        const int64_t key = ((int64_t)t * n_box + lane) * a.box;
+        return key < total ? __ldg(table + (uint32_t)key / (uint32_t)a.page_size) : 0;
       };
-      int32_t page = page_of(p.lo);
-      for (int32_t t = p.lo; ok && t < p.hi; ++t) {
-        const uint32_t key = (uint32_t)t * kRows + lane * (uint32_t)a.box;
-        Tile cur;
-        cur.in = (int)lane < n_box && key < (uint32_t)total;
-        cur.page = page;
-        page = page_of(t + 1);  // a tile ahead of its use
-        cur.row = (int32_t)(key % (uint32_t)a.page_size);
-        cur.kvh = p.kvh;
-        cur.pol = walk.d.units > 1 ? pol_shared : pol_once;
-        const int32_t boxes = min(n_box, (total - t * kRows + a.box - 1) / a.box);
-        cur.bytes = (uint32_t)boxes * (uint32_t)a.box * 256u;
-        if (cur.in && (uint32_t)cur.page >= (uint32_t)a.n_pages) {
-          dev::report_bad_page(a.err);
-          cur.page = a.n_pages;  // outside the tensor map: zeros
+      int32_t pages = pages_from(p.lo), pages_next = pages_from(p.lo + tiles_at_once), window = p.lo;
+      for (int32_t t = p.lo; t < p.hi; ++t) {
+        if (t - window == tiles_at_once) {
+          window = t;
+          pages = pages_next;
+          pages_next = pages_from(t + tiles_at_once);
         }
-        load(&tm_k, cur);
-        if (ok && any) load(&tm_v, prev);
-        prev = cur;
-        any = true;
+        const uint32_t key = (uint32_t)t * kRows + lane * (uint32_t)a.box;
+        const bool in = (int)lane < n_box && key < (uint32_t)total;
+        int32_t page = __shfl_sync(0xffffffffu, pages, (t - window) * n_box + (int)lane & 31);
+        if (in && (uint32_t)page >= (uint32_t)a.n_pages) {
+          dev::report_bad_page(a.err);
+          page = a.n_pages;  // outside the tensor map: zeros
+        }
+        const int32_t row = (int32_t)(key % (uint32_t)a.page_size);
+        const int32_t c1 = a.heads_first ? p.kvh : row, c2 = a.heads_first ? row : p.kvh;
+        const int32_t boxes = min(n_box, (total - t * kRows + a.box - 1) / a.box);
+        const uint32_t entry = is_v ? v_entry(loaded, steps) : k_entry(loaded), slot = entry % kSlots, bar = bars.full(slot);
+        bool good = true;
+        if (lane == 0) {
+          good = dev::mbar_wait(bars.empty(slot), ((entry / kSlots) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
+          if (good) dev::mbar_arrive_expect_tx(bar, (uint32_t)boxes * (uint32_t)a.box * 256u);
+        }
+        ok = __shfl_sync(0xffffffffu, good, 0);
+        if (!ok) break;
+        if (in) {
+          dev::tma_load_4d(dst0 + slot * kTileBytes, tm, bar, 0, c1, c2, page, pol);
+          dev::tma_load_4d(dst0 + slot * kTileBytes + kHalfBytes, tm, bar, 64, c1, c2, page, pol);
+        }
+        ++loaded;
       }
     }
-    if (ok && any) load(&tm_v, prev);
-    if (!ok && lane == 0) {  // drain: wait (bounded) for the copies on their way
-      for (uint32_t r = 1; r <= (uint32_t)kSlots && r <= loaded; ++r)
-        dev::mbar_wait_bounded(bars.full((loaded - r) % kSlots), ((loaded - r) / kSlots) & 1, nullptr, nullptr, kTimeoutNs);
+    if (!ok && lane == 0) {  // drain: wait (bounded) for the copies on their way (every other of five slots)
+      for (int32_t t = max(0, loaded - 3); t < loaded; ++t) {
+        const uint32_t entry = is_v ? v_entry(t, steps) : k_entry(t);
+        dev::mbar_wait_bounded(bars.full(entry % kSlots), (entry / kSlots) & 1, nullptr, nullptr, kTimeoutNs);
+      }
     }
     __syncwarp();
   } else if (warp == kQWarp) {
@@ -441,10 +497,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int32_t j = 0; ok && j < n; ++j) {
           const uint32_t ve = v_entry(t0 + j, steps), ke = k_entry(t0 + j + 1);
           const bool more = j + 1 < n;
+          // (the tiles before P: they landed long ago, and asking takes 200 cycles each, which P would wait for)
+          if (!landed(ve) || (more && !landed(ke))) break;
           for (int s = 0; s < 2; ++s) {
             if (!wait(bars.p_ready(s), p_it[s] & 1)) break;
             ++p_it[s];
-            if (s == 0 && (!landed(ve) || (more && !landed(ke)))) break;
             pv(s, ve, j > 0);
             if (more)
               qk(s, s == 0 ? q0 : q1, ke);
@@ -471,17 +528,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int32_t j = 0; ok && j < n; ++j) {
           const int s = j & 1;
           const uint32_t ve = v_entry(t0 + j, steps);
+          const uint32_t ke = k_entry(t0 + j + 2);
+          if (!landed(ve) || (j + 2 < n && !landed(ke))) break;
           if (!wait(bars.p_ready(s), (s == 0 ? p_it[0] : p_it[1]) & 1)) break;
           if (s == 0)
             ++p_it[0];
           else
             ++p_it[1];
-          if (!landed(ve)) break;
           pv(s, ve, j >= 2);
           release(ve);
           if (j + 2 < n) {
-            const uint32_t ke = k_entry(t0 + j + 2);
-            if (!landed(ke)) break;
             qk(s, q0, ke);
             release(ke);
             if (j + 3 == n) commit_elect(bars.q_empty(q0));
@@ -524,13 +580,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = tok_in < (uint32_t)q.n_tok;  // (rows past pack * toks have larger tok_in)
       const bool busy = (int32_t)(lane_base * a.recip >> 16) < q.n_tok;  // any row of this warp
       const int32_t n = p.hi - p.lo;
-      // the drafts that this row sees
-      uint64_t word = 0;
-      if (valid) {
-        const int32_t i = q.tok0 + (int32_t)tok_in - d.row0;
-        word = a.tree_mask != nullptr ? __ldg(reinterpret_cast<const unsigned long long*>(a.tree_mask) + d.row0 + i) : ~0ull >> (63 - i);
-        word &= ~0ull >> (64 - d.T);
-      }
+      // the drafts that this row sees (of use in the last tiles only: nothing waits for it here)
+      uint64_t mask = 0;
+      if (valid)
+        mask = a.tree_mask != nullptr ? __ldg(reinterpret_cast<const unsigned long long*>(a.tree_mask) + q.tok0 + (int32_t)tok_in)
+                                      : ~0ull >> (63 - (q.tok0 + (int32_t)tok_in - d.row0));
       float m = kLowest, l = 0.f;
       for (int32_t j = two ? 0 : st; ok && j < n; j += two ? 1 : 2) {
         const int32_t t = p.lo + j;
@@ -539,36 +593,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();  // lanes leave the wait separately; the TMEM loads are warp-collective
         dev::tc_fence_after();
         if (busy) {
-          uint32_t r[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) dev::tmem_ld32(t_s + c * 32, r[c]);
-          dev::tmem_wait_ld();
-          float* sv = reinterpret_cast<float*>(&r[0][0]);
           const int32_t base = t * kRows - d.ctx;  // draft of the tile's first key (negative: context)
-          if (base + kRows > 0) {
-            uint64_t lo = ~0ull, hi = 0;           // keys that the row sees
+          const bool edge = base + kRows > 0;
+          uint64_t see[2] = {~0ull, 0};            // keys that the row sees
+          if (edge) {
+            const uint64_t word = mask & (~0ull >> (64 - d.T));
             if (base >= 0) {
-              lo = word >> base;                   // (the last tile begins before the last draft: below 64)
+              see[0] = word >> base;               // (the last tile begins before the last draft: below 64)
             } else if (base > -64) {
-              lo = (word << -base) | ((1ull << -base) - 1);
-              hi = word >> (64 + base);
+              see[0] = (word << -base) | ((1ull << -base) - 1);
+              see[1] = word >> (64 + base);
             } else if (base == -64) {
-              hi = word;
+              see[1] = word;
             } else {
-              hi = (word << (-base - 64)) | ((1ull << (-base - 64)) - 1);
+              see[1] = (word << (-base - 64)) | ((1ull << (-base - 64)) - 1);
             }
-            const uint32_t w[4] = {(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (!((w[c >> 5] >> (c & 31)) & 1u)) sv[c] = -INFINITY;
           }
+          // a half of the tile's scores, 64 keys, at a time: the second half's maximum, the first
+          // half's maximum and weights, the second half again (all 128 at once spilled to local memory,
+          // of which little stays close when shared memory takes most of L1: 4.3 us a step for 1.4)
+          float sv[64];
+          const auto scores = [&](int h) {
+            uint32_t r[2][32];
+            dev::tmem_ld32(t_s + 64 * h, r[0]);
+            dev::tmem_ld32(t_s + 64 * h + 32, r[1]);
+            dev::tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 64; ++c) sv[c] = __uint_as_float(r[c >> 5][c & 31]);
+            if (edge) {
+              const uint64_t half = h == 0 ? see[0] : see[1];
+              const uint32_t w[2] = {(uint32_t)half, (uint32_t)(half >> 32)};
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                if (!((w[c >> 5] >> (c & 31)) & 1u)) sv[c] = -INFINITY;
+            }
+          };
           float mx[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) mx[i] = fmaxf(sv[i], sv[8 + i]);
+          for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+          // (loops as they are, not unrolled: a block that has a few tiles fetches every instruction once)
+#pragma unroll 1
+          for (int h = 1; h >= 0; --h) {
+            scores(h);
 #pragma unroll
-          for (int c = 16; c < 128; c += 16)
+            for (int c = 0; c < 64; c += 16)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) mx[i] = dev::max3(mx[i], sv[c + i], sv[c + 8 + i]);
+              for (int i = 0; i < 8; ++i) mx[i] = dev::max3(mx[i], sv[c + i], sv[c + 8 + i]);
+          }
           const float m_new =
               dev::max3(dev::max3(mx[0], mx[1], mx[2]), dev::max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * a.scale_log2;
           float alpha = 1.f;
@@ -578,20 +649,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float neg = -m;
           float rs8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
+            if (h == 1) scores(1);
             uint32_t pr[32];
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
               float x0, x1;
-              dev::fma2(x0, x1, sv[64 * h + 2 * c], sv[64 * h + 2 * c + 1], a.scale_log2, a.scale_log2, neg, neg);
+              dev::fma2(x0, x1, sv[2 * c], sv[2 * c + 1], a.scale_log2, a.scale_log2, neg, neg);
               const float p0 = dev::ex2_approx(x0), p1 = dev::ex2_approx(x1);
               const int ai = 2 * (c & 3);
               dev::add2(rs8[ai], rs8[ai + 1], rs8[ai], rs8[ai + 1], p0, p1);
               // bf16, as the operand of the tensor cores: half a step of each weight, the sum keeps fp32
               pr[c] = dev::pack_bf16x2(p0, p1);
             }
-            dev::tmem_st32(t_s + 32 * h, pr);
+            dev::tmem_st32(t_s + 32 * h, pr);  // (over the first half's scores, which are read)
           }
           const float rs = ((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7]));
           l = l * alpha + rs;
@@ -755,17 +827,27 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_tree_join_kernel(const _
   const int32_t b = __ldg(a.doc_of + tok), row0 = __ldg(a.cu + b), T = __ldg(a.cu + b + 1) - row0;
   const int32_t kvh = head / a.group, in = head - kvh * a.group, pk = in / a.pack, blk = (tok - row0) / a.toks;
   const int32_t qt = blk * a.packs + pk;
-  const int32_t units = (a.packs * ((T + a.toks - 1) / a.toks) + 1) / 2;
+  const Doc d = make_doc(a, row0, row0 + T, __ldg(a.ctx_lens + b));
+  const int32_t item = kvh * d.units + qt / 2;
   const int32_t row = (qt & 1) * kRows + ((tok - row0) - blk * a.toks) * a.pack + (in - pk * a.pack);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the forward is complete and its writes visible
-  const int64_t total = a.prefix[a.n_docs], first = a.prefix[b], tiles = (a.prefix[b + 1] - first) / ((int64_t)units * a.kv_heads);
-  const int64_t grid = min((int64_t)a.grid, total);
-  const int64_t s0 = first + ((int64_t)kvh * units + qt / 2) * tiles, s1 = s0 + tiles;  // the item's steps
-  // block c has steps [total c / grid, total (c + 1) / grid)
-  const int32_t c0 = (int32_t)(((s0 + 1) * grid - 1) / total), c1 = (int32_t)((s1 * grid - 1) / total);
-  const int32_t n = real && c1 > c0 ? c1 - c0 + 1 : 0;  // (a block's whole items are written by it)
-  // the piece of the first block is its last one unless the item begins there; the others' is their first
-  const int32_t slot0 = 2 * c0 + (total * c0 / grid < s0 ? 1 : 0);
+  const int64_t total = a.prefix[a.n_docs], first = a.prefix[b];
+  const int32_t most = (int32_t)a.prefix[a.n_docs + 1];
+  int32_t c0, n, slot0;  // the blocks that share the item
+  if (most > 0) {
+    n = (d.tiles + most - 1) / most;
+    c0 = (int32_t)(first + (int64_t)item * n);
+    slot0 = 2 * c0;
+  } else {
+    const int64_t grid = min((int64_t)a.grid, total);
+    const int64_t s0 = first + (int64_t)item * d.tiles, s1 = s0 + d.tiles;  // the item's steps
+    // block c has steps [total c / grid, total (c + 1) / grid)
+    c0 = (int32_t)(((s0 + 1) * grid - 1) / total);
+    n = (int32_t)((s1 * grid - 1) / total) - c0 + 1;
+    // the piece of the first block is its last one unless the item begins there; the others' is their first
+    slot0 = 2 * c0 + (total * c0 / grid < s0 ? 1 : 0);
+  }
+  if (!real || n == 1) n = 0;  // (a block's whole items are written by it)
   if (lane == 0) info[warp] = make_int4(c0, n, row, slot0);
   __syncthreads();
   const auto part_row = [&](const int4& x, int32_t i) {

@@ -1330,6 +1330,13 @@ h3attn_status h3attn_plan_set_tree(h3attn_plan_t plan, int32_t num_kv_heads, voi
   t.max_len = plan->max_seqlen;
   const int32_t qtiles = group / t.pack * ((plan->max_seqlen + t.toks - 1) / t.toks);
   t.slot_rows = qtiles > 1 ? 2 * kKeyTile : kKeyTile;
+  int64_t items = 0;
+  for (int32_t d = 0; d < plan->n_docs; ++d) {
+    const int32_t T = plan->cu_host[d + 1] - plan->cu_host[d];
+    items += ((int64_t)(group / t.pack) * ((T + t.toks - 1) / t.toks) + 1) / 2 * num_kv_heads;
+  }
+  if (items >= (int64_t(1) << 24)) return fail(H3ATTN_EUNSUPPORTED, "2^24 or more items (sequences times key heads times row tiles)");
+  t.items = (int32_t)items;
   t.grid = plan->num_sms;
   const size_t rows = (size_t)2 * t.grid * t.slot_rows;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
@@ -1342,7 +1349,7 @@ h3attn_status h3attn_plan_set_tree(h3attn_plan_t plan, int32_t num_kv_heads, voi
   for (int32_t d = 0; d < plan->n_docs; ++d)
     std::fill(doc.begin() + plan->cu_host[d], doc.begin() + plan->cu_host[d + 1], d);
   e = cudaMalloc(&t.d_doc, doc.size() * sizeof(int32_t));
-  if (e == cudaSuccess) e = cudaMalloc(&t.d_prefix, ((size_t)plan->n_docs + 1) * sizeof(int64_t));
+  if (e == cudaSuccess) e = cudaMalloc(&t.d_prefix, ((size_t)plan->n_docs + 2) * sizeof(int64_t));
   if (e == cudaSuccess) e = cudaMalloc(&t.d_part_o, rows * kHeadDim * sizeof(float));
   if (e == cudaSuccess) e = cudaMalloc(&t.d_part_ml, rows * sizeof(float2));
   if (e == cudaSuccess) e = cudaMemcpyAsync(t.d_doc, doc.data(), doc.size() * sizeof(int32_t), cudaMemcpyHostToDevice, st);
@@ -1409,6 +1416,7 @@ h3attn_status h3attn_forward_tree(h3attn_plan_t plan, const void* q, int64_t q_r
   a.packs = a.group / tp.pack;
   a.slot_rows = tp.slot_rows;
   a.grid = tp.grid;
+  a.items = tp.items;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.o_stride = o_row_stride;

@@ -233,9 +233,10 @@ struct TreePlan {
   int32_t toks = 1;
   int32_t slot_rows = 0;               // rows of a partial slot: of one query tile, or of two
   int32_t grid = 0;                    // blocks, two partial slots each
+  int32_t items = 0;                   // (sequence, key head, up to two query tiles)
   int32_t max_len = 0;                 // drafts of the longest document
   int32_t* d_doc = nullptr;            // [S] document of a token
-  int64_t* d_prefix = nullptr;         // [n_docs + 1] steps before each sequence (written by the forward)
+  int64_t* d_prefix = nullptr;         // [n_docs + 2] steps or pieces before each sequence, tiles of a piece (the forward's)
   float* d_part_o = nullptr;           // [2 grid slot_rows, 128]
   float2* d_part_ml = nullptr;         // [2 grid slot_rows]
 };
@@ -474,7 +475,7 @@ struct TreeArgs {
   int64_t S;
   int32_t n_docs, H, kv_heads, group, table_width;
   int32_t pack, toks, packs;   // heads and tokens of a query tile, query tiles that a token's group takes
-  int32_t slot_rows, grid;
+  int32_t slot_rows, grid, items;
   float scale_log2;
   __nv_bfloat16* o;
   int64_t o_stride;
