@@ -231,6 +231,16 @@ __device__ __forceinline__ QTile q_tile(const TreeArgs& a, const Doc& d, int32_t
   return QTile{d.row0 + first, min(a.toks, d.T - first), kvh * a.group + (qt - block * a.packs) * a.pack};
 }
 
+// x / n, in 32 bits where they hold it.
+__device__ __forceinline__ int64_t quotient(int64_t x, int32_t n) {
+  return x < ((int64_t)1 << 32) ? (int64_t)((uint32_t)x / (uint32_t)n) : x / n;
+}
+// floor(total c / grid) for c <= grid < 2^16
+__device__ __forceinline__ int64_t share_of(int64_t total, int64_t c, int64_t grid) {
+  const int64_t q = quotient(total, (int32_t)grid), r = total - q * grid;
+  return q * c + (uint32_t)(r * c) / (uint32_t)grid;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeArgs a) {
@@ -269,12 +279,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     dev::fence_barrier_init();
   }
 
+  if (a.pack * a.toks < kRows) {
+    // rows of a query tile that no load fills (their scores must not be anything: see attn_fwd_tc.cu)
+    for (uint32_t i = threadIdx.x * 16u; i < 2 * kTileBytes; i += kThreads * 16u)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sbase + kSmemQ + i), "r"(0u) : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    dev::tmem_alloc(dev::smem_u32(tmem_slot), kTmemCols);
+    dev::tmem_relinquish();
+  }
+
   // What this block does.  Every thread adds up a run of sequences.
   const int per = (a.n_docs + kThreads - 1) / kThreads;
   const int b0 = min((int)threadIdx.x * per, a.n_docs), b1 = min(b0 + per, a.n_docs);
-  int64_t* const sums = reinterpret_cast<int64_t*>(smem + kSmemMl);
   // the sum over all threads, and over those before this one
-  const auto scan = [&](int64_t mine, int64_t* before) {
+  const auto scan = [&](int64_t* sums, int64_t mine, int64_t* before) {
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -292,88 +312,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return total;
   };
+  int64_t* const sums = reinterpret_cast<int64_t*>(smem + kSmemMl);
   Doc d0 = {};  // (the thread's sequence, where there is one to a thread)
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b) {
     d0 = doc_of(a, b);
     mine += (int64_t)d0.tiles * d0.units * a.kv_heads;
   }
-  int64_t before, total = scan(mine, &before);
+  int64_t before, total = scan(sums, mine, &before);
   int32_t most = 0;  // tiles of a piece; 0: ranges
   if (a.items <= (int)gridDim.x) {
-    // (so there is a thread to every sequence) candidates: a lane each, from the even share on
-    int32_t* const pieces_of = reinterpret_cast<int32_t*>(smem + kSmemMl);  // [kWarps][32]
-    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
-    const int32_t cand = (int32_t)min(share + lane, (int64_t)INT32_MAX / 2);
-    int32_t n = 0;
-    for (int b = warp; b < a.n_docs; b += kWarps) {
-      const Doc d = doc_of(a, b);
-      n += d.units * a.kv_heads * ((d.tiles + cand - 1) / cand);
-    }
-    __syncthreads();
-    pieces_of[warp * 32 + lane] = n;
-    __syncthreads();
-    n = 0;
+    // (so there is a thread to every sequence)  The even share and up to three tiles more, which are quicker
+    // than a second piece: the pieces of each, 16 bits for each (at most twice the blocks at the even share)
+    const int32_t share = (int32_t)min((total + gridDim.x - 1) / gridDim.x, (int64_t)INT32_MAX / 2);
+    int64_t pieces = 0;
+    if (b0 < b1)
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) n += pieces_of[w * 32 + lane];
-    const unsigned fits = __ballot_sync(0xffffffffu, n <= (int)gridDim.x);
-    __syncthreads();
-    // (three tiles more than the even share are quicker than a second piece)
-    if (fits != 0 && __ffs(fits) - 1 <= 3) most = (int32_t)share + __ffs(fits) - 1;
-    if (most > 0) total = scan(b0 < b1 ? (int64_t)d0.units * a.kv_heads * ((d0.tiles + most - 1) / most) : 0, &before);
+      for (int i = 0; i < 4; ++i)
+        pieces |= (int64_t)(d0.units * a.kv_heads * (((uint32_t)d0.tiles + share + i - 1) / (uint32_t)(share + i))) << 16 * i;
+    int64_t first;
+    pieces = scan(sums + kWarps, pieces, &first);
+#pragma unroll
+    for (int i = 3; i >= 0; --i)
+      if (((pieces >> 16 * i) & 0xffff) <= (int64_t)gridDim.x) {
+        most = share + i;
+        before = (first >> 16 * i) & 0xffff;
+      }
+    if (most > 0) total = (pieces >> 16 * (most - share)) & 0xffff;
   }
   const int64_t grid = min((int64_t)gridDim.x, total);
   const int64_t c = blockIdx.x;
-  if (c >= grid) return;  // (the whole block)
-  const int64_t s0 = most > 0 ? c : total * c / grid, s1 = most > 0 ? c + 1 : total * (c + 1) / grid;
-  if (s1 - s0 > INT32_MAX) {  // (hours of work: lengths of 2^31 in thousands of sequences)
-    if (threadIdx.x == 0) dev::report_bad_page(a.err);
-    return;
-  }
+  const int64_t s0 = most > 0 ? c : share_of(total, c, grid), s1 = most > 0 ? c + 1 : share_of(total, c + 1, grid);
+  const bool work = c < grid && s1 - s0 <= INT32_MAX;
+  if (c < grid && !work && threadIdx.x == 0) dev::report_bad_page(a.err);  // (hours of work: thousands of lengths of 2^31)
   for (int b = b0; b < b1; ++b) {
     const Doc d = per == 1 ? d0 : doc_of(a, b);
-    const int32_t cut = most > 0 ? (d.tiles + most - 1) / most : d.tiles;  // pieces (steps) of an item
+    const int32_t cut = most > 0 ? (int32_t)(((uint32_t)d.tiles + most - 1) / (uint32_t)most) : d.tiles;  // pieces (steps) of an item
     const int64_t n = (int64_t)cut * d.units * a.kv_heads;
     if (s0 >= before && s0 < before + n) {
-      const int32_t item = (int32_t)((s0 - before) / cut), i = (int32_t)((s0 - before) - (int64_t)item * cut);
+      const int32_t item = (int32_t)quotient(s0 - before, cut), i = (int32_t)((s0 - before) - (int64_t)item * cut);
+      // (in pieces: tiles < 2^24, i < 2^8)
+      const uint32_t lo = (uint32_t)d.tiles * (uint32_t)i / (uint32_t)cut, hi = (uint32_t)d.tiles * (uint32_t)(i + 1) / (uint32_t)cut;
       start.b = b;
       start.item = item;
-      start.lo = most > 0 ? (int32_t)((int64_t)d.tiles * i / cut) : i;
-      start.steps = most > 0 ? (int32_t)((int64_t)d.tiles * (i + 1) / cut) - (int32_t)((int64_t)d.tiles * i / cut) : (int32_t)(s1 - s0);
+      start.lo = most > 0 ? (int32_t)lo : i;
+      start.steps = most > 0 ? (int32_t)(hi - lo) : (int32_t)(s1 - s0);
       start.row0 = d.row0;
       start.row1 = d.row0 + d.T;
       start.given = d.ctx;
     }
     if (c == 0) {  // for the join
-      a.prefix[b] = before;
-      if (b + 1 == a.n_docs) {
-        a.prefix[b + 1] = total;
-        a.prefix[b + 2] = most;
-      }
+      a.share[b] = TreeShare{before, cut, d.tiles};
+      if (b + 1 == a.n_docs) a.share[b + 1] = TreeShare{total, most, 0};
       if (__ldg(a.ctx_lens + b) != d.ctx) dev::report_bad_page(a.err);
     }
     before += n;
-  }
-  if (a.pack * a.toks < kRows) {
-    // rows of a query tile that no load fills (their scores must not be anything: see attn_fwd_tc.cu)
-    for (uint32_t i = threadIdx.x * 16u; i < 2 * kTileBytes; i += kThreads * 16u)
-      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sbase + kSmemQ + i), "r"(0u) : "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  }
-  if (warp == kMmaWarp) {
-    dev::tmem_alloc(dev::smem_u32(tmem_slot), kTmemCols);
-    dev::tmem_relinquish();
   }
   dev::tc_fence_before();
   __syncthreads();
   dev::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int32_t steps = start.steps;
+  const int32_t steps = work ? start.steps : 0;
   Walk walk;
-  walk.begin(a, start);
+  if (work) walk.begin(a, start);
   Piece p;
 
-  if (warp == kKWarp || warp == kVWarp) {
+  if (!work) {
+    // (more blocks than steps)
+  } else if (warp == kKWarp || warp == kVWarp) {
     // ------------------------------------------------------ K or V tiles ----
     const bool is_v = warp == kVWarp;
     const CUtensorMap* const tm = is_v ? &tm_v : &tm_k;
@@ -801,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // M) l_c over the pieces in the order of their keys.  A warp a row, four dims a lane;
 // the eight warps of a block share out the pieces of rows that have many.
 constexpr int kJoinWarps = 8;
-constexpr int kAtOnce = 8;     // partial rows that a warp has on their way
+constexpr int kAtOnce = 4;     // partial rows that a warp has on their way
 constexpr int kAlone = 16;     // pieces that a warp combines by itself
 
 struct Acc {
@@ -817,43 +823,39 @@ __device__ __forceinline__ void add(Acc& x, float m, float l, const float4& o) {
   x.m = top;
 }
 
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_tree_join_kernel(const __grid_constant__ TreeArgs a) {
+// (Six blocks an SM: with two, at 107 registers, 7,168 rows took three rounds of its chain of loads.)
+__global__ void __launch_bounds__(32 * kJoinWarps, 6) attn_tree_join_kernel(const __grid_constant__ TreeArgs a) {
   __shared__ Acc shared[kJoinWarps][32];
-  __shared__ int4 info[kJoinWarps];  // of each warp's row: first block, pieces, row of the partial tile, its first slot
+  __shared__ int3 info[kJoinWarps];  // of each warp's row: its first slot, the blocks' second one, pieces
+  __shared__ int32_t rows[kJoinWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t id = (int64_t)blockIdx.x * kJoinWarps + warp;
-  const bool real = id < a.S * a.H;
-  const int32_t tok = real ? (int32_t)(id / a.H) : 0, head = real ? (int32_t)(id - (int64_t)tok * a.H) : 0;
-  const int32_t b = __ldg(a.doc_of + tok), row0 = __ldg(a.cu + b), T = __ldg(a.cu + b + 1) - row0;
-  const int32_t kvh = head / a.group, in = head - kvh * a.group, pk = in / a.pack, blk = (tok - row0) / a.toks;
-  const int32_t qt = blk * a.packs + pk;
-  const Doc d = make_doc(a, row0, row0 + T, __ldg(a.ctx_lens + b));
-  const int32_t item = kvh * d.units + qt / 2;
-  const int32_t row = (qt & 1) * kRows + ((tok - row0) - blk * a.toks) * a.pack + (in - pk * a.pack);
+  const uint32_t n_rows = (uint32_t)a.S * (uint32_t)a.H;  // (below 2^31)
+  const uint32_t id = min(blockIdx.x * kJoinWarps + warp, n_rows - 1);
+  const int32_t tok = (int32_t)(id / (uint32_t)a.H), head = (int32_t)(id - (uint32_t)tok * (uint32_t)a.H);
+  const TreeRow r = a.rows[tok];
+  const int32_t kvh = head / a.group, in = head - kvh * a.group, pk = in / a.pack, qt = r.qtile + pk;
+  const int32_t item = kvh * r.units + qt / 2, row = (qt & 1) * kRows + r.in_tile * a.pack + (in - pk * a.pack);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the forward is complete and its writes visible
-  const int64_t total = a.prefix[a.n_docs], first = a.prefix[b];
-  const int32_t most = (int32_t)a.prefix[a.n_docs + 1];
+  const TreeShare x = a.share[r.doc], all = a.share[a.n_docs];
   int32_t c0, n, slot0;  // the blocks that share the item
-  if (most > 0) {
-    n = (d.tiles + most - 1) / most;
-    c0 = (int32_t)(first + (int64_t)item * n);
+  if (all.cut > 0) {     // pieces
+    n = x.cut;
+    c0 = (int32_t)x.first + item * n;
     slot0 = 2 * c0;
   } else {
-    const int64_t grid = min((int64_t)a.grid, total);
-    const int64_t s0 = first + (int64_t)item * d.tiles, s1 = s0 + d.tiles;  // the item's steps
+    const int64_t grid = min((int64_t)a.grid, all.first), s0 = x.first + (int64_t)item * x.tiles, s1 = s0 + x.tiles;  // the item's steps
     // block c has steps [total c / grid, total (c + 1) / grid)
-    c0 = (int32_t)(((s0 + 1) * grid - 1) / total);
-    n = (int32_t)((s1 * grid - 1) / total) - c0 + 1;
+    c0 = (int32_t)(((s0 + 1) * grid - 1) / all.first);
+    n = (int32_t)((s1 * grid - 1) / all.first) - c0 + 1;
     // the piece of the first block is its last one unless the item begins there; the others' is their first
-    slot0 = 2 * c0 + (total * c0 / grid < s0 ? 1 : 0);
+    slot0 = 2 * c0 + (share_of(all.first, c0, grid) < s0 ? 1 : 0);
   }
-  if (!real || n == 1) n = 0;  // (a block's whole items are written by it)
-  if (lane == 0) info[warp] = make_int4(c0, n, row, slot0);
-  __syncthreads();
-  const auto part_row = [&](const int4& x, int32_t i) {
-    return (int64_t)(i == 0 ? x.w : 2 * (x.x + i)) * a.slot_rows + x.z;
-  };
-  const auto run = [&](const int4& x, int32_t i0, int32_t i1, Acc& acc) {
+  if (n == 1 || blockIdx.x * kJoinWarps + warp >= n_rows) n = 0;  // (a block's whole items are written by it)
+  if (lane == 0) {
+    info[warp] = make_int3(slot0, 2 * (c0 + 1), n);
+    rows[warp] = row;
+  }
+  const auto run = [&](const int3& y, int32_t row_in, int32_t i0, int32_t i1, Acc& acc) {
 #pragma unroll 1
     for (int32_t i = i0; i < i1; i += kAtOnce) {
       float2 ml[kAtOnce];
@@ -861,17 +863,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_tree_join_kernel(const _
 #pragma unroll
       for (int e = 0; e < kAtOnce; ++e)
         if (i + e < i1) {
-          const int64_t r = part_row(x, i + e);
-          ml[e] = a.part_ml[r];
-          o[e] = reinterpret_cast<const float4*>(a.part_o + r * kHeadDim)[lane];
+          const int64_t at = (int64_t)(i + e == 0 ? y.x : y.y + 2 * (i + e - 1)) * a.slot_rows + row_in;
+          ml[e] = a.part_ml[at];
+          o[e] = reinterpret_cast<const float4*>(a.part_o + at * kHeadDim)[lane];
         }
 #pragma unroll
       for (int e = 0; e < kAtOnce; ++e)
         if (i + e < i1) add(acc, ml[e].x, ml[e].y, o[e]);
     }
   };
-  const auto finish = [&](const Acc& acc, int64_t row_id) {
-    const int32_t t = (int32_t)(row_id / a.H), h = (int32_t)(row_id - (int64_t)t * a.H);
+  const auto finish = [&](const Acc& acc, uint32_t row_id) {
+    const int32_t t = (int32_t)(row_id / (uint32_t)a.H), h = (int32_t)(row_id - (uint32_t)t * (uint32_t)a.H);
     const float inv = acc.l == 0.f ? 0.f : 1.f / acc.l;
     __nv_bfloat16* const dst = a.o + (int64_t)t * a.o_stride + (int64_t)h * kHeadDim + 4 * lane;
     *reinterpret_cast<uint2*>(dst) =
@@ -880,21 +882,23 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_tree_join_kernel(const _
   };
   if (n > 0 && n <= kAlone) {
     Acc acc = nothing();
-    run(info[warp], 0, n, acc);
+    run(make_int3(slot0, 2 * (c0 + 1), n), row, 0, n, acc);
     finish(acc, id);
   }
+  if (__syncthreads_or(n > kAlone) == 0) return;
 #pragma unroll 1
   for (int w = 0; w < kJoinWarps; ++w) {
-    const int4 x = info[w];
-    if (x.y <= kAlone) continue;  // (the same for the whole block)
+    const int3 y = info[w];
+    if (y.z <= kAlone) continue;  // (the same for the whole block)
     Acc acc = nothing();
-    run(x, x.y * warp / kJoinWarps, x.y * (warp + 1) / kJoinWarps, acc);
+    run(y, rows[w], y.z * warp / kJoinWarps, y.z * (warp + 1) / kJoinWarps, acc);
     shared[warp][lane] = acc;
     __syncthreads();
     if (warp == w) {
-      Acc all = nothing();
-      for (int i = 0; i < kJoinWarps; ++i) add(all, shared[i][lane].m, shared[i][lane].l, shared[i][lane].o);
-      finish(all, (int64_t)blockIdx.x * kJoinWarps + w);
+      Acc sum = nothing();
+#pragma unroll 1
+      for (int i = 0; i < kJoinWarps; ++i) add(sum, shared[i][lane].m, shared[i][lane].l, shared[i][lane].o);
+      finish(sum, blockIdx.x * kJoinWarps + w);
     }
     __syncthreads();
   }
@@ -954,7 +958,7 @@ cudaError_t launch_attn_tree(const TreeArgs& args, const void* q, int64_t q_stri
   attn_tree_kernel<<<(unsigned)a.grid, kThreads, kSmemAlloc, stream>>>(mq, mk, mv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int64_t blocks = (a.S * a.H + kJoinWarps - 1) / kJoinWarps;
+  const int64_t blocks = (a.S * a.H + kJoinWarps - 1) / kJoinWarps;  // (rows below 2^31)
   e = launch_dependent(attn_tree_join_kernel, (unsigned)blocks, 32u * kJoinWarps, stream, a);
   if (e != cudaSuccess) *why = "the join launch failed";
   return e;

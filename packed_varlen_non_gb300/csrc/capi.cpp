@@ -96,8 +96,8 @@ void free_walk(WalkPlan* w) {
 }
 
 void free_tree(TreePlan* t) {
-  if (t->d_doc) cudaFree(t->d_doc);
-  if (t->d_prefix) cudaFree(t->d_prefix);
+  if (t->d_rows) cudaFree(t->d_rows);
+  if (t->d_share) cudaFree(t->d_share);
   if (t->d_part_o) cudaFree(t->d_part_o);
   if (t->d_part_ml) cudaFree(t->d_part_ml);
   *t = TreePlan();
@@ -1340,19 +1340,22 @@ h3attn_status h3attn_plan_set_tree(h3attn_plan_t plan, int32_t num_kv_heads, voi
   t.grid = plan->num_sms;
   const size_t rows = (size_t)2 * t.grid * t.slot_rows;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  std::vector<int32_t> doc;
+  std::vector<TreeRow> token;
   try {
-    doc.resize((size_t)plan->S);
+    token.resize((size_t)plan->S);
   } catch (const std::exception&) {
     return fail(H3ATTN_ENOMEM, "host allocation failed for the tree workspace");
   }
-  for (int32_t d = 0; d < plan->n_docs; ++d)
-    std::fill(doc.begin() + plan->cu_host[d], doc.begin() + plan->cu_host[d + 1], d);
-  e = cudaMalloc(&t.d_doc, doc.size() * sizeof(int32_t));
-  if (e == cudaSuccess) e = cudaMalloc(&t.d_prefix, ((size_t)plan->n_docs + 2) * sizeof(int64_t));
+  const int32_t packs = group / t.pack;
+  for (int32_t d = 0; d < plan->n_docs; ++d) {
+    const int32_t b = plan->cu_host[d], T = plan->cu_host[d + 1] - b, tiles = packs * ((T + t.toks - 1) / t.toks);
+    for (int32_t i = 0; i < T; ++i) token[(size_t)(b + i)] = TreeRow{d, i / t.toks * packs, i % t.toks, (tiles + 1) / 2};
+  }
+  e = cudaMalloc(&t.d_rows, token.size() * sizeof(TreeRow));
+  if (e == cudaSuccess) e = cudaMalloc(&t.d_share, ((size_t)plan->n_docs + 1) * sizeof(TreeShare));
   if (e == cudaSuccess) e = cudaMalloc(&t.d_part_o, rows * kHeadDim * sizeof(float));
   if (e == cudaSuccess) e = cudaMalloc(&t.d_part_ml, rows * sizeof(float2));
-  if (e == cudaSuccess) e = cudaMemcpyAsync(t.d_doc, doc.data(), doc.size() * sizeof(int32_t), cudaMemcpyHostToDevice, st);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(t.d_rows, token.data(), token.size() * sizeof(TreeRow), cudaMemcpyHostToDevice, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) {
     free_tree(&t);
@@ -1401,7 +1404,7 @@ h3attn_status h3attn_forward_tree(h3attn_plan_t plan, const void* q, int64_t q_r
   if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
   TreeArgs a{};
   a.cu = plan->d_cu;
-  a.doc_of = tp.d_doc;
+  a.rows = tp.d_rows;
   a.ctx_lens = ctx_lens;
   a.page_table = page_table;
   a.tree_mask = tree_mask;
@@ -1421,7 +1424,7 @@ h3attn_status h3attn_forward_tree(h3attn_plan_t plan, const void* q, int64_t q_r
   a.o = static_cast<__nv_bfloat16*>(o);
   a.o_stride = o_row_stride;
   a.lse = lse_out;
-  a.prefix = tp.d_prefix;
+  a.share = tp.d_share;
   a.part_o = tp.d_part_o;
   a.part_ml = tp.d_part_ml;
   a.err = plan->d_err;

@@ -225,6 +225,18 @@ struct PrefixPlan {
   int32_t len = 0;
 };
 
+// What the tree forward's join has to know: of a token (fixed by the plan), its
+// document, the first query tile of its heads, its place in it and the document's
+// units of two tiles; and of a sequence (left by the forward), the steps or pieces before it, pieces (steps) of
+// an item, key tiles; behind the last one all of them, and the tiles of a piece (0: ranges of steps).
+struct TreeRow {
+  int32_t doc, qtile, in_tile, units;
+};
+struct TreeShare {
+  int64_t first;
+  int32_t cut, tiles;
+};
+
 // Workspace of the tree forward.
 struct TreePlan {
   bool set = false;
@@ -235,8 +247,8 @@ struct TreePlan {
   int32_t grid = 0;                    // blocks, two partial slots each
   int32_t items = 0;                   // (sequence, key head, up to two query tiles)
   int32_t max_len = 0;                 // drafts of the longest document
-  int32_t* d_doc = nullptr;            // [S] document of a token
-  int64_t* d_prefix = nullptr;         // [n_docs + 2] steps or pieces before each sequence, tiles of a piece (the forward's)
+  TreeRow* d_rows = nullptr;           // [S]
+  TreeShare* d_share = nullptr;        // [n_docs + 1]
   float* d_part_o = nullptr;           // [2 grid slot_rows, 128]
   float2* d_part_ml = nullptr;         // [2 grid slot_rows]
 };
@@ -468,7 +480,7 @@ cudaError_t launch_forward_causal(const ForwardArgs& a, const WalkArgs& w, cudaS
 // Trees of drafts over a paged cache (attn_tree.cu).
 struct TreeArgs {
   const int32_t* cu;           // [n_docs + 1]
-  const int32_t* doc_of;       // [S]
+  const TreeRow* rows;         // [S]
   const int32_t* ctx_lens;     // [n_docs]
   const int32_t* page_table;   // [n_docs, table_width]
   const uint64_t* tree_mask;   // [S] or null
@@ -480,7 +492,7 @@ struct TreeArgs {
   __nv_bfloat16* o;
   int64_t o_stride;
   float* lse;
-  int64_t* prefix;
+  TreeShare* share;
   float* part_o;
   float2* part_ml;
   uint32_t* err;
