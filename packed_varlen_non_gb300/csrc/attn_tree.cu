@@ -155,7 +155,7 @@ __device__ __forceinline__ Doc doc_of(const TreeArgs& a, int b) {
 
 // A block's share of one item: key tiles [lo, hi).
 struct Piece {
-  int32_t b, kvh, lo, hi;
+  int32_t b, item, kvh, lo, hi;
   int32_t qt, n_qt;    // its first query tile, and how many (1 or 2)
   bool whole;
   bool first;          // of the block's pieces
@@ -163,12 +163,13 @@ struct Piece {
 };
 // Where a block's range begins (found once, for all roles).
 struct Start {
-  int32_t b, steps, item, lo, row0, row1, given;
+  int32_t b, steps, item, lo, row0, row1, given, item0;
 };
 // Walks a block's range piece by piece; every role runs its own.
 struct Walk {
   int32_t b, item, lo;
   int32_t left, at;
+  int32_t item0;        // of all sequences' items, this one's first
   bool first;
   Doc d;
   int32_t row2, given;  // of the next sequence: its end and length, on their way while this one runs
@@ -183,6 +184,7 @@ struct Walk {
     at = 0;
     first = true;
     item = s.item;
+    item0 = s.item0;
     lo = s.lo;
     ahead(a);
     d = make_doc(a, s.row0, s.row1, s.given);
@@ -192,11 +194,13 @@ struct Walk {
     if (left <= 0) return false;
     if (item == a.kv_heads * d.units) {
       item = 0;
+      item0 += a.kv_heads * d.units;
       ++b;
       d = make_doc(a, d.row0 + d.T, row2, given);
       ahead(a);
     }
     p->b = b;
+    p->item = item0 + item;
     p->kvh = item / d.units;
     p->qt = 2 * (item - p->kvh * d.units);
     p->n_qt = min(2, d.qtiles - p->qt);
@@ -360,12 +364,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       start.row0 = d.row0;
       start.row1 = d.row0 + d.T;
       start.given = d.ctx;
+      start.item0 = __ldg(a.item0 + b);
     }
-    if (c == 0) {  // for the join
-      a.share[b] = TreeShare{before, cut, d.tiles};
-      if (b + 1 == a.n_docs) a.share[b + 1] = TreeShare{total, most, 0};
-      if (__ldg(a.ctx_lens + b) != d.ctx) dev::report_bad_page(a.err);
-    }
+    if (c == 0 && __ldg(a.ctx_lens + b) != d.ctx) dev::report_bad_page(a.err);
     before += n;
   }
   dev::tc_fence_before();
@@ -446,6 +447,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t n = 0;
       bool ok = true;
       while (ok && walk.next(a, &p)) {
+        if (p.lo == 0) {
+          // an item that begins here: its first slot and its pieces, for the join
+          const int32_t tiles = walk.d.tiles;
+          int64_t n = 1;
+          if (most > 0)
+            n = ((uint32_t)tiles + most - 1) / (uint32_t)most;
+          else if (p.hi < tiles)  // block c has steps [total c / grid, total (c + 1) / grid)
+            n = ((s0 + p.at + tiles) * grid - 1) / total - c + 1;
+          a.joins[p.item] = make_int2((int32_t)(2 * c) + (p.first ? 0 : 1), (int32_t)n);
+        }
         for (int i = 0; ok && i < p.n_qt; ++i) {
           ok = dev::mbar_wait(bars.q_empty(n & 1), ((n >> 1) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
           if (!ok) break;
@@ -823,84 +834,106 @@ __device__ __forceinline__ void add(Acc& x, float m, float l, const float4& o) {
   x.m = top;
 }
 
-// (Six blocks an SM: with two, at 107 registers, 7,168 rows took three rounds of its chain of loads.)
-__global__ void __launch_bounds__(32 * kJoinWarps, 6) attn_tree_join_kernel(const __grid_constant__ TreeArgs a) {
-  __shared__ Acc shared[kJoinWarps][32];
-  __shared__ int3 info[kJoinWarps];  // of each warp's row: its first slot, the blocks' second one, pieces
-  __shared__ int32_t rows[kJoinWarps];
+// kN rows a warp: their loads go out together.  Many rows have few pieces each (32,768 of
+// two: 23 us with a row a warp, 9 with four).  One: the row's pieces go out together, and
+// the eight warps of a block share out the pieces of a row that has many.
+template <int kN>
+__global__ void __launch_bounds__(32 * kJoinWarps, kN == 1 ? 6 : 3) attn_tree_join_kernel(const __grid_constant__ TreeArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t n_rows = (uint32_t)a.S * (uint32_t)a.H;  // (below 2^31)
-  const uint32_t id = min(blockIdx.x * kJoinWarps + warp, n_rows - 1);
-  const int32_t tok = (int32_t)(id / (uint32_t)a.H), head = (int32_t)(id - (uint32_t)tok * (uint32_t)a.H);
-  const TreeRow r = a.rows[tok];
-  const int32_t kvh = head / a.group, in = head - kvh * a.group, pk = in / a.pack, qt = r.qtile + pk;
-  const int32_t item = kvh * r.units + qt / 2, row = (qt & 1) * kRows + r.in_tile * a.pack + (in - pk * a.pack);
+  const uint32_t id = (blockIdx.x * kJoinWarps + warp) * kN;
+  uint32_t tok[kN], head[kN];
+  int32_t item[kN], row[kN], n[kN], slot[kN];  // row of the item's partial slots; pieces (0: nothing to join), first slot
+#pragma unroll
+  for (int e = 0; e < kN; ++e) {
+    tok[e] = min(id + e, n_rows - 1) / (uint32_t)a.H;
+    head[e] = min(id + e, n_rows - 1) - tok[e] * (uint32_t)a.H;
+    const TreeRow r = a.rows[tok[e]];
+    const uint32_t kvh = head[e] / (uint32_t)a.group, in = head[e] - kvh * a.group, pk = in / (uint32_t)a.pack, qt = r.qtile + pk;
+    item[e] = r.item0 + (int32_t)(kvh * r.units + qt / 2);
+    row[e] = (int32_t)((qt & 1) * kRows + r.in_tile * a.pack + (in - pk * a.pack));
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the forward is complete and its writes visible
-  const TreeShare x = a.share[r.doc], all = a.share[a.n_docs];
-  int32_t c0, n, slot0;  // the blocks that share the item
-  if (all.cut > 0) {     // pieces
-    n = x.cut;
-    c0 = (int32_t)x.first + item * n;
-    slot0 = 2 * c0;
-  } else {
-    const int64_t grid = min((int64_t)a.grid, all.first), s0 = x.first + (int64_t)item * x.tiles, s1 = s0 + x.tiles;  // the item's steps
-    // block c has steps [total c / grid, total (c + 1) / grid)
-    c0 = (int32_t)(((s0 + 1) * grid - 1) / all.first);
-    n = (int32_t)((s1 * grid - 1) / all.first) - c0 + 1;
-    // the piece of the first block is its last one unless the item begins there; the others' is their first
-    slot0 = 2 * c0 + (share_of(all.first, c0, grid) < s0 ? 1 : 0);
-  }
-  if (n == 1 || blockIdx.x * kJoinWarps + warp >= n_rows) n = 0;  // (a block's whole items are written by it)
-  if (lane == 0) {
-    info[warp] = make_int3(slot0, 2 * (c0 + 1), n);
-    rows[warp] = row;
-  }
-  const auto run = [&](const int3& y, int32_t row_in, int32_t i0, int32_t i1, Acc& acc) {
-#pragma unroll 1
-    for (int32_t i = i0; i < i1; i += kAtOnce) {
-      float2 ml[kAtOnce];
-      float4 o[kAtOnce];
 #pragma unroll
-      for (int e = 0; e < kAtOnce; ++e)
-        if (i + e < i1) {
-          const int64_t at = (int64_t)(i + e == 0 ? y.x : y.y + 2 * (i + e - 1)) * a.slot_rows + row_in;
-          ml[e] = a.part_ml[at];
-          o[e] = reinterpret_cast<const float4*>(a.part_o + at * kHeadDim)[lane];
-        }
-#pragma unroll
-      for (int e = 0; e < kAtOnce; ++e)
-        if (i + e < i1) add(acc, ml[e].x, ml[e].y, o[e]);
-    }
+  for (int e = 0; e < kN; ++e) {
+    const int2 x = a.joins[item[e]];
+    slot[e] = x.x;
+    n[e] = x.y == 1 || id + e >= n_rows ? 0 : x.y;  // (a block's whole items are written by it)
+  }
+  // piece i of a row: its block's first slot, but for the first one
+  const auto load = [&](int32_t first, int32_t in_slot, int32_t i, float2* ml, float4* o) {
+    const int64_t at = (int64_t)(i == 0 ? first : (first | 1) - 1 + 2 * i) * a.slot_rows + in_slot;
+    *ml = a.part_ml[at];
+    *o = reinterpret_cast<const float4*>(a.part_o + at * kHeadDim)[lane];
   };
-  const auto finish = [&](const Acc& acc, uint32_t row_id) {
-    const int32_t t = (int32_t)(row_id / (uint32_t)a.H), h = (int32_t)(row_id - (uint32_t)t * (uint32_t)a.H);
+  const auto finish = [&](const Acc& acc, uint32_t t, uint32_t h) {
     const float inv = acc.l == 0.f ? 0.f : 1.f / acc.l;
     __nv_bfloat16* const dst = a.o + (int64_t)t * a.o_stride + (int64_t)h * kHeadDim + 4 * lane;
     *reinterpret_cast<uint2*>(dst) =
         make_uint2(dev::pack_bf16x2(acc.o.x * inv, acc.o.y * inv), dev::pack_bf16x2(acc.o.z * inv, acc.o.w * inv));
     if (lane == 0 && a.lse != nullptr) a.lse[(int64_t)h * a.S + t] = (acc.m + __log2f(acc.l)) * 0.6931471805599453f;
   };
-  if (n > 0 && n <= kAlone) {
-    Acc acc = nothing();
-    run(make_int3(slot0, 2 * (c0 + 1), n), row, 0, n, acc);
-    finish(acc, id);
-  }
-  if (__syncthreads_or(n > kAlone) == 0) return;
-#pragma unroll 1
-  for (int w = 0; w < kJoinWarps; ++w) {
-    const int3 y = info[w];
-    if (y.z <= kAlone) continue;  // (the same for the whole block)
-    Acc acc = nothing();
-    run(y, rows[w], y.z * warp / kJoinWarps, y.z * (warp + 1) / kJoinWarps, acc);
-    shared[warp][lane] = acc;
-    __syncthreads();
-    if (warp == w) {
-      Acc sum = nothing();
-#pragma unroll 1
-      for (int i = 0; i < kJoinWarps; ++i) add(sum, shared[i][lane].m, shared[i][lane].l, shared[i][lane].o);
-      finish(sum, blockIdx.x * kJoinWarps + w);
+  if constexpr (kN > 1) {
+    Acc acc[kN];
+    int32_t most = 0;
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      acc[e] = nothing();
+      most = max(most, n[e]);
     }
-    __syncthreads();
+#pragma unroll 1
+    for (int32_t i = 0; i < most; ++i) {
+      float2 ml[kN];
+      float4 o[kN];
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        if (i < n[e]) load(slot[e], row[e], i, &ml[e], &o[e]);
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        if (i < n[e]) add(acc[e], ml[e].x, ml[e].y, o[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < kN; ++e)
+      if (n[e] > 0) finish(acc[e], tok[e], head[e]);
+  } else {
+    __shared__ Acc shared[kJoinWarps][32];
+    __shared__ int3 of[kJoinWarps];
+    if (lane == 0) of[warp] = make_int3(slot[0], row[0], n[0]);
+    const auto run = [&](int32_t first, int32_t in_slot, int32_t i0, int32_t i1, Acc& acc) {
+#pragma unroll 1
+      for (int32_t i = i0; i < i1; i += kAtOnce) {
+        float2 ml[kAtOnce];
+        float4 o[kAtOnce];
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e)
+          if (i + e < i1) load(first, in_slot, i + e, &ml[e], &o[e]);
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e)
+          if (i + e < i1) add(acc, ml[e].x, ml[e].y, o[e]);
+      }
+    };
+    if (n[0] > 0 && n[0] <= kAlone) {
+      Acc acc = nothing();
+      run(slot[0], row[0], 0, n[0], acc);
+      finish(acc, tok[0], head[0]);
+    }
+    if (__syncthreads_or(n[0] > kAlone) == 0) return;
+#pragma unroll 1
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const int3 y = of[w];
+      if (y.z <= kAlone) continue;  // (the same for the whole block)
+      Acc acc = nothing();
+      run(y.x, y.y, y.z * warp / kJoinWarps, y.z * (warp + 1) / kJoinWarps, acc);
+      shared[warp][lane] = acc;
+      __syncthreads();
+      if (warp == w) {
+        Acc sum = nothing();
+#pragma unroll 1
+        for (int i = 0; i < kJoinWarps; ++i) add(sum, shared[i][lane].m, shared[i][lane].l, shared[i][lane].o);
+        finish(sum, tok[0], head[0]);
+      }
+      __syncthreads();
+    }
   }
 }
 
@@ -958,8 +991,12 @@ cudaError_t launch_attn_tree(const TreeArgs& args, const void* q, int64_t q_stri
   attn_tree_kernel<<<(unsigned)a.grid, kThreads, kSmemAlloc, stream>>>(mq, mk, mv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int64_t blocks = (a.S * a.H + kJoinWarps - 1) / kJoinWarps;  // (rows below 2^31)
-  e = launch_dependent(attn_tree_join_kernel, (unsigned)blocks, 32u * kJoinWarps, stream, a);
+  // a row a warp while that is one wave, six blocks an SM (rows are below 2^31)
+  const int64_t rows = a.S * a.H, one = (rows + kJoinWarps - 1) / kJoinWarps;
+  if (one <= (int64_t)6 * a.grid)
+    e = launch_dependent(attn_tree_join_kernel<1>, (unsigned)one, 32u * kJoinWarps, stream, a);
+  else
+    e = launch_dependent(attn_tree_join_kernel<4>, (unsigned)((one + 3) / 4), 32u * kJoinWarps, stream, a);
   if (e != cudaSuccess) *why = "the join launch failed";
   return e;
 }

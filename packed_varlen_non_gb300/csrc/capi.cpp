@@ -97,7 +97,8 @@ void free_walk(WalkPlan* w) {
 
 void free_tree(TreePlan* t) {
   if (t->d_rows) cudaFree(t->d_rows);
-  if (t->d_share) cudaFree(t->d_share);
+  if (t->d_item0) cudaFree(t->d_item0);
+  if (t->d_joins) cudaFree(t->d_joins);
   if (t->d_part_o) cudaFree(t->d_part_o);
   if (t->d_part_ml) cudaFree(t->d_part_ml);
   *t = TreePlan();
@@ -1341,20 +1342,26 @@ h3attn_status h3attn_plan_set_tree(h3attn_plan_t plan, int32_t num_kv_heads, voi
   const size_t rows = (size_t)2 * t.grid * t.slot_rows;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   std::vector<TreeRow> token;
+  std::vector<int32_t> item0;
   try {
     token.resize((size_t)plan->S);
+    item0.resize((size_t)plan->n_docs);
   } catch (const std::exception&) {
     return fail(H3ATTN_ENOMEM, "host allocation failed for the tree workspace");
   }
   const int32_t packs = group / t.pack;
-  for (int32_t d = 0; d < plan->n_docs; ++d) {
-    const int32_t b = plan->cu_host[d], T = plan->cu_host[d + 1] - b, tiles = packs * ((T + t.toks - 1) / t.toks);
-    for (int32_t i = 0; i < T; ++i) token[(size_t)(b + i)] = TreeRow{d, i / t.toks * packs, i % t.toks, (tiles + 1) / 2};
+  for (int32_t d = 0, item = 0; d < plan->n_docs; ++d) {
+    const int32_t b = plan->cu_host[d], T = plan->cu_host[d + 1] - b, units = (packs * ((T + t.toks - 1) / t.toks) + 1) / 2;
+    for (int32_t i = 0; i < T; ++i) token[(size_t)(b + i)] = TreeRow{item, i / t.toks * packs, i % t.toks, units};
+    item0[d] = item;
+    item += units * num_kv_heads;
   }
   e = cudaMalloc(&t.d_rows, token.size() * sizeof(TreeRow));
-  if (e == cudaSuccess) e = cudaMalloc(&t.d_share, ((size_t)plan->n_docs + 1) * sizeof(TreeShare));
+  if (e == cudaSuccess) e = cudaMalloc(&t.d_item0, item0.size() * sizeof(int32_t));
+  if (e == cudaSuccess) e = cudaMalloc(&t.d_joins, (size_t)t.items * sizeof(int2));
   if (e == cudaSuccess) e = cudaMalloc(&t.d_part_o, rows * kHeadDim * sizeof(float));
   if (e == cudaSuccess) e = cudaMalloc(&t.d_part_ml, rows * sizeof(float2));
+  if (e == cudaSuccess) e = cudaMemcpyAsync(t.d_item0, item0.data(), item0.size() * sizeof(int32_t), cudaMemcpyHostToDevice, st);
   if (e == cudaSuccess) e = cudaMemcpyAsync(t.d_rows, token.data(), token.size() * sizeof(TreeRow), cudaMemcpyHostToDevice, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) {
@@ -1424,7 +1431,8 @@ h3attn_status h3attn_forward_tree(h3attn_plan_t plan, const void* q, int64_t q_r
   a.o = static_cast<__nv_bfloat16*>(o);
   a.o_stride = o_row_stride;
   a.lse = lse_out;
-  a.share = tp.d_share;
+  a.item0 = tp.d_item0;
+  a.joins = tp.d_joins;
   a.part_o = tp.d_part_o;
   a.part_ml = tp.d_part_ml;
   a.err = plan->d_err;

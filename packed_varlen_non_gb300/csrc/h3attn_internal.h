@@ -225,16 +225,10 @@ struct PrefixPlan {
   int32_t len = 0;
 };
 
-// What the tree forward's join has to know: of a token (fixed by the plan), its
-// document, the first query tile of its heads, its place in it and the document's
-// units of two tiles; and of a sequence (left by the forward), the steps or pieces before it, pieces (steps) of
-// an item, key tiles; behind the last one all of them, and the tiles of a piece (0: ranges of steps).
+// What the tree forward's join has to know of a token: its document's first item,
+// the first query tile of its heads, its place in it, the document's units of two tiles.
 struct TreeRow {
-  int32_t doc, qtile, in_tile, units;
-};
-struct TreeShare {
-  int64_t first;
-  int32_t cut, tiles;
+  int32_t item0, qtile, in_tile, units;
 };
 
 // Workspace of the tree forward.
@@ -248,7 +242,8 @@ struct TreePlan {
   int32_t items = 0;                   // (sequence, key head, up to two query tiles)
   int32_t max_len = 0;                 // drafts of the longest document
   TreeRow* d_rows = nullptr;           // [S]
-  TreeShare* d_share = nullptr;        // [n_docs + 1]
+  int32_t* d_item0 = nullptr;          // [n_docs] first item of a document
+  int2* d_joins = nullptr;             // [items] first partial slot and pieces (the forward's)
   float* d_part_o = nullptr;           // [2 grid slot_rows, 128]
   float2* d_part_ml = nullptr;         // [2 grid slot_rows]
 };
@@ -492,7 +487,8 @@ struct TreeArgs {
   __nv_bfloat16* o;
   int64_t o_stride;
   float* lse;
-  TreeShare* share;
+  const int32_t* item0;        // [n_docs]
+  int2* joins;                 // [items]
   float* part_o;
   float2* part_ml;
   uint32_t* err;

@@ -609,38 +609,48 @@ class Cache:
                               k.stride(2))
 
 
-def _heads(x, name, n, device):
+def _bad_rows(x, name, n, device):
+    return ValueError(f"{name} must be a bfloat16 tensor [{n}, heads, 128] with contiguous heads on GPU {device} "
+                      f"(got {tuple(x.shape)}, strides {x.stride()}, {x.dtype}, {x.device})")
+
+
+def _heads(x, name, n, device, bf16):
     """(pointer, row stride, heads) of bf16 rows [n, heads, 128] on the device."""
-    if (x.dtype is not _torch().bfloat16 or x.dim() != 3 or x.shape[2] != 128 or x.shape[0] != n or x.stride(2) != 1
-            or (x.stride(1) != 128 and x.shape[1] != 1) or x.get_device() != device):
-        raise ValueError(f"{name} must be a bfloat16 tensor [{n}, heads, 128] with contiguous heads on GPU {device} "
-                         f"(got {tuple(x.shape)}, strides {x.stride()}, {x.dtype}, {x.device})")
-    heads = x.shape[1]
-    return x.data_ptr(), (x.stride(0) if n > 1 else 128 * heads), heads
+    if x.dtype is bf16 and x.dim() == 3 and x.get_device() == device:
+        rows, heads, dims = x.shape
+        step, head, dim = x.stride()
+        if rows == n and dims == 128 and dim == 1 and (head == 128 or heads == 1):
+            return x.data_ptr(), (step if n > 1 else 128 * heads), heads
+    raise _bad_rows(x, name, n, device)
 
 
 def _ints(x, name, shape, device):
     """The pointer of a contiguous int32 tensor of the given shape on the device."""
-    if x.dtype is not _torch().int32 or tuple(x.shape) != tuple(shape) or not x.is_contiguous() or x.get_device() != device:
+    if x.shape != shape or x.dtype is not _torch().int32 or x.get_device() != device or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on GPU {device} "
                          f"(got {tuple(x.shape)}, {x.dtype}, {x.device})")
     return x.data_ptr()
 
 
 def _positions(rope, positions, n, device):
-    if rope.n_axes == 1 and positions.dim() == 1:
-        return _ints(positions, "positions", (n,), device)
-    return _ints(positions, "positions", (rope.n_axes, n), device)
+    axes = rope.n_axes
+    return _ints(positions, "positions", (n,) if axes == 1 and positions.dim() == 1 else (axes, n), device)
 
 
-def _call_on(device, fn, name, *args, stream):
+_NO_ROWS = (None, 0, 0)
+
+
+def _call_on(device, fn, name, stream, *args):
     """The call without a plan, with the tensors' device current."""
-    torch = _torch()
-    if torch.cuda.current_device() == device:
-        _check(fn(*args, _stream(stream, device)), name)
+    c = _torch()._C
+    at = c._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    if c._cuda_getDevice() == device:
+        status = fn(*args, at)
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream, device)), name)
+        with _torch().cuda.device(device):
+            status = fn(*args, at)
+    if status != H3ATTN_OK:
+        _check(status, name)
 
 
 def h3attn_rotary(rope, positions, q_in, q_out, k_in=None, k_out=None, inverse: bool = False, stream=None):
@@ -649,14 +659,18 @@ def h3attn_rotary(rope, positions, q_in, q_out, k_in=None, k_out=None, inverse: 
     first = q_in if q_in is not None else k_in
     if first is None or (q_in is None) != (q_out is None) or (k_in is None) != (k_out is None):
         raise ValueError("an input and its output go together, and one pair is needed")
-    n, device = first.shape[0], first.get_device()
-    none = (None, 0, 0)
-    q = [_heads(x, name, n, device) if x is not None else none for x, name in ((q_in, "q_in"), (q_out, "q_out"))]
-    k = [_heads(x, name, n, device) if x is not None else none for x, name in ((k_in, "k_in"), (k_out, "k_out"))]
-    if q[0][2] != q[1][2] or k[0][2] != k[1][2]:
+    n, device, bf16 = first.shape[0], first.get_device(), _torch().bfloat16
+    q, q_step, heads = q2, q2_step, heads2 = k, k_step, kv = k2, k2_step, kv2 = _NO_ROWS
+    if q_in is not None:
+        q, q_step, heads = _heads(q_in, "q_in", n, device, bf16)
+        q2, q2_step, heads2 = _heads(q_out, "q_out", n, device, bf16)
+    if k_in is not None:
+        k, k_step, kv = _heads(k_in, "k_in", n, device, bf16)
+        k2, k2_step, kv2 = _heads(k_out, "k_out", n, device, bf16)
+    if heads != heads2 or kv != kv2:
         raise ValueError("an input and its output must have the same heads")
-    _call_on(device, load().h3attn_rotary, "h3attn_rotary", rope, _positions(rope, positions, n, device), n, q[0][0], q[0][1],
-             q[1][0], q[1][1], q[0][2], k[0][0], k[0][1], k[1][0], k[1][1], k[0][2], int(bool(inverse)), stream=stream)
+    _call_on(device, load().h3attn_rotary, "h3attn_rotary", stream, rope, _positions(rope, positions, n, device), n, q, q_step, q2,
+             q2_step, heads, k, k_step, k2, k2_step, kv, 1 if inverse else 0)
 
 
 def h3attn_rotary_store(rope, positions, q_in, q_out, k_in, v_in, cache: Cache, slots, stream=None):
@@ -664,24 +678,28 @@ def h3attn_rotary_store(rope, positions, q_in, q_out, k_in, v_in, cache: Cache, 
     int32 [n]."""
     if (q_in is None) != (q_out is None):
         raise ValueError("q_in and q_out go together")
-    n, device = k_in.shape[0], cache.device
-    none = (None, 0, 0)
-    q = [_heads(x, name, n, device) if x is not None else none for x, name in ((q_in, "q_in"), (q_out, "q_out"))]
-    k, v = _heads(k_in, "k_in", n, device), _heads(v_in, "v_in", n, device)
-    if q[0][2] != q[1][2] or k[2] != cache.num_kv_heads or v[2] != cache.num_kv_heads:
+    n, device, bf16 = k_in.shape[0], cache.device, _torch().bfloat16
+    q, q_step, heads = q2, q2_step, heads2 = _NO_ROWS
+    if q_in is not None:
+        q, q_step, heads = _heads(q_in, "q_in", n, device, bf16)
+        q2, q2_step, heads2 = _heads(q_out, "q_out", n, device, bf16)
+    k, k_step, kv = _heads(k_in, "k_in", n, device, bf16)
+    v, v_step, kv2 = _heads(v_in, "v_in", n, device, bf16)
+    if heads != heads2 or kv != cache.num_kv_heads or kv2 != kv:
         raise ValueError("q_in and q_out must have the same heads, and k_in and v_in the cache's")
-    if k[1] != v[1]:
-        raise ValueError(f"k_in and v_in must share one row stride (got {k[1]}, {v[1]})")
-    _call_on(device, load().h3attn_rotary_store, "h3attn_rotary_store", rope, _positions(rope, positions, n, device), n, q[0][0],
-             q[0][1], q[1][0], q[1][1], q[0][2], k[0], v[0], k[1], cache.c, _ints(slots, "slots", (n,), device), stream=stream)
+    if k_step != v_step:
+        raise ValueError(f"k_in and v_in must share one row stride (got {k_step}, {v_step})")
+    _call_on(device, load().h3attn_rotary_store, "h3attn_rotary_store", stream, rope, _positions(rope, positions, n, device), n, q,
+             q_step, q2, q2_step, heads, k, v, k_step, cache.c, _ints(slots, "slots", (n,), device))
 
 
 def h3attn_cache_move(cache: Cache, src, dst, stream=None):
     """Copies rows of the cache to other slots: src, dst int32 [groups, width]."""
     if src.dim() != 2:
         raise ValueError(f"src and dst are [groups, width] (got {tuple(src.shape)})")
-    _call_on(cache.device, load().h3attn_cache_move, "h3attn_cache_move", cache.c, _ints(src, "src", src.shape, cache.device),
-             _ints(dst, "dst", src.shape, cache.device), src.shape[0], src.shape[1], stream=stream)
+    shape = src.shape
+    _call_on(cache.device, load().h3attn_cache_move, "h3attn_cache_move", stream, cache.c, _ints(src, "src", shape, cache.device),
+             _ints(dst, "dst", shape, cache.device), shape[0], shape[1])
 
 
 _tree_docs: dict = {}  # documents of the plans that have a tree workspace
