@@ -476,58 +476,121 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // -------------------------------------------------------- MMA issuer ----
     // (the whole warp; one lane polls, one elected lane issues)
-    uint32_t n_q = 0, p_it[2] = {0, 0};
+    // The operands of an MMA are uniform registers: ring positions are counted up from constants here, and what
+    // a piece says goes through uniform(), so that no value has to be moved there before each instruction.
+    const auto uniform = [](uint32_t x) { return __reduce_or_sync(0xffffffffu, x); };
+    const uint32_t tm = uniform(tmem);
+    uint32_t n_q = 0, p_it[2] = {0, 0};  // query tiles; key tiles of each stream whose P was awaited
+    // slot and phase of the next K and V to come: K of tile t is entry 0, 1, 3, 5, .., V 2, 4, 6, .. (the last one
+    // of the block comes an entry early)
+    uint32_t k_slot = 0, k_ph = 0, v_slot = 2, v_ph = 0;
+    bool k_first = true;
+    int32_t tile = 0;                    // of the block
+    const int32_t all = (int32_t)uniform((uint32_t)steps);
     bool ok = true, issued = false;
     const auto wait = [&](uint32_t bar, uint32_t parity) {
-      bool good = true;
-      if (lane == 0) good = dev::mbar_wait(bar, parity, abort_flag, a.err, kTimeoutNs);
-      ok = ok && __shfl_sync(0xffffffffu, good, 0);
+      bool good = false;
+#pragma unroll 1
+      for (int i = 0; i < 256 && !good; ++i) good = __all_sync(0xffffffffu, dev::mbar_test_wait(bar, parity));
+      if (!good) {
+        if (lane == 0) good = dev::mbar_wait(bar, parity, abort_flag, a.err, kTimeoutNs);
+        ok = __shfl_sync(0xffffffffu, good, 0) && ok;
+      }
       dev::tc_fence_after();
-      return ok;
     };
-    const auto landed = [&](uint32_t entry) { return wait(bars.full(entry % kSlots), (entry / kSlots) & 1); };
-    const auto slot_of = [&](uint32_t entry) { return sbase + kSmemKV + (entry % kSlots) * kTileBytes; };
-    const auto release = [&](uint32_t entry) { commit_elect(bars.empty(entry % kSlots)); };
-    const auto qk = [&](int s, uint32_t q, uint32_t entry) {
-      issue_qk(tmem + s * 128, sbase + kSmemQ + q * kTileBytes, slot_of(entry));
+    const auto next_k = [&] {
+      const uint32_t step = k_first ? 1 : 2;
+      k_first = false;
+      k_slot += step;
+      if (k_slot >= kSlots) {
+        k_slot -= kSlots;
+        k_ph ^= 1;
+      }
+    };
+    const auto next_v = [&] {
+      ++tile;
+      v_slot += tile + 1 < all ? 2 : 1;
+      if (v_slot >= kSlots) {
+        v_slot -= kSlots;
+        v_ph ^= 1;
+      }
+    };
+    if (all == 1) v_slot = 1;
+    const auto qk = [&](int s, uint32_t q, uint32_t slot) {
+      issue_qk(tm + s * 128, sbase + kSmemQ + q * kTileBytes, sbase + kSmemKV + slot * kTileBytes);
       commit_elect(bars.s_ready(s));
-      issued = true;
     };
-    const auto pv = [&](int s, uint32_t entry, bool acc) { issue_pv(tmem + 256 + s * 128, tmem + s * 128, slot_of(entry), acc); };
+    // Asking a barrier takes 200 cycles, a wait that finds it complete too.  So each is asked before the
+    // products of the step before it are issued, and waited for only if it was not complete then.
+    const auto ask = [&](uint32_t bar, uint32_t parity) { return dev::mbar_test_wait(bar, parity); };
+    const auto need = [&](bool asked, uint32_t bar, uint32_t parity) {
+      if (!__all_sync(0xffffffffu, asked)) wait(bar, parity);
+    };
+    bool p_asked = false, v_asked = false, k_asked = false;
+    const auto ask_p = [&](int s, uint32_t it) { p_asked = ask(bars.p_ready(s), it & 1); };
+    // asks for the V and K behind the next ones (more_v, more_k: whether they are this block's, this piece's)
+    const auto ask_tiles = [&](bool more_v, bool more_k) {
+      uint32_t slot = v_slot + 2, ph = v_ph;
+      if (slot >= kSlots) slot -= kSlots, ph ^= 1;
+      v_asked = ask(bars.full(slot), ph) && more_v;
+      slot = k_slot + 2, ph = k_ph;
+      if (slot >= kSlots) slot -= kSlots, ph ^= 1;
+      k_asked = ask(bars.full(slot), ph) && more_k;
+    };
+    // stream s's key tile: its PV, then the next tile's QK into the same columns, or the piece's end; `then`
+    // asks for what comes next
+    const auto step = [&](int s, bool acc, bool more, uint32_t q, auto then) {
+      need(p_asked, bars.p_ready(s), p_it[s] & 1);
+      if (!ok) return;
+      dev::tc_fence_after();
+      then();
+      issue_pv(tm + 256 + s * 128, tm + s * 128, sbase + kSmemKV + v_slot * kTileBytes, acc);
+      if (more)
+        qk(s, q, k_slot);
+      else
+        commit_elect(bars.pv_done(s));
+      ++p_it[s];
+    };
     while (ok && walk.next(a, &p)) {
-      const int32_t n = p.hi - p.lo, t0 = p.at;
+      const int32_t n = (int32_t)uniform((uint32_t)(p.hi - p.lo));
+      const bool two = uniform((uint32_t)p.n_qt) == 2;
+      p_asked = v_asked = k_asked = false;
       const uint32_t q0 = n_q & 1, q1 = q0 ^ 1;
       wait(bars.q_full(q0), (n_q >> 1) & 1);
       ++n_q;
-      if (p.n_qt == 2) {
+      if (two) {
         // stream s: query tile s over every key tile
         wait(bars.q_full(q1), (n_q >> 1) & 1);
         ++n_q;
-        if (!landed(k_entry(t0))) break;
-        qk(0, q0, k_entry(t0));
-        qk(1, q1, k_entry(t0));
-        release(k_entry(t0));
+        wait(bars.full(k_slot), k_ph);
+        if (!ok) break;
+        issued = true;
+        qk(0, q0, k_slot);
+        qk(1, q1, k_slot);
+        commit_elect(bars.empty(k_slot));
+        next_k();
         if (n == 1) {
           commit_elect(bars.q_empty(q0));
           commit_elect(bars.q_empty(q1));
         }
+#pragma unroll 1
         for (int32_t j = 0; ok && j < n; ++j) {
-          const uint32_t ve = v_entry(t0 + j, steps), ke = k_entry(t0 + j + 1);
           const bool more = j + 1 < n;
-          // (the tiles before P: they landed long ago, and asking takes 200 cycles each, which P would wait for)
-          if (!landed(ve) || (more && !landed(ke))) break;
-          for (int s = 0; s < 2; ++s) {
-            if (!wait(bars.p_ready(s), p_it[s] & 1)) break;
-            ++p_it[s];
-            pv(s, ve, j > 0);
-            if (more)
-              qk(s, s == 0 ? q0 : q1, ke);
-            else
-              commit_elect(bars.pv_done(s));
-          }
+          need(v_asked, bars.full(v_slot), v_ph);
+          if (more) need(k_asked, bars.full(k_slot), k_ph);
           if (!ok) break;
-          release(ve);
-          if (more) release(ke);
+          step(0, j > 0, more, q0, [&] { ask_p(1, p_it[1]); });
+          if (ok) step(1, j > 0, more, q1, [&] {
+            ask_p(0, p_it[0]);
+            ask_tiles(tile + 2 < all, j + 2 < n);
+          });
+          if (!ok) break;
+          commit_elect(bars.empty(v_slot));
+          next_v();
+          if (more) {
+            commit_elect(bars.empty(k_slot));
+            next_k();
+          }
           if (j + 2 == n) {
             commit_elect(bars.q_empty(q0));
             commit_elect(bars.q_empty(q1));
@@ -535,33 +598,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         // stream s: the one query tile over the key tiles s, s + 2, ...
-        for (int s = 0; s < 2 && s < n; ++s) {
-          if (!landed(k_entry(t0 + s))) break;
-          qk(s, q0, k_entry(t0 + s));
-          release(k_entry(t0 + s));
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (s >= n) break;
+          wait(bars.full(k_slot), k_ph);
+          if (!ok) break;
+          issued = true;
+          qk(s, q0, k_slot);
+          commit_elect(bars.empty(k_slot));
+          next_k();
         }
         if (!ok) break;
         if (n <= 2) commit_elect(bars.q_empty(q0));
-        for (int32_t j = 0; ok && j < n; ++j) {
-          const int s = j & 1;
-          const uint32_t ve = v_entry(t0 + j, steps);
-          const uint32_t ke = k_entry(t0 + j + 2);
-          if (!landed(ve) || (j + 2 < n && !landed(ke))) break;
-          if (!wait(bars.p_ready(s), (s == 0 ? p_it[0] : p_it[1]) & 1)) break;
-          if (s == 0)
-            ++p_it[0];
-          else
-            ++p_it[1];
-          pv(s, ve, j >= 2);
-          release(ve);
-          if (j + 2 < n) {
-            qk(s, q0, ke);
-            release(ke);
+#pragma unroll 1
+        for (int32_t j0 = 0; ok && j0 < n; j0 += 2)
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const int32_t j = j0 + s;
+            if (!ok || j >= n) break;
+            const bool more = j + 2 < n;
+            need(v_asked, bars.full(v_slot), v_ph);
+            if (more) need(k_asked, bars.full(k_slot), k_ph);
+            if (!ok) break;
+            step(s, j0 > 0, more, q0, [&] {
+              ask_p(s ^ 1, p_it[s ^ 1]);
+              ask_tiles(tile + 2 < all, j + 3 < n);
+            });
+            if (!ok) break;
+            commit_elect(bars.empty(v_slot));
+            next_v();
+            if (more) {
+              commit_elect(bars.empty(k_slot));
+              next_k();
+            }
             if (j + 3 == n) commit_elect(bars.q_empty(q0));
-          } else {
-            commit_elect(bars.pv_done(s));
           }
-        }
       }
     }
     if (!ok && issued) {
