@@ -384,17 +384,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------ K or V tiles ----
     const bool is_v = warp == kVWarp;
     const CUtensorMap* const tm = is_v ? &tm_v : &tm_k;
-    // (tiles that other units read too should stay in L2)
-    const uint64_t pol_once = dev::policy_evict_first(), pol_shared = dev::policy_evict_last();
+    // (kept in L2 instead, tiles that a second unit reads too gain nothing and push the partial rows out of it:
+    // 282 against 276 us for 64 drafts over 20,423 tokens)
+    const uint64_t pol = dev::policy_evict_first();
     const int n_box = kRows / a.box;             // boxes of a tile, a lane each
     const int32_t tiles_at_once = 32 / n_box;
     const uint32_t dst0 = sbase + kSmemKV + lane * (uint32_t)a.box * 128u;
+    const int32_t row_step = kRows % a.page_size;
     int32_t loaded = 0;                          // tiles
-    bool ok = true;
+    uint32_t slot = is_v ? v_entry(0, steps) : 0, ph = 1;  // of the next entry, and its empty barrier's phase
+    bool ok = true, free = true;                 // (the first five entries' slots are)
     while (ok && walk.next(a, &p)) {
       const int32_t total = walk.d.ctx + walk.d.T;
       const int32_t* table = a.page_table + (int64_t)p.b * a.table_width;
-      const uint64_t pol = walk.d.units > 1 ? pol_shared : pol_once;
       // Page numbers a window of 32 boxes at a time, a lane each, the next window on
       // its way (a lookup a tile, though asked for a tile ahead, paced the loads: 1,000 cycles a tile).
       const auto pages_from = [&](int32_t t) {
@@ -402,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return key < total ? __ldg(table + (uint32_t)key / (uint32_t)a.page_size) : 0;
       };
       int32_t pages = pages_from(p.lo), pages_next = pages_from(p.lo + tiles_at_once), window = p.lo;
+      int32_t row = (int32_t)(((uint32_t)p.lo * kRows + lane * (uint32_t)a.box) % (uint32_t)a.page_size);  // in its page
       for (int32_t t = p.lo; t < p.hi; ++t) {
         if (t - window == tiles_at_once) {
           window = t;
@@ -415,21 +418,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           dev::report_bad_page(a.err);
           page = a.n_pages;  // outside the tensor map: zeros
         }
-        const int32_t row = (int32_t)(key % (uint32_t)a.page_size);
         const int32_t c1 = a.heads_first ? p.kvh : row, c2 = a.heads_first ? row : p.kvh;
         const int32_t boxes = min(n_box, (total - t * kRows + a.box - 1) / a.box);
-        const uint32_t entry = is_v ? v_entry(loaded, steps) : k_entry(loaded), slot = entry % kSlots, bar = bars.full(slot);
-        bool good = true;
-        if (lane == 0) {
-          good = dev::mbar_wait(bars.empty(slot), ((entry / kSlots) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
-          if (good) dev::mbar_arrive_expect_tx(bar, (uint32_t)boxes * (uint32_t)a.box * 256u);
+        const uint32_t bar = bars.full(slot);
+        if (!__all_sync(0xffffffffu, free)) {
+          bool good = true;
+          if (lane == 0) good = dev::mbar_wait(bars.empty(slot), ph, abort_flag, a.err, kTimeoutNs);
+          ok = __shfl_sync(0xffffffffu, good, 0);
+          if (!ok) break;
         }
-        ok = __shfl_sync(0xffffffffu, good, 0);
-        if (!ok) break;
+        if (lane == 0) dev::mbar_arrive_expect_tx(bar, (uint32_t)boxes * (uint32_t)a.box * 256u);
+        __syncwarp();
+        const uint32_t dst = dst0 + slot * kTileBytes;
+        // the next entry: asked for while this one's copies are issued
+        slot += is_v ? (loaded + 2 < steps ? 2 : 1) : (loaded == 0 ? 1 : 2);
+        if (slot >= kSlots) {
+          slot -= kSlots;
+          ph ^= 1;
+        }
+        free = dev::mbar_test_wait(bars.empty(slot), ph);
         if (in) {
-          dev::tma_load_4d(dst0 + slot * kTileBytes, tm, bar, 0, c1, c2, page, pol);
-          dev::tma_load_4d(dst0 + slot * kTileBytes + kHalfBytes, tm, bar, 64, c1, c2, page, pol);
+          dev::tma_load_4d(dst, tm, bar, 0, c1, c2, page, pol);
+          dev::tma_load_4d(dst + kHalfBytes, tm, bar, 64, c1, c2, page, pol);
         }
+        row += row_step;
+        if (row >= a.page_size) row -= a.page_size;
         ++loaded;
       }
     }
@@ -661,18 +674,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       else
         ++done[1];
     };
-    while (ok && walk.next(a, &p)) {
+    // What a piece is to this row; looked up before the epilogue of the one before it, so that the
+    // drafts that the row sees are here when its first tile is (of a short context the only one).
+    struct Mine {
+      QTile q;
+      uint64_t mask;
+      int32_t ctx, T;
+      bool valid, busy;  // the row is one; any of this warp's is
+    };
+    const auto look = [&](const Piece& y) {
+      Mine x;
+      x.q = q_tile(a, walk.d, y.kvh, y.qt + (y.n_qt == 2 ? st : 0));
+      x.ctx = walk.d.ctx;
+      x.T = walk.d.T;
+      x.valid = tok_in < (uint32_t)x.q.n_tok;  // (rows past pack * toks have larger tok_in)
+      x.busy = (int32_t)(lane_base * a.recip >> 16) < x.q.n_tok;
+      x.mask = 0;
+      if (x.valid)
+        x.mask = a.tree_mask != nullptr
+                     ? __ldg(reinterpret_cast<const unsigned long long*>(a.tree_mask) + x.q.tok0 + (int32_t)tok_in)
+                     : ~0ull >> (63 - (x.q.tok0 + (int32_t)tok_in - walk.d.row0));
+      return x;
+    };
+    Piece p_next;
+    bool go = walk.next(a, &p_next);
+    Mine next{};
+    if (go) next = look(p_next);
+    while (ok && go) {
+      p = p_next;
+      const Mine me = next;
       const bool two = p.n_qt == 2;
-      const Doc& d = walk.d;
-      const QTile q = q_tile(a, d, p.kvh, p.qt + (two ? st : 0));
-      const bool valid = tok_in < (uint32_t)q.n_tok;  // (rows past pack * toks have larger tok_in)
-      const bool busy = (int32_t)(lane_base * a.recip >> 16) < q.n_tok;  // any row of this warp
+      const QTile& q = me.q;
+      const bool valid = me.valid, busy = me.busy;
       const int32_t n = p.hi - p.lo;
-      // the drafts that this row sees (of use in the last tiles only: nothing waits for it here)
-      uint64_t mask = 0;
-      if (valid)
-        mask = a.tree_mask != nullptr ? __ldg(reinterpret_cast<const unsigned long long*>(a.tree_mask) + q.tok0 + (int32_t)tok_in)
-                                      : ~0ull >> (63 - (q.tok0 + (int32_t)tok_in - d.row0));
       float m = kLowest, l = 0.f;
       for (int32_t j = two ? 0 : st; ok && j < n; j += two ? 1 : 2) {
         const int32_t t = p.lo + j;
@@ -681,11 +715,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();  // lanes leave the wait separately; the TMEM loads are warp-collective
         dev::tc_fence_after();
         if (busy) {
-          const int32_t base = t * kRows - d.ctx;  // draft of the tile's first key (negative: context)
+          const int32_t base = t * kRows - me.ctx;  // draft of the tile's first key (negative: context)
           const bool edge = base + kRows > 0;
           uint64_t see[2] = {~0ull, 0};            // keys that the row sees
           if (edge) {
-            const uint64_t word = mask & (~0ull >> (64 - d.T));
+            const uint64_t word = me.mask & (~0ull >> (64 - me.T));
             if (base >= 0) {
               see[0] = word >> base;               // (the last tile begins before the last draft: below 64)
             } else if (base > -64) {
@@ -772,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         dev::tc_fence_before();
         // the tile ends early: zero the rows of V behind it, a quarter a warp (two query
         // tiles: the first one's warps, whose PV goes first)
-        const int32_t rem = d.ctx + d.T - t * kRows;
+        const int32_t rem = me.ctx + me.T - t * kRows;
         if (rem < kRows && (!two || st == 0)) {
           const uint32_t ve = v_entry(p.at + j, steps);
           ok = dev::mbar_wait(bars.full(ve % kSlots), (ve / kSlots) & 1, abort_flag, a.err, kTimeoutNs) && ok;
@@ -795,6 +829,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         finished(0);
         if (n > 1) finished(1);
       }
+      go = walk.next(a, &p_next);
+      if (go) next = look(p_next);
       float w0 = 1.f, w1 = 0.f;
       const bool both = !two && n > 1;
       if (!two) {
@@ -890,7 +926,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the eight warps of a block share out the pieces of rows that have many.
 constexpr int kJoinWarps = 8;
 constexpr int kAtOnce = 4;     // partial rows that a warp has on their way
-constexpr int kAlone = 16;     // pieces that a warp combines by itself
 
 struct Acc {
   float m, l;
@@ -905,14 +940,15 @@ __device__ __forceinline__ void add(Acc& x, float m, float l, const float4& o) {
   x.m = top;
 }
 
-// kN rows a warp: their loads go out together.  Many rows have few pieces each (32,768 of
-// two: 23 us with a row a warp, 9 with four).  One: the row's pieces go out together, and
-// the eight warps of a block share out the pieces of a row that has many.
-template <int kN>
-__global__ void __launch_bounds__(32 * kJoinWarps, kN == 1 ? 6 : 3) attn_tree_join_kernel(const __grid_constant__ TreeArgs a) {
+// kRowsOf rows a warp, whose loads go out together: many rows have few pieces each
+// (32,768 of two: 23 us with a row a warp, 16 with four).  0: one row a block, whose warps
+// share out its pieces (32 rows of 18: 30 us less than a row after the other).
+template <int kRowsOf>
+__global__ void __launch_bounds__(32 * kJoinWarps, kRowsOf > 1 ? 3 : 6) attn_tree_join_kernel(const __grid_constant__ TreeArgs a) {
+  constexpr int kN = kRowsOf > 1 ? kRowsOf : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t n_rows = (uint32_t)a.S * (uint32_t)a.H;  // (below 2^31)
-  const uint32_t id = (blockIdx.x * kJoinWarps + warp) * kN;
+  const uint32_t id = kRowsOf == 0 ? blockIdx.x : (blockIdx.x * kJoinWarps + warp) * kN;
   uint32_t tok[kN], head[kN];
   int32_t item[kN], row[kN], n[kN], slot[kN];  // row of the item's partial slots; pieces (0: nothing to join), first slot
 #pragma unroll
@@ -967,44 +1003,33 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kN == 1 ? 6 : 3) attn_tree_jo
     for (int e = 0; e < kN; ++e)
       if (n[e] > 0) finish(acc[e], tok[e], head[e]);
   } else {
-    __shared__ Acc shared[kJoinWarps][32];
-    __shared__ int3 of[kJoinWarps];
-    if (lane == 0) of[warp] = make_int3(slot[0], row[0], n[0]);
-    const auto run = [&](int32_t first, int32_t in_slot, int32_t i0, int32_t i1, Acc& acc) {
+    const auto run = [&](int32_t i0, int32_t i1, Acc& acc) {
 #pragma unroll 1
       for (int32_t i = i0; i < i1; i += kAtOnce) {
         float2 ml[kAtOnce];
         float4 o[kAtOnce];
 #pragma unroll
         for (int e = 0; e < kAtOnce; ++e)
-          if (i + e < i1) load(first, in_slot, i + e, &ml[e], &o[e]);
+          if (i + e < i1) load(slot[0], row[0], i + e, &ml[e], &o[e]);
 #pragma unroll
         for (int e = 0; e < kAtOnce; ++e)
           if (i + e < i1) add(acc, ml[e].x, ml[e].y, o[e]);
       }
     };
-    if (n[0] > 0 && n[0] <= kAlone) {
-      Acc acc = nothing();
-      run(slot[0], row[0], 0, n[0], acc);
-      finish(acc, tok[0], head[0]);
-    }
-    if (__syncthreads_or(n[0] > kAlone) == 0) return;
-#pragma unroll 1
-    for (int w = 0; w < kJoinWarps; ++w) {
-      const int3 y = of[w];
-      if (y.z <= kAlone) continue;  // (the same for the whole block)
-      Acc acc = nothing();
-      run(y.x, y.y, y.z * warp / kJoinWarps, y.z * (warp + 1) / kJoinWarps, acc);
-      shared[warp][lane] = acc;
+    if (n[0] == 0) return;  // (the same for the whole block where it has one row)
+    Acc acc = nothing();
+    if constexpr (kRowsOf == 1) {
+      run(0, n[0], acc);
+    } else {
+      __shared__ Acc shared[kJoinWarps][32];
+      run(n[0] * warp / kJoinWarps, n[0] * (warp + 1) / kJoinWarps, acc);
+      if (warp > 0) shared[warp][lane] = acc;
       __syncthreads();
-      if (warp == w) {
-        Acc sum = nothing();
+      if (warp > 0) return;
 #pragma unroll 1
-        for (int i = 0; i < kJoinWarps; ++i) add(sum, shared[i][lane].m, shared[i][lane].l, shared[i][lane].o);
-        finish(sum, tok[0], head[0]);
-      }
-      __syncthreads();
+      for (int i = 1; i < kJoinWarps; ++i) add(acc, shared[i][lane].m, shared[i][lane].l, shared[i][lane].o);
     }
+    finish(acc, tok[0], head[0]);
   }
 }
 
@@ -1062,9 +1087,12 @@ cudaError_t launch_attn_tree(const TreeArgs& args, const void* q, int64_t q_stri
   attn_tree_kernel<<<(unsigned)a.grid, kThreads, kSmemAlloc, stream>>>(mq, mk, mv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // a row a warp while that is one wave, six blocks an SM (rows are below 2^31)
+  // Few rows may have many pieces each (up to one a block of the grid): a block a row.  Else a row a
+  // warp while that is one wave, six blocks an SM.  (Rows are below 2^31.)
   const int64_t rows = a.S * a.H, one = (rows + kJoinWarps - 1) / kJoinWarps;
-  if (one <= (int64_t)6 * a.grid)
+  if (rows <= (int64_t)12 * a.grid)
+    e = launch_dependent(attn_tree_join_kernel<0>, (unsigned)rows, 32u * kJoinWarps, stream, a);
+  else if (one <= (int64_t)6 * a.grid)
     e = launch_dependent(attn_tree_join_kernel<1>, (unsigned)one, 32u * kJoinWarps, stream, a);
   else
     e = launch_dependent(attn_tree_join_kernel<4>, (unsigned)((one + 3) / 4), 32u * kJoinWarps, stream, a);
