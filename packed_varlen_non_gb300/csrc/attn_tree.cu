@@ -17,6 +17,9 @@
 //     blocks enough; otherwise the steps of all items, in order, are cut into equal ranges,
 //     one per SM, which may hold pieces of several items.  (A second piece costs a block
 //     4 us: its first loads and its first step wait for the first one's end.)
+//     Where there are more items than SMs and each is a single query tile (kTwo), a range
+//     goes to each of a block's two streams, whose piece boundaries then fall into the middle of
+//     the other one's pieces.
 //     Lengths are on the device, so each block adds them up itself and finds its
 //     part; no list is built on the host and one captured graph serves growing
 //     sequences.
@@ -62,8 +65,8 @@ constexpr uint32_t kSmemBar = kSmemKV + kSlots * kTileBytes;
 constexpr int kNumBars = 4 + 2 * kSlots + 6 + 2;
 constexpr uint32_t kSmemMl = kSmemBar + kNumBars * 8;   // float2 [2][128]
 constexpr uint32_t kSmemMisc = kSmemMl + 2 * 128 * 8;
-constexpr uint32_t kSlack = 512;                        // the base is 1 KB aligned (declared so; checked in the kernel)
-constexpr size_t kSmemAlloc = kSmemMisc + 64 + kSlack;
+constexpr uint32_t kSlack = 496;                        // the base is 1 KB aligned (declared so; checked in the kernel)
+constexpr size_t kSmemAlloc = kSmemMisc + 96 + kSlack;
 static_assert(kSmemAlloc <= 227 * 1024, "shared memory per CTA");
 static_assert(kSmemMl % 16 == 0, "alignment");
 constexpr uint32_t kTmemCols = 512;                 // S0 S1 O0 O1, 128 columns each
@@ -245,6 +248,8 @@ __device__ __forceinline__ int64_t share_of(int64_t total, int64_t c, int64_t gr
   return q * c + (uint32_t)(r * c) / (uint32_t)grid;
 }
 
+// kTwo: the two streams have ranges of their own (below, "more items than SMs").
+template <bool kTwo>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeArgs a) {
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Bars bars{sbase + kSmemBar};
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kSmemMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kSmemMisc + 4);
-  volatile Start& start = *reinterpret_cast<volatile Start*>(smem + kSmemMisc + 8);
+  volatile Start* const starts = reinterpret_cast<volatile Start*>(smem + kSmemMisc + 8);  // of the block, or of each stream
   const uint32_t warp = dev::warp_id_uniform();
   const uint32_t lane = threadIdx.x & 31;
 
@@ -325,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   int64_t before, total = scan(sums, mine, &before);
   int32_t most = 0;  // tiles of a piece; 0: ranges
-  if (a.items <= (int)gridDim.x) {
+  if (!kTwo && a.items <= (int)gridDim.x) {
     // (so there is a thread to every sequence)  The even share and up to three tiles more, which are quicker
     // than a second piece: the pieces of each, 16 bits for each (at most twice the blocks at the even share)
     const int32_t share = (int32_t)min((total + gridDim.x - 1) / gridDim.x, (int64_t)INT32_MAX / 2);
@@ -344,46 +349,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     if (most > 0) total = (pieces >> 16 * (most - share)) & 0xffff;
   }
-  const int64_t grid = min((int64_t)gridDim.x, total);
-  const int64_t c = blockIdx.x;
-  const int64_t s0 = most > 0 ? c : share_of(total, c, grid), s1 = most > 0 ? c + 1 : share_of(total, c + 1, grid);
-  const bool work = c < grid && s1 - s0 <= INT32_MAX;
-  if (c < grid && !work && threadIdx.x == 0) dev::report_bad_page(a.err);  // (hours of work: thousands of lengths of 2^31)
+  const int64_t grid = min((int64_t)gridDim.x * (kTwo ? 2 : 1), total);  // (blocks, or streams, that have steps)
+  constexpr int kParts = kTwo ? 2 : 1;
+  int64_t s0[kParts], s1[kParts];  // steps of the block, or of each stream
+  bool work = false;
+#pragma unroll
+  for (int x = 0; x < kParts; ++x) {
+    const int64_t c = (int64_t)blockIdx.x * kParts + x;
+    s0[x] = s1[x] = -1;
+    if (c < grid) {
+      s0[x] = most > 0 ? c : share_of(total, c, grid);
+      s1[x] = most > 0 ? c + 1 : share_of(total, c + 1, grid);
+      if (s1[x] - s0[x] > INT32_MAX / 4) {  // (hours of work: thousands of lengths of 2^31)
+        if (threadIdx.x == 0) dev::report_bad_page(a.err);
+        s0[x] = s1[x] = -1;
+      }
+    }
+    work = work || s0[x] < s1[x];
+    if (threadIdx.x == 0 && s0[x] == s1[x]) starts[x].steps = 0;
+  }
   for (int b = b0; b < b1; ++b) {
     const Doc d = per == 1 ? d0 : doc_of(a, b);
     const int32_t cut = most > 0 ? (int32_t)(((uint32_t)d.tiles + most - 1) / (uint32_t)most) : d.tiles;  // pieces (steps) of an item
     const int64_t n = (int64_t)cut * d.units * a.kv_heads;
-    if (s0 >= before && s0 < before + n) {
-      const int32_t item = (int32_t)quotient(s0 - before, cut), i = (int32_t)((s0 - before) - (int64_t)item * cut);
-      // (in pieces: tiles < 2^24, i < 2^8)
-      const uint32_t lo = (uint32_t)d.tiles * (uint32_t)i / (uint32_t)cut, hi = (uint32_t)d.tiles * (uint32_t)(i + 1) / (uint32_t)cut;
-      start.b = b;
-      start.item = item;
-      start.lo = most > 0 ? (int32_t)lo : i;
-      start.steps = most > 0 ? (int32_t)(hi - lo) : (int32_t)(s1 - s0);
-      start.row0 = d.row0;
-      start.row1 = d.row0 + d.T;
-      start.given = d.ctx;
-      start.item0 = __ldg(a.item0 + b);
-    }
-    if (c == 0 && __ldg(a.ctx_lens + b) != d.ctx) dev::report_bad_page(a.err);
+#pragma unroll
+    for (int x = 0; x < kParts; ++x)
+      if (s0[x] >= before && s0[x] < before + n) {
+        volatile Start& start = starts[x];
+        const int32_t item = (int32_t)quotient(s0[x] - before, cut), i = (int32_t)((s0[x] - before) - (int64_t)item * cut);
+        // (in pieces: tiles < 2^24, i < 2^8)
+        const uint32_t lo = (uint32_t)d.tiles * (uint32_t)i / (uint32_t)cut, hi = (uint32_t)d.tiles * (uint32_t)(i + 1) / (uint32_t)cut;
+        start.b = b;
+        start.item = item;
+        start.lo = most > 0 ? (int32_t)lo : i;
+        start.steps = most > 0 ? (int32_t)(hi - lo) : (int32_t)(s1[x] - s0[x]);
+        start.row0 = d.row0;
+        start.row1 = d.row0 + d.T;
+        start.given = d.ctx;
+        start.item0 = __ldg(a.item0 + b);
+      }
+    if (blockIdx.x == 0 && __ldg(a.ctx_lens + b) != d.ctx) dev::report_bad_page(a.err);
     before += n;
   }
   dev::tc_fence_before();
   __syncthreads();
   dev::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int32_t steps = work ? start.steps : 0;
+  // tiles of the block, in the order of the ring: of two ranges one tile each in turn, the longer range's first
+  const int32_t of0 = work ? starts[0].steps : 0, of1 = kTwo && work ? starts[1].steps : 0;
+  const int32_t steps = of0 + of1;
+  const int lead = kTwo && of1 > of0 ? 1 : 0;  // the stream that begins
   Walk walk;
-  if (work) walk.begin(a, start);
   Piece p;
+  if (!kTwo && work) walk.begin(a, starts[0]);
 
   if (!work) {
     // (more blocks than steps)
   } else if (warp == kKWarp || warp == kVWarp) {
-    // ------------------------------------------------------ K or V tiles ----
-    const bool is_v = warp == kVWarp;
-    const CUtensorMap* const tm = is_v ? &tm_v : &tm_k;
+    // ---------------- K tiles, V tiles; kTwo: K and V of stream 0, of stream 1 ----
+    const int me = warp == kVWarp ? 1 : 0;
+    if constexpr (kTwo) {
+      if (starts[me].steps > 0) walk.begin(a, starts[me]);
+      else walk.left = 0;
+    }
     // (kept in L2 instead, tiles that a second unit reads too gain nothing and push the partial rows out of it:
     // 282 against 276 us for 64 drafts over 20,423 tokens)
     const uint64_t pol = dev::policy_evict_first();
@@ -391,9 +419,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t tiles_at_once = 32 / n_box;
     const uint32_t dst0 = sbase + kSmemKV + lane * (uint32_t)a.box * 128u;
     const int32_t row_step = kRows % a.page_size;
-    int32_t loaded = 0;                          // tiles
-    uint32_t slot = is_v ? v_entry(0, steps) : 0, ph = 1;  // of the next entry, and its empty barrier's phase
-    bool ok = true, free = true;                 // (the first five entries' slots are)
+    int32_t loaded = 0;                          // tiles of this warp
+    // the ring entry that comes next (tile i of stream s is the block's tile 2 i, or 2 i + 1)
+    const auto entry_of = [&](int32_t i, bool v) {
+      const int32_t t = kTwo ? 2 * i + (me ^ lead) : i;
+      return v ? v_entry(t, steps) : k_entry(t);
+    };
+    uint32_t entry = entry_of(0, !kTwo && me == 1);
+    bool ok = true, free = entry < kSlots;       // (the first five entries' slots are)
+    // one tile's copies into the entry, and a first look at the slot of the next one
+    const auto load = [&](const CUtensorMap* tm, bool in, int32_t page, int32_t c1, int32_t c2, uint32_t bytes, uint32_t next) {
+      const uint32_t slot = entry % kSlots, bar = bars.full(slot);
+      if (!__all_sync(0xffffffffu, free)) {
+        bool good = true;
+        if (lane == 0) good = dev::mbar_wait(bars.empty(slot), ((entry / kSlots) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
+        ok = __shfl_sync(0xffffffffu, good, 0);
+        if (!ok) return;
+      }
+      if (lane == 0) dev::mbar_arrive_expect_tx(bar, bytes);
+      __syncwarp();
+      entry = next;
+      free = dev::mbar_test_wait(bars.empty(next % kSlots), ((next / kSlots) & 1) ^ 1);
+      if (in) {
+        const uint32_t dst = dst0 + slot * kTileBytes;
+        dev::tma_load_4d(dst, tm, bar, 0, c1, c2, page, pol);
+        dev::tma_load_4d(dst + kHalfBytes, tm, bar, 64, c1, c2, page, pol);
+      }
+    };
     while (ok && walk.next(a, &p)) {
       const int32_t total = walk.d.ctx + walk.d.T;
       const int32_t* table = a.page_table + (int64_t)p.b * a.table_width;
@@ -419,62 +471,57 @@ __global__ void __launch_bounds__(kThreads, 1)
           page = a.n_pages;  // outside the tensor map: zeros
         }
         const int32_t c1 = a.heads_first ? p.kvh : row, c2 = a.heads_first ? row : p.kvh;
-        const int32_t boxes = min(n_box, (total - t * kRows + a.box - 1) / a.box);
-        const uint32_t bar = bars.full(slot);
-        if (!__all_sync(0xffffffffu, free)) {
-          bool good = true;
-          if (lane == 0) good = dev::mbar_wait(bars.empty(slot), ph, abort_flag, a.err, kTimeoutNs);
-          ok = __shfl_sync(0xffffffffu, good, 0);
-          if (!ok) break;
+        const uint32_t bytes = (uint32_t)min(n_box, (total - t * kRows + a.box - 1) / a.box) * (uint32_t)a.box * 256u;
+        ++loaded;
+        if constexpr (kTwo) {
+          load(&tm_k, in, page, c1, c2, bytes, entry_of(loaded - 1, true));
+          if (ok) load(&tm_v, in, page, c1, c2, bytes, entry_of(loaded, false));
+        } else {
+          load(me == 1 ? &tm_v : &tm_k, in, page, c1, c2, bytes, entry_of(loaded, me == 1));
         }
-        if (lane == 0) dev::mbar_arrive_expect_tx(bar, (uint32_t)boxes * (uint32_t)a.box * 256u);
-        __syncwarp();
-        const uint32_t dst = dst0 + slot * kTileBytes;
-        // the next entry: asked for while this one's copies are issued
-        slot += is_v ? (loaded + 2 < steps ? 2 : 1) : (loaded == 0 ? 1 : 2);
-        if (slot >= kSlots) {
-          slot -= kSlots;
-          ph ^= 1;
-        }
-        free = dev::mbar_test_wait(bars.empty(slot), ph);
-        if (in) {
-          dev::tma_load_4d(dst, tm, bar, 0, c1, c2, page, pol);
-          dev::tma_load_4d(dst + kHalfBytes, tm, bar, 64, c1, c2, page, pol);
-        }
+        if (!ok) break;
         row += row_step;
         if (row >= a.page_size) row -= a.page_size;
-        ++loaded;
       }
     }
-    if (!ok && lane == 0) {  // drain: wait (bounded) for the copies on their way (every other of five slots)
-      for (int32_t t = max(0, loaded - 3); t < loaded; ++t) {
-        const uint32_t entry = is_v ? v_entry(t, steps) : k_entry(t);
-        dev::mbar_wait_bounded(bars.full(entry % kSlots), (entry / kSlots) & 1, nullptr, nullptr, kTimeoutNs);
-      }
+    if (!ok && lane == 0) {  // drain: wait (bounded) for the copies on their way (of at most three tiles)
+      for (int32_t i = max(0, loaded - 4); i < loaded - 1; ++i)
+        for (int v = kTwo ? 0 : me; v <= (kTwo ? 1 : me); ++v) {
+          const uint32_t e = entry_of(i, v == 1);
+          dev::mbar_wait_bounded(bars.full(e % kSlots), (e / kSlots) & 1, nullptr, nullptr, kTimeoutNs);
+        }
     }
     __syncwarp();
   } else if (warp == kQWarp) {
-    // ----------------------------------------------------------- Q tiles ----
-    if (lane == 0) {
+    // --------------------------- Q tiles (kTwo: a lane a stream, a slot each) ----
+    if (lane < (kTwo ? 2u : 1u)) {
       const uint64_t pol = dev::policy_evict_first();
+      const int64_t c = kTwo ? 2 * (int64_t)blockIdx.x + lane : blockIdx.x, begin = kTwo && lane == 1 ? s0[kParts - 1] : s0[0];
+      if constexpr (kTwo) {
+        if (starts[lane].steps > 0) walk.begin(a, starts[lane]);
+        else walk.left = 0;
+      }
       uint32_t n = 0;
       bool ok = true;
+      const auto slot_of = [&](uint32_t k) { return kTwo ? lane : k & 1; };
+      const auto phase_of = [&](uint32_t k) { return kTwo ? k & 1 : (k >> 1) & 1; };
       while (ok && walk.next(a, &p)) {
         if (p.lo == 0) {
           // an item that begins here: its first slot and its pieces, for the join
           const int32_t tiles = walk.d.tiles;
-          int64_t n = 1;
+          int64_t pieces = 1;
           if (most > 0)
-            n = ((uint32_t)tiles + most - 1) / (uint32_t)most;
-          else if (p.hi < tiles)  // block c has steps [total c / grid, total (c + 1) / grid)
-            n = ((s0 + p.at + tiles) * grid - 1) / total - c + 1;
-          a.joins[p.item] = make_int2((int32_t)(2 * c) + (p.first ? 0 : 1), (int32_t)n);
+            pieces = ((uint32_t)tiles + most - 1) / (uint32_t)most;
+          else if (p.hi < tiles)  // block (stream) c has steps [total c / grid, total (c + 1) / grid)
+            pieces = ((begin + p.at + tiles) * grid - 1) / total - c + 1;
+          a.joins[p.item] = make_int2((int32_t)(2 * c) + (p.first ? 0 : 1), (int32_t)pieces);
         }
         for (int i = 0; ok && i < p.n_qt; ++i) {
-          ok = dev::mbar_wait(bars.q_empty(n & 1), ((n >> 1) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
+          const uint32_t slot = slot_of(n);
+          ok = dev::mbar_wait(bars.q_empty(slot), phase_of(n) ^ 1, abort_flag, a.err, kTimeoutNs);
           if (!ok) break;
           const QTile q = q_tile(a, walk.d, p.kvh, p.qt + i);
-          const uint32_t dst = sbase + kSmemQ + (n & 1) * kTileBytes, bar = bars.q_full(n & 1);
+          const uint32_t dst = sbase + kSmemQ + slot * kTileBytes, bar = bars.q_full(slot);
           dev::mbar_arrive_expect_tx(bar, 256u * (uint32_t)(a.pack * a.toks));
           dev::tma_load_3d(dst, &tm_q, bar, 0, q.head, q.tok0, pol);
           dev::tma_load_3d(dst + kHalfBytes, &tm_q, bar, 64, q.head, q.tok0, pol);
@@ -482,8 +529,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok)
-        for (uint32_t r = 1; r <= 2 && r <= n; ++r)
-          dev::mbar_wait_bounded(bars.q_full((n - r) & 1), ((n - r) >> 1) & 1, nullptr, nullptr, kTimeoutNs);
+        for (uint32_t r = 1; r <= (kTwo ? 1u : 2u) && r <= n; ++r)
+          dev::mbar_wait_bounded(bars.q_full(slot_of(n - r)), phase_of(n - r), nullptr, nullptr, kTimeoutNs);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
@@ -540,6 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu, asked)) wait(bar, parity);
     };
     bool p_asked = false, v_asked = false, k_asked = false;
+    [[maybe_unused]] bool k_ready = false;
     const auto ask_p = [&](int s, uint32_t it) { p_asked = ask(bars.p_ready(s), it & 1); };
     // asks for the V and K behind the next ones (more_v, more_k: whether they are this block's, this piece's)
     const auto ask_tiles = [&](bool more_v, bool more_k) {
@@ -564,7 +612,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit_elect(bars.pv_done(s));
       ++p_it[s];
     };
-    while (ok && walk.next(a, &p)) {
+    if constexpr (kTwo) {
+      // Stream lead ^ x is x's; its tiles are the block's x, x + 2, ..  At a piece's end "PV done", and the next
+      // QK is the next piece's first, of a Q that was loaded while its last tile was in work.
+      Walk w[2];
+      int32_t left[2] = {0, 0}, done[2] = {0, 0};  // tiles of the piece to go and behind
+      uint32_t qs[2] = {0, 0};
+      const uint32_t ld = uniform((uint32_t)lead);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (x >= all) break;
+        const uint32_t st = ld ^ x;
+        w[x].begin(a, starts[st]);
+        w[x].next(a, &p);
+        left[x] = (int32_t)uniform((uint32_t)(p.hi - p.lo));
+        wait(bars.q_full(st), 0);
+        ++qs[x];
+        wait(bars.full(k_slot), k_ph);
+        if (!ok) break;
+        issued = true;
+        qk(st, st, k_slot);
+        commit_elect(bars.empty(k_slot));
+        next_k();
+        if (left[x] == 1) commit_elect(bars.q_empty(st));
+      }
+#pragma unroll 1
+      for (int32_t t0 = 0; ok && t0 < all; t0 += 2)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int32_t t = t0 + x;
+          if (!ok || t >= all) break;
+          const uint32_t st = ld ^ x;
+          need(v_asked, bars.full(v_slot), v_ph);
+          need(p_asked, bars.p_ready(st), p_it[x] & 1);
+          if (!ok) break;
+          dev::tc_fence_after();
+          p_asked = ask(bars.p_ready(st ^ 1), p_it[x ^ 1] & 1);
+          const bool more = t + 2 < all;
+          ask_tiles(tile + 2 < all, t + 3 < all);
+          issue_pv(tm + 256 + st * 128, tm + st * 128, sbase + kSmemKV + v_slot * kTileBytes, done[x] > 0);
+          ++p_it[x];
+          ++done[x];
+          if (--left[x] == 0) {
+            commit_elect(bars.pv_done(st));
+            done[x] = 0;
+            if (more) {
+              w[x].next(a, &p);
+              left[x] = (int32_t)uniform((uint32_t)(p.hi - p.lo));
+              wait(bars.q_full(st), qs[x] & 1);
+              ++qs[x];
+            }
+          }
+          if (more) {
+            // (what was asked of K concerns the tile behind this one)
+            if (!(k_ready && t0 > 0)) wait(bars.full(k_slot), k_ph);
+            if (!ok) break;
+            qk(st, st, k_slot);
+            if (left[x] == 1) commit_elect(bars.q_empty(st));
+          }
+          commit_elect(bars.empty(v_slot));
+          next_v();
+          if (more) {
+            commit_elect(bars.empty(k_slot));
+            next_k();
+          }
+          k_ready = __all_sync(0xffffffffu, k_asked);
+        }
+    }
+    while (!kTwo && ok && walk.next(a, &p)) {
       const int32_t n = (int32_t)uniform((uint32_t)(p.hi - p.lo));
       const bool two = uniform((uint32_t)p.n_qt) == 2;
       p_asked = v_asked = k_asked = false;
@@ -684,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const auto look = [&](const Piece& y) {
       Mine x;
-      x.q = q_tile(a, walk.d, y.kvh, y.qt + (y.n_qt == 2 ? st : 0));
+      x.q = q_tile(a, walk.d, y.kvh, y.qt + (!kTwo && y.n_qt == 2 ? st : 0));
       x.ctx = walk.d.ctx;
       x.T = walk.d.T;
       x.valid = tok_in < (uint32_t)x.q.n_tok;  // (rows past pack * toks have larger tok_in)
@@ -696,6 +811,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : ~0ull >> (63 - (x.q.tok0 + (int32_t)tok_in - walk.d.row0));
       return x;
     };
+    if constexpr (kTwo) {
+      if (starts[st].steps > 0) walk.begin(a, starts[st]);
+      else walk.left = 0;
+    }
     Piece p_next;
     bool go = walk.next(a, &p_next);
     Mine next{};
@@ -703,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && go) {
       p = p_next;
       const Mine me = next;
-      const bool two = p.n_qt == 2;
+      const bool two = kTwo || p.n_qt == 2;  // the stream has the rows to itself
       const QTile& q = me.q;
       const bool valid = me.valid, busy = me.busy;
       const int32_t n = p.hi - p.lo;
@@ -807,8 +926,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the tile ends early: zero the rows of V behind it, a quarter a warp (two query
         // tiles: the first one's warps, whose PV goes first)
         const int32_t rem = me.ctx + me.T - t * kRows;
-        if (rem < kRows && (!two || st == 0)) {
-          const uint32_t ve = v_entry(p.at + j, steps);
+        if (rem < kRows && (kTwo || !two || st == 0)) {
+          const uint32_t ve = v_entry(kTwo ? 2 * (p.at + j) + (st ^ lead) : p.at + j, steps);
           ok = dev::mbar_wait(bars.full(ve % kSlots), (ve / kSlots) & 1, abort_flag, a.err, kTimeoutNs) && ok;
           const uint32_t v = sbase + kSmemKV + (ve % kSlots) * kTileBytes;
           if (ok)
@@ -854,7 +973,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c0 = two ? 0 : 2 * st, c1 = two ? 4 : 2 * st + 2;
         const int32_t tok = q.tok0 + (int32_t)tok_in, head = q.head + (int32_t)sub;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t part = (int64_t)(2 * blockIdx.x + (p.first ? 0 : 1)) * a.slot_rows + (two ? st * kRows : 0) + row;
+        const int64_t at = kTwo ? 2 * (int64_t)blockIdx.x + st : blockIdx.x;
+        const int64_t part = (2 * at + (p.first ? 0 : 1)) * a.slot_rows + (!kTwo && two ? st * kRows : 0) + row;
 #pragma unroll 1
         for (int c = c0; c < c1; ++c) {
           uint32_t ov[32];
@@ -898,7 +1018,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       dev::tc_fence_before();
-      if (two) {
+      if (kTwo) {
+        // (the streams have nothing in common)
+      } else if (two) {
         finished(st ^ 1);
         ok = __all_sync(0xffffffffu, ok);
       } else {
@@ -1055,8 +1177,10 @@ bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, 
 
 cudaError_t launch_attn_tree(const TreeArgs& args, const void* q, int64_t q_stride, const h3attn_cache& c, cudaStream_t stream,
                              std::string* why) {
-  static SmemAttr attr;
-  cudaError_t e = attr.set(attn_tree_kernel, (int)kSmemAlloc);
+  static SmemAttr attr, attr_two;
+  // more items than blocks, a query tile each
+  const bool two = args.slot_rows == kRows && args.items > args.grid;
+  cudaError_t e = two ? attr_two.set(attn_tree_kernel<true>, (int)kSmemAlloc) : attr.set(attn_tree_kernel<false>, (int)kSmemAlloc);
   if (e != cudaSuccess) {
     *why = "cudaFuncSetAttribute(max dynamic shared memory) failed";
     return e;
@@ -1084,7 +1208,10 @@ cudaError_t launch_attn_tree(const TreeArgs& args, const void* q, int64_t q_stri
   const cuuint32_t kv_box[4] = {64, a.heads_first ? 1u : (cuuint32_t)a.box, a.heads_first ? (cuuint32_t)a.box : 1u, 1};
   if (!encode(&mk, c.k, 4, kv_dims, kv_strides, kv_box, why) || !encode(&mv, c.v, 4, kv_dims, kv_strides, kv_box, why))
     return cudaErrorInvalidValue;
-  attn_tree_kernel<<<(unsigned)a.grid, kThreads, kSmemAlloc, stream>>>(mq, mk, mv, a);
+  if (two)
+    attn_tree_kernel<true><<<(unsigned)a.grid, kThreads, kSmemAlloc, stream>>>(mq, mk, mv, a);
+  else
+    attn_tree_kernel<false><<<(unsigned)a.grid, kThreads, kSmemAlloc, stream>>>(mq, mk, mv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // Few rows may have many pieces each (up to one a block of the grid): a block a row.  Else a row a

@@ -1339,7 +1339,7 @@ h3attn_status h3attn_plan_set_tree(h3attn_plan_t plan, int32_t num_kv_heads, voi
   if (items >= (int64_t(1) << 24)) return fail(H3ATTN_EUNSUPPORTED, "2^24 or more items (sequences times key heads times row tiles)");
   t.items = (int32_t)items;
   t.grid = plan->num_sms;
-  const size_t rows = (size_t)2 * t.grid * t.slot_rows;
+  const size_t rows = (size_t)4 * t.grid * kKeyTile;  // (two slots of two tiles a block, or of one tile a stream)
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   std::vector<TreeRow> token;
   std::vector<int32_t> item0;

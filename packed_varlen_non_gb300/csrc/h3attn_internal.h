@@ -238,14 +238,14 @@ struct TreePlan {
   int32_t pack = 1;                    // query heads in a query tile (a divisor of the group), and tokens
   int32_t toks = 1;
   int32_t slot_rows = 0;               // rows of a partial slot: of one query tile, or of two
-  int32_t grid = 0;                    // blocks, two partial slots each
+  int32_t grid = 0;                    // blocks; two partial slots each, or each stream
   int32_t items = 0;                   // (sequence, key head, up to two query tiles)
   int32_t max_len = 0;                 // drafts of the longest document
   TreeRow* d_rows = nullptr;           // [S]
   int32_t* d_item0 = nullptr;          // [n_docs] first item of a document
   int2* d_joins = nullptr;             // [items] first partial slot and pieces (the forward's)
-  float* d_part_o = nullptr;           // [2 grid slot_rows, 128]
-  float2* d_part_ml = nullptr;         // [2 grid slot_rows]
+  float* d_part_o = nullptr;           // [4 grid 128 rows, 128]
+  float2* d_part_ml = nullptr;         // [4 grid 128 rows]
 };
 constexpr int32_t kTreeMax = 64;       // drafts of a document
 constexpr int32_t kTreeDocs = 4096;

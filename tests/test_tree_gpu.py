@@ -83,7 +83,8 @@ CASES = [
     ([0], [1], 1, 1, 8), ([1], [1], 4, 1, 16), ([127], [1], 8, 2, 16), ([128], [1], 8, 2, 64), ([0, 5, 300], [1, 1, 1], 7, 1, 32),
     ([0], [64], 4, 2, 16), ([100], [28], 2, 2, 128), ([64, 65, 63], [64, 63, 64], 8, 1, 16), ([1000, 3, 513], [5, 64, 17], 6, 2, 24),
     ([700], [33], 28, 4, 256), ([2000, 0, 129, 900], [16, 16, 1, 3], 12, 4, 48), ([333] * 40, [1] * 40, 16, 2, 16),
-    ([40] * 200, [2] * 200, 3, 3, 8), ([777], [9], 71, 1, 64), ([500], [10], 128, 1, 16), ([300, 20], [7, 50], 160, 1, 8),
+    ([40] * 200, [2] * 200, 3, 3, 8), ([(37 * i * i) % 700 for i in range(160)], [1 + i % 5 for i in range(160)], 4, 2, 16),
+    ([0] * 153, [1] * 153, 2, 1, 8), ([3000] + [0, 130, 127, 1] * 40, [1] * 161, 5, 1, 32), ([777], [9], 71, 1, 64), ([500], [10], 128, 1, 16), ([300, 20], [7, 50], 160, 1, 8),
 ]
 
 
