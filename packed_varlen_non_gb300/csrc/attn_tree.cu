@@ -493,44 +493,90 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == kQWarp) {
-    // --------------------------- Q tiles (kTwo: a lane a stream, a slot each) ----
-    if (lane < (kTwo ? 2u : 1u)) {
+    // ----------------------------------------------------------- Q tiles ----
+    if (lane == 0) {
       const uint64_t pol = dev::policy_evict_first();
-      const int64_t c = kTwo ? 2 * (int64_t)blockIdx.x + lane : blockIdx.x, begin = kTwo && lane == 1 ? s0[kParts - 1] : s0[0];
-      if constexpr (kTwo) {
-        if (starts[lane].steps > 0) walk.begin(a, starts[lane]);
-        else walk.left = 0;
-      }
-      uint32_t n = 0;
       bool ok = true;
-      const auto slot_of = [&](uint32_t k) { return kTwo ? lane : k & 1; };
-      const auto phase_of = [&](uint32_t k) { return kTwo ? k & 1 : (k >> 1) & 1; };
-      while (ok && walk.next(a, &p)) {
-        if (p.lo == 0) {
-          // an item that begins here: its first slot and its pieces, for the join
-          const int32_t tiles = walk.d.tiles;
-          int64_t pieces = 1;
-          if (most > 0)
-            pieces = ((uint32_t)tiles + most - 1) / (uint32_t)most;
-          else if (p.hi < tiles)  // block (stream) c has steps [total c / grid, total (c + 1) / grid)
-            pieces = ((begin + p.at + tiles) * grid - 1) / total - c + 1;
-          a.joins[p.item] = make_int2((int32_t)(2 * c) + (p.first ? 0 : 1), (int32_t)pieces);
+      const auto load = [&](const QTile& q, uint32_t slot) {
+        const uint32_t dst = sbase + kSmemQ + slot * kTileBytes, bar = bars.q_full(slot);
+        dev::mbar_arrive_expect_tx(bar, 256u * (uint32_t)(a.pack * a.toks));
+        dev::tma_load_3d(dst, &tm_q, bar, 0, q.head, q.tok0, pol);
+        dev::tma_load_3d(dst + kHalfBytes, &tm_q, bar, 64, q.head, q.tok0, pol);
+      };
+      // an item that begins with piece y of block (stream) c, whose steps begin at `begin`: its first slot and
+      // its pieces, for the join
+      const auto note = [&](const Piece& y, int32_t tiles, int64_t c, int64_t begin) {
+        if (y.lo != 0) return;
+        int64_t pieces = 1;
+        if (most > 0)
+          pieces = ((uint32_t)tiles + most - 1) / (uint32_t)most;
+        else if (y.hi < tiles)  // block (stream) c has steps [total c / grid, total (c + 1) / grid)
+          pieces = ((begin + y.at + tiles) * grid - 1) / total - c + 1;
+        a.joins[y.item] = make_int2((int32_t)(2 * c) + (y.first ? 0 : 1), (int32_t)pieces);
+      };
+      if constexpr (kTwo) {
+        // A slot to each stream.  One thread serves whichever is free: a wait for one stream's slot would
+        // hold up the other's, whose next piece may come first.  (Two lanes, a stream each, would wait
+        // for one another at the end of every wait.)
+        Walk w[2];
+        Piece y[2];
+        bool live[2];
+        uint32_t n[2] = {0, 0}, idle = 0;
+        uint64_t since = 0;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          live[x] = starts[x].steps > 0;
+          if (live[x]) {
+            w[x].begin(a, starts[x]);
+            live[x] = w[x].next(a, &y[x]);
+          }
         }
-        for (int i = 0; ok && i < p.n_qt; ++i) {
-          const uint32_t slot = slot_of(n);
-          ok = dev::mbar_wait(bars.q_empty(slot), phase_of(n) ^ 1, abort_flag, a.err, kTimeoutNs);
-          if (!ok) break;
-          const QTile q = q_tile(a, walk.d, p.kvh, p.qt + i);
-          const uint32_t dst = sbase + kSmemQ + slot * kTileBytes, bar = bars.q_full(slot);
-          dev::mbar_arrive_expect_tx(bar, 256u * (uint32_t)(a.pack * a.toks));
-          dev::tma_load_3d(dst, &tm_q, bar, 0, q.head, q.tok0, pol);
-          dev::tma_load_3d(dst + kHalfBytes, &tm_q, bar, 64, q.head, q.tok0, pol);
-          ++n;
+        while (ok && (live[0] || live[1])) {
+          bool any = false;
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (live[x] && dev::mbar_test_wait(bars.q_empty(x), (n[x] & 1) ^ 1)) {
+              note(y[x], w[x].d.tiles, 2 * (int64_t)blockIdx.x + x, s0[kTwo ? x : 0]);
+              load(q_tile(a, w[x].d, y[x].kvh, y[x].qt), (uint32_t)x);
+              ++n[x];
+              live[x] = w[x].next(a, &y[x]);
+              any = true;
+            }
+          if (any) {
+            idle = 0;
+          } else {
+            __nanosleep(20);
+            if ((++idle & 15u) == 0) {  // bounded: two seconds of nothing, or another thread's abort
+              const uint64_t now = dev::globaltimer_ns();
+              if (idle == 16) since = now;
+              ok = *abort_flag == 0;
+              if (ok && now - since > kTimeoutNs) {
+                *abort_flag = 1;
+                atomicExch(a.err, kErrTimeout);
+                ok = false;
+              }
+            }
+          }
         }
+        if (!ok)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            if (n[x]) dev::mbar_wait_bounded(bars.q_full(x), (n[x] - 1) & 1, nullptr, nullptr, kTimeoutNs);
+      } else {
+        uint32_t n = 0;
+        while (ok && walk.next(a, &p)) {
+          note(p, walk.d.tiles, blockIdx.x, s0[0]);
+          for (int i = 0; ok && i < p.n_qt; ++i) {
+            ok = dev::mbar_wait(bars.q_empty(n & 1), ((n >> 1) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
+            if (!ok) break;
+            load(q_tile(a, walk.d, p.kvh, p.qt + i), n & 1);
+            ++n;
+          }
+        }
+        if (!ok)
+          for (uint32_t r = 1; r <= 2 && r <= n; ++r)
+            dev::mbar_wait_bounded(bars.q_full((n - r) & 1), ((n - r) >> 1) & 1, nullptr, nullptr, kTimeoutNs);
       }
-      if (!ok)
-        for (uint32_t r = 1; r <= (kTwo ? 1u : 2u) && r <= n; ++r)
-          dev::mbar_wait_bounded(bars.q_full(slot_of(n - r)), phase_of(n - r), nullptr, nullptr, kTimeoutNs);
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
@@ -778,16 +824,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_o = tmem + (lane_base << 16) + 256;  // O_0; O_1 128 columns on
     float2* const ml_of = reinterpret_cast<float2*>(smem + kSmemMl);
     const uint32_t tok_in = row * a.recip >> 16, sub = row - tok_in * (uint32_t)a.pack;
-    uint32_t s_it = 0, done[2] = {0, 0}, joined = 0;
+    uint32_t s_it = 0, done[2] = {0, 0}, joined = 0;  // pieces in which each stream had a tile
     bool ok = true;
-    // stream s's last PV of the piece; every warp sees every phase, so that none waits for one that
-    // another has followed
+    // stream s's last PV of the piece
     const auto finished = [&](int s) {
       ok = dev::mbar_wait(bars.pv_done(s), (s == 0 ? done[0] : done[1]) & 1, abort_flag, a.err, kTimeoutNs) && ok;
-      if (s == 0)
-        ++done[0];
-      else
-        ++done[1];
     };
     // What a piece is to this row; looked up before the epilogue of the one before it, so that the
     // drafts that the row sees are here when its first tile is (of a short context the only one).
@@ -948,6 +989,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         finished(0);
         if (n > 1) finished(1);
       }
+      ++done[0];
+      if (two || n > 1) ++done[1];
       go = walk.next(a, &p_next);
       if (go) next = look(p_next);
       float w0 = 1.f, w1 = 0.f;
@@ -1018,14 +1061,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       dev::tc_fence_before();
-      if (kTwo) {
-        // (the streams have nothing in common)
-      } else if (two) {
-        finished(st ^ 1);
-        ok = __all_sync(0xffffffffu, ok);
-      } else {
-        // neither stream's next PV may overwrite an O that the other's warps still read
-        // (nor its next row the other's m and l)
+      // One query tile: neither stream's next PV may overwrite an O that the other's warps still read (nor
+      // its next row the other's m and l).  Two, and one in the next piece, where each stream waits for both's
+      // last PVs: both have seen their own here, so no phase of "PV done" is passed over.
+      if (!kTwo && (!two || (go && p_next.n_qt == 1))) {
         __syncwarp();
         if (lane == 0) dev::mbar_arrive(bars.joined());
         ok = dev::mbar_wait(bars.joined(), joined & 1, abort_flag, a.err, kTimeoutNs);

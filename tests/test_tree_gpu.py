@@ -102,7 +102,12 @@ def test_forward_matches_the_oracle(lib, ctx, drafts, heads, kv, page, head_majo
 
 @pytest.mark.parametrize("ctx,drafts,heads,kv,page", [([20423], [1], 8, 1, 16), ([20423, 9000], [64, 64], 16, 2, 128),
                                                       ([5033] * 32, [1] * 32, 8, 2, 16), ([3000, 100, 7000, 0, 1], [16] * 5, 28, 4, 64),
-                                                      ([12000], [64], 64, 8, 64), ([600] * 64, [4] * 64, 32, 8, 32)])
+                                                      ([12000], [64], 64, 8, 64), ([600] * 64, [4] * 64, 32, 8, 32),
+                                                      # one long sequence among many short ones: ranges of one
+                                                      # piece beside ranges of many, in one block
+                                                      ([7] * 40 + [9000] + [7] * 260, [1] * 301, 2, 1, 16),
+                                                      # items of one query tile and of two, of one key tile and of many
+                                                      ([300, 5, 900, 40, 0] * 40, [64, 1, 16, 2, 17] * 40, 8, 1, 16)])
 def test_longer_contexts(lib, ctx, drafts, heads, kv, page):
     t = Tree(ctx, drafts, heads, kv, page)
     masks = random_masks(drafts, 5)
