@@ -1102,10 +1102,10 @@ __device__ __forceinline__ void add(Acc& x, float m, float l, const float4& o) {
 }
 
 // kRowsOf rows a warp, whose loads go out together: many rows have few pieces each
-// (32,768 of two: 23 us with a row a warp, 16 with four).  0: one row a block, whose warps
+// (32,768 of two: 23 us with a row a warp, 11 with two rows).  0: one row a block, whose warps
 // share out its pieces (32 rows of 18: 30 us less than a row after the other).
 template <int kRowsOf>
-__global__ void __launch_bounds__(32 * kJoinWarps, kRowsOf > 1 ? 3 : 6) attn_tree_join_kernel(const __grid_constant__ TreeArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps, kRowsOf > 1 ? 4 : 6) attn_tree_join_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int kN = kRowsOf > 1 ? kRowsOf : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t n_rows = (uint32_t)a.S * (uint32_t)a.H;  // (below 2^31)
@@ -1261,7 +1261,7 @@ cudaError_t launch_attn_tree(const TreeArgs& args, const void* q, int64_t q_stri
   else if (one <= (int64_t)6 * a.grid)
     e = launch_dependent(attn_tree_join_kernel<1>, (unsigned)one, 32u * kJoinWarps, stream, a);
   else
-    e = launch_dependent(attn_tree_join_kernel<4>, (unsigned)((one + 3) / 4), 32u * kJoinWarps, stream, a);
+    e = launch_dependent(attn_tree_join_kernel<2>, (unsigned)((one + 1) / 2), 32u * kJoinWarps, stream, a);
   if (e != cudaSuccess) *why = "the join launch failed";
   return e;
 }

@@ -183,10 +183,11 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 cudaError_t launch_rotary(const RotaryArgs& args, int num_sms, cudaStream_t stream) {
   if (args.n == 0) return cudaSuccess;
   RotaryArgs a = args;
-  // Tokens of a block: enough that each lane group has kAhead rows, fewer where
-  // that would leave SMs without a block.
+  // Tokens of a block: what a lane group's first kAhead rows hold, so that every load goes
+  // out before the angles are computed (a few rows more, in a second turn: 30.8 instead of 29.9 us for 5,033 tokens
+  // of 63 rows); fewer where that would leave SMs without a block.
   const int64_t rows = a.H + a.Hk + a.Hv;
-  int64_t t = (kAhead * kGroups + rows - 1) / rows;
+  int64_t t = kAhead * kGroups / rows;
   t = std::min<int64_t>(t, a.n / (2 * num_sms));
   a.block_tokens = (int32_t)std::max<int64_t>(1, std::min<int64_t>(t, kMaxTokens));
   rotary_kernel<<<(unsigned)((a.n + a.block_tokens - 1) / a.block_tokens), kThreads, 0, stream>>>(a);
