@@ -1105,7 +1105,7 @@ __device__ __forceinline__ void add(Acc& x, float m, float l, const float4& o) {
 // (32,768 of two: 23 us with a row a warp, 11 with two rows).  0: one row a block, whose warps
 // share out its pieces (32 rows of 18: 30 us less than a row after the other).
 template <int kRowsOf>
-__global__ void __launch_bounds__(32 * kJoinWarps, kRowsOf > 1 ? 4 : 6) attn_tree_join_kernel(const __grid_constant__ TreeArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps, kRowsOf > 1 ? 4 : 5) attn_tree_join_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int kN = kRowsOf > 1 ? kRowsOf : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t n_rows = (uint32_t)a.S * (uint32_t)a.H;  // (below 2^31)
@@ -1253,12 +1253,13 @@ cudaError_t launch_attn_tree(const TreeArgs& args, const void* q, int64_t q_stri
     attn_tree_kernel<false><<<(unsigned)a.grid, kThreads, kSmemAlloc, stream>>>(mq, mk, mv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // Few rows may have many pieces each (up to one a block of the grid): a block a row.  Else a row a
-  // warp while that is one wave, six blocks an SM.  (Rows are below 2^31.)
+  // Few items have many pieces each (about the blocks by the items): a block a row (1,024 rows of two
+  // or three: 7.6 us, 3.7 with a row a warp).  Else a row a warp while that is one wave, five blocks an SM.
+  // (Rows are below 2^31.)
   const int64_t rows = a.S * a.H, one = (rows + kJoinWarps - 1) / kJoinWarps;
-  if (rows <= (int64_t)12 * a.grid)
+  if (8 * (int64_t)a.items <= a.grid)
     e = launch_dependent(attn_tree_join_kernel<0>, (unsigned)rows, 32u * kJoinWarps, stream, a);
-  else if (one <= (int64_t)6 * a.grid)
+  else if (one <= (int64_t)5 * a.grid)
     e = launch_dependent(attn_tree_join_kernel<1>, (unsigned)one, 32u * kJoinWarps, stream, a);
   else
     e = launch_dependent(attn_tree_join_kernel<2>, (unsigned)((one + 1) / 2), 32u * kJoinWarps, stream, a);
