@@ -62,7 +62,7 @@ constexpr uint32_t kHalfBytes = kTileBytes / 2;
 constexpr uint32_t kSmemQ = 0;
 constexpr uint32_t kSmemKV = 2 * kTileBytes;
 constexpr uint32_t kSmemBar = kSmemKV + kSlots * kTileBytes;
-constexpr int kNumBars = 8 + 2 * kSlots + 6 + 2;
+constexpr int kNumBars = 4 + 2 * kSlots + 6 + 2;
 constexpr uint32_t kSmemMl = kSmemBar + kNumBars * 8;   // float2 [2][128]
 constexpr uint32_t kSmemMisc = kSmemMl + 2 * 128 * 8;
 constexpr uint32_t kSlack = 496;                        // the base is 1 KB aligned (declared so; checked in the kernel)
@@ -85,14 +85,14 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
 struct Bars {
   uint32_t base;
   __device__ uint32_t q_full(int i) const { return base + 8 * i; }
-  __device__ uint32_t q_empty(int i) const { return base + 8 * (4 + i); }
-  __device__ uint32_t full(int i) const { return base + 8 * (8 + i); }
-  __device__ uint32_t empty(int i) const { return base + 8 * (8 + kSlots + i); }
-  __device__ uint32_t s_ready(int s) const { return base + 8 * (8 + 2 * kSlots + s); }
-  __device__ uint32_t p_ready(int s) const { return base + 8 * (10 + 2 * kSlots + s); }
-  __device__ uint32_t pv_done(int s) const { return base + 8 * (12 + 2 * kSlots + s); }
-  __device__ uint32_t drain() const { return base + 8 * (14 + 2 * kSlots); }
-  __device__ uint32_t joined() const { return base + 8 * (15 + 2 * kSlots); }  // both streams' softmax warps
+  __device__ uint32_t q_empty(int i) const { return base + 8 * (2 + i); }
+  __device__ uint32_t full(int i) const { return base + 8 * (4 + i); }
+  __device__ uint32_t empty(int i) const { return base + 8 * (4 + kSlots + i); }
+  __device__ uint32_t s_ready(int s) const { return base + 8 * (4 + 2 * kSlots + s); }
+  __device__ uint32_t p_ready(int s) const { return base + 8 * (6 + 2 * kSlots + s); }
+  __device__ uint32_t pv_done(int s) const { return base + 8 * (8 + 2 * kSlots + s); }
+  __device__ uint32_t drain() const { return base + 8 * (10 + 2 * kSlots); }
+  __device__ uint32_t joined() const { return base + 8 * (11 + 2 * kSlots); }  // both streams' softmax warps
 };
 
 // S (TMEM) = Q * K^T, 8 MMAs of 16 dims, issued by one elected lane of the warp.
@@ -272,11 +272,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kKWarp && lane < 3) dev::tma_prefetch_desc(lane == 0 ? &tm_k : lane == 1 ? &tm_v : &tm_q);
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       dev::mbar_init(bars.q_full(i), 1);
       dev::mbar_init(bars.q_empty(i), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
       dev::mbar_init(bars.s_ready(i), 1);
       dev::mbar_init(bars.p_ready(i), 4);
       dev::mbar_init(bars.pv_done(i), 1);
@@ -401,12 +399,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t of0 = work ? starts[0].steps : 0, of1 = kTwo && work ? starts[1].steps : 0;
   const int32_t steps = of0 + of1;
   const int lead = kTwo && of1 > of0 ? 1 : 0;  // the stream that begins
-  // kTwo: the Q slots of a stream, and of its k-th piece the slot and its phase.  Tiles of up to 32 rows have two
-  // each, 4 KB apart: what a product reads behind a tile's rows are lanes of their own that no warp looks at.
-  const bool small = a.pack * a.toks <= 32;
-  const auto q_slot = [&](uint32_t st, uint32_t k) { return small ? 2 * st + (k & 1) : st; };
-  const auto q_phase = [&](uint32_t k) { return small ? (k >> 1) & 1 : k & 1; };
-  const auto q_at = [&](uint32_t slot) { return sbase + kSmemQ + slot * (kTwo && small ? kTileBytes / 8 : kTileBytes); };
   Walk walk;
   Piece p;
   if (!kTwo && work) walk.begin(a, starts[0]);
@@ -506,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t pol = dev::policy_evict_first();
       bool ok = true;
       const auto load = [&](const QTile& q, uint32_t slot) {
-        const uint32_t dst = q_at(slot), bar = bars.q_full(slot);
+        const uint32_t dst = sbase + kSmemQ + slot * kTileBytes, bar = bars.q_full(slot);
         dev::mbar_arrive_expect_tx(bar, 256u * (uint32_t)(a.pack * a.toks));
         dev::tma_load_3d(dst, &tm_q, bar, 0, q.head, q.tok0, pol);
         dev::tma_load_3d(dst + kHalfBytes, &tm_q, bar, 64, q.head, q.tok0, pol);
@@ -523,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         a.joins[y.item] = make_int2((int32_t)(2 * c) + (y.first ? 0 : 1), (int32_t)pieces);
       };
       if constexpr (kTwo) {
-        // Slots to each stream.  One thread serves whichever is free: a wait for one stream's slot would
+        // A slot to each stream.  One thread serves whichever is free: a wait for one stream's slot would
         // hold up the other's, whose next piece may come first.  (Two lanes, a stream each, would wait
         // for one another at the end of every wait.)
         Walk w[2];
@@ -543,9 +535,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool any = false;
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            if (live[x] && dev::mbar_test_wait(bars.q_empty(q_slot(x, n[x])), q_phase(n[x]) ^ 1)) {
+            if (live[x] && dev::mbar_test_wait(bars.q_empty(x), (n[x] & 1) ^ 1)) {
               note(y[x], w[x].d.tiles, 2 * (int64_t)blockIdx.x + x, s0[kTwo ? x : 0]);
-              load(q_tile(a, w[x].d, y[x].kvh, y[x].qt), q_slot(x, n[x]));
+              load(q_tile(a, w[x].d, y[x].kvh, y[x].qt), (uint32_t)x);
               ++n[x];
               live[x] = w[x].next(a, &y[x]);
               any = true;
@@ -569,8 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok)
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            for (uint32_t r = 1; r <= (small ? 2u : 1u) && r <= n[x]; ++r)
-              dev::mbar_wait_bounded(bars.q_full(q_slot(x, n[x] - r)), q_phase(n[x] - r), nullptr, nullptr, kTimeoutNs);
+            if (n[x]) dev::mbar_wait_bounded(bars.q_full(x), (n[x] - 1) & 1, nullptr, nullptr, kTimeoutNs);
       } else {
         uint32_t n = 0;
         while (ok && walk.next(a, &p)) {
@@ -632,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (all == 1) v_slot = 1;
     const auto qk = [&](int s, uint32_t q, uint32_t slot) {
-      issue_qk(tm + s * 128, q_at(q), sbase + kSmemKV + slot * kTileBytes);
+      issue_qk(tm + s * 128, sbase + kSmemQ + q * kTileBytes, sbase + kSmemKV + slot * kTileBytes);
       commit_elect(bars.s_ready(s));
     };
     // Asking a barrier takes 200 cycles, a wait that finds it complete too.  So each is asked before the
@@ -672,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // QK is the next piece's first, of a Q that was loaded while its last tile was in work.
       Walk w[2];
       int32_t left[2] = {0, 0}, done[2] = {0, 0};  // tiles of the piece to go and behind
-      uint32_t qs[2] = {0, 0};  // its pieces behind
+      uint32_t qs[2] = {0, 0};
       const uint32_t ld = uniform((uint32_t)lead);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -681,14 +672,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         w[x].begin(a, starts[st]);
         w[x].next(a, &p);
         left[x] = (int32_t)uniform((uint32_t)(p.hi - p.lo));
-        wait(bars.q_full(q_slot(st, 0)), 0);
+        wait(bars.q_full(st), 0);
+        ++qs[x];
         wait(bars.full(k_slot), k_ph);
         if (!ok) break;
         issued = true;
-        qk(st, q_slot(st, 0), k_slot);
+        qk(st, st, k_slot);
         commit_elect(bars.empty(k_slot));
         next_k();
-        if (left[x] == 1) commit_elect(bars.q_empty(q_slot(st, 0)));
+        if (left[x] == 1) commit_elect(bars.q_empty(st));
       }
 #pragma unroll 1
       for (int32_t t0 = 0; ok && t0 < all; t0 += 2)
@@ -713,16 +705,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (more) {
               w[x].next(a, &p);
               left[x] = (int32_t)uniform((uint32_t)(p.hi - p.lo));
+              wait(bars.q_full(st), qs[x] & 1);
               ++qs[x];
-              wait(bars.q_full(q_slot(st, qs[x])), q_phase(qs[x]));
             }
           }
           if (more) {
             // (what was asked of K concerns the tile behind this one)
             if (!(k_ready && t0 > 0)) wait(bars.full(k_slot), k_ph);
             if (!ok) break;
-            qk(st, q_slot(st, qs[x]), k_slot);
-            if (left[x] == 1) commit_elect(bars.q_empty(q_slot(st, qs[x])));
+            qk(st, st, k_slot);
+            if (left[x] == 1) commit_elect(bars.q_empty(st));
           }
           commit_elect(bars.empty(v_slot));
           next_v();
