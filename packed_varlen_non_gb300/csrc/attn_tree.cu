@@ -142,18 +142,21 @@ __device__ __forceinline__ int32_t context(const TreeArgs& a, int32_t T, int32_t
   const int64_t most = (int64_t)a.table_width * a.page_size - T;  // (not negative, and below 2^31: checked by the caller)
   return max(0, (int32_t)min((int64_t)given, most));
 }
+// (kOne, here and below: every item is a single query tile, which spares the divisions)
+template <bool kOne>
 __device__ __forceinline__ Doc make_doc(const TreeArgs& a, int32_t row0, int32_t row1, int32_t given) {
   Doc d;
   d.row0 = row0;
   d.T = row1 - row0;
   d.ctx = context(a, d.T, given);
   d.tiles = (int32_t)(((int64_t)d.ctx + d.T + kRows - 1) / kRows);
-  d.qtiles = a.packs * ((d.T + a.toks - 1) / a.toks);
-  d.units = (d.qtiles + 1) / 2;
+  d.qtiles = kOne ? 1 : a.packs * ((d.T + a.toks - 1) / a.toks);
+  d.units = kOne ? 1 : (d.qtiles + 1) / 2;
   return d;
 }
+template <bool kOne>
 __device__ __forceinline__ Doc doc_of(const TreeArgs& a, int b) {
-  return make_doc(a, __ldg(a.cu + b), __ldg(a.cu + b + 1), __ldg(a.ctx_lens + b));
+  return make_doc<kOne>(a, __ldg(a.cu + b), __ldg(a.cu + b + 1), __ldg(a.ctx_lens + b));
 }
 
 // A block's share of one item: key tiles [lo, hi).
@@ -169,6 +172,7 @@ struct Start {
   int32_t b, steps, item, lo, row0, row1, given, item0;
 };
 // Walks a block's range piece by piece; every role runs its own.
+template <bool kOne>
 struct Walk {
   int32_t b, item, lo;
   int32_t left, at;
@@ -190,7 +194,7 @@ struct Walk {
     item0 = s.item0;
     lo = s.lo;
     ahead(a);
-    d = make_doc(a, s.row0, s.row1, s.given);
+    d = make_doc<kOne>(a, s.row0, s.row1, s.given);
   }
   // the next piece; false at the end
   __device__ bool next(const TreeArgs& a, Piece* p) {
@@ -199,14 +203,14 @@ struct Walk {
       item = 0;
       item0 += a.kv_heads * d.units;
       ++b;
-      d = make_doc(a, d.row0 + d.T, row2, given);
+      d = make_doc<kOne>(a, d.row0 + d.T, row2, given);
       ahead(a);
     }
     p->b = b;
     p->item = item0 + item;
-    p->kvh = item / d.units;
-    p->qt = 2 * (item - p->kvh * d.units);
-    p->n_qt = min(2, d.qtiles - p->qt);
+    p->kvh = kOne ? item : item / d.units;
+    p->qt = kOne ? 0 : 2 * (item - p->kvh * d.units);
+    p->n_qt = kOne ? 1 : min(2, d.qtiles - p->qt);
     p->lo = lo;
     p->hi = min(d.tiles, lo + left);
     p->whole = lo == 0 && p->hi == d.tiles;
@@ -233,7 +237,9 @@ __device__ __forceinline__ uint32_t v_entry(int32_t t, int32_t steps) { return t
 struct QTile {
   int32_t tok0, n_tok, head;
 };
+template <bool kOne>
 __device__ __forceinline__ QTile q_tile(const TreeArgs& a, const Doc& d, int32_t kvh, int32_t qt) {
+  if constexpr (kOne) return QTile{d.row0, d.T, kvh * a.group};
   const int32_t block = qt / a.packs, first = block * a.toks;
   return QTile{d.row0 + first, min(a.toks, d.T - first), kvh * a.group + (qt - block * a.packs) * a.pack};
 }
@@ -325,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Doc d0 = {};  // (the thread's sequence, where there is one to a thread)
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b) {
-    d0 = doc_of(a, b);
+    d0 = doc_of<kTwo>(a, b);
     mine += (int64_t)d0.tiles * d0.units * a.kv_heads;
   }
   int64_t before, total = scan(sums, mine, &before);
@@ -369,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && s0[x] == s1[x]) starts[x].steps = 0;
   }
   for (int b = b0; b < b1; ++b) {
-    const Doc d = per == 1 ? d0 : doc_of(a, b);
+    const Doc d = per == 1 ? d0 : doc_of<kTwo>(a, b);
     const int32_t cut = most > 0 ? (int32_t)(((uint32_t)d.tiles + most - 1) / (uint32_t)most) : d.tiles;  // pieces (steps) of an item
     const int64_t n = (int64_t)cut * d.units * a.kv_heads;
 #pragma unroll
@@ -399,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t of0 = work ? starts[0].steps : 0, of1 = kTwo && work ? starts[1].steps : 0;
   const int32_t steps = of0 + of1;
   const int lead = kTwo && of1 > of0 ? 1 : 0;  // the stream that begins
-  Walk walk;
+  Walk<kTwo> walk;
   Piece p;
   if (!kTwo && work) walk.begin(a, starts[0]);
 
@@ -518,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A slot to each stream.  One thread serves whichever is free: a wait for one stream's slot would
         // hold up the other's, whose next piece may come first.  (Two lanes, a stream each, would wait
         // for one another at the end of every wait.)
-        Walk w[2];
+        Walk<kTwo> w[2];
         Piece y[2];
         bool live[2];
         uint32_t n[2] = {0, 0}, idle = 0;
@@ -537,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 2; ++x)
             if (live[x] && dev::mbar_test_wait(bars.q_empty(x), (n[x] & 1) ^ 1)) {
               note(y[x], w[x].d.tiles, 2 * (int64_t)blockIdx.x + x, s0[kTwo ? x : 0]);
-              load(q_tile(a, w[x].d, y[x].kvh, y[x].qt), (uint32_t)x);
+              load(q_tile<kTwo>(a, w[x].d, y[x].kvh, y[x].qt), (uint32_t)x);
               ++n[x];
               live[x] = w[x].next(a, &y[x]);
               any = true;
@@ -569,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; ok && i < p.n_qt; ++i) {
             ok = dev::mbar_wait(bars.q_empty(n & 1), ((n >> 1) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
             if (!ok) break;
-            load(q_tile(a, walk.d, p.kvh, p.qt + i), n & 1);
+            load(q_tile<kTwo>(a, walk.d, p.kvh, p.qt + i), n & 1);
             ++n;
           }
         }
@@ -661,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (kTwo) {
       // Stream lead ^ x is x's; its tiles are the block's x, x + 2, ..  At a piece's end "PV done", and the next
       // QK is the next piece's first, of a Q that was loaded while its last tile was in work.
-      Walk w[2];
+      Walk<kTwo> w[2];
       int32_t left[2] = {0, 0}, done[2] = {0, 0};  // tiles of the piece to go and behind
       uint32_t qs[2] = {0, 0};
       const uint32_t ld = uniform((uint32_t)lead);
@@ -840,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const auto look = [&](const Piece& y) {
       Mine x;
-      x.q = q_tile(a, walk.d, y.kvh, y.qt + (!kTwo && y.n_qt == 2 ? st : 0));
+      x.q = q_tile<kTwo>(a, walk.d, y.kvh, y.qt + (!kTwo && y.n_qt == 2 ? st : 0));
       x.ctx = walk.d.ctx;
       x.T = walk.d.T;
       x.valid = tok_in < (uint32_t)x.q.n_tok;  // (rows past pack * toks have larger tok_in)
@@ -1018,39 +1024,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t at = kTwo ? 2 * (int64_t)blockIdx.x + st : blockIdx.x;
         const int64_t part = (2 * at + (p.first ? 0 : 1)) * a.slot_rows + (!kTwo && two ? st * kRows : 0) + row;
+        // (two chunks of 32 dims a turn: one chunk after the other waits for tensor memory each time)
 #pragma unroll 1
-        for (int c = c0; c < c1; ++c) {
-          uint32_t ov[32];
-          dev::tmem_ld32(t_o + (two ? st * 128 : 0) + c * 32, ov);
+        for (int c = c0; c < c1; c += 2) {
+          uint32_t ov[2][32];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) dev::tmem_ld32(t_o + (two ? st * 128 : 0) + (c + y) * 32, ov[y]);
           dev::tmem_wait_ld();
           if (!two) {
-            uint32_t o1[32];
-            if (both) {
-              dev::tmem_ld32(t_o + 128 + c * 32, o1);
-              dev::tmem_wait_ld();
-            }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float x = w0 * __uint_as_float(ov[e]);
-              ov[e] = __float_as_uint(both ? fmaf(w1, __uint_as_float(o1[e]), x) : x);
+            for (int y = 0; y < 2; ++y) {
+              uint32_t o1[32];
+              if (both) {
+                dev::tmem_ld32(t_o + 128 + (c + y) * 32, o1);
+                dev::tmem_wait_ld();
+              }
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float x = w0 * __uint_as_float(ov[y][e]);
+                ov[y][e] = __float_as_uint(both ? fmaf(w1, __uint_as_float(o1[e]), x) : x);
+              }
             }
           }
           if (valid && p.whole) {
             __nv_bfloat16* const dst = a.o + (int64_t)tok * a.o_stride + (int64_t)head * kHeadDim + c * 32;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 8; ++e) {
               uint32_t w[4];
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                w[x] = dev::pack_bf16x2(__uint_as_float(ov[8 * e + 2 * x]) * inv, __uint_as_float(ov[8 * e + 2 * x + 1]) * inv);
+              for (int x = 0; x < 4; ++x) {
+                const int at = 8 * (e & 3) + 2 * x;
+                w[x] = dev::pack_bf16x2(__uint_as_float(ov[e >> 2][at]) * inv, __uint_as_float(ov[e >> 2][at + 1]) * inv);
+              }
               *reinterpret_cast<uint4*>(dst + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else if (valid) {
             float* const dst = a.part_o + part * kHeadDim + c * 32;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dev::st_global_v8(dst + 8 * e, ov[8 * e], ov[8 * e + 1], ov[8 * e + 2], ov[8 * e + 3], ov[8 * e + 4],
-                                ov[8 * e + 5], ov[8 * e + 6], ov[8 * e + 7]);
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t(&w)[32] = ov[e >> 2];
+              const int at = 8 * (e & 3);
+              dev::st_global_v8(dst + 8 * e, w[at], w[at + 1], w[at + 2], w[at + 3], w[at + 4], w[at + 5], w[at + 6], w[at + 7]);
+            }
           }
         }
         if (valid && (two || st == 0)) {
