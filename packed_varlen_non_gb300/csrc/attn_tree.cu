@@ -437,9 +437,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto load = [&](const CUtensorMap* tm, bool in, int32_t page, int32_t c1, int32_t c2, uint32_t bytes, uint32_t next) {
       const uint32_t slot = entry % kSlots, bar = bars.full(slot);
       if (!__all_sync(0xffffffffu, free)) {
-        bool good = true;
-        if (lane == 0) good = dev::mbar_wait(bars.empty(slot), ((entry / kSlots) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
-        ok = __shfl_sync(0xffffffffu, good, 0);
+        // (asked again and again: the wait that suspends a thread wakes it some 400 cycles late, 141 against
+        // 126 us for 512 sequences of 300 tokens; the softmax warps, waiting so, take the other stream's issue slots)
+        bool good = false;
+#pragma unroll 1
+        for (int i = 0; i < 64 && !good; ++i) good = __all_sync(0xffffffffu, dev::mbar_test_wait(bars.empty(slot), ((entry / kSlots) & 1) ^ 1));
+        if (!good) {
+          if (lane == 0) good = dev::mbar_wait(bars.empty(slot), ((entry / kSlots) & 1) ^ 1, abort_flag, a.err, kTimeoutNs);
+          ok = __shfl_sync(0xffffffffu, good, 0);
+        }
         if (!ok) return;
       }
       if (lane == 0) dev::mbar_arrive_expect_tx(bar, bytes);
@@ -897,15 +903,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               see[1] = (word << (-base - 64)) | ((1ull << (-base - 64)) - 1);
             }
           }
-          // a half of the tile's scores, 64 keys, at a time: the second half's maximum, the first
-          // half's maximum and weights, the second half again (all 128 at once spilled to local memory,
-          // of which little stays close when shared memory takes most of L1: 4.3 us a step for 1.4)
-          float sv[64];
-          const auto scores = [&](int h) {
+          // Half of the tile's scores, 64 keys, at a time, each a step of the online softmax: its maximum, then its
+          // weights over the first half's columns.  A reference that the second half moves scales the first
+          // half's weights where they lie, exactly: references are whole numbers, so alpha is a power of two.
+          // (All 128 scores at once spilled to local memory, of which little stays close when shared memory
+          // takes most of L1: 4.3 us a step for 1.4.  A loop as it is, not unrolled: a block that has a few
+          // tiles fetches every instruction once.)
+          float alpha = 1.f;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
             uint32_t r[2][32];
             dev::tmem_ld32(t_s + 64 * h, r[0]);
             dev::tmem_ld32(t_s + 64 * h + 32, r[1]);
             dev::tmem_wait_ld();
+            float sv[64];
 #pragma unroll
             for (int c = 0; c < 64; ++c) sv[c] = __uint_as_float(r[c >> 5][c & 31]);
             if (edge) {
@@ -915,31 +926,39 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 0; c < 64; ++c)
                 if (!((w[c >> 5] >> (c & 31)) & 1u)) sv[c] = -INFINITY;
             }
-          };
-          float mx[8];
+            float mx[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
-          // (loops as they are, not unrolled: a block that has a few tiles fetches every instruction once)
-#pragma unroll 1
-          for (int h = 1; h >= 0; --h) {
-            scores(h);
+            for (int i = 0; i < 8; ++i) mx[i] = dev::max3(sv[i], sv[8 + i], sv[16 + i]);
 #pragma unroll
-            for (int c = 0; c < 64; c += 16)
+            for (int c = 24; c < 56; c += 16)
 #pragma unroll
               for (int i = 0; i < 8; ++i) mx[i] = dev::max3(mx[i], sv[c + i], sv[c + 8 + i]);
-          }
-          const float m_new =
-              dev::max3(dev::max3(mx[0], mx[1], mx[2]), dev::max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * a.scale_log2;
-          float alpha = 1.f;
-          if (m_new > m + kRescale) {
-            alpha = dev::ex2_approx(m - m_new);
-            m = m_new;
-          }
-          const float neg = -m;
-          float rs8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            if (h == 1) scores(1);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mx[i] = fmaxf(mx[i], sv[56 + i]);
+            const float m_new =
+                dev::max3(dev::max3(mx[0], mx[1], mx[2]), dev::max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])) * a.scale_log2;
+            if (__any_sync(0xffffffffu, m_new > m + kRescale)) {
+              float beta = 1.f;
+              if (m_new > m + kRescale) {
+                const float up = ceilf(m_new);
+                beta = dev::ex2_approx(m - up);
+                m = up;
+              }
+              alpha *= beta;
+              l *= beta;
+              if (h == 1) {
+                uint32_t pr[32];
+                dev::tmem_wait_st();
+                dev::tmem_ld32(t_s, pr);
+                dev::tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  pr[c] = dev::pack_bf16x2(__uint_as_float(pr[c] << 16) * beta, __uint_as_float(pr[c] & 0xffff0000u) * beta);
+                dev::tmem_st32(t_s, pr);
+              }
+            }
+            const float neg = -m;
+            float rs8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             uint32_t pr[32];
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
@@ -952,9 +971,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               pr[c] = dev::pack_bf16x2(p0, p1);
             }
             dev::tmem_st32(t_s + 32 * h, pr);  // (over the first half's scores, which are read)
+            l += ((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7]));
           }
-          const float rs = ((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7]));
-          l = l * alpha + rs;
           // (every PV of this stream so far completed before the QK whose S was just read)
           if (j >= (two ? 1 : 2) && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1

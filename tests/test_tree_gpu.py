@@ -152,6 +152,20 @@ def test_wide_scores_and_large_values(lib, spread, size):
     t.check(o, lse)
 
 
+@pytest.mark.parametrize("steps", [[0, 24] * 8, [24 * i for i in range(8)], [0, 0, 0, 48, 0, 96, 24, 120]])
+@pytest.mark.parametrize("ctx,drafts", [([496], [16]), ([448, 300, 60] * 60, [1] * 180)])
+def test_scores_that_step_up_between_halves_of_a_tile(lib, steps, ctx, drafts):
+    # every 64 keys the scores of even heads step by 34 (49 in powers of two) a 24, those of odd heads fall; the
+    # references move inside a tile, in some rows of a warp only, and what was summed before them counts 2^-49 or 0
+    t = Tree(ctx, drafts, 8, 2, 16)
+    t.q[:, 0::2, 0], t.q[:, 1::2, 0] = 16.0, -16.0
+    for b, (c, d) in enumerate(zip(ctx, drafts)):
+        k, v = W.rows(c + d, 2, 100 + b), W.rows(c + d, 2, 500 + b)
+        k[:, :, 0] = torch.tensor([float(steps[i // 64]) for i in range(c + d)], device="cuda")[:, None]
+        t.put(b, 0, k, v)
+    t.check(*t.forward(), what=steps)
+
+
 def test_stacked_layers_strides_and_guards(lib):
     # a cache whose layers, k and v share one buffer; q out of a fused one; o with guards
     ctx, drafts, heads, kv, page = [300, 40], [6, 1], 6, 2, 16
