@@ -134,6 +134,25 @@ __device__ __forceinline__ void commit_elect(uint32_t bar) {
       : "memory");
 }
 
+// Four lanes' four blocks of eight words, transposed: block k of lane i becomes lane k's block i.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[32], uint32_t lane) {
+#pragma unroll
+  for (int m = 1; m <= 2; m <<= 1) {
+    const bool upper = (lane & m) != 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j & m) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint32_t &x = w[8 * j + e], &y = w[8 * (j | m) + e];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? x : y, m);
+        if (upper) x = got;
+        else y = got;
+      }
+    }
+  }
+}
+
 // A sequence: its drafts [row0, row0 + T), context, key tiles, and items (key head, unit of up to two query tiles).
 struct Doc {
   int32_t row0, T, ctx, tiles, qtiles, units;
@@ -150,7 +169,8 @@ __device__ __forceinline__ Doc make_doc(const TreeArgs& a, int32_t row0, int32_t
   d.T = row1 - row0;
   d.ctx = context(a, d.T, given);
   d.tiles = (int32_t)(((int64_t)d.ctx + d.T + kRows - 1) / kRows);
-  d.qtiles = kOne ? 1 : a.packs * ((d.T + a.toks - 1) / a.toks);
+  // (T / toks rounded up: 65536 / toks rounded up is exact here, 191 toks < 65536)
+  d.qtiles = kOne ? 1 : a.packs * (int32_t)((uint32_t)(d.T + a.toks - 1) * a.recip_toks >> 16);
   d.units = kOne ? 1 : (d.qtiles + 1) / 2;
   return d;
 }
@@ -169,12 +189,12 @@ struct Piece {
 };
 // Where a block's range begins (found once, for all roles).
 struct Start {
-  int32_t b, steps, item, lo, row0, row1, given, item0;
+  int32_t b, steps, kvh, unit, lo, row0, row1, given, item0;
 };
 // Walks a block's range piece by piece; every role runs its own.
 template <bool kOne>
 struct Walk {
-  int32_t b, item, lo;
+  int32_t b, kvh, unit, lo;
   int32_t left, at;
   int32_t item0;        // of all sequences' items, this one's first
   bool first;
@@ -190,7 +210,8 @@ struct Walk {
     left = s.steps;
     at = 0;
     first = true;
-    item = s.item;
+    kvh = s.kvh;
+    unit = s.unit;
     item0 = s.item0;
     lo = s.lo;
     ahead(a);
@@ -199,17 +220,17 @@ struct Walk {
   // the next piece; false at the end
   __device__ bool next(const TreeArgs& a, Piece* p) {
     if (left <= 0) return false;
-    if (item == a.kv_heads * d.units) {
-      item = 0;
+    if (kvh == a.kv_heads) {
+      kvh = 0;
       item0 += a.kv_heads * d.units;
       ++b;
       d = make_doc<kOne>(a, d.row0 + d.T, row2, given);
       ahead(a);
     }
     p->b = b;
-    p->item = item0 + item;
-    p->kvh = kOne ? item : item / d.units;
-    p->qt = kOne ? 0 : 2 * (item - p->kvh * d.units);
+    p->item = item0 + (kOne ? kvh : kvh * d.units + unit);
+    p->kvh = kvh;
+    p->qt = kOne ? 0 : 2 * unit;
     p->n_qt = kOne ? 1 : min(2, d.qtiles - p->qt);
     p->lo = lo;
     p->hi = min(d.tiles, lo + left);
@@ -222,7 +243,10 @@ struct Walk {
     lo = p->hi;
     if (lo == d.tiles) {
       lo = 0;
-      ++item;
+      if (kOne || ++unit == d.units) {
+        unit = 0;
+        ++kvh;
+      }
     }
     return true;
   }
@@ -339,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!kTwo && a.items <= (int)gridDim.x) {
     // (so there is a thread to every sequence)  The even share and up to three tiles more, which are quicker
     // than a second piece: the pieces of each, 16 bits for each (at most twice the blocks at the even share)
-    const int32_t share = (int32_t)min((total + gridDim.x - 1) / gridDim.x, (int64_t)INT32_MAX / 2);
+    const int32_t share = (int32_t)max((int64_t)1, min(quotient(total + gridDim.x - 1, (int32_t)gridDim.x), (int64_t)INT32_MAX / 2));
     int64_t pieces = 0;
     if (b0 < b1)
 #pragma unroll
@@ -384,9 +408,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         volatile Start& start = starts[x];
         const int32_t item = (int32_t)quotient(s0[x] - before, cut), i = (int32_t)((s0[x] - before) - (int64_t)item * cut);
         // (in pieces: tiles < 2^24, i < 2^8)
-        const uint32_t lo = (uint32_t)d.tiles * (uint32_t)i / (uint32_t)cut, hi = (uint32_t)d.tiles * (uint32_t)(i + 1) / (uint32_t)cut;
+        uint32_t lo = 0, hi = 0;
+        if (most > 0) {
+          lo = (uint32_t)d.tiles * (uint32_t)i / (uint32_t)cut;
+          hi = (uint32_t)d.tiles * (uint32_t)(i + 1) / (uint32_t)cut;
+        }
+        const int32_t kvh = kTwo ? item : (int32_t)((uint32_t)item / (uint32_t)d.units);
         start.b = b;
-        start.item = item;
+        start.kvh = kvh;
+        start.unit = kTwo ? 0 : item - kvh * d.units;
         start.lo = most > 0 ? (int32_t)lo : i;
         start.steps = most > 0 ? (int32_t)(hi - lo) : (int32_t)(s1[x] - s0[x]);
         start.row0 = d.row0;
@@ -421,10 +451,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (kept in L2 instead, tiles that a second unit reads too gain nothing and push the partial rows out of it:
     // 282 against 276 us for 64 drafts over 20,423 tokens)
     const uint64_t pol = dev::policy_evict_first();
-    const int n_box = kRows / a.box;             // boxes of a tile, a lane each
-    const int32_t tiles_at_once = 32 / n_box;
+    const int n_box = a.n_box;                   // boxes of a tile, a lane each
+    const int32_t tiles_at_once = a.at_once;
     const uint32_t dst0 = sbase + kSmemKV + lane * (uint32_t)a.box * 128u;
-    const int32_t row_step = kRows % a.page_size;
     int32_t loaded = 0;                          // tiles of this warp
     // the ring entry that comes next (tile i of stream s is the block's tile 2 i, or 2 i + 1)
     const auto entry_of = [&](int32_t i, bool v) {
@@ -463,12 +492,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* table = a.page_table + (int64_t)p.b * a.table_width;
       // Page numbers a window of 32 boxes at a time, a lane each, the next window on
       // its way (a lookup a tile, though asked for a tile ahead, paced the loads: 1,000 cycles a tile).
+      const auto box_page = [&](uint32_t i) { return (uint32_t)((uint64_t)i * a.page_mul >> a.page_shift); };
       const auto pages_from = [&](int32_t t) {
-        const int64_t key = ((int64_t)t * n_box + lane) * a.box;
-        return key < total ? __ldg(table + (uint32_t)key / (uint32_t)a.page_size) : 0;
+        const uint32_t i = (uint32_t)t * n_box + lane;  // (below 2^28 + 32)
+        return (int64_t)i * a.box < total ? __ldg(table + box_page(i)) : 0;
       };
       int32_t pages = pages_from(p.lo), pages_next = pages_from(p.lo + tiles_at_once), window = p.lo;
-      int32_t row = (int32_t)(((uint32_t)p.lo * kRows + lane * (uint32_t)a.box) % (uint32_t)a.page_size);  // in its page
+      const uint32_t first = (uint32_t)p.lo * n_box + lane;
+      int32_t row = (int32_t)((first - box_page(first) * (uint32_t)a.page_boxes) * (uint32_t)a.box);  // in its page
       for (int32_t t = p.lo; t < p.hi; ++t) {
         if (t - window == tiles_at_once) {
           window = t;
@@ -492,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           load(me == 1 ? &tm_v : &tm_k, in, page, c1, c2, bytes, entry_of(loaded, me == 1));
         }
         if (!ok) break;
-        row += row_step;
+        row += a.row_step;
         if (row >= a.page_size) row -= a.page_size;
       }
     }
@@ -1076,13 +1107,28 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               *reinterpret_cast<uint4*>(dst + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-          } else if (valid) {
+          } else if (kTwo && valid) {
+            // (few pieces of a range are shared; with the transposition 512 sequences of 300 tokens took 132 us for 119)
             float* const dst = a.part_o + part * kHeadDim + c * 32;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const uint32_t(&w)[32] = ov[e >> 2];
               const int at = 8 * (e & 3);
               dev::st_global_v8(dst + 8 * e, w[at], w[at + 1], w[at + 2], w[at + 3], w[at + 4], w[at + 5], w[at + 6], w[at + 7]);
+            }
+          } else if (!kTwo && !p.whole) {
+            // (a line of a row from four lanes: a row a lane, 32 lines an instruction, 64 rows took 6,300 cycles)
+            float* const dst = a.part_o + (part - (lane & 3)) * kHeadDim + c * 32 + 8 * (lane & 3);
+            const int32_t rows = q.n_tok * a.pack - (int32_t)(row & ~3u);  // of this row's four on
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              uint32_t(&w)[32] = ov[y];
+              transpose4(w, lane);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (k < rows)
+                  dev::st_global_v8(dst + k * kHeadDim + 32 * y, w[8 * k], w[8 * k + 1], w[8 * k + 2], w[8 * k + 3], w[8 * k + 4],
+                                    w[8 * k + 5], w[8 * k + 6], w[8 * k + 7]);
             }
           }
         }
@@ -1263,6 +1309,17 @@ cudaError_t launch_attn_tree(const TreeArgs& args, const void* q, int64_t q_stri
   a.n_pages = c.n_pages;
   a.box = c.page_size & -c.page_size;  // gcd(page_size, 128), of a multiple of 8
   if (a.box > kRows) a.box = kRows;
+  a.n_box = kRows / a.box;
+  a.at_once = 32 / a.n_box;
+  a.row_step = kRows % a.page_size;
+  a.page_boxes = a.page_size / a.box;
+  // i / page_boxes = i mul >> shift for i < 2^29: mul exceeds 2^shift / page_boxes by less than 1, and i by that stays
+  // below 2^shift / page_boxes
+  int bits = 0;
+  while ((1ll << bits) < a.page_boxes) ++bits;
+  a.page_shift = 29 + bits;
+  a.page_mul = (uint32_t)(((1ull << a.page_shift) + a.page_boxes - 1) / a.page_boxes);
+  a.recip_toks = (65536u + (uint32_t)a.toks - 1) / (uint32_t)a.toks;
   CUtensorMap mq, mk, mv;
   {
     const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)a.H, (cuuint64_t)a.S};

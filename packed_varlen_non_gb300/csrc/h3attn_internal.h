@@ -493,9 +493,12 @@ struct TreeArgs {
   float2* part_ml;
   uint32_t* err;
   // (the launcher's)
-  uint32_t recip;              // row / pack = row * recip >> 16
+  uint32_t recip, recip_toks;  // row / pack = row * recip >> 16, and of toks
   int32_t page_size, n_pages;
   int32_t box;                 // rows of the cache that a copy takes: gcd(page_size, 128)
+  int32_t n_box, at_once;      // boxes of a 128-key tile, tiles of 32 boxes
+  int32_t page_boxes, row_step;  // boxes of a page; 128 mod page_size
+  uint32_t page_mul, page_shift;  // box / page_boxes = box * page_mul >> page_shift
   int32_t heads_first;         // the cache's heads lie closer together than its tokens
 };
 cudaError_t launch_attn_tree(const TreeArgs& a, const void* q, int64_t q_stride, const h3attn_cache& cache, cudaStream_t stream,
