@@ -1068,7 +1068,7 @@ h3attn_status check_cache(const h3attn_cache* c) {
   for (const Dim& x : d) {
     if (x.stride < 0 || x.stride % 8) return fail(H3ATTN_EINVAL, "the cache's strides must be multiples of 8 (got %lld)", (long long)x.stride);
     if (x.n == 1) continue;
-    if (x.stride < span || x.stride > (int64_t(1) << 38))
+    if (x.stride < span || x.stride > (int64_t(1) << 38) || x.stride > (int64_t(1) << 60) / x.n)
       return fail(H3ATTN_EINVAL, "the cache's rows share elements, or lie too far apart (stride %lld)", (long long)x.stride);
     span += (x.n - 1) * x.stride;
   }

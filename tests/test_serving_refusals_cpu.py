@@ -4,6 +4,7 @@ import ctypes
 import math
 
 import pytest
+import torch
 
 from packed_varlen_non_gb300 import h3attn as H
 
@@ -117,3 +118,11 @@ def test_move(lib):
 def test_the_tree_calls_refuse_a_null_plan(lib):
     assert status(lambda: H.h3attn_plan_set_tree(None, 1, stream=0)) == E
     assert lib.load().h3attn_forward_tree(None, Q, 512, ctypes.byref(cache()), POS, 4, LIST, None, Q2, 512, 0.1, None, None) == E
+
+
+def test_a_cache_whose_size_passes_64_bits(lib):
+    # (its span would wrap around to a small one)
+    for kw in (dict(n_pages=1 << 27, page_stride=1 << 38), dict(n_pages=1 << 24, page_stride=1 << 37),
+               dict(page_size=1 << 28, n_pages=1, token_stride=1 << 36)):
+        assert store(lib, cache=cache(**kw)) == E, kw
+        assert lib.load().h3attn_cache_move(ctypes.byref(cache(**kw)), LIST, POS, 3, 4, None) == E, kw
