@@ -616,7 +616,7 @@ def _bad_rows(x, name, n, device):
 
 def _heads(x, name, n, device, bf16):
     """(pointer, row stride, heads) of bf16 rows [n, heads, 128] on the device."""
-    if x.dtype is bf16 and x.dim() == 3 and x.get_device() == device:
+    if x.dtype is bf16 and x.dim() == 3 and x.get_device() == device >= 0:
         rows, heads, dims = x.shape
         step, head, dim = x.stride()
         if rows == n and dims == 128 and dim == 1 and (head == 128 or heads == 1):

@@ -126,3 +126,15 @@ def test_a_cache_whose_size_passes_64_bits(lib):
                dict(page_size=1 << 28, n_pages=1, token_stride=1 << 36)):
         assert store(lib, cache=cache(**kw)) == E, kw
         assert lib.load().h3attn_cache_move(ctypes.byref(cache(**kw)), LIST, POS, 3, 4, None) == E, kw
+
+
+def test_the_binding_refuses_host_tensors(lib):
+    # all of them: each agrees with the others on its device
+    rope, n = H.h3attn_rope_init(), 4
+    q = [torch.zeros(n, 2, 128, dtype=torch.bfloat16) for _ in range(4)]
+    pos = torch.zeros(n, dtype=torch.int32)
+    for args in ((q[0], q[1]), (q[0], q[1], q[2], q[3]), (None, None, q[2], q[3])):
+        with pytest.raises(ValueError, match="GPU"):
+            H.h3attn_rotary(rope, pos, *args)
+    with pytest.raises(ValueError, match="GPU"):
+        H.Cache(torch.zeros(2, 8, 2, 128, dtype=torch.bfloat16), torch.zeros(2, 8, 2, 128, dtype=torch.bfloat16))
