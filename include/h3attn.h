@@ -8,6 +8,9 @@
  *      through);
  *   2. attention that is bidirectional inside each cu_seqlens document of the
  *      packed sequence and never crosses a document boundary.
+ * Beside it, further down: FP8, block-sparse and shared-prefix forwards; and for
+ * a text tower and for answering from a context, rotary positions, causal
+ * attention over prompts, a paged cache and attention of drafted tokens over it.
  *
  * Pages defining it (page title, then section):
  *   [PR26]  vllm.cpp PR #26 "feat(minimax-h3): port the MiniMax-H3 omni-modal
@@ -577,7 +580,7 @@ h3attn_status h3attn_forward_causal(h3attn_plan_t plan, const void* q, int64_t q
  *
  * h3attn_plan_set_tree adds the workspace to a plan; allocation, capture and
  * "once per plan" as h3attn_plan_set_sparse.
- * (Partial rows: 80 MB at most.)  Errors: EINVAL for a NULL plan, num_kv_heads < 1
+ * (Partial rows: 40 MB.)  Errors: EINVAL for a NULL plan, num_kv_heads < 1
  * or not a divisor of num_heads, workspace already set; EUNSUPPORTED for a document
  * of more than 64 tokens, more than 4,096 documents, 2^31 rows (tokens times heads) or 2^24 items (documents times
  * key heads times pairs of 128-row tiles) or more; ENOMEM / ECUDA. */

@@ -15,7 +15,9 @@ definitions on the pages:
 * ``oracle.fp8``        -- the FP8 (e4m3) variant: quantisers, dequantisation
                            and the error bound of the kernel's P rounding;
 * ``oracle.walks``      -- block selection, block-sparse attention, attention
-                           with a shared prefix.
+                           with a shared prefix;
+* ``oracle.serving``    -- rotary positions, causal attention with grouped
+                           heads, trees of drafts over a paged cache, row moves.
 
 Pages cited (page title, then section):
   [PR26]   vllm.cpp PR #26 "feat(minimax-h3): port the MiniMax-H3 omni-modal

@@ -40,6 +40,14 @@
 // Rows behind a sequence's last draft: their scores are masked, their V rows are
 // zeroed in shared memory before the PV reads them (0 times a stranger's NaN is not 0).
 // Every wait is bounded, as in the forward (attn_fwd_tc.cu).
+//
+// Measured, in a graph: 32 single tokens over 5,033 (32 heads, 8 key heads, pages of 16) 104 us, 6.4 TB/s, 95 % of the
+// measured copy; 512 over 300 tokens 119 us; one over 20,000 22 us, over none 10 us; 16 trees of 16 drafts (28 and 4
+// heads, 32,768 tokens) 25 us; 8 trees of 64 drafts over 20,423 (64 and 8 heads) 258 us, 1,330 TFLOP/s.  There the step of two
+// query tiles takes 3,500 cycles, 2,048 of them products: a stream's chain is 1,750 cycles of softmax (one warp an SM
+// sub-partition, bound by its own latencies), 450 until its PV is issued, 1,300 for PV and the next QK.  Two warps a row
+// would halve the softmax, but leave 96 registers a thread, which spill into the step (833 us).  Few sequences: 5,400
+// cycles until a block knows its part, 2,900 to its first loads' issue, 1,400 for them, and the join (4 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -466,8 +474,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto load = [&](const CUtensorMap* tm, bool in, int32_t page, int32_t c1, int32_t c2, uint32_t bytes, uint32_t next) {
       const uint32_t slot = entry % kSlots, bar = bars.full(slot);
       if (!__all_sync(0xffffffffu, free)) {
-        // (asked again and again: the wait that suspends a thread wakes it some 400 cycles late, 141 against
-        // 126 us for 512 sequences of 300 tokens; the softmax warps, waiting so, take the other stream's issue slots)
+        // (asked again and again before the bounded wait, whose call costs some 400 cycles: 141 against 126 us for
+        // 512 sequences of 300 tokens; softmax warps that wait so take the other stream's issue slots, 265 against 271 us
+        // for 64 drafts over 20,423 tokens)
         bool good = false;
 #pragma unroll 1
         for (int i = 0; i < 64 && !good; ++i) good = __all_sync(0xffffffffu, dev::mbar_test_wait(bars.empty(slot), ((entry / kSlots) & 1) ^ 1));

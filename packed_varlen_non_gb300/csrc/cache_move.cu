@@ -4,7 +4,8 @@
 // HBM-bound: a row is read and written once.  A block takes a group's rows of one
 // head, of k or of v: sixteen lanes a row, all of them read into registers (up to
 // 16 chunks a thread) before the barrier and written behind it, which is what
-// makes a group's moves simultaneous whatever their slots overlap in.
+// makes a group's moves simultaneous whatever their slots overlap in.  512 pages of
+// 64 rows, 8 heads: 45 us, 6.0 TB/s, 89 % of the measured copy.
 #include "device_common.cuh"
 
 namespace h3 {
