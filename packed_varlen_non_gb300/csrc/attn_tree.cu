@@ -197,14 +197,14 @@ struct Piece {
 };
 // Where a block's range begins (found once, for all roles).
 struct Start {
-  int32_t b, steps, kvh, unit, lo, row0, row1, given, item0;
+  int32_t b, steps, kvh, unit, lo, row0, row1, given;
 };
 // Walks a block's range piece by piece; every role runs its own.
 template <bool kOne>
 struct Walk {
   int32_t b, kvh, unit, lo;
   int32_t left, at;
-  int32_t item0;        // of all sequences' items, this one's first
+  int32_t item0;        // of all sequences' items, this one's first (set by the one role that wants it)
   bool first;
   Doc d;
   int32_t row2, given;  // of the next sequence: its end and length, on their way while this one runs
@@ -213,14 +213,15 @@ struct Walk {
     row2 = __ldg(a.cu + n + 1);
     given = __ldg(a.ctx_lens + n);
   }
-  __device__ void begin(const TreeArgs& a, const volatile Start& s) {
+  template <class S>
+  __device__ void begin(const TreeArgs& a, const S& s) {
     b = s.b;
     left = s.steps;
     at = 0;
     first = true;
     kvh = s.kvh;
     unit = s.unit;
-    item0 = s.item0;
+    item0 = 0;
     lo = s.lo;
     ahead(a);
     d = make_doc<kOne>(a, s.row0, s.row1, s.given);
@@ -276,6 +277,15 @@ __device__ __forceinline__ QTile q_tile(const TreeArgs& a, const Doc& d, int32_t
   return QTile{d.row0 + first, min(a.toks, d.T - first), kvh * a.group + (qt - block * a.packs) * a.pack};
 }
 
+// x / d for x < 2^22, d > 0: the reciprocal's quotient is off by less than one before it is cut off.  (Ten instructions
+// for the compiler's twenty-five: a block's first instructions take about ten cycles each, as they are fetched.)
+__device__ __forceinline__ uint32_t div_small(uint32_t x, uint32_t d) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"((float)d));
+  const uint32_t q = (uint32_t)((float)x * r);
+  const int32_t rest = (int32_t)(x - q * d);
+  return rest < 0 ? q - 1 : rest >= (int32_t)d ? q + 1 : q;
+}
 // x / n, in 32 bits where they hold it.
 __device__ __forceinline__ int64_t quotient(int64_t x, int32_t n) {
   return x < ((int64_t)1 << 32) ? (int64_t)((uint32_t)x / (uint32_t)n) : x / n;
@@ -332,16 +342,141 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sbase + kSmemQ + i), "r"(0u) : "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  __syncthreads();  // the barriers are set
   if (warp == kMmaWarp) {
     dev::tmem_alloc(dev::smem_u32(tmem_slot), kTmemCols);
     dev::tmem_relinquish();
   }
 
-  // What this block does.  Every thread adds up a run of sequences.
-  const int per = (a.n_docs + kThreads - 1) / kThreads;
-  const int b0 = min((int)threadIdx.x * per, a.n_docs), b1 = min(b0 + per, a.n_docs);
-  // the sum over all threads, and over those before this one
-  const auto scan = [&](int64_t* sums, int64_t mine, int64_t* before) {
+  // What this block does.
+  constexpr int kParts = kTwo ? 2 : 1;
+  int64_t s0[kParts], s1[kParts];  // steps (pieces) of the block, or steps of each stream
+  int64_t total = 0;               // of all
+  int32_t most = 0;                // tiles of a piece; 0: ranges
+  bool work = false;
+  Start own = {};                  // of the block (kTwo: starts, of each stream)
+  if (!kTwo && a.by_warp) {
+    // Few items, each below 2^21 tiles: every warp adds up the sequences and finds the block's piece by itself.
+    const int per = (a.n_docs + 31) / 32, b0 = min((int)lane * per, a.n_docs), b1 = min(b0 + per, a.n_docs);
+    Doc d0 = {};  // (the lane's sequence, where there is one to a lane)
+    uint32_t tiles = 0;
+    for (int b = b0; b < b1; ++b) {
+      d0 = doc_of<kTwo>(a, b);
+      tiles += (uint32_t)(d0.tiles * d0.units * a.kv_heads);
+    }
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    // About the even share and up to three tiles more, which are quicker than a second piece: the pieces of each, 16
+    // bits for each (not much above twice the blocks)
+    const uint32_t share = max(1u, (uint32_t)((float)(tiles + gridDim.x - 1) * a.inv_grid));
+    uint32_t pieces[2] = {0, 0};
+    for (int b = b0; b < b1; ++b) {
+      const Doc d = per == 1 ? d0 : doc_of<kTwo>(a, b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        pieces[i >> 1] += (uint32_t)(d.units * a.kv_heads) * div_small((uint32_t)d.tiles + share + i - 1, share + i) << 16 * (i & 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) pieces[i] = __reduce_add_sync(0xffffffffu, pieces[i]);
+#pragma unroll
+    for (int i = 3; i >= 0; --i) {
+      const uint32_t n = pieces[i >> 1] >> 16 * (i & 1) & 0xffff;
+      if (n <= gridDim.x) {
+        most = (int32_t)share + i;
+        total = n;
+      }
+    }
+    if (most > 0) {
+      uint32_t mine = 0;
+      for (int b = b0; b < b1; ++b) {
+        const Doc d = per == 1 ? d0 : doc_of<kTwo>(a, b);
+        mine += (uint32_t)(d.units * a.kv_heads) * div_small((uint32_t)(d.tiles + most - 1), (uint32_t)most);
+      }
+      uint32_t from = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, from, o);
+        if ((int)lane >= o) from += x;
+      }
+      from -= mine;
+      const uint32_t c = blockIdx.x;
+      s0[0] = c;
+      s1[0] = c + 1;
+      work = c < (uint32_t)total;
+      bool here = false;
+      for (int b = b0; b < b1; ++b) {
+        const Doc d = per == 1 ? d0 : doc_of<kTwo>(a, b);
+        const uint32_t cut = div_small((uint32_t)(d.tiles + most - 1), (uint32_t)most);  // pieces of an item
+        const uint32_t n = cut * (uint32_t)(d.units * a.kv_heads);
+        if (c - from < n) {  // (c >= from, or the difference is large)
+          const uint32_t item = div_small(c - from, cut), i = c - from - item * cut;
+          const uint32_t size = div_small((uint32_t)d.tiles, cut), rest = (uint32_t)d.tiles - size * cut;  // the first `rest` have one more
+          const int32_t kvh = (int32_t)div_small(item, (uint32_t)d.units);
+          own = Start{b, (int32_t)(size + (i < rest)), kvh, (int32_t)item - kvh * d.units, (int32_t)(size * i + min(i, rest)),
+                      d.row0, d.row0 + d.T, d.ctx};
+          here = true;
+        }
+        from += n;
+      }
+      const int src = max(0, __ffs((int)__ballot_sync(0xffffffffu, here)) - 1);
+      own = Start{__shfl_sync(0xffffffffu, own.b, src),    __shfl_sync(0xffffffffu, own.steps, src),
+                  __shfl_sync(0xffffffffu, own.kvh, src),  __shfl_sync(0xffffffffu, own.unit, src),
+                  __shfl_sync(0xffffffffu, own.lo, src),   __shfl_sync(0xffffffffu, own.row0, src),
+                  __shfl_sync(0xffffffffu, own.row1, src), __shfl_sync(0xffffffffu, own.given, src)};
+    } else {  // ranges after all
+      int64_t mine = 0;
+      for (int b = b0; b < b1; ++b) {
+        const Doc d = per == 1 ? d0 : doc_of<kTwo>(a, b);
+        mine += (int64_t)d.tiles * d.units * a.kv_heads;
+      }
+      int64_t from = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, from, o);
+        if ((int)lane >= o) from += x;
+      }
+      from -= mine;
+      total = tiles;
+      const int64_t c = blockIdx.x, parts = min((int64_t)gridDim.x, total);
+      s0[0] = s1[0] = -1;
+      if (c < parts) {
+        s0[0] = share_of(total, c, parts);
+        s1[0] = share_of(total, c + 1, parts);
+      }
+      work = s0[0] < s1[0];
+      bool here = false;
+      for (int b = b0; b < b1; ++b) {
+        const Doc d = per == 1 ? d0 : doc_of<kTwo>(a, b);
+        const int64_t n = (int64_t)d.tiles * d.units * a.kv_heads;
+        if (s0[0] >= from && s0[0] < from + n) {
+          const int32_t item = (int32_t)((uint32_t)(s0[0] - from) / (uint32_t)d.tiles), kvh = item / d.units;
+          own = Start{b, (int32_t)(s1[0] - s0[0]), kvh, item - kvh * d.units, (int32_t)((s0[0] - from) - (int64_t)item * d.tiles),
+                      d.row0, d.row0 + d.T, d.ctx};
+          here = true;
+        }
+        from += n;
+      }
+      const int src = max(0, __ffs((int)__ballot_sync(0xffffffffu, here)) - 1);
+      own = Start{__shfl_sync(0xffffffffu, own.b, src),    __shfl_sync(0xffffffffu, own.steps, src),
+                  __shfl_sync(0xffffffffu, own.kvh, src),  __shfl_sync(0xffffffffu, own.unit, src),
+                  __shfl_sync(0xffffffffu, own.lo, src),   __shfl_sync(0xffffffffu, own.row0, src),
+                  __shfl_sync(0xffffffffu, own.row1, src), __shfl_sync(0xffffffffu, own.given, src)};
+    }
+    if (blockIdx.x == 0 && warp == 0)
+      for (int b = b0; b < b1; ++b) {
+        const int32_t given = __ldg(a.ctx_lens + b);
+        if (context(a, __ldg(a.cu + b + 1) - __ldg(a.cu + b), given) != given) dev::report_bad_page(a.err);
+      }
+  } else {
+    // Every thread adds up a run of sequences; the one that finds the block's first step in its own tells all.
+    const int per = (a.n_docs + kThreads - 1) / kThreads;
+    const int b0 = min((int)threadIdx.x * per, a.n_docs), b1 = min(b0 + per, a.n_docs);
+    int64_t* const sums = reinterpret_cast<int64_t*>(smem + kSmemMl);
+    Doc d0 = {};  // (the thread's sequence, where there is one to a thread)
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      d0 = doc_of<kTwo>(a, b);
+      mine += (int64_t)d0.tiles * d0.units * a.kv_heads;
+    }
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -350,102 +485,69 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
-    int64_t total = 0;
-    *before = incl - mine;
+    int64_t before = incl - mine;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (w < (int)warp) *before += sums[w];
+      if (w < (int)warp) before += sums[w];
       total += sums[w];
     }
-    return total;
-  };
-  int64_t* const sums = reinterpret_cast<int64_t*>(smem + kSmemMl);
-  Doc d0 = {};  // (the thread's sequence, where there is one to a thread)
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    d0 = doc_of<kTwo>(a, b);
-    mine += (int64_t)d0.tiles * d0.units * a.kv_heads;
-  }
-  int64_t before, total = scan(sums, mine, &before);
-  int32_t most = 0;  // tiles of a piece; 0: ranges
-  if (!kTwo && a.items <= (int)gridDim.x) {
-    // (so there is a thread to every sequence)  The even share and up to three tiles more, which are quicker
-    // than a second piece: the pieces of each, 16 bits for each (at most twice the blocks at the even share)
-    const int32_t share = (int32_t)max((int64_t)1, min(quotient(total + gridDim.x - 1, (int32_t)gridDim.x), (int64_t)INT32_MAX / 2));
-    int64_t pieces = 0;
-    if (b0 < b1)
+    const int64_t parts = min((int64_t)gridDim.x * kParts, total);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        pieces |= (int64_t)(d0.units * a.kv_heads * (((uint32_t)d0.tiles + share + i - 1) / (uint32_t)(share + i))) << 16 * i;
-    int64_t first;
-    pieces = scan(sums + kWarps, pieces, &first);
-#pragma unroll
-    for (int i = 3; i >= 0; --i)
-      if (((pieces >> 16 * i) & 0xffff) <= (int64_t)gridDim.x) {
-        most = share + i;
-        before = (first >> 16 * i) & 0xffff;
-      }
-    if (most > 0) total = (pieces >> 16 * (most - share)) & 0xffff;
-  }
-  const int64_t grid = min((int64_t)gridDim.x * (kTwo ? 2 : 1), total);  // (blocks, or streams, that have steps)
-  constexpr int kParts = kTwo ? 2 : 1;
-  int64_t s0[kParts], s1[kParts];  // steps of the block, or of each stream
-  bool work = false;
-#pragma unroll
-  for (int x = 0; x < kParts; ++x) {
-    const int64_t c = (int64_t)blockIdx.x * kParts + x;
-    s0[x] = s1[x] = -1;
-    if (c < grid) {
-      s0[x] = most > 0 ? c : share_of(total, c, grid);
-      s1[x] = most > 0 ? c + 1 : share_of(total, c + 1, grid);
-      if (s1[x] - s0[x] > INT32_MAX / 4) {  // (hours of work: thousands of lengths of 2^31)
-        if (threadIdx.x == 0) dev::report_bad_page(a.err);
-        s0[x] = s1[x] = -1;
-      }
-    }
-    work = work || s0[x] < s1[x];
-    if (threadIdx.x == 0 && s0[x] == s1[x]) starts[x].steps = 0;
-  }
-  for (int b = b0; b < b1; ++b) {
-    const Doc d = per == 1 ? d0 : doc_of<kTwo>(a, b);
-    const int32_t cut = most > 0 ? (int32_t)(((uint32_t)d.tiles + most - 1) / (uint32_t)most) : d.tiles;  // pieces (steps) of an item
-    const int64_t n = (int64_t)cut * d.units * a.kv_heads;
-#pragma unroll
-    for (int x = 0; x < kParts; ++x)
-      if (s0[x] >= before && s0[x] < before + n) {
-        volatile Start& start = starts[x];
-        const int32_t item = (int32_t)quotient(s0[x] - before, cut), i = (int32_t)((s0[x] - before) - (int64_t)item * cut);
-        // (in pieces: tiles < 2^24, i < 2^8)
-        uint32_t lo = 0, hi = 0;
-        if (most > 0) {
-          lo = (uint32_t)d.tiles * (uint32_t)i / (uint32_t)cut;
-          hi = (uint32_t)d.tiles * (uint32_t)(i + 1) / (uint32_t)cut;
+    for (int x = 0; x < kParts; ++x) {
+      const int64_t c = (int64_t)blockIdx.x * kParts + x;
+      s0[x] = s1[x] = -1;
+      if (c < parts) {
+        s0[x] = share_of(total, c, parts);
+        s1[x] = share_of(total, c + 1, parts);
+        if (s1[x] - s0[x] > INT32_MAX / 4) {  // (hours of work: thousands of lengths of 2^31)
+          if (threadIdx.x == 0) dev::report_bad_page(a.err);
+          s0[x] = s1[x] = -1;
         }
-        const int32_t kvh = kTwo ? item : (int32_t)((uint32_t)item / (uint32_t)d.units);
-        start.b = b;
-        start.kvh = kvh;
-        start.unit = kTwo ? 0 : item - kvh * d.units;
-        start.lo = most > 0 ? (int32_t)lo : i;
-        start.steps = most > 0 ? (int32_t)(hi - lo) : (int32_t)(s1[x] - s0[x]);
-        start.row0 = d.row0;
-        start.row1 = d.row0 + d.T;
-        start.given = d.ctx;
-        start.item0 = __ldg(a.item0 + b);
       }
-    if (blockIdx.x == 0 && __ldg(a.ctx_lens + b) != d.ctx) dev::report_bad_page(a.err);
-    before += n;
+      work = work || s0[x] < s1[x];
+      if (threadIdx.x == 0 && s0[x] == s1[x]) starts[x].steps = 0;
+    }
+    for (int b = b0; b < b1; ++b) {
+      const Doc d = per == 1 ? d0 : doc_of<kTwo>(a, b);
+      const int64_t n = (int64_t)d.tiles * d.units * a.kv_heads;
+#pragma unroll
+      for (int x = 0; x < kParts; ++x)
+        if (s0[x] >= before && s0[x] < before + n) {
+          volatile Start& start = starts[x];
+          const int32_t item = (int32_t)quotient(s0[x] - before, d.tiles);
+          const int32_t kvh = kTwo ? item : (int32_t)((uint32_t)item / (uint32_t)d.units);
+          start.b = b;
+          start.kvh = kvh;
+          start.unit = kTwo ? 0 : item - kvh * d.units;
+          start.lo = (int32_t)((s0[x] - before) - (int64_t)item * d.tiles);
+          start.steps = (int32_t)(s1[x] - s0[x]);
+          start.row0 = d.row0;
+          start.row1 = d.row0 + d.T;
+          start.given = d.ctx;
+        }
+      if (blockIdx.x == 0 && __ldg(a.ctx_lens + b) != d.ctx) dev::report_bad_page(a.err);
+      before += n;
+    }
+    __syncthreads();
+    if (!kTwo && work)
+      own = Start{starts[0].b,  starts[0].steps, starts[0].kvh,  starts[0].unit,
+                  starts[0].lo, starts[0].row0,  starts[0].row1, starts[0].given};
   }
-  dev::tc_fence_before();
-  __syncthreads();
-  dev::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const int64_t grid = min((int64_t)gridDim.x * kParts, total);  // (blocks, or streams, that have steps)
+  uint32_t tmem = 0;
+  if (warp <= kMmaWarp) {  // (softmax and issuer: tensor memory is allocated)
+    dev::tc_fence_before();
+    asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * (kMmaWarp + 1)) : "memory");
+    dev::tc_fence_after();
+    tmem = *tmem_slot;
+  }
   // tiles of the block, in the order of the ring: of two ranges one tile each in turn, the longer range's first
-  const int32_t of0 = work ? starts[0].steps : 0, of1 = kTwo && work ? starts[1].steps : 0;
+  const int32_t of0 = !work ? 0 : kTwo ? starts[0].steps : own.steps, of1 = kTwo && work ? starts[1].steps : 0;
   const int32_t steps = of0 + of1;
   const int lead = kTwo && of1 > of0 ? 1 : 0;  // the stream that begins
   Walk<kTwo> walk;
   Piece p;
-  if (!kTwo && work) walk.begin(a, starts[0]);
+  if (!kTwo && work) walk.begin(a, own);
 
   if (!work) {
     // (more blocks than steps)
@@ -580,6 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           live[x] = starts[x].steps > 0;
           if (live[x]) {
             w[x].begin(a, starts[x]);
+            w[x].item0 = __ldg(a.item0 + w[x].b);
             live[x] = w[x].next(a, &y[x]);
           }
         }
@@ -616,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n[x]) dev::mbar_wait_bounded(bars.q_full(x), (n[x] - 1) & 1, nullptr, nullptr, kTimeoutNs);
       } else {
         uint32_t n = 0;
+        walk.item0 = __ldg(a.item0 + walk.b);
         while (ok && walk.next(a, &p)) {
           note(p, walk.d.tiles, blockIdx.x, s0[0]);
           for (int i = 0; ok && i < p.n_qt; ++i) {
@@ -1083,15 +1187,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t at = kTwo ? 2 * (int64_t)blockIdx.x + st : blockIdx.x;
         const int64_t part = (2 * at + (p.first ? 0 : 1)) * a.slot_rows + (!kTwo && two ? st * kRows : 0) + row;
         // (two chunks of 32 dims a turn: one chunk after the other waits for tensor memory each time)
+        constexpr int kChunks = 2;
 #pragma unroll 1
-        for (int c = c0; c < c1; c += 2) {
-          uint32_t ov[2][32];
+        for (int c = c0; c < c1; c += kChunks) {
+          uint32_t ov[kChunks][32];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) dev::tmem_ld32(t_o + (two ? st * 128 : 0) + (c + y) * 32, ov[y]);
+          for (int y = 0; y < kChunks; ++y) dev::tmem_ld32(t_o + (two ? st * 128 : 0) + (c + y) * 32, ov[y]);
           dev::tmem_wait_ld();
           if (!two) {
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
+            for (int y = 0; y < kChunks; ++y) {
               uint32_t o1[32];
               if (both) {
                 dev::tmem_ld32(t_o + 128 + (c + y) * 32, o1);
@@ -1107,7 +1212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (valid && p.whole) {
             __nv_bfloat16* const dst = a.o + (int64_t)tok * a.o_stride + (int64_t)head * kHeadDim + c * 32;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 4 * kChunks; ++e) {
               uint32_t w[4];
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
@@ -1120,7 +1225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (few pieces of a range are shared; with the transposition 512 sequences of 300 tokens took 132 us for 119)
             float* const dst = a.part_o + part * kHeadDim + c * 32;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 4 * kChunks; ++e) {
               const uint32_t(&w)[32] = ov[e >> 2];
               const int at = 8 * (e & 3);
               dev::st_global_v8(dst + 8 * e, w[at], w[at + 1], w[at + 2], w[at + 3], w[at + 4], w[at + 5], w[at + 6], w[at + 7]);
@@ -1130,7 +1235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float* const dst = a.part_o + (part - (lane & 3)) * kHeadDim + c * 32 + 8 * (lane & 3);
             const int32_t rows = q.n_tok * a.pack - (int32_t)(row & ~3u);  // of this row's four on
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
+            for (int y = 0; y < kChunks; ++y) {
               uint32_t(&w)[32] = ov[y];
               transpose4(w, lane);
 #pragma unroll
@@ -1328,6 +1433,8 @@ cudaError_t launch_attn_tree(const TreeArgs& args, const void* q, int64_t q_stri
   while ((1ll << bits) < a.page_boxes) ++bits;
   a.page_shift = 29 + bits;
   a.page_mul = (uint32_t)(((1ull << a.page_shift) + a.page_boxes - 1) / a.page_boxes);
+  a.inv_grid = 1.f / (float)a.grid;
+  a.by_warp = !two && a.items <= a.grid && (int64_t)a.table_width * a.page_size < ((int64_t)1 << 28);
   a.recip_toks = (65536u + (uint32_t)a.toks - 1) / (uint32_t)a.toks;
   CUtensorMap mq, mk, mv;
   {

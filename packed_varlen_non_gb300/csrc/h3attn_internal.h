@@ -494,6 +494,8 @@ struct TreeArgs {
   uint32_t* err;
   // (the launcher's)
   uint32_t recip, recip_toks;  // row / pack = row * recip >> 16, and of toks
+  float inv_grid;              // 1 / grid
+  int32_t by_warp;             // not more items than blocks, each below 2^21 tiles
   int32_t page_size, n_pages;
   int32_t box;                 // rows of the cache that a copy takes: gcd(page_size, 128)
   int32_t n_box, at_once;      // boxes of a 128-key tile, tiles of 32 boxes
