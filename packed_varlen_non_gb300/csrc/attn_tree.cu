@@ -277,7 +277,7 @@ __device__ __forceinline__ QTile q_tile(const TreeArgs& a, const Doc& d, int32_t
   return QTile{d.row0 + first, min(a.toks, d.T - first), kvh * a.group + (qt - block * a.packs) * a.pack};
 }
 
-// x / d for x < 2^22, d > 0: the reciprocal's quotient is off by less than one before it is cut off.  (Ten instructions
+// x / d for x < 2^24, d > 0, x / d < 2^22: the reciprocal's quotient is off by less than one before it is cut off.  (Ten instructions
 // for the compiler's twenty-five: a block's first instructions take about ten cycles each, as they are fetched.)
 __device__ __forceinline__ uint32_t div_small(uint32_t x, uint32_t d) {
   float r;
@@ -365,15 +365,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       tiles += (uint32_t)(d0.tiles * d0.units * a.kv_heads);
     }
     tiles = __reduce_add_sync(0xffffffffu, tiles);
-    // About the even share and up to three tiles more, which are quicker than a second piece: the pieces of each, 16
-    // bits for each (not much above twice the blocks)
+    // About the even share and three lengths above it, which are quicker than a second piece: up to three tiles more,
+    // or, where an item is one query tile, up to a quarter (memory sets the time, and a block can take more than its
+    // share of it: 16 sequences of 5,033 tokens, 128 items of 40 tiles, 57.9 against 60.3 us; up to five eighths was
+    // slower, 12 of 20,423 tokens 184 for 155).  The pieces of each, 16 bits for each (not much above twice the blocks).
     const uint32_t share = max(1u, (uint32_t)((float)(tiles + gridDim.x - 1) * a.inv_grid));
+    const uint32_t more = a.slot_rows == kRows ? share / 8 : 0;
+    const auto length = [&](int i) { return share + max((uint32_t)i, min(i, 2) * more); };
     uint32_t pieces[2] = {0, 0};
     for (int b = b0; b < b1; ++b) {
       const Doc d = per == 1 ? d0 : doc_of<kTwo>(a, b);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        pieces[i >> 1] += (uint32_t)(d.units * a.kv_heads) * div_small((uint32_t)d.tiles + share + i - 1, share + i) << 16 * (i & 1);
+        pieces[i >> 1] += (uint32_t)(d.units * a.kv_heads) * div_small((uint32_t)d.tiles + length(i) - 1, length(i)) << 16 * (i & 1);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) pieces[i] = __reduce_add_sync(0xffffffffu, pieces[i]);
@@ -381,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 3; i >= 0; --i) {
       const uint32_t n = pieces[i >> 1] >> 16 * (i & 1) & 0xffff;
       if (n <= gridDim.x) {
-        most = (int32_t)share + i;
+        most = (int32_t)length(i);
         total = n;
       }
     }
