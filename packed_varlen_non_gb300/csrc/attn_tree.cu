@@ -42,12 +42,12 @@
 // Every wait is bounded, as in the forward (attn_fwd_tc.cu).
 //
 // Measured, in a graph: 32 single tokens over 5,033 (32 heads, 8 key heads, pages of 16) 104 us, 6.4 TB/s, 95 % of the
-// measured copy; 512 over 300 tokens 119 us; one over 20,000 22 us, over none 10 us; 16 trees of 16 drafts (28 and 4
+// measured copy; 512 over 300 tokens 112 to 114 us; one over 20,000 21 us, over none 9.4 us; 16 trees of 16 drafts (28 and 4
 // heads, 32,768 tokens) 25 us; 8 trees of 64 drafts over 20,423 (64 and 8 heads) 258 us, 1,330 TFLOP/s.  There the step of two
 // query tiles takes 3,500 cycles, 2,048 of them products: a stream's chain is 1,750 cycles of softmax (one warp an SM
 // sub-partition, bound by its own latencies), 450 until its PV is issued, 1,300 for PV and the next QK.  Two warps a row
-// would halve the softmax, but leave 96 registers a thread, which spill into the step (833 us).  Few sequences: 5,400
-// cycles until a block knows its part, 2,900 to its first loads' issue, 1,400 for them, and the join (4 us).
+// would halve the softmax, but leave 96 registers a thread, which spill into the step (833 us).  Few sequences: 4,500
+// cycles until a block knows its part, 2,800 to its first loads' issue, 1,400 to 2,400 for them, and the join (4 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 

@@ -166,6 +166,33 @@ def test_scores_that_step_up_between_halves_of_a_tile(lib, steps, ctx, drafts):
     t.check(*t.forward(), what=steps)
 
 
+@pytest.mark.parametrize("ctx,drafts,heads,kv", [
+    ([(53 * i * i) % 1400 for i in range(140)], [1 + i % 3 for i in range(140)], 4, 1),   # a block to an item and a bit: ranges, one tile
+    ([(53 * i * i) % 1400 for i in range(120)], [16 + i % 9 for i in range(120)], 16, 1),  # and up to three tiles an item
+    ([(53 * i * i) % 1400 for i in range(70)], [40] * 70, 32, 2),   # more items than blocks, of two tiles and of one
+    ([700 + 9 * i for i in range(100)], [1] * 100, 8, 1),           # pieces, several sequences to a lane
+    ([1200] * 33, [2] * 33, 8, 4)])                                 # pieces above the even share
+def test_every_way_of_cutting_the_work(lib, ctx, drafts, heads, kv):
+    t = Tree(ctx, drafts, heads, kv, 32)
+    first = t.forward()
+    t.check(*first)
+    again = t.forward()
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_a_table_for_very_long_sequences(lib):
+    # 2^28 rows and more to a sequence's table: the lengths are added up another way
+    ctx, page = [4000, 130, 1], 1 << 16
+    t = Tree(ctx, [3, 1, 64], 8, 1, page)
+    t.check(*t.forward())
+    wide = torch.full((3, (1 << 28) // page + 1), -9, dtype=torch.int32, device="cuda")
+    wide[:, :t.table.shape[1]] = t.d_table
+    t.d_table = wide
+    o, lse = t.forward()
+    t.table = wide.cpu().numpy()
+    t.check(o, lse)
+
+
 def test_stacked_layers_strides_and_guards(lib):
     # a cache whose layers, k and v share one buffer; q out of a fused one; o with guards
     ctx, drafts, heads, kv, page = [300, 40], [6, 1], 6, 2, 16
