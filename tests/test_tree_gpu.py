@@ -168,7 +168,7 @@ def test_scores_that_step_up_between_halves_of_a_tile(lib, steps, ctx, drafts):
 
 @pytest.mark.parametrize("ctx,drafts,heads,kv", [
     ([(53 * i * i) % 1400 for i in range(140)], [1 + i % 3 for i in range(140)], 4, 1),   # a block to an item and a bit: ranges, one tile
-    ([(53 * i * i) % 1400 for i in range(120)], [9 + i % 8 for i in range(120)], 16, 1),   # and two tiles
+    ([(53 * i * i) % 1400 for i in range(140)], [9 + i % 8 for i in range(140)], 16, 1),   # and two tiles
     ([(53 * i * i) % 1400 for i in range(70)], [40] * 70, 32, 2),   # more items than blocks, of two tiles and of one
     ([700 + 9 * i for i in range(100)], [1] * 100, 8, 1),           # pieces, several sequences to a lane
     ([1200] * 33, [2] * 33, 8, 4)])                                 # pieces above the even share
