@@ -665,6 +665,18 @@ h3attn_status h3attn_selftest_bounded_wait(uint64_t timeout_ns, void* cuda_strea
  * Errors: EINVAL for a NULL plan or a limit out of range. */
 h3attn_status h3attn_selftest_plan_wait(h3attn_plan_t plan, uint64_t timeout_ns, void* cuda_stream);
 
+/* Launches the tree forward's second kernel, which joins the pieces of shared
+ * items, by itself: with joins = NULL as behind a forward that stopped before it
+ * reached any item, on the entries that the plan has; else on joins (int32
+ * [n_joins, 2] on the device: first partial slot and pieces of each item, n_joins
+ * as many as the plan has) in their place.  Items of fewer than two pieces, and
+ * entries that name slots the workspace has not, leave their rows of o and lse_out
+ * (may be NULL) as they are.  Asynchronous on cuda_stream.
+ * Errors: EINVAL for a NULL plan or one without h3attn_plan_set_tree, another
+ * number of entries, and bad tensors as in h3attn_forward_tree. */
+h3attn_status h3attn_selftest_tree_join(h3attn_plan_t plan, const int32_t* joins, int64_t n_joins, void* o, int64_t o_row_stride,
+                                        float* lse_out, void* cuda_stream);
+
 /* Message for the last failing call on this host thread ("" if none). */
 const char* h3attn_last_error(void);
 

@@ -1298,11 +1298,19 @@ __device__ __forceinline__ void add(Acc& x, float m, float l, const float4& o) {
   x.m = top;
 }
 
+// Pieces of an item that the join is to combine: none of one that a single block wrote, none where the entry names slots
+// that do not exist (a forward that stopped early leaves entries as they were).
+__device__ __forceinline__ int32_t pieces_of(const int2& x, int32_t slots) {
+  const bool there = x.y > 1 && x.y <= slots && (uint32_t)x.x < (uint32_t)slots && (x.x | 1) + 2 * x.y - 3 < slots;
+  return there ? x.y : 0;
+}
+
 // kRowsOf rows a warp, whose loads go out together: many rows have few pieces each
 // (32,768 of two: 23 us with a row a warp, 11 with two rows).  0: one row a block, whose warps
-// share out its pieces (32 rows of 18: 30 us less than a row after the other).
+// share out its pieces (32 rows of 18: 30 us less than a row after the other).  A row a warp: five blocks an
+// SM, 48 registers a thread (52 bytes spilled), so that its rows are one wave; the others have four, 64 registers.
 template <int kRowsOf>
-__global__ void __launch_bounds__(32 * kJoinWarps, kRowsOf > 1 ? 4 : 5) attn_tree_join_kernel(const __grid_constant__ TreeArgs a) {
+__global__ void __launch_bounds__(32 * kJoinWarps, kRowsOf == 1 ? 5 : 4) attn_tree_join_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int kN = kRowsOf > 1 ? kRowsOf : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t n_rows = (uint32_t)a.S * (uint32_t)a.H;  // (below 2^31)
@@ -1323,7 +1331,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, kRowsOf > 1 ? 4 : 5) attn_tre
   for (int e = 0; e < kN; ++e) {
     const int2 x = a.joins[item[e]];
     slot[e] = x.x;
-    n[e] = x.y == 1 || id + e >= n_rows ? 0 : x.y;  // (a block's whole items are written by it)
+    n[e] = id + e >= n_rows ? 0 : pieces_of(x, a.slots);
   }
   // piece i of a row: its block's first slot, but for the first one
   const auto load = [&](int32_t first, int32_t in_slot, int32_t i, float2* ml, float4* o) {
@@ -1411,11 +1419,13 @@ bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, 
 
 }  // namespace
 
+// More items than blocks, a query tile each: a block's streams have ranges of their own.
+static bool two_ranges(const TreeArgs& a) { return a.slot_rows == kRows && a.items > a.grid; }
+
 cudaError_t launch_attn_tree(const TreeArgs& args, const void* q, int64_t q_stride, const h3attn_cache& c, cudaStream_t stream,
                              std::string* why) {
   static SmemAttr attr, attr_two;
-  // more items than blocks, a query tile each
-  const bool two = args.slot_rows == kRows && args.items > args.grid;
+  const bool two = two_ranges(args);
   cudaError_t e = two ? attr_two.set(attn_tree_kernel<true>, (int)kSmemAlloc) : attr.set(attn_tree_kernel<false>, (int)kSmemAlloc);
   if (e != cudaSuccess) {
     *why = "cudaFuncSetAttribute(max dynamic shared memory) failed";
@@ -1462,7 +1472,13 @@ cudaError_t launch_attn_tree(const TreeArgs& args, const void* q, int64_t q_stri
   else
     attn_tree_kernel<false><<<(unsigned)a.grid, kThreads, kSmemAlloc, stream>>>(mq, mk, mv, a);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  return e != cudaSuccess ? e : launch_tree_join(a, stream, why);
+}
+
+cudaError_t launch_tree_join(const TreeArgs& args, cudaStream_t stream, std::string* why) {
+  TreeArgs a = args;
+  a.slots = (two_ranges(a) ? 4 : 2) * a.grid;
+  cudaError_t e = cudaSuccess;
   // Few items have many pieces each (about the blocks by the items): a block a row (1,024 rows of two
   // or three: 7.6 us, 3.7 with a row a warp).  Else a row a warp while that is one wave, five blocks an SM.
   // (Rows are below 2^31.)

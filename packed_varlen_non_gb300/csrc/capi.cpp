@@ -1361,6 +1361,8 @@ h3attn_status h3attn_plan_set_tree(h3attn_plan_t plan, int32_t num_kv_heads, voi
   if (e == cudaSuccess) e = cudaMalloc(&t.d_joins, (size_t)t.items * sizeof(int2));
   if (e == cudaSuccess) e = cudaMalloc(&t.d_part_o, rows * kHeadDim * sizeof(float));
   if (e == cudaSuccess) e = cudaMalloc(&t.d_part_ml, rows * sizeof(float2));
+  // (no pieces: a forward whose wait runs out leaves the entries of the items that it did not reach)
+  if (e == cudaSuccess) e = cudaMemsetAsync(t.d_joins, 0, (size_t)t.items * sizeof(int2), st);
   if (e == cudaSuccess) e = cudaMemcpyAsync(t.d_item0, item0.data(), item0.size() * sizeof(int32_t), cudaMemcpyHostToDevice, st);
   if (e == cudaSuccess) e = cudaMemcpyAsync(t.d_rows, token.data(), token.size() * sizeof(TreeRow), cudaMemcpyHostToDevice, st);
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
@@ -1373,6 +1375,38 @@ h3attn_status h3attn_plan_set_tree(h3attn_plan_t plan, int32_t num_kv_heads, voi
   tp = t;
   return H3ATTN_OK;
 }
+
+namespace {
+
+// What the tree forward and its join have of the plan and the outputs.
+TreeArgs tree_args(const Plan* plan, void* o, int64_t o_row_stride, float* lse_out) {
+  const TreePlan& tp = plan->tree;
+  TreeArgs a{};
+  a.cu = plan->d_cu;
+  a.rows = tp.d_rows;
+  a.S = plan->S;
+  a.n_docs = plan->n_docs;
+  a.H = plan->num_heads;
+  a.kv_heads = tp.kv_heads;
+  a.group = plan->num_heads / tp.kv_heads;
+  a.pack = tp.pack;
+  a.toks = tp.toks;
+  a.packs = a.group / tp.pack;
+  a.slot_rows = tp.slot_rows;
+  a.grid = tp.grid;
+  a.items = tp.items;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.o_stride = o_row_stride;
+  a.lse = lse_out;
+  a.item0 = tp.d_item0;
+  a.joins = tp.d_joins;
+  a.part_o = tp.d_part_o;
+  a.part_ml = tp.d_part_ml;
+  a.err = plan->d_err;
+  return a;
+}
+
+}  // namespace
 
 h3attn_status h3attn_forward_tree(h3attn_plan_t plan, const void* q, int64_t q_row_stride, const h3attn_cache* cache,
                                   const int32_t* page_table, int32_t table_width, const int32_t* ctx_lens,
@@ -1409,33 +1443,12 @@ h3attn_status h3attn_forward_tree(h3attn_plan_t plan, const void* q, int64_t q_r
   DeviceGuard g;
   cudaError_t e = g.enter(plan->device);
   if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
-  TreeArgs a{};
-  a.cu = plan->d_cu;
-  a.rows = tp.d_rows;
+  TreeArgs a = tree_args(plan, o, o_row_stride, lse_out);
   a.ctx_lens = ctx_lens;
   a.page_table = page_table;
   a.tree_mask = tree_mask;
-  a.S = S;
-  a.n_docs = plan->n_docs;
-  a.H = plan->num_heads;
-  a.kv_heads = tp.kv_heads;
-  a.group = plan->num_heads / tp.kv_heads;
   a.table_width = table_width;
-  a.pack = tp.pack;
-  a.toks = tp.toks;
-  a.packs = a.group / tp.pack;
-  a.slot_rows = tp.slot_rows;
-  a.grid = tp.grid;
-  a.items = tp.items;
   a.scale_log2 = softmax_scale * 1.4426950408889634f;
-  a.o = static_cast<__nv_bfloat16*>(o);
-  a.o_stride = o_row_stride;
-  a.lse = lse_out;
-  a.item0 = tp.d_item0;
-  a.joins = tp.d_joins;
-  a.part_o = tp.d_part_o;
-  a.part_ml = tp.d_part_ml;
-  a.err = plan->d_err;
   std::string why;
   e = launch_attn_tree(a, q, q_row_stride, *cache, static_cast<cudaStream_t>(cuda_stream), &why);
   if (e != cudaSuccess) {
@@ -1494,6 +1507,27 @@ h3attn_status h3attn_selftest_plan_wait(h3attn_plan_t plan, uint64_t timeout_ns,
   cudaError_t e = g.enter(plan->device);
   if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
   e = launch_selftest_bounded_wait(timeout_ns, plan->d_err, static_cast<cudaStream_t>(cuda_stream));
+  return e == cudaSuccess ? H3ATTN_OK : cuda_fail(e, "selftest launch");
+}
+
+h3attn_status h3attn_selftest_tree_join(h3attn_plan_t plan, const int32_t* joins, int64_t n_joins, void* o, int64_t o_row_stride,
+                                        float* lse_out, void* cuda_stream) {
+  clear_error();
+  if (h3attn_status s = check_plan(plan)) return s;
+  if (!plan->tree.set) return fail(H3ATTN_EINVAL, "h3attn_plan_set_tree has not been called on this plan");
+  const Rows ro{"o", o, o_row_stride, plan->num_heads};
+  if (h3attn_status s = check_rows(ro, plan->S)) return s;
+  if (!aligned4(lse_out) || (reinterpret_cast<uintptr_t>(joins) & 7u))
+    return fail(H3ATTN_EINVAL, "lse_out must be 4-byte and joins 8-byte aligned");
+  if (joins && n_joins != plan->tree.items)
+    return fail(H3ATTN_EINVAL, "joins must have an entry for each of the %d items (got %lld)", plan->tree.items, (long long)n_joins);
+  DeviceGuard g;
+  cudaError_t e = g.enter(plan->device);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+  TreeArgs a = tree_args(plan, o, o_row_stride, lse_out);
+  if (joins) a.joins = reinterpret_cast<int2*>(const_cast<int32_t*>(joins));  // (the join reads it)
+  std::string why;
+  e = launch_tree_join(a, static_cast<cudaStream_t>(cuda_stream), &why);
   return e == cudaSuccess ? H3ATTN_OK : cuda_fail(e, "selftest launch");
 }
 

@@ -488,13 +488,14 @@ struct TreeArgs {
   int64_t o_stride;
   float* lse;
   const int32_t* item0;        // [n_docs]
-  int2* joins;                 // [items]
+  int2* joins;                 // [items]; pieces below two: none to join
   float* part_o;
   float2* part_ml;
   uint32_t* err;
   // (the launcher's)
   uint32_t recip, recip_toks;  // row / pack = row * recip >> 16, and of toks
   float inv_grid;              // 1 / grid
+  int32_t slots;               // partial slots: two a block, or a stream
   int32_t by_warp;             // not more items than blocks, each below 2^21 tiles
   int32_t page_size, n_pages;
   int32_t box;                 // rows of the cache that a copy takes: gcd(page_size, 128)
@@ -505,6 +506,7 @@ struct TreeArgs {
 };
 cudaError_t launch_attn_tree(const TreeArgs& a, const void* q, int64_t q_stride, const h3attn_cache& cache, cudaStream_t stream,
                              std::string* why);
+cudaError_t launch_tree_join(const TreeArgs& a, cudaStream_t stream, std::string* why);  // (its second launch)
 
 // Block scores and selection (block_select.cu).
 struct SelectArgs {

@@ -111,6 +111,7 @@ _SIGS = {
     "h3attn_get_device_error": [c_void_p, c_void_p],
     "h3attn_selftest_bounded_wait": [c_uint64, c_void_p],
     "h3attn_selftest_plan_wait": [c_void_p, c_uint64, c_void_p],
+    "h3attn_selftest_tree_join": [c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p],
 }
 
 _lib = None
@@ -752,6 +753,19 @@ def h3attn_selftest_bounded_wait(timeout_ns: int, stream=None) -> int:
 def h3attn_selftest_plan_wait(plan, timeout_ns: int, stream=None):
     """A wait that runs out, recorded in the plan's device error word."""
     _check(load().h3attn_selftest_plan_wait(plan, int(timeout_ns), _plan_stream(plan, stream)), "h3attn_selftest_plan_wait")
+
+
+def h3attn_selftest_tree_join(plan, o, lse=None, joins=None, o_row_stride=None, stream=None):
+    """The tree forward's join by itself, on the plan's entries or on joins (int32 [items, 2])."""
+    sizes = _plan_rows.get(plan)
+    stride = _rows((o,), o_row_stride, sizes[0] if sizes else 0, sizes)
+    _check_lse(lse, sizes)
+    n = 0
+    if joins is not None:
+        n = joins.shape[0]
+        _ints(joins, "joins", (n, 2), o.get_device())
+    _check(load().h3attn_selftest_tree_join(plan, _ptr(joins), n, _ptr(o), stride, _ptr(lse), _plan_stream(plan, stream)),
+           "h3attn_selftest_tree_join")
 
 
 class Plan:
