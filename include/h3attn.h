@@ -506,7 +506,8 @@ h3attn_status h3attn_rotary(const h3attn_rope* rope, const int32_t* positions, i
  * [n_pages, page_size, num_kv_heads, 128], element (page, token, head, dim) at
  * page*page_stride + token*token_stride + head*head_stride + dim, so that a page
  * may hold a token's heads together or a head's tokens.  Strides (elements, the same for k
- * and v) are multiples of 8, rows must not share elements; 16-byte aligned.
+ * and v) are multiples of 8, rows must not share elements, k's with v's neither
+ * (which may lie between them, in one buffer); 16-byte aligned.
  * A slot is a row of the cache: page * page_size + token, below 2^31 in all. */
 typedef struct {
   void* k;

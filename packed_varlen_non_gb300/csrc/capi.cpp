@@ -1052,6 +1052,24 @@ bool rows_overlap(const Rows& a, const Rows& b, int64_t n) {
   return r < a.width() || r + b.width() > a.stride;
 }
 
+// A dimension of the cache's rows.
+struct CacheDim {
+  int64_t n, stride;
+};
+
+// Whether a row of the cache `delta` elements on meets a row: d[0 .. dims) sorted by stride, each stride past what the
+// smaller ones span, so that only the two multiples of a stride around delta come near it.
+bool rows_meet(const CacheDim* d, int dims, int64_t delta) {
+  if (dims == 0) return delta > -kHeadDim && delta < kHeadDim;
+  const CacheDim& x = d[dims - 1];
+  if (x.n == 1) return rows_meet(d, dims - 1, delta);
+  int64_t i = delta / x.stride;
+  if (delta % x.stride < 0) --i;
+  for (int64_t at = i; at <= i + 1; ++at)
+    if (at > -x.n && at < x.n && rows_meet(d, dims - 1, delta - at * x.stride)) return true;
+  return false;
+}
+
 h3attn_status check_cache(const h3attn_cache* c) {
   if (!c || !c->k || !c->v) return fail(H3ATTN_EINVAL, "NULL cache or cache tensor");
   if (!aligned16(c->k) || !aligned16(c->v)) return fail(H3ATTN_EINVAL, "the cache's tensors must be 16-byte aligned");
@@ -1060,19 +1078,19 @@ h3attn_status check_cache(const h3attn_cache* c) {
                 c->num_kv_heads);
   if ((int64_t)c->n_pages * c->page_size > INT32_MAX) return fail(H3ATTN_EINVAL, "the cache has 2^31 or more slots");
   // rows share no element where every stride reaches past what the smaller ones span
-  struct Dim {
-    int64_t n, stride;
-  } d[3] = {{c->n_pages, c->page_stride}, {c->page_size, c->token_stride}, {c->num_kv_heads, c->head_stride}};
-  std::sort(d, d + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+  CacheDim d[3] = {{c->n_pages, c->page_stride}, {c->page_size, c->token_stride}, {c->num_kv_heads, c->head_stride}};
+  std::sort(d, d + 3, [](const CacheDim& x, const CacheDim& y) { return x.stride < y.stride; });
   int64_t span = kHeadDim;
-  for (const Dim& x : d) {
+  for (const CacheDim& x : d) {
     if (x.stride < 0 || x.stride % 8) return fail(H3ATTN_EINVAL, "the cache's strides must be multiples of 8 (got %lld)", (long long)x.stride);
     if (x.n == 1) continue;
     if (x.stride < span || x.stride > (int64_t(1) << 38) || x.stride > (int64_t(1) << 60) / x.n)
       return fail(H3ATTN_EINVAL, "the cache's rows share elements, or lie too far apart (stride %lld)", (long long)x.stride);
     span += (x.n - 1) * x.stride;
   }
-  if (c->k == c->v) return fail(H3ATTN_EINVAL, "the cache's k and v are the same");
+  // (v's rows may lie between k's; the distance of addresses below 2^63 in elements)
+  const int64_t delta = ((int64_t)reinterpret_cast<uintptr_t>(c->v) - (int64_t)reinterpret_cast<uintptr_t>(c->k)) / 2;
+  if (rows_meet(d, 3, delta)) return fail(H3ATTN_EINVAL, "the cache's k and v share elements");
   return H3ATTN_OK;
 }
 
