@@ -536,8 +536,8 @@ h3attn_status h3attn_rotary_store(const h3attn_rope* rope, const int32_t* positi
  * group's sources are read before its first destination is written, so accepted
  * drafts move up past one another, rows change places and pages are forked; a
  * pair with a slot that is not a row of the cache is left out (padding: -1).  A
- * slot may be a source any number of times.  No group may write a slot that another one names, and of
- * equal destinations any one may stay.  n_groups = 0 is allowed.  Runs on the
+ * slot may be a source any number of times; of a group's pairs with equal destinations (and not left out)
+ * the last one's row stays.  No group may write a slot that another one names.  n_groups = 0 is allowed.  Runs on the
  * current device, as h3attn_rotary.
  * Errors: EINVAL for a bad cache (above), NULL or misaligned lists, n_groups < 0
  * or above 2^31 - 1, lists that overlap the cache; EUNSUPPORTED for width outside [1, 256] or more

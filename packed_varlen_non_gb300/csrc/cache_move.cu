@@ -4,8 +4,12 @@
 // HBM-bound: a row is read and written once.  A block takes a group's rows of one
 // head, of k or of v: sixteen lanes a row, all of them read into registers (up to
 // 16 chunks a thread) before the barrier and written behind it, which is what
-// makes a group's moves simultaneous whatever their slots overlap in.  512 pages of
-// 64 rows, 8 heads: 45 us, 6.0 TB/s, 89 % of the measured copy.
+// makes a group's moves simultaneous whatever their slots overlap in.  Every row's
+// lanes hold the group's list among them: of equal destinations the last pair's
+// row is written, which each row finds out with comparisons and a vote while its
+// loads are on their way (from a list in shared memory 0.6 us more for 2,048 pages of
+// 16 rows; behind the barrier 12 us more for 512 of 64).  512 pages of 64 rows, 8
+// heads: 42 us, 6.3 TB/s, 95 % of the measured copy; 2,048 of 16 rows 51 us.
 #include "device_common.cuh"
 
 namespace h3 {
@@ -17,7 +21,7 @@ constexpr int kRows = kThreads / 16;  // rows in work at once
 
 // kN: chunks of a thread (groups of up to 16 kN rows).
 template <int kN>
-__global__ void __launch_bounds__(kThreads) cache_move_kernel(const __grid_constant__ CacheMoveArgs a) {
+__global__ void __launch_bounds__(kThreads, kN <= 4 ? 8 : 2) cache_move_kernel(const __grid_constant__ CacheMoveArgs a) {
   const int c = threadIdx.x & 15, r0 = threadIdx.x >> 4;
   const int64_t list = (int64_t)blockIdx.x * a.width;
   __nv_bfloat16* const rows = ((blockIdx.z != 0) ? a.v : a.k) + (int64_t)blockIdx.y * a.head_stride + 8 * c;
@@ -25,21 +29,32 @@ __global__ void __launch_bounds__(kThreads) cache_move_kernel(const __grid_const
     const int32_t page = slot / a.page_size;
     return reinterpret_cast<uint4*>(rows + page * a.page_stride + (int64_t)(slot - page * a.page_size) * a.token_stride);
   };
-  int32_t to[kN];
+  // every row's sixteen lanes hold the group's pairs, pair c + 16 i in lane c; a row's own one is its lane r0's
+  const int own = (threadIdx.x & 16) | r0;
+  int32_t src[kN], dst[kN], to[kN];
   uint4 x[kN];
 #pragma unroll
   for (int i = 0; i < kN; ++i) {
-    const int r = r0 + i * kRows;
-    int32_t from = -1;
-    to[i] = -1;
-    if (r < a.width) {
-      from = __ldg(a.src + list + r);
-      to[i] = __ldg(a.dst + list + r);
+    const int p = c + i * kRows;
+    src[i] = dst[i] = -1;
+    if (p < a.width) {
+      src[i] = __ldg(a.src + list + p);
+      dst[i] = __ldg(a.dst + list + p);
     }
-    if ((uint32_t)from >= (uint32_t)a.n_slots || (uint32_t)to[i] >= (uint32_t)a.n_slots)
-      to[i] = -1;
-    else
-      x[i] = *at(from);
+    if ((uint32_t)src[i] >= (uint32_t)a.n_slots || (uint32_t)dst[i] >= (uint32_t)a.n_slots) dst[i] = -1;  // left out
+  }
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const int32_t from = __shfl_sync(0xffffffffu, src[i], own);
+    to[i] = __shfl_sync(0xffffffffu, dst[i], own);
+    if (to[i] >= 0) x[i] = *at(from);
+  }
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    bool again = c > r0 && dst[i] == to[i];
+#pragma unroll
+    for (int j = i + 1; j < kN; ++j) again = again || dst[j] == to[i];
+    if ((__ballot_sync(0xffffffffu, again) >> (threadIdx.x & 16) & 0xffffu) != 0) to[i] = -1;
   }
   __syncthreads();
 #pragma unroll
