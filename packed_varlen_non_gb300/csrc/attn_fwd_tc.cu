@@ -2279,14 +2279,17 @@ cudaError_t launch_forward_causal(const ForwardArgs& a, const WalkArgs& w, cudaS
   walk.recip = (65536u + (uint32_t)w.pack - 1) / (uint32_t)w.pack;
   walk.group = a.H / w.kv_heads;
   ForwardMaps m;
-  const uint64_t S = (uint64_t)a.S, kv_width = (uint64_t)w.kv_heads * kHeadDim, kv_row = (uint64_t)w.kv_stride * 2;
-  if (!make_map_heads(&m.q, a.q, (uint64_t)a.H, S, (uint64_t)a.qkv_stride * 2, (uint32_t)walk.pack, (uint32_t)walk.toks, why) ||
+  // (bytes from row to row; one row has no stride: a map's is below 2^40)
+  const auto step = [&](int64_t stride, uint64_t width) { return a.S > 1 ? (uint64_t)stride * 2 : width * 2; };
+  const uint64_t S = (uint64_t)a.S, width = (uint64_t)a.H * kHeadDim, kv_width = (uint64_t)w.kv_heads * kHeadDim;
+  const uint64_t kv_row = step(w.kv_stride, kv_width);
+  if (!make_map_heads(&m.q, a.q, (uint64_t)a.H, S, step(a.qkv_stride, width), (uint32_t)walk.pack, (uint32_t)walk.toks, why) ||
       !make_map(&m.k, a.k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kv_width, S, kv_row, kTileRows / 2, why) ||
       !make_map(&m.v, a.v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kv_width, S, kv_row, kTileRows, why))
     return cudaErrorInvalidValue;
   std::memset(&m.o, 0, sizeof(m.o));
   // (O tiles go out by TMA where a warp's 32 rows are whole tokens)
-  m.o_tma = 32 % walk.pack == 0 && make_map_heads(&m.o, a.o, (uint64_t)a.H, S, (uint64_t)a.o_stride * 2, (uint32_t)walk.pack,
+  m.o_tma = 32 % walk.pack == 0 && make_map_heads(&m.o, a.o, (uint64_t)a.H, S, step(a.o_stride, width), (uint32_t)walk.pack,
                                                   32u / (uint32_t)walk.pack, nullptr);
   return w.pair ? launch_walk<kWalkCausal, true>(m, a, w, walk, stream, why)
                 : launch_walk<kWalkCausal, false>(m, a, w, walk, stream, why);

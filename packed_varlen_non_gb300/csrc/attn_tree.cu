@@ -1456,7 +1456,8 @@ cudaError_t launch_attn_tree(const TreeArgs& args, const void* q, int64_t q_stri
   CUtensorMap mq, mk, mv;
   {
     const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)a.H, (cuuint64_t)a.S};
-    const cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)q_stride * 2};
+    // (one row has no stride: a map's is below 2^40 bytes)
+    const cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)(a.S > 1 ? q_stride : (int64_t)a.H * kHeadDim) * 2};
     const cuuint32_t box[3] = {64, (cuuint32_t)a.pack, (cuuint32_t)a.toks};
     if (!encode(&mq, q, 3, dims, strides, box, why)) return cudaErrorInvalidValue;
   }
