@@ -442,7 +442,8 @@ h3attn_status h3attn_walk_list_host(int32_t kind, const int32_t* cu_seqlens, int
  *     LINEAR    f_j / factor
  *     NTK       f_j of the base  base factor^(d/(d-2))
  *     BY_PARTS  f_j (g + (1 - g)/factor),  g = clamp((original_len f_j/(2 pi) -
- *               beta_slow)/(beta_fast - beta_slow), 0, 1)
+ *               beta_slow)/(beta_fast - beta_slow), 0, 1): a ramp over the turns
+ *               that a pair makes in original_len, not over the pair's index j
  * A = amplitude, or where that is 0: 0.1 ln(factor) + 1 BY_PARTS, else 1.  axis:
  * the position axis of each pair (rope_dims/2 bytes below n_axes), NULL for axis
  * 0; so (t, h, w) positions may take sections or every third pair.
@@ -470,7 +471,9 @@ typedef struct {
 } h3attn_rope_opts;
 
 /* What the rotary calls need of it: plain data of the caller's, read by each
- * call before it returns. */
+ * call before it returns.  turns and amplitude of one that h3attn_rope_init filled
+ * may be overwritten: frequencies of the caller's own (a ramp over pair indices, a
+ * table), each below one turn a position. */
 typedef struct {
   int32_t rope_dims, interleaved, n_axes;
   float amplitude;
@@ -600,7 +603,9 @@ h3attn_status h3attn_plan_set_tree(h3attn_plan_t plan, int32_t num_kv_heads, voi
  * last draft reach nothing, whatever they hold; a NaN or an infinity in v of a draft
  * reaches the whole tree.  |v| may be up to 2^64.  A page outside the cache is read as rows of zeros, a
  * length outside [0, table_width * page_size - T] as the nearest one inside, and
- * both are reported by h3attn_get_device_error (EINVAL).
+ * both are reported by h3attn_get_device_error (EINVAL).  Lengths that give an SM
+ * more than 2^29 tiles of 128 keys (near 2^31, thousands of them) are reported so
+ * too, and the outputs are then invalid.
  * Errors: as h3attn_forward; EINVAL without h3attn_plan_set_tree, for a bad cache
  * or one of other key heads than the plan's, NULL or misaligned (tree_mask 8, the
  * others 4 bytes) lists, a table too narrow for the drafts or of 2^31 - 128 rows or more,
