@@ -119,10 +119,10 @@
 // head share segments too: a tile's rows are (token, head of the pack) pairs, token
 // by token, which one box of a three-dimensional tensor map fetches in that order.
 // So a segment spans fewer tokens (4 x 128 / pack), whose keys end at nearly the same
-// place, and K and V pass once for all of them.  Tensor-bound: 20,423 tokens, 28 heads over 4, 1,770 us, 1,690
+// place, and K and V pass once for all of them.  Tensor-bound: 20,423 tokens, 28 heads over 4, 1,780 us, 1,680
 // TFLOP/s (1,683 us in a short burst; 32 heads over 4, whose packs fill the tiles, 1,855 TFLOP/s; the dense forward with
-// the same products 1,569 us); sixteen prompts of 32,768 tokens in all, 21 heads, 346 us in two streams, whose step of
-// 1.50 us sets it.
+// the same products 1,569 us); sixteen prompts of 32,768 tokens in all, 21 heads, 344 to 350 us in two streams, whose step of
+// 1.50 us sets it (370 to 380 of a hundred calls in a row, under the power limit).
 // Bound by the tensor pipe for long walks (1.28 us a tile and CTA pair, 512 rows,
 // which is the dense forward's rate: 682 us for 1.12e12 flops in a loop, 1,640
 // TFLOP/s; 628 us alone); a segment costs another 4 us for its boundary, where

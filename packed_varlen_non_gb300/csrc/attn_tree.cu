@@ -1,8 +1,9 @@
 // Attention for trees of drafted tokens (a single token among them) over a paged
 // cache, heads grouped: include/h3attn.h, h3attn_forward_tree.
 //
-// Pages: "h3-spark" model card, "What this config does" (caches that outlive a
-// step).  The mathematics is the online softmax over key tiles: per query row a
+// The pages that define this library have no cache of keys and values; the text tower
+// that they name (vllm.cpp PR #26 "feat(minimax-h3)", the device-encoder commit) is
+// what answers from one.  The mathematics is the online softmax over key tiles: per query row a
 // running reference m and sum l, p = 2^(s - m), O += P V, o = O / l.
 //
 // What bounds it: reading the cache.  A sequence's T drafts and the G query heads of
@@ -41,12 +42,15 @@
 // zeroed in shared memory before the PV reads them (0 times a stranger's NaN is not 0).
 // Every wait is bounded, as in the forward (attn_fwd_tc.cu).
 //
-// Measured, in a graph: 32 single tokens over 5,033 (32 heads, 8 key heads, pages of 16) 104 us, 6.4 TB/s, 95 % of the
-// measured copy; 512 over 300 tokens 112 to 114 us; one over 20,000 21 us, over none 9.4 us; 16 trees of 16 drafts (28 and 4
-// heads, 32,768 tokens) 25 us; 8 trees of 64 drafts over 20,423 (64 and 8 heads) 258 us, 1,330 TFLOP/s.  There the step of two
+// Measured, in a graph on new inputs for each call: 32 single tokens over 5,033 (32 heads, 8 key heads, pages of 16) 104 to 106
+// us, 6.2 to 6.3 TB/s, 93 to 95 % of the measured copy; 512 over 300 tokens 112 us; one over 20,000 24 us (22 where its 82 MB of
+// cache lie in L2, as when a graph repeats the call), over none 9.3 us; 16 trees of 16 drafts (28 and 4
+// heads, 32,768 tokens) 27 us (26); 8 trees of 64 drafts over 20,423 (64 and 8 heads) 262 us, 1,310 TFLOP/s, in short runs, 283 in
+// long ones, under the power limit.  (Figures beside the code are of a graph that repeats one call.)  There the step of two
 // query tiles takes 3,500 cycles, 2,048 of them products: a stream's chain is 1,750 cycles of softmax (one warp an SM
 // sub-partition, bound by its own latencies), 450 until its PV is issued, 1,300 for PV and the next QK.  Two warps a row
-// would halve the softmax, but leave 96 registers a thread, which spill into the step (833 us).  Few sequences: 4,500
+// would halve the softmax, but leave 96 registers a thread, which spill into the step (833 us; as it is, the kernel of one
+// range a block spills 176 bytes).  Few sequences: 4,500
 // cycles until a block knows its part, 2,800 to its first loads' issue, 1,400 to 2,400 for them, and the join (4 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (c < parts) {
         s0[x] = share_of(total, c, parts);
         s1[x] = share_of(total, c + 1, parts);
-        if (s1[x] - s0[x] > INT32_MAX / 4) {  // (hours of work: thousands of lengths of 2^31)
+        if (s1[x] - s0[x] > INT32_MAX / 4) {  // (thousands of lengths near 2^31: more than the ring's counters hold)
           if (threadIdx.x == 0) dev::report_bad_page(a.err);
           s0[x] = s1[x] = -1;
         }

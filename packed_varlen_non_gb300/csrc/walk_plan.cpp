@@ -83,7 +83,7 @@ double rows_cost(int32_t tiles, int64_t blocks, int pairs, int32_t S) {
 
 // Row numbers are 32-bit, and the walks' go up to a segment past the last row.
 bool too_long(const int32_t* cu, int32_t n_docs) { return cu[n_docs] > INT32_MAX - kUnitRows; }
-constexpr char kTooLong[] = "too many tokens for a list of the sparse or prefix forward";
+constexpr char kTooLong[] = "too many tokens for the work list of a sparse, prefix or causal forward";
 
 // Splits a tail of the items (in list order) so that the pairs finish together;
 // returns the estimated time.
